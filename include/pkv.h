@@ -75,6 +75,8 @@ extern "C" {
 #define PKV_DEV_BAD_PAGE 4u        /* block-table entry outside [0, num_pages) inside the context;
                                       that page's tokens are left out of the softmax */
 #define PKV_DEV_TIMEOUT 8u         /* an internal pipeline wait gave up (about 2 s); the CTA stopped */
+#define PKV_DEV_BAD_PATH 16u       /* tree_commit: an accepted path that is not an ascending list of its
+                                      sequence's nodes; that sequence's rows stay as they are */
 
 /*
  * Pool descriptor (plain data; copying it is free).
@@ -324,6 +326,104 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
                                        const int32_t *context_lens, int num_seqs, int max_context,
                                        float scale, int32_t *device_status, void *stream);
 
+/* ---- speculative decoding: a tree of drafted tokens, verified in one call ------------------
+ *
+ * One step of a sequence with `base` committed tokens: the n drafted tokens (nodes, parents
+ * before children, node 0 usually the last sampled token) are appended at positions base ..
+ * base + n - 1 with pkv_kv_append; pkv_paged_tree_attention attends every node to the committed
+ * prefix and to its ancestors; once the caller has verified the drafts, pkv_tree_commit moves
+ * the K/V rows of the accepted path behind the prefix, in every layer, and gives the new
+ * context lengths (pkv_alloc_truncate then frees the pages behind them).
+ */
+
+/*
+ * pkv_paged_tree_attention - attention of a tree of drafted tokens per sequence over its paged K/V.
+ *
+ *   out[i][h][:] = sum_{t in A_i} w_t V_t[h / group][:],
+ *   w = softmax_{t in A_i}( scale * q[i][h] . K_t[h / group] ),
+ *   A_i = { t < base_s } and { base_s + j : j < n_s, bit j of row i's mask is set },
+ *   n_s = query_start[s+1] - query_start[s], base_s = context_lens[s] - n_s,
+ *   for query row i of sequence s: the nodes are the last n_s cached tokens.
+ *   A row that may attend to nothing (base_s = 0 and no bit set) gets zeros.
+ *
+ *   out            device; [total][num_q_heads][head_dim], total = query_start[num_seqs], 16-byte
+ *                  aligned: float32, or bf16 with PKV_OUT_BF16.  Rows at or past total are not written.
+ *   q              device; bf16 [total][num_q_heads][head_dim], 16-byte aligned.
+ *   num_q_rows     rows of q, out and tree_mask (>= total); no row at or past it is read or written.
+ *   query_start    device; int32 [num_seqs + 1], non-decreasing, query_start[0] = 0.
+ *   tree_mask      device; uint32, row i at tree_mask + i * mask_stride: bit j of the row is bit
+ *                  j % 32 of word j / 32.  Bits at or past n_s are ignored; a node attends to itself
+ *                  only if its own bit is set.
+ *   mask_stride    words between rows, 32 * mask_stride >= max_query.
+ *   block_tables, block_table_stride, context_lens, max_context: as for decode.
+ *   max_query      host bound on every n_s.
+ *   scale          any finite value, negative ones and 0 (a plain average) included.
+ *   workspace      device, >= pkv_tree_workspace_bytes(num_seqs, max_query, ...), 16-byte aligned,
+ *                  zero-filled before its first use; every completed call leaves it ready for the
+ *                  next, of any shape whose size it covers.  Calls sharing a workspace must not
+ *                  overlap on the GPU (nor may graphs that captured it).  After PKV_DEV_TIMEOUT, zero it again.
+ *   flags          PKV_OVERLAP_PREVIOUS: launched with programmatic stream serialization; query_start,
+ *                  context_lens, block_tables and q are read at once, the pool pages and tree_mask only
+ *                  after the kernel before it on the stream has completed, and nothing is written
+ *                  before that.  Use it only when that kernel writes none of the first four - for
+ *                  example pkv_kv_append of the drafted tokens.
+ *                  PKV_OUT_BF16: out is bf16 (rounded to nearest even); the softmax weights then
+ *                  carry bf16's 8 significant bits into the product with V.  Other bits return
+ *                  PKV_ERR_SHAPE.
+ * A sequence whose lengths do not fit (n_s < 0, > max_query or > context_lens[s], a context < 0 or
+ * > max_context, query rows past num_q_rows) gets zero rows and PKV_DEV_BAD_CONTEXT; an invalid page
+ * id inside a context sets PKV_DEV_BAD_PAGE and that page is left out.  A NaN or infinity in the K or
+ * V of a node reaches only the rows whose mask names that node.
+ * No allocation, one kernel launch.
+ */
+#define PKV_OUT_BF16 2u
+int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const void *q, int num_q_heads, int num_q_rows,
+                             const int32_t *query_start, const uint32_t *tree_mask, int64_t mask_stride,
+                             const int32_t *block_tables, int64_t block_table_stride, const int32_t *context_lens,
+                             int num_seqs, int max_query, int max_context, float scale, void *workspace,
+                             size_t workspace_bytes, int32_t *device_status, unsigned flags, void *stream);
+
+/* Workspace bytes of pkv_paged_tree_attention for up to num_seqs sequences of up to max_query nodes
+ * (partial softmax states of the split and ticket counters).  0 on bad arguments. */
+size_t pkv_tree_workspace_bytes(int num_seqs, int max_query, int num_q_heads, int head_dim);
+
+/*
+ * pkv_tree_commit - keep the accepted path of every sequence's tree: in each layer, the K and V rows
+ * of position base_s + path[k] move to position base_s + k, k < count (bit copies), with
+ * base_s = context_lens[s] - n_s and n_s = query_start[s+1] - query_start[s] as above.
+ *   block_tables      device; int32; the row of (s, layer) is at s * block_table_stride + layer * layer_stride
+ *                     and holds at least ceil(max_context / page_tokens) entries.
+ *   num_layers        >= 1; all layers' pages are in this pool.
+ *   accepted          device; int32, row s at accepted + s * accepted_stride: the path's nodes, strictly
+ *                     ascending (a path from the root down when parents come before children).
+ *   accept_counts     device; int32 [num_seqs]: nodes on the path, 0 .. min(n_s, max_accept).
+ *   max_accept        host bound on the counts, <= accepted_stride.
+ *   new_context_lens  device int32 [num_seqs], nullable; receives base_s + count.  Must not overlap
+ *                     context_lens, query_start, accepted or accept_counts (PKV_ERR_SHAPE).
+ * Rows behind the path keep their bytes.  Lengths that do not fit (as above) set PKV_DEV_BAD_CONTEXT, a
+ * path that is not as described PKV_DEV_BAD_PATH: that sequence's rows all stay, and its new context
+ * length is the old one.  A row whose source or target page id is invalid is not moved (PKV_DEV_BAD_PAGE).
+ * Sequences must not share the pages that hold their nodes (pkv_alloc_write_page sees to that).
+ * One kernel launch.
+ */
+int pkv_tree_commit(const pkv_pool *pool, const int32_t *block_tables, int64_t block_table_stride,
+                    int64_t layer_stride, int num_layers, const int32_t *query_start, const int32_t *context_lens,
+                    const int32_t *accepted, int64_t accepted_stride, const int32_t *accept_counts, int num_seqs,
+                    int max_accept, int max_context, int32_t *new_context_lens, int32_t *device_status, void *stream);
+
+/*
+ * pkv_kv_copy_pages - copy whole pages inside the pool: page dst_pages[i] = page src_pages[i], K and V
+ * (the copies that pkv_alloc_fork, pkv_alloc_write_page and pkv_alloc_compact ask for).
+ *   src_pages, dst_pages  device or mapped host; int32 [num_copies].  A pair with a negative id is
+ *                         padding and is skipped, as is a page copied onto itself; an id >= num_pages
+ *                         skips the pair and sets PKV_DEV_BAD_PAGE.
+ * The copies run in no order: one source may have several destinations, but a page that is a
+ * destination twice, or a destination and a source, ends up with an unspecified mix.
+ * num_copies = 0 enqueues nothing.  One kernel launch.
+ */
+int pkv_kv_copy_pages(const pkv_pool *pool, const int32_t *src_pages, const int32_t *dst_pages, int num_copies,
+                      int32_t *device_status, void *stream);
+
 /* ---- host page allocator (no GPU) ------------------------------------------------------
  *
  * The admission credits, lazy page assignment and page release that the scheduler below
@@ -370,6 +470,38 @@ int pkv_alloc_free_seq(pkv_alloc *alloc, int seq);
 const int32_t *pkv_alloc_block_tables(const pkv_alloc *alloc);
 /* Pages on the free list and credits held now (either pointer nullable). */
 int pkv_alloc_state(const pkv_alloc *alloc, int32_t *free_pages, int32_t *credits_in_use);
+
+/*
+ * Shared pages.  After pkv_alloc_fork two sequences name the same pages; a page goes back on the free
+ * list when the last sequence naming it lets go of it.  Every sequence holds credits for its whole
+ * length, shared pages included, so a fork never takes a page another sequence's credits promised.
+ * The page copies that these calls ask for are done by the caller, with pkv_kv_copy_pages, before
+ * anything is written to or read from the new pages.
+ */
+/* Fork: dst (not admitted now) becomes a sequence of the first `tokens` tokens of src, admitted with a
+ * budget of max_new_tokens more as pkv_alloc_admit would.  In every layer it shares src's full pages; a
+ * last page that is only partly filled by `tokens` gets a page of its own, and (source, new page) goes
+ * into copy_src/copy_dst (host int32 [capacity]; capacity >= num_layers always suffices).
+ * *num_copies receives their count.  Blocks that src has not assigned stay unassigned.
+ * Returns PKV_OK, PKV_ERR_NULL, PKV_ERR_STATE (src not admitted, dst admitted already),
+ * PKV_ERR_EXCEEDS_POOL or PKV_ERR_NO_CREDIT as admit does, PKV_ERR_NO_PAGE, or PKV_ERR_SHAPE
+ * (src = dst, tokens or max_new_tokens out of range, capacity too small); on error nothing has changed. */
+int pkv_alloc_fork(pkv_alloc *alloc, int src_seq, int dst_seq, int tokens, int max_new_tokens, int32_t *copy_src,
+                   int32_t *copy_dst, int capacity, int32_t *num_copies);
+/* Page of block `block` of (seq, layer) for writing: as pkv_alloc_page, but a page that another sequence
+ * names too is replaced by a page of this sequence's own, and *copy_src (required) receives the shared
+ * page, to be copied into *page first; -1 when there is nothing to copy. */
+int pkv_alloc_write_page(pkv_alloc *alloc, int seq, int layer, int block, int32_t *page, int32_t *copy_src);
+/* Let go of the pages behind the first `tokens` tokens of seq, in every layer (its credits stay): the
+ * blocks from ceil(tokens / page_tokens) on become unassigned. */
+int pkv_alloc_truncate(pkv_alloc *alloc, int seq, int tokens);
+/* Defragment: pages in use move so that they fill ids 0 .. used - 1.  copy_src/copy_dst (host int32
+ * [capacity]) receive the moves, *num_copies their count; no page is both a source and a destination.
+ * Every block table entry is updated; the free list then hands out the lowest free id first.
+ * PKV_ERR_SHAPE when capacity is too small (nothing has changed; *num_copies holds the count needed). */
+int pkv_alloc_compact(pkv_alloc *alloc, int32_t *copy_src, int32_t *copy_dst, int capacity, int32_t *num_copies);
+/* How many sequences' table entries name `page` now (0: free, -1: bad arguments). */
+int pkv_alloc_page_refs(const pkv_alloc *alloc, int page);
 
 /* ---- continuous-batching scheduler (no GPU) ----------------------------------------------
  *

@@ -10,6 +10,7 @@ missing that raises ImportError (there is no fallback path).
 _PUBLIC = ("KVPool", "PkvError", "PkvPool", "decode_max_ctas", "decode_plan", "decode_step", "decode_workspace", "decode_workspace_bytes",
            "kv_append", "kv_pool_bytes", "kv_pool_create", "paged_decode_attention",
            "paged_decode_attention_noalloc", "paged_prefill_attention", "Scheduler", "Allocator",
+           "kv_copy_pages", "paged_tree_attention", "tree_commit", "tree_workspace", "tree_workspace_bytes",
            "status_string")
 
 

@@ -29,6 +29,7 @@ DEV_BAD_SLOT = 1
 DEV_BAD_CONTEXT = 2
 DEV_BAD_PAGE = 4
 DEV_TIMEOUT = 8
+DEV_BAD_PATH = 16
 
 
 class PkvPool(ctypes.Structure):
@@ -79,6 +80,11 @@ EXPORTS = {
     "pkv_paged_prefill_attention": (_I, [_PP, _P, _P, _I, _I, _P, _P, _L, _P, _I, _I, _I, _F, _P, _P]),
     "pkv_paged_prefill_attention_ex": (_I, [_PP, _P, _P, _I, _I, _P, _P, _L, _P, _I, _I, _I, _F, _P, ctypes.c_uint,
                                             _P]),
+    "pkv_paged_tree_attention": (_I, [_PP, _P, _P, _I, _I, _P, _P, _L, _P, _L, _P, _I, _I, _I, _F, _P, _Z, _P,
+                                      ctypes.c_uint, _P]),
+    "pkv_tree_workspace_bytes": (_Z, [_I, _I, _I, _I]),
+    "pkv_tree_commit": (_I, [_PP, _P, _L, _L, _I, _P, _P, _P, _L, _P, _I, _I, _I, _P, _P, _P]),
+    "pkv_kv_copy_pages": (_I, [_PP, _P, _P, _I, _P, _P]),
     "pkv_alloc_create": (_I, [_I, _I, _I, _I, _I, _P, ctypes.POINTER(_P)]),
     "pkv_alloc_destroy": (None, [_P]),
     "pkv_alloc_admit": (_I, [_P, _I, _I, _I, ctypes.POINTER(ctypes.c_int32)]),
@@ -86,6 +92,11 @@ EXPORTS = {
     "pkv_alloc_free_seq": (_I, [_P, _I]),
     "pkv_alloc_block_tables": (ctypes.POINTER(ctypes.c_int32), [_P]),
     "pkv_alloc_state": (_I, [_P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
+    "pkv_alloc_fork": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, ctypes.POINTER(ctypes.c_int32)]),
+    "pkv_alloc_write_page": (_I, [_P, _I, _I, _I, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
+    "pkv_alloc_truncate": (_I, [_P, _I, _I]),
+    "pkv_alloc_compact": (_I, [_P, _P, _P, _I, ctypes.POINTER(ctypes.c_int32)]),
+    "pkv_alloc_page_refs": (_I, [_P, _I]),
     "pkv_sched_create": (_I, [_I, _I, _I, _I, _I, _P, ctypes.POINTER(_P)]),
     "pkv_sched_destroy": (None, [_P]),
     "pkv_sched_submit": (_I, [_P, _L, _I, _I]),
@@ -95,6 +106,7 @@ EXPORTS = {
 
 NOALLOC_MAX_SEQS = 512  # PKV_NOALLOC_MAX_SEQS
 OVERLAP_PREVIOUS = 1  # PKV_OVERLAP_PREVIOUS
+OUT_BF16 = 2  # PKV_OUT_BF16
 
 for _name, (_res, _args) in EXPORTS.items():
     _fn = getattr(_lib, _name)
@@ -267,6 +279,100 @@ def paged_decode_attention_noalloc(pool: KVPool | PkvPool, out: torch.Tensor, q:
     _check("pkv_paged_decode_attention_noalloc", rc)
 
 
+def _require(where: str, device: torch.device, dtype, *tensors: torch.Tensor) -> None:
+    """The tensors' pointers are what the kernel will see: their type, order and device have to be right."""
+    for t in tensors:
+        if t.dtype is not dtype or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{where}: expected a contiguous {dtype} tensor on {device}, got {t.dtype} on {t.device} "
+                             f"with strides {tuple(t.stride())}")
+
+
+def _device_of(where: str, t: torch.Tensor) -> torch.device:
+    device = t.device
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def tree_workspace_bytes(num_seqs: int, max_query: int, num_q_heads: int = 32, head_dim: int = 64) -> int:
+    return int(_lib.pkv_tree_workspace_bytes(num_seqs, max_query, num_q_heads, head_dim))
+
+
+def tree_workspace(num_seqs: int, max_query: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for pkv_paged_tree_attention (zeroed once; calls keep it valid)."""
+    return torch.zeros(tree_workspace_bytes(num_seqs, max_query), dtype=torch.uint8, device=device)
+
+
+def paged_tree_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Tensor, query_start: torch.Tensor,
+                         tree_mask: torch.Tensor, block_tables: torch.Tensor, block_table_stride: int,
+                         context_lens: torch.Tensor, max_query: int, max_context: int, scale: float,
+                         workspace: torch.Tensor, status: torch.Tensor | None = None, stream=None,
+                         overlap_previous: bool = False) -> None:
+    """Attention of the last n_s cached tokens of each sequence, the nodes of a tree: every node attends
+    to the prefix before them and to the nodes whose bits its row of tree_mask (int32 [rows, words]) has.
+    out: float32 or bfloat16 [rows, heads, dim].  overlap_previous: launch with PKV_OVERLAP_PREVIOUS (only
+    when the kernel before it on the stream writes none of q, query_start, context_lens or block_tables,
+    e.g. the drafted tokens' kv_append)."""
+    where = "pkv_paged_tree_attention"
+    desc = pool.desc if isinstance(pool, KVPool) else pool
+    device = _device_of(where, q)
+    bf16_out = out.dtype is torch.bfloat16
+    _require(where, device, torch.bfloat16, q)
+    _require(where, device, torch.bfloat16 if bf16_out else torch.float32, out)
+    _require(where, device, torch.int32, query_start, tree_mask, context_lens)
+    num_seqs = int(context_lens.shape[0])
+    rows = min(int(q.shape[0]), int(out.shape[0]), int(tree_mask.shape[0]))
+    if q.dim() != 3 or out.shape[1:] != q.shape[1:] or tree_mask.dim() != 2 or query_start.shape[0] != num_seqs + 1:
+        raise ValueError(f"{where}: q and out are [rows, heads, dim], tree_mask [rows, words], query_start [seqs + 1]")
+    flags = (OVERLAP_PREVIOUS if overlap_previous else 0) | (OUT_BF16 if bf16_out else 0)
+    _check(where, _lib.pkv_paged_tree_attention(
+        ctypes.byref(desc), _ptr(out), _ptr(q), int(q.shape[1]), rows, _ptr(query_start), _ptr(tree_mask),
+        int(tree_mask.shape[1]), _ptr(block_tables), block_table_stride, _ptr(context_lens), num_seqs, max_query,
+        max_context, scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status), flags,
+        _stream(stream)))
+
+
+def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_stride: int, layer_stride: int,
+                num_layers: int, query_start: torch.Tensor, context_lens: torch.Tensor, accepted: torch.Tensor,
+                accept_counts: torch.Tensor, max_context: int, new_context_lens: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, stream=None) -> None:
+    """Move the rows of each sequence's accepted path (accepted: int32 [seqs, width], ascending nodes, the
+    first accept_counts[s] of row s) behind its committed prefix in every layer; new_context_lens receives
+    the lengths after it."""
+    where = "pkv_tree_commit"
+    desc = pool.desc if isinstance(pool, KVPool) else pool
+    device = _device_of(where, context_lens)
+    _require(where, device, torch.int32, query_start, context_lens, accepted, accept_counts)
+    num_seqs = int(context_lens.shape[0])
+    if accepted.dim() != 2 or accepted.shape[0] != num_seqs or accept_counts.shape[0] != num_seqs or \
+            query_start.shape[0] != num_seqs + 1:
+        raise ValueError(f"{where}: accepted is [seqs, width], accept_counts [seqs], query_start [seqs + 1]")
+    if new_context_lens is not None:
+        _require(where, device, torch.int32, new_context_lens)
+        if new_context_lens.shape[0] < num_seqs:
+            raise ValueError(f"{where}: new_context_lens has {new_context_lens.shape[0]} entries for {num_seqs} sequences")
+    width = int(accepted.shape[1])
+    _check(where, _lib.pkv_tree_commit(
+        ctypes.byref(desc), _ptr(block_tables), block_table_stride, layer_stride, num_layers, _ptr(query_start),
+        _ptr(context_lens), _ptr(accepted), width, _ptr(accept_counts), num_seqs, width, max_context,
+        _ptr(new_context_lens), _ptr(status), _stream(stream)))
+
+
+def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: torch.Tensor,
+                  status: torch.Tensor | None = None, stream=None) -> None:
+    """Copy page src_pages[i] onto page dst_pages[i] (int32; a negative id is padding), K and V."""
+    where = "pkv_kv_copy_pages"
+    desc = pool.desc if isinstance(pool, KVPool) else pool
+    for t in (src_pages, dst_pages):
+        if t.dtype is not torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{where}: page ids are contiguous int32 tensors")
+    n = int(src_pages.shape[0])
+    if dst_pages.shape[0] != n:
+        raise ValueError(f"{where}: {n} source pages, {dst_pages.shape[0]} destinations")
+    _check(where, _lib.pkv_kv_copy_pages(ctypes.byref(desc), _ptr(src_pages), _ptr(dst_pages), n, _ptr(status),
+                                         _stream(stream)))
+
+
 class Allocator:
     """Host page allocator of ``libpkv.so`` (see ``pkv_alloc_*``): admission credits, lazy pages
     from a LIFO free list, release of a sequence's pages.  Methods raise PkvError on a negative
@@ -278,7 +384,7 @@ class Allocator:
                  max_seqs: int = 32, free_order=None):
         import numpy as np
         self._np = np
-        self.num_layers, self.max_seqs = num_layers, max_seqs
+        self.num_pages, self.num_layers, self.max_seqs = num_pages, num_layers, max_seqs
         self.max_blocks = -(-max_context // page_tokens)
         order = None
         if free_order is not None:
@@ -310,6 +416,41 @@ class Allocator:
 
     def free_seq(self, seq: int) -> None:
         _check("pkv_alloc_free_seq", _lib.pkv_alloc_free_seq(self._h, seq))
+
+    def fork(self, src_seq: int, dst_seq: int, tokens: int, max_new_tokens: int):
+        """(status, source pages, new pages): dst_seq shares the first ``tokens`` tokens of src_seq; copy the
+        pages (``kv_copy_pages``) before using the fork.  Status as for ``admit``."""
+        np = self._np
+        src, dst, n = np.zeros(self.num_layers, np.int32), np.zeros(self.num_layers, np.int32), ctypes.c_int32(0)
+        rc = _lib.pkv_alloc_fork(self._h, src_seq, dst_seq, tokens, max_new_tokens, src.ctypes.data, dst.ctypes.data,
+                                 self.num_layers, ctypes.byref(n))
+        if rc not in (self.OK, self.NO_CREDIT, self.EXCEEDS_POOL):
+            raise PkvError("pkv_alloc_fork", rc)
+        k = n.value if rc == self.OK else 0
+        return rc, src[:k].copy(), dst[:k].copy()
+
+    def write_page(self, seq: int, layer: int, block: int) -> tuple[int, int]:
+        """(page, shared page to copy into it first, or -1) of a block about to be written."""
+        p, c = ctypes.c_int32(-1), ctypes.c_int32(-1)
+        _check("pkv_alloc_write_page", _lib.pkv_alloc_write_page(self._h, seq, layer, block, ctypes.byref(p),
+                                                                 ctypes.byref(c)))
+        return p.value, c.value
+
+    def truncate(self, seq: int, tokens: int) -> None:
+        """Give back the pages behind the first ``tokens`` tokens."""
+        _check("pkv_alloc_truncate", _lib.pkv_alloc_truncate(self._h, seq, tokens))
+
+    def compact(self):
+        """(source pages, destination pages) of the moves that put the used pages at 0 .. used - 1."""
+        np = self._np
+        src, dst = np.zeros(self.num_pages, np.int32), np.zeros(self.num_pages, np.int32)
+        n = ctypes.c_int32(0)
+        _check("pkv_alloc_compact", _lib.pkv_alloc_compact(self._h, src.ctypes.data, dst.ctypes.data, self.num_pages,
+                                                           ctypes.byref(n)))
+        return src[:n.value].copy(), dst[:n.value].copy()
+
+    def page_refs(self, page: int) -> int:
+        return int(_lib.pkv_alloc_page_refs(self._h, page))
 
     def block_tables(self):
         """A copy of the block table [max_seqs, num_layers, max_blocks]."""

@@ -11,7 +11,9 @@
 // On completion a request returns its pages and credits.
 //
 // pkv_alloc holds the pieces the policy is made of - credits, the free list and the
-// block tables - and is exported on its own for callers that schedule themselves;
+// block tables - and is exported on its own for callers that schedule themselves; for
+// these it also shares pages between sequences (forks, copy on write by reference
+// counts), cuts sequences back and defragments the pool.
 // pkv_sched adds the FIFO queue, slots and the per-step plan on top of it.
 #include <stdint.h>
 
@@ -26,6 +28,7 @@ struct pkv_alloc {
   int num_pages, num_layers, page_tokens, max_context, max_seqs, max_blocks;
   std::vector<int32_t> free_list;     // back = next page handed out
   std::vector<int32_t> block_tables;  // [seq][layer][block], -1 = unassigned
+  std::vector<int32_t> refs;          // per page: table entries that name it, 0 = free
   std::vector<int32_t> seq_credits;   // credits held by each sequence, 0 = not admitted
   std::vector<char> admitted;
   int credits_used = 0;
@@ -52,6 +55,25 @@ struct pkv_alloc {
     return PKV_OK;
   }
 
+  // A page of its own from the back of the free list, which the caller has seen is not empty.
+  // (The list was made with room for every page, so giving one back never allocates.)
+  int32_t take() {
+    const int32_t p = free_list.back();
+    free_list.pop_back();
+    refs[p] = 1;
+    ++assigned;
+    return p;
+  }
+
+  // One table entry lets go of its page; the last one gives the page back.
+  void let_go(int32_t *entry) {
+    if (--refs[*entry] == 0) {
+      free_list.push_back(*entry);
+      --assigned;
+    }
+    *entry = -1;
+  }
+
   // Page of block `block` of (seq, layer), taken from the back of the free list on first use.
   int page(int seq, int layer, int block, int32_t *out) {
     if (seq < 0 || seq >= max_seqs || layer < 0 || layer >= num_layers || block < 0 || block >= max_blocks)
@@ -60,11 +82,98 @@ struct pkv_alloc {
     int32_t *r = row(seq, layer);
     if (r[block] < 0) {
       if (free_list.empty()) return PKV_ERR_NO_PAGE;
-      r[block] = free_list.back();
-      free_list.pop_back();
-      ++assigned;
+      r[block] = take();
     }
     if (out != nullptr) *out = r[block];
+    return PKV_OK;
+  }
+
+  // The same for a block about to be written: a page shared with another sequence is exchanged
+  // for one of this sequence's own, to be filled from *copy_src.  A sequence's table entries stay
+  // within its credits, and a shared page counts against every holder's, so a free page is there.
+  int write_page(int seq, int layer, int block, int32_t *out, int32_t *copy_src) {
+    int32_t p = -1;
+    const int rc = page(seq, layer, block, &p);
+    if (rc != PKV_OK) return rc;
+    *copy_src = -1;
+    if (refs[p] > 1) {
+      if (free_list.empty()) return PKV_ERR_NO_PAGE;
+      int32_t *entry = row(seq, layer) + block;
+      *copy_src = p;
+      --refs[p];
+      *entry = p = take();
+    }
+    if (out != nullptr) *out = p;
+    return PKV_OK;
+  }
+
+  // dst becomes the first `tokens` tokens of src: full pages shared, a partly filled one copied.
+  int fork(int src, int dst, int tokens, int new_tokens, int32_t *copy_src, int32_t *copy_dst, int capacity,
+           int32_t *num_copies) {
+    if (src < 0 || src >= max_seqs || dst < 0 || dst >= max_seqs || src == dst || tokens < 1 || tokens > max_context ||
+        new_tokens < 1 || capacity < 0)
+      return PKV_ERR_SHAPE;
+    if (!admitted[src] || admitted[dst]) return PKV_ERR_STATE;
+    const int full = tokens / page_tokens;
+    const bool partial = tokens % page_tokens != 0;
+    int need = 0;
+    for (int l = 0; partial && l < num_layers; ++l) need += row(src, l)[full] >= 0;
+    *num_copies = need;
+    if (need > capacity) return PKV_ERR_SHAPE;
+    if (need > 0 && (copy_src == nullptr || copy_dst == nullptr)) return PKV_ERR_NULL;
+    if (size_t(need) > free_list.size()) return PKV_ERR_NO_PAGE;
+    const int rc = admit(dst, tokens, new_tokens, nullptr);
+    if (rc != PKV_OK) return rc;
+    int k = 0;
+    for (int l = 0; l < num_layers; ++l) {
+      const int32_t *from = row(src, l);
+      int32_t *to = row(dst, l);
+      for (int b = 0; b < full; ++b) {
+        to[b] = from[b];
+        if (from[b] >= 0) ++refs[from[b]];
+      }
+      if (partial && from[full] >= 0) {
+        copy_src[k] = from[full];
+        copy_dst[k++] = to[full] = take();
+      }
+    }
+    return PKV_OK;
+  }
+
+  // Lets go of the blocks behind the first `tokens` tokens (layers in order, blocks ascending).
+  int truncate(int seq, int tokens) {
+    if (seq < 0 || seq >= max_seqs || tokens < 0 || tokens > max_context) return PKV_ERR_SHAPE;
+    if (!admitted[seq]) return PKV_ERR_STATE;
+    for (int l = 0; l < num_layers; ++l) {
+      int32_t *r = row(seq, l);
+      for (int b = (tokens + page_tokens - 1) / page_tokens; b < max_blocks; ++b)
+        if (r[b] >= 0) let_go(r + b);
+    }
+    return PKV_OK;
+  }
+
+  // Moves the used pages with ids at or past the number of used pages into the free ids below it.
+  int compact(int32_t *copy_src, int32_t *copy_dst, int capacity, int32_t *num_copies) {
+    if (capacity < 0) return PKV_ERR_SHAPE;
+    int moves = 0;
+    for (int p = assigned; p < num_pages; ++p) moves += refs[p] > 0;
+    *num_copies = moves;
+    if (moves > capacity) return PKV_ERR_SHAPE;
+    if (moves > 0 && (copy_src == nullptr || copy_dst == nullptr)) return PKV_ERR_NULL;
+    std::vector<int32_t> moved(num_pages, -1);  // new id of a moved page
+    int hole = 0, k = 0;
+    for (int p = assigned; p < num_pages; ++p) {
+      if (refs[p] == 0) continue;
+      while (refs[hole] > 0) ++hole;
+      copy_src[k] = p;
+      copy_dst[k++] = moved[p] = hole;
+      refs[hole] = refs[p];
+      refs[p] = 0;
+    }
+    for (int32_t &e : block_tables)
+      if (e >= 0 && moved[e] >= 0) e = moved[e];
+    free_list.clear();
+    for (int p = num_pages - 1; p >= assigned; --p) free_list.push_back(p);
     return PKV_OK;
   }
 
@@ -74,13 +183,8 @@ struct pkv_alloc {
     if (!admitted[seq]) return PKV_ERR_STATE;
     for (int l = 0; l < num_layers; ++l) {
       int32_t *r = row(seq, l);
-      for (int b = 0; b < max_blocks; ++b) {
-        if (r[b] >= 0) {
-          free_list.push_back(r[b]);
-          r[b] = -1;
-          --assigned;
-        }
-      }
+      for (int b = 0; b < max_blocks; ++b)
+        if (r[b] >= 0) let_go(r + b);
     }
     credits_used -= seq_credits[seq];
     seq_credits[seq] = 0;
@@ -114,6 +218,7 @@ int alloc_init(pkv_alloc *a, int num_pages, int num_layers, int page_tokens, int
   } else {
     for (int i = 0; i < num_pages; ++i) a->free_list[i] = i;
   }
+  a->refs.assign(num_pages, 0);
   a->block_tables.assign(size_t(max_seqs) * num_layers * a->max_blocks, -1);
   a->seq_credits.assign(max_seqs, 0);
   a->admitted.assign(max_seqs, 0);
@@ -177,6 +282,40 @@ extern "C" int pkv_alloc_state(const pkv_alloc *alloc, int32_t *free_pages, int3
   if (free_pages != nullptr) *free_pages = int32_t(alloc->free_list.size());
   if (credits_in_use != nullptr) *credits_in_use = alloc->credits_used;
   return PKV_OK;
+}
+
+extern "C" int pkv_alloc_fork(pkv_alloc *alloc, int src_seq, int dst_seq, int tokens, int max_new_tokens,
+                              int32_t *copy_src, int32_t *copy_dst, int capacity, int32_t *num_copies) {
+  if (alloc == nullptr || num_copies == nullptr) return PKV_ERR_NULL;
+  *num_copies = 0;
+  return alloc->fork(src_seq, dst_seq, tokens, max_new_tokens, copy_src, copy_dst, capacity, num_copies);
+}
+
+extern "C" int pkv_alloc_write_page(pkv_alloc *alloc, int seq, int layer, int block, int32_t *page,
+                                    int32_t *copy_src) {
+  if (alloc == nullptr || copy_src == nullptr) return PKV_ERR_NULL;
+  return alloc->write_page(seq, layer, block, page, copy_src);
+}
+
+extern "C" int pkv_alloc_truncate(pkv_alloc *alloc, int seq, int tokens) {
+  if (alloc == nullptr) return PKV_ERR_NULL;
+  return alloc->truncate(seq, tokens);
+}
+
+extern "C" int pkv_alloc_compact(pkv_alloc *alloc, int32_t *copy_src, int32_t *copy_dst, int capacity,
+                                 int32_t *num_copies) {
+  if (alloc == nullptr || num_copies == nullptr) return PKV_ERR_NULL;
+  *num_copies = 0;
+  try {
+    return alloc->compact(copy_src, copy_dst, capacity, num_copies);
+  } catch (const std::bad_alloc &) {  // the list of moved ids, before anything has changed
+    return PKV_ERR_SHAPE;
+  }
+}
+
+extern "C" int pkv_alloc_page_refs(const pkv_alloc *alloc, int page) {
+  if (alloc == nullptr || page < 0 || page >= alloc->num_pages) return -1;
+  return alloc->refs[page];
 }
 
 // ---- scheduler ----------------------------------------------------------------------
