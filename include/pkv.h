@@ -356,7 +356,7 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
  *                  only if its own bit is set.
  *   mask_stride    words between rows, 32 * mask_stride >= max_query.
  *   block_tables, block_table_stride, context_lens, max_context: as for decode.
- *   max_query      host bound on every n_s.
+ *   max_query      host bound on every n_s, at most 2^20 (and num_seqs at most 2^24).
  *   scale          any finite value, negative ones and 0 (a plain average) included.
  *   workspace      device, >= pkv_tree_workspace_bytes(num_seqs, max_query, ...), 16-byte aligned,
  *                  zero-filled before its first use; every completed call leaves it ready for the

@@ -298,6 +298,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       PKV_S8(0), PKV_S8(8), PKV_S8(16), PKV_S8(24)
       : "memory");
 }
+
+// Stores 16 consecutive columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      PKV_S8(0), PKV_S8(8)
+      : "memory");
+}
 #undef PKV_R8
 #undef PKV_S8
 
@@ -326,6 +336,16 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
       "fma.rn.f32x2 d, aa, ba, ca;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 add_f32x2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 xa, ya, d;\n\t"
+      "mov.b64 xa, {%2, %3};\n\tmov.b64 ya, {%4, %5};\n\t"
+      "add.rn.f32x2 d, xa, ya;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return r;
 }
 

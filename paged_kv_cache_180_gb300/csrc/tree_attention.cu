@@ -3,14 +3,40 @@
 //   out[i][h] = sum_{t in A_i} softmax_t(scale * q[i][h] . K_t[h/4]) V_t[h/4],
 //   A_i = the committed prefix (t < base_s) and the nodes base_s + j whose bit j is set in row i's mask
 //
-// One pass over a sequence's pages with the running maximum and sum of the softmax; a masked key is
-// skipped, so whatever its K and V hold (NaN included) never meets a row that may not see it.
+// evaluated in one pass over the keys: with m a reference for the row's scores, l = sum 2^((s_t - m) c)
+// and O = sum 2^((s_t - m) c) V_t (c = scale log2 e); two disjoint key sets merge by
+// M = max(m_a, m_b), L = sum l 2^((m - M) c), O = sum O 2^((m - M) c), out = O / L.
 //
-// One CTA = (sequence, K/V head, 4 nodes): the 16 rows (4 nodes x 4 query heads) share each page's
-// K and V rows, staged in shared memory.  Eight threads share a row, 8 dims each.
+// GB300 design (tcgen05 tensor cores, accumulators in tensor memory)
+//  * Unit: 32 nodes of a sequence against one K/V head g.  Its 128 rows (4 * node + head in group) share
+//    every K/V row loaded: M = 128.  Keys in blocks of 64 (4 pages).
+//  * Work split: the key blocks of all units form one list; the grid's CTAs (two per SM) take equal
+//    shares of it, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
+//    state (m, l, O) per CTA in the workspace, and the warp that takes the last of its tickets (an
+//    atomic counter, nobody waits) merges them.
+//  * Warp roles (320 threads): 8 softmax warps, a loader (tiled TMA: Q as boxes of 8 nodes x 4 heads,
+//    two buffers; head g's 16 rows of each page as 2 KiB boxes into a ring of 4 blocks), an MMA issuer.
+//  * S = Q K^T is 4 tcgen05.mma (M 128, N 64, K 16) into one of two TMEM buffers, so S of block j + 1 runs
+//    while the softmax works on block j.  A row belongs to two threads, one for the block's keys
+//    0-31 and one for keys 32-63, each with a reference, row sum and accumulator (O_a, O_b in tensor memory)
+//    of its own, so that they meet only at the unit's end.  P overwrites its S and is the TMEM A operand of
+//    O_a += P_a V[0:32], O_b += P_b V[32:64].
+//  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits; two
+//    products); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
+//    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
+//  * A row's reference moves only when a block's maximum exceeds it by more than 8 (a factor 256); then
+//    the row of O is rescaled in TMEM, after the product before it completed.
+//  * Masks: a key a row may not see gets weight 0 by selection, so a NaN score stays out.  V rows at or
+//    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
+//    NaN or an infinity (0 * NaN in the product would reach every row); the rows that see such a node add
+//    its contribution at the unit's end, from global memory.
+//  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing
+//    work, waits (bounded) for what is in flight, frees its tensor memory and exits.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <math.h>
+#include <mutex>
 
 #include "host_common.h"
 #include "pkv_device.cuh"
@@ -18,20 +44,45 @@
 namespace pkv {
 namespace {
 
-constexpr int kTreeTok = 32;                      // nodes per tile of the workspace's accounting
-constexpr int kTreeRows = kTreeTok * kGroup;
-constexpr int kTreeMaxCtas = 320;
-constexpr size_t kTreeSlotBytes = size_t(kTreeRows) * (kHeadDim + 2) * sizeof(float);
+constexpr int kTok = 32;                            // nodes per unit
+constexpr int kRows = kTok * kGroup;                // M = 128
+constexpr int kOctet = 8;                           // nodes per Q box: one warp's 32 TMEM lanes
+constexpr int kKeys = 64;                           // keys per block
+constexpr int kHalf = kKeys / 2;                    // keys of a block that one thread of a row has
+constexpr int kPagesPerBlock = kKeys / kPageTokens;
+constexpr int kStages = 4;                          // K/V blocks in flight
+constexpr int kSoftWarps = 8;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr int kThreads = kSoftThreads + 64;
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 320;
+constexpr int kMinBlocks = 2;                       // least key blocks a CTA is given
+constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
+constexpr int kTileBytes = kKeys * kRowBytes;       // K (or V) of one block: 8 KiB
+constexpr int kOctetBytes = kOctet * kGroup * kRowBytes;  // 4 KiB
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColO = 2 * kKeys;               // S buffers at columns 0 and 64, O_a at 128, O_b at 192
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.f;
 
-constexpr int kSimpleNodes = 4;
-constexpr int kSimpleThreads = 128;
+constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, false);     // B = K rows (K-major)
+constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows (MN-major)
+
+// Partial state of one (CTA, unit) pair.
+struct Part {
+  float o[kRows][kHeadDim];
+  float2 ml[kRows];
+};
 
 struct TreeArgs {
+  CUtensorMap tmap_k;  // boxes of one head's 16 rows of one page
+  CUtensorMap tmap_v;
+  CUtensorMap tmap_q;  // boxes of 8 query rows x one group's 4 heads (rows past num_q_rows read as zeros)
   const uint8_t *k_base, *v_base;
   long long page_stride;
   int num_pages;
-  void *out;
+  void *out;  // [total][32][64] float32 or bf16
   const uint16_t *q;
   int num_q_rows;
   const int32_t *query_start;
@@ -41,107 +92,703 @@ struct TreeArgs {
   long long bt_stride;
   const int32_t *context_lens;
   int num_seqs, max_query, max_context;
-  float scale_log2;
-  int out_bf16;
+  int max_tiles;      // units a sequence may have per K/V head
+  float scale_log2;   // |scale| * log2(e)
+  float move_thresh;  // scores (unscaled) by which a block's max must pass the reference to move it
+  int neg;            // scale < 0: the scores are negated
+  int *tickets;       // [num_seqs * max_tiles * 8 heads][8 warps], 0 between calls
+  Part *parts;        // [2 * kMaxCtas]
   int32_t *status;
 };
 
-__global__ void __launch_bounds__(kSimpleThreads) tree_attention_kernel(const TreeArgs a) {
-  __shared__ uint4 ks[kPageTokens * 8], vs[kPageTokens * 8];
-  const int tid = threadIdx.x;
-  const int s = int(blockIdx.x), g = int(blockIdx.y), j0 = int(blockIdx.z) * kSimpleNodes;
-  const int q0 = __ldg(a.query_start + s), n = __ldg(a.query_start + s + 1) - q0, ctx = __ldg(a.context_lens + s);
-  const bool bad = n < 0 || n > a.max_query || ctx < 0 || ctx > a.max_context || n > ctx || q0 < 0 ||
-                   q0 > a.num_q_rows - n;
-  if (bad && g == 0 && j0 == 0 && tid == 0 && n != 0) report(a.status, PKV_DEV_BAD_CONTEXT);
-  const int r = tid >> 3, c = tid & 7, node = j0 + (r >> 2), h = g * kGroup + (r & 3);
-  auto write = [&](long long row, const float (&o)[8]) {
-    const long long at = (row * kQHeads + h) * kHeadDim + c * 8;
-    if (a.out_bf16) {
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) =
-          make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-    } else {
-      float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-      dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+struct __align__(1024) Smem {
+  uint8_t q[2][kRows * kRowBytes];
+  uint8_t k[kStages][kTileBytes];
+  uint8_t v[kStages][kTileBytes];
+  float2 ml[2][2][kRows];  // [turn][half]: a row's (reference, sum), exchanged at a segment's end
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2];
+  uint64_t p_full[2];  // every softmax warp has written its P of the buffer (and is done with what it replaces)
+  uint64_t p_free[2];  // the products of a block are done: its buffer may be written, O read
+  uint64_t mma_done;
+  int kv_bad[kStages];     // bit pp: page pp of the stage's block is invalid (loaded as zeros)
+  int nonfinite[4];        // [segment % 4]: the last segment in which a node's V was zeroed (the softmax
+                           // warps are never more than two segments apart: a block's S waits for the P two before)
+  long long sums[kThreads / 32];
+  long long total, first;  // blocks in the list; global index of seq0's first block
+  int seq0, found;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+
+// A sequence's lengths and what it asks for: tiles of 32 nodes, blocks of 64 keys.  Sequences with no
+// nodes, and those whose lengths do not fit, have no blocks.
+struct Seq {
+  int q0, n, ctx, tiles, nb;
+  __device__ void load(const TreeArgs &a, int s) {
+    q0 = __ldg(a.query_start + s);
+    n = __ldg(a.query_start + s + 1) - q0;
+    ctx = __ldg(a.context_lens + s);
+    tiles = nb = 0;
+    if (n > 0 && valid(a)) {
+      tiles = (n + kTok - 1) / kTok;
+      nb = (ctx - 1) / kKeys + 1;
+    }
+  }
+  __device__ bool valid(const TreeArgs &a) const {
+    return n >= 0 && n <= a.max_query && ctx >= 0 && ctx <= a.max_context && n <= ctx && q0 >= 0 &&
+           q0 <= a.num_q_rows - n;
+  }
+  __device__ long long blocks() const { return (long long)kKvHeads * tiles * nb; }
+};
+
+// A CTA's share of one unit: key blocks j0 .. j1 - 1 of (sequence, K/V head, tile).  List order:
+// sequence, head, tile, block.
+struct Segment {
+  int s, g, tile, j0, j1;
+  long long unit0;  // the list index of the unit's block 0
+};
+
+struct Walk {
+  long long pos, end, first;  // list position, end of the CTA's share, first block of sequence s
+  int s;
+  Seq seq;
+  __device__ bool next(const TreeArgs &a, Segment &x) {
+    if (pos >= end) return false;
+    while (pos - first >= seq.blocks()) {
+      first += seq.blocks();
+      seq.load(a, ++s);
+    }
+    const long long u = (pos - first) / seq.nb;
+    x.s = s;
+    x.g = int(u / seq.tiles);
+    x.tile = int(u % seq.tiles);
+    x.unit0 = first + u * seq.nb;
+    x.j0 = int(pos - x.unit0);
+    x.j1 = int(min((long long)seq.nb, x.j0 + (end - pos)));
+    pos += x.j1 - x.j0;
+    return true;
+  }
+};
+
+// CTA that owns block p of the list when T blocks are split over G CTAs.
+__device__ __forceinline__ int cta_of_block(long long p, long long T, int G) { return int(((p + 1) * G - 1) / T); }
+
+// Bounded wait that gives up at once when another role has already aborted; true when the phase completed.
+__device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (*reinterpret_cast<volatile int *>(&sm.abort)) return false;
+  if (mbar_wait(bar, parity)) return true;
+  *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+  report(status, PKV_DEV_TIMEOUT);
+  return false;
+}
+
+// Largest of 32 values: a tree of three-input max.
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+  float m[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i) m[i] = max3f(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
+  m[10] = fmaxf(x[30], x[31]);
+  const float a = max3f(m[0], m[1], m[2]), b = max3f(m[3], m[4], m[5]), c = max3f(m[6], m[7], m[8]);
+  return max3f(max3f(a, b, c), m[9], m[10]);
+}
+
+// The keys of a 32-key window starting at position key0 that a row may see: the prefix, then the nodes
+// named by its mask words; nothing at or past the context.
+__device__ __forceinline__ uint32_t window_bits(const uint32_t *mask, int key0, int base, int ctx, int n) {
+  if (key0 >= ctx) return 0u;
+  const int lim = base - key0;  // prefix keys in the window
+  if (lim >= 32) return ~0u;
+  uint32_t bits;
+  const int off = -lim;  // node of the window's first key
+  if (off >= 0) {
+    const int w = off >> 5;
+    const uint32_t lo = __ldg(mask + w), hi = (w + 1) * 32 < n ? __ldg(mask + w + 1) : 0u;
+    bits = __funnelshift_r(lo, hi, off & 31);
+  } else {
+    bits = (__ldg(mask) << lim) | ((1u << lim) - 1u);
+  }
+  const int left = ctx - key0;
+  return left >= 32 ? bits : bits & ((1u << left) - 1u);
+}
+
+__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool nonfinite_chunk(const uint4 &x) {
+  return nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) || nonfinite_pair(x.w);
+}
+
+// The weight of a state (m, l) merged under the reference M; a state that has seen no key has l = 0.
+__device__ __forceinline__ float state_weight(float2 ml, float M, float c) {
+  return ml.y == 0.f ? 0.f : ex2_approx((ml.x - M) * c);
+}
+
+// Writes 32 dims of a row.
+template <bool kBf16>
+__device__ __forceinline__ void write_row(const TreeArgs &a, long long at, const float (&r)[32]) {
+  if constexpr (kBf16) {
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dst[i] = make_uint4(pack_bf16x2(r[8 * i], r[8 * i + 1]), pack_bf16x2(r[8 * i + 2], r[8 * i + 3]),
+                          pack_bf16x2(r[8 * i + 4], r[8 * i + 5]), pack_bf16x2(r[8 * i + 6], r[8 * i + 7]));
+  } else {
+    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+  }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(const __grid_constant__ TreeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = int(gridDim.x), cta = int(blockIdx.x);
+
+  // ---- blocks in the list, and this CTA's share of them ----
+  long long mine = 0;
+  for (int s = tid; s < a.num_seqs; s += kThreads) {
+    Seq q;
+    q.load(a, s);
+    mine += q.blocks();
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sm.sums[warp] = mine;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kSoftWarps);
+      mbar_init(&sm.p_free[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) sm.nonfinite[i] = -1;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    mbar_init(&sm.mma_done, 1);
+    sm.abort = 0;
+    sm.found = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  long long T = 0;
+  for (int w = 0; w < kThreads / 32; ++w) T += sm.sums[w];
+  const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));
+
+  // rows of sequences whose lengths do not fit, spread over the CTAs (a global write: after griddep_wait)
+  auto zero_invalid = [&](int t, int threads) {
+    for (int s = cta; s < a.num_seqs; s += G) {
+      Seq q;
+      q.load(a, s);
+      if (q.n == 0 || q.valid(a)) continue;
+      if (t == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
+      const long long r0 = max((long long)q.q0, 0LL), r1 = min((long long)q.q0 + q.n, (long long)a.num_q_rows);
+      constexpr int kChunks = kQHeads * kHeadDim * (kBf16 ? 2 : 4) / 16;  // 16-byte chunks of a row
+      for (long long i = r0 * kChunks + t; i < r1 * kChunks; i += threads)
+        static_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  if (bad) {
-    const float zero[8] = {};
-    for (long long j = node; j < n; j += (long long)gridDim.z * kSimpleNodes) {
-      const long long row = (long long)q0 + j;
-      if (row >= 0 && row < a.num_q_rows) write(row, zero);
-    }
+  if (T == 0 || cta >= Gu) {
+    griddep_launch_dependents();
+    griddep_wait();
+    zero_invalid(tid, kThreads);
     return;
   }
-  if (j0 >= n) return;
-  const bool real = node < n;
-  const int base = ctx - n;
-  float q[8], o[8];
-  {
-    const uint4 x = real ? *reinterpret_cast<const uint4 *>(a.q + ((long long)(q0 + node) * kQHeads + h) * kHeadDim + c * 8)
-                         : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[2 * i] = bf16_lo(w[i]);
-      q[2 * i + 1] = bf16_hi(w[i]);
-      o[2 * i] = o[2 * i + 1] = 0.f;
+  const long long pa = (long long)cta * T / Gu, pb = (long long)(cta + 1) * T / Gu;
+
+  // ---- the sequence that holds block pa ----
+  long long before = 0;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+    __syncthreads();
+    if (sm.found) break;
+    const int s = s0 + tid;
+    long long v = 0;
+    if (s < a.num_seqs) {
+      Seq q;
+      q.load(a, s);
+      v = q.blocks();
     }
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sm.sums[warp] = x;
+    __syncthreads();
+    long long chunk = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) x += sm.sums[w];
+      chunk += sm.sums[w];
+    }
+    x += before;
+    if (x - v <= pa && pa < x) {
+      sm.seq0 = s;
+      sm.first = x - v;
+      sm.found = 1;
+    }
+    before += chunk;
   }
-  const uint32_t *mask = a.mask + (long long)(q0 + (real ? node : 0)) * a.mask_stride;
-  const int32_t *table = a.block_tables + (long long)s * a.bt_stride;
-  float m = -INFINITY, l = 0.f;
-  for (int p = 0; p * kPageTokens < ctx; ++p) {
-    const int page = __ldg(table + p);
-    if (page < 0 || page >= a.num_pages) {
-      if (tid == 0) report(a.status, PKV_DEV_BAD_PAGE);
-      continue;
+  if (warp == kMmaWarp) tmem_alloc(&sm.tmem_base, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  griddep_launch_dependents();  // a kernel that starts beside this one finds what tensor memory is left
+  Walk walk;
+  walk.pos = pa;
+  walk.end = pb;
+  walk.first = sm.first;
+  walk.s = sm.seq0;
+  walk.seq.load(a, walk.s);
+  // Small trees fill the lanes of one warp only: units start at another quarter of the lanes each, so
+  // that the quarters (the SM's sub-partitions) share the work.
+  const int turn = cta * 2 >= G ? 2 : 0;
+
+  if (warp == kLoadWarp) {
+    // ================= loader: Q boxes and K/V blocks (tiled TMA) =================
+    const uint64_t once = policy_evict_first(), again = policy_evict_last();
+    if (lane == 0) {
+      prefetch_tensormap(&a.tmap_k);
+      prefetch_tensormap(&a.tmap_v);
+      prefetch_tensormap(&a.tmap_q);
     }
-    const long long at = (long long)page * a.page_stride + g * kPageTokens * kRowBytes;
-    __syncthreads();
-    ks[tid] = reinterpret_cast<const uint4 *>(a.k_base + at)[tid];
-    vs[tid] = reinterpret_cast<const uint4 *>(a.v_base + at)[tid];
-    __syncthreads();
-    for (int t = 0; t < kPageTokens && p * kPageTokens + t < ctx; ++t) {
-      const uint4 kx = ks[t * 8 + c];
-      const uint32_t kw[4] = {kx.x, kx.y, kx.z, kx.w};
-      float x = 0.f;
+    long long gb = 0;  // blocks issued
+    int k = 0;         // segments started
+    bool ok = true, waited = false;
+    Segment x;
+    while (ok && walk.next(a, x)) {
+      const int t = min(kTok, walk.seq.n - x.tile * kTok), octets = (t + kOctet - 1) / kOctet, qb = k & 1;
+      if (k >= 2) {
+        const bool w = wait(sm, &sm.q_empty[qb], uint32_t(k / 2 - 1) & 1, a.status);
+        if (!__all_sync(0xffffffffu, w)) break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full[qb], uint32_t(octets * kOctetBytes));
+        for (int o = 0; o < octets; ++o)
+          tma_load_3d(sm.q[qb] + ((o + k + turn) & 3) * kOctetBytes, &a.tmap_q, 0, x.g * kGroup,
+                      walk.seq.q0 + x.tile * kTok + o * kOctet, &sm.q_full[qb], once);
+      }
+      __syncwarp();
+      // launched with overlap (PKV_OVERLAP_PREVIOUS), the kernel before this one may still be writing
+      // the pool: it is read only once that kernel has completed
+      if (!waited) griddep_wait();
+      waited = true;
+      // block-table entries 32 at a time (8 blocks), the next 32 in flight
+      const int32_t *table = a.block_tables + (long long)x.s * a.bt_stride;
+      const int npages = (walk.seq.ctx - 1) / kPageTokens + 1, p0 = x.j0 * kPagesPerBlock;
+      const uint64_t policy = walk.seq.tiles > 1 ? again : once;  // several tiles read the same K/V
+      auto entries = [&](int p) { return p + lane < npages ? __ldg(table + p + lane) : -1; };
+      int ent = entries(p0), ent_next = entries(p0 + 32);
+      for (int j = x.j0; j < x.j1; ++j, ++gb) {
+        const int st = int(gb % kStages), at = (j - x.j0) * kPagesPerBlock & 31;
+        if (at == 0 && j > x.j0) {
+          ent = ent_next;
+          ent_next = entries(j * kPagesPerBlock + 32);
+        }
+        if (gb >= kStages) {
+          const bool w = wait(sm, &sm.kv_empty[st], uint32_t(gb / kStages - 1) & 1, a.status);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+        }
+        int page[kPagesPerBlock], bad = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x += q[2 * i] * bf16_lo(kw[i]) + q[2 * i + 1] * bf16_hi(kw[i]);
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      const int j = p * kPageTokens + t - base;
-      if (j >= 0 && !((__ldg(mask + (j >> 5)) >> (j & 31)) & 1u)) continue;
-      x *= a.scale_log2;
-      const float mn = fmaxf(m, x), keep = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(x - mn);
-      m = mn;
-      l = l * keep + w;
-      const uint4 vx = vs[t * 8 + c];
-      const uint32_t vw[4] = {vx.x, vx.y, vx.z, vx.w};
+        for (int pp = 0; pp < kPagesPerBlock; ++pp) {
+          const int e = __shfl_sync(0xffffffffu, ent, at + pp);
+          page[pp] = -1;  // outside the pool: TMA fills the box with zeros
+          if (j * kPagesPerBlock + pp < npages) {
+            if (e >= 0 && e < a.num_pages)
+              page[pp] = e;
+            else
+              bad |= 1 << pp;
+          }
+        }
+        if (lane == 0) {
+          if (bad) report(a.status, PKV_DEV_BAD_PAGE);
+          sm.kv_bad[st] = bad;
+          mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[2 * i] = o[2 * i] * keep + w * bf16_lo(vw[i]);
-        o[2 * i + 1] = o[2 * i + 1] * keep + w * bf16_hi(vw[i]);
+          for (int pp = 0; pp < kPagesPerBlock; ++pp)
+            tma_load_3d(sm.k[st] + pp * kBox, &a.tmap_k, 0, x.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
+#pragma unroll
+          for (int pp = 0; pp < kPagesPerBlock; ++pp)
+            tma_load_3d(sm.v[st] + pp * kBox, &a.tmap_v, 0, x.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
+        }
+        __syncwarp();
+      }
+      ++k;
+    }
+    // every copy issued has landed before the CTA exits
+    if (lane == 0) {
+      for (long long j = gb > kStages ? gb - kStages : 0; j < gb; ++j)
+        mbar_wait(&sm.kv_full[int(j % kStages)], uint32_t(j / kStages) & 1);
+      for (int j = k > 2 ? k - 2 : 0; j < k; ++j) mbar_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ================= MMA issuer (one thread issues, the warp waits) =================
+    long long gb = 0;         // blocks whose S was issued
+    bool pend = false;        // block gb - 1's products are still to issue
+    bool pend_first = false;  // ... and start a segment (O is overwritten, not accumulated)
+    int k = 0;
+    bool ok = true;
+    auto issue_pv = [&]() {
+      const long long pb_ = gb - 1;
+      const int b = int(pb_ & 1), st = int(pb_ % kStages);
+      const bool w = wait(sm, &sm.p_full[b], uint32_t(pb_ >> 1) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t vb = smem_addr(sm.v[st]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t pcol = tmem + b * kKeys + h * kHalf, ocol = tmem + kColO + h * kHeadDim;
+#pragma unroll
+          for (int term = 0; term < (kBf16 ? 1 : 2); ++term)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              tc_mma_tmem_a(ocol, pcol + term * 16 + kk * 8, sw128_desc(vb + (2 * h + kk) * 2048, 16, 1024), kIdescPV,
+                            (pend_first && term == 0 && kk == 0) ? 0u : 1u);
+        }
+        tc_commit(&sm.p_free[b]);
+        tc_commit(&sm.kv_empty[st]);
+      }
+      __syncwarp();
+      pend = false;
+      return true;
+    };
+    Segment x;
+    while (ok && walk.next(a, x)) {
+      const int qb = k & 1;
+      bool w = wait(sm, &sm.q_full[qb], uint32_t(k / 2) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) break;
+      const uint32_t q_base = smem_addr(sm.q[qb]);
+      for (int j = x.j0; j < x.j1; ++j) {
+        const int st = int(gb % kStages), b = int(gb & 1);
+        w = wait(sm, &sm.kv_full[st], uint32_t(gb / kStages) & 1, a.status);
+        if (w && gb >= 2) w = wait(sm, &sm.p_free[b], uint32_t(gb / 2 - 1) & 1, a.status);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t kb = smem_addr(sm.k[st]);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma(tmem + b * kKeys, sw128_desc(q_base + kk * 32, 16, 1024), sw128_desc(kb + kk * 32, 16, 1024),
+                   kIdescS, kk > 0 ? 1u : 0u);
+          tc_commit(&sm.s_full[b]);
+          if (j == x.j1 - 1) tc_commit(&sm.q_empty[qb]);  // the segment's last read of its Q
+        }
+        __syncwarp();
+        if (pend && !issue_pv()) {
+          ok = false;
+          break;
+        }
+        ++gb;
+        pend = true;
+        pend_first = j == x.j0;
+      }
+      ++k;
+    }
+    if (ok && pend) issue_pv();
+    // every MMA issued has completed before the tensor memory is freed
+    if (lane == 0) {
+      tc_commit(&sm.mma_done);
+      mbar_wait(&sm.mma_done, 0);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax: warp = (quarter of the lanes, half of each block's keys) =================
+    griddep_wait();  // the mask and every global write come after the kernel before this one
+    zero_invalid(tid, kSoftThreads);
+    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    const uint32_t my_tmem = tmem + (uint32_t(32 * quarter) << 16);
+    const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
+    long long gb = 0;
+    int k = 0, ends = 0;  // segments begun; segments this warp has ended (the warps of a quarter agree)
+    bool ok = true;
+    Segment x;
+    for (; ok && walk.next(a, x); ++k) {
+      const Seq &seq = walk.seq;
+      const int octet = (quarter - k - turn) & 3, t = min(kTok, seq.n - x.tile * kTok);
+      const int node = octet * kOctet + (lane >> 2);
+      const bool active = octet * kOctet < t, real = node < t;  // the warp's, this thread's row
+      const int base = seq.ctx - seq.n;
+      const long long qrow = (long long)seq.q0 + x.tile * kTok + (real ? node : 0);
+      const uint32_t *mask = a.mask + qrow * a.mask_stride;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int j = x.j0; j < x.j1; ++j, ++gb) {
+        const int b = int(gb & 1), st = int(gb % kStages);
+        // S of the block, and (already complete) its load, for V's check and the bad-page bits
+        bool w = wait(sm, &sm.s_full[b], uint32_t(gb >> 1) & 1, a.status) &&
+                 wait(sm, &sm.kv_full[st], uint32_t(gb / kStages) & 1, a.status);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        if ((j + 1) * kKeys > base) {
+          // the block holds nodes: four threads to a V row
+          const int r = tid >> 2, pos = j * kKeys + r, c0 = 2 * (tid & 3);
+          uint4 *p0 = reinterpret_cast<uint4 *>(sm.v[st] + r * kRowBytes + ((c0 ^ (r & 7)) << 4));
+          uint4 *p1 = reinterpret_cast<uint4 *>(sm.v[st] + r * kRowBytes + (((c0 + 1) ^ (r & 7)) << 4));
+          const bool inf = pos >= base && pos < seq.ctx && (nonfinite_chunk(*p0) || nonfinite_chunk(*p1));
+          const unsigned any = __ballot_sync(0xffffffffu, inf) >> (lane & ~3) & 0xfu;
+          if (pos >= seq.ctx || any) *p0 = *p1 = make_uint4(0u, 0u, 0u, 0u);
+          if (any) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
+          fence_proxy_async_smem();
+        }
+        if (active) {
+          tc_fence_after();
+          float s[32];
+          {
+            uint32_t u[32];
+            tmem_ld32(my_tmem + b * kKeys + half * kHalf, u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(u[i]);
+          }
+          if (a.neg) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = -s[i];
+          }
+          const int key0 = j * kKeys + half * kHalf;
+          const int bad = sm.kv_bad[st] >> (2 * half) & 3;
+          const bool masked = key0 + kHalf > base || bad != 0;  // uniform over the warp
+          uint32_t see = ~0u;
+          float mx;
+          if (masked) {
+            see = real ? window_bits(mask, key0, base, seq.ctx, seq.n) : 0u;
+            if (bad & 1) see &= 0xffff0000u;
+            if (bad & 2) see &= 0x0000ffffu;
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = see >> i & 1u ? s[i] : -INFINITY;
+            mx = max32(y);
+          } else {
+            mx = max32(s);
+          }
+          const bool move = mx > m + a.move_thresh || (m == -INFINITY && mx > m);
+          float alpha = 1.f;
+          if (move) {
+            alpha = m == -INFINITY ? 0.f : ex2_approx((m - mx) * a.scale_log2);
+            m = mx;
+            l2.x *= alpha;
+            l2.y *= alpha;
+          }
+          const float2 mc = make_float2(-m * a.scale_log2, -m * a.scale_log2);
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = fma_f32x2(make_float2(s[2 * i], s[2 * i + 1]), c2, mc);
+            float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            if (masked) {
+              p.x = see >> (2 * i) & 1u ? p.x : 0.f;
+              p.y = see >> (2 * i + 1) & 1u ? p.y : 0.f;
+            }
+            l2 = add_f32x2(l2, p);
+            hi[i] = pack_bf16x2(p.x, p.y);
+            if constexpr (!kBf16) {
+              const float2 r = sub_f32x2(p, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
+              lo[i] = pack_bf16x2(r.x, r.y);
+            }
+          }
+          tmem_st16(my_tmem + b * kKeys + half * kHalf, hi);
+          if constexpr (!kBf16) tmem_st16(my_tmem + b * kKeys + half * kHalf + 16, lo);
+          if (j > x.j0 && __any_sync(0xffffffffu, move)) {
+            // a reference moved: once the products before this block are done, rescale the row of O
+            w = wait(sm, &sm.p_free[b ^ 1], uint32_t((gb - 1) >> 1) & 1, a.status);
+            if (!__all_sync(0xffffffffu, w)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t o[32];
+              const uint32_t col = my_tmem + kColO + half * kHeadDim + 32 * i;
+              tmem_ld32(col, o);
+#pragma unroll
+              for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * alpha);
+              tmem_st32(col, o);
+            }
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[b]);
+      }
+      if (!ok) break;
+      // ---- the segment's end: the row's two states merge; this thread has dims 32 half .. + 31 ----
+      if (!active) continue;
+      const float2 mine_ml = make_float2(m, l2.x + l2.y);
+      sm.ml[ends & 1][half][row] = mine_ml;  // its place is written again after one more such barrier
+      named_barrier_sync(1 + quarter, 64);
+      const float2 other = sm.ml[ends++ & 1][half ^ 1][row];
+      const bool w = wait(sm, &sm.p_free[(gb - 1) & 1], uint32_t((gb - 1) >> 1) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float M = fmaxf(mine_ml.x, other.x);
+      const float w_mine = state_weight(mine_ml, M, a.scale_log2), w_other = state_weight(other, M, a.scale_log2);
+      float L = mine_ml.y * w_mine + other.y * w_other;
+      float r[32];
+      {
+        uint32_t u[32];
+        tmem_ld32(my_tmem + kColO + half * kHeadDim + half * 32, u);
+#pragma unroll
+        for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]) * w_mine;
+        tmem_ld32(my_tmem + kColO + (half ^ 1) * kHeadDim + half * 32, u);
+#pragma unroll
+        for (int d = 0; d < 32; ++d) r[d] += __uint_as_float(u[d]) * w_other;
+      }
+      tc_fence_before();  // these reads come before the next segment's products (ordered by p_full)
+      const int h = x.g * kGroup + (lane & 3);
+      if (*reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k && real) {
+        // nodes whose V holds a NaN or an infinity were zeroed for the product: the rows that see
+        // them add p V here
+        const int32_t *table = a.block_tables + (long long)x.s * a.bt_stride;
+        for (int pos = max(base, x.j0 * kKeys); pos < min(seq.ctx, x.j1 * kKeys); ++pos) {
+          const int page = __ldg(table + pos / kPageTokens), nd = pos - base;
+          if (page < 0 || page >= a.num_pages || !(__ldg(mask + (nd >> 5)) >> (nd & 31) & 1u)) continue;
+          const long long at = (long long)page * a.page_stride + (x.g * kPageTokens + pos % kPageTokens) * kRowBytes;
+          const uint4 *vrow = reinterpret_cast<const uint4 *>(a.v_base + at);
+          bool inf = false;
+          for (int i = 0; i < 8; ++i) inf |= nonfinite_chunk(vrow[i]);
+          if (!inf) continue;
+          const uint32_t *krow = reinterpret_cast<const uint32_t *>(a.k_base + at);
+          const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + (qrow * kQHeads + h) * kHeadDim);
+          float dot = 0.f;
+          for (int i = 0; i < kHeadDim / 2; ++i)
+            dot += bf16_lo(q[i]) * bf16_lo(krow[i]) + bf16_hi(q[i]) * bf16_hi(krow[i]);
+          const float p = ex2_approx(((a.neg ? -dot : dot) - M) * a.scale_log2);
+          const uint32_t *v = reinterpret_cast<const uint32_t *>(vrow) + half * 16;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            r[2 * i] += p * bf16_lo(v[i]);
+            r[2 * i + 1] += p * bf16_hi(v[i]);
+          }
+        }
+      }
+      const long long out_at = (qrow * kQHeads + h) * kHeadDim + half * 32;
+      if (x.j0 == 0 && x.j1 == seq.nb) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int d = 0; d < 32; ++d) r[d] *= inv;
+        if (real) write_row<kBf16>(a, out_at, r);
+        continue;
+      }
+      // ---- cut unit: a partial state, then the ticket of (unit, warp's lanes and dims) ----
+      {
+        Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
+        if (real) {
+          float4 *dst = reinterpret_cast<float4 *>(&part.o[octet * 32 + lane][half * 32]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) __stcg(dst + i, make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+          if (half == 0) __stcg(&part.ml[octet * 32 + lane], make_float2(M, L));
+        }
+      }
+      // both halves read the row sums that half 0 stores: its stores come before either ticket
+      named_barrier_sync(1 + quarter, 64);
+      const int c0 = cta_of_block(x.unit0, T, Gu), c1 = cta_of_block(x.unit0 + seq.nb - 1, T, Gu);
+      int last = 0;
+      if (lane == 0) {
+        __threadfence();
+        int *ticket = a.tickets + (((long long)x.s * a.max_tiles + x.tile) * kKvHeads + x.g) * kSoftWarps + octet * 2 + half;
+        last = atomic_add_acq_rel_gpu(ticket, 1) == c1 - c0;
+        if (last) atomicExch(ticket, 0);  // ready for the next call
+      }
+      last = __shfl_sync(0xffffffffu, last, 0);
+      if (!last) continue;
+      __syncwarp();
+      M = -INFINITY;
+      L = 0.f;
+#pragma unroll
+      for (int d = 0; d < 32; ++d) r[d] = 0.f;
+      if (real) {
+        for (int c = c0; c <= c1; ++c) {
+          const Part &part = a.parts[2 * c + (c == c0 ? 1 : 0)];
+          const float2 ml = __ldcg(&part.ml[octet * 32 + lane]);
+          const float4 *src = reinterpret_cast<const float4 *>(&part.o[octet * 32 + lane][half * 32]);
+          const float Mn = fmaxf(M, ml.x);
+          const float keep = state_weight(make_float2(M, L), Mn, a.scale_log2), wgt = state_weight(ml, Mn, a.scale_log2);
+          L = L * keep + ml.y * wgt;
+          M = Mn;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = __ldcg(src + i);
+            r[4 * i] = r[4 * i] * keep + y.x * wgt;
+            r[4 * i + 1] = r[4 * i + 1] * keep + y.y * wgt;
+            r[4 * i + 2] = r[4 * i + 2] * keep + y.z * wgt;
+            r[4 * i + 3] = r[4 * i + 3] * keep + y.w * wgt;
+          }
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int d = 0; d < 32; ++d) r[d] *= inv;
+        write_row<kBf16>(a, out_at, r);
       }
     }
   }
-  if (!real) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] *= inv;
-  write((long long)q0 + node, o);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+constexpr int kMaxSeqs = 1 << 24, kMaxNodes = 1 << 20;
+
+size_t ticket_bytes(int num_seqs, int max_tiles) {
+  return (size_t(num_seqs) * size_t(max_tiles) * kKvHeads * kSoftWarps * sizeof(int32_t) + 127) / 128 * 128;
+}
+// The partial states come first: their place does not depend on the call's shape, and tickets return to zero.
+size_t workspace_size(int num_seqs, int max_tiles) {
+  return 2 * size_t(kMaxCtas) * sizeof(Part) + ticket_bytes(num_seqs, max_tiles);
+}
+
+// The kernels' shared-memory limit, set once per device.
+int setup_attributes() {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return PKV_ERR_CUDA;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return PKV_OK;
+  constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if (cudaFuncSetAttribute(tree_attention_kernel<false>, attr, int(kSmemBytes)) != cudaSuccess ||
+      cudaFuncSetAttribute(tree_attention_kernel<true>, attr, int(kSmemBytes)) != cudaSuccess) {
+    cudaGetLastError();
+    return PKV_ERR_CUDA;
+  }
+  done[dev] = true;
+  return PKV_OK;
 }
 
 }  // namespace
 }  // namespace pkv
 
 extern "C" size_t pkv_tree_workspace_bytes(int num_seqs, int max_query, int num_q_heads, int head_dim) {
-  if (num_seqs < 0 || max_query < 0 || num_q_heads != pkv::kQHeads || head_dim != pkv::kHeadDim) return 0;
-  const size_t tiles = (size_t(max_query) + pkv::kTreeTok - 1) / pkv::kTreeTok;
-  const size_t counters = (size_t(num_seqs) * tiles * pkv::kKvHeads * sizeof(int32_t) + 127) / 128 * 128;
-  return counters + 2 * size_t(pkv::kTreeMaxCtas) * pkv::kTreeSlotBytes;
+  if (num_seqs < 0 || num_seqs > pkv::kMaxSeqs || max_query < 0 || max_query > pkv::kMaxNodes ||
+      num_q_heads != pkv::kQHeads || head_dim != pkv::kHeadDim)
+    return 0;
+  return pkv::workspace_size(num_seqs, max_query / pkv::kTok + (max_query % pkv::kTok != 0));
 }
 
 extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
@@ -151,15 +798,14 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
                                         float scale, void *workspace, size_t workspace_bytes, int32_t *device_status,
                                         unsigned flags, void *stream) {
   if (flags & ~unsigned(PKV_OVERLAP_PREVIOUS | PKV_OUT_BF16)) return PKV_ERR_SHAPE;
-  const int rc = pkv::check_pool(pool);
+  int rc = pkv::check_pool(pool);
   if (rc != PKV_OK) return rc;
   if (num_q_heads != pkv::kQHeads) return PKV_ERR_UNSUPPORTED;
   if (num_seqs < 0 || max_query < 0 || max_context < 0 || block_table_stride < 0 || num_q_rows < 0 ||
-      mask_stride < 0 || mask_stride > (1 << 24) || mask_stride * 32 < max_query)
+      num_seqs > pkv::kMaxSeqs || max_query > pkv::kMaxNodes || mask_stride < 0 || mask_stride > (1 << 26) ||
+      mask_stride * 32 < max_query)
     return PKV_ERR_SHAPE;
   if (num_seqs == 0 || max_query == 0 || num_q_rows == 0) return PKV_OK;
-  const long long tiles = (max_query + pkv::kSimpleNodes - 1) / pkv::kSimpleNodes;
-  if (tiles > 65535) return PKV_ERR_SHAPE;
   if (out == nullptr || q == nullptr || query_start == nullptr || tree_mask == nullptr || block_tables == nullptr ||
       context_lens == nullptr || workspace == nullptr)
     return PKV_ERR_NULL;
@@ -168,9 +814,15 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
       ((reinterpret_cast<uintptr_t>(query_start) | reinterpret_cast<uintptr_t>(tree_mask) |
         reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u))
     return PKV_ERR_ALIGN;
-  if (workspace_bytes < pkv_tree_workspace_bytes(num_seqs, max_query, num_q_heads, pkv::kHeadDim))
-    return PKV_ERR_WORKSPACE;
+  const int tiles = max_query / pkv::kTok + (max_query % pkv::kTok != 0);
+  if (workspace_bytes < pkv::workspace_size(num_seqs, tiles)) return PKV_ERR_WORKSPACE;
+  rc = pkv::setup_attributes();
+  if (rc != PKV_OK) return rc;
   pkv::TreeArgs a;
+  rc = pkv::pool_tensor_maps(pool, pkv::kPageTokens, &a.tmap_k, &a.tmap_v);
+  if (rc != PKV_OK) return rc;
+  rc = pkv::query_tensor_map(q, num_q_rows, pkv::kQHeads, pkv::kHeadDim, pkv::kGroup, pkv::kOctet, &a.tmap_q);
+  if (rc != PKV_OK) return rc;
   a.k_base = static_cast<const uint8_t *>(pool->k_base);
   a.v_base = static_cast<const uint8_t *>(pool->v_base);
   a.page_stride = pool->page_stride_bytes;
@@ -187,10 +839,35 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   a.num_seqs = num_seqs;
   a.max_query = max_query;
   a.max_context = max_context;
-  a.scale_log2 = scale * pkv::kLog2e;
-  a.out_bf16 = (flags & PKV_OUT_BF16) ? 1 : 0;
+  a.max_tiles = tiles;
+  a.scale_log2 = fabsf(scale) * pkv::kLog2e;
+  a.move_thresh = a.scale_log2 > 0.f ? pkv::kRescaleLog2 / a.scale_log2 : INFINITY;
+  a.neg = scale < 0.f ? 1 : 0;
+  a.parts = static_cast<pkv::Part *>(workspace);
+  a.tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + 2 * size_t(pkv::kMaxCtas) * sizeof(pkv::Part));
   a.status = device_status;
-  const dim3 grid(unsigned(num_seqs), pkv::kKvHeads, unsigned(tiles));
-  pkv::tree_attention_kernel<<<grid, pkv::kSimpleThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
+  // no more CTAs than the list can have shares of kMinBlocks blocks
+  const double blocks = double(num_seqs) * tiles * pkv::kKvHeads * (max_context / pkv::kKeys + 1);
+  const int sms = pkv::device_sm_count();
+  long long grid = (long long)(sms > 0 ? sms : 152) * pkv::kCtasPerSm;
+  if (grid > pkv::kMaxCtas) grid = pkv::kMaxCtas;
+  if (double(grid) > blocks / pkv::kMinBlocks) grid = (long long)(blocks / pkv::kMinBlocks);
+  if (grid < 1) grid = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(pkv::kThreads);
+  cfg.dynamicSmemBytes = pkv::kSmemBytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = (flags & PKV_OVERLAP_PREVIOUS) ? 1 : 0;
+  const cudaError_t err = (flags & PKV_OUT_BF16) ? cudaLaunchKernelEx(&cfg, pkv::tree_attention_kernel<true>, a)
+                                                 : cudaLaunchKernelEx(&cfg, pkv::tree_attention_kernel<false>, a);
+  if (err != cudaSuccess) {
+    cudaGetLastError();
+    return PKV_ERR_LAUNCH;
+  }
+  return PKV_OK;
 }
