@@ -129,10 +129,18 @@ def status_string(code: int) -> str:
     return _lib.pkv_status_string(int(code)).decode()
 
 
+# The current stream's handle and the current device without the Stream object that
+# torch.cuda.current_stream() builds (2.9 us a call on the Grace host, against 0.2 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return int(stream.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(_current_device())
+    return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -279,19 +287,20 @@ def paged_decode_attention_noalloc(pool: KVPool | PkvPool, out: torch.Tensor, q:
     _check("pkv_paged_decode_attention_noalloc", rc)
 
 
-def _require(where: str, device: torch.device, dtype, *tensors: torch.Tensor) -> None:
-    """The tensors' pointers are what the kernel will see: their type, order and device have to be right."""
+def _device_of(where: str, t: torch.Tensor) -> int:
+    """Index of t's device, which has to be the current one (a stream and a launch belong to that)."""
+    d = t.get_device()
+    if d < 0 or d != _current_device():
+        raise ValueError(f"{where}: tensors on {t.device}, but the current device is cuda:{_current_device()}")
+    return d
+
+
+def _require(where: str, device: int, dtype, *tensors: torch.Tensor) -> None:
+    """The kernel sees pointers only: the tensors' type, order and device have to be what it takes them for."""
     for t in tensors:
-        if t.dtype is not dtype or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{where}: expected a contiguous {dtype} tensor on {device}, got {t.dtype} on {t.device} "
-                             f"with strides {tuple(t.stride())}")
-
-
-def _device_of(where: str, t: torch.Tensor) -> torch.device:
-    device = t.device
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return device
+        if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{where}: expected a contiguous {dtype} tensor on cuda:{device}, got {t.dtype} on "
+                             f"{t.device} with strides {tuple(t.stride())}")
 
 
 def tree_workspace_bytes(num_seqs: int, max_query: int, num_q_heads: int = 32, head_dim: int = 64) -> int:
@@ -320,16 +329,15 @@ def paged_tree_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Ten
     _require(where, device, torch.bfloat16, q)
     _require(where, device, torch.bfloat16 if bf16_out else torch.float32, out)
     _require(where, device, torch.int32, query_start, tree_mask, context_lens)
-    num_seqs = int(context_lens.shape[0])
-    rows = min(int(q.shape[0]), int(out.shape[0]), int(tree_mask.shape[0]))
-    if q.dim() != 3 or out.shape[1:] != q.shape[1:] or tree_mask.dim() != 2 or query_start.shape[0] != num_seqs + 1:
+    num_seqs, shape, out_shape, mask_shape = context_lens.numel(), q.shape, out.shape, tree_mask.shape
+    if len(shape) != 3 or out_shape[1:] != shape[1:] or len(mask_shape) != 2 or query_start.numel() != num_seqs + 1:
         raise ValueError(f"{where}: q and out are [rows, heads, dim], tree_mask [rows, words], query_start [seqs + 1]")
+    rows = min(shape[0], out_shape[0], mask_shape[0])
     flags = (OVERLAP_PREVIOUS if overlap_previous else 0) | (OUT_BF16 if bf16_out else 0)
     _check(where, _lib.pkv_paged_tree_attention(
-        ctypes.byref(desc), _ptr(out), _ptr(q), int(q.shape[1]), rows, _ptr(query_start), _ptr(tree_mask),
-        int(tree_mask.shape[1]), _ptr(block_tables), block_table_stride, _ptr(context_lens), num_seqs, max_query,
-        max_context, scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status), flags,
-        _stream(stream)))
+        ctypes.byref(desc), out.data_ptr(), q.data_ptr(), shape[1], rows, query_start.data_ptr(), tree_mask.data_ptr(),
+        mask_shape[1], block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_query,
+        max_context, scale, workspace.data_ptr(), workspace.nbytes, _ptr(status), flags, _stream(stream)))
 
 
 def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_stride: int, layer_stride: int,
@@ -343,19 +351,18 @@ def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_
     desc = pool.desc if isinstance(pool, KVPool) else pool
     device = _device_of(where, context_lens)
     _require(where, device, torch.int32, query_start, context_lens, accepted, accept_counts)
-    num_seqs = int(context_lens.shape[0])
-    if accepted.dim() != 2 or accepted.shape[0] != num_seqs or accept_counts.shape[0] != num_seqs or \
-            query_start.shape[0] != num_seqs + 1:
+    num_seqs, shape = context_lens.numel(), accepted.shape
+    if len(shape) != 2 or shape[0] != num_seqs or accept_counts.numel() != num_seqs or \
+            query_start.numel() != num_seqs + 1:
         raise ValueError(f"{where}: accepted is [seqs, width], accept_counts [seqs], query_start [seqs + 1]")
     if new_context_lens is not None:
         _require(where, device, torch.int32, new_context_lens)
-        if new_context_lens.shape[0] < num_seqs:
-            raise ValueError(f"{where}: new_context_lens has {new_context_lens.shape[0]} entries for {num_seqs} sequences")
-    width = int(accepted.shape[1])
+        if new_context_lens.numel() < num_seqs:
+            raise ValueError(f"{where}: new_context_lens has {new_context_lens.numel()} entries for {num_seqs} sequences")
     _check(where, _lib.pkv_tree_commit(
-        ctypes.byref(desc), _ptr(block_tables), block_table_stride, layer_stride, num_layers, _ptr(query_start),
-        _ptr(context_lens), _ptr(accepted), width, _ptr(accept_counts), num_seqs, width, max_context,
-        _ptr(new_context_lens), _ptr(status), _stream(stream)))
+        ctypes.byref(desc), block_tables.data_ptr(), block_table_stride, layer_stride, num_layers,
+        query_start.data_ptr(), context_lens.data_ptr(), accepted.data_ptr(), shape[1], accept_counts.data_ptr(),
+        num_seqs, shape[1], max_context, _ptr(new_context_lens), _ptr(status), _stream(stream)))
 
 
 def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: torch.Tensor,
@@ -363,14 +370,14 @@ def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: to
     """Copy page src_pages[i] onto page dst_pages[i] (int32; a negative id is padding), K and V."""
     where = "pkv_kv_copy_pages"
     desc = pool.desc if isinstance(pool, KVPool) else pool
+    n = src_pages.numel()
     for t in (src_pages, dst_pages):
-        if t.dtype is not torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{where}: page ids are contiguous int32 tensors")
-    n = int(src_pages.shape[0])
-    if dst_pages.shape[0] != n:
-        raise ValueError(f"{where}: {n} source pages, {dst_pages.shape[0]} destinations")
-    _check(where, _lib.pkv_kv_copy_pages(ctypes.byref(desc), _ptr(src_pages), _ptr(dst_pages), n, _ptr(status),
-                                         _stream(stream)))
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{where}: page ids are contiguous int32 tensors, as many sources as destinations")
+        if t.get_device() not in (-1, _current_device()):
+            raise ValueError(f"{where}: page ids on {t.device}, but the current device is cuda:{_current_device()}")
+    _check(where, _lib.pkv_kv_copy_pages(ctypes.byref(desc), src_pages.data_ptr(), dst_pages.data_ptr(), n,
+                                         _ptr(status), _stream(stream)))
 
 
 class Allocator:

@@ -212,6 +212,13 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   return p;
 }
 
+// True in one thread of the warp, the same one each time (all 32 lanes call).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- tcgen05: 5th-generation tensor cores with tensor-memory (TMEM) accumulators ----
 // TMEM addresses: bits 31..16 lane, bits 15..0 column (32-bit cells).  A warp may
 // touch only lanes 32 * (warp % 4) .. + 31.
@@ -289,6 +296,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "memory");
 }
 
+// The same, not waited for: v may be used after tmem_ld_wait(v), which the compiler sees write it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
+      : "r"(taddr)
+      : "memory");
+}
+
+#define PKV_RW8(i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
+                   "+r"(v[i + 6]), "+r"(v[i + 7])
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_RW8(0), PKV_RW8(8), PKV_RW8(16), PKV_RW8(24) : : "memory");
+}
+#undef PKV_RW8
+
 // Stores 32 consecutive columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -299,15 +323,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
-// Stores 16 consecutive columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// Stores 16 consecutive columns of this thread's TMEM lane; complete after tmem_st_wait().
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "%15, %16};" ::"r"(taddr),
       PKV_S8(0), PKV_S8(8)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 #undef PKV_R8
 #undef PKV_S8
 

@@ -12,7 +12,7 @@
 //    every K/V row loaded: M = 128.  Keys in blocks of 64 (4 pages).
 //  * Work split: the key blocks of all units form one list; the grid's CTAs (two per SM) take equal
 //    shares of it, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
-//    state (m, l, O) per CTA in the workspace, and the warp that takes the last of its tickets (an
+//    state (m, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
 //    atomic counter, nobody waits) merges them.
 //  * Warp roles (320 threads): 8 softmax warps, a loader (tiled TMA: Q as boxes of 8 nodes x 4 heads,
 //    two buffers; head g's 16 rows of each page as 2 KiB boxes into a ring of 4 blocks), an MMA issuer.
@@ -24,8 +24,11 @@
 //  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits; two
 //    products); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
 //    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
-//  * A row's reference moves only when a block's maximum exceeds it by more than 8 (a factor 256); then
-//    the row of O is rescaled in TMEM, after the product before it completed.
+//  * The reference only has to keep the weights in range (their precision is relative), so most blocks
+//    take no maximum: the weights are computed from the reference at hand, and only where a thread's sum over
+//    the block exceeds 2^16, where no reference is known yet or where keys are masked is the block's
+//    maximum taken; the reference moves when that exceeds it by more than 8 (a factor 256), and the row
+//    of O is rescaled in TMEM, after the product before it completed.
 //  * Masks: a key a row may not see gets weight 0 by selection, so a NaN score stays out.  V rows at or
 //    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
 //    NaN or an infinity (0 * NaN in the product would reach every row); the rows that see such a node add
@@ -65,14 +68,15 @@ constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColO = 2 * kKeys;               // S buffers at columns 0 and 64, O_a at 128, O_b at 192
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;
+constexpr float kSumLimit = 65536.f;
 
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, false);     // B = K rows (K-major)
 constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows (MN-major)
 
 // Partial state of one (CTA, unit) pair.
 struct Part {
-  float o[kRows][kHeadDim];
-  float2 ml[kRows];
+  float4 o[kHeadDim / 4][kRows];  // [4 dims][row]: neighbouring lanes hold neighbouring rows
+  float2 ml[kRows];               // (reference, sum) of a row
 };
 
 struct TreeArgs {
@@ -95,33 +99,11 @@ struct TreeArgs {
   int max_tiles;      // units a sequence may have per K/V head
   float scale_log2;   // |scale| * log2(e)
   float move_thresh;  // scores (unscaled) by which a block's max must pass the reference to move it
-  int neg;            // scale < 0: the scores are negated
-  int *tickets;       // [num_seqs * max_tiles * 8 heads][8 warps], 0 between calls
+  int neg;            // scale < 0: a row's reference is the largest -s (sigma = -1)
+  int *tickets;       // [num_seqs * max_tiles][8 heads], 0 between calls
   Part *parts;        // [2 * kMaxCtas]
   int32_t *status;
 };
-
-struct __align__(1024) Smem {
-  uint8_t q[2][kRows * kRowBytes];
-  uint8_t k[kStages][kTileBytes];
-  uint8_t v[kStages][kTileBytes];
-  float2 ml[2][2][kRows];  // [turn][half]: a row's (reference, sum), exchanged at a segment's end
-  uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2];
-  uint64_t p_full[2];  // every softmax warp has written its P of the buffer (and is done with what it replaces)
-  uint64_t p_free[2];  // the products of a block are done: its buffer may be written, O read
-  uint64_t mma_done;
-  int kv_bad[kStages];     // bit pp: page pp of the stage's block is invalid (loaded as zeros)
-  int nonfinite[4];        // [segment % 4]: the last segment in which a node's V was zeroed (the softmax
-                           // warps are never more than two segments apart: a block's S waits for the P two before)
-  long long sums[kThreads / 32];
-  long long total, first;  // blocks in the list; global index of seq0's first block
-  int seq0, found;
-  uint32_t tmem_base;
-  int abort;
-};
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 
 // A sequence's lengths and what it asks for: tiles of 32 nodes, blocks of 64 keys.  Sequences with no
 // nodes, and those whose lengths do not fit, have no blocks.
@@ -145,17 +127,21 @@ struct Seq {
 };
 
 // A CTA's share of one unit: key blocks j0 .. j1 - 1 of (sequence, K/V head, tile).  List order:
-// sequence, head, tile, block.
+// sequence, head, tile, block.  The loader walks the list and passes the segments on in shared memory.
 struct Segment {
-  int s, g, tile, j0, j1;
-  long long unit0;  // the list index of the unit's block 0
+  int s, g, tile, j0, j1;  // s < 0: there are no more
+  int q0, n, ctx, nb;      // the sequence's
+  long long unit0;         // the list index of the unit's block 0
 };
+constexpr int kSegments = 8;  // places for segments; the roles are never more than four segments apart
 
+// Walk over the segments of a CTA's share.
 struct Walk {
-  long long pos, end, first;  // list position, end of the CTA's share, first block of sequence s
+  long long pos, end, first;  // list position, end of the share, first block of sequence s
   int s;
   Seq seq;
   __device__ bool next(const TreeArgs &a, Segment &x) {
+    x.s = -1;
     if (pos >= end) return false;
     while (pos - first >= seq.blocks()) {
       first += seq.blocks();
@@ -165,6 +151,10 @@ struct Walk {
     x.s = s;
     x.g = int(u / seq.tiles);
     x.tile = int(u % seq.tiles);
+    x.q0 = seq.q0;
+    x.n = seq.n;
+    x.ctx = seq.ctx;
+    x.nb = seq.nb;
     x.unit0 = first + u * seq.nb;
     x.j0 = int(pos - x.unit0);
     x.j1 = int(min((long long)seq.nb, x.j0 + (end - pos)));
@@ -173,26 +163,114 @@ struct Walk {
   }
 };
 
+struct __align__(1024) Smem {
+  uint8_t q[2][kRows * kRowBytes];
+  uint8_t k[kStages][kTileBytes];
+  uint8_t v[kStages][kTileBytes];
+  float2 ml[2][2][kRows];  // [turn][half]: a row's (reference, sum), exchanged at a segment's end
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2];
+  uint64_t p_full[2];  // every softmax warp has written its P of the buffer (and is done with what it replaces)
+  uint64_t p_free[2];  // the products of a block are done: its buffer may be written, O read
+  uint64_t seg_full[kSegments];
+  uint64_t mma_done;
+  Segment seg[kSegments];
+  Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
+  int merge[2];     // this CTA took the last ticket
+  int kv_bad[kStages];     // bit pp: page pp of the stage's block is invalid (loaded as zeros)
+  int nonfinite[4];        // [segment % 4]: the last segment in which a node's V was zeroed (the softmax
+                           // warps are never more than two segments apart: a block's S waits for the P two before)
+  long long sums[kThreads / 32];
+  long long total, first;  // blocks in the list; global index of seq0's first block
+  int seq0, found;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+
 // CTA that owns block p of the list when T blocks are split over G CTAs.
 __device__ __forceinline__ int cta_of_block(long long p, long long T, int G) { return int(((p + 1) * G - 1) / T); }
 
-// Bounded wait that gives up at once when another role has already aborted; true when the phase completed.
-__device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (*reinterpret_cast<volatile int *>(&sm.abort)) return false;
-  if (mbar_wait(bar, parity)) return true;
-  *reinterpret_cast<volatile int *>(&sm.abort) = 1;
-  report(status, PKV_DEV_TIMEOUT);
-  return false;
+// Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitCycles) return false;
+  return true;
 }
 
-// Largest of 32 values: a tree of three-input max.
-__device__ __forceinline__ float max32(const float (&x)[32]) {
-  float m[11];
+// The same for a role's waits: gives up when another role has aborted, and makes the others do so.
+__device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int *>(&sm.abort)) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+      report(status, PKV_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// P = 2^((s - sigma m) c) of a thread's 32 keys as bf16 terms, two keys to a word: hi, and with fp32 output lo.
+// `sum` takes the fp32 weights.  With kMasked a key whose bit in `see` is clear gets 0 by selection (its
+// score may be NaN).
+template <bool kBf16, bool kMasked>
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t see, float2 c2, float2 mc, float2 &sum,
+                                        uint32_t (&hi)[16], uint32_t (&lo)[16]) {
 #pragma unroll
-  for (int i = 0; i < 10; ++i) m[i] = max3f(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
-  m[10] = fmaxf(x[30], x[31]);
-  const float a = max3f(m[0], m[1], m[2]), b = max3f(m[3], m[4], m[5]), c = max3f(m[6], m[7], m[8]);
-  return max3f(max3f(a, b, c), m[9], m[10]);
+  for (int i = 0; i < 16; ++i) {
+    const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, mc);
+    float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+    if (kMasked) {
+      p.x = see >> (2 * i) & 1u ? p.x : 0.f;
+      p.y = see >> (2 * i + 1) & 1u ? p.y : 0.f;
+    }
+    sum = add_f32x2(sum, p);
+    hi[i] = pack_bf16x2(p.x, p.y);
+    if constexpr (!kBf16) {
+      const float2 r = sub_f32x2(p, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
+      lo[i] = pack_bf16x2(r.x, r.y);
+    }
+  }
+}
+
+// P over its S in tensor memory: hi in the first 16 columns, lo in the next.
+template <bool kBf16>
+__device__ __forceinline__ void store_weights(uint32_t taddr, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+  tmem_st16_async(taddr, hi);
+  if constexpr (!kBf16) tmem_st16_async(taddr + 16, lo);
+  tmem_st_wait();
+}
+
+// A block half whose keys not every row sees (`see`: the row's), whose reference m is still to be found, or too
+// far below: takes the maximum, moves the reference, computes and stores the weights.  Returns the
+// reference, the factor 2^((m_old - m) |c|) for what was summed before, and the weights' sums.
+template <bool kBf16>
+__device__ __forceinline__ float4 careful_block(uint32_t taddr, uint32_t see, float m, float c, float move_thresh) {
+  uint32_t s[32];
+  tmem_ld32(taddr, s);
+  float mx = -INFINITY;  // in units of sigma * s
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float y = __uint_as_float(s[i]);
+    mx = fmaxf(mx, see >> i & 1u ? (c < 0.f ? -y : y) : -INFINITY);
+  }
+  float alpha = 1.f;
+  if (mx > m + move_thresh || (m == -INFINITY && mx > m)) {
+    alpha = m == -INFINITY ? 0.f : ex2_approx((m - mx) * fabsf(c));
+    m = mx;
+  }
+  float2 sum = make_float2(0.f, 0.f);
+  uint32_t hi[16], lo[16];
+  weights<kBf16, true>(s, see, make_float2(c, c), make_float2(-m * fabsf(c), -m * fabsf(c)), sum, hi, lo);
+  store_weights<kBf16>(taddr, hi, lo);
+  return make_float4(m, alpha, sum.x, sum.y);
 }
 
 // The keys of a 32-key window starting at position key0 that a row may see: the prefix, then the nodes
@@ -226,19 +304,22 @@ __device__ __forceinline__ float state_weight(float2 ml, float M, float c) {
   return ml.y == 0.f ? 0.f : ex2_approx((ml.x - M) * c);
 }
 
-// Writes 32 dims of a row.
-template <bool kBf16>
-__device__ __forceinline__ void write_row(const TreeArgs &a, long long at, const float (&r)[32]) {
-  if constexpr (kBf16) {
+// Writes kDims dims of a row.
+template <bool kBf16, int kDims>
+__device__ __forceinline__ void write_row(const TreeArgs &a, long long at, const float (&r)[kDims]) {
+  if constexpr (kBf16 && kDims == 4) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+        make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+  } else if constexpr (kBf16) {
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kDims / 8; ++i)
       dst[i] = make_uint4(pack_bf16x2(r[8 * i], r[8 * i + 1]), pack_bf16x2(r[8 * i + 2], r[8 * i + 3]),
                           pack_bf16x2(r[8 * i + 4], r[8 * i + 5]), pack_bf16x2(r[8 * i + 6], r[8 * i + 7]));
   } else {
     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dst[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    for (int i = 0; i < kDims / 4; ++i) dst[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
   }
 }
 
@@ -246,7 +327,8 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp index by a shuffle: the compiler then knows that a role's values are the same in all lanes
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = int(gridDim.x), cta = int(blockIdx.x);
 
   // ---- blocks in the list, and this CTA's share of them ----
@@ -272,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       mbar_init(&sm.kv_full[i], 1);
       mbar_init(&sm.kv_empty[i], 1);
     }
+    for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1);
     mbar_init(&sm.mma_done, 1);
     sm.abort = 0;
     sm.found = 0;
@@ -342,12 +425,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   griddep_launch_dependents();  // a kernel that starts beside this one finds what tensor memory is left
-  Walk walk;
-  walk.pos = pa;
-  walk.end = pb;
-  walk.first = sm.first;
-  walk.s = sm.seq0;
-  walk.seq.load(a, walk.s);
   // Small trees fill the lanes of one warp only: units start at another quarter of the lanes each, so
   // that the quarters (the SM's sub-partitions) share the work.
   const int turn = cta * 2 >= G ? 2 : 0;
@@ -360,21 +437,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       prefetch_tensormap(&a.tmap_v);
       prefetch_tensormap(&a.tmap_q);
     }
-    long long gb = 0;  // blocks issued
+    Walk walk;
+    walk.pos = pa;
+    walk.end = pb;
+    walk.first = sm.first;
+    walk.s = sm.seq0;
+    walk.seq.load(a, walk.s);
+    unsigned gb = 0;   // blocks issued
     int k = 0;         // segments started
     bool ok = true, waited = false;
     Segment x;
-    while (ok && walk.next(a, x)) {
-      const int t = min(kTok, walk.seq.n - x.tile * kTok), octets = (t + kOctet - 1) / kOctet, qb = k & 1;
+    while (ok) {
+      const bool more = walk.next(a, x);
+      const int qb = k & 1;
       if (k >= 2) {
         const bool w = wait(sm, &sm.q_empty[qb], uint32_t(k / 2 - 1) & 1, a.status);
         if (!__all_sync(0xffffffffu, w)) break;
       }
       if (lane == 0) {
+        sm.seg[k % kSegments] = x;
+        mbar_arrive(&sm.seg_full[k % kSegments]);
+      }
+      __syncwarp();
+      if (!more) break;
+      const int t = min(kTok, x.n - x.tile * kTok), octets = (t + kOctet - 1) / kOctet;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&sm.q_full[qb], uint32_t(octets * kOctetBytes));
         for (int o = 0; o < octets; ++o)
           tma_load_3d(sm.q[qb] + ((o + k + turn) & 3) * kOctetBytes, &a.tmap_q, 0, x.g * kGroup,
-                      walk.seq.q0 + x.tile * kTok + o * kOctet, &sm.q_full[qb], once);
+                      x.q0 + x.tile * kTok + o * kOctet, &sm.q_full[qb], once);
       }
       __syncwarp();
       // launched with overlap (PKV_OVERLAP_PREVIOUS), the kernel before this one may still be writing
@@ -383,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       waited = true;
       // block-table entries 32 at a time (8 blocks), the next 32 in flight
       const int32_t *table = a.block_tables + (long long)x.s * a.bt_stride;
-      const int npages = (walk.seq.ctx - 1) / kPageTokens + 1, p0 = x.j0 * kPagesPerBlock;
+      const int npages = (x.ctx - 1) / kPageTokens + 1, p0 = x.j0 * kPagesPerBlock;
       const uint64_t policy = walk.seq.tiles > 1 ? again : once;  // several tiles read the same K/V
       auto entries = [&](int p) { return p + lane < npages ? __ldg(table + p + lane) : -1; };
       int ent = entries(p0), ent_next = entries(p0 + 32);
@@ -394,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           ent_next = entries(j * kPagesPerBlock + 32);
         }
         if (gb >= kStages) {
-          const bool w = wait(sm, &sm.kv_empty[st], uint32_t(gb / kStages - 1) & 1, a.status);
+          const bool w = wait(sm, &sm.kv_empty[st], (gb / kStages - 1) & 1, a.status);
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
@@ -412,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
               bad |= 1 << pp;
           }
         }
-        if (lane == 0) {
+        if (elect_one()) {
           if (bad) report(a.status, PKV_DEV_BAD_PAGE);
           sm.kv_bad[st] = bad;
           mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
@@ -429,26 +520,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     }
     // every copy issued has landed before the CTA exits
     if (lane == 0) {
-      for (long long j = gb > kStages ? gb - kStages : 0; j < gb; ++j)
-        mbar_wait(&sm.kv_full[int(j % kStages)], uint32_t(j / kStages) & 1);
-      for (int j = k > 2 ? k - 2 : 0; j < k; ++j) mbar_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
+      for (unsigned j = gb > kStages ? gb - kStages : 0; j < gb; ++j)
+        bounded_wait(&sm.kv_full[j % kStages], (j / kStages) & 1);
+      for (int j = k > 2 ? k - 2 : 0; j < k; ++j) bounded_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ================= MMA issuer (one thread issues, the warp waits) =================
-    long long gb = 0;         // blocks whose S was issued
+    const uint64_t q_desc = sw128_desc(smem_addr(sm.q), 16, 1024), k_desc = sw128_desc(smem_addr(sm.k), 16, 1024),
+                   v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);  // a later address adds to the low bits
+    unsigned gb = 0;          // blocks whose S was issued
     bool pend = false;        // block gb - 1's products are still to issue
     bool pend_first = false;  // ... and start a segment (O is overwritten, not accumulated)
     int k = 0;
     bool ok = true;
     auto issue_pv = [&]() {
-      const long long pb_ = gb - 1;
+      const unsigned pb_ = gb - 1;
       const int b = int(pb_ & 1), st = int(pb_ % kStages);
-      const bool w = wait(sm, &sm.p_full[b], uint32_t(pb_ >> 1) & 1, a.status);
+      const bool w = wait(sm, &sm.p_full[b], (pb_ >> 1) & 1, a.status);
       if (!__all_sync(0xffffffffu, w)) return false;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t vb = smem_addr(sm.v[st]);
+      if (elect_one()) {
+        const uint64_t vdesc = v_desc + uint32_t(st * kTileBytes >> 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t pcol = tmem + b * kKeys + h * kHalf, ocol = tmem + kColO + h * kHeadDim;
@@ -456,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           for (int term = 0; term < (kBf16 ? 1 : 2); ++term)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-              tc_mma_tmem_a(ocol, pcol + term * 16 + kk * 8, sw128_desc(vb + (2 * h + kk) * 2048, 16, 1024), kIdescPV,
+              tc_mma_tmem_a(ocol, pcol + term * 16 + kk * 8, vdesc + (2 * h + kk) * (2048 >> 4), kIdescPV,
                             (pend_first && term == 0 && kk == 0) ? 0u : 1u);
         }
         tc_commit(&sm.p_free[b]);
@@ -466,29 +559,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       pend = false;
       return true;
     };
-    Segment x;
-    while (ok && walk.next(a, x)) {
+    while (ok) {
       const int qb = k & 1;
-      bool w = wait(sm, &sm.q_full[qb], uint32_t(k / 2) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) break;
-      const uint32_t q_base = smem_addr(sm.q[qb]);
-      for (int j = x.j0; j < x.j1; ++j) {
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
+      }
+      const Segment &seg = sm.seg[k % kSegments];
+      if (seg.s < 0) break;
+      const int j0 = seg.j0, j1 = seg.j1;
+      w = wait(sm, &sm.q_full[qb], uint32_t(k / 2) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
+      }
+      const uint64_t qdesc = q_desc + uint32_t(qb * kRows * kRowBytes >> 4);
+      for (int j = j0; j < j1; ++j) {
         const int st = int(gb % kStages), b = int(gb & 1);
-        w = wait(sm, &sm.kv_full[st], uint32_t(gb / kStages) & 1, a.status);
-        if (w && gb >= 2) w = wait(sm, &sm.p_free[b], uint32_t(gb / 2 - 1) & 1, a.status);
+        w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status);
+        if (w && gb >= 2) w = wait(sm, &sm.p_free[b], (gb / 2 - 1) & 1, a.status);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t kb = smem_addr(sm.k[st]);
+        if (elect_one()) {
+          const uint64_t kdesc = k_desc + uint32_t(st * kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma(tmem + b * kKeys, sw128_desc(q_base + kk * 32, 16, 1024), sw128_desc(kb + kk * 32, 16, 1024),
-                   kIdescS, kk > 0 ? 1u : 0u);
+            tc_mma(tmem + b * kKeys, qdesc + kk * (32 >> 4), kdesc + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
           tc_commit(&sm.s_full[b]);
-          if (j == x.j1 - 1) tc_commit(&sm.q_empty[qb]);  // the segment's last read of its Q
+          if (j == j1 - 1) tc_commit(&sm.q_empty[qb]);  // the segment's last read of its Q
         }
         __syncwarp();
         if (pend && !issue_pv()) {
@@ -497,15 +599,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         }
         ++gb;
         pend = true;
-        pend_first = j == x.j0;
+        pend_first = j == j0;
       }
       ++k;
     }
     if (ok && pend) issue_pv();
     // every MMA issued has completed before the tensor memory is freed
-    if (lane == 0) {
+    if (elect_one()) {
       tc_commit(&sm.mma_done);
-      mbar_wait(&sm.mma_done, 0);
+      bounded_wait(&sm.mma_done, 0);
     }
     __syncwarp();
   } else {
@@ -514,104 +616,88 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     zero_invalid(tid, kSoftThreads);
     const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
     const uint32_t my_tmem = tmem + (uint32_t(32 * quarter) << 16);
-    const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
-    long long gb = 0;
-    int k = 0, ends = 0;  // segments begun; segments this warp has ended (the warps of a quarter agree)
+    const float c = a.neg ? -a.scale_log2 : a.scale_log2;
+    const float2 c2 = make_float2(c, c);  // exponents: |c| (sigma s - m) = c s - |c| m
+    unsigned gb = 0;
+    int k = 0, ends = 0;  // segments begun; segments this warp has ended
+    int cuts = 0;         // bit 0, 1: the share's first, last unit is cut
     bool ok = true;
-    Segment x;
-    for (; ok && walk.next(a, x); ++k) {
-      const Seq &seq = walk.seq;
-      const int octet = (quarter - k - turn) & 3, t = min(kTok, seq.n - x.tile * kTok);
-      const int node = octet * kOctet + (lane >> 2);
-      const bool active = octet * kOctet < t, real = node < t;  // the warp's, this thread's row
-      const int base = seq.ctx - seq.n;
-      const long long qrow = (long long)seq.q0 + x.tile * kTok + (real ? node : 0);
-      const uint32_t *mask = a.mask + qrow * a.mask_stride;
+    for (; ok; ++k) {
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) {
+        ok = false;
+        break;
+      }
+      const Segment &x = sm.seg[k % kSegments];
+      if (x.s < 0) break;
+      const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, j0 = x.j0, j1 = x.j1;
+      const bool active = octet * kOctet < x.n - x.tile * kTok;  // the warp has rows
+      // this thread's row, valid where `real`
+      const int node = x.tile * kTok + octet * kOctet + (lane >> 2);
+      const bool real = node < x.n;
       float m = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f);
-      for (int j = x.j0; j < x.j1; ++j, ++gb) {
+      float2 l2 = make_float2(0.f, 0.f), mc = l2;  // mc: -m |c|
+      bool ready = false;  // every row of the warp has a reference
+      for (int j = j0; j < j1; ++j, ++gb) {
         const int b = int(gb & 1), st = int(gb % kStages);
-        // S of the block, and (already complete) its load, for V's check and the bad-page bits
-        bool w = wait(sm, &sm.s_full[b], uint32_t(gb >> 1) & 1, a.status) &&
-                 wait(sm, &sm.kv_full[st], uint32_t(gb / kStages) & 1, a.status);
+        w = wait(sm, &sm.s_full[b], (gb >> 1) & 1, a.status);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
-        if ((j + 1) * kKeys > base) {
+        // the block's load, complete since before S, is seen here too, for V's check and the bad-page bits
+        auto check_values = [&]() {
+          w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status);
+          if ((j + 1) * kKeys <= base) return;
           // the block holds nodes: four threads to a V row
           const int r = tid >> 2, pos = j * kKeys + r, c0 = 2 * (tid & 3);
           uint4 *p0 = reinterpret_cast<uint4 *>(sm.v[st] + r * kRowBytes + ((c0 ^ (r & 7)) << 4));
           uint4 *p1 = reinterpret_cast<uint4 *>(sm.v[st] + r * kRowBytes + (((c0 + 1) ^ (r & 7)) << 4));
-          const bool inf = pos >= base && pos < seq.ctx && (nonfinite_chunk(*p0) || nonfinite_chunk(*p1));
+          const bool inf = pos >= base && pos < x.ctx && (nonfinite_chunk(*p0) || nonfinite_chunk(*p1));
           const unsigned any = __ballot_sync(0xffffffffu, inf) >> (lane & ~3) & 0xfu;
-          if (pos >= seq.ctx || any) *p0 = *p1 = make_uint4(0u, 0u, 0u, 0u);
+          if (pos >= x.ctx || any) *p0 = *p1 = make_uint4(0u, 0u, 0u, 0u);
           if (any) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
           fence_proxy_async_smem();
-        }
-        if (active) {
+        };
+        if (!active) {
+          check_values();
+        } else {
           tc_fence_after();
-          float s[32];
-          {
-            uint32_t u[32];
-            tmem_ld32(my_tmem + b * kKeys + half * kHalf, u);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(u[i]);
-          }
-          if (a.neg) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = -s[i];
-          }
+          uint32_t s[32];
+          tmem_ld32_async(my_tmem + b * kKeys + half * kHalf, s);
+          check_values();
           const int key0 = j * kKeys + half * kHalf;
           const int bad = sm.kv_bad[st] >> (2 * half) & 3;
-          const bool masked = key0 + kHalf > base || bad != 0;  // uniform over the warp
-          uint32_t see = ~0u;
-          float mx;
-          if (masked) {
-            see = real ? window_bits(mask, key0, base, seq.ctx, seq.n) : 0u;
+          bool slow = !ready || key0 + kHalf > base || bad != 0;  // uniform over the warp
+          tmem_ld_wait(s);
+          float2 sum = make_float2(0.f, 0.f);
+          if (!slow) {
+            uint32_t hi[16], lo[16];
+            weights<kBf16, false>(s, 0u, c2, mc, sum, hi, lo);
+            slow = __any_sync(0xffffffffu, sum.x + sum.y > kSumLimit);
+            if (!slow) store_weights<kBf16>(my_tmem + b * kKeys + half * kHalf, hi, lo);
+          }
+          bool moved = false;
+          float alpha = 1.f;
+          if (slow) {
+            uint32_t see = ~0u;
+            if (key0 + kHalf > base)
+              see = real ? window_bits(a.mask + (long long)(x.q0 + node) * a.mask_stride, key0, base, x.ctx, x.n) : 0u;
             if (bad & 1) see &= 0xffff0000u;
             if (bad & 2) see &= 0x0000ffffu;
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = see >> i & 1u ? s[i] : -INFINITY;
-            mx = max32(y);
-          } else {
-            mx = max32(s);
+            const float4 y = careful_block<kBf16>(my_tmem + b * kKeys + half * kHalf, see, m, c2.x, a.move_thresh);
+            alpha = y.y;
+            moved = __any_sync(0xffffffffu, y.x != m);
+            m = y.x;
+            mc = make_float2(-m * a.scale_log2, -m * a.scale_log2);
+            l2 = make_float2(l2.x * alpha, l2.y * alpha);
+            sum = make_float2(y.z, y.w);
+            ready = __all_sync(0xffffffffu, m != -INFINITY);
           }
-          const bool move = mx > m + a.move_thresh || (m == -INFINITY && mx > m);
-          float alpha = 1.f;
-          if (move) {
-            alpha = m == -INFINITY ? 0.f : ex2_approx((m - mx) * a.scale_log2);
-            m = mx;
-            l2.x *= alpha;
-            l2.y *= alpha;
-          }
-          const float2 mc = make_float2(-m * a.scale_log2, -m * a.scale_log2);
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = fma_f32x2(make_float2(s[2 * i], s[2 * i + 1]), c2, mc);
-            float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            if (masked) {
-              p.x = see >> (2 * i) & 1u ? p.x : 0.f;
-              p.y = see >> (2 * i + 1) & 1u ? p.y : 0.f;
-            }
-            l2 = add_f32x2(l2, p);
-            hi[i] = pack_bf16x2(p.x, p.y);
-            if constexpr (!kBf16) {
-              const float2 r = sub_f32x2(p, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
-              lo[i] = pack_bf16x2(r.x, r.y);
-            }
-          }
-          tmem_st16(my_tmem + b * kKeys + half * kHalf, hi);
-          if constexpr (!kBf16) tmem_st16(my_tmem + b * kKeys + half * kHalf + 16, lo);
-          if (j > x.j0 && __any_sync(0xffffffffu, move)) {
+          l2 = add_f32x2(l2, sum);
+          if (j > j0 && moved) {
             // a reference moved: once the products before this block are done, rescale the row of O
-            w = wait(sm, &sm.p_free[b ^ 1], uint32_t((gb - 1) >> 1) & 1, a.status);
-            if (!__all_sync(0xffffffffu, w)) {
-              ok = false;
-              break;
-            }
+            w = wait(sm, &sm.p_free[b ^ 1], ((gb - 1) >> 1) & 1, a.status) && w;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -625,17 +711,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           }
           tc_fence_before();
         }
-        __syncwarp();
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
         if (lane == 0) mbar_arrive(&sm.p_full[b]);
       }
       if (!ok) break;
+      if (j0 != 0 || j1 != x.nb) {
+        const int i = j0 == 0 ? 1 : 0;  // the share's last unit goes on in the next, its first began before
+        cuts |= 1 << i;
+        if (tid == 0) sm.cuts[i] = x;
+      }
       // ---- the segment's end: the row's two states merge; this thread has dims 32 half .. + 31 ----
       if (!active) continue;
       const float2 mine_ml = make_float2(m, l2.x + l2.y);
       sm.ml[ends & 1][half][row] = mine_ml;  // its place is written again after one more such barrier
       named_barrier_sync(1 + quarter, 64);
       const float2 other = sm.ml[ends++ & 1][half ^ 1][row];
-      const bool w = wait(sm, &sm.p_free[(gb - 1) & 1], uint32_t((gb - 1) >> 1) & 1, a.status);
+      w = wait(sm, &sm.p_free[(gb - 1) & 1], ((gb - 1) >> 1) & 1, a.status);
       if (!__all_sync(0xffffffffu, w)) {
         ok = false;
         break;
@@ -656,11 +750,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       }
       tc_fence_before();  // these reads come before the next segment's products (ordered by p_full)
       const int h = x.g * kGroup + (lane & 3);
+      const long long qrow = (long long)x.q0 + node;
       if (*reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k && real) {
         // nodes whose V holds a NaN or an infinity were zeroed for the product: the rows that see
         // them add p V here
         const int32_t *table = a.block_tables + (long long)x.s * a.bt_stride;
-        for (int pos = max(base, x.j0 * kKeys); pos < min(seq.ctx, x.j1 * kKeys); ++pos) {
+        const uint32_t *mask = a.mask + qrow * a.mask_stride;
+        for (int pos = max(base, j0 * kKeys); pos < min(x.ctx, j1 * kKeys); ++pos) {
           const int page = __ldg(table + pos / kPageTokens), nd = pos - base;
           if (page < 0 || page >= a.num_pages || !(__ldg(mask + (nd >> 5)) >> (nd & 31) & 1u)) continue;
           const long long at = (long long)page * a.page_stride + (x.g * kPageTokens + pos % kPageTokens) * kRowBytes;
@@ -683,62 +779,84 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         }
       }
       const long long out_at = (qrow * kQHeads + h) * kHeadDim + half * 32;
-      if (x.j0 == 0 && x.j1 == seq.nb) {
+      if (j0 == 0 && j1 == x.nb) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
         for (int d = 0; d < 32; ++d) r[d] *= inv;
         if (real) write_row<kBf16>(a, out_at, r);
         continue;
       }
-      // ---- cut unit: a partial state, then the ticket of (unit, warp's lanes and dims) ----
-      {
-        Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
-        if (real) {
-          float4 *dst = reinterpret_cast<float4 *>(&part.o[octet * 32 + lane][half * 32]);
+      // ---- cut unit: a partial state; its ticket is taken at the end ----
+      if (real) {
+        Part &part = a.parts[2 * cta + (j0 == 0 ? 1 : 0)];
+        const int at = octet * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) __stcg(dst + i, make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
-          if (half == 0) __stcg(&part.ml[octet * 32 + lane], make_float2(M, L));
-        }
+        for (int i = 0; i < 8; ++i)
+          __stcg(&part.o[half * 8 + i][at], make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+        if (half == 0) __stcg(&part.ml[at], make_float2(M, L));
       }
-      // both halves read the row sums that half 0 stores: its stores come before either ticket
-      named_barrier_sync(1 + quarter, 64);
-      const int c0 = cta_of_block(x.unit0, T, Gu), c1 = cta_of_block(x.unit0 + seq.nb - 1, T, Gu);
+    }
+    // ---- the tickets of the cut units: the CTA that takes a unit's last one merges its parts ----
+    // (every softmax warp comes here, whatever became of its waits)
+    named_barrier_sync(5, kSoftThreads);
+    if (tid < 2) {
       int last = 0;
-      if (lane == 0) {
-        __threadfence();
-        int *ticket = a.tickets + (((long long)x.s * a.max_tiles + x.tile) * kKvHeads + x.g) * kSoftWarps + octet * 2 + half;
-        last = atomic_add_acq_rel_gpu(ticket, 1) == c1 - c0;
+      if (cuts >> tid & 1 && *reinterpret_cast<volatile int *>(&sm.abort) == 0) {
+        const Segment &u = sm.cuts[tid];
+        const int parts = cta_of_block(u.unit0 + u.nb - 1, T, Gu) - cta_of_block(u.unit0, T, Gu);
+        int *ticket = a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g;
+        last = atomic_add_acq_rel_gpu(ticket, 1) == parts;
         if (last) atomicExch(ticket, 0);  // ready for the next call
       }
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (!last) continue;
-      __syncwarp();
-      M = -INFINITY;
-      L = 0.f;
+      sm.merge[tid] = last;
+    }
+    named_barrier_sync(5, kSoftThreads);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      if (!sm.merge[i]) continue;
+      const Segment &u = sm.cuts[i];
+      const int c0 = cta_of_block(u.unit0, T, Gu), c1 = cta_of_block(u.unit0 + u.nb - 1, T, Gu);
+      const int rows = min(kTok, u.n - u.tile * kTok) * kGroup;
+      const long long row0 = ((long long)u.q0 + u.tile * kTok) * kQHeads + u.g * kGroup;
+      // thread: one row's 4 dims at a time; kBatch parts at a time, all their loads in flight
+      constexpr int kBatch = 8;
+#pragma unroll 1
+      for (int e = tid; e < rows * (kHeadDim / 4); e += kSoftThreads) {
+        const int at = e % rows, d4 = e / rows;
+        float M = -INFINITY, L = 0.f;
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int p = c0; p <= c1; p += kBatch) {
+          float2 ml[kBatch];
+          float4 y[kBatch];
 #pragma unroll
-      for (int d = 0; d < 32; ++d) r[d] = 0.f;
-      if (real) {
-        for (int c = c0; c <= c1; ++c) {
-          const Part &part = a.parts[2 * c + (c == c0 ? 1 : 0)];
-          const float2 ml = __ldcg(&part.ml[octet * 32 + lane]);
-          const float4 *src = reinterpret_cast<const float4 *>(&part.o[octet * 32 + lane][half * 32]);
-          const float Mn = fmaxf(M, ml.x);
-          const float keep = state_weight(make_float2(M, L), Mn, a.scale_log2), wgt = state_weight(ml, Mn, a.scale_log2);
-          L = L * keep + ml.y * wgt;
-          M = Mn;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = __ldcg(src + i);
-            r[4 * i] = r[4 * i] * keep + y.x * wgt;
-            r[4 * i + 1] = r[4 * i + 1] * keep + y.y * wgt;
-            r[4 * i + 2] = r[4 * i + 2] * keep + y.z * wgt;
-            r[4 * i + 3] = r[4 * i + 3] * keep + y.w * wgt;
+          for (int k2 = 0; k2 < kBatch; ++k2) {
+            const int c = p + k2;
+            ml[k2] = make_float2(-INFINITY, 0.f);
+            y[k2] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c <= c1) {
+              const Part &part = a.parts[2 * c + (c == c0 ? 1 : 0)];
+              ml[k2] = __ldcg(&part.ml[at]);
+              y[k2] = __ldcg(&part.o[d4][at]);
+            }
           }
+          float Mn = M;
+#pragma unroll
+          for (int k2 = 0; k2 < kBatch; ++k2) Mn = fmaxf(Mn, ml[k2].x);
+          const float keep = state_weight(make_float2(M, L), Mn, a.scale_log2);
+          L *= keep;
+          r = make_float4(r.x * keep, r.y * keep, r.z * keep, r.w * keep);
+#pragma unroll
+          for (int k2 = 0; k2 < kBatch; ++k2) {
+            const float wgt = state_weight(ml[k2], Mn, a.scale_log2);
+            L += ml[k2].y * wgt;
+            r = make_float4(r.x + y[k2].x * wgt, r.y + y[k2].y * wgt, r.z + y[k2].z * wgt, r.w + y[k2].w * wgt);
+          }
+          M = Mn;
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-        for (int d = 0; d < 32; ++d) r[d] *= inv;
-        write_row<kBf16>(a, out_at, r);
+        const float v[4] = {r.x * inv, r.y * inv, r.z * inv, r.w * inv};
+        write_row<kBf16>(a, (row0 + (at >> 2) * kQHeads + (at & 3)) * kHeadDim + d4 * 4, v);
       }
     }
   }
@@ -753,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 constexpr int kMaxSeqs = 1 << 24, kMaxNodes = 1 << 20;
 
 size_t ticket_bytes(int num_seqs, int max_tiles) {
-  return (size_t(num_seqs) * size_t(max_tiles) * kKvHeads * kSoftWarps * sizeof(int32_t) + 127) / 128 * 128;
+  return (size_t(num_seqs) * size_t(max_tiles) * kKvHeads * sizeof(int32_t) + 127) / 128 * 128;
 }
 // The partial states come first: their place does not depend on the call's shape, and tickets return to zero.
 size_t workspace_size(int num_seqs, int max_tiles) {
