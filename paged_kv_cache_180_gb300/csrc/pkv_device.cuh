@@ -205,6 +205,9 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// The same into L1.
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // L2 policy for data read exactly once per call (K/V pages): evict first.
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;

@@ -60,12 +60,14 @@ constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kThreads = kSoftThreads + 64;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 320;
-constexpr int kMinBlocks = 2;                       // least key blocks a CTA is given
+constexpr int kMinBlocks = 2;                       // least list entries a CTA is given
+constexpr int kUnitCost = 4;                        // what a unit's start and end weigh in the list, in blocks
 constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
 constexpr int kTileBytes = kKeys * kRowBytes;       // K (or V) of one block: 8 KiB
 constexpr int kOctetBytes = kOctet * kGroup * kRowBytes;  // 4 KiB
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColO = 2 * kKeys;               // S buffers at columns 0 and 64, O_a at 128, O_b at 192
+constexpr int kMergeGroup = 5;                      // a unit in more parts than this merges groups of them first
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kSumLimit = 65536.f;
@@ -77,6 +79,8 @@ constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows 
 struct Part {
   float4 o[kHeadDim / 4][kRows];  // [4 dims][row]: neighbouring lanes hold neighbouring rows
   float2 ml[kRows];               // (reference, sum) of a row
+  float2 group_ml[kRows];         // of the merged state of the group of parts that this one is the first of
+  int ticket, unused[3];          // of that group; 0 between calls
 };
 
 struct TreeArgs {
@@ -123,43 +127,48 @@ struct Seq {
     return n >= 0 && n <= a.max_query && ctx >= 0 && ctx <= a.max_context && n <= ctx && q0 >= 0 &&
            q0 <= a.num_q_rows - n;
   }
-  __device__ long long blocks() const { return (long long)kKvHeads * tiles * nb; }
+  __device__ long long entries() const { return (long long)kKvHeads * tiles * (nb ? nb + kUnitCost : 0); }
 };
 
-// A CTA's share of one unit: key blocks j0 .. j1 - 1 of (sequence, K/V head, tile).  List order:
-// sequence, head, tile, block.  The loader walks the list and passes the segments on in shared memory.
+// A CTA's share of one unit: key blocks j0 .. j1 - 1 of (sequence, K/V head, tile).  The list holds the
+// units in the order sequence, head, tile; a unit has kUnitCost entries of weight, then its blocks.  (Without
+// the weight, CTAs with many short units took twice as long as the others in a ragged batch.)  The loader walks the list and passes the segments on in shared memory.
 struct Segment {
   int s, g, tile, j0, j1;  // s < 0: there are no more
   int q0, n, ctx, nb;      // the sequence's
-  long long unit0;         // the list index of the unit's block 0
+  long long unit0;         // list index of the unit's block 0
 };
 constexpr int kSegments = 8;  // places for segments; the roles are never more than four segments apart
 
 // Walk over the segments of a CTA's share.
 struct Walk {
-  long long pos, end, first;  // list position, end of the share, first block of sequence s
+  long long pos, end, first;  // list position, end of the share, first entry of sequence s
   int s;
   Seq seq;
   __device__ bool next(const TreeArgs &a, Segment &x) {
     x.s = -1;
-    if (pos >= end) return false;
-    while (pos - first >= seq.blocks()) {
-      first += seq.blocks();
-      seq.load(a, ++s);
+    while (pos < end) {
+      while (pos - first >= seq.entries()) {
+        first += seq.entries();
+        seq.load(a, ++s);
+      }
+      const long long len = seq.nb + kUnitCost, u = (pos - first) / len, v0 = pos - first - u * len;
+      const long long v1 = min(len, v0 + (end - pos));
+      pos += v1 - v0;
+      if (v1 <= kUnitCost) continue;  // nothing but the unit's weight
+      x.s = s;
+      x.g = int(u / seq.tiles);
+      x.tile = int(u % seq.tiles);
+      x.q0 = seq.q0;
+      x.n = seq.n;
+      x.ctx = seq.ctx;
+      x.nb = seq.nb;
+      x.unit0 = first + u * len + kUnitCost;
+      x.j0 = int(max(v0 - kUnitCost, 0LL));
+      x.j1 = int(v1 - kUnitCost);
+      return true;
     }
-    const long long u = (pos - first) / seq.nb;
-    x.s = s;
-    x.g = int(u / seq.tiles);
-    x.tile = int(u % seq.tiles);
-    x.q0 = seq.q0;
-    x.n = seq.n;
-    x.ctx = seq.ctx;
-    x.nb = seq.nb;
-    x.unit0 = first + u * seq.nb;
-    x.j0 = int(pos - x.unit0);
-    x.j1 = int(min((long long)seq.nb, x.j0 + (end - pos)));
-    pos += x.j1 - x.j0;
-    return true;
+    return false;
   }
 };
 
@@ -177,20 +186,20 @@ struct __align__(1024) Smem {
   uint64_t mma_done;
   Segment seg[kSegments];
   Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
-  int merge[2];     // this CTA took the last ticket
+  int merge[2];     // this CTA took the last ticket of the cut unit (1) or of its group of parts (2)
   int kv_bad[kStages];     // bit pp: page pp of the stage's block is invalid (loaded as zeros)
   int nonfinite[4];        // [segment % 4]: the last segment in which a node's V was zeroed (the softmax
                            // warps are never more than two segments apart: a block's S waits for the P two before)
   long long sums[kThreads / 32];
-  long long total, first;  // blocks in the list; global index of seq0's first block
+  long long first;  // list index of seq0's first entry
   int seq0, found;
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 
-// CTA that owns block p of the list when T blocks are split over G CTAs.
-__device__ __forceinline__ int cta_of_block(long long p, long long T, int G) { return int(((p + 1) * G - 1) / T); }
+// CTA that owns entry p of the list when T entries are split over G CTAs.
+__device__ __forceinline__ int cta_of_entry(long long p, long long T, int G) { return int(((p + 1) * G - 1) / T); }
 
 // Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
 constexpr long long kWaitCycles = 4000000000ll;
@@ -255,12 +264,13 @@ template <bool kBf16>
 __device__ __forceinline__ float4 careful_block(uint32_t taddr, uint32_t see, float m, float c, float move_thresh) {
   uint32_t s[32];
   tmem_ld32(taddr, s);
-  float mx = -INFINITY;  // in units of sigma * s
+  float top[8];  // in units of sigma * s
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const float y = __uint_as_float(s[i]);
-    mx = fmaxf(mx, see >> i & 1u ? (c < 0.f ? -y : y) : -INFINITY);
+    const float y = __uint_as_float(s[i]), z = see >> i & 1u ? (c < 0.f ? -y : y) : -INFINITY;
+    top[i & 7] = i < 8 ? z : fmaxf(top[i & 7], z);
   }
+  const float mx = fmaxf(max3f(top[0], top[1], top[2]), fmaxf(max3f(top[3], top[4], top[5]), fmaxf(top[6], top[7])));
   float alpha = 1.f;
   if (mx > m + move_thresh || (m == -INFINITY && mx > m)) {
     alpha = m == -INFINITY ? 0.f : ex2_approx((m - mx) * fabsf(c));
@@ -306,20 +316,83 @@ __device__ __forceinline__ float state_weight(float2 ml, float M, float c) {
 
 // Writes kDims dims of a row.
 template <bool kBf16, int kDims>
-__device__ __forceinline__ void write_row(const TreeArgs &a, long long at, const float (&r)[kDims]) {
-  if constexpr (kBf16 && kDims == 4) {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
-        make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
-  } else if constexpr (kBf16) {
-    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
+__device__ __forceinline__ void write_row(void *out, long long at, const float (&r)[kDims]) {
+  if constexpr (kBf16) {
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
 #pragma unroll
     for (int i = 0; i < kDims / 8; ++i)
       dst[i] = make_uint4(pack_bf16x2(r[8 * i], r[8 * i + 1]), pack_bf16x2(r[8 * i + 2], r[8 * i + 3]),
                           pack_bf16x2(r[8 * i + 4], r[8 * i + 5]), pack_bf16x2(r[8 * i + 6], r[8 * i + 7]));
   } else {
-    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
 #pragma unroll
     for (int i = 0; i < kDims / 4; ++i) dst[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+  }
+}
+
+// Merges `count` partial states of a unit whose first part is CTA c0's: those of CTAs c, c + stride, ...
+// Writes the unit's rows, or (dst, their first part) the merged state in its place: a thread overwrites only
+// what it has read itself, and the merged (M, L) have a place of their own.  kPad: the number of rows rounded up to 32, 64 or 128; a thread
+// has one row and an equal share of its dims, with kBatch * kVec loads of 16 bytes in flight.  (A call of its own
+// takes values: a reference to the kernel's arguments would be read through memory.)
+template <bool kBf16, int kPad>
+__device__ __noinline__ void merge_parts(const Part *parts, void *out, float scale_log2, int c0, int c, int stride,
+                                         int count, int rows, long long row0, Part *dst, int tid) {
+  constexpr int kShare = kPad * (kHeadDim / 4) / kSoftThreads;  // 16-byte vectors of a row that a thread has
+  constexpr int kVec = kShare < 4 ? kShare : 4, kBatch = 12 / kVec;
+  const int at = tid % kPad;
+  if (at >= rows) return;
+#pragma unroll 1
+  for (int d0 = tid / kPad * kShare, e = d0 + kShare; d0 < e; d0 += kVec) {
+    float M = -INFINITY, L = 0.f;
+    float r[4 * kVec];
+#pragma unroll
+    for (int d = 0; d < 4 * kVec; ++d) r[d] = 0.f;
+#pragma unroll 1
+    for (int p = 0; p < count; p += kBatch) {
+      float2 ml[kBatch];
+      float4 y[kBatch][kVec];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int q = c + (p + i) * stride;
+        const Part &part = parts[2 * q + (q == c0 ? 1 : 0)];
+        const bool there = p + i < count;
+        ml[i] = there ? __ldcg(stride > 1 ? &part.group_ml[at] : &part.ml[at]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int d = 0; d < kVec; ++d) y[i][d] = there ? __ldcg(&part.o[d0 + d][at]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float Mn = M;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, ml[i].x);
+      const float keep = state_weight(make_float2(M, L), Mn, scale_log2);
+      L *= keep;
+#pragma unroll
+      for (int d = 0; d < 4 * kVec; ++d) r[d] *= keep;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float wgt = state_weight(ml[i], Mn, scale_log2);
+        L += ml[i].y * wgt;
+#pragma unroll
+        for (int d = 0; d < kVec; ++d) {
+          r[4 * d] += y[i][d].x * wgt;
+          r[4 * d + 1] += y[i][d].y * wgt;
+          r[4 * d + 2] += y[i][d].z * wgt;
+          r[4 * d + 3] += y[i][d].w * wgt;
+        }
+      }
+      M = Mn;
+    }
+    if (dst != nullptr) {
+#pragma unroll
+      for (int d = 0; d < kVec; ++d)
+        __stcg(&dst->o[d0 + d][at], make_float4(r[4 * d], r[4 * d + 1], r[4 * d + 2], r[4 * d + 3]));
+      if (d0 == 0) __stcg(&dst->group_ml[at], make_float2(M, L));
+    } else {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int d = 0; d < 4 * kVec; ++d) r[d] *= inv;
+      write_row<kBf16>(out, (row0 + (at >> 2) * kQHeads + (at & 3)) * kHeadDim + d0 * 4, r);
+    }
   }
 }
 
@@ -336,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   for (int s = tid; s < a.num_seqs; s += kThreads) {
     Seq q;
     q.load(a, s);
-    mine += q.blocks();
+    mine += q.entries();
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -396,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     if (s < a.num_seqs) {
       Seq q;
       q.load(a, s);
-      v = q.blocks();
+      v = q.entries();
     }
     long long x = v;
 #pragma unroll
@@ -635,6 +708,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       // this thread's row, valid where `real`
       const int node = x.tile * kTok + octet * kOctet + (lane >> 2);
       const bool real = node < x.n;
+      if (real && j1 * kKeys > base)  // the mask word of the segment's first node key, needed at its end
+        prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f), mc = l2;  // mc: -m |c|
       bool ready = false;  // every row of the warp has a reference
@@ -783,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
         for (int d = 0; d < 32; ++d) r[d] *= inv;
-        if (real) write_row<kBf16>(a, out_at, r);
+        if (real) write_row<kBf16>(a.out, out_at, r);
         continue;
       }
       // ---- cut unit: a partial state; its ticket is taken at the end ----
@@ -796,68 +871,57 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         if (half == 0) __stcg(&part.ml[at], make_float2(M, L));
       }
     }
-    // ---- the tickets of the cut units: the CTA that takes a unit's last one merges its parts ----
+    // ---- the tickets of the cut units: the CTA that takes a unit's last one merges its parts; in a unit of
+    // many parts first the parts of a group, then the CTA with the last group the groups ----
     // (every softmax warp comes here, whatever became of its waits)
+    auto ticket_taken = [&](int *ticket, int before) {
+      const bool last = atomic_add_acq_rel_gpu(ticket, 1) == before;
+      if (last) atomicExch(ticket, 0);  // ready for the next call
+      return last;
+    };
     named_barrier_sync(5, kSoftThreads);
     if (tid < 2) {
-      int last = 0;
+      int merge = 0;
       if (cuts >> tid & 1 && *reinterpret_cast<volatile int *>(&sm.abort) == 0) {
         const Segment &u = sm.cuts[tid];
-        const int parts = cta_of_block(u.unit0 + u.nb - 1, T, Gu) - cta_of_block(u.unit0, T, Gu);
-        int *ticket = a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g;
-        last = atomic_add_acq_rel_gpu(ticket, 1) == parts;
-        if (last) atomicExch(ticket, 0);  // ready for the next call
+        const int c0 = cta_of_entry(u.unit0, T, Gu), parts = cta_of_entry(u.unit0 + u.nb - 1, T, Gu) - c0 + 1;
+        if (parts <= 2 * kMergeGroup) {
+          merge = ticket_taken(a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g, parts - 1) ? 1 : 0;
+        } else {
+          const int lo = (cta - c0) / kMergeGroup * kMergeGroup, hi = min(lo + kMergeGroup, parts) - 1;
+          merge = ticket_taken(&a.parts[2 * (c0 + lo) + (lo == 0 ? 1 : 0)].ticket, hi - lo) ? 2 : 0;
+        }
       }
-      sm.merge[tid] = last;
+      sm.merge[tid] = merge;
     }
     named_barrier_sync(5, kSoftThreads);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      if (!sm.merge[i]) continue;
+      int merge = sm.merge[i];
+      if (merge == 0) continue;
       const Segment &u = sm.cuts[i];
-      const int c0 = cta_of_block(u.unit0, T, Gu), c1 = cta_of_block(u.unit0 + u.nb - 1, T, Gu);
+      const int c0 = cta_of_entry(u.unit0, T, Gu), parts = cta_of_entry(u.unit0 + u.nb - 1, T, Gu) - c0 + 1;
       const int rows = min(kTok, u.n - u.tile * kTok) * kGroup;
       const long long row0 = ((long long)u.q0 + u.tile * kTok) * kQHeads + u.g * kGroup;
-      // thread: one row's 4 dims at a time; kBatch parts at a time, all their loads in flight
-      constexpr int kBatch = 8;
-#pragma unroll 1
-      for (int e = tid; e < rows * (kHeadDim / 4); e += kSoftThreads) {
-        const int at = e % rows, d4 = e / rows;
-        float M = -INFINITY, L = 0.f;
-        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int p = c0; p <= c1; p += kBatch) {
-          float2 ml[kBatch];
-          float4 y[kBatch];
-#pragma unroll
-          for (int k2 = 0; k2 < kBatch; ++k2) {
-            const int c = p + k2;
-            ml[k2] = make_float2(-INFINITY, 0.f);
-            y[k2] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c <= c1) {
-              const Part &part = a.parts[2 * c + (c == c0 ? 1 : 0)];
-              ml[k2] = __ldcg(&part.ml[at]);
-              y[k2] = __ldcg(&part.o[d4][at]);
-            }
-          }
-          float Mn = M;
-#pragma unroll
-          for (int k2 = 0; k2 < kBatch; ++k2) Mn = fmaxf(Mn, ml[k2].x);
-          const float keep = state_weight(make_float2(M, L), Mn, a.scale_log2);
-          L *= keep;
-          r = make_float4(r.x * keep, r.y * keep, r.z * keep, r.w * keep);
-#pragma unroll
-          for (int k2 = 0; k2 < kBatch; ++k2) {
-            const float wgt = state_weight(ml[k2], Mn, a.scale_log2);
-            L += ml[k2].y * wgt;
-            r = make_float4(r.x + y[k2].x * wgt, r.y + y[k2].y * wgt, r.z + y[k2].z * wgt, r.w + y[k2].w * wgt);
-          }
-          M = Mn;
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const float v[4] = {r.x * inv, r.y * inv, r.z * inv, r.w * inv};
-        write_row<kBf16>(a, (row0 + (at >> 2) * kQHeads + (at & 3)) * kHeadDim + d4 * 4, v);
+      auto merge_rows = [&](int c, int stride, int count, Part *dst) {
+        if (rows <= 32)
+          merge_parts<kBf16, 32>(a.parts, a.out, a.scale_log2, c0, c, stride, count, rows, row0, dst, tid);
+        else if (rows <= 64)
+          merge_parts<kBf16, 64>(a.parts, a.out, a.scale_log2, c0, c, stride, count, rows, row0, dst, tid);
+        else
+          merge_parts<kBf16, 128>(a.parts, a.out, a.scale_log2, c0, c, stride, count, rows, row0, dst, tid);
+      };
+      if (merge == 1) {
+        merge_rows(c0, 1, parts, nullptr);
+        continue;
       }
+      const int lo = (cta - c0) / kMergeGroup * kMergeGroup, groups = (parts + kMergeGroup - 1) / kMergeGroup;
+      merge_rows(c0 + lo, 1, min(kMergeGroup, parts - lo), &a.parts[2 * (c0 + lo) + (lo == 0 ? 1 : 0)]);
+      named_barrier_sync(5, kSoftThreads);
+      if (tid == 0)
+        sm.merge[i] = ticket_taken(a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g, groups - 1) ? 1 : 0;
+      named_barrier_sync(5, kSoftThreads);
+      if (sm.merge[i]) merge_rows(c0, kMergeGroup, groups, nullptr);
     }
   }
   tc_fence_before();
@@ -964,12 +1028,12 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   a.parts = static_cast<pkv::Part *>(workspace);
   a.tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + 2 * size_t(pkv::kMaxCtas) * sizeof(pkv::Part));
   a.status = device_status;
-  // no more CTAs than the list can have shares of kMinBlocks blocks
-  const double blocks = double(num_seqs) * tiles * pkv::kKvHeads * (max_context / pkv::kKeys + 1);
+  // no more CTAs than the list can have shares of kMinBlocks entries
+  const double entries = double(num_seqs) * tiles * pkv::kKvHeads * (max_context / pkv::kKeys + 1 + pkv::kUnitCost);
   const int sms = pkv::device_sm_count();
   long long grid = (long long)(sms > 0 ? sms : 152) * pkv::kCtasPerSm;
   if (grid > pkv::kMaxCtas) grid = pkv::kMaxCtas;
-  if (double(grid) > blocks / pkv::kMinBlocks) grid = (long long)(blocks / pkv::kMinBlocks);
+  if (double(grid) > entries / pkv::kMinBlocks) grid = (long long)(entries / pkv::kMinBlocks);
   if (grid < 1) grid = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
