@@ -3,36 +3,37 @@
 //   out[i][h] = sum_{t in A_i} softmax_t(scale * q[i][h] . K_t[h/4]) V_t[h/4],
 //   A_i = the committed prefix (t < base_s) and the nodes base_s + j whose bit j is set in row i's mask
 //
-// evaluated in one pass over the keys: with m a reference for the row's scores, l = sum 2^((s_t - m) c)
-// and O = sum 2^((s_t - m) c) V_t (c = scale log2 e); two disjoint key sets merge by
-// M = max(m_a, m_b), L = sum l 2^((m - M) c), O = sum O 2^((m - M) c), out = O / L.
+// evaluated in one pass over the keys: with r a reference for the row's exponents, l = sum 2^(c s_t - r) and
+// O = sum 2^(c s_t - r) V_t (c = scale log2 e); two disjoint key sets merge by
+// R = max(r_a, r_b), L = sum l 2^(r - R), O = sum O 2^(r - R), out = O / L.
 //
 // GB300 design (tcgen05 tensor cores, accumulators in tensor memory)
 //  * Unit: 32 nodes of a sequence against one K/V head g.  Its 128 rows (4 * node + head in group) share
 //    every K/V row loaded: M = 128.  Keys in blocks of 64 (4 pages).
 //  * Work split: the key blocks of all units form one list; the grid's CTAs (two per SM) take equal
 //    shares of it, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
-//    state (m, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
+//    state (r, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
 //    atomic counter, nobody waits) merges them.
-//  * Warp roles (320 threads): 8 softmax warps, a loader (tiled TMA: Q as boxes of 8 nodes x 4 heads,
-//    two buffers; head g's 16 rows of each page as 2 KiB boxes into a ring of 4 blocks), an MMA issuer.
-//  * S = Q K^T is 4 tcgen05.mma (M 128, N 64, K 16) into one of two TMEM buffers, so S of block j + 1 runs
-//    while the softmax works on block j.  A row belongs to two threads, one for the block's keys
-//    0-31 and one for keys 32-63, each with a reference, row sum and accumulator (O_a, O_b in tensor memory)
-//    of its own, so that they meet only at the unit's end.  P overwrites its S and is the TMEM A operand of
-//    O_a += P_a V[0:32], O_b += P_b V[32:64].
+//  * Warp roles (352 threads): 8 softmax warps, a loader (tiled TMA: Q as boxes of 8 nodes x 4 heads, two
+//    buffers; head g's 16 rows of each page as 2 KiB boxes into a ring of 4 blocks), one warp that issues S
+//    and one that issues the products with V: neither's waits hold up the other.
+//  * S = Q K^T is 4 tcgen05.mma (M 128, N 64, K 16) into one of three TMEM buffers.  The softmax warps form two
+//    groups that take the blocks in turn, a thread to a row; P overwrites its S and is the TMEM A operand
+//    of O += P V.  A block takes a softmax warp some 1300 cycles, nearly all of it latency (tensor memory,
+//    barriers, dependent arithmetic), so what counts is how many blocks are under way: two groups, and the S of
+//    one block more in reserve.  (Two threads to a row on the same block, with S buffers for two blocks, took
+//    1650 cycles a block.)
+//  * The reference is the row's largest exponent in the segment's first block and stays: weights are floats, so
+//    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
+//    that.  A row whose sum leaves [2^-64, 2^64] is computed again from global memory, slowly and exactly, by
+//    redo_row().
 //  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits; two
 //    products); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
 //    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
-//  * The reference only has to keep the weights in range (their precision is relative), so most blocks
-//    take no maximum: the weights are computed from the reference at hand, and only where a thread's sum over
-//    the block exceeds 2^16, where no reference is known yet or where keys are masked is the block's
-//    maximum taken; the reference moves when that exceeds it by more than 8 (a factor 256), and the row
-//    of O is rescaled in TMEM, after the product before it completed.
 //  * Masks: a key a row may not see gets weight 0 by selection, so a NaN score stays out.  V rows at or
 //    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
-//    NaN or an infinity (0 * NaN in the product would reach every row); the rows that see such a node add
-//    its contribution at the unit's end, from global memory.
+//    NaN or an infinity (0 * NaN in the product would reach every row); the segment's rows are then
+//    computed again by redo_row().
 //  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing
 //    work, waits (bounded) for what is in flight, frees its tensor memory and exits.
 #include <cuda.h>
@@ -51,13 +52,13 @@ constexpr int kTok = 32;                            // nodes per unit
 constexpr int kRows = kTok * kGroup;                // M = 128
 constexpr int kOctet = 8;                           // nodes per Q box: one warp's 32 TMEM lanes
 constexpr int kKeys = 64;                           // keys per block
-constexpr int kHalf = kKeys / 2;                    // keys of a block that one thread of a row has
 constexpr int kPagesPerBlock = kKeys / kPageTokens;
 constexpr int kStages = 4;                          // K/V blocks in flight
-constexpr int kSoftWarps = 8;
+constexpr int kScores = 3;                          // S / P buffers in tensor memory
+constexpr int kSoftWarps = 8;                       // two groups of four
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = kSoftThreads + 64;
+constexpr int kLoadWarp = kSoftWarps, kScoreWarp = kSoftWarps + 1, kValueWarp = kSoftWarps + 2;
+constexpr int kThreads = kSoftThreads + 96;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 320;
 constexpr int kMinBlocks = 2;                       // least list entries a CTA is given
@@ -66,11 +67,10 @@ constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one pa
 constexpr int kTileBytes = kKeys * kRowBytes;       // K (or V) of one block: 8 KiB
 constexpr int kOctetBytes = kOctet * kGroup * kRowBytes;  // 4 KiB
 constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kColO = 2 * kKeys;               // S buffers at columns 0 and 64, O_a at 128, O_b at 192
+constexpr uint32_t kColO = kScores * kKeys;         // S buffers at columns 0, 64 and 128, O at 192
 constexpr int kMergeGroup = 5;                      // a unit in more parts than this merges groups of them first
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleLog2 = 8.f;
-constexpr float kSumLimit = 65536.f;
+constexpr float kSumMin = 5.42101086e-20f, kSumMax = 1.84467441e19f;  // 2^-64, 2^64
 
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, false);     // B = K rows (K-major)
 constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows (MN-major)
@@ -78,8 +78,8 @@ constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows 
 // Partial state of one (CTA, unit) pair.
 struct Part {
   float4 o[kHeadDim / 4][kRows];  // [4 dims][row]: neighbouring lanes hold neighbouring rows
-  float2 ml[kRows];               // (reference, sum) of a row
-  float2 group_ml[kRows];         // of the merged state of the group of parts that this one is the first of
+  float2 rl[2][kRows];            // (reference, sum) of a row, for either half of its dims
+  float2 group_rl[2][kRows];      // of the merged state of the group of parts that this one is the first of
   int ticket, unused[3];          // of that group; 0 between calls
 };
 
@@ -101,9 +101,7 @@ struct TreeArgs {
   const int32_t *context_lens;
   int num_seqs, max_query, max_context;
   int max_tiles;      // units a sequence may have per K/V head
-  float scale_log2;   // |scale| * log2(e)
-  float move_thresh;  // scores (unscaled) by which a block's max must pass the reference to move it
-  int neg;            // scale < 0: a row's reference is the largest -s (sigma = -1)
+  float scale_log2;   // scale * log2(e)
   int *tickets;       // [num_seqs * max_tiles][8 heads], 0 between calls
   Part *parts;        // [2 * kMaxCtas]
   int32_t *status;
@@ -176,21 +174,25 @@ struct __align__(1024) Smem {
   uint8_t q[2][kRows * kRowBytes];
   uint8_t k[kStages][kTileBytes];
   uint8_t v[kStages][kTileBytes];
-  float2 ml[2][2][kRows];  // [turn][half]: a row's (reference, sum), exchanged at a segment's end
+  float ref[2][kRows];       // [turn]: a row's reference, from the group with the segment's first block
+  float2 sums[2][2][kRows];  // [turn][group]: a row's sum, and whether it has seen a key
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2];
-  uint64_t p_full[2];  // every softmax warp has written its P of the buffer (and is done with what it replaces)
-  uint64_t p_free[2];  // the products of a block are done: its buffer may be written, O read
+  uint64_t s_full[2 * kScores];  // [block % 6], so that a group sees every phase of the ones it waits on
+  uint64_t p_full[kScores];      // the group's four warps have written their P of the buffer
+  uint64_t p_free[kScores];      // the product of a block is done: its buffer may be written
+  uint64_t o_full, o_free;       // a segment's products are done; every softmax warp has read O
+  uint64_t ref_full[4], sums_full[4];  // per quarter of the lanes: ref, both sums are there
   uint64_t seg_full[kSegments];
-  uint64_t mma_done;
+  uint64_t mma_done[2];
   Segment seg[kSegments];
   Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
   int merge[2];     // this CTA took the last ticket of the cut unit (1) or of its group of parts (2)
-  int kv_bad[kStages];     // bit pp: page pp of the stage's block is invalid (loaded as zeros)
-  int nonfinite[4];        // [segment % 4]: the last segment in which a node's V was zeroed (the softmax
-                           // warps are never more than two segments apart: a block's S waits for the P two before)
-  long long sums[kThreads / 32];
+  int kv_bad[kStages];       // bit pp: page pp of the stage's block is invalid (loaded as zeros)
+  int block_bad[2 * kScores];  // the same for the block whose S is in s_full's place
+  int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
+                     // never more than two segments apart: O is written again when all have read it)
+  long long warp_sums[kThreads / 32];
   long long first;  // list index of seq0's first entry
   int seq0, found;
   uint32_t tmem_base;
@@ -226,15 +228,14 @@ __device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity, i
   return true;
 }
 
-// P = 2^((s - sigma m) c) of a thread's 32 keys as bf16 terms, two keys to a word: hi, and with fp32 output lo.
-// `sum` takes the fp32 weights.  With kMasked a key whose bit in `see` is clear gets 0 by selection (its
-// score may be NaN).
+// P = 2^(c s - r) of 16 keys as bf16 terms, two keys to a word: hi, and with fp32 output lo.  `sum` takes the
+// fp32 weights.  With kMasked a key whose bit in `see` is clear gets 0 by selection (its score may be NaN).
 template <bool kBf16, bool kMasked>
-__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t see, float2 c2, float2 mc, float2 &sum,
-                                        uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+__device__ __forceinline__ void weights(const uint32_t (&s)[16], uint32_t see, float2 c, float2 minus_r, float2 &sum,
+                                        uint32_t (&hi)[8], uint32_t (&lo)[8]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, mc);
+  for (int i = 0; i < 8; ++i) {
+    const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c, minus_r);
     float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
     if (kMasked) {
       p.x = see >> (2 * i) & 1u ? p.x : 0.f;
@@ -243,44 +244,60 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t see, f
     sum = add_f32x2(sum, p);
     hi[i] = pack_bf16x2(p.x, p.y);
     if constexpr (!kBf16) {
-      const float2 r = sub_f32x2(p, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
-      lo[i] = pack_bf16x2(r.x, r.y);
+      const float2 d = sub_f32x2(p, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
+      lo[i] = pack_bf16x2(d.x, d.y);
     }
   }
 }
 
-// P over its S in tensor memory: hi in the first 16 columns, lo in the next.
+// P of 16 keys to the S columns of keys 16i and on: of each 32 columns, hi in the first 16, lo in the others.
 template <bool kBf16>
-__device__ __forceinline__ void store_weights(uint32_t taddr, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
-  tmem_st16_async(taddr, hi);
-  if constexpr (!kBf16) tmem_st16_async(taddr + 16, lo);
+__device__ __forceinline__ void store_weights(uint32_t taddr, int i, const uint32_t (&hi)[8], const uint32_t (&lo)[8]) {
+  const uint32_t col = taddr + (i >> 1) * 32 + (i & 1) * 8;
+  tmem_st8_async(col, hi);
+  if constexpr (!kBf16) tmem_st8_async(col + 16, lo);
+}
+
+// The weights of a row's 64 keys, from S to P in place.  16 keys at a time: the next 16 scores are on their way
+// while these are worked on, and P of 16 keys is stored once the scores that lay there have been read.
+template <bool kBf16, bool kMasked>
+__device__ __forceinline__ void block_weights(uint32_t taddr, uint32_t see0, uint32_t see1, float2 c, float2 minus_r,
+                                              float2 &sum) {
+  uint32_t a[16], b[16], hi[8], lo[8];
+  tmem_ld16_async(taddr, a);
+  tmem_ld_wait(a);
+  tmem_ld16_async(taddr + 16, b);
+  weights<kBf16, kMasked>(a, see0, c, minus_r, sum, hi, lo);
+  tmem_ld_wait(b);
+  store_weights<kBf16>(taddr, 0, hi, lo);
+  tmem_ld16_async(taddr + 32, a);
+  weights<kBf16, kMasked>(b, see0 >> 16, c, minus_r, sum, hi, lo);
+  tmem_ld_wait(a);
+  store_weights<kBf16>(taddr, 1, hi, lo);
+  tmem_ld16_async(taddr + 48, b);
+  weights<kBf16, kMasked>(a, see1, c, minus_r, sum, hi, lo);
+  tmem_ld_wait(b);
+  store_weights<kBf16>(taddr, 2, hi, lo);
+  weights<kBf16, kMasked>(b, see1 >> 16, c, minus_r, sum, hi, lo);
+  store_weights<kBf16>(taddr, 3, hi, lo);
   tmem_st_wait();
 }
 
-// A block half whose keys not every row sees (`see`: the row's), whose reference m is still to be found, or too
-// far below: takes the maximum, moves the reference, computes and stores the weights.  Returns the
-// reference, the factor 2^((m_old - m) |c|) for what was summed before, and the weights' sums.
-template <bool kBf16>
-__device__ __forceinline__ float4 careful_block(uint32_t taddr, uint32_t see, float m, float c, float move_thresh) {
-  uint32_t s[32];
-  tmem_ld32(taddr, s);
-  float top[8];  // in units of sigma * s
+// A row's reference: the largest exponent among the visible keys of a block, 0 if there is none that is finite.
+__device__ __forceinline__ float block_reference(uint32_t taddr, uint32_t see0, uint32_t see1, float c) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float y = __uint_as_float(s[i]), z = see >> i & 1u ? (c < 0.f ? -y : y) : -INFINITY;
-    top[i & 7] = i < 8 ? z : fmaxf(top[i & 7], z);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t s[16];
+    tmem_ld16_async(taddr + 16 * i, s);
+    tmem_ld_wait(s);
+    const uint32_t see = (i < 2 ? see0 : see1) >> (16 * (i & 1));
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      top[j & 3] = fmaxf(top[j & 3], see >> j & 1u ? __uint_as_float(s[j]) * c : -INFINITY);
   }
-  const float mx = fmaxf(max3f(top[0], top[1], top[2]), fmaxf(max3f(top[3], top[4], top[5]), fmaxf(top[6], top[7])));
-  float alpha = 1.f;
-  if (mx > m + move_thresh || (m == -INFINITY && mx > m)) {
-    alpha = m == -INFINITY ? 0.f : ex2_approx((m - mx) * fabsf(c));
-    m = mx;
-  }
-  float2 sum = make_float2(0.f, 0.f);
-  uint32_t hi[16], lo[16];
-  weights<kBf16, true>(s, see, make_float2(c, c), make_float2(-m * fabsf(c), -m * fabsf(c)), sum, hi, lo);
-  store_weights<kBf16>(taddr, hi, lo);
-  return make_float4(m, alpha, sum.x, sum.y);
+  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  return isfinite(m) ? m : 0.f;
 }
 
 // The keys of a 32-key window starting at position key0 that a row may see: the prefix, then the nodes
@@ -309,9 +326,35 @@ __device__ __forceinline__ bool nonfinite_chunk(const uint4 &x) {
   return nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) || nonfinite_pair(x.w);
 }
 
-// The weight of a state (m, l) merged under the reference M; a state that has seen no key has l = 0.
-__device__ __forceinline__ float state_weight(float2 ml, float M, float c) {
-  return ml.y == 0.f ? 0.f : ex2_approx((ml.x - M) * c);
+// The weight of a state (r, l) merged under the reference R; a state that has seen no key has l = 0.
+__device__ __forceinline__ float state_weight(float2 rl, float R) { return rl.y == 0.f ? 0.f : ex2_approx(rl.x - R); }
+
+// One row's state (r, l, 32 dims of O from dim d0) over the keys pos .. end - 1, straight from global memory with a
+// running maximum: for rows whose sums left the range of the fast path, and for segments with nodes whose V is not
+// finite.  A key the row does not see is skipped.
+__device__ __noinline__ float2 redo_row(const uint8_t *k_base, const uint8_t *v_base, long long page_stride,
+                                        int num_pages, const int32_t *table, const uint32_t *mask, const uint16_t *q,
+                                        int g, int pos, int end, int base, float c, int d0, float *o) {
+  float R = -INFINITY, L = 0.f;
+  for (int d = 0; d < 32; ++d) o[d] = 0.f;
+  for (; pos < end; ++pos) {
+    const int page = __ldg(table + pos / kPageTokens), node = pos - base;
+    if (page < 0 || page >= num_pages || (node >= 0 && !(__ldg(mask + (node >> 5)) >> (node & 31) & 1u))) continue;
+    const long long at = (long long)page * page_stride + (g * kPageTokens + pos % kPageTokens) * kRowBytes;
+    const uint32_t *k = reinterpret_cast<const uint32_t *>(k_base + at), *x = reinterpret_cast<const uint32_t *>(q);
+    float dot = 0.f;
+    for (int i = 0; i < kHeadDim / 2; ++i) dot += bf16_lo(x[i]) * bf16_lo(k[i]) + bf16_hi(x[i]) * bf16_hi(k[i]);
+    const float e = dot * c, Rn = fmaxf(R, e);
+    const float keep = R == -INFINITY ? 0.f : exp2f(R - Rn), w = exp2f(e - Rn);
+    R = Rn;
+    L = L * keep + w;
+    const uint32_t *v = reinterpret_cast<const uint32_t *>(v_base + at) + d0 / 2;
+    for (int i = 0; i < 16; ++i) {
+      o[2 * i] = o[2 * i] * keep + w * bf16_lo(v[i]);
+      o[2 * i + 1] = o[2 * i + 1] * keep + w * bf16_hi(v[i]);
+    }
+  }
+  return make_float2(R, L);
 }
 
 // Writes kDims dims of a row.
@@ -332,11 +375,11 @@ __device__ __forceinline__ void write_row(void *out, long long at, const float (
 
 // Merges `count` partial states of a unit whose first part is CTA c0's: those of CTAs c, c + stride, ...
 // Writes the unit's rows, or (dst, their first part) the merged state in its place: a thread overwrites only
-// what it has read itself, and the merged (M, L) have a place of their own.  kPad: the number of rows rounded up to 32, 64 or 128; a thread
+// what it has read itself, and the merged (reference, sum) have a place of their own.  kPad: the number of rows rounded up to 32, 64 or 128; a thread
 // has one row and an equal share of its dims, with kBatch * kVec loads of 16 bytes in flight.  (A call of its own
 // takes values: a reference to the kernel's arguments would be read through memory.)
 template <bool kBf16, int kPad>
-__device__ __noinline__ void merge_parts(const Part *parts, void *out, float scale_log2, int c0, int c, int stride,
+__device__ __noinline__ void merge_parts(const Part *parts, void *out, int c0, int c, int stride,
                                          int count, int rows, long long row0, Part *dst, int tid) {
   constexpr int kShare = kPad * (kHeadDim / 4) / kSoftThreads;  // 16-byte vectors of a row that a thread has
   constexpr int kVec = kShare < 4 ? kShare : 4, kBatch = 12 / kVec;
@@ -344,34 +387,35 @@ __device__ __noinline__ void merge_parts(const Part *parts, void *out, float sca
   if (at >= rows) return;
 #pragma unroll 1
   for (int d0 = tid / kPad * kShare, e = d0 + kShare; d0 < e; d0 += kVec) {
+    const int half = d0 / (kHeadDim / 8);
     float M = -INFINITY, L = 0.f;
     float r[4 * kVec];
 #pragma unroll
     for (int d = 0; d < 4 * kVec; ++d) r[d] = 0.f;
 #pragma unroll 1
     for (int p = 0; p < count; p += kBatch) {
-      float2 ml[kBatch];
+      float2 rl[kBatch];
       float4 y[kBatch][kVec];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int q = c + (p + i) * stride;
         const Part &part = parts[2 * q + (q == c0 ? 1 : 0)];
         const bool there = p + i < count;
-        ml[i] = there ? __ldcg(stride > 1 ? &part.group_ml[at] : &part.ml[at]) : make_float2(-INFINITY, 0.f);
+        rl[i] = there ? __ldcg(stride > 1 ? &part.group_rl[half][at] : &part.rl[half][at]) : make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int d = 0; d < kVec; ++d) y[i][d] = there ? __ldcg(&part.o[d0 + d][at]) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float Mn = M;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, ml[i].x);
-      const float keep = state_weight(make_float2(M, L), Mn, scale_log2);
+      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, rl[i].x);
+      const float keep = state_weight(make_float2(M, L), Mn);
       L *= keep;
 #pragma unroll
       for (int d = 0; d < 4 * kVec; ++d) r[d] *= keep;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float wgt = state_weight(ml[i], Mn, scale_log2);
-        L += ml[i].y * wgt;
+        const float wgt = state_weight(rl[i], Mn);
+        L += rl[i].y * wgt;
 #pragma unroll
         for (int d = 0; d < kVec; ++d) {
           r[4 * d] += y[i][d].x * wgt;
@@ -386,7 +430,7 @@ __device__ __noinline__ void merge_parts(const Part *parts, void *out, float sca
 #pragma unroll
       for (int d = 0; d < kVec; ++d)
         __stcg(&dst->o[d0 + d][at], make_float4(r[4 * d], r[4 * d + 1], r[4 * d + 2], r[4 * d + 3]));
-      if (d0 == 0) __stcg(&dst->group_ml[at], make_float2(M, L));
+      if (d0 % (kHeadDim / 8) == 0) __stcg(&dst->group_rl[half][at], make_float2(M, L));
     } else {
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
@@ -413,29 +457,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sm.sums[warp] = mine;
+  if (lane == 0) sm.warp_sums[warp] = mine;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kSoftWarps);
+    }
+    for (int i = 0; i < 2 * kScores; ++i) mbar_init(&sm.s_full[i], 2);
+    for (int i = 0; i < kScores; ++i) {
+      mbar_init(&sm.p_full[i], kSoftWarps / 2);
       mbar_init(&sm.p_free[i], 1);
     }
-    for (int i = 0; i < 4; ++i) sm.nonfinite[i] = -1;
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_free, kSoftWarps);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.ref_full[i], 1);
+      mbar_init(&sm.sums_full[i], 2);
+      sm.nonfinite[i] = -1;
+    }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.kv_full[i], 1);
       mbar_init(&sm.kv_empty[i], 1);
     }
     for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1);
-    mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.mma_done[0], 1);
+    mbar_init(&sm.mma_done[1], 1);
     sm.abort = 0;
     sm.found = 0;
     mbar_init_fence();
   }
   __syncthreads();
   long long T = 0;
-  for (int w = 0; w < kThreads / 32; ++w) T += sm.sums[w];
+  for (int w = 0; w < kThreads / 32; ++w) T += sm.warp_sums[w];
   const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));
 
   // rows of sequences whose lengths do not fit, spread over the CTAs (a global write: after griddep_wait)
@@ -477,12 +530,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) sm.sums[warp] = x;
+    if (lane == 31) sm.warp_sums[warp] = x;
     __syncthreads();
     long long chunk = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) x += sm.sums[w];
-      chunk += sm.sums[w];
+      if (w < warp) x += sm.warp_sums[w];
+      chunk += sm.warp_sums[w];
     }
     x += before;
     if (x - v <= pa && pa < x) {
@@ -492,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     }
     before += chunk;
   }
-  if (warp == kMmaWarp) tmem_alloc(&sm.tmem_base, kTmemCols);
+  if (warp == kScoreWarp) tmem_alloc(&sm.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -598,60 +651,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       for (int j = k > 2 ? k - 2 : 0; j < k; ++j) bounded_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ================= MMA issuer (one thread issues, the warp waits) =================
-    const uint64_t q_desc = sw128_desc(smem_addr(sm.q), 16, 1024), k_desc = sw128_desc(smem_addr(sm.k), 16, 1024),
-                   v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);  // a later address adds to the low bits
-    unsigned gb = 0;          // blocks whose S was issued
-    bool pend = false;        // block gb - 1's products are still to issue
-    bool pend_first = false;  // ... and start a segment (O is overwritten, not accumulated)
-    int k = 0;
+  } else if (warp == kScoreWarp) {
+    // ================= S = Q K^T (one thread issues, the warp waits) =================
+    const uint64_t q_desc = sw128_desc(smem_addr(sm.q), 16, 1024),
+                   k_desc = sw128_desc(smem_addr(sm.k), 16, 1024);  // a later address adds to the low bits
+    unsigned gb = 0;  // blocks issued
     bool ok = true;
-    auto issue_pv = [&]() {
-      const unsigned pb_ = gb - 1;
-      const int b = int(pb_ & 1), st = int(pb_ % kStages);
-      const bool w = wait(sm, &sm.p_full[b], (pb_ >> 1) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t vdesc = v_desc + uint32_t(st * kTileBytes >> 4);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t pcol = tmem + b * kKeys + h * kHalf, ocol = tmem + kColO + h * kHeadDim;
-#pragma unroll
-          for (int term = 0; term < (kBf16 ? 1 : 2); ++term)
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              tc_mma_tmem_a(ocol, pcol + term * 16 + kk * 8, vdesc + (2 * h + kk) * (2048 >> 4), kIdescPV,
-                            (pend_first && term == 0 && kk == 0) ? 0u : 1u);
-        }
-        tc_commit(&sm.p_free[b]);
-        tc_commit(&sm.kv_empty[st]);
-      }
-      __syncwarp();
-      pend = false;
-      return true;
-    };
-    while (ok) {
+    for (int k = 0; ok; ++k) {
       const int qb = k & 1;
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
-      }
-      const Segment &seg = sm.seg[k % kSegments];
-      if (seg.s < 0) break;
-      const int j0 = seg.j0, j1 = seg.j1;
+      if (!__all_sync(0xffffffffu, w)) break;
+      const Segment &x = sm.seg[k % kSegments];
+      if (x.s < 0) break;
+      const int blocks = x.j1 - x.j0;
       w = wait(sm, &sm.q_full[qb], uint32_t(k / 2) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
-      }
+      if (!__all_sync(0xffffffffu, w)) break;
       const uint64_t qdesc = q_desc + uint32_t(qb * kRows * kRowBytes >> 4);
-      for (int j = j0; j < j1; ++j) {
-        const int st = int(gb % kStages), b = int(gb & 1);
+      for (int j = 0; j < blocks; ++j, ++gb) {
+        const int st = int(gb % kStages), b = int(gb % kScores), f = int(gb % (2 * kScores));
         w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status);
-        if (w && gb >= 2) w = wait(sm, &sm.p_free[b], (gb / 2 - 1) & 1, a.status);
+        if (w && gb >= kScores) w = wait(sm, &sm.p_free[b], (gb / kScores - 1) & 1, a.status);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -662,45 +681,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tmem + b * kKeys, qdesc + kk * (32 >> 4), kdesc + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
-          tc_commit(&sm.s_full[b]);
-          if (j == j1 - 1) tc_commit(&sm.q_empty[qb]);  // the segment's last read of its Q
+          tc_commit(&sm.s_full[f]);
+          sm.block_bad[f] = sm.kv_bad[st];
+          mbar_arrive(&sm.s_full[f]);  // passes on what this thread has seen: the block's load, its bad pages
+          if (j == blocks - 1) tc_commit(&sm.q_empty[qb]);  // the segment's last read of its Q
         }
         __syncwarp();
-        if (pend && !issue_pv()) {
+      }
+    }
+    // every MMA issued has completed before the tensor memory is freed
+    if (elect_one()) {
+      tc_commit(&sm.mma_done[0]);
+      bounded_wait(&sm.mma_done[0], 0);
+    }
+    __syncwarp();
+  } else if (warp == kValueWarp) {
+    // ================= O += P V (one thread issues, the warp waits) =================
+    const uint64_t v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
+    unsigned gb = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
+      if (!__all_sync(0xffffffffu, w)) break;
+      const Segment &x = sm.seg[k % kSegments];
+      if (x.s < 0) break;
+      const int blocks = x.j1 - x.j0;
+      for (int j = 0; j < blocks; ++j, ++gb) {
+        const int st = int(gb % kStages), b = int(gb % kScores);
+        w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status) &&
+            wait(sm, &sm.p_full[b], (gb / kScores) & 1, a.status);
+        // a segment's first product overwrites O, once every softmax warp has read the one before
+        if (w && j == 0 && k > 0) w = wait(sm, &sm.o_free, uint32_t(k - 1) & 1, a.status);
+        if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
-        ++gb;
-        pend = true;
-        pend_first = j == j0;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vdesc = v_desc + uint32_t(st * kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+#pragma unroll
+            for (int term = 0; term < (kBf16 ? 1 : 2); ++term)
+              tc_mma_tmem_a(tmem + kColO, tmem + b * kKeys + (kk >> 1) * 32 + (kk & 1) * 8 + term * 16,
+                            vdesc + kk * (2048 >> 4), kIdescPV, (j == 0 && kk == 0 && term == 0) ? 0u : 1u);
+          tc_commit(&sm.p_free[b]);
+          tc_commit(&sm.kv_empty[st]);
+          if (j == blocks - 1) tc_commit(&sm.o_full);
+        }
+        __syncwarp();
       }
-      ++k;
     }
-    if (ok && pend) issue_pv();
-    // every MMA issued has completed before the tensor memory is freed
     if (elect_one()) {
-      tc_commit(&sm.mma_done);
-      bounded_wait(&sm.mma_done, 0);
+      tc_commit(&sm.mma_done[1]);
+      bounded_wait(&sm.mma_done[1], 0);
     }
     __syncwarp();
   } else {
-    // ================= softmax: warp = (quarter of the lanes, half of each block's keys) =================
+    // ================= softmax: warp = (quarter of the lanes, group), thread = row =================
     griddep_wait();  // the mask and every global write come after the kernel before this one
     zero_invalid(tid, kSoftThreads);
-    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;  // half: the group, and dims 32 half .. + 31
     const uint32_t my_tmem = tmem + (uint32_t(32 * quarter) << 16);
-    const float c = a.neg ? -a.scale_log2 : a.scale_log2;
-    const float2 c2 = make_float2(c, c);  // exponents: |c| (sigma s - m) = c s - |c| m
-    unsigned gb = 0;
-    int k = 0, ends = 0;  // segments begun; segments this warp has ended
-    int cuts = 0;         // bit 0, 1: the share's first, last unit is cut
+    const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
+    unsigned gb0 = 0;  // blocks before the segment
+    int ends = 0;      // segments in which this warp had rows (the two warps of a quarter agree)
+    int cuts = 0;      // bit 0, 1: the share's first, last unit is cut
     bool ok = true;
-    for (; ok; ++k) {
+    for (int k = 0; ok; ++k) {
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
-      }
+      if (!__all_sync(0xffffffffu, w)) break;
       const Segment &x = sm.seg[k % kSegments];
       if (x.s < 0) break;
       const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, j0 = x.j0, j1 = x.j1;
@@ -710,148 +760,125 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const bool real = node < x.n;
       if (real && j1 * kKeys > base)  // the mask word of the segment's first node key, needed at its end
         prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
-      float m = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f), mc = l2;  // mc: -m |c|
-      bool ready = false;  // every row of the warp has a reference
-      for (int j = j0; j < j1; ++j, ++gb) {
-        const int b = int(gb & 1), st = int(gb % kStages);
-        w = wait(sm, &sm.s_full[b], (gb >> 1) & 1, a.status);
+      const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
+      float ref = 0.f;
+      float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
+      bool seen = false;
+      if (active && !leads) {
+        w = wait(sm, &sm.ref_full[quarter], uint32_t(ends) & 1, a.status);
+        if (!__all_sync(0xffffffffu, w)) break;
+        ref = sm.ref[ends & 1][row];
+        minus_r = make_float2(-ref, -ref);
+      }
+      for (int j = j0 + (leads ? 0 : 1); j < j1; j += 2) {
+        const unsigned gb = gb0 + unsigned(j - j0);
+        const int b = int(gb % kScores), f = int(gb % (2 * kScores)), key0 = j * kKeys;
+        w = wait(sm, &sm.s_full[f], (gb / (2 * kScores)) & 1, a.status);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
-        // the block's load, complete since before S, is seen here too, for V's check and the bad-page bits
-        auto check_values = [&]() {
-          w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status);
-          if ((j + 1) * kKeys <= base) return;
-          // the block holds nodes: four threads to a V row
-          const int r = tid >> 2, pos = j * kKeys + r, c0 = 2 * (tid & 3);
-          uint4 *p0 = reinterpret_cast<uint4 *>(sm.v[st] + r * kRowBytes + ((c0 ^ (r & 7)) << 4));
-          uint4 *p1 = reinterpret_cast<uint4 *>(sm.v[st] + r * kRowBytes + (((c0 + 1) ^ (r & 7)) << 4));
-          const bool inf = pos >= base && pos < x.ctx && (nonfinite_chunk(*p0) || nonfinite_chunk(*p1));
-          const unsigned any = __ballot_sync(0xffffffffu, inf) >> (lane & ~3) & 0xfu;
-          if (pos >= x.ctx || any) *p0 = *p1 = make_uint4(0u, 0u, 0u, 0u);
-          if (any) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
+        if (key0 + kKeys > base) {
+          // the block holds nodes: the group's threads look through V, two to a row
+          const int st = int(gb % kStages), r = (tid & 127) >> 1, pos = key0 + r;
+          uint8_t *vrow = sm.v[st] + r * kRowBytes;
+          bool inf = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            inf |= nonfinite_chunk(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
+          inf = inf && pos >= base && pos < x.ctx;
+          inf |= __shfl_xor_sync(0xffffffffu, int(inf), 1) != 0;
+          if (pos >= x.ctx || inf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (inf) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
           fence_proxy_async_smem();
-        };
-        if (!active) {
-          check_values();
-        } else {
+        }
+        if (active) {
           tc_fence_after();
-          uint32_t s[32];
-          tmem_ld32_async(my_tmem + b * kKeys + half * kHalf, s);
-          check_values();
-          const int key0 = j * kKeys + half * kHalf;
-          const int bad = sm.kv_bad[st] >> (2 * half) & 3;
-          bool slow = !ready || key0 + kHalf > base || bad != 0;  // uniform over the warp
-          tmem_ld_wait(s);
-          float2 sum = make_float2(0.f, 0.f);
-          if (!slow) {
-            uint32_t hi[16], lo[16];
-            weights<kBf16, false>(s, 0u, c2, mc, sum, hi, lo);
-            slow = __any_sync(0xffffffffu, sum.x + sum.y > kSumLimit);
-            if (!slow) store_weights<kBf16>(my_tmem + b * kKeys + half * kHalf, hi, lo);
-          }
-          bool moved = false;
-          float alpha = 1.f;
-          if (slow) {
-            uint32_t see = ~0u;
-            if (key0 + kHalf > base)
-              see = real ? window_bits(a.mask + (long long)(x.q0 + node) * a.mask_stride, key0, base, x.ctx, x.n) : 0u;
-            if (bad & 1) see &= 0xffff0000u;
-            if (bad & 2) see &= 0x0000ffffu;
-            const float4 y = careful_block<kBf16>(my_tmem + b * kKeys + half * kHalf, see, m, c2.x, a.move_thresh);
-            alpha = y.y;
-            moved = __any_sync(0xffffffffu, y.x != m);
-            m = y.x;
-            mc = make_float2(-m * a.scale_log2, -m * a.scale_log2);
-            l2 = make_float2(l2.x * alpha, l2.y * alpha);
-            sum = make_float2(y.z, y.w);
-            ready = __all_sync(0xffffffffu, m != -INFINITY);
-          }
-          l2 = add_f32x2(l2, sum);
-          if (j > j0 && moved) {
-            // a reference moved: once the products before this block are done, rescale the row of O
-            w = wait(sm, &sm.p_free[b ^ 1], ((gb - 1) >> 1) & 1, a.status) && w;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t o[32];
-              const uint32_t col = my_tmem + kColO + half * kHeadDim + 32 * i;
-              tmem_ld32(col, o);
-#pragma unroll
-              for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * alpha);
-              tmem_st32(col, o);
+          const uint32_t taddr = my_tmem + b * kKeys;
+          const int bad = sm.block_bad[f];
+          const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
+          uint32_t see0 = ~0u, see1 = ~0u;
+          if (masked) {
+            if (key0 + kKeys > base) {
+              const uint32_t *mask = a.mask + (long long)(x.q0 + node) * a.mask_stride;
+              see0 = real ? window_bits(mask, key0, base, x.ctx, x.n) : 0u;
+              see1 = real ? window_bits(mask, key0 + 32, base, x.ctx, x.n) : 0u;
             }
+            if (bad & 1) see0 &= 0xffff0000u;
+            if (bad & 2) see0 &= 0x0000ffffu;
+            if (bad & 4) see1 &= 0xffff0000u;
+            if (bad & 8) see1 &= 0x0000ffffu;
           }
+          seen |= (see0 | see1) != 0u;
+          if (j == j0) {
+            ref = block_reference(taddr, see0, see1, c2.x);
+            minus_r = make_float2(-ref, -ref);
+            sm.ref[ends & 1][row] = ref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ref_full[quarter]);
+          }
+          if (masked)
+            block_weights<kBf16, true>(taddr, see0, see1, c2, minus_r, l2);
+          else
+            block_weights<kBf16, false>(taddr, 0u, 0u, c2, minus_r, l2);
           tc_fence_before();
         }
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
+        __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[b]);
       }
       if (!ok) break;
+      gb0 += unsigned(j1 - j0);
       if (j0 != 0 || j1 != x.nb) {
         const int i = j0 == 0 ? 1 : 0;  // the share's last unit goes on in the next, its first began before
         cuts |= 1 << i;
         if (tid == 0) sm.cuts[i] = x;
       }
-      // ---- the segment's end: the row's two states merge; this thread has dims 32 half .. + 31 ----
-      if (!active) continue;
-      const float2 mine_ml = make_float2(m, l2.x + l2.y);
-      sm.ml[ends & 1][half][row] = mine_ml;  // its place is written again after one more such barrier
-      named_barrier_sync(1 + quarter, 64);
-      const float2 other = sm.ml[ends++ & 1][half ^ 1][row];
-      w = wait(sm, &sm.p_free[(gb - 1) & 1], ((gb - 1) >> 1) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
+      // ---- the segment's end: a row's sums meet; this thread has its dims 32 half .. + 31 ----
+      float L = l2.x + l2.y;
+      if (active) {
+        sm.sums[ends & 1][half][row] = make_float2(L, seen ? 1.f : 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sums_full[quarter]);
+        w = wait(sm, &sm.sums_full[quarter], uint32_t(ends) & 1, a.status);
+        const float2 other = sm.sums[ends & 1][half ^ 1][row];
+        ++ends;
+        L += other.x;
+        seen |= other.y != 0.f;
       }
-      tc_fence_after();
-      float M = fmaxf(mine_ml.x, other.x);
-      const float w_mine = state_weight(mine_ml, M, a.scale_log2), w_other = state_weight(other, M, a.scale_log2);
-      float L = mine_ml.y * w_mine + other.y * w_other;
+      w = wait(sm, &sm.o_full, uint32_t(k) & 1, a.status) && w;
+      if (!__all_sync(0xffffffffu, w)) break;
       float r[32];
-      {
+      if (active) {
+        tc_fence_after();
         uint32_t u[32];
-        tmem_ld32(my_tmem + kColO + half * kHeadDim + half * 32, u);
+        tmem_ld32(my_tmem + kColO + half * 32, u);
 #pragma unroll
-        for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]) * w_mine;
-        tmem_ld32(my_tmem + kColO + (half ^ 1) * kHeadDim + half * 32, u);
-#pragma unroll
-        for (int d = 0; d < 32; ++d) r[d] += __uint_as_float(u[d]) * w_other;
+        for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]);
+        tc_fence_before();
       }
-      tc_fence_before();  // these reads come before the next segment's products (ordered by p_full)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_free);
+      if (!active) continue;
       const int h = x.g * kGroup + (lane & 3);
       const long long qrow = (long long)x.q0 + node;
-      if (*reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k && real) {
-        // nodes whose V holds a NaN or an infinity were zeroed for the product: the rows that see
-        // them add p V here
-        const int32_t *table = a.block_tables + (long long)x.s * a.bt_stride;
-        const uint32_t *mask = a.mask + qrow * a.mask_stride;
-        for (int pos = max(base, j0 * kKeys); pos < min(x.ctx, j1 * kKeys); ++pos) {
-          const int page = __ldg(table + pos / kPageTokens), nd = pos - base;
-          if (page < 0 || page >= a.num_pages || !(__ldg(mask + (nd >> 5)) >> (nd & 31) & 1u)) continue;
-          const long long at = (long long)page * a.page_stride + (x.g * kPageTokens + pos % kPageTokens) * kRowBytes;
-          const uint4 *vrow = reinterpret_cast<const uint4 *>(a.v_base + at);
-          bool inf = false;
-          for (int i = 0; i < 8; ++i) inf |= nonfinite_chunk(vrow[i]);
-          if (!inf) continue;
-          const uint32_t *krow = reinterpret_cast<const uint32_t *>(a.k_base + at);
-          const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + (qrow * kQHeads + h) * kHeadDim);
-          float dot = 0.f;
-          for (int i = 0; i < kHeadDim / 2; ++i)
-            dot += bf16_lo(q[i]) * bf16_lo(krow[i]) + bf16_hi(q[i]) * bf16_hi(krow[i]);
-          const float p = ex2_approx(((a.neg ? -dot : dot) - M) * a.scale_log2);
-          const uint32_t *v = reinterpret_cast<const uint32_t *>(vrow) + half * 16;
+      float z = 0.f;  // NaN when the row of O is not finite
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            r[2 * i] += p * bf16_lo(v[i]);
-            r[2 * i + 1] += p * bf16_hi(v[i]);
-          }
-        }
+      for (int d = 0; d < 32; ++d) z += r[d] * 0.f;
+      if (real && seen && (!(L >= kSumMin && L <= kSumMax) || z != 0.f ||
+                           *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k)) {
+        float o[32];
+        const float2 rl = redo_row(a.k_base, a.v_base, a.page_stride, a.num_pages,
+                                   a.block_tables + (long long)x.s * a.bt_stride, a.mask + qrow * a.mask_stride,
+                                   a.q + (qrow * kQHeads + h) * kHeadDim, x.g, j0 * kKeys, min(x.ctx, j1 * kKeys), base,
+                                   c2.x, half * 32, o);
+        ref = rl.x;
+        L = rl.y;
+#pragma unroll
+        for (int d = 0; d < 32; ++d) r[d] = o[d];
       }
       const long long out_at = (qrow * kQHeads + h) * kHeadDim + half * 32;
       if (j0 == 0 && j1 == x.nb) {
@@ -868,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           __stcg(&part.o[half * 8 + i][at], make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
-        if (half == 0) __stcg(&part.ml[at], make_float2(M, L));
+        __stcg(&part.rl[half][at], make_float2(ref, L));
       }
     }
     // ---- the tickets of the cut units: the CTA that takes a unit's last one merges its parts; in a unit of
@@ -905,11 +932,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const long long row0 = ((long long)u.q0 + u.tile * kTok) * kQHeads + u.g * kGroup;
       auto merge_rows = [&](int c, int stride, int count, Part *dst) {
         if (rows <= 32)
-          merge_parts<kBf16, 32>(a.parts, a.out, a.scale_log2, c0, c, stride, count, rows, row0, dst, tid);
+          merge_parts<kBf16, 32>(a.parts, a.out, c0, c, stride, count, rows, row0, dst, tid);
         else if (rows <= 64)
-          merge_parts<kBf16, 64>(a.parts, a.out, a.scale_log2, c0, c, stride, count, rows, row0, dst, tid);
+          merge_parts<kBf16, 64>(a.parts, a.out, c0, c, stride, count, rows, row0, dst, tid);
         else
-          merge_parts<kBf16, 128>(a.parts, a.out, a.scale_log2, c0, c, stride, count, rows, row0, dst, tid);
+          merge_parts<kBf16, 128>(a.parts, a.out, c0, c, stride, count, rows, row0, dst, tid);
       };
       if (merge == 1) {
         merge_rows(c0, 1, parts, nullptr);
@@ -926,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -1022,9 +1049,7 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   a.max_query = max_query;
   a.max_context = max_context;
   a.max_tiles = tiles;
-  a.scale_log2 = fabsf(scale) * pkv::kLog2e;
-  a.move_thresh = a.scale_log2 > 0.f ? pkv::kRescaleLog2 / a.scale_log2 : INFINITY;
-  a.neg = scale < 0.f ? 1 : 0;
+  a.scale_log2 = scale * pkv::kLog2e;
   a.parts = static_cast<pkv::Part *>(workspace);
   a.tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + 2 * size_t(pkv::kMaxCtas) * sizeof(pkv::Part));
   a.status = device_status;

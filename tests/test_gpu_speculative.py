@@ -100,6 +100,32 @@ def test_scales(pkv, scale):
     _check(pkv, S.TreeCase([700, 40, 90], [12, 40, 3], seed=51), scale=scale)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_scores_that_outgrow_the_first_block(pkv, bf16):
+    # later keys score hundreds of times higher (or every later key far lower) than the first 64: a reference taken
+    # from those alone would overflow (or vanish), on whole rows and on some of them
+    for gain, where in ((64, slice(100, 400)), (256, slice(333, 334)), (1 / 64, slice(70, 600)), (512, slice(590, 600))):
+        c = S.TreeCase([600, 70], [20, 9], seed=71)
+        for s in range(2):
+            for t in range(*where.indices(int(c.lens[s]))):
+                k = c.pool.data[c.bt[s, t // 16], 0, :, t % 16]
+                k[:] = ((rng.bf16_bits_to_f64(k) * gain).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+        _check(pkv, c, bf16)
+
+
+def test_large_values_stay_finite(pkv):
+    # V about 2^101, and a reference below the maximum: sums of 2^x V pass the range of fp32, the output does not
+    c = S.TreeCase([400], [10], seed=72)
+    for t in range(400):
+        v = c.pool.data[c.bt[0, t // 16], 1, :, t % 16]
+        v[:] = (v & 0x8000) | 0x7200 | (v & 0x7F)
+        if t >= 128:
+            k = c.pool.data[c.bt[0, t // 16], 0, :, t % 16]
+            k[:] = ((rng.bf16_bits_to_f64(k) * 8).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    got = _check(pkv, c)
+    assert np.isfinite(got).all()
+
+
 def test_wide_mask_rows_and_ignored_bits(pkv):
     c = S.TreeCase([90, 33], [7, 33], seed=52, words=5)
     got = _check(pkv, c)
