@@ -215,6 +215,17 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   return p;
 }
 
+// Registers per thread of a warpgroup (four warps, all of which call it): regs_dec gives some back to the
+// block's own pool, regs_inc waits until the pool has enough.
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // True in one thread of the warp, the same one each time (all 32 lanes call).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

@@ -14,9 +14,10 @@
 //    shares of it, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
 //    state (r, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
 //    atomic counter, nobody waits) merges them.
-//  * Warp roles (352 threads): 8 softmax warps, a loader (tiled TMA: Q as boxes of 8 nodes x 4 heads, two
-//    buffers; head g's 16 rows of each page as 2 KiB boxes into a ring of 4 blocks), one warp that issues S
-//    and one that issues the products with V: neither's waits hold up the other.
+//  * Warp roles (384 threads): 8 softmax warps, a loader of K and one of V (tiled TMA, head g's 16 rows of
+//    each page as 2 KiB boxes, into rings of 5 and 6 blocks: a K block is free once its S is there, a V block waits
+//    for the softmax too), one warp that loads Q (boxes of 8 nodes x 4 heads) and issues S, and one that
+//    issues the products with V: nobody's waits hold up another's work.
 //  * S = Q K^T is 4 tcgen05.mma (M 128, N 64, K 16) into one of three TMEM buffers.  The softmax warps form two
 //    groups that take the blocks in turn, a thread to a row; P overwrites its S and is the TMEM A operand
 //    of O += P V.  A block takes a softmax warp some 1300 cycles, nearly all of it latency (tensor memory,
@@ -53,13 +54,18 @@ constexpr int kRows = kTok * kGroup;                // M = 128
 constexpr int kOctet = 8;                           // nodes per Q box: one warp's 32 TMEM lanes
 constexpr int kKeys = 64;                           // keys per block
 constexpr int kPagesPerBlock = kKeys / kPageTokens;
-constexpr int kStages = 4;                          // K/V blocks in flight
+constexpr int kStagesK = 4, kStagesV = 5;           // K and V blocks in shared memory (V waits for the softmax)
 constexpr int kScores = 3;                          // S / P buffers in tensor memory
 constexpr int kSoftWarps = 8;                       // two groups of four
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kLoadWarp = kSoftWarps, kScoreWarp = kSoftWarps + 1, kValueWarp = kSoftWarps + 2;
-constexpr int kThreads = kSoftThreads + 96;
+constexpr int kLoadWarpK = kSoftWarps, kLoadWarpV = kSoftWarps + 1, kScoreWarp = kSoftWarps + 2,
+              kValueWarp = kSoftWarps + 3;
+constexpr int kThreads = kSoftThreads + 128;
 constexpr int kCtasPerSm = 2;
+// Registers per thread: a launch at two CTAs per SM has 80; the four loading and issuing warps give up theirs above
+// 40, which raises the softmax warps' to 96: 4 * 32 * 40 + 8 * 32 * 96 < 12 * 32 * 80.
+constexpr int kRegsOthers = 40, kRegsSoftmax = 96;
+static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax <= kThreads * 80, "registers of a CTA");
 constexpr int kMaxCtas = 320;
 constexpr int kMinBlocks = 2;                       // least list entries a CTA is given
 constexpr int kUnitCost = 4;                        // what a unit's start and end weigh in the list, in blocks
@@ -101,7 +107,7 @@ struct TreeArgs {
   const int32_t *context_lens;
   int num_seqs, max_query, max_context;
   int max_tiles;      // units a sequence may have per K/V head
-  float scale_log2;   // scale * log2(e)
+  float2 c;           // scale * log2(e), twice
   int *tickets;       // [num_seqs * max_tiles][8 heads], 0 between calls
   Part *parts;        // [2 * kMaxCtas]
   int32_t *status;
@@ -136,15 +142,18 @@ struct Segment {
   int q0, n, ctx, nb;      // the sequence's
   long long unit0;         // list index of the unit's block 0
 };
-constexpr int kSegments = 8;  // places for segments; the roles are never more than four segments apart
+// Places for segments.  The K loader is at most 5 blocks (and so segments) ahead of S, S 3 ahead of the products,
+// these one segment ahead of the softmax warps: place k is free when segment k + 16 is written to it.
+constexpr int kSegments = 16;
 
-// Walk over the segments of a CTA's share.
+// Walk over the segments of a CTA's share.  (It keeps little between segments and reads a sequence's lengths
+// again for each: the loader has few registers.)
 struct Walk {
   long long pos, end, first;  // list position, end of the share, first entry of sequence s
   int s;
-  Seq seq;
   __device__ bool next(const TreeArgs &a, Segment &x) {
-    x.s = -1;
+    Seq seq;
+    seq.load(a, s);
     while (pos < end) {
       while (pos - first >= seq.entries()) {
         first += seq.entries();
@@ -166,29 +175,30 @@ struct Walk {
       x.j1 = int(v1 - kUnitCost);
       return true;
     }
+    x.s = -1;
     return false;
   }
 };
 
 struct __align__(1024) Smem {
   uint8_t q[2][kRows * kRowBytes];
-  uint8_t k[kStages][kTileBytes];
-  uint8_t v[kStages][kTileBytes];
-  float ref[2][kRows];       // [turn]: a row's reference, from the group with the segment's first block
-  float2 sums[2][2][kRows];  // [turn][group]: a row's sum, and whether it has seen a key
+  uint8_t k[kStagesK][kTileBytes];
+  uint8_t v[kStagesV][kTileBytes];
+  float ref[4][kRows];       // [turn]: a row's reference, from the group with the segment's first block
+  float sums[4][2][kRows];   // [turn][group]: a row's sum
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
   uint64_t s_full[2 * kScores];  // [block % 6], so that a group sees every phase of the ones it waits on
   uint64_t p_full[kScores];      // the group's four warps have written their P of the buffer
   uint64_t p_free[kScores];      // the product of a block is done: its buffer may be written
   uint64_t o_full, o_free;       // a segment's products are done; every softmax warp has read O
-  uint64_t ref_full[4], sums_full[4];  // per quarter of the lanes: ref, both sums are there
+  uint64_t ref_full[4][2], sums_full[4];  // per quarter of the lanes: ref (by turn), both sums are there
   uint64_t seg_full[kSegments];
   uint64_t mma_done[2];
   Segment seg[kSegments];
   Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
   int merge[2];     // this CTA took the last ticket of the cut unit (1) or of its group of parts (2)
-  int kv_bad[kStages];       // bit pp: page pp of the stage's block is invalid (loaded as zeros)
+  int page_bad[kStagesK];      // bit pp: page pp of the K stage's block is invalid (loaded as zeros)
   int block_bad[2 * kScores];  // the same for the block whose S is in s_full's place
   int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
                      // never more than two segments apart: O is written again when all have read it)
@@ -204,26 +214,28 @@ constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 __device__ __forceinline__ int cta_of_entry(long long p, long long T, int G) { return int(((p + 1) * G - 1) / T); }
 
 // Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
-constexpr long long kWaitCycles = 4000000000ll;
+constexpr unsigned kWaitCycles = 3800000000u;
+__device__ __forceinline__ unsigned clock32() {
+  unsigned c;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(c));
+  return c;
+}
 __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
+  const unsigned t0 = clock32();
   while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitCycles) return false;
+    if (clock32() - t0 > kWaitCycles) return false;
   return true;
 }
 
-// The same for a role's waits: gives up when another role has aborted, and makes the others do so.
-__device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
+// The same for a role's waits: gives up when another role has, and makes the others do so.
+__device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
+  const unsigned t0 = clock32();
+  volatile int *abort = &sm.abort;
   while (!mbar_try_wait(bar, parity)) {
-    if (*reinterpret_cast<volatile int *>(&sm.abort)) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *reinterpret_cast<volatile int *>(&sm.abort) = 1;
-      report(status, PKV_DEV_TIMEOUT);
-      return false;
-    }
+    if (clock32() - t0 > kWaitCycles) *abort = 1;
+    if (*abort) return false;
   }
   return true;
 }
@@ -317,6 +329,14 @@ __device__ __forceinline__ uint32_t window_bits(const uint32_t *mask, int key0, 
   }
   const int left = ctx - key0;
   return left >= 32 ? bits : bits & ((1u << left) - 1u);
+}
+
+// Whether a row may see any of the keys pos .. end - 1 (a sum of 0 is right if not).
+__device__ __forceinline__ bool sees_any(const uint32_t *mask, int pos, int end, int base, int n) {
+  if (pos < base) return true;
+  for (; pos < end; pos += 32)
+    if (window_bits(mask, pos, base, end, n)) return true;
+  return false;
 }
 
 __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
@@ -471,13 +491,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, kSoftWarps);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.ref_full[i], 1);
+      mbar_init(&sm.ref_full[i][0], 1);
+      mbar_init(&sm.ref_full[i][1], 1);
       mbar_init(&sm.sums_full[i], 2);
       sm.nonfinite[i] = -1;
     }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 1);
+    for (int i = 0; i < kStagesK; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < kStagesV; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1);
     mbar_init(&sm.mma_done[0], 1);
@@ -555,122 +580,171 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   // that the quarters (the SM's sub-partitions) share the work.
   const int turn = cta * 2 >= G ? 2 : 0;
 
-  if (warp == kLoadWarp) {
-    // ================= loader: Q boxes and K/V blocks (tiled TMA) =================
-    const uint64_t once = policy_evict_first(), again = policy_evict_last();
-    if (lane == 0) {
-      prefetch_tensormap(&a.tmap_k);
-      prefetch_tensormap(&a.tmap_v);
-      prefetch_tensormap(&a.tmap_q);
+  // The pages of a segment's blocks: table entries 32 at a time (8 blocks), the next 32 in flight.
+  struct Pages {
+    const int32_t *table;
+    int npages, first, ent, ent_next;
+    __device__ int entries(int p, int lane) const { return p + lane < npages ? __ldg(table + p + lane) : -1; }
+    __device__ void start(const TreeArgs &a, const Segment &x, int lane) {
+      table = a.block_tables + (long long)x.s * a.bt_stride;
+      npages = (x.ctx - 1) / kPageTokens + 1;
+      first = x.j0 * kPagesPerBlock;
+      ent = entries(first, lane);
+      ent_next = entries(first + 32, lane);
     }
+    // Pages of block j (taken in order), -1 for what is not in the pool: TMA fills these with zeros.  Returns
+    // the bits of those inside the context.
+    __device__ int block(int j, int num_pages, int lane, int (&page)[kPagesPerBlock]) {
+      const int p = j * kPagesPerBlock, at = (p - first) & 31;
+      if (at == 0 && p > first) {
+        ent = ent_next;
+        ent_next = entries(p + 32, lane);
+      }
+      int bad = 0;
+#pragma unroll
+      for (int i = 0; i < kPagesPerBlock; ++i) {
+        const int e = __shfl_sync(0xffffffffu, ent, at + i);
+        page[i] = e >= 0 && e < num_pages ? e : -1;
+        if (page[i] < 0 && p + i < npages) bad |= 1 << i;
+      }
+      return bad;
+    }
+  };
+
+  if (warp >= kSoftWarps) regs_dec<kRegsOthers>();
+  if (warp == kLoadWarpK) {
+    // ================= K loader (tiled TMA); it walks the list =================
+    const uint64_t once = policy_evict_first(), again = policy_evict_last();
     Walk walk;
     walk.pos = pa;
     walk.end = pb;
     walk.first = sm.first;
     walk.s = sm.seq0;
-    walk.seq.load(a, walk.s);
-    unsigned gb = 0;   // blocks issued
-    int k = 0;         // segments started
+    if (lane == 0) {
+      prefetch_tensormap(&a.tmap_k);
+      prefetch_tensormap(&a.tmap_q);
+    }
+    unsigned gb = 0;  // blocks issued
+    int loads = 0;    // segments whose Q was asked for
     bool ok = true, waited = false;
-    Segment x;
-    while (ok) {
-      const bool more = walk.next(a, x);
-      const int qb = k & 1;
+    for (int k = 0; ok; ++k) {
+      Segment &x = sm.seg[k % kSegments];
+      const bool more = walk.next(a, x);  // every lane writes the same
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.seg_full[k % kSegments]);
+      if (!more) break;
+      // Q: boxes of 8 nodes x 4 heads, once the segment before the last has read its own
       if (k >= 2) {
-        const bool w = wait(sm, &sm.q_empty[qb], uint32_t(k / 2 - 1) & 1, a.status);
+        const bool w = wait(sm, &sm.q_empty[k & 1], uint32_t(k / 2 - 1) & 1);
         if (!__all_sync(0xffffffffu, w)) break;
       }
-      if (lane == 0) {
-        sm.seg[k % kSegments] = x;
-        mbar_arrive(&sm.seg_full[k % kSegments]);
-      }
-      __syncwarp();
-      if (!more) break;
-      const int t = min(kTok, x.n - x.tile * kTok), octets = (t + kOctet - 1) / kOctet;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&sm.q_full[qb], uint32_t(octets * kOctetBytes));
+        const int octets = (min(kTok, x.n - x.tile * kTok) + kOctet - 1) / kOctet;
+        mbar_arrive_expect_tx(&sm.q_full[k & 1], uint32_t(octets * kOctetBytes));
         for (int o = 0; o < octets; ++o)
-          tma_load_3d(sm.q[qb] + ((o + k + turn) & 3) * kOctetBytes, &a.tmap_q, 0, x.g * kGroup,
-                      x.q0 + x.tile * kTok + o * kOctet, &sm.q_full[qb], once);
+          tma_load_3d(sm.q[k & 1] + ((o + k + turn) & 3) * kOctetBytes, &a.tmap_q, 0, x.g * kGroup,
+                      x.q0 + x.tile * kTok + o * kOctet, &sm.q_full[k & 1], once);
       }
       __syncwarp();
+      ++loads;
       // launched with overlap (PKV_OVERLAP_PREVIOUS), the kernel before this one may still be writing
       // the pool: it is read only once that kernel has completed
+      Pages pages;
+      pages.start(a, x, lane);
       if (!waited) griddep_wait();
       waited = true;
-      // block-table entries 32 at a time (8 blocks), the next 32 in flight
-      const int32_t *table = a.block_tables + (long long)x.s * a.bt_stride;
-      const int npages = (x.ctx - 1) / kPageTokens + 1, p0 = x.j0 * kPagesPerBlock;
-      const uint64_t policy = walk.seq.tiles > 1 ? again : once;  // several tiles read the same K/V
-      auto entries = [&](int p) { return p + lane < npages ? __ldg(table + p + lane) : -1; };
-      int ent = entries(p0), ent_next = entries(p0 + 32);
-      for (int j = x.j0; j < x.j1; ++j, ++gb) {
-        const int st = int(gb % kStages), at = (j - x.j0) * kPagesPerBlock & 31;
-        if (at == 0 && j > x.j0) {
-          ent = ent_next;
-          ent_next = entries(j * kPagesPerBlock + 32);
-        }
-        if (gb >= kStages) {
-          const bool w = wait(sm, &sm.kv_empty[st], (gb / kStages - 1) & 1, a.status);
+      const uint64_t policy = x.n > kTok ? again : once;  // several tiles read the same K/V
+      const int j1 = x.j1, y = x.g * kPageTokens;
+      for (int j = x.j0; j < j1; ++j, ++gb) {
+        const int st = int(gb % kStagesK);
+        int page[kPagesPerBlock];
+        const int bad = pages.block(j, a.num_pages, lane, page);
+        if (gb >= kStagesK) {
+          const bool w = wait(sm, &sm.k_empty[st], (gb / kStagesK - 1) & 1);
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
           }
         }
-        int page[kPagesPerBlock], bad = 0;
-#pragma unroll
-        for (int pp = 0; pp < kPagesPerBlock; ++pp) {
-          const int e = __shfl_sync(0xffffffffu, ent, at + pp);
-          page[pp] = -1;  // outside the pool: TMA fills the box with zeros
-          if (j * kPagesPerBlock + pp < npages) {
-            if (e >= 0 && e < a.num_pages)
-              page[pp] = e;
-            else
-              bad |= 1 << pp;
-          }
-        }
         if (elect_one()) {
           if (bad) report(a.status, PKV_DEV_BAD_PAGE);
-          sm.kv_bad[st] = bad;
-          mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
+          sm.page_bad[st] = bad;
+          mbar_arrive_expect_tx(&sm.k_full[st], kTileBytes);
 #pragma unroll
-          for (int pp = 0; pp < kPagesPerBlock; ++pp)
-            tma_load_3d(sm.k[st] + pp * kBox, &a.tmap_k, 0, x.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
-#pragma unroll
-          for (int pp = 0; pp < kPagesPerBlock; ++pp)
-            tma_load_3d(sm.v[st] + pp * kBox, &a.tmap_v, 0, x.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
+          for (int i = 0; i < kPagesPerBlock; ++i)
+            tma_load_3d(sm.k[st] + i * kBox, &a.tmap_k, 0, y, page[i], &sm.k_full[st], policy);
         }
         __syncwarp();
       }
-      ++k;
     }
     // every copy issued has landed before the CTA exits
-    if (lane == 0) {
-      for (unsigned j = gb > kStages ? gb - kStages : 0; j < gb; ++j)
-        bounded_wait(&sm.kv_full[j % kStages], (j / kStages) & 1);
-      for (int j = k > 2 ? k - 2 : 0; j < k; ++j) bounded_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
+    if (lane == 0)
+      for (unsigned j = gb > kStagesK ? gb - kStagesK : 0; j < gb; ++j)
+        bounded_wait(&sm.k_full[j % kStagesK], (j / kStagesK) & 1);
+    if (lane == 0)
+      for (int j = loads > 2 ? loads - 2 : 0; j < loads; ++j) bounded_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
+    __syncwarp();
+  } else if (warp == kLoadWarpV) {
+    // ================= V loader =================
+    const uint64_t once = policy_evict_first(), again = policy_evict_last();
+    if (lane == 0) prefetch_tensormap(&a.tmap_v);
+    unsigned gb = 0;
+    bool ok = true, waited = false;
+    for (int k = 0; ok; ++k) {
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
+      if (!__all_sync(0xffffffffu, w)) break;
+      const Segment &x = sm.seg[k % kSegments];
+      if (x.s < 0) break;
+      Pages pages;
+      pages.start(a, x, lane);
+      if (!waited) griddep_wait();
+      waited = true;
+      const uint64_t policy = x.n > kTok ? again : once;
+      const int j1 = x.j1, y = x.g * kPageTokens;
+      for (int j = x.j0; j < j1; ++j, ++gb) {
+        const int st = int(gb % kStagesV);
+        int page[kPagesPerBlock];
+        pages.block(j, a.num_pages, lane, page);
+        if (gb >= kStagesV) {
+          w = wait(sm, &sm.v_empty[st], (gb / kStagesV - 1) & 1);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.v_full[st], kTileBytes);
+#pragma unroll
+          for (int i = 0; i < kPagesPerBlock; ++i)
+            tma_load_3d(sm.v[st] + i * kBox, &a.tmap_v, 0, y, page[i], &sm.v_full[st], policy);
+        }
+        __syncwarp();
+      }
     }
+    if (lane == 0)
+      for (unsigned j = gb > kStagesV ? gb - kStagesV : 0; j < gb; ++j)
+        bounded_wait(&sm.v_full[j % kStagesV], (j / kStagesV) & 1);
     __syncwarp();
   } else if (warp == kScoreWarp) {
     // ================= S = Q K^T (one thread issues, the warp waits) =================
+    griddep_wait();  // nothing to do before the loaders; its waits are not to run out on the kernel before
     const uint64_t q_desc = sw128_desc(smem_addr(sm.q), 16, 1024),
                    k_desc = sw128_desc(smem_addr(sm.k), 16, 1024);  // a later address adds to the low bits
     unsigned gb = 0;  // blocks issued
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int qb = k & 1;
-      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
       const Segment &x = sm.seg[k % kSegments];
       if (x.s < 0) break;
       const int blocks = x.j1 - x.j0;
-      w = wait(sm, &sm.q_full[qb], uint32_t(k / 2) & 1, a.status);
+      w = wait(sm, &sm.q_full[k & 1], uint32_t(k / 2) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
-      const uint64_t qdesc = q_desc + uint32_t(qb * kRows * kRowBytes >> 4);
+      const uint64_t qdesc = q_desc + uint32_t((k & 1) * kRows * kRowBytes >> 4);
       for (int j = 0; j < blocks; ++j, ++gb) {
-        const int st = int(gb % kStages), b = int(gb % kScores), f = int(gb % (2 * kScores));
-        w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status);
-        if (w && gb >= kScores) w = wait(sm, &sm.p_free[b], (gb / kScores - 1) & 1, a.status);
+        const int st = int(gb % kStagesK), b = int(gb % kScores), f = int(gb % (2 * kScores));
+        w = wait(sm, &sm.k_full[st], (gb / kStagesK) & 1);
+        if (w && gb >= kScores) w = wait(sm, &sm.p_free[b], (gb / kScores - 1) & 1);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -682,9 +756,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tmem + b * kKeys, qdesc + kk * (32 >> 4), kdesc + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
           tc_commit(&sm.s_full[f]);
-          sm.block_bad[f] = sm.kv_bad[st];
-          mbar_arrive(&sm.s_full[f]);  // passes on what this thread has seen: the block's load, its bad pages
-          if (j == blocks - 1) tc_commit(&sm.q_empty[qb]);  // the segment's last read of its Q
+          sm.block_bad[f] = sm.page_bad[st];
+          mbar_arrive(&sm.s_full[f]);  // passes block_bad on
+          tc_commit(&sm.k_empty[st]);
+          if (j == blocks - 1) tc_commit(&sm.q_empty[k & 1]);  // the segment's last read of its Q
         }
         __syncwarp();
       }
@@ -697,21 +772,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     __syncwarp();
   } else if (warp == kValueWarp) {
     // ================= O += P V (one thread issues, the warp waits) =================
+    griddep_wait();
     const uint64_t v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
     unsigned gb = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
       const Segment &x = sm.seg[k % kSegments];
       if (x.s < 0) break;
       const int blocks = x.j1 - x.j0;
       for (int j = 0; j < blocks; ++j, ++gb) {
-        const int st = int(gb % kStages), b = int(gb % kScores);
-        w = wait(sm, &sm.kv_full[st], (gb / kStages) & 1, a.status) &&
-            wait(sm, &sm.p_full[b], (gb / kScores) & 1, a.status);
+        const int st = int(gb % kStagesV), b = int(gb % kScores);
+        w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1) &&
+            wait(sm, &sm.p_full[b], (gb / kScores) & 1);
         // a segment's first product overwrites O, once every softmax warp has read the one before
-        if (w && j == 0 && k > 0) w = wait(sm, &sm.o_free, uint32_t(k - 1) & 1, a.status);
+        if (w && j == 0 && k > 0) w = wait(sm, &sm.o_free, uint32_t(k - 1) & 1);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -726,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
               tc_mma_tmem_a(tmem + kColO, tmem + b * kKeys + (kk >> 1) * 32 + (kk & 1) * 8 + term * 16,
                             vdesc + kk * (2048 >> 4), kIdescPV, (j == 0 && kk == 0 && term == 0) ? 0u : 1u);
           tc_commit(&sm.p_free[b]);
-          tc_commit(&sm.kv_empty[st]);
+          tc_commit(&sm.v_empty[st]);
           if (j == blocks - 1) tc_commit(&sm.o_full);
         }
         __syncwarp();
@@ -739,164 +815,175 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     __syncwarp();
   } else {
     // ================= softmax: warp = (quarter of the lanes, group), thread = row =================
+    regs_inc<kRegsSoftmax>();
     griddep_wait();  // the mask and every global write come after the kernel before this one
     zero_invalid(tid, kSoftThreads);
     const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;  // half: the group, and dims 32 half .. + 31
     const uint32_t my_tmem = tmem + (uint32_t(32 * quarter) << 16);
-    const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
     unsigned gb0 = 0;  // blocks before the segment
-    int ends = 0;      // segments in which this warp had rows (the two warps of a quarter agree)
+    int turns = 0;     // segments in which this warp has had rows (the two warps of a quarter agree)
     int cuts = 0;      // bit 0, 1: the share's first, last unit is cut
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) break;
+    // A segment ends while the next one's first block is under way: its sums are posted, and once that block's P is
+    // stored finish() divides and writes its rows (or their partial state).
+    bool pending = false;
+    // Segment k's end for this warp: a row's sums meet; this thread has the row's dims 32 half .. + 31.
+    auto finish = [&](int k) {
       const Segment &x = sm.seg[k % kSegments];
-      if (x.s < 0) break;
-      const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, j0 = x.j0, j1 = x.j1;
-      const bool active = octet * kOctet < x.n - x.tile * kTok;  // the warp has rows
-      // this thread's row, valid where `real`
-      const int node = x.tile * kTok + octet * kOctet + (lane >> 2);
+      const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, pos0 = x.j0 * kKeys, pos1 = min(x.ctx, x.j1 * kKeys);
+      const bool active = octet * kOctet < x.n - x.tile * kTok;
+      const int node = x.tile * kTok + octet * kOctet + (lane >> 2), t = turns - 1;
       const bool real = node < x.n;
-      if (real && j1 * kKeys > base)  // the mask word of the segment's first node key, needed at its end
-        prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
-      const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
-      float ref = 0.f;
-      float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
-      bool seen = false;
-      if (active && !leads) {
-        w = wait(sm, &sm.ref_full[quarter], uint32_t(ends) & 1, a.status);
-        if (!__all_sync(0xffffffffu, w)) break;
-        ref = sm.ref[ends & 1][row];
-        minus_r = make_float2(-ref, -ref);
-      }
-      for (int j = j0 + (leads ? 0 : 1); j < j1; j += 2) {
-        const unsigned gb = gb0 + unsigned(j - j0);
-        const int b = int(gb % kScores), f = int(gb % (2 * kScores)), key0 = j * kKeys;
-        w = wait(sm, &sm.s_full[f], (gb / (2 * kScores)) & 1, a.status);
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
-        if (key0 + kKeys > base) {
-          // the block holds nodes: the group's threads look through V, two to a row
-          const int st = int(gb % kStages), r = (tid & 127) >> 1, pos = key0 + r;
-          uint8_t *vrow = sm.v[st] + r * kRowBytes;
-          bool inf = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            inf |= nonfinite_chunk(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
-          inf = inf && pos >= base && pos < x.ctx;
-          inf |= __shfl_xor_sync(0xffffffffu, int(inf), 1) != 0;
-          if (pos >= x.ctx || inf) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          if (inf) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
-          fence_proxy_async_smem();
-        }
-        if (active) {
-          tc_fence_after();
-          const uint32_t taddr = my_tmem + b * kKeys;
-          const int bad = sm.block_bad[f];
-          const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
-          uint32_t see0 = ~0u, see1 = ~0u;
-          if (masked) {
-            if (key0 + kKeys > base) {
-              const uint32_t *mask = a.mask + (long long)(x.q0 + node) * a.mask_stride;
-              see0 = real ? window_bits(mask, key0, base, x.ctx, x.n) : 0u;
-              see1 = real ? window_bits(mask, key0 + 32, base, x.ctx, x.n) : 0u;
-            }
-            if (bad & 1) see0 &= 0xffff0000u;
-            if (bad & 2) see0 &= 0x0000ffffu;
-            if (bad & 4) see1 &= 0xffff0000u;
-            if (bad & 8) see1 &= 0x0000ffffu;
-          }
-          seen |= (see0 | see1) != 0u;
-          if (j == j0) {
-            ref = block_reference(taddr, see0, see1, c2.x);
-            minus_r = make_float2(-ref, -ref);
-            sm.ref[ends & 1][row] = ref;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ref_full[quarter]);
-          }
-          if (masked)
-            block_weights<kBf16, true>(taddr, see0, see1, c2, minus_r, l2);
-          else
-            block_weights<kBf16, false>(taddr, 0u, 0u, c2, minus_r, l2);
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[b]);
-      }
-      if (!ok) break;
-      gb0 += unsigned(j1 - j0);
-      if (j0 != 0 || j1 != x.nb) {
-        const int i = j0 == 0 ? 1 : 0;  // the share's last unit goes on in the next, its first began before
-        cuts |= 1 << i;
-        if (tid == 0) sm.cuts[i] = x;
-      }
-      // ---- the segment's end: a row's sums meet; this thread has its dims 32 half .. + 31 ----
-      float L = l2.x + l2.y;
-      if (active) {
-        sm.sums[ends & 1][half][row] = make_float2(L, seen ? 1.f : 0.f);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sums_full[quarter]);
-        w = wait(sm, &sm.sums_full[quarter], uint32_t(ends) & 1, a.status);
-        const float2 other = sm.sums[ends & 1][half ^ 1][row];
-        ++ends;
-        L += other.x;
-        seen |= other.y != 0.f;
-      }
-      w = wait(sm, &sm.o_full, uint32_t(k) & 1, a.status) && w;
-      if (!__all_sync(0xffffffffu, w)) break;
-      float r[32];
+      bool w = wait(sm, &sm.o_full, uint32_t(k) & 1);
+      if (active) w = wait(sm, &sm.sums_full[quarter], uint32_t(t) & 1) && w;
+      if (!__all_sync(0xffffffffu, w)) return false;
+      uint32_t u[32];
       if (active) {
         tc_fence_after();
-        uint32_t u[32];
         tmem_ld32(my_tmem + kColO + half * 32, u);
-#pragma unroll
-        for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]);
         tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free);
-      if (!active) continue;
-      const int h = x.g * kGroup + (lane & 3);
-      const long long qrow = (long long)x.q0 + node;
+      if (!active) return true;
+      float L = sm.sums[t & 3][0][row] + sm.sums[t & 3][1][row], ref = sm.ref[t & 3][row], r[32];
       float z = 0.f;  // NaN when the row of O is not finite
 #pragma unroll
-      for (int d = 0; d < 32; ++d) z += r[d] * 0.f;
-      if (real && seen && (!(L >= kSumMin && L <= kSumMax) || z != 0.f ||
-                           *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k)) {
+      for (int d = 0; d < 32; ++d) {
+        r[d] = __uint_as_float(u[d]);
+        z += r[d] * 0.f;
+      }
+      const int h = x.g * kGroup + (lane & 3);
+      const long long qrow = (long long)x.q0 + node;
+      if (real && (!(L >= kSumMin && L <= kSumMax) || z != 0.f ||
+                   *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k) &&
+          (L != 0.f || sees_any(a.mask + qrow * a.mask_stride, pos0, pos1, base, x.n))) {
         float o[32];
         const float2 rl = redo_row(a.k_base, a.v_base, a.page_stride, a.num_pages,
                                    a.block_tables + (long long)x.s * a.bt_stride, a.mask + qrow * a.mask_stride,
-                                   a.q + (qrow * kQHeads + h) * kHeadDim, x.g, j0 * kKeys, min(x.ctx, j1 * kKeys), base,
-                                   c2.x, half * 32, o);
+                                   a.q + (qrow * kQHeads + h) * kHeadDim, x.g, pos0, pos1, base, a.c.x, half * 32, o);
         ref = rl.x;
         L = rl.y;
 #pragma unroll
         for (int d = 0; d < 32; ++d) r[d] = o[d];
       }
-      const long long out_at = (qrow * kQHeads + h) * kHeadDim + half * 32;
-      if (j0 == 0 && j1 == x.nb) {
+      if (!real) return true;
+      if (x.j0 == 0 && x.j1 == x.nb) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
         for (int d = 0; d < 32; ++d) r[d] *= inv;
-        if (real) write_row<kBf16>(a.out, out_at, r);
-        continue;
-      }
-      // ---- cut unit: a partial state; its ticket is taken at the end ----
-      if (real) {
-        Part &part = a.parts[2 * cta + (j0 == 0 ? 1 : 0)];
+        write_row<kBf16>(a.out, (qrow * kQHeads + h) * kHeadDim + half * 32, r);
+      } else {
+        // a cut unit: a partial state; its ticket is taken when the share is done
+        Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
         const int at = octet * 32 + lane;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           __stcg(&part.o[half * 8 + i][at], make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
         __stcg(&part.rl[half][at], make_float2(ref, L));
       }
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
+      if (!__all_sync(0xffffffffu, w)) break;
+      const Segment &x = sm.seg[k % kSegments];
+      const bool more = x.s >= 0;  // if not, one round of the loop below ends the last segment
+      const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, j0 = more ? x.j0 : 0, j1 = more ? x.j1 : 0;
+      const bool active = more && octet * kOctet < x.n - x.tile * kTok;  // the warp has rows
+      // this thread's row, valid where `real`
+      const int node = x.tile * kTok + octet * kOctet + (lane >> 2);
+      const bool real = active && node < x.n;
+      if (real && j1 * kKeys > base)  // the mask word of the segment's first node key, needed at its end
+        prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
+      const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
+      float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
+      for (int j = j0 + (leads ? 0 : 1); ok && (j < j1 || pending); j += 2) {
+        const unsigned gb = gb0 + unsigned(j - j0);
+        const int b = int(gb % kScores), f = int(gb % (2 * kScores)), key0 = j * kKeys;
+        if (j < j1) {
+          w = wait(sm, &sm.s_full[f], (gb / (2 * kScores)) & 1);
+          if (w && key0 + kKeys > base) {
+            // the block holds nodes: the group's threads look through V, two to a row
+            const int st = int(gb % kStagesV), r = (tid & 127) >> 1, pos = key0 + r;
+            w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1);  // (the phase before has been consumed)
+            __syncwarp();
+            uint8_t *vrow = sm.v[st] + r * kRowBytes;
+            bool inf = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              inf |= nonfinite_chunk(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
+            inf = inf && pos >= base && pos < x.ctx;
+            inf |= __shfl_xor_sync(0xffffffffu, int(inf), 1) != 0;
+            if (pos >= x.ctx || inf) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (inf) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
+            fence_proxy_async_smem();
+          }
+          if (active && j > j0 && j == j0 + 1) {  // (this group does not lead: the row's reference is the other's)
+            w = wait(sm, &sm.ref_full[quarter][turns & 1], uint32_t(turns >> 1) & 1) && w;
+            const float ref = sm.ref[turns & 3][row];
+            minus_r = make_float2(-ref, -ref);
+          }
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          if (active) {
+            tc_fence_after();
+            const uint32_t taddr = my_tmem + b * kKeys;
+            const int bad = sm.block_bad[f];
+            const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
+            uint32_t see0 = ~0u, see1 = ~0u;
+            if (masked) {
+              if (key0 + kKeys > base) {
+                const uint32_t *mask = a.mask + (long long)(x.q0 + node) * a.mask_stride;
+                see0 = real ? window_bits(mask, key0, base, x.ctx, x.n) : 0u;
+                see1 = real ? window_bits(mask, key0 + 32, base, x.ctx, x.n) : 0u;
+              }
+              if (bad & 1) see0 &= 0xffff0000u;
+              if (bad & 2) see0 &= 0x0000ffffu;
+              if (bad & 4) see1 &= 0xffff0000u;
+              if (bad & 8) see1 &= 0x0000ffffu;
+            }
+            if (j == j0) {
+              const float ref = block_reference(taddr, see0, see1, a.c.x);
+              minus_r = make_float2(-ref, -ref);
+              sm.ref[turns & 3][row] = ref;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.ref_full[quarter][turns & 1]);
+            }
+            if (masked)
+              block_weights<kBf16, true>(taddr, see0, see1, a.c, minus_r, l2);
+            else
+              block_weights<kBf16, false>(taddr, 0u, 0u, a.c, minus_r, l2);
+            tc_fence_before();
+          }
+        }
+        if (pending) {
+          ok = finish(k - 1);
+          pending = false;
+        }
+        __syncwarp();
+        if (j < j1 && lane == 0) mbar_arrive(&sm.p_full[b]);
+      }
+      if (!ok || !more) break;
+      gb0 += unsigned(j1 - j0);
+      if (j0 != 0 || j1 != x.nb) {
+        const int i = j0 == 0 ? 1 : 0;  // the share's last unit goes on in the next, its first began before
+        cuts |= 1 << i;
+        if (tid == 0) sm.cuts[i] = x;
+      }
+      if (active) {
+        sm.sums[turns & 3][half][row] = l2.x + l2.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sums_full[quarter]);
+        ++turns;
+      }
+      pending = true;
     }
     // ---- the tickets of the cut units: the CTA that takes a unit's last one merges its parts; in a unit of
     // many parts first the parts of a group, then the CTA with the last group the groups ----
@@ -953,6 +1040,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && sm.abort) report(a.status, PKV_DEV_TIMEOUT);
   if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -1049,7 +1137,7 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   a.max_query = max_query;
   a.max_context = max_context;
   a.max_tiles = tiles;
-  a.scale_log2 = scale * pkv::kLog2e;
+  a.c = make_float2(scale * pkv::kLog2e, scale * pkv::kLog2e);
   a.parts = static_cast<pkv::Part *>(workspace);
   a.tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + 2 * size_t(pkv::kMaxCtas) * sizeof(pkv::Part));
   a.status = device_status;
