@@ -31,7 +31,7 @@
 //  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits; two
 //    products); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
 //    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
-//  * Masks: a key a row may not see gets weight 0 by selection, so a NaN score stays out.  V rows at or
+//  * Masks: the score of a key a row may not see is replaced by an infinity, so a NaN score stays out.  V rows at or
 //    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
 //    NaN or an infinity (0 * NaN in the product would reach every row); the segment's rows are then
 //    computed again by redo_row().
@@ -77,6 +77,7 @@ constexpr uint32_t kColO = kScores * kKeys;         // S buffers at columns 0, 6
 constexpr int kMergeGroup = 5;                      // a unit in more parts than this merges groups of them first
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSumMin = 5.42101086e-20f, kSumMax = 1.84467441e19f;  // 2^-64, 2^64
+constexpr float kSumPlain = 1048576.f;              // 2^20: up to here O is finite unless V is about to be not
 
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, false);     // B = K rows (K-major)
 constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows (MN-major)
@@ -146,6 +147,10 @@ struct Segment {
 // these one segment ahead of the softmax warps: place k is free when segment k + 16 is written to it.
 constexpr int kSegments = 16;
 
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return (long long)((unsigned long long)a / (unsigned long long)b);
+}
+
 // Walk over the segments of a CTA's share.  (It keeps little between segments and reads a sequence's lengths
 // again for each: the loader has few registers.)
 struct Walk {
@@ -154,18 +159,20 @@ struct Walk {
   __device__ bool next(const TreeArgs &a, Segment &x) {
     Seq seq;
     seq.load(a, s);
+#pragma unroll 1
     while (pos < end) {
+#pragma unroll 1
       while (pos - first >= seq.entries()) {
         first += seq.entries();
         seq.load(a, ++s);
       }
-      const long long len = seq.nb + kUnitCost, u = (pos - first) / len, v0 = pos - first - u * len;
+      const long long len = seq.nb + kUnitCost, u = divide(pos - first, len), v0 = pos - first - u * len;
       const long long v1 = min(len, v0 + (end - pos));
       pos += v1 - v0;
       if (v1 <= kUnitCost) continue;  // nothing but the unit's weight
       x.s = s;
-      x.g = int(u / seq.tiles);
-      x.tile = int(u % seq.tiles);
+      x.g = int(u) / seq.tiles;  // (8 heads x at most 2^15 tiles)
+      x.tile = int(u) - x.g * seq.tiles;
       x.q0 = seq.q0;
       x.n = seq.n;
       x.ctx = seq.ctx;
@@ -197,6 +204,7 @@ struct __align__(1024) Smem {
   uint64_t mma_done[2];
   Segment seg[kSegments];
   Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
+  int cut_first[2], cut_parts[2];  // CTA with the unit's first part; parts
   int merge[2];     // this CTA took the last ticket of the cut unit (1) or of its group of parts (2)
   int page_bad[kStagesK];      // bit pp: page pp of the K stage's block is invalid (loaded as zeros)
   int block_bad[2 * kScores];  // the same for the block whose S is in s_full's place
@@ -210,8 +218,18 @@ struct __align__(1024) Smem {
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 
-// CTA that owns entry p of the list when T entries are split over G CTAs.
-__device__ __forceinline__ int cta_of_entry(long long p, long long T, int G) { return int(((p + 1) * G - 1) / T); }
+// T list entries over G CTAs: each has `each`, the first `more` of them one more.
+struct Shares {
+  long long each;
+  int more;
+  __device__ long long first(int cta) const { return cta * each + min(cta, more); }
+  // CTA that has entry p
+  __device__ int owner(long long p) const {
+    const long long big = more * (each + 1);
+    const bool in_big = p < big;
+    return int(divide(in_big ? p : p - big, in_big ? each + 1 : each)) + (in_big ? 0 : more);
+  }
+};
 
 // Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
 constexpr unsigned kWaitCycles = 3800000000u;
@@ -223,6 +241,7 @@ __device__ __forceinline__ unsigned clock32() {
 __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned t0 = clock32();
+#pragma unroll 1
   while (!mbar_try_wait(bar, parity))
     if (clock32() - t0 > kWaitCycles) return false;
   return true;
@@ -233,6 +252,7 @@ __device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned t0 = clock32();
   volatile int *abort = &sm.abort;
+#pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
     if (clock32() - t0 > kWaitCycles) *abort = 1;
     if (*abort) return false;
@@ -241,18 +261,14 @@ __device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity) {
 }
 
 // P = 2^(c s - r) of 16 keys as bf16 terms, two keys to a word: hi, and with fp32 output lo.  `sum` takes the
-// fp32 weights.  With kMasked a key whose bit in `see` is clear gets 0 by selection (its score may be NaN).
-template <bool kBf16, bool kMasked>
-__device__ __forceinline__ void weights(const uint32_t (&s)[16], uint32_t see, float2 c, float2 minus_r, float2 &sum,
+// fp32 weights.
+template <bool kBf16>
+__device__ __forceinline__ void weights(const uint32_t (&s)[16], float2 c, float2 minus_r, float2 &sum,
                                         uint32_t (&hi)[8], uint32_t (&lo)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c, minus_r);
-    float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-    if (kMasked) {
-      p.x = see >> (2 * i) & 1u ? p.x : 0.f;
-      p.y = see >> (2 * i + 1) & 1u ? p.y : 0.f;
-    }
+    const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
     sum = add_f32x2(sum, p);
     hi[i] = pack_bf16x2(p.x, p.y);
     if constexpr (!kBf16) {
@@ -262,53 +278,58 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[16], uint32_t see, f
   }
 }
 
-// P of 16 keys to the S columns of keys 16i and on: of each 32 columns, hi in the first 16, lo in the others.
+// The weights of a row's 64 keys, from S to P in place: of each 32 keys, hi in the first 16 columns, lo in the
+// others.  16 keys at a time: the next 16 scores are on their way while these are worked on, and P of 16
+// keys is stored once the scores that lay there have been read.
 template <bool kBf16>
-__device__ __forceinline__ void store_weights(uint32_t taddr, int i, const uint32_t (&hi)[8], const uint32_t (&lo)[8]) {
-  const uint32_t col = taddr + (i >> 1) * 32 + (i & 1) * 8;
-  tmem_st8_async(col, hi);
-  if constexpr (!kBf16) tmem_st8_async(col + 16, lo);
-}
-
-// The weights of a row's 64 keys, from S to P in place.  16 keys at a time: the next 16 scores are on their way
-// while these are worked on, and P of 16 keys is stored once the scores that lay there have been read.
-template <bool kBf16, bool kMasked>
-__device__ __forceinline__ void block_weights(uint32_t taddr, uint32_t see0, uint32_t see1, float2 c, float2 minus_r,
-                                              float2 &sum) {
+__device__ __forceinline__ void block_weights(uint32_t taddr, float2 c, float2 minus_r, float2 &sum) {
   uint32_t a[16], b[16], hi[8], lo[8];
   tmem_ld16_async(taddr, a);
   tmem_ld_wait(a);
-  tmem_ld16_async(taddr + 16, b);
-  weights<kBf16, kMasked>(a, see0, c, minus_r, sum, hi, lo);
-  tmem_ld_wait(b);
-  store_weights<kBf16>(taddr, 0, hi, lo);
-  tmem_ld16_async(taddr + 32, a);
-  weights<kBf16, kMasked>(b, see0 >> 16, c, minus_r, sum, hi, lo);
-  tmem_ld_wait(a);
-  store_weights<kBf16>(taddr, 1, hi, lo);
-  tmem_ld16_async(taddr + 48, b);
-  weights<kBf16, kMasked>(a, see1, c, minus_r, sum, hi, lo);
-  tmem_ld_wait(b);
-  store_weights<kBf16>(taddr, 2, hi, lo);
-  weights<kBf16, kMasked>(b, see1 >> 16, c, minus_r, sum, hi, lo);
-  store_weights<kBf16>(taddr, 3, hi, lo);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i, taddr += 32) {
+    tmem_ld16_async(taddr + 16, b);
+    weights<kBf16>(a, c, minus_r, sum, hi, lo);
+    tmem_ld_wait(b);
+    tmem_st8_async(taddr, hi);
+    if constexpr (!kBf16) tmem_st8_async(taddr + 16, lo);
+    if (i == 0) tmem_ld16_async(taddr + 32, a);
+    weights<kBf16>(b, c, minus_r, sum, hi, lo);
+    tmem_ld_wait(a);
+    tmem_st8_async(taddr + 8, hi);
+    if constexpr (!kBf16) tmem_st8_async(taddr + 24, lo);
+  }
   tmem_st_wait();
 }
 
-// A row's reference: the largest exponent among the visible keys of a block, 0 if there is none that is finite.
-__device__ __forceinline__ float block_reference(uint32_t taddr, uint32_t see0, uint32_t see1, float c) {
-  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+// The scores of keys a row may not see (bit clear in see0, see1: 32 keys each) become the infinity whose weight is 0.
+__device__ __forceinline__ void hide_keys(uint32_t taddr, uint32_t see0, uint32_t see1, float c) {
+  const uint32_t hidden = c < 0.f ? 0x7f800000u : 0xff800000u;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i, taddr += 16) {
     uint32_t s[16];
-    tmem_ld16_async(taddr + 16 * i, s);
+    tmem_ld16_async(taddr, s);
     tmem_ld_wait(s);
-    const uint32_t see = (i < 2 ? see0 : see1) >> (16 * (i & 1));
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      top[j & 3] = fmaxf(top[j & 3], see >> j & 1u ? __uint_as_float(s[j]) * c : -INFINITY);
+    for (int j = 0; j < 16; ++j) s[j] = see0 >> j & 1u ? s[j] : hidden;
+    see0 = i == 1 ? see1 : see0 >> 16;
+    tmem_st16_async(taddr, s);
   }
-  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  tmem_st_wait();
+}
+
+// A row's reference: the largest exponent of a block's keys, 0 if there is none that is finite.
+__device__ __forceinline__ float block_reference(uint32_t taddr, float c) {
+  float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i, taddr += 16) {
+    uint32_t s[16];
+    tmem_ld16_async(taddr, s);
+    tmem_ld_wait(s);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top[j & 1] = fmaxf(top[j & 1], __uint_as_float(s[j]) * c);
+  }
+  const float m = fmaxf(top[0], top[1]);
   return isfinite(m) ? m : 0.f;
 }
 
@@ -334,16 +355,16 @@ __device__ __forceinline__ uint32_t window_bits(const uint32_t *mask, int key0, 
 // Whether a row may see any of the keys pos .. end - 1 (a sum of 0 is right if not).
 __device__ __forceinline__ bool sees_any(const uint32_t *mask, int pos, int end, int base, int n) {
   if (pos < base) return true;
+#pragma unroll 1
   for (; pos < end; pos += 32)
     if (window_bits(mask, pos, base, end, n)) return true;
   return false;
 }
 
-__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-__device__ __forceinline__ bool nonfinite_chunk(const uint4 &x) {
-  return nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) || nonfinite_pair(x.w);
+// Bits 15, 31: the low, high bf16 of a word is a NaN or an infinity (its exponent is all ones).
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t nonfinite(const uint4 &x) {
+  return nonfinite(x.x) | nonfinite(x.y) | nonfinite(x.z) | nonfinite(x.w);
 }
 
 // The weight of a state (r, l) merged under the reference R; a state that has seen no key has l = 0.
@@ -356,19 +377,23 @@ __device__ __noinline__ float2 redo_row(const uint8_t *k_base, const uint8_t *v_
                                         int num_pages, const int32_t *table, const uint32_t *mask, const uint16_t *q,
                                         int g, int pos, int end, int base, float c, int d0, float *o) {
   float R = -INFINITY, L = 0.f;
+#pragma unroll 1
   for (int d = 0; d < 32; ++d) o[d] = 0.f;
+#pragma unroll 1
   for (; pos < end; ++pos) {
     const int page = __ldg(table + pos / kPageTokens), node = pos - base;
     if (page < 0 || page >= num_pages || (node >= 0 && !(__ldg(mask + (node >> 5)) >> (node & 31) & 1u))) continue;
     const long long at = (long long)page * page_stride + (g * kPageTokens + pos % kPageTokens) * kRowBytes;
     const uint32_t *k = reinterpret_cast<const uint32_t *>(k_base + at), *x = reinterpret_cast<const uint32_t *>(q);
     float dot = 0.f;
+#pragma unroll 1
     for (int i = 0; i < kHeadDim / 2; ++i) dot += bf16_lo(x[i]) * bf16_lo(k[i]) + bf16_hi(x[i]) * bf16_hi(k[i]);
     const float e = dot * c, Rn = fmaxf(R, e);
     const float keep = R == -INFINITY ? 0.f : exp2f(R - Rn), w = exp2f(e - Rn);
     R = Rn;
     L = L * keep + w;
     const uint32_t *v = reinterpret_cast<const uint32_t *>(v_base + at) + d0 / 2;
+#pragma unroll 1
     for (int i = 0; i < 16; ++i) {
       o[2 * i] = o[2 * i] * keep + w * bf16_lo(v[i]);
       o[2 * i + 1] = o[2 * i + 1] * keep + w * bf16_hi(v[i]);
@@ -393,22 +418,37 @@ __device__ __forceinline__ void write_row(void *out, long long at, const float (
   }
 }
 
+// Zeroes the rows of sequences whose lengths do not fit, spread over the CTAs (after griddep_wait).
+template <bool kBf16>
+__device__ __forceinline__ void zero_rows(const TreeArgs &a, int cta, int G, int tid) {
+#pragma unroll 1
+  for (int s = cta; s < a.num_seqs; s += G) {
+    Seq q;
+    q.load(a, s);
+    if (q.n == 0 || q.valid(a)) continue;
+    if (tid == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
+    const long long r0 = max((long long)q.q0, 0LL), r1 = min((long long)q.q0 + q.n, (long long)a.num_q_rows);
+    constexpr int kChunks = kQHeads * kHeadDim * (kBf16 ? 2 : 4) / 16;  // 16-byte chunks of a row
+#pragma unroll 1
+    for (long long i = r0 * kChunks + tid; i < r1 * kChunks; i += kThreads)
+      static_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // Merges `count` partial states of a unit whose first part is CTA c0's: those of CTAs c, c + stride, ...
 // Writes the unit's rows, or (dst, their first part) the merged state in its place: a thread overwrites only
-// what it has read itself, and the merged (reference, sum) have a place of their own.  kPad: the number of rows rounded up to 32, 64 or 128; a thread
-// has one row and an equal share of its dims, with kBatch * kVec loads of 16 bytes in flight.  (A call of its own
-// takes values: a reference to the kernel's arguments would be read through memory.)
-template <bool kBf16, int kPad>
-__device__ __noinline__ void merge_parts(const Part *parts, void *out, int c0, int c, int stride,
-                                         int count, int rows, long long row0, Part *dst, int tid) {
-  constexpr int kShare = kPad * (kHeadDim / 4) / kSoftThreads;  // 16-byte vectors of a row that a thread has
-  constexpr int kVec = kShare < 4 ? kShare : 4, kBatch = 12 / kVec;
-  const int at = tid % kPad;
+// what it has read itself, and the merged (reference, sum) have a place of their own.  A thread has one of the
+// rows (2^shift of them at the most) and 16 of its dims at a time, with kBatch * kVec loads of 16 bytes in flight.
+template <bool kBf16>
+__device__ __forceinline__ void merge_parts(const Part *parts, void *out, int c0, int c, int stride, int count, int rows,
+                                         int shift, long long row0, Part *dst, int tid) {
+  constexpr int kVec = 4, kBatch = 3;
+  const int at = tid & ((1 << shift) - 1);
   if (at >= rows) return;
 #pragma unroll 1
-  for (int d0 = tid / kPad * kShare, e = d0 + kShare; d0 < e; d0 += kVec) {
+  for (int d0 = (tid >> shift) * kVec; d0 < kHeadDim / 4; d0 += (kSoftThreads >> shift) * kVec) {
     const int half = d0 / (kHeadDim / 8);
-    float M = -INFINITY, L = 0.f;
+    float R = -INFINITY, L = 0.f;
     float r[4 * kVec];
 #pragma unroll
     for (int d = 0; d < 4 * kVec; ++d) r[d] = 0.f;
@@ -418,39 +458,41 @@ __device__ __noinline__ void merge_parts(const Part *parts, void *out, int c0, i
       float4 y[kBatch][kVec];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int q = c + (p + i) * stride;
-        const Part &part = parts[2 * q + (q == c0 ? 1 : 0)];
         const bool there = p + i < count;
-        rl[i] = there ? __ldcg(stride > 1 ? &part.group_rl[half][at] : &part.rl[half][at]) : make_float2(-INFINITY, 0.f);
+        const int q = c + (there ? p + i : p) * stride;
+        const Part &part = parts[2 * q + (q == c0 ? 1 : 0)];
+        rl[i] = __ldcg(stride > 1 ? &part.group_rl[half][at] : &part.rl[half][at]);
+        if (!there) rl[i].y = 0.f;  // weight 0
 #pragma unroll
-        for (int d = 0; d < kVec; ++d) y[i][d] = there ? __ldcg(&part.o[d0 + d][at]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int d = 0; d < kVec; ++d) y[i][d] = __ldcg(&part.o[d0 + d][at]);
       }
-      float Mn = M;
+      float Rn = R;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, rl[i].x);
-      const float keep = state_weight(make_float2(M, L), Mn);
+      for (int i = 0; i < kBatch; ++i) Rn = rl[i].y == 0.f ? Rn : fmaxf(Rn, rl[i].x);
+      const float keep = state_weight(make_float2(R, L), Rn);
       L *= keep;
 #pragma unroll
       for (int d = 0; d < 4 * kVec; ++d) r[d] *= keep;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float wgt = state_weight(rl[i], Mn);
-        L += rl[i].y * wgt;
+        const float w = state_weight(rl[i], Rn);
+        if (rl[i].y == 0.f) continue;  // (what it holds does not count, infinities included)
+        L += rl[i].y * w;
 #pragma unroll
         for (int d = 0; d < kVec; ++d) {
-          r[4 * d] += y[i][d].x * wgt;
-          r[4 * d + 1] += y[i][d].y * wgt;
-          r[4 * d + 2] += y[i][d].z * wgt;
-          r[4 * d + 3] += y[i][d].w * wgt;
+          r[4 * d] += y[i][d].x * w;
+          r[4 * d + 1] += y[i][d].y * w;
+          r[4 * d + 2] += y[i][d].z * w;
+          r[4 * d + 3] += y[i][d].w * w;
         }
       }
-      M = Mn;
+      R = Rn;
     }
     if (dst != nullptr) {
 #pragma unroll
       for (int d = 0; d < kVec; ++d)
         __stcg(&dst->o[d0 + d][at], make_float4(r[4 * d], r[4 * d + 1], r[4 * d + 2], r[4 * d + 3]));
-      if (d0 % (kHeadDim / 8) == 0) __stcg(&dst->group_rl[half][at], make_float2(M, L));
+      if (d0 % (kHeadDim / 8) == 0) __stcg(&dst->group_rl[half][at], make_float2(R, L));
     } else {
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
@@ -470,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 
   // ---- blocks in the list, and this CTA's share of them ----
   long long mine = 0;
+#pragma unroll 1
   for (int s = tid; s < a.num_seqs; s += kThreads) {
     Seq q;
     q.load(a, s);
@@ -479,31 +522,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) sm.warp_sums[warp] = mine;
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
     }
+#pragma unroll 1
     for (int i = 0; i < 2 * kScores; ++i) mbar_init(&sm.s_full[i], 2);
+#pragma unroll 1
     for (int i = 0; i < kScores; ++i) {
       mbar_init(&sm.p_full[i], kSoftWarps / 2);
       mbar_init(&sm.p_free[i], 1);
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, kSoftWarps);
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sm.ref_full[i][0], 1);
       mbar_init(&sm.ref_full[i][1], 1);
       mbar_init(&sm.sums_full[i], 2);
       sm.nonfinite[i] = -1;
     }
+#pragma unroll 1
     for (int i = 0; i < kStagesK; ++i) {
       mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kStagesV; ++i) {
       mbar_init(&sm.v_full[i], 1);
       mbar_init(&sm.v_empty[i], 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1);
     mbar_init(&sm.mma_done[0], 1);
     mbar_init(&sm.mma_done[1], 1);
@@ -513,32 +563,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   }
   __syncthreads();
   long long T = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) T += sm.warp_sums[w];
-  const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));
+  const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));  // CTAs with a share
 
-  // rows of sequences whose lengths do not fit, spread over the CTAs (a global write: after griddep_wait)
-  auto zero_invalid = [&](int t, int threads) {
-    for (int s = cta; s < a.num_seqs; s += G) {
-      Seq q;
-      q.load(a, s);
-      if (q.n == 0 || q.valid(a)) continue;
-      if (t == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
-      const long long r0 = max((long long)q.q0, 0LL), r1 = min((long long)q.q0 + q.n, (long long)a.num_q_rows);
-      constexpr int kChunks = kQHeads * kHeadDim * (kBf16 ? 2 : 4) / 16;  // 16-byte chunks of a row
-      for (long long i = r0 * kChunks + t; i < r1 * kChunks; i += threads)
-        static_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
   if (T == 0 || cta >= Gu) {
     griddep_launch_dependents();
     griddep_wait();
-    zero_invalid(tid, kThreads);
+    zero_rows<kBf16>(a, cta, G, tid);
     return;
   }
-  const long long pa = (long long)cta * T / Gu, pb = (long long)(cta + 1) * T / Gu;
+  Shares shares;
+  shares.each = divide(T, Gu);
+  shares.more = int(T - shares.each * Gu);
+  const long long pa = shares.first(cta), pb = shares.first(cta + 1);
 
   // ---- the sequence that holds block pa ----
   long long before = 0;
+#pragma unroll 1
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     __syncthreads();
     if (sm.found) break;
@@ -558,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     if (lane == 31) sm.warp_sums[warp] = x;
     __syncthreads();
     long long chunk = 0;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) x += sm.warp_sums[w];
       chunk += sm.warp_sums[w];
@@ -627,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     unsigned gb = 0;  // blocks issued
     int loads = 0;    // segments whose Q was asked for
     bool ok = true, waited = false;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       Segment &x = sm.seg[k % kSegments];
       const bool more = walk.next(a, x);  // every lane writes the same
@@ -641,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       if (elect_one()) {
         const int octets = (min(kTok, x.n - x.tile * kTok) + kOctet - 1) / kOctet;
         mbar_arrive_expect_tx(&sm.q_full[k & 1], uint32_t(octets * kOctetBytes));
+#pragma unroll 1
         for (int o = 0; o < octets; ++o)
           tma_load_3d(sm.q[k & 1] + ((o + k + turn) & 3) * kOctetBytes, &a.tmap_q, 0, x.g * kGroup,
                       x.q0 + x.tile * kTok + o * kOctet, &sm.q_full[k & 1], once);
@@ -655,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       waited = true;
       const uint64_t policy = x.n > kTok ? again : once;  // several tiles read the same K/V
       const int j1 = x.j1, y = x.g * kPageTokens;
+#pragma unroll 1
       for (int j = x.j0; j < j1; ++j, ++gb) {
         const int st = int(gb % kStagesK);
         int page[kPagesPerBlock];
@@ -679,9 +725,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     }
     // every copy issued has landed before the CTA exits
     if (lane == 0)
+#pragma unroll 1
       for (unsigned j = gb > kStagesK ? gb - kStagesK : 0; j < gb; ++j)
         bounded_wait(&sm.k_full[j % kStagesK], (j / kStagesK) & 1);
     if (lane == 0)
+#pragma unroll 1
       for (int j = loads > 2 ? loads - 2 : 0; j < loads; ++j) bounded_wait(&sm.q_full[j & 1], uint32_t(j / 2) & 1);
     __syncwarp();
   } else if (warp == kLoadWarpV) {
@@ -690,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     if (lane == 0) prefetch_tensormap(&a.tmap_v);
     unsigned gb = 0;
     bool ok = true, waited = false;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
@@ -701,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       waited = true;
       const uint64_t policy = x.n > kTok ? again : once;
       const int j1 = x.j1, y = x.g * kPageTokens;
+#pragma unroll 1
       for (int j = x.j0; j < j1; ++j, ++gb) {
         const int st = int(gb % kStagesV);
         int page[kPagesPerBlock];
@@ -722,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       }
     }
     if (lane == 0)
+#pragma unroll 1
       for (unsigned j = gb > kStagesV ? gb - kStagesV : 0; j < gb; ++j)
         bounded_wait(&sm.v_full[j % kStagesV], (j / kStagesV) & 1);
     __syncwarp();
@@ -732,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
                    k_desc = sw128_desc(smem_addr(sm.k), 16, 1024);  // a later address adds to the low bits
     unsigned gb = 0;  // blocks issued
     bool ok = true;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
@@ -741,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       w = wait(sm, &sm.q_full[k & 1], uint32_t(k / 2) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
       const uint64_t qdesc = q_desc + uint32_t((k & 1) * kRows * kRowBytes >> 4);
+#pragma unroll 1
       for (int j = 0; j < blocks; ++j, ++gb) {
         const int st = int(gb % kStagesK), b = int(gb % kScores), f = int(gb % (2 * kScores));
         w = wait(sm, &sm.k_full[st], (gb / kStagesK) & 1);
@@ -776,12 +829,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     const uint64_t v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
     unsigned gb = 0;
     bool ok = true;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
       const Segment &x = sm.seg[k % kSegments];
       if (x.s < 0) break;
       const int blocks = x.j1 - x.j0;
+#pragma unroll 1
       for (int j = 0; j < blocks; ++j, ++gb) {
         const int st = int(gb % kStagesV), b = int(gb % kScores);
         w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1) &&
@@ -817,7 +872,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     // ================= softmax: warp = (quarter of the lanes, group), thread = row =================
     regs_inc<kRegsSoftmax>();
     griddep_wait();  // the mask and every global write come after the kernel before this one
-    zero_invalid(tid, kSoftThreads);
     const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;  // half: the group, and dims 32 half .. + 31
     const uint32_t my_tmem = tmem + (uint32_t(32 * quarter) << 16);
     unsigned gb0 = 0;  // blocks before the segment
@@ -847,16 +901,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       if (lane == 0) mbar_arrive(&sm.o_free);
       if (!active) return true;
       float L = sm.sums[t & 3][0][row] + sm.sums[t & 3][1][row], ref = sm.ref[t & 3][row], r[32];
-      float z = 0.f;  // NaN when the row of O is not finite
 #pragma unroll
-      for (int d = 0; d < 32; ++d) {
-        r[d] = __uint_as_float(u[d]);
-        z += r[d] * 0.f;
-      }
+      for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]);
       const int h = x.g * kGroup + (lane & 3);
       const long long qrow = (long long)x.q0 + node;
-      if (real && (!(L >= kSumMin && L <= kSumMax) || z != 0.f ||
-                   *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k) &&
+      bool redo = !(L >= kSumMin && L <= kSumMax);
+      if (L > kSumPlain) {
+        float z = 0.f;  // NaN when the row of O is not finite
+#pragma unroll
+        for (int d = 0; d < 32; ++d) z += r[d] * 0.f;
+        redo |= z != 0.f;
+      }
+      if (real && (redo || *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k) &&
           (L != 0.f || sees_any(a.mask + qrow * a.mask_stride, pos0, pos1, base, x.n))) {
         float o[32];
         const float2 rl = redo_row(a.k_base, a.v_base, a.page_stride, a.num_pages,
@@ -865,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         ref = rl.x;
         L = rl.y;
 #pragma unroll
-        for (int d = 0; d < 32; ++d) r[d] = o[d];
+        for (int d = 0; d < 32; ++d) r[d] = o[d];  // (o lies in memory: few come here)
       }
       if (!real) return true;
       if (x.j0 == 0 && x.j1 == x.nb) {
@@ -884,6 +940,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       }
       return true;
     };
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
@@ -898,6 +955,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
       const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
       float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
+#pragma unroll 1
       for (int j = j0 + (leads ? 0 : 1); ok && (j < j1 || pending); j += 2) {
         const unsigned gb = gb0 + unsigned(j - j0);
         const int b = int(gb % kScores), f = int(gb % (2 * kScores)), key0 = j * kKeys;
@@ -909,11 +967,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
             w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1);  // (the phase before has been consumed)
             __syncwarp();
             uint8_t *vrow = sm.v[st] + r * kRowBytes;
-            bool inf = false;
+            uint32_t bits = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              inf |= nonfinite_chunk(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
-            inf = inf && pos >= base && pos < x.ctx;
+              bits |= nonfinite(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
+            bool inf = bits != 0 && pos >= base && pos < x.ctx;
             inf |= __shfl_xor_sync(0xffffffffu, int(inf), 1) != 0;
             if (pos >= x.ctx || inf) {
 #pragma unroll
@@ -937,8 +995,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
             const uint32_t taddr = my_tmem + b * kKeys;
             const int bad = sm.block_bad[f];
             const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
-            uint32_t see0 = ~0u, see1 = ~0u;
             if (masked) {
+              uint32_t see0 = ~0u, see1 = ~0u;
               if (key0 + kKeys > base) {
                 const uint32_t *mask = a.mask + (long long)(x.q0 + node) * a.mask_stride;
                 see0 = real ? window_bits(mask, key0, base, x.ctx, x.n) : 0u;
@@ -948,18 +1006,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
               if (bad & 2) see0 &= 0x0000ffffu;
               if (bad & 4) see1 &= 0xffff0000u;
               if (bad & 8) see1 &= 0x0000ffffu;
+              hide_keys(taddr, see0, see1, a.c.x);
             }
             if (j == j0) {
-              const float ref = block_reference(taddr, see0, see1, a.c.x);
+              const float ref = block_reference(taddr, a.c.x);
               minus_r = make_float2(-ref, -ref);
               sm.ref[turns & 3][row] = ref;
               __syncwarp();
               if (lane == 0) mbar_arrive(&sm.ref_full[quarter][turns & 1]);
             }
-            if (masked)
-              block_weights<kBf16, true>(taddr, see0, see1, a.c, minus_r, l2);
-            else
-              block_weights<kBf16, false>(taddr, 0u, 0u, a.c, minus_r, l2);
+            block_weights<kBf16>(taddr, a.c, minus_r, l2);
             tc_fence_before();
           }
         }
@@ -998,7 +1054,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       int merge = 0;
       if (cuts >> tid & 1 && *reinterpret_cast<volatile int *>(&sm.abort) == 0) {
         const Segment &u = sm.cuts[tid];
-        const int c0 = cta_of_entry(u.unit0, T, Gu), parts = cta_of_entry(u.unit0 + u.nb - 1, T, Gu) - c0 + 1;
+        int ends[2];
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) ends[i] = shares.owner(u.unit0 + (i ? u.nb - 1 : 0));
+        const int c0 = ends[0], parts = ends[1] - ends[0] + 1;
+        sm.cut_first[tid] = c0;
+        sm.cut_parts[tid] = parts;
         if (parts <= 2 * kMergeGroup) {
           merge = ticket_taken(a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g, parts - 1) ? 1 : 0;
         } else {
@@ -1014,33 +1075,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       int merge = sm.merge[i];
       if (merge == 0) continue;
       const Segment &u = sm.cuts[i];
-      const int c0 = cta_of_entry(u.unit0, T, Gu), parts = cta_of_entry(u.unit0 + u.nb - 1, T, Gu) - c0 + 1;
+      const int c0 = sm.cut_first[i], parts = sm.cut_parts[i];
       const int rows = min(kTok, u.n - u.tile * kTok) * kGroup;
       const long long row0 = ((long long)u.q0 + u.tile * kTok) * kQHeads + u.g * kGroup;
+      const int shift = rows <= 32 ? 5 : rows <= 64 ? 6 : 7;
       auto merge_rows = [&](int c, int stride, int count, Part *dst) {
-        if (rows <= 32)
-          merge_parts<kBf16, 32>(a.parts, a.out, c0, c, stride, count, rows, row0, dst, tid);
-        else if (rows <= 64)
-          merge_parts<kBf16, 64>(a.parts, a.out, c0, c, stride, count, rows, row0, dst, tid);
-        else
-          merge_parts<kBf16, 128>(a.parts, a.out, c0, c, stride, count, rows, row0, dst, tid);
+        merge_parts<kBf16>(a.parts, a.out, c0, c, stride, count, rows, shift, row0, dst, tid);
       };
-      if (merge == 1) {
-        merge_rows(c0, 1, parts, nullptr);
-        continue;
+      int c = c0, stride = 1, count = parts;  // what to merge: all parts, or first this CTA's group of them
+      Part *dst = nullptr;
+      if (merge == 2) {
+        const int lo = (cta - c0) / kMergeGroup * kMergeGroup;
+        c = c0 + lo;
+        count = min(kMergeGroup, parts - lo);
+        dst = &a.parts[2 * c + (lo == 0 ? 1 : 0)];
       }
-      const int lo = (cta - c0) / kMergeGroup * kMergeGroup, groups = (parts + kMergeGroup - 1) / kMergeGroup;
-      merge_rows(c0 + lo, 1, min(kMergeGroup, parts - lo), &a.parts[2 * (c0 + lo) + (lo == 0 ? 1 : 0)]);
-      named_barrier_sync(5, kSoftThreads);
-      if (tid == 0)
-        sm.merge[i] = ticket_taken(a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g, groups - 1) ? 1 : 0;
-      named_barrier_sync(5, kSoftThreads);
-      if (sm.merge[i]) merge_rows(c0, kMergeGroup, groups, nullptr);
+#pragma unroll 1
+      for (;;) {
+        merge_rows(c, stride, count, dst);
+        if (dst == nullptr) break;
+        c = c0;
+        stride = kMergeGroup;
+        count = (parts + kMergeGroup - 1) / kMergeGroup;
+        dst = nullptr;
+        named_barrier_sync(5, kSoftThreads);
+        if (tid == 0)
+          sm.merge[i] = ticket_taken(a.tickets + ((long long)u.s * a.max_tiles + u.tile) * kKvHeads + u.g, count - 1);
+        named_barrier_sync(5, kSoftThreads);
+        if (!sm.merge[i]) break;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort) report(a.status, PKV_DEV_TIMEOUT);
+  zero_rows<kBf16>(a, cta, G, tid);
   if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -1137,7 +1206,10 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   a.max_query = max_query;
   a.max_context = max_context;
   a.max_tiles = tiles;
-  a.c = make_float2(scale * pkv::kLog2e, scale * pkv::kLog2e);
+  // a scale of 0 (all weights alike) becomes one whose product with a finite score vanishes, and with an infinite one
+  // (a hidden key) does not
+  const float c = scale * pkv::kLog2e, least = 1e-42f;
+  a.c.x = a.c.y = fabsf(c) < least ? copysignf(least, c) : c;
   a.parts = static_cast<pkv::Part *>(workspace);
   a.tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + 2 * size_t(pkv::kMaxCtas) * sizeof(pkv::Part));
   a.status = device_status;
