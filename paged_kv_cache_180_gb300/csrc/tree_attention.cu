@@ -147,7 +147,9 @@ struct Segment {
 // these one segment ahead of the softmax warps: place k is free when segment k + 16 is written to it.
 constexpr int kSegments = 16;
 
+// Division of non-negative numbers; nearly always they have 32 bits.
 __device__ __forceinline__ long long divide(long long a, long long b) {
+  if ((a | b) >> 32 == 0) return unsigned(a) / unsigned(b);
   return (long long)((unsigned long long)a / (unsigned long long)b);
 }
 
@@ -193,15 +195,21 @@ struct __align__(1024) Smem {
   uint8_t v[kStagesV][kTileBytes];
   float ref[4][kRows];       // [turn]: a row's reference, from the group with the segment's first block
   float sums[4][2][kRows];   // [turn][group]: a row's sum
+  // barriers of one arrival ...
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
-  uint64_t s_full[2 * kScores];  // [block % 6], so that a group sees every phase of the ones it waits on
-  uint64_t p_full[kScores];      // the group's four warps have written their P of the buffer
   uint64_t p_free[kScores];      // the product of a block is done: its buffer may be written
-  uint64_t o_full, o_free;       // a segment's products are done; every softmax warp has read O
-  uint64_t ref_full[4][2], sums_full[4];  // per quarter of the lanes: ref (by turn), both sums are there
+  uint64_t o_full;               // a segment's products are done
+  uint64_t ref_full[4][2];       // per quarter of the lanes, by turn: ref is there
   uint64_t seg_full[kSegments];
   uint64_t mma_done[2];
+  // ... of two ...
+  uint64_t s_full[2 * kScores];  // [block % 6], so that a group sees every phase of the ones it waits on
+  uint64_t sums_full[4];         // per quarter: both sums are there
+  // ... of a group's four warps: they have written their P of the buffer ...
+  uint64_t p_full[kScores];
+  // ... and of all softmax warps: they have read O
+  uint64_t o_free;
   Segment seg[kSegments];
   Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
   int cut_first[2], cut_parts[2];  // CTA with the unit's first part; parts
@@ -210,9 +218,9 @@ struct __align__(1024) Smem {
   int block_bad[2 * kScores];  // the same for the block whose S is in s_full's place
   int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
                      // never more than two segments apart: O is written again when all have read it)
-  long long warp_sums[kThreads / 32];
+  long long warp_sums[2][kThreads / 32];
   long long first;  // list index of seq0's first entry
-  int seq0, found;
+  int seq0;
   uint32_t tmem_base;
   int abort;
 };
@@ -510,64 +518,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = int(gridDim.x), cta = int(blockIdx.x);
 
-  // ---- blocks in the list, and this CTA's share of them ----
-  long long mine = 0;
-#pragma unroll 1
-  for (int s = tid; s < a.num_seqs; s += kThreads) {
-    Seq q;
-    q.load(a, s);
-    mine += q.entries();
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sm.warp_sums[warp] = mine;
-  if (tid == 0) {
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.q_full[i], 1);
-      mbar_init(&sm.q_empty[i], 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < 2 * kScores; ++i) mbar_init(&sm.s_full[i], 2);
-#pragma unroll 1
-    for (int i = 0; i < kScores; ++i) {
-      mbar_init(&sm.p_full[i], kSoftWarps / 2);
-      mbar_init(&sm.p_free[i], 1);
-    }
-    mbar_init(&sm.o_full, 1);
-    mbar_init(&sm.o_free, kSoftWarps);
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.ref_full[i][0], 1);
-      mbar_init(&sm.ref_full[i][1], 1);
-      mbar_init(&sm.sums_full[i], 2);
-      sm.nonfinite[i] = -1;
-    }
-#pragma unroll 1
-    for (int i = 0; i < kStagesK; ++i) {
-      mbar_init(&sm.k_full[i], 1);
-      mbar_init(&sm.k_empty[i], 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < kStagesV; ++i) {
-      mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1);
-    mbar_init(&sm.mma_done[0], 1);
-    mbar_init(&sm.mma_done[1], 1);
-    sm.abort = 0;
-    sm.found = 0;
+  // ---- entries of the list, this CTA's share of them, and the sequence where it begins ----
+  if (warp == kScoreWarp) tmem_alloc(&sm.tmem_base, kTmemCols);
+  if (uint64_t *bar = sm.q_full + tid; bar <= &sm.o_free) {
+    mbar_init(bar, bar < sm.s_full ? 1 : bar < sm.p_full ? 2 : bar < &sm.o_free ? kSoftWarps / 2 : kSoftWarps);
     mbar_init_fence();
   }
-  __syncthreads();
-  long long T = 0;
+  if (tid < 4) sm.nonfinite[tid] = -1;
+  if (tid == 4) sm.abort = 0;
+  // Entries of sequences s0 + tid; with the total over all threads and, in `end`, up to and with this thread.
+  // (Both places of warp_sums are in use in turn: one barrier a call.)
+  int place = 0;
+  auto scan = [&](int s0, long long &mine, long long &end) {
+    mine = 0;
+    if (s0 + tid < a.num_seqs) {
+      Seq q;
+      q.load(a, s0 + tid);
+      mine = q.entries();
+    }
+    end = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    if (lane == 31) sm.warp_sums[place][warp] = end;
+    __syncthreads();
+    long long x = lane < kThreads / 32 ? sm.warp_sums[place][lane] : 0;
+    place ^= 1;
+#pragma unroll
+    for (int o = 1; o < kThreads / 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (warp > 0) end += __shfl_sync(0xffffffffu, x, warp - 1);
+    return __shfl_sync(0xffffffffu, x, kThreads / 32 - 1);
+  };
+  long long mine, end, T = 0;
 #pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) T += sm.warp_sums[w];
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) T += scan(s0, mine, end);
   const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));  // CTAs with a share
-
   if (T == 0 || cta >= Gu) {
+    if (warp == kScoreWarp) tmem_dealloc(sm.tmem_base, kTmemCols);
     griddep_launch_dependents();
     griddep_wait();
     zero_rows<kBf16>(a, cta, G, tid);
@@ -577,43 +569,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   shares.each = divide(T, Gu);
   shares.more = int(T - shares.each * Gu);
   const long long pa = shares.first(cta), pb = shares.first(cta + 1);
-
-  // ---- the sequence that holds block pa ----
+  // the sequence that holds entry pa: of the one batch that was scanned, or of a second look at all of them
   long long before = 0;
 #pragma unroll 1
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
-    __syncthreads();
-    if (sm.found) break;
-    const int s = s0 + tid;
-    long long v = 0;
-    if (s < a.num_seqs) {
-      Seq q;
-      q.load(a, s);
-      v = q.entries();
+    long long total = 0;
+    if (a.num_seqs > kThreads) total = scan(s0, mine, end);
+    if (before + end - mine <= pa && pa < before + end) {
+      sm.seq0 = s0 + tid;
+      sm.first = before + end - mine;
     }
-    long long x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) sm.warp_sums[warp] = x;
-    __syncthreads();
-    long long chunk = 0;
-#pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) x += sm.warp_sums[w];
-      chunk += sm.warp_sums[w];
-    }
-    x += before;
-    if (x - v <= pa && pa < x) {
-      sm.seq0 = s;
-      sm.first = x - v;
-      sm.found = 1;
-    }
-    before += chunk;
+    before += total;
+    if (pa < before) break;
   }
-  if (warp == kScoreWarp) tmem_alloc(&sm.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
