@@ -68,7 +68,7 @@ constexpr int kRegsOthers = 40, kRegsSoftmax = 96;
 static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax <= kThreads * 80, "registers of a CTA");
 constexpr int kMaxCtas = 320;
 constexpr int kMinBlocks = 2;                       // least list entries a CTA is given
-constexpr int kUnitCost = 4;                        // what a unit's start and end weigh in the list, in blocks
+constexpr int kUnitCost = 5;                        // what a unit's start and end weigh in the list, in blocks
 constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
 constexpr int kTileBytes = kKeys * kRowBytes;       // K (or V) of one block: 8 KiB
 constexpr int kOctetBytes = kOctet * kGroup * kRowBytes;  // 4 KiB
@@ -132,12 +132,17 @@ struct Seq {
     return n >= 0 && n <= a.max_query && ctx >= 0 && ctx <= a.max_context && n <= ctx && q0 >= 0 &&
            q0 <= a.num_q_rows - n;
   }
-  __device__ long long entries() const { return (long long)kKvHeads * tiles * (nb ? nb + kUnitCost : 0); }
+  // Of its tiles the even (part 0) or the odd ones, and the list entries of these.
+  __device__ int part_tiles(int part) const { return (tiles + 1 - part) >> 1; }
+  __device__ long long entries(int part) const { return (long long)kKvHeads * part_tiles(part) * (nb + kUnitCost); }
 };
 
-// A CTA's share of one unit: key blocks j0 .. j1 - 1 of (sequence, K/V head, tile).  The list holds the
-// units in the order sequence, head, tile; a unit has kUnitCost entries of weight, then its blocks.  (Without
-// the weight, CTAs with many short units took twice as long as the others in a ragged batch.)  The loader walks the list and passes the segments on in shared memory.
+// A CTA's share of one unit: key blocks j0 .. j1 - 1 of (sequence, K/V head, tile).  A unit has kUnitCost list
+// entries of weight, then its blocks.  (Without the weight, CTAs with many short units took twice as long as the
+// others in a ragged batch.)  The list holds the units of all even tiles, then those of the odd ones, each
+// in the order sequence, head, tile: in a batch of trees of 33 to 64 nodes the CTAs that work on a K/V head's two
+// tiles are half the grid apart and there at the same time, so its pages come from memory once.  The loader walks
+// the list and passes the segments on in shared memory.
 struct Segment {
   int s, g, tile, j0, j1;  // s < 0: there are no more
   int q0, n, ctx, nb;      // the sequence's
@@ -156,25 +161,28 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 // Walk over the segments of a CTA's share.  (It keeps little between segments and reads a sequence's lengths
 // again for each: the loader has few registers.)
 struct Walk {
-  long long pos, end, first;  // list position, end of the share, first entry of sequence s
-  int s;
+  long long pos, end, first;  // list position, end of the share, first entry of sequence s in its part
+  int s, part;
   __device__ bool next(const TreeArgs &a, Segment &x) {
     Seq seq;
     seq.load(a, s);
-#pragma unroll 1
     while (pos < end) {
-#pragma unroll 1
-      while (pos - first >= seq.entries()) {
-        first += seq.entries();
-        seq.load(a, ++s);
+      while (pos - first >= seq.entries(part)) {
+        first += seq.entries(part);
+        if (++s == a.num_seqs) {
+          s = 0;
+          part = 1;
+        }
+        seq.load(a, s);
       }
       const long long len = seq.nb + kUnitCost, u = divide(pos - first, len), v0 = pos - first - u * len;
       const long long v1 = min(len, v0 + (end - pos));
       pos += v1 - v0;
       if (v1 <= kUnitCost) continue;  // nothing but the unit's weight
+      const int tiles = seq.part_tiles(part);
       x.s = s;
-      x.g = int(u) / seq.tiles;  // (8 heads x at most 2^15 tiles)
-      x.tile = int(u) - x.g * seq.tiles;
+      x.g = int(u) / tiles;  // (8 heads x at most 2^14 tiles)
+      x.tile = 2 * (int(u) - x.g * tiles) + part;
       x.q0 = seq.q0;
       x.n = seq.n;
       x.ctx = seq.ctx;
@@ -526,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   }
   if (tid < 4) sm.nonfinite[tid] = -1;
   if (tid == 4) sm.abort = 0;
-  // Entries of sequences s0 + tid; with the total over all threads and, in `end`, up to and with this thread.
-  // (Both places of warp_sums are in use in turn: one barrier a call.)
+  // Entries of sequences s0 + tid in a part; `end`: up to and with this thread.  Returns the total over all threads.
+  // (The places of warp_sums are used in turn: one barrier a call.)
   int place = 0;
-  auto scan = [&](int s0, long long &mine, long long &end) {
+  auto scan = [&](int s0, int part, long long &mine, long long &end) {
     mine = 0;
     if (s0 + tid < a.num_seqs) {
       Seq q;
       q.load(a, s0 + tid);
-      mine = q.entries();
+      mine = q.entries(part);
     }
     end = mine;
 #pragma unroll
@@ -554,9 +562,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     if (warp > 0) end += __shfl_sync(0xffffffffu, x, warp - 1);
     return __shfl_sync(0xffffffffu, x, kThreads / 32 - 1);
   };
-  long long mine, end, T = 0;
+  // (a batch without second tiles has no odd part)
+  const int parts = a.max_tiles > 1 ? 2 : 1;
+  long long mine, end, T = 0, T0 = 0;
 #pragma unroll 1
-  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) T += scan(s0, mine, end);
+  for (int part = 0; part < parts; ++part) {
+    T0 = T;
+#pragma unroll 1
+    for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) T += scan(s0, part, mine, end);
+  }
+  if (parts == 1) T0 = T;
   const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));  // CTAs with a share
   if (T == 0 || cta >= Gu) {
     if (warp == kScoreWarp) tmem_dealloc(sm.tmem_base, kTmemCols);
@@ -569,12 +584,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   shares.each = divide(T, Gu);
   shares.more = int(T - shares.each * Gu);
   const long long pa = shares.first(cta), pb = shares.first(cta + 1);
-  // the sequence that holds entry pa: of the one batch that was scanned, or of a second look at all of them
-  long long before = 0;
+  // the sequence that holds entry pa: among those just scanned, or with a second look
+  const int part0 = pa >= T0 ? 1 : 0;
+  const bool again = a.num_seqs > kThreads || part0 != parts - 1;
+  long long before = part0 ? T0 : 0;
 #pragma unroll 1
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     long long total = 0;
-    if (a.num_seqs > kThreads) total = scan(s0, mine, end);
+    if (again) total = scan(s0, part0, mine, end);
     if (before + end - mine <= pa && pa < before + end) {
       sm.seq0 = s0 + tid;
       sm.first = before + end - mine;
@@ -631,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     walk.end = pb;
     walk.first = sm.first;
     walk.s = sm.seq0;
+    walk.part = part0;
     if (lane == 0) {
       prefetch_tensormap(&a.tmap_k);
       prefetch_tensormap(&a.tmap_q);
