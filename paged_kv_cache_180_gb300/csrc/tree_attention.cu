@@ -68,6 +68,10 @@ constexpr int kRegsOthers = 40, kRegsSoftmax = 96;
 static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax <= kThreads * 80, "registers of a CTA");
 constexpr int kMaxCtas = 320;
 constexpr int kMinBlocks = 2;                       // least list entries a CTA is given
+// With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
+// which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
+// a run's O goes to the segment's part in the workspace, where the runs are added with rounding.
+constexpr int kRunBlocks = 16;
 constexpr int kUnitCost = 5;                        // what a unit's start and end weigh in the list, in blocks
 constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
 constexpr int kTileBytes = kKeys * kRowBytes;       // K (or V) of one block: 8 KiB
@@ -207,7 +211,7 @@ struct __align__(1024) Smem {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
   uint64_t p_free[kScores];      // the product of a block is done: its buffer may be written
-  uint64_t o_full;               // a segment's products are done
+  uint64_t o_full;               // a run's products are done
   uint64_t ref_full[4][2];       // per quarter of the lanes, by turn: ref is there
   uint64_t seg_full[kSegments];
   uint64_t mma_done[2];
@@ -587,17 +591,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   // the sequence that holds entry pa: among those just scanned, or with a second look
   const int part0 = pa >= T0 ? 1 : 0;
   const bool again = a.num_seqs > kThreads || part0 != parts - 1;
-  long long before = part0 ? T0 : 0;
+  long long start = part0 ? T0 : 0;
 #pragma unroll 1
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     long long total = 0;
     if (again) total = scan(s0, part0, mine, end);
-    if (before + end - mine <= pa && pa < before + end) {
+    if (start + end - mine <= pa && pa < start + end) {
       sm.seq0 = s0 + tid;
-      sm.first = before + end - mine;
+      sm.first = start + end - mine;
     }
-    before += total;
-    if (pa < before) break;
+    start += total;
+    if (pa < start) break;
   }
   tc_fence_before();
   __syncthreads();
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     // ================= O += P V (one thread issues, the warp waits) =================
     griddep_wait();
     const uint64_t v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
-    unsigned gb = 0;
+    unsigned gb = 0, runs = 0;  // blocks and runs issued
     bool ok = true;
 #pragma unroll 1
     for (int k = 0; ok; ++k) {
@@ -824,11 +828,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const int blocks = x.j1 - x.j0;
 #pragma unroll 1
       for (int j = 0; j < blocks; ++j, ++gb) {
+        const int in_run = kBf16 ? j : j % kRunBlocks;
+        const bool run_ends = j == blocks - 1 || (!kBf16 && in_run == kRunBlocks - 1);
         const int st = int(gb % kStagesV), b = int(gb % kScores);
         w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1) &&
             wait(sm, &sm.p_full[b], (gb / kScores) & 1);
-        // a segment's first product overwrites O, once every softmax warp has read the one before
-        if (w && j == 0 && k > 0) w = wait(sm, &sm.o_free, uint32_t(k - 1) & 1);
+        // a run's first product overwrites O, once every softmax warp has read the one before
+        if (w && in_run == 0 && runs > 0) w = wait(sm, &sm.o_free, (runs - 1) & 1);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -841,12 +847,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 #pragma unroll
             for (int term = 0; term < (kBf16 ? 1 : 2); ++term)
               tc_mma_tmem_a(tmem + kColO, tmem + b * kKeys + (kk >> 1) * 32 + (kk & 1) * 8 + term * 16,
-                            vdesc + kk * (2048 >> 4), kIdescPV, (j == 0 && kk == 0 && term == 0) ? 0u : 1u);
+                            vdesc + kk * (2048 >> 4), kIdescPV, (in_run == 0 && kk == 0 && term == 0) ? 0u : 1u);
           tc_commit(&sm.p_free[b]);
           tc_commit(&sm.v_empty[st]);
-          if (j == blocks - 1) tc_commit(&sm.o_full);
+          if (run_ends) tc_commit(&sm.o_full);
         }
         __syncwarp();
+        runs += run_ends ? 1 : 0;
       }
     }
     if (elect_one()) {
@@ -864,18 +871,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     int turns = 0;     // segments in which this warp has had rows (the two warps of a quarter agree)
     int cuts = 0;      // bit 0, 1: the share's first, last unit is cut
     bool ok = true;
-    // A segment ends while the next one's first block is under way: its sums are posted, and once that block's P is
-    // stored finish() divides and writes its rows (or their partial state).
-    bool pending = false;
-    // Segment k's end for this warp: a row's sums meet; this thread has the row's dims 32 half .. + 31.
-    auto finish = [&](int k) {
+    // A run ends while the next one's first block is under way: once that block's P is stored, end_run() takes the
+    // run's O, and at a segment's end (its sums have been posted) divides and writes its rows or their partial state.
+    unsigned ended = 0;            // runs this warp has ended
+    unsigned runs = 0, before = 0;  // runs before the current segment, before the one before it
+    // The end of a run of segment k (whose first run is `first`), its last or not, for this warp: this thread has its
+    // row's dims 32 half .. + 31.
+    auto end_run = [&](int k, unsigned first, bool last) {
       const Segment &x = sm.seg[k % kSegments];
       const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, pos0 = x.j0 * kKeys, pos1 = min(x.ctx, x.j1 * kKeys);
       const bool active = octet * kOctet < x.n - x.tile * kTok;
       const int node = x.tile * kTok + octet * kOctet + (lane >> 2), t = turns - 1;
       const bool real = node < x.n;
-      bool w = wait(sm, &sm.o_full, uint32_t(k) & 1);
-      if (active) w = wait(sm, &sm.sums_full[quarter], uint32_t(t) & 1) && w;
+      bool w = wait(sm, &sm.o_full, ended & 1);
+      ++ended;
+      if (active && last) w = wait(sm, &sm.sums_full[quarter], uint32_t(t) & 1) && w;
       if (!__all_sync(0xffffffffu, w)) return false;
       uint32_t u[32];
       if (active) {
@@ -886,9 +896,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free);
       if (!active) return true;
-      float L = sm.sums[t & 3][0][row] + sm.sums[t & 3][1][row], ref = sm.ref[t & 3][row], r[32];
+      float r[32];
 #pragma unroll
       for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]);
+      // the segment's part; between runs it holds their sum, each thread its own row and dims
+      Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
+      const int at = octet * 32 + lane;
+      if constexpr (!kBf16) {
+        if (ended - 1 > first) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = __ldcg(&part.o[half * 8 + i][at]);
+            r[4 * i] += y.x;
+            r[4 * i + 1] += y.y;
+            r[4 * i + 2] += y.z;
+            r[4 * i + 3] += y.w;
+          }
+        }
+      }
+      auto store_part = [&]() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          __stcg(&part.o[half * 8 + i][at], make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+      };
+      if (!last) {
+        store_part();
+        return true;
+      }
+      float L = sm.sums[t & 3][0][row] + sm.sums[t & 3][1][row], ref = sm.ref[t & 3][row];
       const int h = x.g * kGroup + (lane & 3);
       const long long qrow = (long long)x.q0 + node;
       bool redo = !(L >= kSumMin && L <= kSumMax);
@@ -917,11 +952,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         write_row<kBf16>(a.out, (qrow * kQHeads + h) * kHeadDim + half * 32, r);
       } else {
         // a cut unit: a partial state; its ticket is taken when the share is done
-        Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
-        const int at = octet * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          __stcg(&part.o[half * 8 + i][at], make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+        store_part();
         __stcg(&part.rl[half][at], make_float2(ref, L));
       }
       return true;
@@ -931,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       bool w = wait(sm, &sm.seg_full[k % kSegments], uint32_t(k / kSegments) & 1);
       if (!__all_sync(0xffffffffu, w)) break;
       const Segment &x = sm.seg[k % kSegments];
-      const bool more = x.s >= 0;  // if not, one round of the loop below ends the last segment
+      const bool more = x.s >= 0;  // if not, a round of the loop below ends the last segment
       const int octet = (quarter - k - turn) & 3, base = x.ctx - x.n, j0 = more ? x.j0 : 0, j1 = more ? x.j1 : 0;
       const bool active = more && octet * kOctet < x.n - x.tile * kTok;  // the warp has rows
       // this thread's row, valid where `real`
@@ -941,11 +972,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
       const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
       float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
+      const int last_run = kBf16 || !more ? 0 : (j1 - j0 - 1) / kRunBlocks;
 #pragma unroll 1
-      for (int j = j0 + (leads ? 0 : 1); ok && (j < j1 || pending); j += 2) {
+      for (int j = j0 + (leads ? 0 : 1); ok; j += 2) {
+        const bool has = j < j1;
+        // the runs to end before this block's P is handed over: all before its own; after the last block
+        // all but the segment's last
+        const unsigned due = runs + (has && !kBf16 ? (j - j0) / kRunBlocks : has ? 0 : last_run);
+        if (!has && ended == due) break;
         const unsigned gb = gb0 + unsigned(j - j0);
         const int b = int(gb % kScores), f = int(gb % (2 * kScores)), key0 = j * kKeys;
-        if (j < j1) {
+        if (has) {
           w = wait(sm, &sm.s_full[f], (gb / (2 * kScores)) & 1);
           if (w && key0 + kKeys > base) {
             // the block holds nodes: the group's threads look through V, two to a row
@@ -1005,12 +1042,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
             tc_fence_before();
           }
         }
-        if (pending) {
-          ok = finish(k - 1);
-          pending = false;
+#pragma unroll 1
+        while (ok && ended != due) {
+          const bool last = ended < runs;  // of the segment before
+          ok = end_run(last ? k - 1 : k, last ? before : runs, last);
         }
         __syncwarp();
-        if (j < j1 && lane == 0) mbar_arrive(&sm.p_full[b]);
+        if (has && lane == 0) mbar_arrive(&sm.p_full[b]);
+        if (!has) break;
       }
       if (!ok || !more) break;
       gb0 += unsigned(j1 - j0);
@@ -1025,7 +1064,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         if (lane == 0) mbar_arrive(&sm.sums_full[quarter]);
         ++turns;
       }
-      pending = true;
+      before = runs;
+      runs += last_run + 1;
     }
     // ---- the tickets of the cut units: the CTA that takes a unit's last one merges its parts; in a unit of
     // many parts first the parts of a group, then the CTA with the last group the groups ----
