@@ -133,13 +133,17 @@ def status_string(code: int) -> str:
 # torch.cuda.current_stream() builds (2.9 us a call on the Grace host, against 0.2 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_cuda_ready = False
 
 
 def _stream(stream) -> int:
+    global _cuda_ready
     if stream is not None:
         return int(stream.cuda_stream)
-    if _raw_stream is not None and torch.cuda.is_initialized():
+    if _cuda_ready:
         return _raw_stream(_current_device())
+    _cuda_ready = _raw_stream is not None and torch.cuda.is_initialized()
     return int(torch.cuda.current_stream().cuda_stream)
 
 
@@ -287,20 +291,9 @@ def paged_decode_attention_noalloc(pool: KVPool | PkvPool, out: torch.Tensor, q:
     _check("pkv_paged_decode_attention_noalloc", rc)
 
 
-def _device_of(where: str, t: torch.Tensor) -> int:
-    """Index of t's device, which has to be the current one (a stream and a launch belong to that)."""
-    d = t.get_device()
-    if d < 0 or d != _current_device():
-        raise ValueError(f"{where}: tensors on {t.device}, but the current device is cuda:{_current_device()}")
-    return d
-
-
-def _require(where: str, device: int, dtype, *tensors: torch.Tensor) -> None:
-    """The kernel sees pointers only: the tensors' type, order and device have to be what it takes them for."""
-    for t in tensors:
-        if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-            raise ValueError(f"{where}: expected a contiguous {dtype} tensor on cuda:{device}, got {t.dtype} on "
-                             f"{t.device} with strides {tuple(t.stride())}")
+def _refuse(where: str, t: torch.Tensor, dtype) -> None:
+    raise ValueError(f"{where}: expected a contiguous {dtype} tensor on the current device (cuda:{_current_device()}), got "
+                     f"{t.dtype} on {t.device} with strides {tuple(t.stride())}")
 
 
 def tree_workspace_bytes(num_seqs: int, max_query: int, num_q_heads: int = 32, head_dim: int = 64) -> int:
@@ -323,21 +316,26 @@ def paged_tree_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Ten
     when the kernel before it on the stream writes none of q, query_start, context_lens or block_tables,
     e.g. the drafted tokens' kv_append)."""
     where = "pkv_paged_tree_attention"
-    desc = pool.desc if isinstance(pool, KVPool) else pool
-    device = _device_of(where, q)
-    bf16_out = out.dtype is torch.bfloat16
-    _require(where, device, torch.bfloat16, q)
-    _require(where, device, torch.bfloat16 if bf16_out else torch.float32, out)
-    _require(where, device, torch.int32, query_start, tree_mask, context_lens)
+    # the kernel sees pointers only: type, order and device have to be what it takes them for
+    dev, kind = _current_device(), out.dtype
+    for t in (query_start, tree_mask, context_lens):
+        if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+            _refuse(where, t, _I32)
+    if q.dtype is not _BF16 or q.get_device() != dev or not q.is_contiguous():
+        _refuse(where, q, _BF16)
+    if (kind is not _F32 and kind is not _BF16) or out.get_device() != dev or not out.is_contiguous():
+        _refuse(where, out, "float32 or bfloat16")
     num_seqs, shape, out_shape, mask_shape = context_lens.numel(), q.shape, out.shape, tree_mask.shape
     if len(shape) != 3 or out_shape[1:] != shape[1:] or len(mask_shape) != 2 or query_start.numel() != num_seqs + 1:
         raise ValueError(f"{where}: q and out are [rows, heads, dim], tree_mask [rows, words], query_start [seqs + 1]")
-    rows = min(shape[0], out_shape[0], mask_shape[0])
-    flags = (OVERLAP_PREVIOUS if overlap_previous else 0) | (OUT_BF16 if bf16_out else 0)
-    _check(where, _lib.pkv_paged_tree_attention(
-        ctypes.byref(desc), out.data_ptr(), q.data_ptr(), shape[1], rows, query_start.data_ptr(), tree_mask.data_ptr(),
-        mask_shape[1], block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_query,
-        max_context, scale, workspace.data_ptr(), workspace.nbytes, _ptr(status), flags, _stream(stream)))
+    flags = (OVERLAP_PREVIOUS if overlap_previous else 0) | (OUT_BF16 if kind is _BF16 else 0)
+    rc = _lib.pkv_paged_tree_attention(
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), shape[1],
+        min(shape[0], out_shape[0], mask_shape[0]), query_start.data_ptr(), tree_mask.data_ptr(), mask_shape[1],
+        block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_query, max_context, scale,
+        workspace.data_ptr(), workspace.nbytes, None if status is None else status.data_ptr(), flags, _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
 
 
 def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_stride: int, layer_stride: int,
@@ -348,36 +346,47 @@ def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_
     first accept_counts[s] of row s) behind its committed prefix in every layer; new_context_lens receives
     the lengths after it."""
     where = "pkv_tree_commit"
-    desc = pool.desc if isinstance(pool, KVPool) else pool
-    device = _device_of(where, context_lens)
-    _require(where, device, torch.int32, query_start, context_lens, accepted, accept_counts)
+    dev = _current_device()
+    for t in (query_start, context_lens, accepted, accept_counts):
+        if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+            _refuse(where, t, _I32)
     num_seqs, shape = context_lens.numel(), accepted.shape
     if len(shape) != 2 or shape[0] != num_seqs or accept_counts.numel() != num_seqs or \
             query_start.numel() != num_seqs + 1:
         raise ValueError(f"{where}: accepted is [seqs, width], accept_counts [seqs], query_start [seqs + 1]")
+    new = None
     if new_context_lens is not None:
-        _require(where, device, torch.int32, new_context_lens)
+        new = new_context_lens.data_ptr()
+        if new_context_lens.dtype is not _I32 or new_context_lens.get_device() != dev or \
+                not new_context_lens.is_contiguous():
+            _refuse(where, new_context_lens, _I32)
         if new_context_lens.numel() < num_seqs:
             raise ValueError(f"{where}: new_context_lens has {new_context_lens.numel()} entries for {num_seqs} sequences")
-    _check(where, _lib.pkv_tree_commit(
-        ctypes.byref(desc), block_tables.data_ptr(), block_table_stride, layer_stride, num_layers,
-        query_start.data_ptr(), context_lens.data_ptr(), accepted.data_ptr(), shape[1], accept_counts.data_ptr(),
-        num_seqs, shape[1], max_context, _ptr(new_context_lens), _ptr(status), _stream(stream)))
+    width = shape[1]
+    rc = _lib.pkv_tree_commit(
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), block_tables.data_ptr(), block_table_stride,
+        layer_stride, num_layers, query_start.data_ptr(), context_lens.data_ptr(), accepted.data_ptr(), width,
+        accept_counts.data_ptr(), num_seqs, width, max_context, new, None if status is None else status.data_ptr(),
+        _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
 
 
 def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: torch.Tensor,
                   status: torch.Tensor | None = None, stream=None) -> None:
     """Copy page src_pages[i] onto page dst_pages[i] (int32; a negative id is padding), K and V."""
     where = "pkv_kv_copy_pages"
-    desc = pool.desc if isinstance(pool, KVPool) else pool
-    n = src_pages.numel()
+    n, dev = src_pages.numel(), _current_device()
     for t in (src_pages, dst_pages):
-        if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() != n:
+        if t.dtype is not _I32 or not t.is_contiguous() or t.numel() != n:
             raise ValueError(f"{where}: page ids are contiguous int32 tensors, as many sources as destinations")
-        if t.get_device() not in (-1, _current_device()):
-            raise ValueError(f"{where}: page ids on {t.device}, but the current device is cuda:{_current_device()}")
-    _check(where, _lib.pkv_kv_copy_pages(ctypes.byref(desc), src_pages.data_ptr(), dst_pages.data_ptr(), n,
-                                         _ptr(status), _stream(stream)))
+        if t.get_device() not in (-1, dev):
+            raise ValueError(f"{where}: page ids on {t.device}, but the current device is cuda:{dev}")
+    rc = _lib.pkv_kv_copy_pages(ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), src_pages.data_ptr(),
+                                dst_pages.data_ptr(), n, None if status is None else status.data_ptr(),
+                                _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
 
 
 class Allocator:

@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_pages_kernel(
 
 // ---- tree_commit -----------------------------------------------------------------------------
 constexpr int kCommitThreads = 2 * kKvHeads * (kRowBytes / 16);  // one thread per 16-byte chunk of a token: 128
-constexpr int kCommitBatch = 4;                                  // rows a thread has in flight
+constexpr int kCommitRows = 32;                                  // rows whose places are looked up at once
+constexpr int kCommitBatch = 8;                                  // rows a thread has in flight
 
 struct CommitArgs {
   uint8_t *k_base, *v_base;
@@ -55,18 +56,21 @@ struct CommitArgs {
   int32_t *new_lens, *status;
 };
 
-// One CTA commits one (sequence, layer).  Thread = one 16-byte chunk (K or V, head, chunk) of a
-// token's rows, the same chunk for every row of the path.  The path is ascending, so path[k] >= k
-// and path[k + 1] > path[k]: the rows a batch of loads reads all lie at or behind the rows its
-// stores write, and every row a later batch reads lies behind them.  Each thread reads and
-// writes its own chunk only, so loading a batch before storing it is all the ordering there is.
+// One CTA commits one (sequence, layer).  The places of up to 32 rows are looked up in parallel (path, then table
+// entries: two round trips for all of them), then every thread moves one 16-byte chunk (K or V, head, chunk) of
+// each row, the same chunk for every row.  The path is ascending, so path[k] >= k and path[k + 1] > path[k]: the rows
+// a batch of loads reads all lie at or behind the rows its stores write, and every row a later batch reads lies
+// behind them.  Each thread reads and writes its own chunk only, so loading a batch before storing it is all
+// the ordering there is.
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a) {
+  __shared__ long long from[kCommitRows], to[kCommitRows];  // byte offsets in either half of the pool; to < 0: stays
   griddep_launch_dependents();
-  const int s = int(blockIdx.x / a.num_layers), layer = int(blockIdx.x % a.num_layers);
+  const int s = int(blockIdx.x / unsigned(a.num_layers)), layer = int(blockIdx.x % unsigned(a.num_layers));
   const int tid = threadIdx.x;
   const int n = __ldg(a.query_start + s + 1) - __ldg(a.query_start + s);
   const int ctx = __ldg(a.context_lens + s), count = __ldg(a.accept_counts + s);
   const int base = ctx - n;
+  const int32_t *path = a.accepted + (long long)s * a.accepted_stride;
   if (n < 0 || ctx < 0 || ctx > a.max_context || n > ctx) {
     if (layer == 0 && tid == 0) {
       report(a.status, PKV_DEV_BAD_CONTEXT);
@@ -74,7 +78,6 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     }
     return;
   }
-  const int32_t *path = a.accepted + (long long)s * a.accepted_stride;
   bool bad = count < 0 || count > n || count > a.max_accept;
   if (!bad)
     for (int k = tid; k < count; k += kCommitThreads) {
@@ -90,34 +93,33 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
   const int32_t *table = a.block_tables + (long long)s * a.bt_stride + (long long)layer * a.layer_stride;
   const int is_v = tid / (kCommitThreads / 2), g = (tid / 8) % kKvHeads, c = tid % 8;
   uint8_t *half = (is_v ? a.v_base : a.k_base) + g * kPageTokens * kRowBytes + c * 16;
-  // this thread's chunk of position t; null when the page is invalid
-  auto chunk = [&](int t) -> uint4 * {
-    const int page = __ldg(table + t / kPageTokens);
-    if (page < 0 || page >= a.num_pages) return nullptr;
-    return reinterpret_cast<uint4 *>(half + (long long)page * a.page_stride + (t % kPageTokens) * kRowBytes);
-  };
-  for (int k0 = 0; k0 < count; k0 += kCommitBatch) {
-    uint4 x[kCommitBatch];
-    uint4 *to[kCommitBatch];
-#pragma unroll
-    for (int j = 0; j < kCommitBatch; ++j) {
-      to[j] = nullptr;
-      const int k = k0 + j;
-      if (k >= count) continue;
-      const int p = __ldg(path + k);
-      if (p == k) continue;  // already in place
-      const uint4 *from = chunk(base + p);
-      to[j] = chunk(base + k);
-      if (from == nullptr || to[j] == nullptr) {
-        to[j] = nullptr;
-        if (tid == 0) report(a.status, PKV_DEV_BAD_PAGE);
-        continue;
+  for (int k0 = 0; k0 < count; k0 += kCommitRows) {
+    const int rows = min(kCommitRows, count - k0);
+    if (k0 > 0) __syncthreads();  // (the places before have been used)
+    if (tid < rows) {
+      const int k = k0 + tid, p = __ldg(path + k);
+      to[tid] = -1;
+      if (p != k) {
+        const int src = base + p, dst = base + k;
+        const int src_page = __ldg(table + src / kPageTokens), dst_page = __ldg(table + dst / kPageTokens);
+        if (src_page < 0 || src_page >= a.num_pages || dst_page < 0 || dst_page >= a.num_pages) {
+          report(a.status, PKV_DEV_BAD_PAGE);
+        } else {
+          from[tid] = src_page * a.page_stride + (src % kPageTokens) * kRowBytes;
+          to[tid] = dst_page * a.page_stride + (dst % kPageTokens) * kRowBytes;
+        }
       }
-      x[j] = *from;
     }
+    __syncthreads();
+    for (int r0 = 0; r0 < rows; r0 += kCommitBatch) {
+      uint4 x[kCommitBatch];
 #pragma unroll
-    for (int j = 0; j < kCommitBatch; ++j)
-      if (to[j] != nullptr) *to[j] = x[j];
+      for (int j = 0; j < kCommitBatch; ++j)
+        if (r0 + j < rows && to[r0 + j] >= 0) x[j] = *reinterpret_cast<const uint4 *>(half + from[r0 + j]);
+#pragma unroll
+      for (int j = 0; j < kCommitBatch; ++j)
+        if (r0 + j < rows && to[r0 + j] >= 0) *reinterpret_cast<uint4 *>(half + to[r0 + j]) = x[j];
+    }
   }
 }
 
