@@ -356,7 +356,7 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
  *                  only if its own bit is set.
  *   mask_stride    words between rows, 32 * mask_stride >= max_query.
  *   block_tables, block_table_stride, context_lens, max_context: as for decode.
- *   max_query      host bound on every n_s, at most 2^20 (and num_seqs at most 2^24).
+ *   max_query      host bound on every n_s, at most 2^20 (num_seqs at most 2^24, max_context at most 2^31 - 64).
  *   scale          any finite value, negative ones and 0 (a plain average) included.
  *   workspace      device, >= pkv_tree_workspace_bytes(num_seqs, max_query, ...), 16-byte aligned,
  *                  zero-filled before its first use; every completed call leaves it ready for the
@@ -373,8 +373,10 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
  * A sequence whose lengths do not fit (n_s < 0, > max_query or > context_lens[s], a context < 0 or
  * > max_context, query rows past num_q_rows) gets zero rows and PKV_DEV_BAD_CONTEXT; an invalid page
  * id inside a context sets PKV_DEV_BAD_PAGE and that page is left out.  A NaN or infinity in the K or
- * V of a node reaches only the rows whose mask names that node.
- * No allocation, one kernel launch.
+ * V of a node reaches only the rows whose mask names that node.  A key whose score is -infinity has no
+ * weight; a row with no other key gets zeros.  Rows whose scores rise by more than 77 (2^112 in
+ * weight) above those of a part's first 64 keys, or that meet infinities, are computed again key by key: slowly.
+ * num_seqs, max_query or num_q_rows = 0 enqueues nothing.  No allocation, one kernel launch.
  */
 #define PKV_OUT_BF16 2u
 int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const void *q, int num_q_heads, int num_q_rows,

@@ -26,8 +26,8 @@
 //    1650 cycles a block.)
 //  * The reference is the row's largest exponent in the segment's first block and stays: weights are floats, so
 //    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
-//    that.  A row whose sum leaves [2^-64, 2^64] is computed again from global memory, slowly and exactly, by
-//    redo_row().
+//    that.  A row whose sum leaves [2^-90, 2^112] is computed again from global memory by redo_row(), slowly (with every
+//    row of 64 x 2048 tokens and 32 nodes computed again a call takes 15.1 ms instead of 0.08).
 //  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits; two
 //    products); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
 //    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
@@ -80,8 +80,9 @@ constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColO = kScores * kKeys;         // S buffers at columns 0, 64 and 128, O at 192
 constexpr int kMergeGroup = 5;                      // a unit in more parts than this merges groups of them first
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSumMin = 5.42101086e-20f, kSumMax = 1.84467441e19f;  // 2^-64, 2^64
-constexpr float kSumPlain = 1048576.f;              // 2^20: up to here O is finite unless V is about to be not
+// A row's sum may lie in [2^-90, 2^112] (the scores 77 above the first block's largest) and its O below 2^118: what a
+// merge adds up, 320 parts at the most, then stays in the range of fp32.
+constexpr float kSumMin = 0x1p-90f, kSumMax = 0x1p112f, kInfOverMaxO = 0x1p10f;
 
 constexpr uint32_t kIdescS = idesc_bf16(kRows, kKeys, false);     // B = K rows (K-major)
 constexpr uint32_t kIdescPV = idesc_bf16(kRows, kHeadDim, true);  // B = V rows (MN-major)
@@ -390,33 +391,44 @@ __device__ __forceinline__ uint32_t nonfinite(const uint4 &x) {
 // The weight of a state (r, l) merged under the reference R; a state that has seen no key has l = 0.
 __device__ __forceinline__ float state_weight(float2 rl, float R) { return rl.y == 0.f ? 0.f : ex2_approx(rl.x - R); }
 
+// sum + x y, either half
+__device__ __forceinline__ float2 dot_bf16x2(uint32_t x, uint32_t y, float2 sum) {
+  return make_float2(sum.x + bf16_lo(x) * bf16_lo(y), sum.y + bf16_hi(x) * bf16_hi(y));
+}
+
 // One row's state (r, l, 32 dims of O from dim d0) over the keys pos .. end - 1, straight from global memory with a
-// running maximum: for rows whose sums left the range of the fast path, and for segments with nodes whose V is not
-// finite.  A key the row does not see is skipped.
+// running maximum: for rows whose sums left the range of the fast path or whose O is not finite, and for segments with
+// nodes whose V is not finite.  A key the row does not see is skipped.
 __device__ __noinline__ float2 redo_row(const uint8_t *k_base, const uint8_t *v_base, long long page_stride,
                                         int num_pages, const int32_t *table, const uint32_t *mask, const uint16_t *q,
-                                        int g, int pos, int end, int base, float c, int d0, float *o) {
+                                        int g, int pos, int end, int base, float c, int d0, float4 *o) {
   float R = -INFINITY, L = 0.f;
 #pragma unroll 1
-  for (int d = 0; d < 32; ++d) o[d] = 0.f;
+  for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (; pos < end; ++pos) {
     const int page = __ldg(table + pos / kPageTokens), node = pos - base;
     if (page < 0 || page >= num_pages || (node >= 0 && !(__ldg(mask + (node >> 5)) >> (node & 31) & 1u))) continue;
     const long long at = (long long)page * page_stride + (g * kPageTokens + pos % kPageTokens) * kRowBytes;
-    const uint32_t *k = reinterpret_cast<const uint32_t *>(k_base + at), *x = reinterpret_cast<const uint32_t *>(q);
-    float dot = 0.f;
-#pragma unroll 1
-    for (int i = 0; i < kHeadDim / 2; ++i) dot += bf16_lo(x[i]) * bf16_lo(k[i]) + bf16_hi(x[i]) * bf16_hi(k[i]);
-    const float e = dot * c, Rn = fmaxf(R, e);
+    const uint4 *k = reinterpret_cast<const uint4 *>(k_base + at), *x = reinterpret_cast<const uint4 *>(q);
+    float2 dot = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < kHeadDim / 8; ++i) {
+      const uint4 y = k[i], z = x[i];
+      dot = dot_bf16x2(y.w, z.w, dot_bf16x2(y.z, z.z, dot_bf16x2(y.y, z.y, dot_bf16x2(y.x, z.x, dot))));
+    }
+    const float e = (dot.x + dot.y) * c, Rn = fmaxf(R, e);
+    if (e == -INFINITY) continue;  // (weight 0, and no reference)
     const float keep = R == -INFINITY ? 0.f : exp2f(R - Rn), w = exp2f(e - Rn);
     R = Rn;
     L = L * keep + w;
-    const uint32_t *v = reinterpret_cast<const uint32_t *>(v_base + at) + d0 / 2;
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      o[2 * i] = o[2 * i] * keep + w * bf16_lo(v[i]);
-      o[2 * i + 1] = o[2 * i + 1] * keep + w * bf16_hi(v[i]);
+    const uint2 *v = reinterpret_cast<const uint2 *>(v_base + at) + d0 / 4;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const uint2 y = v[i];
+      const float4 z = o[i];
+      o[i] = make_float4(z.x * keep + w * bf16_lo(y.x), z.y * keep + w * bf16_hi(y.x), z.z * keep + w * bf16_lo(y.y),
+                         z.w * keep + w * bf16_hi(y.y));
     }
   }
   return make_float2(R, L);
@@ -579,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));  // CTAs with a share
   if (T == 0 || cta >= Gu) {
     if (warp == kScoreWarp) tmem_dealloc(sm.tmem_base, kTmemCols);
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     zero_rows<kBf16>(a, cta, G, tid);
     return;
   }
@@ -607,7 +619,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  griddep_launch_dependents();  // a kernel that starts beside this one finds what tensor memory is left
   // Small trees fill the lanes of one warp only: units start at another quarter of the lanes each, so
   // that the quarters (the SM's sub-partitions) share the work.
   const int turn = cta * 2 >= G ? 2 : 0;
@@ -769,6 +780,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   } else if (warp == kScoreWarp) {
     // ================= S = Q K^T (one thread issues, the warp waits) =================
     griddep_wait();  // nothing to do before the loaders; its waits are not to run out on the kernel before
+    // The next kernel may start once every CTA of this one is past its wait, so that what it reads at once is
+    // complete if a kernel before this one wrote it.
+    griddep_launch_dependents();
     const uint64_t q_desc = sw128_desc(smem_addr(sm.q), 16, 1024),
                    k_desc = sw128_desc(smem_addr(sm.k), 16, 1024);  // a later address adds to the low bits
     unsigned gb = 0;  // blocks issued
@@ -926,23 +940,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       float L = sm.sums[t & 3][0][row] + sm.sums[t & 3][1][row], ref = sm.ref[t & 3][row];
       const int h = x.g * kGroup + (lane & 3);
       const long long qrow = (long long)x.q0 + node;
-      bool redo = !(L >= kSumMin && L <= kSumMax);
-      if (L > kSumPlain) {
-        float z = 0.f;  // NaN when the row of O is not finite
+      float z = 0.f;  // NaN when O is too large or not finite (an infinite V: hi and lo terms make a NaN of it)
 #pragma unroll
-        for (int d = 0; d < 32; ++d) z += r[d] * 0.f;
-        redo |= z != 0.f;
-      }
+      for (int d = 0; d < 32; ++d) z += r[d] * kInfOverMaxO * 0.f;
+      const bool redo = !(L >= kSumMin && L <= kSumMax) || z != 0.f;
       if (real && (redo || *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) == k) &&
           (L != 0.f || sees_any(a.mask + qrow * a.mask_stride, pos0, pos1, base, x.n))) {
-        float o[32];
+        float4 o[8];  // (it lies in memory: few come here)
         const float2 rl = redo_row(a.k_base, a.v_base, a.page_stride, a.num_pages,
                                    a.block_tables + (long long)x.s * a.bt_stride, a.mask + qrow * a.mask_stride,
                                    a.q + (qrow * kQHeads + h) * kHeadDim, x.g, pos0, pos1, base, a.c.x, half * 32, o);
         ref = rl.x;
         L = rl.y;
 #pragma unroll
-        for (int d = 0; d < 32; ++d) r[d] = o[d];  // (o lies in memory: few come here)
+        for (int i = 0; i < 8; ++i) {
+          r[4 * i] = o[i].x;
+          r[4 * i + 1] = o[i].y;
+          r[4 * i + 2] = o[i].z;
+          r[4 * i + 3] = o[i].w;
+        }
       }
       if (!real) return true;
       if (x.j0 == 0 && x.j1 == x.nb) {
@@ -1143,6 +1159,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 }
 
 constexpr int kMaxSeqs = 1 << 24, kMaxNodes = 1 << 20;
+constexpr int kMaxContext = 0x7fffffff / kKeys * kKeys;  // the last block's end is an int too
 
 size_t ticket_bytes(int num_seqs, int max_tiles) {
   return (size_t(num_seqs) * size_t(max_tiles) * kKvHeads * sizeof(int32_t) + 127) / 128 * 128;
@@ -1194,7 +1211,7 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   if (rc != PKV_OK) return rc;
   if (num_q_heads != pkv::kQHeads) return PKV_ERR_UNSUPPORTED;
   if (num_seqs < 0 || max_query < 0 || max_context < 0 || block_table_stride < 0 || num_q_rows < 0 ||
-      num_seqs > pkv::kMaxSeqs || max_query > pkv::kMaxNodes || mask_stride < 0 || mask_stride > (1 << 26) ||
+      num_seqs > pkv::kMaxSeqs || max_query > pkv::kMaxNodes || max_context > pkv::kMaxContext || mask_stride < 0 || mask_stride > (1 << 26) ||
       mask_stride * 32 < max_query)
     return PKV_ERR_SHAPE;
   if (num_seqs == 0 || max_query == 0 || num_q_rows == 0) return PKV_OK;

@@ -328,6 +328,16 @@ def test_tree_attention_refusals(pkv):
     assert b.tree_workspace_bytes(4000, 256) > need
 
 
+def test_tree_attention_refuses_contexts_whose_last_block_passes_32_bits(pkv):
+    b = pkv.binding
+    d = b.kv_pool_create(1 << 20, (1 << 20) + 16384, 0, 8)
+    p, need = ctypes.c_void_p(1 << 20), b.tree_workspace_bytes(1, 1)
+    call = lambda mc, wsb: b._lib.pkv_paged_tree_attention(  # noqa: E731
+        ctypes.byref(d), p, p, 32, 1, p, p, 1, p, 1 << 27, p, 1, 1, mc, 0.125, p, wsb, None, 0, None)
+    assert call(2 ** 31 - 1, need) == call(2 ** 31 - 63, need) == -2
+    assert call(2 ** 31 - 64, need - 1) == -6          # the largest one passes on to the next check
+
+
 def test_commit_and_copy_refusals(pkv):
     b = pkv.binding
     lib, P, base = b._lib, ctypes.c_void_p, 1 << 20
