@@ -323,6 +323,10 @@ def paged_tree_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Ten
             _refuse(where, t, _I32)
     if q.dtype is not _BF16 or q.get_device() != dev or not q.is_contiguous():
         _refuse(where, q, _BF16)
+    if block_tables.dtype is not _I32 or block_tables.get_device() != dev or block_tables.stride(-1) != 1:
+        _refuse(where, block_tables, _I32)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(where, workspace, "uint8")
     if (kind is not _F32 and kind is not _BF16) or out.get_device() != dev or not out.is_contiguous():
         _refuse(where, out, "float32 or bfloat16")
     num_seqs, shape, out_shape, mask_shape = context_lens.numel(), q.shape, out.shape, tree_mask.shape
@@ -350,6 +354,8 @@ def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_
     for t in (query_start, context_lens, accepted, accept_counts):
         if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
             _refuse(where, t, _I32)
+    if block_tables.dtype is not _I32 or block_tables.get_device() != dev or block_tables.stride(-1) != 1:
+        _refuse(where, block_tables, _I32)
     num_seqs, shape = context_lens.numel(), accepted.shape
     if len(shape) != 2 or shape[0] != num_seqs or accept_counts.numel() != num_seqs or \
             query_start.numel() != num_seqs + 1:
@@ -380,8 +386,9 @@ def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: to
     for t in (src_pages, dst_pages):
         if t.dtype is not _I32 or not t.is_contiguous() or t.numel() != n:
             raise ValueError(f"{where}: page ids are contiguous int32 tensors, as many sources as destinations")
-        if t.get_device() not in (-1, dev):
-            raise ValueError(f"{where}: page ids on {t.device}, but the current device is cuda:{dev}")
+        if t.get_device() != dev and not (n == 0 or t.get_device() == -1 and t.is_pinned()):
+            raise ValueError(f"{where}: page ids on {t.device}; they lie on the current device (cuda:{dev}) or in pinned "
+                             "host memory")
     rc = _lib.pkv_kv_copy_pages(ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), src_pages.data_ptr(),
                                 dst_pages.data_ptr(), n, None if status is None else status.data_ptr(),
                                 _stream(stream))

@@ -527,3 +527,174 @@ def test_a_speculative_step_end_to_end(pkv):
         U.assert_close(out.double().cpu().numpy(), ref, "decode after the commit")
     torch.cuda.synchronize()
     assert int(status.item()) == 0
+
+
+# ---- the ends of the ranges ------------------------------------------------------------------------
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("gain", [1, 256])
+def test_infinities_in_the_prefix(pkv, gain, bf16):
+    """A key whose score is -infinity has no weight, an infinite V of the prefix is infinite in the output; in the
+    fast path and (scores that grow behind the first keys) in rows that are computed again."""
+    c = S.TreeCase([300, 90], [20, 9], seed=73)
+    c.q[:, :, 7] = np.maximum(c.q[:, :, 7] & 0x7FFF, 0x3C00)  # q_7 > 0 everywhere
+    for s in range(2):
+        for t in range(70, 270 if s == 0 else 81):
+            k = c.pool.data[c.bt[s, t // 16], 0, :, t % 16]
+            k[:] = ((rng.bf16_bits_to_f64(k) * gain).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    ref, err, size, spread = c.reference()
+    bt = c.bt
+    for t in (0, 37):                                         # gone: left out of what the oracle sums
+        c.pool.data[bt[0, t // 16], 0, :, t % 16, 7] = 0xFF80
+    want = []
+    for s in range(2):
+        k, v = (np.concatenate([rng.bf16_bits_to_f64(c.pool.data[bt[s, b], i]).transpose(1, 0, 2)
+                                for b in range(-(-int(c.lens[s]) // 16))])[:c.lens[s]] for i in (0, 1))
+        n, base = c.nodes[s], int(c.lens[s]) - c.nodes[s]
+        keep = np.ones(int(c.lens[s]), bool)
+        if s == 0:
+            keep[[0, 37]] = False
+        for j in range(n):
+            word = int(np.uint32(c.mask[c.starts[s] + j, 0]))
+            see = np.flatnonzero(keep & np.r_[np.ones(base, bool), [(word >> i) & 1 == 1 for i in range(n)]])
+            q = rng.bf16_bits_to_f64(c.q[c.starts[s] + j]).reshape(8, 4, 64)
+            x = np.einsum("ghd,tgd->ght", q, k[see]) * c.wl.scale
+            w = np.exp(x - x.max(-1, keepdims=True))
+            want.append(np.einsum("ght,tgd->ghd", w / w.sum(-1, keepdims=True), v[see]).reshape(32, 64))
+    want = np.array(want)
+    lim = S.bound(want, np.maximum(size, 8.0), spread, c.wl.scale, 300, bf16)
+    got, status = Run(pkv, c, bf16).call().result()
+    assert status == 0
+    S.assert_within(got, want, lim, "keys of score -infinity")
+    if gain == 1:                                             # (every weight is far from 0 here)
+        for t, bits in ((5, 0x7F80), (200, 0xFF80)):
+            c.pool.data[bt[0, t // 16], 1, :, t % 16, t % 64] = bits
+        got, status = Run(pkv, c, bf16).call().result()
+        first = got[:20]
+        assert np.isposinf(first[:, :, 5]).all() and np.isneginf(first[:, :, 200 % 64]).all()
+        dims = np.delete(np.arange(64), [5, 200 % 64])
+        S.assert_within(first[:, :, dims], want[:20][:, :, dims], lim[:20][:, :, dims], "the other dims")
+        S.assert_within(got[20:], want[20:], lim[20:], "the other sequence")
+
+
+def test_a_row_whose_scores_are_all_minus_infinity_is_zero(pkv):
+    c = S.TreeCase([30], [6], seed=74)
+    c.q[:, :, 7] = 0x3F80
+    for t in range(30):
+        c.pool.data[c.bt[0, t // 16], 0, :, t % 16, 7] = 0xFF80
+    got, status = Run(pkv, c).call().result()
+    assert status == 0 and not got.any()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("contexts,nodes", [([9000], [3]), ([30000, 700], [40, 64]), ([20000, 64], [8, 64])])
+def test_long_contexts_split_over_many_parts(pkv, contexts, nodes, bf16):
+    # units in tens of parts (merged in groups), and units cut into parts of many blocks
+    _check(pkv, S.TreeCase(contexts, nodes, seed=75), bf16)
+
+
+def test_segments_of_several_runs(pkv):
+    # as many units as there are CTAs and more: whole units of 47 blocks, their products added up in runs
+    c = S.TreeCase([3000, 2990, 2500, 3000] * 10, [2, 8, 1, 3] * 10, seed=76)
+    got = _check(pkv, c)
+    ref, _, size, _ = c.reference()
+    # weights in two bf16 terms (2^-18), 16 truncating blocks a run (16 * 1.4e-7 = 2^-18.8), 3 runs and the scores in fp32 (of
+    # exponents below 2^4: 2^-19): below 2^-16 of the size of the values
+    assert (np.abs(got - ref) <= size * 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_batches_larger_than_a_block(pkv, bf16):
+    # more sequences than the kernel has threads, one in three without nodes, some with two tiles
+    r = np.random.RandomState(11)
+    nodes = [0 if s % 3 == 1 else int(r.randint(1, 70 if s % 17 == 0 else 6)) for s in range(900)]
+    contexts = [n + int(r.randint(0, 60)) for n in nodes]
+    _check(pkv, S.TreeCase(contexts, nodes, seed=77), bf16)
+
+
+def test_pages_past_four_gigabytes(pkv):
+    """Tree attention (the fast path and rows computed again), commit and copies on pages whose byte offsets need
+    more than 32 bits."""
+    pages = 140_000                                            # 4.6 GB
+    pool = pkv.KVPool(pages, device=U.dev())
+    c = S.TreeCase([90, 40], [20, 7], seed=78)
+    used = c.wl.num_pages
+    view = pool.buffer.view(pages, -1)
+    for gain in (1, 256):
+        for s in range(2):
+            for t in range(65, int(c.lens[s])):
+                k = c.pool.data[c.bt[s, t // 16], 0, :, t % 16]
+                k[:] = ((rng.bf16_bits_to_f64(k) * gain).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+        view[pages - used:].copy_(U.to_dev(c.pool.data).view(used, -1))
+        bt = np.where(c.bt >= 0, c.bt + pages - used, -1).astype(np.int32)
+        small = Run(pkv, c).call().result()[0]
+        got, status = Run(pkv, c, pool=pool, bt=bt).call().result()
+        assert status == 0 and np.array_equal(got, small)
+    path, count = np.array([[1, 4, 19], [0, 6, -1]], np.int32), np.array([3, 2], np.int32)
+    status = torch.zeros(1, dtype=torch.int32, device=U.dev())
+    new = torch.zeros(2, dtype=torch.int32, device=U.dev())
+    pkv.tree_commit(pool, U.to_dev(bt), bt.shape[1], 0, 1, U.to_dev(c.starts), U.to_dev(c.lens), U.to_dev(path),
+                    U.to_dev(count), c.max_context, new, status)
+    spec.tree_commit(c.pool, c.bt[:, None], c.starts, c.lens, path, count, c.max_context)
+    high = np.arange(pages - used, pages, dtype=np.int32)
+    assert np.array_equal(U.bits(view[pages - used:]).reshape(c.pool.data.shape), c.pool.data)
+    pkv.kv_copy_pages(pool, U.to_dev(high), U.to_dev(high - used), status)
+    torch.cuda.synchronize()
+    assert torch.equal(view[pages - used:].view(torch.int16), view[pages - 2 * used:pages - used].view(torch.int16))
+    assert int(status.item()) == 0
+
+
+def test_calls_on_two_streams_at_once(pkv):
+    # each with its own workspace and output; the results are those of a call alone, bit for bit
+    cases = [S.TreeCase([2000] * 4, [40, 3, 64, 1], seed=79), S.TreeCase([5000, 17], [9, 17], seed=80)]
+    runs = [Run(pkv, c) for c in cases]
+    want = [r.call().result()[0] for r in runs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for r in runs:
+        r.out[:r.c.rows].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r, s in zip(runs, streams):
+            r.call(stream=s)
+    for r, w in zip(runs, want):
+        got, status = r.result()
+        assert status == 0 and np.array_equal(got, w)
+
+
+def test_two_graphs_of_one_workspace_in_turn(pkv):
+    # replayed one after the other on one stream: each leaves the workspace ready for the other
+    cases = [S.TreeCase([900, 33], [64, 33], seed=81), S.TreeCase([70] * 5, [2, 9, 1, 0, 70], seed=82)]
+    ws = pkv.tree_workspace(8, 70)
+    runs = [Run(pkv, c, workspace=ws) for c in cases]
+    want = [r.call().result()[0] for r in runs]
+    graphs = []
+    for r in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r.call()
+        graphs.append(g)
+        r.out[:r.c.rows].zero_()
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    for r, w in zip(runs, want):
+        got, status = r.result()
+        assert status == 0 and np.array_equal(got, w)
+
+
+def test_binding_refuses_tables_and_workspaces_of_the_wrong_kind(pkv):
+    c = S.TreeCase([50], [5], seed=83)
+    r = Run(pkv, c)
+    for name, bad in (("bt", r.bt.long()), ("bt", r.bt.cpu()), ("ws", r.ws.cpu())):
+        good = getattr(r, name)
+        setattr(r, name, bad)
+        with pytest.raises(ValueError):
+            r.call()
+        setattr(r, name, good)
+    with pytest.raises(ValueError):
+        pkv.tree_commit(r.pool, r.bt.long(), r.bt.shape[1], 0, 1, r.starts, r.lens, r.mask[:, :1], r.lens, 64)
+    with pytest.raises(ValueError):                            # host memory that is not pinned
+        pkv.kv_copy_pages(r.pool, torch.zeros(1, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+    with pytest.raises(pkv.PkvError):
+        c.max_context = 0x7FFFFFFF
+        r.call()
+    assert r.status.item() == 0
