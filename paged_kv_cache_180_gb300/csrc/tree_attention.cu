@@ -239,17 +239,14 @@ struct __align__(1024) Smem {
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 
-// T list entries over G CTAs: each has `each`, the first `more` of them one more.
+// T list entries over G CTAs: CTA i has those from i T / G on, rounded down, so that in a batch where every tile of a head
+// has a twin CTAs i and i + G / 2 work on the same keys at the same time.  (T < 2^54: at most 2^29 units of 2^25 blocks.)
 struct Shares {
-  long long each;
-  int more;
-  __device__ long long first(int cta) const { return cta * each + min(cta, more); }
+  long long T;
+  int G;
+  __device__ long long first(int cta) const { return divide(cta * T, G); }
   // CTA that has entry p
-  __device__ int owner(long long p) const {
-    const long long big = more * (each + 1);
-    const bool in_big = p < big;
-    return int(divide(in_big ? p : p - big, in_big ? each + 1 : each)) + (in_big ? 0 : more);
-  }
+  __device__ int owner(long long p) const { return int(divide((p + 1) * G - 1, T)); }
 };
 
 // Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
@@ -597,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     return;
   }
   Shares shares;
-  shares.each = divide(T, Gu);
-  shares.more = int(T - shares.each * Gu);
+  shares.T = T;
+  shares.G = Gu;
   const long long pa = shares.first(cta), pb = shares.first(cta + 1);
   // the sequence that holds entry pa: among those just scanned, or with a second look
   const int part0 = pa >= T0 ? 1 : 0;
