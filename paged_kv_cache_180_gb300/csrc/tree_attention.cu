@@ -156,6 +156,11 @@ struct Segment {
 // Places for segments.  The K loader is at most 5 blocks (and so segments) ahead of S, S 3 ahead of the products,
 // these one segment ahead of the softmax warps: place k is free when segment k + 16 is written to it.
 constexpr int kSegments = 16;
+// s_full barriers, and places for the blocks' invalid pages.  The K loader arrives at block n's when S of block n - 4 is
+// done, which was issued when the product of block n - 7 was: all softmax warps are past the place's last use, block
+// n - 8.  (An even number, so that a group sees every phase of the ones it waits on.)
+constexpr int kReady = 8;
+static_assert(kReady >= kStagesK + kScores + 1 && kReady % 2 == 0, "places in use");
 
 // Division of non-negative numbers; nearly always they have 32 bits.
 __device__ __forceinline__ long long divide(long long a, long long b) {
@@ -217,7 +222,7 @@ struct __align__(1024) Smem {
   uint64_t seg_full[kSegments];
   uint64_t mma_done[2];
   // ... of two ...
-  uint64_t s_full[2 * kScores];  // [block % 6], so that a group sees every phase of the ones it waits on
+  uint64_t s_full[kReady];       // [block % 8]: S, and from the K loader block_bad
   uint64_t sums_full[4];         // per quarter: both sums are there
   // ... of a group's four warps: they have written their P of the buffer ...
   uint64_t p_full[kScores];
@@ -227,8 +232,7 @@ struct __align__(1024) Smem {
   Segment cuts[2];  // a share cuts at most its first and its last unit: tickets taken at the end
   int cut_first[2], cut_parts[2];  // CTA with the unit's first part; parts
   int merge[2];     // this CTA took the last ticket of the cut unit (1) or of its group of parts (2)
-  int page_bad[kStagesK];      // bit pp: page pp of the K stage's block is invalid (loaded as zeros)
-  int block_bad[2 * kScores];  // the same for the block whose S is in s_full's place
+  int block_bad[kReady];  // [block % 8] bit pp: page pp of the block is invalid (loaded as zeros)
   int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
                      // never more than two segments apart: O is written again when all have read it)
   long long warp_sums[2][kThreads / 32];
@@ -712,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         }
         if (elect_one()) {
           if (bad) report(a.status, PKV_DEV_BAD_PAGE);
-          sm.page_bad[st] = bad;
+          sm.block_bad[gb % kReady] = bad;
+          mbar_arrive(&sm.s_full[gb % kReady]);
           mbar_arrive_expect_tx(&sm.k_full[st], kTileBytes);
 #pragma unroll
           for (int i = 0; i < kPagesPerBlock; ++i)
@@ -796,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const uint64_t qdesc = q_desc + uint32_t((k & 1) * kRows * kRowBytes >> 4);
 #pragma unroll 1
       for (int j = 0; j < blocks; ++j, ++gb) {
-        const int st = int(gb % kStagesK), b = int(gb % kScores), f = int(gb % (2 * kScores));
+        const int st = int(gb % kStagesK), b = int(gb % kScores);
         w = wait(sm, &sm.k_full[st], (gb / kStagesK) & 1);
         if (w && gb >= kScores) w = wait(sm, &sm.p_free[b], (gb / kScores - 1) & 1);
         if (!__all_sync(0xffffffffu, w)) {
@@ -809,9 +814,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tmem + b * kKeys, qdesc + kk * (32 >> 4), kdesc + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
-          tc_commit(&sm.s_full[f]);
-          sm.block_bad[f] = sm.page_bad[st];
-          mbar_arrive(&sm.s_full[f]);  // passes block_bad on
+          tc_commit(&sm.s_full[gb % kReady]);
           tc_commit(&sm.k_empty[st]);
           if (j == blocks - 1) tc_commit(&sm.q_empty[k & 1]);  // the segment's last read of its Q
         }
@@ -879,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;  // half: the group, and dims 32 half .. + 31
     const uint32_t my_tmem = tmem + (uint32_t(32 * quarter) << 16);
     unsigned gb0 = 0;  // blocks before the segment
+    unsigned gb = half, b = half;  // the group's next block, its S / P buffer
     int turns = 0;     // segments in which this warp has had rows (the two warps of a quarter agree)
     int cuts = 0;      // bit 0, 1: the share's first, last unit is cut
     bool ok = true;
@@ -986,83 +990,102 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
       float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
       const int last_run = kBf16 || !more ? 0 : (j1 - j0 - 1) / kRunBlocks;
+      // Blocks before `plain_end` hold no nodes, no run ends at them and the reference is there.
+      int plain_end = 0;
 #pragma unroll 1
-      for (int j = j0 + (leads ? 0 : 1); ok; j += 2) {
-        const bool has = j < j1;
-        // the runs to end before this block's P is handed over: all before its own; after the last block
-        // all but the segment's last
-        const unsigned due = runs + (has && !kBf16 ? (j - j0) / kRunBlocks : has ? 0 : last_run);
-        if (!has && ended == due) break;
-        const unsigned gb = gb0 + unsigned(j - j0);
-        const int b = int(gb % kScores), f = int(gb % (2 * kScores)), key0 = j * kKeys;
-        if (has) {
-          w = wait(sm, &sm.s_full[f], (gb / (2 * kScores)) & 1);
-          if (w && key0 + kKeys > base) {
-            // the block holds nodes: the group's threads look through V, two to a row
-            const int st = int(gb % kStagesV), r = (tid & 127) >> 1, pos = key0 + r;
-            w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1);  // (the phase before has been consumed)
-            __syncwarp();
-            uint8_t *vrow = sm.v[st] + r * kRowBytes;
-            uint32_t bits = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              bits |= nonfinite(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
-            bool inf = bits != 0 && pos >= base && pos < x.ctx;
-            inf |= __shfl_xor_sync(0xffffffffu, int(inf), 1) != 0;
-            if (pos >= x.ctx || inf) {
+      for (int j = j0 + (leads ? 0 : 1);; j += 2) {
+        const uint32_t taddr = my_tmem + b * kKeys;
+        bool plain = j < plain_end, has = true;
+        unsigned due = 0;
+        if (__builtin_expect(plain, 1)) {
+          w = wait(sm, &sm.s_full[gb % kReady], (gb / kReady) & 1);
+          ok = __all_sync(0xffffffffu, w);
+          if (!ok) break;
+          tc_fence_after();
+          plain = sm.block_bad[gb % kReady] == 0;
+        }
+        if (__builtin_expect(!plain, 0)) {
+          has = j < j1;
+          // the runs to end before this block's P is handed over: all before its own; after the last block
+          // all but the segment's last
+          due = runs + (has && !kBf16 ? (j - j0) / kRunBlocks : has ? 0 : last_run);
+          if (!has && ended == due) break;
+          if (has) {
+            const int key0 = j * kKeys;
+            w = wait(sm, &sm.s_full[gb % kReady], (gb / kReady) & 1);
+            if (w && key0 + kKeys > base) {
+              // the block holds nodes: the group's threads look through V, two to a row
+              const int st = int(gb % kStagesV), r = (tid & 127) >> 1, pos = key0 + r;
+              w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1);  // (the phase before has been consumed)
+              __syncwarp();
+              uint8_t *vrow = sm.v[st] + r * kRowBytes;
+              uint32_t bits = 0;
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (inf) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
-            fence_proxy_async_smem();
-          }
-          if (active && j > j0 && j == j0 + 1) {  // (this group does not lead: the row's reference is the other's)
-            w = wait(sm, &sm.ref_full[quarter][turns & 1], uint32_t(turns >> 1) & 1) && w;
-            const float ref = sm.ref[turns & 3][row];
-            minus_r = make_float2(-ref, -ref);
-          }
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
-          if (active) {
-            tc_fence_after();
-            const uint32_t taddr = my_tmem + b * kKeys;
-            const int bad = sm.block_bad[f];
-            const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
-            if (masked) {
-              uint32_t see0 = ~0u, see1 = ~0u;
-              if (key0 + kKeys > base) {
-                const uint32_t *mask = a.mask + (long long)(x.q0 + node) * a.mask_stride;
-                see0 = real ? window_bits(mask, key0, base, x.ctx, x.n) : 0u;
-                see1 = real ? window_bits(mask, key0 + 32, base, x.ctx, x.n) : 0u;
+                bits |= nonfinite(*reinterpret_cast<const uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16));
+              bool inf = bits != 0 && pos >= base && pos < x.ctx;
+              inf |= __shfl_xor_sync(0xffffffffu, int(inf), 1) != 0;
+              if (pos >= x.ctx || inf) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<uint4 *>(vrow + (((tid & 1) * 4 + i) ^ (r & 7)) * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
-              if (bad & 1) see0 &= 0xffff0000u;
-              if (bad & 2) see0 &= 0x0000ffffu;
-              if (bad & 4) see1 &= 0xffff0000u;
-              if (bad & 8) see1 &= 0x0000ffffu;
-              hide_keys(taddr, see0, see1, a.c.x);
+              if (inf) *reinterpret_cast<volatile int *>(&sm.nonfinite[k & 3]) = k;
+              fence_proxy_async_smem();
             }
-            if (j == j0) {
-              const float ref = block_reference(taddr, a.c.x);
+            if (active && j > j0 && j == j0 + 1) {  // (this group does not lead: the row's reference is the other's)
+              w = wait(sm, &sm.ref_full[quarter][turns & 1], uint32_t(turns >> 1) & 1) && w;
+              const float ref = sm.ref[turns & 3][row];
               minus_r = make_float2(-ref, -ref);
-              sm.ref[turns & 3][row] = ref;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.ref_full[quarter][turns & 1]);
             }
-            block_weights<kBf16>(taddr, a.c, minus_r, l2);
-            tc_fence_before();
+            ok = __all_sync(0xffffffffu, w);
+            if (!ok) break;
+            if (active) {
+              tc_fence_after();
+              const int bad = sm.block_bad[gb % kReady];
+              const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
+              if (masked) {
+                uint32_t see0 = ~0u, see1 = ~0u;
+                if (key0 + kKeys > base) {
+                  const uint32_t *mask = a.mask + (long long)(x.q0 + node) * a.mask_stride;
+                  see0 = real ? window_bits(mask, key0, base, x.ctx, x.n) : 0u;
+                  see1 = real ? window_bits(mask, key0 + 32, base, x.ctx, x.n) : 0u;
+                }
+                if (bad & 1) see0 &= 0xffff0000u;
+                if (bad & 2) see0 &= 0x0000ffffu;
+                if (bad & 4) see1 &= 0xffff0000u;
+                if (bad & 8) see1 &= 0x0000ffffu;
+                hide_keys(taddr, see0, see1, a.c.x);
+              }
+              if (j == j0) {
+                const float ref = block_reference(taddr, a.c.x);
+                minus_r = make_float2(-ref, -ref);
+                sm.ref[turns & 3][row] = ref;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ref_full[quarter][turns & 1]);
+              }
+            }
           }
         }
+        if (active && has) {
+          block_weights<kBf16>(taddr, a.c, minus_r, l2);
+          tc_fence_before();
+        }
+        if (__builtin_expect(!plain, 0)) {
 #pragma unroll 1
-        while (ok && ended != due) {
-          const bool last = ended < runs;  // of the segment before
-          ok = end_run(last ? k - 1 : k, last ? before : runs, last);
+          while (ok && ended != due) {
+            const bool last = ended < runs;  // of the segment before
+            ok = end_run(last ? k - 1 : k, last ? before : runs, last);
+          }
+          plain_end = min(j1, base / kKeys);
+          if constexpr (!kBf16) plain_end = min(plain_end, j0 + ((j - j0) / kRunBlocks + 1) * kRunBlocks);
         }
         __syncwarp();
-        if (has && lane == 0) mbar_arrive(&sm.p_full[b]);
         if (!has) break;
+        if (lane == 0) mbar_arrive(&sm.p_full[b]);
+        if (!ok) break;
+        gb += 2;
+        b = b == 0 ? kScores - 1 : b - 1;  // + 2 modulo 3
       }
       if (!ok || !more) break;
       gb0 += unsigned(j1 - j0);
