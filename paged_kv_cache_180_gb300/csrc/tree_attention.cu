@@ -627,31 +627,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   // The pages of a segment's blocks: table entries 32 at a time (8 blocks), the next 32 in flight.
   struct Pages {
     const int32_t *table;
-    int npages, first, ent, ent_next;
-    __device__ int entries(int p, int lane) const { return p + lane < npages ? __ldg(table + p + lane) : -1; }
+    int npages, next, ent, ent_next;  // of this lane; -1: not in the pool
+    unsigned bad;                     // bit i: lane i's is inside the context and not in the pool
+    __device__ int entry(int p) const { return p < npages ? __ldg(table + p) : -1; }
+    __device__ void check(int p, int num_pages) {
+      if (ent >= num_pages) ent = -1;
+      bad = __ballot_sync(0xffffffffu, ent < 0 && p < npages);
+    }
     __device__ void start(const TreeArgs &a, const Segment &x, int lane) {
       table = a.block_tables + (long long)x.s * a.bt_stride;
       npages = (x.ctx - 1) / kPageTokens + 1;
-      first = x.j0 * kPagesPerBlock;
-      ent = entries(first, lane);
-      ent_next = entries(first + 32, lane);
+      next = x.j0 * kPagesPerBlock;
+      ent = entry(next + lane);
+      ent_next = entry(next + 32 + lane);
+      check(next + lane, a.num_pages);
     }
-    // Pages of block j (taken in order), -1 for what is not in the pool: TMA fills these with zeros.  Returns
-    // the bits of those inside the context.
-    __device__ int block(int j, int num_pages, int lane, int (&page)[kPagesPerBlock]) {
-      const int p = j * kPagesPerBlock, at = (p - first) & 31;
-      if (at == 0 && p > first) {
+    // Pages of the segment's block number i (in order), -1 for what is not in the pool: TMA fills these with zeros.
+    // Returns the bits of those inside the context.
+    __device__ int block(int i, int num_pages, int lane, int (&page)[kPagesPerBlock]) {
+      const int at = i * kPagesPerBlock & 31;
+      if (at == 0 && i > 0) {
+        next += 32;
         ent = ent_next;
-        ent_next = entries(p + 32, lane);
+        ent_next = entry(next + 32 + lane);
+        check(next + lane, num_pages);
       }
-      int bad = 0;
 #pragma unroll
-      for (int i = 0; i < kPagesPerBlock; ++i) {
-        const int e = __shfl_sync(0xffffffffu, ent, at + i);
-        page[i] = e >= 0 && e < num_pages ? e : -1;
-        if (page[i] < 0 && p + i < npages) bad |= 1 << i;
-      }
-      return bad;
+      for (int k = 0; k < kPagesPerBlock; ++k) page[k] = __shfl_sync(0xffffffffu, ent, at + k);
+      return bad >> at & ((1 << kPagesPerBlock) - 1);
     }
   };
 
@@ -701,12 +704,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       if (!waited) griddep_wait();
       waited = true;
       const uint64_t policy = x.n > kTok ? again : once;  // several tiles read the same K/V
-      const int j1 = x.j1, y = x.g * kPageTokens;
+      const int j0 = x.j0, j1 = x.j1, y = x.g * kPageTokens;
 #pragma unroll 1
-      for (int j = x.j0; j < j1; ++j, ++gb) {
+      for (int j = j0; j < j1; ++j, ++gb) {
         const int st = int(gb % kStagesK);
         int page[kPagesPerBlock];
-        const int bad = pages.block(j, a.num_pages, lane, page);
+        const int bad = pages.block(j - j0, a.num_pages, lane, page);
         if (gb >= kStagesK) {
           const bool w = wait(sm, &sm.k_empty[st], (gb / kStagesK - 1) & 1);
           if (!__all_sync(0xffffffffu, w)) {
@@ -752,12 +755,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       if (!waited) griddep_wait();
       waited = true;
       const uint64_t policy = x.n > kTok ? again : once;
-      const int j1 = x.j1, y = x.g * kPageTokens;
+      const int j0 = x.j0, j1 = x.j1, y = x.g * kPageTokens;
 #pragma unroll 1
-      for (int j = x.j0; j < j1; ++j, ++gb) {
+      for (int j = j0; j < j1; ++j, ++gb) {
         const int st = int(gb % kStagesV);
         int page[kPagesPerBlock];
-        pages.block(j, a.num_pages, lane, page);
+        pages.block(j - j0, a.num_pages, lane, page);
         if (gb >= kStagesV) {
           w = wait(sm, &sm.v_empty[st], (gb / kStagesV - 1) & 1);
           if (!__all_sync(0xffffffffu, w)) {
