@@ -67,7 +67,9 @@ constexpr int kCtasPerSm = 2;
 constexpr int kRegsOthers = 40, kRegsSoftmax = 96;
 static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax <= kThreads * 80, "registers of a CTA");
 constexpr int kMaxCtas = 320;
-constexpr int kMinBlocks = 2;                       // least list entries a CTA is given
+// Least list entries a CTA is given: 2, and up to 6 where the longest unit would be in more parts than one merge takes
+// (a second level of merges takes as long as 6 blocks).
+constexpr int kMinEntries = 2, kMostEntries = 6;
 // With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
 // a run's O goes to the segment's part in the workspace, where the runs are added with rounding.
@@ -215,14 +217,14 @@ struct __align__(1024) Smem {
   float sums[4][2][kRows];   // [turn][group]: a row's sum
   // barriers of one arrival ...
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[kStagesK], k_empty[kStagesK], v_full[kStagesV], v_empty[kStagesV];
-  uint64_t p_free[kScores];      // the product of a block is done: its buffer may be written
+  uint64_t k_full[kStagesK], v_full[kStagesV];
+  uint64_t p_free[kReady];       // [block % 8]: the product of a block is done: its buffer may be written, its V replaced
   uint64_t o_full;               // a run's products are done
   uint64_t ref_full[4][2];       // per quarter of the lanes, by turn: ref is there
   uint64_t seg_full[kSegments];
   uint64_t mma_done[2];
   // ... of two ...
-  uint64_t s_full[kReady];       // [block % 8]: S, and from the K loader block_bad
+  uint64_t s_full[kReady];       // [block % 8]: S (its K may be replaced), and from the K loader block_bad
   uint64_t sums_full[4];         // per quarter: both sums are there
   // ... of a group's four warps: they have written their P of the buffer ...
   uint64_t p_full[kScores];
@@ -236,6 +238,7 @@ struct __align__(1024) Smem {
   int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
                      // never more than two segments apart: O is written again when all have read it)
   long long warp_sums[2][kThreads / 32];
+  int warp_longest[2][kThreads / 32];
   long long first;  // list index of seq0's first entry
   int seq0;
   uint32_t tmem_base;
@@ -300,26 +303,18 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[16], float2 c, float
   }
 }
 
-// The weights of a row's 64 keys, from S to P in place: of each 32 keys, hi in the first 16 columns, lo in the
-// others.  16 keys at a time: the next 16 scores are on their way while these are worked on, and P of 16
-// keys is stored once the scores that lay there have been read.
+// The weights of a row's 64 keys, from S to P in place: of each 16 keys, hi in the first 8 columns, lo in the others.
+// (Loading the next 16 scores ahead changed nothing: other warps fill the time.)
 template <bool kBf16>
 __device__ __forceinline__ void block_weights(uint32_t taddr, float2 c, float2 minus_r, float2 &sum) {
-  uint32_t a[16], b[16], hi[8], lo[8];
-  tmem_ld16_async(taddr, a);
-  tmem_ld_wait(a);
 #pragma unroll 1
-  for (int i = 0; i < 2; ++i, taddr += 32) {
-    tmem_ld16_async(taddr + 16, b);
-    weights<kBf16>(a, c, minus_r, sum, hi, lo);
-    tmem_ld_wait(b);
+  for (int i = 0; i < 4; ++i, taddr += 16) {
+    uint32_t x[16], hi[8], lo[8];
+    tmem_ld16_async(taddr, x);
+    tmem_ld_wait(x);
+    weights<kBf16>(x, c, minus_r, sum, hi, lo);
     tmem_st8_async(taddr, hi);
-    if constexpr (!kBf16) tmem_st8_async(taddr + 16, lo);
-    if (i == 0) tmem_ld16_async(taddr + 32, a);
-    weights<kBf16>(b, c, minus_r, sum, hi, lo);
-    tmem_ld_wait(a);
-    tmem_st8_async(taddr + 8, hi);
-    if constexpr (!kBf16) tmem_st8_async(taddr + 24, lo);
+    if constexpr (!kBf16) tmem_st8_async(taddr + 8, lo);
   }
   tmem_st_wait();
 }
@@ -553,23 +548,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   if (tid == 4) sm.abort = 0;
   // Entries of sequences s0 + tid in a part; `end`: up to and with this thread.  Returns the total over all threads.
   // (The places of warp_sums are used in turn: one barrier a call.)
-  int place = 0;
+  int place = 0, longest = 0;  // blocks of the longest unit
   auto scan = [&](int s0, int part, long long &mine, long long &end) {
     mine = 0;
+    int nb = 0;
     if (s0 + tid < a.num_seqs) {
       Seq q;
       q.load(a, s0 + tid);
       mine = q.entries(part);
+      nb = q.nb;
     }
+    nb = __reduce_max_sync(0xffffffffu, nb);
     end = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += y;
     }
-    if (lane == 31) sm.warp_sums[place][warp] = end;
+    if (lane == 31) {
+      sm.warp_sums[place][warp] = end;
+      sm.warp_longest[place][warp] = nb;
+    }
     __syncthreads();
     long long x = lane < kThreads / 32 ? sm.warp_sums[place][lane] : 0;
+    longest = max(longest, __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_longest[place][lane] : 0));
     place ^= 1;
 #pragma unroll
     for (int o = 1; o < kThreads / 32; o <<= 1) {
@@ -589,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) T += scan(s0, part, mine, end);
   }
   if (parts == 1) T0 = T;
-  const int Gu = int(min((long long)G, max(1LL, T / kMinBlocks)));  // CTAs with a share
+  const int least = min(max((longest + kUnitCost) / (2 * kMergeGroup - 1) + 1, kMinEntries), kMostEntries);
+  const int Gu = int(min((long long)G, max(1LL, divide(T, least))));  // CTAs with a share
   if (T == 0 || cta >= Gu) {
     if (warp == kScoreWarp) tmem_dealloc(sm.tmem_base, kTmemCols);
     griddep_wait();
@@ -711,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         int page[kPagesPerBlock];
         const int bad = pages.block(j - j0, a.num_pages, lane, page);
         if (gb >= kStagesK) {
-          const bool w = wait(sm, &sm.k_empty[st], (gb / kStagesK - 1) & 1);
+          const unsigned before = gb - kStagesK;  // S of the block whose place it takes is done
+          const bool w = wait(sm, &sm.s_full[before % kReady], (before / kReady) & 1);
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
@@ -762,7 +766,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         int page[kPagesPerBlock];
         pages.block(j - j0, a.num_pages, lane, page);
         if (gb >= kStagesV) {
-          w = wait(sm, &sm.v_empty[st], (gb / kStagesV - 1) & 1);
+          const unsigned before = gb - kStagesV;
+          w = wait(sm, &sm.p_free[before % kReady], (before / kReady) & 1);
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       for (int j = 0; j < blocks; ++j, ++gb) {
         const int st = int(gb % kStagesK), b = int(gb % kScores);
         w = wait(sm, &sm.k_full[st], (gb / kStagesK) & 1);
-        if (w && gb >= kScores) w = wait(sm, &sm.p_free[b], (gb / kScores - 1) & 1);
+        if (w && gb >= kScores) w = wait(sm, &sm.p_free[(gb - kScores) % kReady], ((gb - kScores) / kReady) & 1);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
@@ -818,7 +823,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tmem + b * kKeys, qdesc + kk * (32 >> 4), kdesc + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
           tc_commit(&sm.s_full[gb % kReady]);
-          tc_commit(&sm.k_empty[st]);
           if (j == blocks - 1) tc_commit(&sm.q_empty[k & 1]);  // the segment's last read of its Q
         }
         __syncwarp();
@@ -863,10 +867,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           for (int kk = 0; kk < kKeys / 16; ++kk)
 #pragma unroll
             for (int term = 0; term < (kBf16 ? 1 : 2); ++term)
-              tc_mma_tmem_a(tmem + kColO, tmem + b * kKeys + (kk >> 1) * 32 + (kk & 1) * 8 + term * 16,
+              tc_mma_tmem_a(tmem + kColO, tmem + b * kKeys + kk * 16 + term * 8,
                             vdesc + kk * (2048 >> 4), kIdescPV, (in_run == 0 && kk == 0 && term == 0) ? 0u : 1u);
-          tc_commit(&sm.p_free[b]);
-          tc_commit(&sm.v_empty[st]);
+          tc_commit(&sm.p_free[gb % kReady]);
           if (run_ends) tc_commit(&sm.o_full);
         }
         __syncwarp();
@@ -1279,12 +1282,12 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   a.parts = static_cast<pkv::Part *>(workspace);
   a.tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + 2 * size_t(pkv::kMaxCtas) * sizeof(pkv::Part));
   a.status = device_status;
-  // no more CTAs than the list can have shares of kMinBlocks entries
+  // no more CTAs than the list can have shares
   const double entries = double(num_seqs) * tiles * pkv::kKvHeads * (max_context / pkv::kKeys + 1 + pkv::kUnitCost);
   const int sms = pkv::device_sm_count();
   long long grid = (long long)(sms > 0 ? sms : 152) * pkv::kCtasPerSm;
   if (grid > pkv::kMaxCtas) grid = pkv::kMaxCtas;
-  if (double(grid) > entries / pkv::kMinBlocks) grid = (long long)(entries / pkv::kMinBlocks);
+  if (double(grid) > entries / pkv::kMinEntries) grid = (long long)(entries / pkv::kMinEntries);
   if (grid < 1) grid = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
