@@ -15,7 +15,8 @@ namespace {
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunks = kHalfPageBytes / 16 / kCopyThreads;  // 16-byte chunks a thread moves: 4
 
-// One CTA moves the K or the V half of one pair (16 KiB).
+// One CTA moves the K or the V half of one pair (16 KiB): 16384 pages take 158 us, 6.8 TB/s of reads and writes, the
+// rate of one plain large copy; 512 take 5.4 us and 16, bound by the launch and two round trips, 2.2.
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_pages_kernel(
     uint8_t *__restrict__ k_base, uint8_t *__restrict__ v_base, long long page_stride, int num_pages,
     const int32_t *__restrict__ src_pages, const int32_t *__restrict__ dst_pages, int32_t *status) {
@@ -62,6 +63,9 @@ struct CommitArgs {
 // a batch of loads reads all lie at or behind the rows its stores write, and every row a later batch reads lies
 // behind them.  Each thread reads and writes its own chunk only, so loading a batch before storing it is all
 // the ordering there is.
+// What bounds it is three dependent round trips (lengths, path and tables, rows) and rows that lie in pieces of 128
+// bytes: 256 sequences x 16 layers with paths of up to 12 of 32 nodes take 19.4 us (13.5 for the bytes), 64 with up to
+// 8 take 4.1, one sequence 2.8.  (4 or 16 rows in flight: 19.4 and 23.5 us; two layers to a CTA: 20 us, and 4.4 for 64.)
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a) {
   __shared__ long long from[kCommitRows], to[kCommitRows];  // byte offsets in either half of the pool; to < 0: stays
   griddep_launch_dependents();

@@ -13,17 +13,22 @@
 //  * Work split: the key blocks of all units form one list; the grid's CTAs (two per SM) take equal
 //    shares of it, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
 //    state (r, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
-//    atomic counter, nobody waits) merges them.
+//    atomic counter, nobody waits) merges them.  (A merge takes 1.8 us with 24 rows and 3 to 5 us with 128.)
 //  * Warp roles (384 threads): 8 softmax warps, a loader of K and one of V (tiled TMA, head g's 16 rows of
-//    each page as 2 KiB boxes, into rings of 5 and 6 blocks: a K block is free once its S is there, a V block waits
-//    for the softmax too), one warp that loads Q (boxes of 8 nodes x 4 heads) and issues S, and one that
-//    issues the products with V: nobody's waits hold up another's work.
+//    each page as 2 KiB boxes, into rings of 4 and 5 blocks: a K block is free once its S is there, a V block waits
+//    for the softmax too), one warp that issues S and one that issues the products with V: nobody's waits hold up
+//    another's work.  The K loader walks the list and loads Q too (boxes of 8 nodes x 4 heads).
 //  * S = Q K^T is 4 tcgen05.mma (M 128, N 64, K 16) into one of three TMEM buffers.  The softmax warps form two
 //    groups that take the blocks in turn, a thread to a row; P overwrites its S and is the TMEM A operand
-//    of O += P V.  A block takes a softmax warp some 1300 cycles, nearly all of it latency (tensor memory,
-//    barriers, dependent arithmetic), so what counts is how many blocks are under way: two groups, and the S of
-//    one block more in reserve.  (Two threads to a row on the same block, with S buffers for two blocks, took
-//    1650 cycles a block.)
+//    of O += P V.  (Two threads to a row on the same block, with S buffers for two blocks, took 1650 cycles a block
+//    against 1300.)
+//  * What bounds it, by the time a call takes: with many keys a node the K/V bytes: 256 sequences of 2048 tokens and 8
+//    nodes take 179 us, 6.1 TB/s, 90 % of a plain copy's rate.  With many short units their starts and ends: each costs
+//    as much as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 62 us, 24 for the bytes).  With 64 nodes two
+//    tiles share the bytes, and the steps from barrier to barrier count: 64 x 2048 in bf16 takes 83 us; without
+//    all of the softmax's arithmetic it would be 76, without the loads too 66, without the merges 73.  The
+//    smallest call (600 tokens, 6 nodes) takes 10.3 us: launch 2, lengths and list 1.5, tables and first K 1.7,
+//    two blocks 2.5, tickets and merge 2.6.
 //  * The reference is the row's largest exponent in the segment's first block and stays: weights are floats, so
 //    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
 //    that.  A row whose sum leaves [2^-90, 2^112] is computed again from global memory by redo_row(), slowly (with every
@@ -74,7 +79,8 @@ constexpr int kMinEntries = 2, kMostEntries = 6;
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
 // a run's O goes to the segment's part in the workspace, where the runs are added with rounding.
 constexpr int kRunBlocks = 16;
-constexpr int kUnitCost = 5;                        // what a unit's start and end weigh in the list, in blocks
+constexpr int kUnitCost = 5;                        // what a unit's start and end weigh in the list, in blocks (4, 6 and 7
+                                                    // were 0 to 2 % slower or faster, each on some batches)
 constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
 constexpr int kTileBytes = kKeys * kRowBytes;       // K (or V) of one block: 8 KiB
 constexpr int kOctetBytes = kOctet * kGroup * kRowBytes;  // 4 KiB
