@@ -74,6 +74,7 @@ static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax
 constexpr int kMaxCtas = 320;
 // Least list entries a CTA is given: 2, and up to 6 where the longest unit would be in more parts than one merge takes
 // (a second level of merges takes as long as 6 blocks).
+constexpr int kClaimUnits = 2;
 constexpr int kMinEntries = 2, kMostEntries = 6;
 // With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
@@ -100,7 +101,8 @@ struct Part {
   float4 o[kHeadDim / 4][kRows];  // [4 dims][row]: neighbouring lanes hold neighbouring rows
   float2 rl[2][kRows];            // (reference, sum) of a row, for either half of its dims
   float2 group_rl[2][kRows];      // of the merged state of the group of parts that this one is the first of
-  int ticket, unused[3];          // of that group; 0 between calls
+  int ticket;                     // of that group; 0 between calls
+  int claimed, done, unused;      // in the first part: units claimed, CTAs that are done; 0 between calls
 };
 
 struct TreeArgs {
@@ -215,6 +217,46 @@ struct Walk {
   }
 };
 
+// The same where the CTAs claim whole units, one after the other (`Claims` below): unit `u` of the batch in the order sequence,
+// head, tile, looked for from the sequences s0 .. s0 + 31 on, by all lanes of a warp.  Units come in ascending order.
+struct Claimed {
+  int s0, before;  // units before sequence s0
+  __device__ bool find(const TreeArgs &a, int u, int lane, Segment &x) {
+    for (;; s0 += 32) {
+      if (s0 >= a.num_seqs) {
+        x.s = -1;
+        return false;
+      }
+      Seq seq;
+      seq.tiles = 0;
+      if (s0 + lane < a.num_seqs) seq.load(a, s0 + lane);
+      const int units = seq.tiles * kKvHeads;
+      int end = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, end, 31);
+      if (u - before < total) {
+        const int l = __ffs(__ballot_sync(0xffffffffu, u - before < end)) - 1;
+        const int v = u - before - __shfl_sync(0xffffffffu, end - units, l);
+        seq.load(a, s0 + l);
+        x.s = s0 + l;
+        x.g = v / seq.tiles;
+        x.tile = v - x.g * seq.tiles;
+        x.q0 = seq.q0;
+        x.n = seq.n;
+        x.ctx = seq.ctx;
+        x.nb = x.j1 = seq.nb;
+        x.j0 = 0;
+        return true;
+      }
+      before += total;
+    }
+  }
+};
+
 struct __align__(1024) Smem {
   uint8_t q[2][kRows * kRowBytes];
   uint8_t k[kStagesK][kTileBytes];
@@ -244,7 +286,7 @@ struct __align__(1024) Smem {
   int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
                      // never more than two segments apart: O is written again when all have read it)
   long long warp_sums[2][kThreads / 32];
-  int warp_longest[2][kThreads / 32];
+  int warp_longest[2][kThreads / 32], warp_units[2][kThreads / 32];
   long long first;  // list index of seq0's first entry
   int seq0;
   uint32_t tmem_base;
@@ -554,17 +596,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   if (tid == 4) sm.abort = 0;
   // Entries of sequences s0 + tid in a part; `end`: up to and with this thread.  Returns the total over all threads.
   // (The places of warp_sums are used in turn: one barrier a call.)
-  int place = 0, longest = 0;  // blocks of the longest unit
+  int place = 0, longest = 0, units = 0;  // blocks of the longest unit; units of both parts
+  const bool many = (long long)a.num_seqs * a.max_tiles * kKvHeads >= kClaimUnits * G;
   auto scan = [&](int s0, int part, long long &mine, long long &end) {
     mine = 0;
-    int nb = 0;
+    int nb = 0, tiles = 0;
     if (s0 + tid < a.num_seqs) {
       Seq q;
       q.load(a, s0 + tid);
       mine = q.entries(part);
       nb = q.nb;
+      tiles = q.part_tiles(part);
     }
     nb = __reduce_max_sync(0xffffffffu, nb);
+    if (many) tiles = __reduce_add_sync(0xffffffffu, tiles);
     end = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -574,10 +619,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     if (lane == 31) {
       sm.warp_sums[place][warp] = end;
       sm.warp_longest[place][warp] = nb;
+      sm.warp_units[place][warp] = tiles * kKvHeads;
     }
     __syncthreads();
     long long x = lane < kThreads / 32 ? sm.warp_sums[place][lane] : 0;
     longest = max(longest, __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_longest[place][lane] : 0));
+    if (many) units += __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_units[place][lane] : 0);
     place ^= 1;
 #pragma unroll
     for (int o = 1; o < kThreads / 32; o <<= 1) {
@@ -606,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     zero_rows<kBf16>(a, cta, G, tid);
     return;
   }
+  const bool claims = units >= kClaimUnits * G && (longest + kUnitCost) * (long long)G <= T;
   Shares shares;
   shares.T = T;
   shares.G = Gu;
@@ -615,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   const bool again = a.num_seqs > kThreads || part0 != parts - 1;
   long long start = part0 ? T0 : 0;
 #pragma unroll 1
-  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+  for (int s0 = 0; s0 < a.num_seqs && !claims; s0 += kThreads) {
     long long total = 0;
     if (again) total = scan(s0, part0, mine, end);
     if (start + end - mine <= pa && pa < start + end) {
@@ -671,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   if (warp == kLoadWarpK) {
     // ================= K loader (tiled TMA); it walks the list =================
     const uint64_t once = policy_evict_first(), again = policy_evict_last();
+    Claimed claimed = {0, 0};
     Walk walk;
     walk.pos = pa;
     walk.end = pb;
@@ -687,7 +736,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
 #pragma unroll 1
     for (int k = 0; ok; ++k) {
       Segment &x = sm.seg[k % kSegments];
-      const bool more = walk.next(a, x);  // every lane writes the same
+      bool more;  // every lane writes the same
+      if (claims) {
+        int u = cta;
+        if (k > 0) {
+          if (lane == 0) u = G + atomicAdd(&a.parts->claimed, 1);
+          u = __shfl_sync(0xffffffffu, u, 0);
+        }
+        more = claimed.find(a, u, lane, x);
+      } else {
+        more = walk.next(a, x);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.seg_full[k % kSegments]);
       if (!more) break;
@@ -1183,6 +1242,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort) report(a.status, PKV_DEV_TIMEOUT);
+  if (tid == 0 && claims && atomicAdd(&a.parts->done, 1) == G - 1) {
+    atomicExch(&a.parts->claimed, 0);  // ready for the next call
+    atomicExch(&a.parts->done, 0);
+  }
   zero_rows<kBf16>(a, cta, G, tid);
   if (warp == kScoreWarp) {
     tc_fence_after();
