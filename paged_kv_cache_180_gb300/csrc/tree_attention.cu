@@ -74,7 +74,7 @@ static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax
 constexpr int kMaxCtas = 320;
 // Least list entries a CTA is given: 2, and up to 6 where the longest unit would be in more parts than one merge takes
 // (a second level of merges takes as long as 6 blocks).
-constexpr int kClaimUnits = 2;
+constexpr int kClaimQuarters = 7, kClasses = 2;
 constexpr int kMinEntries = 2, kMostEntries = 6;
 // With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
@@ -191,7 +191,10 @@ struct Walk {
         first += seq.entries(part);
         if (++s == a.num_seqs) {
           s = 0;
-          part = 1;
+          if (++part == 2) {  // (never with lengths that stay as they are)
+            x.s = -1;
+            return false;
+          }
         }
         seq.load(a, s);
       }
@@ -217,20 +220,27 @@ struct Walk {
   }
 };
 
-// The same where the CTAs claim whole units, one after the other (`Claims` below): unit `u` of the batch in the order sequence,
-// head, tile, looked for from the sequences s0 .. s0 + 31 on, by all lanes of a warp.  Units come in ascending order.
+// The same where the CTAs claim whole units, one after the other: unit `u` in the order length class, sequence, head, tile,
+// looked for from the sequences s0 .. s0 + 31 of a class on, by all lanes of a warp.  Units come in ascending order.
+// The classes are kClasses equal ranges of lengths, the longest first, so that the CTAs end closer together.
 struct Claimed {
-  int s0, before;  // units before sequence s0
+  int all, longest;     // units, blocks of the longest one
+  int cls, s0, before;  // units before sequence s0 of the class
   __device__ bool find(const TreeArgs &a, int u, int lane, Segment &x) {
+#pragma unroll 1
     for (;; s0 += 32) {
       if (s0 >= a.num_seqs) {
+        s0 = 0;
+        ++cls;
+      }
+      if (u >= all || cls == kClasses) {
         x.s = -1;
         return false;
       }
       Seq seq;
       seq.tiles = 0;
       if (s0 + lane < a.num_seqs) seq.load(a, s0 + lane);
-      const int units = seq.tiles * kKvHeads;
+      const int units = int((long long)(longest - seq.nb) * kClasses / longest) == cls ? seq.tiles * kKvHeads : 0;
       int end = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -597,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   // Entries of sequences s0 + tid in a part; `end`: up to and with this thread.  Returns the total over all threads.
   // (The places of warp_sums are used in turn: one barrier a call.)
   int place = 0, longest = 0, units = 0;  // blocks of the longest unit; units of both parts
-  const bool many = (long long)a.num_seqs * a.max_tiles * kKvHeads >= kClaimUnits * G;
+  const bool many = (long long)a.num_seqs * a.max_tiles * kKvHeads * 4 >= kClaimQuarters * G;
   auto scan = [&](int s0, int part, long long &mine, long long &end) {
     mine = 0;
     int nb = 0, tiles = 0;
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     zero_rows<kBf16>(a, cta, G, tid);
     return;
   }
-  const bool claims = units >= kClaimUnits * G && (longest + kUnitCost) * (long long)G <= T;
+  const bool claims = units * 4LL >= kClaimQuarters * G && (longest + kUnitCost) * (long long)G <= T;
   Shares shares;
   shares.T = T;
   shares.G = Gu;
@@ -719,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   if (warp == kLoadWarpK) {
     // ================= K loader (tiled TMA); it walks the list =================
     const uint64_t once = policy_evict_first(), again = policy_evict_last();
-    Claimed claimed = {0, 0};
+    Claimed claimed = {units, longest, 0, 0, 0};
     Walk walk;
     walk.pos = pa;
     walk.end = pb;
