@@ -698,3 +698,41 @@ def test_binding_refuses_tables_and_workspaces_of_the_wrong_kind(pkv):
         c.max_context = 0x7FFFFFFF
         r.call()
     assert r.status.item() == 0
+
+
+def test_claimed_units_are_bit_exact_call_after_call(pkv):
+    # many short units: the CTAs claim them in whatever order they get free; the workspace serves other calls between
+    r = np.random.RandomState(12)
+    nodes = [int(r.randint(1, 64)) for _ in range(72)]
+    contexts = [n + int(r.randint(0, 1600)) for n in nodes]
+    c = S.TreeCase(contexts, nodes, seed=84)
+    assert sum(8 * -(-n // 32) for n in nodes) >= 2 * 304
+    ws = pkv.tree_workspace(72, 64)
+    run, other = Run(pkv, c, workspace=ws), Run(pkv, S.TreeCase([700, 30], [5, 30], seed=85), workspace=ws)
+    first, alone = run.call().result()[0], other.call().result()[0]
+    ref, err, size, spread = c.reference()
+    S.assert_within(first, ref, S.bound(ref, size, spread, c.wl.scale, max(contexts), False), "claimed units")
+    for _ in range(6):
+        run.out[:c.rows].zero_()
+        got, status = run.call().result()
+        assert status == err == 0 and np.array_equal(got, first)
+        assert np.array_equal(other.call().result()[0], alone)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_one_long_sequence_among_many_short_ones(pkv, bf16):
+    # units enough to be claimed whole, but one that is longer than a CTA's share: cut
+    r = np.random.RandomState(13)
+    contexts = [20000] + [int(r.randint(8, 200)) for _ in range(90)]
+    _check(pkv, S.TreeCase(contexts, [8] + [int(r.randint(1, 8)) for _ in range(90)], seed=86), bf16)
+
+
+def test_overlapped_calls_that_claim_units(pkv):
+    # the next call starts while the last CTAs of the one before are at work on the same counters
+    c = S.TreeCase([130 + s % 90 for s in range(80)], [1 + s % 9 for s in range(80)], seed=87)
+    r = Run(pkv, c)
+    want = r.call().result()[0]
+    for _ in range(10):
+        r.call(overlap_previous=True)
+    got, status = r.result()
+    assert status == 0 and np.array_equal(got, want)
