@@ -10,8 +10,12 @@
 // GB300 design (tcgen05 tensor cores, accumulators in tensor memory)
 //  * Unit: 32 nodes of a sequence against one K/V head g.  Its 128 rows (4 * node + head in group) share
 //    every K/V row loaded: M = 128.  Keys in blocks of 64 (4 pages).
-//  * Work split: the key blocks of all units form one list; the grid's CTAs (two per SM) take equal
-//    shares of it, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
+//  * Work split, two CTAs per SM.  In batches of many units, each at most as long as a CTA's share, the CTAs claim whole units
+//    from a counter in the workspace, one after the other: nothing is cut, and they end together.  (From 1.75
+//    units a CTA on: with 1.5 and 1.05 uniform batches of 4096 tokens took 8 and 24 % longer than with shares, with 2 to 7
+//    4 % longer to 14 % less, ragged ones 0 to 10 % less, trees of two tiles 14 to 25 % less at any number.)
+//    Otherwise the key blocks of all units form one list, of which the CTAs take equal
+//    shares, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
 //    state (r, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
 //    atomic counter, nobody waits) merges them.  (A merge takes 1.8 us with 24 rows and 3 to 5 us with 128.)
 //  * Warp roles (384 threads): 8 softmax warps, a loader of K and one of V (tiled TMA, head g's 16 rows of
@@ -23,12 +27,12 @@
 //    of O += P V.  (Two threads to a row on the same block, with S buffers for two blocks, took 1650 cycles a block
 //    against 1300.)
 //  * What bounds it, by the time a call takes: with many keys a node the K/V bytes: 256 sequences of 2048 tokens and 8
-//    nodes take 179 us, 6.1 TB/s, 90 % of a plain copy's rate.  With many short units their starts and ends: each costs
-//    as much as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 62 us, 24 for the bytes).  With 64 nodes two
-//    tiles share the bytes, and the steps from barrier to barrier count: 64 x 2048 in bf16 takes 83 us; without
-//    all of the softmax's arithmetic it would be 76, without the loads too 66, without the merges 73.  The
-//    smallest call (600 tokens, 6 nodes) takes 10.3 us: launch 2, lengths and list 1.5, tables and first K 1.7,
-//    two blocks 2.5, tickets and merge 2.6.
+//    nodes take 171 us, 6.4 TB/s, 95 % of a plain copy's rate.  With many short units their starts and ends, each
+//    as long as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 52 us, 24 for the bytes).  With 64 nodes two
+//    tiles share the bytes, and the steps from barrier to barrier count (64 x 2048 in bf16: 71 to 75 us, 45 for the
+//    bytes): leaving out all of the softmax's arithmetic took 8 % off, the loads 13 more.  The
+//    smallest call (600 tokens, 6 nodes) takes 10.6 us: launch 2, lengths and list 1.7, tables and first K 1.7,
+//    two blocks 2.5, tickets and merge 2.7.
 //  * The reference is the row's largest exponent in the segment's first block and stays: weights are floats, so
 //    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
 //    that.  A row whose sum leaves [2^-90, 2^112] is computed again from global memory by redo_row(), slowly (with every
@@ -74,7 +78,8 @@ static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax
 constexpr int kMaxCtas = 320;
 // Least list entries a CTA is given: 2, and up to 6 where the longest unit would be in more parts than one merge takes
 // (a second level of merges takes as long as 6 blocks).
-constexpr int kClaimQuarters = 7, kClasses = 2;
+constexpr int kClaimQuarters = 7;  // units are claimed whole from this many quarters of a unit a CTA on
+constexpr int kClasses = 2;        // (1, 2, 3 and 4: 57, 51.4, 52 and 53.7 us for 64 x 64..2048 tokens, 1..64 nodes)
 constexpr int kMinEntries = 2, kMostEntries = 6;
 // With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
