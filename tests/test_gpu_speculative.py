@@ -736,3 +736,58 @@ def test_overlapped_calls_that_claim_units(pkv):
         r.call(overlap_previous=True)
     got, status = r.result()
     assert status == 0 and np.array_equal(got, want)
+
+
+# ---- calls the interface allows ---------------------------------------------------------------------
+@pytest.mark.parametrize("seqs", [3, 80])
+def test_bounds_far_above_what_is_there(pkv, seqs):
+    # max_query and max_context are bounds: results do not depend on them
+    nodes, contexts = [1 + s % 7 for s in range(seqs)], [20 + 13 * (s % 11) for s in range(seqs)]
+    c = S.TreeCase(contexts, nodes, seed=88, words=32)
+    got = _check(pkv, c)
+    c.max_query, c.max_context = 1000, c.max_context * 1000
+    assert np.array_equal(Run(pkv, c).call().result()[0], got)
+
+
+def test_a_batch_without_nodes_writes_nothing(pkv):
+    c = S.TreeCase([30, 0, 17], [0, 0, 0], seed=89)
+    r = Run(pkv, c)
+    r.call()
+    torch.cuda.synchronize()
+    assert torch.isnan(r.out).all() and int(r.status.item()) == 0
+    r.c.max_query = 0
+    r.call()
+
+
+def test_faults_without_a_status_word(pkv):
+    c = S.TreeCase([10, 200, 70], [11, 20, 9], seed=90, num_pages=40)
+    c.bt[1, 3] = -1
+    want, _, size, spread = c.reference()
+    r = Run(pkv, c)
+    r.status = None
+    r.call()
+    torch.cuda.synchronize()
+    S.assert_within(r.out[:c.rows].double().cpu().numpy(), want, S.bound(want, size, spread, c.wl.scale, 200, False),
+                    "without a status word")
+
+
+def test_a_query_that_is_not_finite_stays_in_its_row(pkv):
+    c = S.TreeCase([300, 90], [20, 9], seed=91)
+    good = _check(pkv, c)
+    c.q[3, 5, 7], c.q[22, 0, 1] = 0x7FC0, 0x7F80
+    got, status = Run(pkv, c).call().result()
+    assert status == 0 and np.isnan(got[3, 5]).all() and not np.isfinite(got[22, 0]).any()
+    keep = np.ones(got.shape[:2], bool)
+    keep[3, 5] = keep[22, 0] = False
+    assert np.array_equal(got[keep], good[keep])
+
+
+def test_commit_of_nothing_and_of_everything(pkv):
+    pool, table, starts, lens, path, count = _commit_case(5, 3, 92, nodes_hi=30, width=30)
+    count[:] = 0
+    assert _commit(pkv, (pool, table, starts, lens, path, count)) == 0          # only the lengths change
+    n = np.diff(starts)
+    for s in range(5):
+        path[s, :n[s]] = np.arange(n[s])
+    assert _commit(pkv, (pool, table, starts, lens, path, n.astype(np.int32))) == 0  # every row stays
+    assert _commit(pkv, (pool, table, starts, lens, np.zeros((5, 0), np.int32), count)) == 0
