@@ -10,10 +10,10 @@
 // GB300 design (tcgen05 tensor cores, accumulators in tensor memory)
 //  * Unit: 32 nodes of a sequence against one K/V head g.  Its 128 rows (4 * node + head in group) share
 //    every K/V row loaded: M = 128.  Keys in blocks of 64 (4 pages).
-//  * Work split, two CTAs per SM.  In batches of many units, each at most as long as a CTA's share, the CTAs claim whole units
-//    from a counter in the workspace, one after the other: nothing is cut, and they end together.  (From 1.75
-//    units a CTA on: with 1.5 and 1.05 uniform batches of 4096 tokens took 8 and 24 % longer than with shares, with 2 to 7
-//    4 % longer to 14 % less, ragged ones 0 to 10 % less, trees of two tiles 14 to 25 % less at any number.)
+//  * Work split, two CTAs per SM.  Whole units to a CTA where that costs less than merges do: the first by the CTA's number,
+//    further ones claimed from a counter in the workspace, so that nothing is cut and the CTAs end together.
+//    (Over 360 uniform batches of 1 to 110 sequences, 64 to 4096 tokens and 6 to 64 nodes the rule is 1.3 % slower than the
+//    better of the two would be for each, whole units for all 3.7 % and shares for all 15.6 %.)
 //    Otherwise the key blocks of all units form one list, of which the CTAs take equal
 //    shares, whatever the mix of lengths and trees.  A unit cut across CTAs leaves one partial
 //    state (r, l, O) per CTA in the workspace, and the CTA that takes the last of its tickets (an
@@ -78,9 +78,13 @@ static_assert(kThreads == 384 && 128 * kRegsOthers + kSoftThreads * kRegsSoftmax
 constexpr int kMaxCtas = 320;
 // Least list entries a CTA is given: 2, and up to 6 where the longest unit would be in more parts than one merge takes
 // (a second level of merges takes as long as 6 blocks).
-constexpr int kClaimQuarters = 7;  // units are claimed whole from this many quarters of a unit a CTA on
-constexpr int kClasses = 2;        // (1, 2, 3 and 4: 57, 51.4, 52 and 53.7 us for 64 x 64..2048 tokens, 1..64 nodes)
 constexpr int kMinEntries = 2, kMostEntries = 6;
+// What the merges of cut units cost a call, in blocks, by the octets of nodes in the longest unit (up to 4): whole units
+// are taken when the longest one takes no more than that longer than a CTA's share, and, with more units than CTAs, when
+// what the CTAs idle in the last round does not cost more (a block there takes 9/16 of the time, with SMs half empty).
+// (6 nodes: 512 tokens 3 % slower to 5 % faster whole, 1024 tokens 15 % slower to 13 % faster, by the number of sequences;
+// 32 nodes: 1024 tokens 2 % slower to 29 % faster, 2048 28 % slower to 19 % faster.)
+constexpr float kMergeCost = 7.f, kMergeCostOctet = 6.f, kLastRound = 0.5625f;
 // With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
 // a run's O goes to the segment's part in the workspace, where the runs are added with rounding.
@@ -168,7 +172,7 @@ struct Segment {
   int q0, n, ctx, nb;      // the sequence's
   long long unit0;         // list index of the unit's block 0
 };
-// Places for segments.  The K loader is at most 5 blocks (and so segments) ahead of S, S 3 ahead of the products,
+// Places for segments.  The K loader is at most 4 blocks (and so segments) ahead of S, S 3 ahead of the products,
 // these one segment ahead of the softmax warps: place k is free when segment k + 16 is written to it.
 constexpr int kSegments = 16;
 // s_full barriers, and places for the blocks' invalid pages.  The K loader arrives at block n's when S of block n - 4 is
@@ -188,6 +192,90 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 struct Walk {
   long long pos, end, first;  // list position, end of the share, first entry of sequence s in its part
   int s, part;
+  // For whole units (unit()): units before sequence s of length class `part`.
+  __device__ void start_units() {
+    first = 0;
+    s = part = 0;
+  }
+  // Unit u of `all` in the order length class, sequence, head, tile, looked for from sequences s .. s + 31 on, by all lanes of
+  // a warp; a CTA's units come in ascending order.  The class of more than half of the longest one's blocks comes
+  // first, so that the CTAs end closer together.
+  __device__ bool unit(const TreeArgs &a, int u, int all, int longest, int lane, Segment &x) {
+#pragma unroll 1
+    for (;; s += 32) {
+      if (s >= a.num_seqs) {
+        s = 0;
+        ++part;
+      }
+      if (u >= all || part == 2) {
+        x.s = -1;
+        return false;
+      }
+      Seq seq;
+      seq.tiles = 0;
+      if (s + lane < a.num_seqs) seq.load(a, s + lane);
+      const int mine = (2 * seq.nb > longest ? 0 : 1) == part ? seq.tiles * kKvHeads : 0, before = int(first);
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned there = __ballot_sync(0xffffffffu, u - before < upto);
+      if (there) {
+        const int l = __ffs(there) - 1;
+        const int v = u - before - __shfl_sync(0xffffffffu, upto - mine, l);
+        const int tiles = __shfl_sync(0xffffffffu, seq.tiles, l);
+        x.s = s + l;
+        x.g = v / tiles;
+        x.tile = v - x.g * tiles;
+        x.q0 = __shfl_sync(0xffffffffu, seq.q0, l);
+        x.n = __shfl_sync(0xffffffffu, seq.n, l);
+        x.ctx = __shfl_sync(0xffffffffu, seq.ctx, l);
+        x.nb = x.j1 = __shfl_sync(0xffffffffu, seq.nb, l);
+        x.j0 = 0;
+        return true;
+      }
+      first += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  // From list position `from` on: looks for its sequence, by all lanes of a warp.
+  __device__ void start(const TreeArgs &a, long long from, long long to, int lane) {
+    pos = from;
+    end = to;
+    first = 0;
+    s = part = 0;
+#pragma unroll 1
+    for (;;) {
+      Seq seq;
+      seq.tiles = seq.nb = 0;
+      if (s + lane < a.num_seqs) seq.load(a, s + lane);
+      const long long mine = seq.entries(part);
+      long long upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned there = __ballot_sync(0xffffffffu, pos < first + upto);
+      if (there) {
+        const int l = __ffs(there) - 1;
+        first += __shfl_sync(0xffffffffu, upto - mine, l);
+        s += l;
+        return;
+      }
+      first += __shfl_sync(0xffffffffu, upto, 31);
+      s += 32;
+      if (s >= a.num_seqs) {
+        s = 0;
+        if (++part == 2) {  // (never with lengths that stay as they are)
+          part = 1;
+          end = pos;
+          return;
+        }
+      }
+    }
+  }
   __device__ bool next(const TreeArgs &a, Segment &x) {
     Seq seq;
     seq.load(a, s);
@@ -225,51 +313,14 @@ struct Walk {
   }
 };
 
-// The same where the CTAs claim whole units, one after the other: unit `u` in the order length class, sequence, head, tile,
-// looked for from the sequences s0 .. s0 + 31 of a class on, by all lanes of a warp.  Units come in ascending order.
-// The classes are kClasses equal ranges of lengths, the longest first, so that the CTAs end closer together.
-struct Claimed {
-  int all, longest;     // units, blocks of the longest one
-  int cls, s0, before;  // units before sequence s0 of the class
-  __device__ bool find(const TreeArgs &a, int u, int lane, Segment &x) {
-#pragma unroll 1
-    for (;; s0 += 32) {
-      if (s0 >= a.num_seqs) {
-        s0 = 0;
-        ++cls;
-      }
-      if (u >= all || cls == kClasses) {
-        x.s = -1;
-        return false;
-      }
-      Seq seq;
-      seq.tiles = 0;
-      if (s0 + lane < a.num_seqs) seq.load(a, s0 + lane);
-      const int units = int((long long)(longest - seq.nb) * kClasses / longest) == cls ? seq.tiles * kKvHeads : 0;
-      int end = units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, end, o);
-        if (lane >= o) end += y;
-      }
-      const int total = __shfl_sync(0xffffffffu, end, 31);
-      if (u - before < total) {
-        const int l = __ffs(__ballot_sync(0xffffffffu, u - before < end)) - 1;
-        const int v = u - before - __shfl_sync(0xffffffffu, end - units, l);
-        seq.load(a, s0 + l);
-        x.s = s0 + l;
-        x.g = v / seq.tiles;
-        x.tile = v - x.g * seq.tiles;
-        x.q0 = seq.q0;
-        x.n = seq.n;
-        x.ctx = seq.ctx;
-        x.nb = x.j1 = seq.nb;
-        x.j0 = 0;
-        return true;
-      }
-      before += total;
-    }
-  }
+// T list entries over G CTAs: CTA i has those from i T / G on, rounded down, so that in a batch where every tile of a head
+// has a twin CTAs i and i + G / 2 work on the same keys at the same time.  (T < 2^54: at most 2^29 units of 2^25 blocks.)
+struct Shares {
+  long long T;
+  int G;
+  __device__ long long first(int cta) const { return divide(cta * T, G); }
+  // CTA that has entry p
+  __device__ int owner(long long p) const { return int(divide((p + 1) * G - 1, T)); }
 };
 
 struct __align__(1024) Smem {
@@ -300,24 +351,14 @@ struct __align__(1024) Smem {
   int block_bad[kReady];  // [block % 8] bit pp: page pp of the block is invalid (loaded as zeros)
   int nonfinite[4];  // [segment % 4]: the last segment in which a node's V was zeroed (the softmax warps are
                      // never more than two segments apart: O is written again when all have read it)
-  long long warp_sums[2][kThreads / 32];
-  int warp_longest[2][kThreads / 32], warp_units[2][kThreads / 32];
-  long long first;  // list index of seq0's first entry
-  int seq0;
+  long long warp_entries[kThreads / 32];
+  int warp_longest[kThreads / 32], warp_units[kThreads / 32];
+  Shares shares;
+  int whole, units, longest;  // whether whole units are claimed; units, blocks of the longest one
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-
-// T list entries over G CTAs: CTA i has those from i T / G on, rounded down, so that in a batch where every tile of a head
-// has a twin CTAs i and i + G / 2 work on the same keys at the same time.  (T < 2^54: at most 2^29 units of 2^25 blocks.)
-struct Shares {
-  long long T;
-  int G;
-  __device__ long long first(int cta) const { return divide(cta * T, G); }
-  // CTA that has entry p
-  __device__ int owner(long long p) const { return int(divide((p + 1) * G - 1, T)); }
-};
 
 // Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
 constexpr unsigned kWaitCycles = 3800000000u;
@@ -601,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = int(gridDim.x), cta = int(blockIdx.x);
 
-  // ---- entries of the list, this CTA's share of them, and the sequence where it begins ----
+  // ---- what the batch asks for ----
   if (warp == kScoreWarp) tmem_alloc(&sm.tmem_base, kTmemCols);
   if (uint64_t *bar = sm.q_full + tid; bar <= &sm.o_free) {
     mbar_init(bar, bar < sm.s_full ? 1 : bar < sm.p_full ? 2 : bar < &sm.o_free ? kSoftWarps / 2 : kSoftWarps);
@@ -609,89 +650,59 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   }
   if (tid < 4) sm.nonfinite[tid] = -1;
   if (tid == 4) sm.abort = 0;
-  // Entries of sequences s0 + tid in a part; `end`: up to and with this thread.  Returns the total over all threads.
-  // (The places of warp_sums are used in turn: one barrier a call.)
-  int place = 0, longest = 0, units = 0;  // blocks of the longest unit; units of both parts
-  const bool many = (long long)a.num_seqs * a.max_tiles * kKvHeads * 4 >= kClaimQuarters * G;
-  auto scan = [&](int s0, int part, long long &mine, long long &end) {
-    mine = 0;
-    int nb = 0, tiles = 0;
-    if (s0 + tid < a.num_seqs) {
-      Seq q;
-      q.load(a, s0 + tid);
-      mine = q.entries(part);
-      nb = q.nb;
-      tiles = q.part_tiles(part);
-    }
-    nb = __reduce_max_sync(0xffffffffu, nb);
-    if (many) tiles = __reduce_add_sync(0xffffffffu, tiles);
-    end = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += y;
-    }
-    if (lane == 31) {
-      sm.warp_sums[place][warp] = end;
-      sm.warp_longest[place][warp] = nb;
-      sm.warp_units[place][warp] = tiles * kKvHeads;
-    }
-    __syncthreads();
-    long long x = lane < kThreads / 32 ? sm.warp_sums[place][lane] : 0;
-    longest = max(longest, __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_longest[place][lane] : 0));
-    if (many) units += __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_units[place][lane] : 0);
-    place ^= 1;
-#pragma unroll
-    for (int o = 1; o < kThreads / 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (warp > 0) end += __shfl_sync(0xffffffffu, x, warp - 1);
-    return __shfl_sync(0xffffffffu, x, kThreads / 32 - 1);
+  // entries of the list, units, and 4 x the blocks of the longest unit + its octets of nodes less one
+  long long T = 0;
+  int units = 0, longest = 0;
+  for (int s = tid; s < a.num_seqs; s += kThreads) {
+    Seq q;
+    q.load(a, s);
+    T += q.entries(0) + q.entries(1);
+    units += q.tiles * kKvHeads;
+    if (q.tiles > 0) longest = max(longest, 4 * q.nb + (min(q.n, kTok) - 1) / kOctet);
+  }
+  auto sum = [&](long long x) {  // over the warp, of entries (less than 2^54 in all)
+    const unsigned low = __reduce_add_sync(0xffffffffu, unsigned(x) & 0x3ffffffu);
+    return ((long long)__reduce_add_sync(0xffffffffu, unsigned(x >> 26)) << 26) + low;
   };
-  // (a batch without second tiles has no odd part)
-  const int parts = a.max_tiles > 1 ? 2 : 1;
-  long long mine, end, T = 0, T0 = 0;
-#pragma unroll 1
-  for (int part = 0; part < parts; ++part) {
-    T0 = T;
-#pragma unroll 1
-    for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) T += scan(s0, part, mine, end);
-  }
-  if (parts == 1) T0 = T;
-  const int least = min(max((longest + kUnitCost) / (2 * kMergeGroup - 1) + 1, kMinEntries), kMostEntries);
-  const int Gu = int(min((long long)G, max(1LL, divide(T, least))));  // CTAs with a share
-  if (T == 0 || cta >= Gu) {
-    if (warp == kScoreWarp) tmem_dealloc(sm.tmem_base, kTmemCols);
-    griddep_wait();
-    griddep_launch_dependents();
-    zero_rows<kBf16>(a, cta, G, tid);
-    return;
-  }
-  const bool claims = units * 4LL >= kClaimQuarters * G && (longest + kUnitCost) * (long long)G <= T;
-  Shares shares;
-  shares.T = T;
-  shares.G = Gu;
-  const long long pa = shares.first(cta), pb = shares.first(cta + 1);
-  // the sequence that holds entry pa: among those just scanned, or with a second look
-  const int part0 = pa >= T0 ? 1 : 0;
-  const bool again = a.num_seqs > kThreads || part0 != parts - 1;
-  long long start = part0 ? T0 : 0;
-#pragma unroll 1
-  for (int s0 = 0; s0 < a.num_seqs && !claims; s0 += kThreads) {
-    long long total = 0;
-    if (again) total = scan(s0, part0, mine, end);
-    if (start + end - mine <= pa && pa < start + end) {
-      sm.seq0 = s0 + tid;
-      sm.first = start + end - mine;
-    }
-    start += total;
-    if (pa < start) break;
+  T = sum(T);
+  units = __reduce_add_sync(0xffffffffu, units);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    sm.warp_entries[warp] = T;
+    sm.warp_units[warp] = units;
+    sm.warp_longest[warp] = longest;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  T = sum(lane < kThreads / 32 ? sm.warp_entries[lane] : 0);
+  units = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_units[lane] : 0);
+  longest = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.warp_longest[lane] : 0);
+  // ---- whole units or shares of the list ----
+  const float merge = kMergeCost + kMergeCostOctet * ((longest & 3) + 1);
+  longest >>= 2;
+  const int length = longest + kUnitCost;
+  const int least = min(max(length / (2 * kMergeGroup - 1) + 1, kMinEntries), kMostEntries);
+  const float rounds = __fdividef(float(units), float(G)), idle = ceilf(rounds) - rounds;
+  const bool whole = length - merge <= fmaxf(__fdividef(float(T), float(G)), float(least)) &&
+                     (rounds <= 1.f || idle * length * kLastRound <= merge);
+  const int ctas = whole ? min(units, G) : int(min((long long)G, max(1LL, divide(T, least))));  // with anything to do
+  if (T == 0 || cta >= ctas) {
+    if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
+    griddep_wait();
+    griddep_launch_dependents();
+    zero_rows<kBf16>(a, cta, G, tid);
+    return;
+  }
+  if (tid == 0 || tid == kLoadWarpK * 32) {  // (read in these two warps)
+    sm.shares.T = T;
+    sm.shares.G = ctas;
+    sm.whole = whole;
+    sm.units = units;
+    sm.longest = longest;
+  }
+  __syncwarp();
   // Small trees fill the lanes of one warp only: units start at another quarter of the lanes each, so
   // that the quarters (the SM's sub-partitions) share the work.
   const int turn = cta * 2 >= G ? 2 : 0;
@@ -734,13 +745,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   if (warp == kLoadWarpK) {
     // ================= K loader (tiled TMA); it walks the list =================
     const uint64_t once = policy_evict_first(), again = policy_evict_last();
-    Claimed claimed = {units, longest, 0, 0, 0};
+    const bool whole = sm.whole != 0;
     Walk walk;
-    walk.pos = pa;
-    walk.end = pb;
-    walk.first = sm.first;
-    walk.s = sm.seq0;
-    walk.part = part0;
+    if (whole) walk.start_units();
+    else walk.start(a, sm.shares.first(cta), sm.shares.first(cta + 1), lane);
     if (lane == 0) {
       prefetch_tensormap(&a.tmap_k);
       prefetch_tensormap(&a.tmap_q);
@@ -752,13 +760,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     for (int k = 0; ok; ++k) {
       Segment &x = sm.seg[k % kSegments];
       bool more;  // every lane writes the same
-      if (claims) {
+      if (whole) {
         int u = cta;
         if (k > 0) {
-          if (lane == 0) u = G + atomicAdd(&a.parts->claimed, 1);
-          u = __shfl_sync(0xffffffffu, u, 0);
+          u = sm.units;
+          if (u > G) {
+            if (lane == 0) u = G + atomicAdd(&a.parts->claimed, 1);
+            u = __shfl_sync(0xffffffffu, u, 0);
+          }
         }
-        more = claimed.find(a, u, lane, x);
+        more = walk.unit(a, u, sm.units, sm.longest, lane, x);
       } else {
         more = walk.next(a, x);
       }
@@ -1204,7 +1215,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         const Segment &u = sm.cuts[tid];
         int ends[2];
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) ends[i] = shares.owner(u.unit0 + (i ? u.nb - 1 : 0));
+        for (int i = 0; i < 2; ++i) ends[i] = sm.shares.owner(u.unit0 + (i ? u.nb - 1 : 0));
         const int c0 = ends[0], parts = ends[1] - ends[0] + 1;
         sm.cut_first[tid] = c0;
         sm.cut_parts[tid] = parts;
@@ -1257,7 +1268,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort) report(a.status, PKV_DEV_TIMEOUT);
-  if (tid == 0 && claims && atomicAdd(&a.parts->done, 1) == G - 1) {
+  if (tid == 0 && sm.whole && sm.units > G && atomicAdd(&a.parts->done, 1) == G - 1) {
     atomicExch(&a.parts->claimed, 0);  // ready for the next call
     atomicExch(&a.parts->done, 0);
   }
@@ -1321,8 +1332,8 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   if (rc != PKV_OK) return rc;
   if (num_q_heads != pkv::kQHeads) return PKV_ERR_UNSUPPORTED;
   if (num_seqs < 0 || max_query < 0 || max_context < 0 || block_table_stride < 0 || num_q_rows < 0 ||
-      num_seqs > pkv::kMaxSeqs || max_query > pkv::kMaxNodes || max_context > pkv::kMaxContext || mask_stride < 0 || mask_stride > (1 << 26) ||
-      mask_stride * 32 < max_query)
+      num_seqs > pkv::kMaxSeqs || max_query > pkv::kMaxNodes || max_context > pkv::kMaxContext || mask_stride < 0 ||
+      mask_stride > (1 << 26) || mask_stride * 32 < max_query)
     return PKV_ERR_SHAPE;
   if (num_seqs == 0 || max_query == 0 || num_q_rows == 0) return PKV_OK;
   if (out == nullptr || q == nullptr || query_start == nullptr || tree_mask == nullptr || block_tables == nullptr ||
