@@ -27,9 +27,9 @@
 //    of O += P V.  (Two threads to a row on the same block, with S buffers for two blocks, took 1650 cycles a block
 //    against 1300.)
 //  * What bounds it, by the time a call takes: with many keys a node the K/V bytes: 256 sequences of 2048 tokens and 8
-//    nodes take 171 us, 6.4 TB/s, 95 % of a plain copy's rate.  With many short units their starts and ends, each
-//    as long as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 52 us, 24 for the bytes).  With 64 nodes two
-//    tiles share the bytes, and the steps from barrier to barrier count (64 x 2048 in bf16: 71 to 75 us, 45 for the
+//    nodes take 170 us, 6.5 TB/s, 96 % of a plain copy's rate.  With many short units their starts and ends, each
+//    as long as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 51 us, 24 for the bytes).  With 64 nodes two
+//    tiles share the bytes, and the steps from barrier to barrier count (64 x 2048 in bf16: 70 us, 45 for the
 //    bytes): leaving out all of the softmax's arithmetic took 8 % off, the loads 13 more.  The
 //    smallest call (600 tokens, 6 nodes) takes 10.6 us: launch 2, lengths and list 1.7, tables and first K 1.7,
 //    two blocks 2.5, tickets and merge 2.7.
