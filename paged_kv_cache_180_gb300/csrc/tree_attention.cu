@@ -37,8 +37,9 @@
 //    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
 //    that.  A row whose sum leaves [2^-90, 2^112] is computed again from global memory by redo_row(), slowly (with every
 //    row of 64 x 2048 tokens and 32 nodes computed again a call takes 15.1 ms instead of 0.08).
-//  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits; two
-//    products); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
+//  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits, two products: an error of
+//    2.4e-6 of the output; a third term with two S buffers and runs of 4 blocks would give 0.9e-6 and take 30 to 45 %
+//    longer); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
 //    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
 //  * Masks: the score of a key a row may not see is replaced by an infinity, so a NaN score stays out.  V rows at or
 //    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
