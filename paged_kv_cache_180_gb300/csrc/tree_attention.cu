@@ -31,8 +31,8 @@
 //    as long as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 51 us, 24 for the bytes).  With 64 nodes two
 //    tiles share the bytes, and the steps from barrier to barrier count (64 x 2048 in bf16: 70 us, 45 for the
 //    bytes): leaving out all of the softmax's arithmetic took 8 % off, the loads 13 more.  The
-//    smallest call (600 tokens, 6 nodes) takes 10.6 us: launch 2, lengths and list 1.7, tables and first K 1.7,
-//    two blocks 2.5, tickets and merge 2.7.
+//    smallest call (600 tokens, 6 nodes) takes 10.6 us: launch 2, lengths 1.5, tables and first K 1.9, ten blocks
+//    4.5, the end 0.7.
 //  * The reference is the row's largest exponent in the segment's first block and stays: weights are floats, so
 //    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
 //    that.  A row whose sum leaves [2^-90, 2^112] is computed again from global memory by redo_row(), slowly (with every
