@@ -724,7 +724,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       next = x.j0 * kPagesPerBlock;
       ent = entry(next + lane);
       ent_next = entry(next + 32 + lane);
-      check(next + lane, a.num_pages);
     }
     // Pages of the segment's block number i (in order), -1 for what is not in the pool: TMA fills these with zeros.
     // Returns the bits of those inside the context.
@@ -777,6 +776,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.seg_full[k % kSegments]);
       if (!more) break;
+      Pages pages;
+      pages.start(a, x, lane);
       // Q: boxes of 8 nodes x 4 heads, once the segment before the last has read its own
       if (k >= 2) {
         const bool w = wait(sm, &sm.q_empty[k & 1], uint32_t(k / 2 - 1) & 1);
@@ -794,10 +795,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       ++loads;
       // launched with overlap (PKV_OVERLAP_PREVIOUS), the kernel before this one may still be writing
       // the pool: it is read only once that kernel has completed
-      Pages pages;
-      pages.start(a, x, lane);
       if (!waited) griddep_wait();
       waited = true;
+      pages.check(pages.next + lane, a.num_pages);
       const uint64_t policy = x.n > kTok ? again : once;  // several tiles read the same K/V
       const int j0 = x.j0, j1 = x.j1, y = x.g * kPageTokens;
 #pragma unroll 1
@@ -850,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       pages.start(a, x, lane);
       if (!waited) griddep_wait();
       waited = true;
+      pages.check(pages.next + lane, a.num_pages);
       const uint64_t policy = x.n > kTok ? again : once;
       const int j0 = x.j0, j1 = x.j1, y = x.g * kPageTokens;
 #pragma unroll 1
