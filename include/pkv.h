@@ -386,7 +386,7 @@ int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const void *q, int
                              size_t workspace_bytes, int32_t *device_status, unsigned flags, void *stream);
 
 /* Workspace bytes of pkv_paged_tree_attention for up to num_seqs sequences of up to max_query nodes
- * (partial softmax states of the split and ticket counters).  0 on bad arguments. */
+ * (partial softmax states of the split, counters of tickets and of claimed units).  0 on bad arguments. */
 size_t pkv_tree_workspace_bytes(int num_seqs, int max_query, int num_q_heads, int head_dim);
 
 /*

@@ -597,8 +597,8 @@ def test_segments_of_several_runs(pkv):
     c = S.TreeCase([3000, 2990, 2500, 3000] * 10, [2, 8, 1, 3] * 10, seed=76)
     got = _check(pkv, c)
     ref, _, size, _ = c.reference()
-    # weights in two bf16 terms (2^-18), 16 truncating blocks a run (16 * 1.4e-7 = 2^-18.8), 3 runs and the scores in fp32 (of
-    # exponents below 2^4: 2^-19): below 2^-16 of the size of the values
+    # weights in two bf16 terms (2^-18), 16 truncating blocks a run (16 * 1.4e-7 = 2^-18.8), 3 runs and the scores in fp32
+    # (of exponents below 2^4: 2^-19): below 2^-16 of the size of the values
     assert (np.abs(got - ref) <= size * 2.0 ** -16).all()
 
 
