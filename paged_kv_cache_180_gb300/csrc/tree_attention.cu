@@ -997,37 +997,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const bool active = octet * kOctet < x.n - x.tile * kTok;
       const int node = x.tile * kTok + octet * kOctet + (lane >> 2), t = turns - 1;
       const bool real = node < x.n;
+      // the segment's part; between runs it holds their sum, each thread its own row and dims
+      Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
+      const int at = octet * 32 + lane;
+      float r[32];
+#pragma unroll
+      for (int d = 0; d < 32; ++d) r[d] = 0.f;
+      // The sum of the runs before is read before o_free is arrived at: the next segment's rows have other threads, which
+      // write the same part, and what orders their stores behind these loads is o_free, a product and o_full.
+      if constexpr (!kBf16) {
+        if (active && ended > first) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = __ldcg(&part.o[half * 8 + i][at]);
+            r[4 * i] = y.x;
+            r[4 * i + 1] = y.y;
+            r[4 * i + 2] = y.z;
+            r[4 * i + 3] = y.w;
+          }
+        }
+      }
       bool w = wait(sm, &sm.o_full, ended & 1);
       ++ended;
       if (active && last) w = wait(sm, &sm.sums_full[quarter], uint32_t(t) & 1) && w;
       if (!__all_sync(0xffffffffu, w)) return false;
-      uint32_t u[32];
       if (active) {
+        uint32_t u[32];
         tc_fence_after();
         tmem_ld32(my_tmem + kColO + half * 32, u);
         tc_fence_before();
+#pragma unroll
+        for (int d = 0; d < 32; ++d) r[d] += __uint_as_float(u[d]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free);
       if (!active) return true;
-      float r[32];
-#pragma unroll
-      for (int d = 0; d < 32; ++d) r[d] = __uint_as_float(u[d]);
-      // the segment's part; between runs it holds their sum, each thread its own row and dims
-      Part &part = a.parts[2 * cta + (x.j0 == 0 ? 1 : 0)];
-      const int at = octet * 32 + lane;
-      if constexpr (!kBf16) {
-        if (ended - 1 > first) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = __ldcg(&part.o[half * 8 + i][at]);
-            r[4 * i] += y.x;
-            r[4 * i + 1] += y.y;
-            r[4 * i + 2] += y.z;
-            r[4 * i + 3] += y.w;
-          }
-        }
-      }
       auto store_part = [&]() {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
