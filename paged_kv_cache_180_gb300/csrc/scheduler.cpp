@@ -41,14 +41,22 @@ struct pkv_alloc {
   int clamp_new(int prompt, int new_tokens) const { return std::min(new_tokens, max_context + 1 - prompt); }
   int32_t *row(int seq, int layer) { return &block_tables[(size_t(seq) * num_layers + layer) * max_blocks]; }
 
-  // Reserves the credits of a request for `seq`.
-  int admit(int seq, int prompt, int new_tokens, int32_t *credits_out) {
+  // Whether a request may be admitted into `seq` now, and its credits; changes nothing.
+  int may_admit(int seq, int prompt, int new_tokens, int *credits) const {
     if (seq < 0 || seq >= max_seqs || prompt < 1 || prompt > max_context || new_tokens < 1) return PKV_ERR_SHAPE;
     if (admitted[seq]) return PKV_ERR_STATE;
-    const int credits = credits_for(prompt, clamp_new(prompt, new_tokens));
-    if (credits_out != nullptr) *credits_out = credits;
-    if (credits > num_pages) return PKV_ERR_EXCEEDS_POOL;
-    if (credits_used + credits > num_pages) return PKV_ERR_NO_CREDIT;
+    *credits = credits_for(prompt, clamp_new(prompt, new_tokens));
+    if (*credits > num_pages) return PKV_ERR_EXCEEDS_POOL;
+    if (credits_used + *credits > num_pages) return PKV_ERR_NO_CREDIT;
+    return PKV_OK;
+  }
+
+  // Reserves the credits of a request for `seq`.
+  int admit(int seq, int prompt, int new_tokens, int32_t *credits_out) {
+    int credits = -1;
+    const int rc = may_admit(seq, prompt, new_tokens, &credits);
+    if (credits_out != nullptr && credits >= 0) *credits_out = credits;
+    if (rc != PKV_OK) return rc;
     admitted[seq] = 1;
     seq_credits[seq] = credits;
     credits_used += credits;
@@ -114,6 +122,10 @@ struct pkv_alloc {
         new_tokens < 1 || capacity < 0)
       return PKV_ERR_SHAPE;
     if (!admitted[src] || admitted[dst]) return PKV_ERR_STATE;
+    // Credits first: whoever stays within them has a free page for all that this takes, so in a full pool the
+    // answer is theirs.
+    int credits;
+    if (const int rc = may_admit(dst, tokens, new_tokens, &credits); rc != PKV_OK) return rc;
     const int full = tokens / page_tokens;
     const bool partial = tokens % page_tokens != 0;
     int need = 0;
@@ -122,8 +134,7 @@ struct pkv_alloc {
     if (need > capacity) return PKV_ERR_SHAPE;
     if (need > 0 && (copy_src == nullptr || copy_dst == nullptr)) return PKV_ERR_NULL;
     if (size_t(need) > free_list.size()) return PKV_ERR_NO_PAGE;
-    const int rc = admit(dst, tokens, new_tokens, nullptr);
-    if (rc != PKV_OK) return rc;
+    admit(dst, tokens, new_tokens, nullptr);
     int k = 0;
     for (int l = 0; l < num_layers; ++l) {
       const int32_t *from = row(src, l);
