@@ -171,18 +171,19 @@ struct pkv_alloc {
     *num_copies = moves;
     if (moves > capacity) return PKV_ERR_SHAPE;
     if (moves > 0 && (copy_src == nullptr || copy_dst == nullptr)) return PKV_ERR_NULL;
-    std::vector<int32_t> moved(num_pages, -1);  // new id of a moved page
+    // (No memory is asked for: until the tables are updated the count of a moved page holds -1 - its new id.)
     int hole = 0, k = 0;
     for (int p = assigned; p < num_pages; ++p) {
       if (refs[p] == 0) continue;
       while (refs[hole] > 0) ++hole;
       copy_src[k] = p;
-      copy_dst[k++] = moved[p] = hole;
+      copy_dst[k++] = hole;
       refs[hole] = refs[p];
-      refs[p] = 0;
+      refs[p] = -1 - hole;
     }
     for (int32_t &e : block_tables)
-      if (e >= 0 && moved[e] >= 0) e = moved[e];
+      if (e >= 0 && refs[e] < 0) e = -1 - refs[e];
+    for (int p = assigned; p < num_pages; ++p) refs[p] = 0;
     free_list.clear();
     for (int p = num_pages - 1; p >= assigned; --p) free_list.push_back(p);
     return PKV_OK;
@@ -317,11 +318,7 @@ extern "C" int pkv_alloc_compact(pkv_alloc *alloc, int32_t *copy_src, int32_t *c
                                  int32_t *num_copies) {
   if (alloc == nullptr || num_copies == nullptr) return PKV_ERR_NULL;
   *num_copies = 0;
-  try {
-    return alloc->compact(copy_src, copy_dst, capacity, num_copies);
-  } catch (const std::bad_alloc &) {  // the list of moved ids, before anything has changed
-    return PKV_ERR_SHAPE;
-  }
+  return alloc->compact(copy_src, copy_dst, capacity, num_copies);
 }
 
 extern "C" int pkv_alloc_page_refs(const pkv_alloc *alloc, int page) {
