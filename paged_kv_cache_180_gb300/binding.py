@@ -296,6 +296,15 @@ def _refuse(where: str, t: torch.Tensor, dtype) -> None:
                      f"{t.dtype} on {t.device} with strides {tuple(t.stride())}")
 
 
+def _status_ptr(where: str, status: torch.Tensor | None, dev: int) -> int | None:
+    if status is None:
+        return None
+    if (status.dtype is not _I32 and status.dtype is not torch.uint32) or status.get_device() != dev or status.numel() < 1:
+        raise ValueError(f"{where}: status is an int32 word on the current device (cuda:{dev}), got {status.numel()} of "
+                         f"{status.dtype} on {status.device}")
+    return status.data_ptr()
+
+
 def tree_workspace_bytes(num_seqs: int, max_query: int, num_q_heads: int = 32, head_dim: int = 64) -> int:
     return int(_lib.pkv_tree_workspace_bytes(num_seqs, max_query, num_q_heads, head_dim))
 
@@ -337,7 +346,7 @@ def paged_tree_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Ten
         ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), shape[1],
         min(shape[0], out_shape[0], mask_shape[0]), query_start.data_ptr(), tree_mask.data_ptr(), mask_shape[1],
         block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_query, max_context, scale,
-        workspace.data_ptr(), workspace.nbytes, None if status is None else status.data_ptr(), flags, _stream(stream))
+        workspace.data_ptr(), workspace.nbytes, _status_ptr(where, status, dev), flags, _stream(stream))
     if rc:
         raise PkvError(where, rc)
 
@@ -372,8 +381,7 @@ def tree_commit(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_
     rc = _lib.pkv_tree_commit(
         ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), block_tables.data_ptr(), block_table_stride,
         layer_stride, num_layers, query_start.data_ptr(), context_lens.data_ptr(), accepted.data_ptr(), width,
-        accept_counts.data_ptr(), num_seqs, width, max_context, new, None if status is None else status.data_ptr(),
-        _stream(stream))
+        accept_counts.data_ptr(), num_seqs, width, max_context, new, _status_ptr(where, status, dev), _stream(stream))
     if rc:
         raise PkvError(where, rc)
 
@@ -390,8 +398,7 @@ def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: to
             raise ValueError(f"{where}: page ids on {t.device}; they lie on the current device (cuda:{dev}) or in pinned "
                              "host memory")
     rc = _lib.pkv_kv_copy_pages(ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), src_pages.data_ptr(),
-                                dst_pages.data_ptr(), n, None if status is None else status.data_ptr(),
-                                _stream(stream))
+                                dst_pages.data_ptr(), n, _status_ptr(where, status, dev), _stream(stream))
     if rc:
         raise PkvError(where, rc)
 
