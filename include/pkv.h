@@ -58,7 +58,7 @@ extern "C" {
 #define PKV_ERR_SHAPE (-2)         /* a size or count is out of range */
 #define PKV_ERR_UNSUPPORTED (-3)   /* geometry this build does not compile */
 #define PKV_ERR_ALIGN (-4)         /* pointer or stride not 16-byte aligned */
-#define PKV_ERR_SCALE (-5)         /* scale is not finite */
+#define PKV_ERR_SCALE (-5)         /* scale is not finite (tree attention: nor is scale * log2(e)) */
 #define PKV_ERR_WORKSPACE (-6)     /* workspace smaller than pkv_decode_workspace_bytes() */
 #define PKV_ERR_LAUNCH (-7)        /* the CUDA runtime refused a kernel launch */
 #define PKV_ERR_CUDA (-8)          /* another CUDA runtime call failed */
@@ -357,7 +357,9 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
  *   mask_stride    words between rows, 32 * mask_stride >= max_query.
  *   block_tables, block_table_stride, context_lens, max_context: as for decode.
  *   max_query      host bound on every n_s, at most 2^20 (num_seqs at most 2^24, max_context at most 2^31 - 64).
- *   scale          any finite value, negative ones and 0 (a plain average) included.
+ *   scale          any value of at most 2.3e38 in size (scale * log2(e) has to be finite, PKV_ERR_SCALE if not),
+ *                  negative ones and 0 (a plain average) included.  A score whose product with scale * log2(e)
+ *                  leaves fp32 counts as the infinity it becomes.
  *   workspace      device, >= pkv_tree_workspace_bytes(num_seqs, max_query, ...), 16-byte aligned,
  *                  zero-filled before its first use; every completed call leaves it ready for the
  *                  next, of any shape whose size it covers.  Calls sharing a workspace must not

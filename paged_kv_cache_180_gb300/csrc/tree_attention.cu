@@ -1345,7 +1345,7 @@ extern "C" int pkv_paged_tree_attention(const pkv_pool *pool, void *out, const v
   if (out == nullptr || q == nullptr || query_start == nullptr || tree_mask == nullptr || block_tables == nullptr ||
       context_lens == nullptr || workspace == nullptr)
     return PKV_ERR_NULL;
-  if (!isfinite(scale)) return PKV_ERR_SCALE;
+  if (!isfinite(scale * pkv::kLog2e)) return PKV_ERR_SCALE;  // the exponents' factor: infinite, a score of 0 were a NaN
   if (!pkv::aligned16(q) || !pkv::aligned16(out) || !pkv::aligned16(workspace) ||
       ((reinterpret_cast<uintptr_t>(query_start) | reinterpret_cast<uintptr_t>(tree_mask) |
         reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u))
