@@ -90,6 +90,10 @@ constexpr float kMergeCost = 7.f, kMergeCostOctet = 6.f, kLastRound = 0.5625f;
 // which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
 // a run's O goes to the segment's part in the workspace, where the runs are added with rounding.
 constexpr int kRunBlocks = 16;
+// Row sums are added up in three levels: over a block's keys, over the blocks of a run (with bf16 output of this many
+// blocks), over the runs.  Nearly equal weights, whose additions all round the same way, then cost at most (20 + half the
+// runs) 2^-24 of the sum.  (One sum over all keys was off by up to 8e-5 at 28000 equal ones; the levels take 0 to 1 % of a call.)
+constexpr int kSumBlocks = 64;
 constexpr int kUnitCost = 5;                        // what a unit's start and end weigh in the list, in blocks (4, 6 and 7
                                                     // were 0 to 2 % slower or faster, each on some batches)
 constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
@@ -329,7 +333,7 @@ struct __align__(1024) Smem {
   uint8_t k[kStagesK][kTileBytes];
   uint8_t v[kStagesV][kTileBytes];
   float ref[4][kRows];       // [turn]: a row's reference, from the group with the segment's first block
-  float sums[4][2][kRows];   // [turn][group]: a row's sum
+  float sums[4][2][kRows];   // [turn][group]: a row's sum, of the runs so far until it is posted
   // barriers of one arrival ...
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kStagesK], v_full[kStagesV];
@@ -411,7 +415,8 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[16], float2 c, float
 // The weights of a row's 64 keys, from S to P in place: of each 16 keys, hi in the first 8 columns, lo in the others.
 // (Loading the next 16 scores ahead changed nothing: other warps fill the time.)
 template <bool kBf16>
-__device__ __forceinline__ void block_weights(uint32_t taddr, float2 c, float2 minus_r, float2 &sum) {
+__device__ __forceinline__ void block_weights(uint32_t taddr, float2 c, float2 minus_r, float2 &total) {
+  float2 sum = make_float2(0.f, 0.f);  // of the block alone: few additions to a number of a few blocks' size
 #pragma unroll 1
   for (int i = 0; i < 4; ++i, taddr += 16) {
     uint32_t x[16], hi[8], lo[8];
@@ -421,6 +426,7 @@ __device__ __forceinline__ void block_weights(uint32_t taddr, float2 c, float2 m
     tmem_st8_async(taddr, hi);
     if constexpr (!kBf16) tmem_st8_async(taddr + 8, lo);
   }
+  total = add_f32x2(total, sum);
   tmem_st_wait();
 }
 
@@ -1091,9 +1097,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       if (real && j1 * kKeys > base)  // the mask word of the segment's first node key, needed at its end
         prefetch_l1(a.mask + (long long)(x.q0 + node) * a.mask_stride + (max(j0 * kKeys - base, 0) >> 5));
       const bool leads = int(gb0 & 1) == half;  // the segment's first block is this group's
-      float2 l2 = make_float2(0.f, 0.f), minus_r = l2;
+      float2 l2 = make_float2(0.f, 0.f), minus_r = l2;  // sum of the blocks since keep_sum(), - reference, both twice
+      if (active) sm.sums[turns & 3][half][row] = 0.f;
+      auto keep_sum = [&]() {
+        sm.sums[turns & 3][half][row] += l2.x + l2.y;
+        l2 = make_float2(0.f, 0.f);
+      };
       const int last_run = kBf16 || !more ? 0 : (j1 - j0 - 1) / kRunBlocks;
-      // Blocks before `plain_end` hold no nodes, no run ends at them and the reference is there.
+      // Blocks before `plain_end` hold no nodes, no run (or stretch of sums) ends at them and the reference is there.
       int plain_end = 0;
 #pragma unroll 1
       for (int j = j0 + (leads ? 0 : 1);; j += 2) {
@@ -1144,6 +1155,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
             ok = __all_sync(0xffffffffu, w);
             if (!ok) break;
             if (active) {
+              keep_sum();
               tc_fence_after();
               const int bad = sm.block_bad[gb % kReady];
               const bool masked = key0 + kKeys > base || bad != 0;  // uniform over the warp
@@ -1181,7 +1193,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
             ok = end_run(last ? k - 1 : k, last ? before : runs, last);
           }
           plain_end = min(j1, base / kKeys);
-          if constexpr (!kBf16) plain_end = min(plain_end, j0 + ((j - j0) / kRunBlocks + 1) * kRunBlocks);
+          constexpr int kNext = kBf16 ? kSumBlocks : kRunBlocks;
+          plain_end = min(plain_end, j0 + ((j - j0) / kNext + 1) * kNext);
         }
         __syncwarp();
         if (!has) break;
@@ -1198,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         if (tid == 0) sm.cuts[i] = x;
       }
       if (active) {
-        sm.sums[turns & 3][half][row] = l2.x + l2.y;
+        keep_sum();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.sums_full[quarter]);
         ++turns;
