@@ -86,14 +86,15 @@ constexpr int kMinEntries = 2, kMostEntries = 6;
 // (6 nodes: 512 tokens 3 % slower to 5 % faster whole, 1024 tokens 15 % slower to 13 % faster, by the number of sequences;
 // 32 nodes: 1024 tokens 2 % slower to 29 % faster, 2048 28 % slower to 19 % faster.)
 constexpr float kMergeCost = 7.f, kMergeCostOctet = 6.f, kLastRound = 0.5625f;
-// With fp32 output a segment's products are added up in runs of this many blocks: every MMA truncates the accumulator,
-// which costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one run), so
-// a run's O goes to the segment's part in the workspace, where the runs are added with rounding.
-constexpr int kRunBlocks = 16;
-// Row sums are added up in three levels: over a block's keys, over the blocks of a run (with bf16 output of this many
-// blocks), over the runs.  Nearly equal weights, whose additions all round the same way, then cost at most (20 + half the
-// runs) 2^-24 of the sum.  (One sum over all keys was off by up to 8e-5 at 28000 equal ones; the levels take 0 to 1 % of a call.)
-constexpr int kSumBlocks = 64;
+// A segment's products are added up in runs of this many blocks: every MMA truncates the accumulator, which with fp32
+// output (eight MMAs a block) costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one
+// run), with bf16 output (four) half of that, and more where all products have one sign: 15 % over 2^24 keys.  So a run's O
+// goes to the segment's part in the workspace, where the runs are added with rounding.
+template <bool kBf16>
+constexpr int kRunBlocks = kBf16 ? 256 : 16;
+// Row sums are added up in three levels: over a block's keys, over a run's blocks, over the runs.  Nearly equal weights, whose
+// additions all round the same way, then cost at most (16 + a run's blocks / 4 + the runs / 2) 2^-24 of the sum.  (One sum over all
+// keys was off by up to 8e-5 at 28000 equal ones; the levels take 0 to 1 % of a call.)
 constexpr int kUnitCost = 5;                        // what a unit's start and end weigh in the list, in blocks (4, 6 and 7
                                                     // were 0 to 2 % slower or faster, each on some batches)
 constexpr int kBox = kPageTokens * kRowBytes;       // one head's rows of one page: 2 KiB
@@ -948,8 +949,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       const int blocks = x.j1 - x.j0;
 #pragma unroll 1
       for (int j = 0; j < blocks; ++j, ++gb) {
-        const int in_run = kBf16 ? j : j % kRunBlocks;
-        const bool run_ends = j == blocks - 1 || (!kBf16 && in_run == kRunBlocks - 1);
+        const int in_run = j % kRunBlocks<kBf16>;
+        const bool run_ends = j == blocks - 1 || in_run == kRunBlocks<kBf16> - 1;
         const int st = int(gb % kStagesV), b = int(gb % kScores);
         w = wait(sm, &sm.v_full[st], (gb / kStagesV) & 1) &&
             wait(sm, &sm.p_full[b], (gb / kScores) & 1);
@@ -1011,16 +1012,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
       for (int d = 0; d < 32; ++d) r[d] = 0.f;
       // The sum of the runs before is read before o_free is arrived at: the next segment's rows have other threads, which
       // write the same part, and what orders their stores behind these loads is o_free, a product and o_full.
-      if constexpr (!kBf16) {
-        if (active && ended > first) {
+      if (active && ended > first) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = __ldcg(&part.o[half * 8 + i][at]);
-            r[4 * i] = y.x;
-            r[4 * i + 1] = y.y;
-            r[4 * i + 2] = y.z;
-            r[4 * i + 3] = y.w;
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float4 y = __ldcg(&part.o[half * 8 + i][at]);
+          r[4 * i] = y.x;
+          r[4 * i + 1] = y.y;
+          r[4 * i + 2] = y.z;
+          r[4 * i + 3] = y.w;
         }
       }
       bool w = wait(sm, &sm.o_full, ended & 1);
@@ -1103,8 +1102,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
         sm.sums[turns & 3][half][row] += l2.x + l2.y;
         l2 = make_float2(0.f, 0.f);
       };
-      const int last_run = kBf16 || !more ? 0 : (j1 - j0 - 1) / kRunBlocks;
-      // Blocks before `plain_end` hold no nodes, no run (or stretch of sums) ends at them and the reference is there.
+      const int last_run = more ? (j1 - j0 - 1) / kRunBlocks<kBf16> : 0;
+      // Blocks before `plain_end` hold no nodes, no run ends at them and the reference is there.
       int plain_end = 0;
 #pragma unroll 1
       for (int j = j0 + (leads ? 0 : 1);; j += 2) {
@@ -1122,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
           has = j < j1;
           // the runs to end before this block's P is handed over: all before its own; after the last block
           // all but the segment's last
-          due = runs + (has && !kBf16 ? (j - j0) / kRunBlocks : has ? 0 : last_run);
+          due = runs + (has ? (j - j0) / kRunBlocks<kBf16> : last_run);
           if (!has && ended == due) break;
           if (has) {
             const int key0 = j * kKeys;
@@ -1193,8 +1192,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
             ok = end_run(last ? k - 1 : k, last ? before : runs, last);
           }
           plain_end = min(j1, base / kKeys);
-          constexpr int kNext = kBf16 ? kSumBlocks : kRunBlocks;
-          plain_end = min(plain_end, j0 + ((j - j0) / kNext + 1) * kNext);
+          plain_end = min(plain_end, j0 + ((j - j0) / kRunBlocks<kBf16> + 1) * kRunBlocks<kBf16>);
         }
         __syncwarp();
         if (!has) break;

@@ -73,3 +73,12 @@ def test_row_sums_of_equal_weights(pkv):
     lim = 2.0 ** -18 + 2.8e-6 + 2.0 ** -19 + 2.0 ** -22 + (34 + 14) * 2.0 ** -24
     assert lim < 2.0 ** -16
     assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
+
+
+def test_bf16_output_of_a_context_of_millions_of_equal_weights(pkv):
+    got, ref, size = repeated_pages(pkv, 1 << 20, True, 122, positive=True)
+    assert np.allclose(ref, size)
+    # the one weight as a single bf16 term 2^-8 and the output 2^-8; 256 truncating blocks of four MMAs a run (256 * 4 * 2^-24),
+    # 1024 runs added up in O and in the row sum (512 * 2^-24 each), a run's row sum (16 + 64) 2^-24, score and exponential
+    lim = 2 * 2.0 ** -8 + (1024 + 1024 + 80) * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22
+    assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
