@@ -506,40 +506,59 @@ __device__ __forceinline__ float2 dot_bf16x2(uint32_t x, uint32_t y, float2 sum)
 
 // One row's state (r, l, 32 dims of O from dim d0) over the keys pos .. end - 1, straight from global memory with a
 // running maximum: for rows whose sums left the range of the fast path or whose O is not finite, and for segments with
-// nodes whose V is not finite.  A key the row does not see is skipped.
+// nodes whose V is not finite.  A key the row does not see is skipped.  Stretches of kStretch keys are summed apart and then
+// added up: of n keys that weigh the same the sums are off by at most (kStretch + n / kStretch) / 2 times 2^-24.
+constexpr int kStretch = 256;
 __device__ __noinline__ float2 redo_row(const uint8_t *k_base, const uint8_t *v_base, long long page_stride,
                                         int num_pages, const int32_t *table, const uint32_t *mask, const uint16_t *q,
                                         int g, int pos, int end, int base, float c, int d0, float4 *o) {
-  float R = -INFINITY, L = 0.f;
+  float R = -INFINITY, l = 0.f;    // the running maximum, the stretch's sum under it
+  float Rt = -INFINITY, L = 0.f;   // the same of the stretches before (Rt <= R)
+  float4 y[8];                     // the stretch's O
 #pragma unroll 1
-  for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < 8; ++i) o[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (; pos < end; ++pos) {
+  for (int left = kStretch; pos < end; ++pos) {
     const int page = __ldg(table + pos / kPageTokens), node = pos - base;
-    if (page < 0 || page >= num_pages || (node >= 0 && !(__ldg(mask + (node >> 5)) >> (node & 31) & 1u))) continue;
-    const long long at = (long long)page * page_stride + (g * kPageTokens + pos % kPageTokens) * kRowBytes;
-    const uint4 *k = reinterpret_cast<const uint4 *>(k_base + at), *x = reinterpret_cast<const uint4 *>(q);
-    float2 dot = make_float2(0.f, 0.f);
+    if (!(page < 0 || page >= num_pages || (node >= 0 && !(__ldg(mask + (node >> 5)) >> (node & 31) & 1u)))) {
+      const long long at = (long long)page * page_stride + (g * kPageTokens + pos % kPageTokens) * kRowBytes;
+      const uint4 *k = reinterpret_cast<const uint4 *>(k_base + at), *x = reinterpret_cast<const uint4 *>(q);
+      float2 dot = make_float2(0.f, 0.f);
 #pragma unroll 2
-    for (int i = 0; i < kHeadDim / 8; ++i) {
-      const uint4 y = k[i], z = x[i];
-      dot = dot_bf16x2(y.w, z.w, dot_bf16x2(y.z, z.z, dot_bf16x2(y.y, z.y, dot_bf16x2(y.x, z.x, dot))));
-    }
-    const float e = (dot.x + dot.y) * c, Rn = fmaxf(R, e);
-    if (e == -INFINITY) continue;  // (weight 0, and no reference)
-    const float keep = R == -INFINITY ? 0.f : exp2f(R - Rn), w = exp2f(e - Rn);
-    R = Rn;
-    L = L * keep + w;
-    const uint2 *v = reinterpret_cast<const uint2 *>(v_base + at) + d0 / 4;
+      for (int i = 0; i < kHeadDim / 8; ++i) {
+        const uint4 u = k[i], z = x[i];
+        dot = dot_bf16x2(u.w, z.w, dot_bf16x2(u.z, z.z, dot_bf16x2(u.y, z.y, dot_bf16x2(u.x, z.x, dot))));
+      }
+      const float e = (dot.x + dot.y) * c, Rn = fmaxf(R, e);
+      if (e != -INFINITY) {  // (weight 0, and no reference)
+        const float keep = R == -INFINITY ? 0.f : exp2f(R - Rn), w = exp2f(e - Rn);
+        R = Rn;
+        l = l * keep + w;
+        const uint2 *v = reinterpret_cast<const uint2 *>(v_base + at) + d0 / 4;
 #pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const uint2 y = v[i];
-      const float4 z = o[i];
-      o[i] = make_float4(z.x * keep + w * bf16_lo(y.x), z.y * keep + w * bf16_hi(y.x), z.z * keep + w * bf16_lo(y.y),
-                         z.w * keep + w * bf16_hi(y.y));
+        for (int i = 0; i < 8; ++i) {
+          const uint2 u = v[i];
+          const float4 z = y[i];
+          y[i] = make_float4(z.x * keep + w * bf16_lo(u.x), z.y * keep + w * bf16_hi(u.x), z.z * keep + w * bf16_lo(u.y),
+                             z.w * keep + w * bf16_hi(u.y));
+        }
+      }
     }
+    if ((--left == 0 || pos == end - 1) && (R != -INFINITY || l != 0.f)) {  // (a NaN leaves R as it is)
+      const float keep = Rt == -INFINITY ? 0.f : exp2f(Rt - R);
+      Rt = R;
+      L = L * keep + l;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const float4 z = o[i], u = y[i];
+        o[i] = make_float4(z.x * keep + u.x, z.y * keep + u.y, z.z * keep + u.z, z.w * keep + u.w);
+        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      l = 0.f;
+    }
+    if (left == 0) left = kStretch;
   }
-  return make_float2(R, L);
+  return make_float2(Rt, L);
 }
 
 // Writes kDims dims of a row.

@@ -26,29 +26,31 @@ def pkv():
     return p
 
 
-def repeated_pages(pkv, pages, bf16, seed, positive=False, poke=None):
-    """(output, expected output, weighted sum of |V|) of one drafted token behind a context of `pages` pages; as many
-    sequences as make every CTA take one whole unit."""
+def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None):
+    """(output, expected output, weighted sum of |V|) of one drafted token behind a context of `pages` pages: those of `order`,
+    then page 1 again and again; as many sequences as make every CTA take one whole unit.  keys(K): sets the K of the pages
+    [page][head][row][dim] as bits."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    seqs, ctx = 2 * sms // 8, 16 * pages
+    seqs, ctx, ids = 2 * sms // 8, 16 * pages, max(2, max(order) + 1)
     if pages < 10000:
         assert tree_split.split([ctx] * seqs, [1] * seqs, sms=sms)[0]
-    host = oracle.Pool(2)
+    host = oracle.Pool(ids)
     draw = lambda tag, n: rng.normal_bf16(rng.stream_key(seed, tag), 0, n)  # noqa: E731
-    kv = draw("kv", 2 * 2 * 8 * 16 * 64).reshape(2, 2, 8, 16, 64)
+    kv = draw("kv", ids * 2 * 8 * 16 * 64).reshape(ids, 2, 8, 16, 64)
     kv[1, 0] = kv[1, 0, :, :1]                                  # one K row, sixteen times
-    kv[0, 0, :, 0, 7] = 0x4180                                  # token 0: K_7 = 16
+    if keys is None:
+        kv[0, 0, :, 0, 7] = 0x4180                              # token 0: K_7 = 16
+    else:
+        keys(kv[:, 0])
     if positive:
         kv[:, 1] = kv[:, 1] & 0x7FFF                            # V > 0
     host.data[:] = kv
     q = draw("q", seqs * 32 * 64).reshape(seqs, 32, 64)
     q[..., 7] = (q[..., 7] & 0x7F) | 0x3F80                     # q_7 in [1, 2)
-    if poke:
-        poke(host)
-    pool = pkv.KVPool(2, device=U.dev())
+    pool = pkv.KVPool(ids, device=U.dev())
     pool.buffer.copy_(U.to_dev(host.data).view(-1))
     bt = torch.ones(seqs, pages, dtype=torch.int32, device=U.dev())
-    bt[:, 0] = 0
+    bt[:, :len(order)] = torch.tensor(order, dtype=torch.int32, device=U.dev())
     out = torch.full((seqs, 32, 64), float("nan"), device=U.dev(), dtype=torch.bfloat16 if bf16 else torch.float32)
     status = torch.zeros(1, dtype=torch.int32, device=U.dev())
     pkv.paged_tree_attention(pool, out, U.to_dev(q), torch.arange(seqs + 1, dtype=torch.int32, device=U.dev()),
@@ -57,10 +59,12 @@ def repeated_pages(pkv, pages, bf16, seed, positive=False, poke=None):
                              pkv.tree_workspace(seqs, 1), status)
     torch.cuda.synchronize()
     assert int(status.item()) == 0
-    K, V = (rng.bf16_bits_to_f64(kv[:, i]).transpose(1, 0, 2, 3).reshape(8, 32, 64) for i in (0, 1))
-    times = np.repeat([1.0, pages - 1.0], 16)
+    K, V = (rng.bf16_bits_to_f64(kv[:, i]).transpose(1, 0, 2, 3).reshape(8, ids * 16, 64) for i in (0, 1))
+    times = np.array([order.count(i) for i in range(ids)], float)
+    times[1] += pages - len(order)
+    times = np.repeat(times, 16)
     x = np.einsum("sghd,gtd->sght", rng.bf16_bits_to_f64(q).reshape(seqs, 8, 4, 64), K) * 0.125
-    w = np.exp(x - x.max(-1, keepdims=True)) * times
+    w = np.exp(x - x[..., times > 0].max(-1, keepdims=True)) * times
     w /= w.sum(-1, keepdims=True)
     ref, size = (np.einsum("sght,gtd->sghd", w, v).reshape(seqs, 32, 64) for v in (V, np.abs(V)))
     return out.double().cpu().numpy(), ref, size
@@ -81,4 +85,16 @@ def test_bf16_output_of_a_context_of_millions_of_equal_weights(pkv):
     # the one weight as a single bf16 term 2^-8 and the output 2^-8; 256 truncating blocks of four MMAs a run (256 * 4 * 2^-24),
     # 1024 runs added up in O and in the row sum (512 * 2^-24 each), a run's row sum (16 + 64) 2^-24, score and exponential
     lim = 2 * 2.0 ** -8 + (1024 + 1024 + 80) * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22
+    assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
+
+
+def test_sums_of_rows_that_are_computed_again(pkv):
+    # the first 64 keys score about 0, a later one about 200 and the repeated ones a little less: out of the fast path's range
+    def keys(K):
+        K[1, :, :, 7] = 0x447A                                  # 1000
+        K[2, :, 5, 7] = 0x447C                                  # 1008
+    got, ref, size = repeated_pages(pkv, 1750, False, 123, order=(0, 0, 0, 0, 2), keys=keys)
+    # 110 stretches of 256 equal weights: (256 + 110) / 2 * 2^-24 in O and in the row sum; the exponential and the division 2^-22;
+    # the scores (exponents of up to 2^9.5: 6 roundings of 2^-24) move weight between the one key, 0.2 % at the most, and the others
+    lim = (256 + 110) * 2.0 ** -24 + 2.0 ** -22 + 0.002 * 6 * 2.0 ** (9.5 - 24)
     assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
