@@ -377,7 +377,8 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
  * id inside a context sets PKV_DEV_BAD_PAGE and that page is left out.  A NaN or infinity in the K or
  * V of a node reaches only the rows whose mask names that node.  A key whose score is -infinity has no
  * weight; a row with no other key gets zeros.  Rows whose scores rise by more than 77 (2^112 in
- * weight) above those of a part's first 64 keys, or that meet infinities, are computed again key by key: slowly.
+ * weight) above those of a part's first 64 keys, or that meet infinities, are computed again key by key: slowly
+ * (microseconds for each key; the limit of PKV_DEV_TIMEOUT does not run meanwhile).
  * num_seqs, max_query or num_q_rows = 0 enqueues nothing.  No allocation, one kernel launch.
  */
 #define PKV_OUT_BF16 2u

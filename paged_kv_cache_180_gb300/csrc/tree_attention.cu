@@ -45,8 +45,8 @@
 //    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
 //    NaN or an infinity (0 * NaN in the product would reach every row); the segment's rows are then
 //    computed again by redo_row().
-//  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing
-//    work, waits (bounded) for what is in flight, frees its tensor memory and exits.
+//  * Every mbarrier wait is bounded (about 2 s, without the time of rows that are computed again): on expiry the CTA
+//    reports PKV_DEV_TIMEOUT, stops issuing work, waits (bounded) for what is in flight, frees its tensor memory and exits.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -362,9 +362,15 @@ struct __align__(1024) Smem {
   Shares shares;
   int whole, units, longest;  // whether whole units are claimed; units, blocks of the longest one
   uint32_t tmem_base;
-  int abort;
+  alignas(8) int abort;  // (read together)
+  unsigned alive;        // the clock at redo_row()'s last sign of progress
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+
+__device__ __forceinline__ Smem &shared_memory() {
+  extern __shared__ uint8_t smem_raw[];
+  return *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+}
 
 // Waits for a phase, at most kWaitCycles (about 2 s); true when it completed.
 constexpr unsigned kWaitCycles = 3800000000u;
@@ -382,15 +388,23 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity) {
   return true;
 }
 
-// The same for a role's waits: gives up when another role has, and makes the others do so.
+// The same for a role's waits: gives up when another role has, and makes the others do so.  While a softmax warp is in
+// redo_row(), which ends by itself but may take seconds on a long segment, the limit counts from that one's last sign of
+// progress.  (One load for both words: with two the ragged batch took 1 % longer, with a call for expired waits 2 %.)
 __device__ __forceinline__ bool wait(Smem &sm, uint64_t *bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned t0 = clock32();
-  volatile int *abort = &sm.abort;
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
-    if (clock32() - t0 > kWaitCycles) *abort = 1;
-    if (*abort) return false;
+    int stop;
+    unsigned alive;
+    asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(stop), "=r"(alive)
+                 : "r"(smem_addr(&sm.abort))
+                 : "memory");
+    const unsigned now = clock32();
+    if (min(now - t0, now - alive) > kWaitCycles) *reinterpret_cast<volatile int *>(&sm.abort) = stop = 1;
+    if (stop) return false;
   }
   return true;
 }
@@ -556,7 +570,10 @@ __device__ __noinline__ float2 redo_row(const uint8_t *k_base, const uint8_t *v_
       }
       l = 0.f;
     }
-    if (left == 0) left = kStretch;
+    if (left == 0) {
+      left = kStretch;
+      *reinterpret_cast<volatile unsigned *>(&shared_memory().alive) = clock32();
+    }
   }
   return make_float2(Rt, L);
 }
@@ -663,8 +680,7 @@ __device__ __forceinline__ void merge_parts(const Part *parts, void *out, int c0
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(const __grid_constant__ TreeArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  Smem &sm = shared_memory();
   // the warp index by a shuffle: the compiler then knows that a role's values are the same in all lanes
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = int(gridDim.x), cta = int(blockIdx.x);
@@ -676,7 +692,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_attention_kernel(co
     mbar_init_fence();
   }
   if (tid < 4) sm.nonfinite[tid] = -1;
-  if (tid == 4) sm.abort = 0;
+  if (tid == 4) {
+    sm.abort = 0;
+    sm.alive = clock32() - kWaitCycles - 1;  // none
+  }
   // entries of the list, units, and 4 x the blocks of the longest unit + its octets of nodes less one
   long long T = 0;
   int units = 0, longest = 0;

@@ -26,10 +26,10 @@ def pkv():
     return p
 
 
-def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None):
+def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None, seconds=None):
     """(output, expected output, weighted sum of |V|) of one drafted token behind a context of `pages` pages: those of `order`,
     then page 1 again and again; as many sequences as make every CTA take one whole unit.  keys(K): sets the K of the pages
-    [page][head][row][dim] as bits."""
+    [page][head][row][dim] as bits.  `seconds`: a list that receives the time the call took."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     seqs, ctx, ids = 2 * sms // 8, 16 * pages, max(2, max(order) + 1)
     if pages < 10000:
@@ -53,12 +53,17 @@ def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None
     bt[:, :len(order)] = torch.tensor(order, dtype=torch.int32, device=U.dev())
     out = torch.full((seqs, 32, 64), float("nan"), device=U.dev(), dtype=torch.bfloat16 if bf16 else torch.float32)
     status = torch.zeros(1, dtype=torch.int32, device=U.dev())
-    pkv.paged_tree_attention(pool, out, U.to_dev(q), torch.arange(seqs + 1, dtype=torch.int32, device=U.dev()),
-                             torch.ones(seqs, 1, dtype=torch.int32, device=U.dev()), bt, pages,
-                             torch.full((seqs,), ctx, dtype=torch.int32, device=U.dev()), 1, ctx, 0.125,
-                             pkv.tree_workspace(seqs, 1), status)
+    args = (pool, out, U.to_dev(q), torch.arange(seqs + 1, dtype=torch.int32, device=U.dev()),
+            torch.ones(seqs, 1, dtype=torch.int32, device=U.dev()), bt, pages,
+            torch.full((seqs,), ctx, dtype=torch.int32, device=U.dev()), 1, ctx, 0.125, pkv.tree_workspace(seqs, 1), status)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ends[0].record()
+    pkv.paged_tree_attention(*args)
+    ends[1].record()
     torch.cuda.synchronize()
     assert int(status.item()) == 0
+    if seconds is not None:
+        seconds.append(ends[0].elapsed_time(ends[1]) * 1e-3)
     K, V = (rng.bf16_bits_to_f64(kv[:, i]).transpose(1, 0, 2, 3).reshape(8, ids * 16, 64) for i in (0, 1))
     times = np.array([order.count(i) for i in range(ids)], float)
     times[1] += pages - len(order)
@@ -88,13 +93,31 @@ def test_bf16_output_of_a_context_of_millions_of_equal_weights(pkv):
     assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
 
 
-def test_sums_of_rows_that_are_computed_again(pkv):
+def _grown(K):
     # the first 64 keys score about 0, a later one about 200 and the repeated ones a little less: out of the fast path's range
-    def keys(K):
-        K[1, :, :, 7] = 0x447A                                  # 1000
-        K[2, :, 5, 7] = 0x447C                                  # 1008
-    got, ref, size = repeated_pages(pkv, 1750, False, 123, order=(0, 0, 0, 0, 2), keys=keys)
+    K[1, :, :, 7] = 0x447A                                      # 1000
+    K[2, :, 5, 7] = 0x447C                                      # 1008
+
+
+def test_sums_of_rows_that_are_computed_again(pkv):
+    got, ref, size = repeated_pages(pkv, 1750, False, 123, order=(0, 0, 0, 0, 2), keys=_grown)
     # 110 stretches of 256 equal weights: (256 + 110) / 2 * 2^-24 in O and in the row sum; the exponential and the division 2^-22;
     # the scores (exponents of up to 2^9.5: 6 roundings of 2^-24) move weight between the one key, 0.2 % at the most, and the others
     lim = (256 + 110) * 2.0 ** -24 + 2.0 ** -22 + 0.002 * 6 * 2.0 ** (9.5 - 24)
+    assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
+
+
+def test_rows_computed_again_for_longer_than_a_wait_may_take(pkv):
+    # A wait inside the kernel gives up after 3.8e9 cycles, 1.8 s at the highest clock.  Rows that are computed again over a
+    # long segment take longer; the other warps wait for them.
+    def call(pages, seconds):
+        return repeated_pages(pkv, pages, False, 124, order=(0, 0, 0, 0, 2), keys=_grown, seconds=seconds)
+    seconds = []
+    for _ in range(2):
+        call(4000, seconds)
+    pages = int(4000 * 3.2 / seconds[-1])
+    assert pages < 400_000, seconds                             # (what a key takes: 0.5 us at the least)
+    got, ref, size = call(pages, seconds)
+    assert seconds[-1] > 2.4, (seconds, pages)
+    lim = (256 + 16 * pages / 256) * 2.0 ** -24 + 2.0 ** -22 + 0.002 * 6 * 2.0 ** (9.5 - 24)
     assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
