@@ -370,8 +370,12 @@ int pkv_paged_decode_attention_noalloc(const pkv_pool *pool, float *out, const v
  *                  before that.  Use it only when that kernel writes none of the first four - for
  *                  example pkv_kv_append of the drafted tokens.
  *                  PKV_OUT_BF16: out is bf16 (rounded to nearest even); the softmax weights then
- *                  carry bf16's 8 significant bits into the product with V.  Other bits return
- *                  PKV_ERR_SHAPE.
+ *                  carry bf16's 8 significant bits into the product with V: an error of 2.3e-3 of the
+ *                  output's norm, where rounding it alone has 1.7e-3.  Other bits return PKV_ERR_SHAPE.
+ * Precision of fp32 output: the weights carry 16 significant bits into the product with V (row sums all 24), and
+ * the tensor cores truncate what they add up over 1024 keys at a time.  On normal values that is an error of 1.3e-6
+ * (64 keys) to 3.7e-6 (2048 and more) of the output's norm, up to 5e-6 where all of V has one sign; it does not
+ * grow with the context (fp32 arithmetic throughout has 0.5e-6 to 4e-6).
  * A sequence whose lengths do not fit (n_s < 0, > max_query or > context_lens[s], a context < 0 or
  * > max_context, query rows past num_q_rows) gets zero rows and PKV_DEV_BAD_CONTEXT; an invalid page
  * id inside a context sets PKV_DEV_BAD_PAGE and that page is left out.  A NaN or infinity in the K or
@@ -489,7 +493,8 @@ int pkv_alloc_state(const pkv_alloc *alloc, int32_t *free_pages, int32_t *credit
  * into copy_src/copy_dst (host int32 [capacity]; capacity >= num_layers always suffices).
  * *num_copies receives their count.  Blocks that src has not assigned stay unassigned.
  * Returns PKV_OK, PKV_ERR_NULL, PKV_ERR_STATE (src not admitted, dst admitted already),
- * PKV_ERR_EXCEEDS_POOL or PKV_ERR_NO_CREDIT as admit does, PKV_ERR_NO_PAGE, or PKV_ERR_SHAPE
+ * PKV_ERR_EXCEEDS_POOL or PKV_ERR_NO_CREDIT as admit does (before it looks for pages), PKV_ERR_NO_PAGE (only
+ * where sequences have assigned blocks beyond their credits), or PKV_ERR_SHAPE
  * (src = dst, tokens or max_new_tokens out of range, capacity too small); on error nothing has changed. */
 int pkv_alloc_fork(pkv_alloc *alloc, int src_seq, int dst_seq, int tokens, int max_new_tokens, int32_t *copy_src,
                    int32_t *copy_dst, int capacity, int32_t *num_copies);

@@ -63,9 +63,10 @@ struct CommitArgs {
 // a batch of loads reads all lie at or behind the rows its stores write, and every row a later batch reads lies
 // behind them.  Each thread reads and writes its own chunk only, so loading a batch before storing it is all
 // the ordering there is.
-// What bounds it is three dependent round trips (lengths, path and tables, rows) and rows that lie in pieces of 128
-// bytes: 256 sequences x 16 layers with paths of up to 12 of 32 nodes take 19.4 us (13.5 for the bytes), 64 with up to
-// 8 take 4.1, one sequence 2.8.  (4 or 16 rows in flight: 19.4 and 23.5 us; two layers to a CTA: 20 us, and 4.4 for 64.)
+// What bounds it is latency: each CTA makes three dependent round trips (lengths, path and tables, rows), and a large batch
+// is some three waves of CTAs that do so one after the other.  256 sequences x 16 layers with paths of up to 12 of 32
+// nodes take 19.5 us (13.5 for the bytes; DRAM 37 %, issue slots 22 %, half the warps there), 64 with up to 8 take 4.1,
+// one sequence 3.0.  (4 or 16 rows in flight: 19.4 and 23.5 us; two layers to a CTA: 20 us, and 4.4 for 64.)
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a) {
   __shared__ long long from[kCommitRows], to[kCommitRows];  // byte offsets in either half of the pool; to < 0: stays
   griddep_launch_dependents();

@@ -26,20 +26,22 @@
 //    groups that take the blocks in turn, a thread to a row; P overwrites its S and is the TMEM A operand
 //    of O += P V.  (Two threads to a row on the same block, with S buffers for two blocks, took 1650 cycles a block
 //    against 1300.)
-//  * What bounds it, by the time a call takes: with many keys a node the K/V bytes: 256 sequences of 2048 tokens and 8
-//    nodes take 170 us, 6.5 TB/s, 96 % of a plain copy's rate.  With many short units their starts and ends, each
-//    as long as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 51 us, 24 for the bytes).  With 64 nodes two
-//    tiles share the bytes, and the steps from barrier to barrier count (64 x 2048 in bf16: 70 us, 45 for the
-//    bytes): leaving out all of the softmax's arithmetic took 8 % off, the loads 13 more.  The
-//    smallest call (600 tokens, 6 nodes) takes 10.6 us: launch 2, lengths 1.5, tables and first K 1.9, ten blocks
+//  * What bounds it, by the time a call takes on the device (replayed from a graph; calls one after the other from a
+//    program take 1.5 to 3 us more each, and up to 5 % more on some machines): with many keys a node the K/V bytes: 256
+//    sequences of 2048 tokens and 8 nodes take 168 to 170 us, 6.4 to 6.5 TB/s, 95 % of a plain copy's rate.  With many
+//    short units their starts and ends, each as long as 7 blocks (64 trees of 1..64 nodes over 64..2048 tokens: 51 us, 24
+//    for the bytes).  With 64 nodes two tiles share the bytes, and the steps from barrier to barrier count (64 x 2048 in
+//    bf16: 73 us, 45 for the bytes): leaving out all of the softmax's arithmetic took 8 % off, the loads 13 more.  The
+//    smallest call (600 tokens, 6 nodes) takes 10.7 to 11.1 us: launch 2, lengths 1.5, tables and first K 1.9, ten blocks
 //    4.5, the end 0.7.
 //  * The reference is the row's largest exponent in the segment's first block and stays: weights are floats, so
 //    it only has to keep them in range, and no maximum, rescaling or exchange between the groups is needed after
 //    that.  A row whose sum leaves [2^-90, 2^112] is computed again from global memory by redo_row(), slowly (with every
-//    row of 64 x 2048 tokens and 32 nodes computed again a call takes 15.1 ms instead of 0.08).
+//    row of 64 x 2048 tokens and 32 nodes computed again a call takes 17 ms instead of 0.08).
 //  * Weights: with fp32 output P is split into bf16 hi + lo terms (16 significant bits, two products: an error of
-//    2.4e-6 of the output; a third term with two S buffers and runs of 4 blocks would give 0.9e-6 and take 30 to 45 %
-//    longer); with bf16 output P is one bf16 term, rounded as the output will be.  Row sums are taken in
+//    2.4e-6 of the output, and 2.3e-6 from the truncating accumulator over a run; a third term with two S buffers and
+//    runs of 4 blocks would give 0.9e-6 in all and take 30 to 45 % longer); with bf16 output P is one bf16 term, rounded as
+//    the output will be (1.6e-3 each; with two terms 64 x 2048 and 64 nodes took 94.7 us for 74.1).  Row sums are taken in
 //    fp32 registers from the unrounded weights (a sum inside the MMA would be truncated at every step).
 //  * Masks: the score of a key a row may not see is replaced by an infinity, so a NaN score stays out.  V rows at or
 //    past the context (stale pool bytes) are zeroed in shared memory, and so are nodes' V rows that hold a
@@ -86,10 +88,11 @@ constexpr int kMinEntries = 2, kMostEntries = 6;
 // (6 nodes: 512 tokens 3 % slower to 5 % faster whole, 1024 tokens 15 % slower to 13 % faster, by the number of sequences;
 // 32 nodes: 1024 tokens 2 % slower to 29 % faster, 2048 28 % slower to 19 % faster.)
 constexpr float kMergeCost = 7.f, kMergeCostOctet = 6.f, kLastRound = 0.5625f;
-// A segment's products are added up in runs of this many blocks: every MMA truncates the accumulator, which with fp32
-// output (eight MMAs a block) costs a row about 1.4e-7 of its size a block (5.5e-6 over 2048 keys, 3e-5 over 14000, in one
-// run), with bf16 output (four) half of that, and more where all products have one sign: 15 % over 2^24 keys.  So a run's O
-// goes to the segment's part in the workspace, where the runs are added with rounding.
+// A segment's products are added up in runs of this many blocks: every MMA truncates the accumulator.  With fp32 output
+// (eight MMAs a block) a row is 1.4e-7 of its size too small for each block of a run, 2.3e-6 for a whole one (where V has
+// one sign 3e-7 and 4.8e-6), whatever the number of runs; in one run it was 3e-5 over 14000 keys.  With bf16 output (four)
+// one run over 2^24 keys of V of one sign lost 15 %.  So a run's O goes to the segment's part in the workspace, where the
+// runs are added with rounding.
 template <bool kBf16>
 constexpr int kRunBlocks = kBf16 ? 256 : 16;
 // Row sums are added up in three levels: over a block's keys, over a run's blocks, over the runs.  Nearly equal weights, whose

@@ -4,8 +4,8 @@ Relative to the output's norm over a sequence's rows.  The errors of different k
 signs, as the outputs' terms w V are, so both shrink alike as the number of keys grows:
 
 fp32 output: a weight as two bf16 terms is off by at most 2^-18 of itself, 2^-18 / sqrt(3) = 2.2e-6 in the mean square;
-the tensor core truncates its accumulator, at most 2.8e-6 over a run of 16 blocks, and what is added up behind that
-rounds, (blocks / 16 + parts) 2^-25 in the mean, below 2e-6 for 500 runs; score and exponential 2^-19 / sqrt(3) = 1.1e-6 at
+the tensor core truncates its accumulator, 2.3e-6 over a run of 16 blocks (V of both signs; taken as 2.8e-6), and what is
+added up behind that rounds, (blocks / 16 + parts) 2^-25 in the mean, below 2e-6 for 500 runs; score and exponential 2^-19 / sqrt(3) = 1.1e-6 at
 exponents of up to 2^4.  The root of the squares' sum is 4.2e-6; twice that and a little: 1e-5.
 
 bf16 output: half a step of 2^-8 in the weights and in the output, each 2^-8 / sqrt(3) at the most in the mean square (all
