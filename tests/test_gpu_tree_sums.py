@@ -26,13 +26,14 @@ def pkv():
     return p
 
 
-def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None, seconds=None):
+def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None, seconds=None, seqs=None):
     """(output, expected output, weighted sum of |V|) of one drafted token behind a context of `pages` pages: those of `order`,
-    then page 1 again and again; as many sequences as make every CTA take one whole unit.  keys(K): sets the K of the pages
-    [page][head][row][dim] as bits.  `seconds`: a list that receives the time the call took."""
+    then page 1 again and again; as many sequences as make every CTA take one whole unit, or `seqs`.  keys(K): sets the K of
+    the pages [page][head][row][dim] as bits.  `seconds`: a list that receives the time the call took."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    seqs, ctx, ids = 2 * sms // 8, 16 * pages, max(2, max(order) + 1)
-    if pages < 10000:
+    cut, seqs = seqs is not None, seqs or 2 * sms // 8
+    ctx, ids = 16 * pages, max(2, max(order) + 1)
+    if not cut and pages < 10000:
         assert tree_split.split([ctx] * seqs, [1] * seqs, sms=sms)[0]
     host = oracle.Pool(ids)
     draw = lambda tag, n: rng.normal_bf16(rng.stream_key(seed, tag), 0, n)  # noqa: E731
@@ -120,4 +121,18 @@ def test_rows_computed_again_for_longer_than_a_wait_may_take(pkv):
     got, ref, size = call(pages, seconds)
     assert seconds[-1] > 2.4, (seconds, pages)
     lim = (256 + 16 * pages / 256) * 2.0 ** -24 + 2.0 ** -22 + 0.002 * 6 * 2.0 ** (9.5 - 24)
+    assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_runs_in_units_that_are_cut(pkv, bf16):
+    # one sequence, each unit in 38 parts of over 256 blocks: runs inside parts, parts merged in groups
+    whole, shares = tree_split.split([800_000], [1])
+    assert not whole and min(j1 - j0 for x in shares for *_, j0, j1, _ in x) > 256
+    got, ref, size = repeated_pages(pkv, 50_000, bf16, 125, seqs=1)
+    # as above: 21 runs a part and 38 parts for fp32, two runs a part for bf16 output
+    if bf16:
+        lim = 2 * 2.0 ** -8 + (1024 + 2 * (16 + 64) + 2 * 38) * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22
+    else:
+        lim = 2.0 ** -18 + 2.8e-6 + 2.0 ** -19 + 2.0 ** -22 + (20 + 2 * (21 + 38) / 2) * 2.0 ** -24
     assert (np.abs(got - ref) <= size * lim).all(), float((np.abs(got - ref) / size).max())
