@@ -75,6 +75,7 @@ extern "C" {
 #define PKV_DEV_BAD_PAGE 4u        /* block-table entry outside [0, num_pages) inside the context;
                                       that page's tokens are left out of the softmax */
 #define PKV_DEV_TIMEOUT 8u         /* an internal pipeline wait gave up (about 2 s); the CTA stopped */
+#define PKV_DEV_BAD_BUDGET 32u     /* kv_evict: a budget below 0, or above max_budget; that sequence stays as it is */
 #define PKV_DEV_BAD_PATH 16u       /* tree_commit: an accepted path that is not an ascending list of its
                                       sequence's nodes; that sequence's rows stay as they are */
 
@@ -432,6 +433,115 @@ int pkv_tree_commit(const pkv_pool *pool, const int32_t *block_tables, int64_t b
  */
 int pkv_kv_copy_pages(const pkv_pool *pool, const int32_t *src_pages, const int32_t *dst_pages, int num_copies,
                       int32_t *device_status, void *stream);
+
+/* ---- bounded caches: a window with sinks, weight sums, eviction ------------------------------
+ *
+ * A sequence need not look at (or keep) all of its cached tokens.  The window calls attend to the most
+ * recent tokens and to the first few ("sinks") only; pages between them are not read, and their block-table
+ * entries may be -1.  pkv_paged_decode_attention_weights is decode attention that also adds up the
+ * weight that each cached token receives; pkv_kv_evict then keeps, for each K/V head, the tokens with the largest sums.
+ * After it the caller's lengths are the new ones (pkv_alloc_truncate frees the pages behind them), and
+ * decode, prefill and the window calls go on as before: tokens keep their order.
+ */
+
+/*
+ * pkv_paged_window_decode_attention - one decode step of attention with a sliding window and sinks.
+ *
+ *   out[s][h][:] = sum_{t in A_s} w_t V_t[h / group][:],  w = softmax_{t in A_s}( scale * q[s][h] . K_t[h / group] ),
+ *   A_s = { t < ctx_s : t < sinks or t >= ctx_s - window }.
+ *
+ *   out            device; [num_seqs][num_q_heads][head_dim], 16-byte aligned: float32, or bf16 with PKV_OUT_BF16.
+ *   q              device; bf16 [num_seqs][num_q_heads][head_dim], 16-byte aligned.
+ *   window         >= 1 tokens, the new one included; sinks >= 0 (both may exceed the context: plain attention).
+ *   scale          as for tree attention (scale * log2(e) has to be finite).
+ *   flags          PKV_OVERLAP_PREVIOUS: launched with programmatic stream serialization; context_lens, block_tables and q
+ *                  are read at once, the pool pages only after the kernel before it on the stream has completed, and
+ *                  nothing is written before that (for example behind the new tokens' pkv_kv_append).
+ *                  PKV_OUT_BF16.  Other bits return PKV_ERR_SHAPE.
+ * Other arguments as for pkv_paged_decode_attention (max_context at most 2^31 - 64).  Entries of blocks that hold no
+ * token of A_s are not read.  A context of 0 gives zero rows; a context < 0 or > max_context also sets
+ * PKV_DEV_BAD_CONTEXT; a bad page id inside A_s sets PKV_DEV_BAD_PAGE and that page is left out.  What pages hold at
+ * tokens outside A_s reaches nothing.  Sums run over V times weights of at most 1: keep |V| * context below 2^127; an
+ * infinity in a visible V row gives NaN.  No workspace, no allocation, one kernel launch; calls may overlap.
+ */
+int pkv_paged_window_decode_attention(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
+                                      const int32_t *block_tables, int64_t block_table_stride,
+                                      const int32_t *context_lens, int num_seqs, int max_context, float scale,
+                                      int window, int sinks, int32_t *device_status, unsigned flags, void *stream);
+
+/*
+ * pkv_paged_window_prefill_attention - the same for the last n_s cached tokens of each sequence (prefill, chunked prefill):
+ *
+ *   A_i = { t <= p_i : t < sinks or t > p_i - window },  p_i = context_lens[s] - n_s + (i - query_start[s]).
+ *
+ * Arguments as for pkv_paged_prefill_attention, except: out is float32, or bf16 with PKV_OUT_BF16 (the weights then carry
+ * bf16's 8 significant bits into the product with V; with float32 16); max_query at most 2^20; window, sinks, scale
+ * and flags as above (with PKV_OVERLAP_PREVIOUS query_start is read at once, too).
+ * A sequence whose lengths do not fit (n_s < 0, > max_query or > context_lens[s], a context < 0 or > max_context, query
+ * rows past num_q_rows) gets zero rows and PKV_DEV_BAD_CONTEXT; a bad page id inside a row's A_i sets PKV_DEV_BAD_PAGE and
+ * that page is left out.  A NaN or infinity in K or V reaches only the rows that see its token: rows whose output would not be
+ * finite are computed again from the keys that they see (microseconds for each key).  No workspace, one kernel launch.
+ */
+int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *out, const void *q, int num_q_heads, int num_q_rows,
+                                       const int32_t *query_start, const int32_t *block_tables,
+                                       int64_t block_table_stride, const int32_t *context_lens, int num_seqs,
+                                       int max_query, int max_context, float scale, int window, int sinks,
+                                       int32_t *device_status, unsigned flags, void *stream);
+
+/*
+ * pkv_paged_decode_attention_weights - pkv_paged_decode_attention that also adds up the weights:
+ *
+ *   sums[s][g][t] = decay * sums[s][g][t] + sum_{h / group = g} w_t(s, h)      for t < ctx_s
+ *
+ *   weight_sums    device float32; sequence s, K/V head g, token t at weight_sums + s * seq_stride + g * head_stride + t,
+ *                  rows of at least max_context tokens (one layer of [seqs][layers][heads][tokens], for example).  No two
+ *                  (s, g) share an element.  Sums at or past ctx_s are neither read nor written; a new token's
+ *                  sum has to be 0 when it is first attended (decay 0 does not read the old sums).
+ *   decay          0 .. 1 (PKV_ERR_SCALE): 1 adds up over all steps, less lets older steps fade, 0 keeps the last step's weights.
+ *   workspace      device, >= pkv_weights_workspace_bytes(num_seqs, max_context), 16-byte aligned, of any contents; null where
+ *                  that is 0.  Calls sharing it must not overlap on the GPU (nor may graphs that captured it).
+ *   out, q, scale, flags  as for pkv_paged_window_decode_attention (with PKV_OVERLAP_PREVIOUS the sums are read after the
+ *                  kernel before it has completed).  max_context at most 2^30.
+ * A token of a page that is left out (PKV_DEV_BAD_PAGE) has weight 0.  A sequence of invalid context gets zero rows and keeps its
+ * sums.  Results do not depend on timing.  One kernel launch.
+ */
+int pkv_paged_decode_attention_weights(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
+                                       const int32_t *block_tables, int64_t block_table_stride,
+                                       const int32_t *context_lens, int num_seqs, int max_context, float scale,
+                                       float *weight_sums, int64_t seq_stride, int64_t head_stride, float decay,
+                                       void *workspace, size_t workspace_bytes, int32_t *device_status, unsigned flags,
+                                       void *stream);
+
+/* Workspace bytes of pkv_paged_decode_attention_weights: the scores of contexts too long to keep them on chip.  0 up to
+ * max_context = 57344, and on bad arguments. */
+size_t pkv_weights_workspace_bytes(int num_seqs, int max_context);
+
+/*
+ * pkv_kv_evict - keep, of the ctx tokens of each sequence, B = min(budgets[s], ctx) in every layer and K/V head:
+ * the first a = min(sinks, B), the last r = min(recent, B - a), and of the tokens between them the B - a - r with the largest
+ * weight sums; of equal sums the earlier token (-0 equals 0, NaN is below everything).  The kept tokens' K and V rows move, in
+ * their order, to positions 0 .. B - 1, in place (bit copies); heads keep tokens of their own, layers too.
+ *   block_tables      as for pkv_tree_commit: the row of (s, layer) is at s * block_table_stride + layer * layer_stride.
+ *   budgets           device int32 [num_seqs]: tokens to keep, 0 .. max_budget (any size where the context is not larger
+ *                     than max_budget).
+ *   weight_sums       device float32; (s, layer, g, t) at s * sums_seq_stride + layer * sums_layer_stride +
+ *                     g * sums_head_stride + t; rows of at least max_context tokens that do not share elements.
+ *   new_weight_sums   device float32, same strides: the kept tokens' sums at 0 .. B - 1, zeros at B .. ctx - 1 (tokens to come
+ *                     start there).  weight_sums itself, or memory that does not overlap it.
+ *   kept              device int32 [num_seqs][num_layers][num_kv_heads][kept_stride], kept_stride >= max_budget: entry k < B is the
+ *                     position that row k came from, ascending; entries at or past B are not written.
+ *   new_context_lens  device int32 [num_seqs], nullable; receives B.
+ * What is written may not overlap context_lens, budgets, the sums that are read, or each other (PKV_ERR_SHAPE).
+ * A context < 0 or > max_context sets PKV_DEV_BAD_CONTEXT, a budget < 0 or min(budget, ctx) > max_budget PKV_DEV_BAD_BUDGET: that
+ * sequence's rows, sums and list stay, its new length is the old one.  A row whose source or target page id is
+ * invalid is not moved (PKV_DEV_BAD_PAGE).  Rows behind B keep their bytes.  Sequences must not share the pages that hold
+ * their tokens (pkv_alloc_write_page sees to that).  max_context at most 2^30.  No workspace, one kernel launch.
+ */
+int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, int64_t block_table_stride, int64_t layer_stride,
+                 int num_layers, const int32_t *context_lens, const int32_t *budgets, int num_seqs, int max_context,
+                 int max_budget, int sinks, int recent, const float *weight_sums, float *new_weight_sums,
+                 int64_t sums_seq_stride, int64_t sums_layer_stride, int64_t sums_head_stride, int32_t *kept,
+                 int64_t kept_stride, int32_t *new_context_lens, int32_t *device_status, void *stream);
 
 /* ---- host page allocator (no GPU) ------------------------------------------------------
  *

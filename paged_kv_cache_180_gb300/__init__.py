@@ -11,7 +11,8 @@ _PUBLIC = ("KVPool", "PkvError", "PkvPool", "decode_max_ctas", "decode_plan", "d
            "kv_append", "kv_pool_bytes", "kv_pool_create", "paged_decode_attention",
            "paged_decode_attention_noalloc", "paged_prefill_attention", "Scheduler", "Allocator",
            "kv_copy_pages", "paged_tree_attention", "tree_commit", "tree_workspace", "tree_workspace_bytes",
-           "status_string")
+           "paged_window_decode_attention", "paged_window_prefill_attention", "paged_decode_attention_weights",
+           "weights_workspace", "weights_workspace_bytes", "kv_evict", "status_string")
 
 
 def __getattr__(name):

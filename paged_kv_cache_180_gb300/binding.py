@@ -30,6 +30,7 @@ DEV_BAD_CONTEXT = 2
 DEV_BAD_PAGE = 4
 DEV_TIMEOUT = 8
 DEV_BAD_PATH = 16
+DEV_BAD_BUDGET = 32
 
 
 class PkvPool(ctypes.Structure):
@@ -85,6 +86,13 @@ EXPORTS = {
     "pkv_tree_workspace_bytes": (_Z, [_I, _I, _I, _I]),
     "pkv_tree_commit": (_I, [_PP, _P, _L, _L, _I, _P, _P, _P, _L, _P, _I, _I, _I, _P, _P, _P]),
     "pkv_kv_copy_pages": (_I, [_PP, _P, _P, _I, _P, _P]),
+    "pkv_paged_window_decode_attention": (_I, [_PP, _P, _P, _I, _P, _L, _P, _I, _I, _F, _I, _I, _P, ctypes.c_uint, _P]),
+    "pkv_paged_window_prefill_attention": (_I, [_PP, _P, _P, _I, _I, _P, _P, _L, _P, _I, _I, _I, _F, _I, _I, _P,
+                                                ctypes.c_uint, _P]),
+    "pkv_paged_decode_attention_weights": (_I, [_PP, _P, _P, _I, _P, _L, _P, _I, _I, _F, _P, _L, _L, _F, _P, _Z, _P,
+                                                ctypes.c_uint, _P]),
+    "pkv_weights_workspace_bytes": (_Z, [_I, _I]),
+    "pkv_kv_evict": (_I, [_PP, _P, _L, _L, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _L, _L, _L, _P, _L, _P, _P, _P]),
     "pkv_alloc_create": (_I, [_I, _I, _I, _I, _I, _P, ctypes.POINTER(_P)]),
     "pkv_alloc_destroy": (None, [_P]),
     "pkv_alloc_admit": (_I, [_P, _I, _I, _I, ctypes.POINTER(ctypes.c_int32)]),
@@ -399,6 +407,148 @@ def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: to
                              "host memory")
     rc = _lib.pkv_kv_copy_pages(ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), src_pages.data_ptr(),
                                 dst_pages.data_ptr(), n, _status_ptr(where, status, dev), _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
+
+
+def _attention_args(where: str, out, q, ints, block_tables, status) -> tuple[int, int | None]:
+    """Checks what the window and weights calls share; (flag of out's type, pointer of the status word)."""
+    dev, kind = _current_device(), out.dtype
+    for t in ints:
+        if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+            _refuse(where, t, _I32)
+    if q.dtype is not _BF16 or q.get_device() != dev or not q.is_contiguous():
+        _refuse(where, q, _BF16)
+    if block_tables.dtype is not _I32 or block_tables.get_device() != dev or block_tables.stride(-1) != 1:
+        _refuse(where, block_tables, _I32)
+    if (kind is not _F32 and kind is not _BF16) or out.get_device() != dev or not out.is_contiguous():
+        _refuse(where, out, "float32 or bfloat16")
+    if len(q.shape) != 3 or out.shape[1:] != q.shape[1:] or len(out.shape) != 3:
+        raise ValueError(f"{where}: q and out are [rows, heads, dim]")
+    return OUT_BF16 if kind is _BF16 else 0, _status_ptr(where, status, dev)
+
+
+def paged_window_decode_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Tensor, block_tables: torch.Tensor,
+                                  block_table_stride: int, context_lens: torch.Tensor, max_context: int, scale: float,
+                                  window: int, sinks: int = 0, status: torch.Tensor | None = None, stream=None,
+                                  overlap_previous: bool = False) -> None:
+    """paged_decode_attention over the last ``window`` tokens of each sequence and its first ``sinks``.  out: float32 or
+    bfloat16 [seqs, heads, dim].  Table entries of pages in between may be -1.  overlap_previous: launch with
+    PKV_OVERLAP_PREVIOUS (only when the kernel before it on the stream writes none of q, context_lens or
+    block_tables, e.g. the new tokens' kv_append)."""
+    where = "pkv_paged_window_decode_attention"
+    flags, st = _attention_args(where, out, q, (context_lens,), block_tables, status)
+    num_seqs = context_lens.numel()
+    if q.shape[0] < num_seqs or out.shape[0] < num_seqs:
+        raise ValueError(f"{where}: {num_seqs} sequences, q has {q.shape[0]} rows and out {out.shape[0]}")
+    rc = _lib.pkv_paged_window_decode_attention(
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q.shape[1],
+        block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_context, scale, window, sinks,
+        st, flags | (OVERLAP_PREVIOUS if overlap_previous else 0), _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
+
+
+def paged_window_prefill_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Tensor, query_start: torch.Tensor,
+                                   block_tables: torch.Tensor, block_table_stride: int, context_lens: torch.Tensor,
+                                   max_query: int, max_context: int, scale: float, window: int, sinks: int = 0,
+                                   status: torch.Tensor | None = None, stream=None, overlap_previous: bool = False) -> None:
+    """Attention of the last n_s cached tokens of each sequence (rows query_start[s] ..), each over the ``window``
+    tokens up to itself and the first ``sinks``.  out: float32 or bfloat16 [rows, heads, dim].
+    overlap_previous: launch with PKV_OVERLAP_PREVIOUS (only when the kernel before it on the stream writes none of q,
+    query_start, context_lens or block_tables, e.g. the prompt's kv_append)."""
+    where = "pkv_paged_window_prefill_attention"
+    flags, st = _attention_args(where, out, q, (query_start, context_lens), block_tables, status)
+    num_seqs = context_lens.numel()
+    if query_start.numel() != num_seqs + 1:
+        raise ValueError(f"{where}: query_start is [seqs + 1]")
+    rc = _lib.pkv_paged_window_prefill_attention(
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q.shape[1],
+        min(q.shape[0], out.shape[0]), query_start.data_ptr(), block_tables.data_ptr(), block_table_stride,
+        context_lens.data_ptr(), num_seqs, max_query, max_context, scale, window, sinks, st,
+        flags | (OVERLAP_PREVIOUS if overlap_previous else 0), _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
+
+
+def weights_workspace_bytes(num_seqs: int, max_context: int) -> int:
+    return int(_lib.pkv_weights_workspace_bytes(num_seqs, max_context))
+
+
+def weights_workspace(num_seqs: int, max_context: int, device="cuda") -> torch.Tensor:
+    """A workspace for paged_decode_attention_weights (empty up to max_context = 57344)."""
+    return torch.empty(weights_workspace_bytes(num_seqs, max_context), dtype=torch.uint8, device=device)
+
+
+def paged_decode_attention_weights(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Tensor, block_tables: torch.Tensor,
+                                   block_table_stride: int, context_lens: torch.Tensor, max_context: int, scale: float,
+                                   weight_sums: torch.Tensor, decay: float = 1.0, workspace: torch.Tensor | None = None,
+                                   status: torch.Tensor | None = None, stream=None, overlap_previous: bool = False) -> None:
+    """paged_decode_attention that also adds the weight of every cached token, over the query heads of a K/V head, to
+    weight_sums (float32 [seqs, kv_heads, tokens], any strides with contiguous tokens): sums = decay * sums + weights.
+    out: float32 or bfloat16 [seqs, heads, dim].  overlap_previous: as for paged_window_decode_attention."""
+    where = "pkv_paged_decode_attention_weights"
+    flags, st = _attention_args(where, out, q, (context_lens,), block_tables, status)
+    num_seqs, dev, shape = context_lens.numel(), _current_device(), weight_sums.shape
+    if q.shape[0] < num_seqs or out.shape[0] < num_seqs:
+        raise ValueError(f"{where}: {num_seqs} sequences, q has {q.shape[0]} rows and out {out.shape[0]}")
+    if weight_sums.dtype is not _F32 or weight_sums.get_device() != dev or weight_sums.stride(-1) != 1:
+        _refuse(where, weight_sums, _F32)
+    heads = (pool.num_kv_heads if isinstance(pool, (KVPool, PkvPool)) else 0)
+    if len(shape) != 3 or shape[0] < num_seqs or shape[1] != heads or shape[2] < max_context:
+        raise ValueError(f"{where}: weight_sums is [seqs, kv_heads, max_context tokens or more], got {tuple(shape)}")
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _refuse(where, workspace, "uint8")
+    rc = _lib.pkv_paged_decode_attention_weights(
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q.shape[1],
+        block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_context, scale,
+        weight_sums.data_ptr(), weight_sums.stride(0), weight_sums.stride(1), decay,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, st,
+        flags | (OVERLAP_PREVIOUS if overlap_previous else 0), _stream(stream))
+    if rc:
+        raise PkvError(where, rc)
+
+
+def kv_evict(pool: KVPool | PkvPool, block_tables: torch.Tensor, block_table_stride: int, layer_stride: int,
+             context_lens: torch.Tensor, budgets: torch.Tensor, weight_sums: torch.Tensor,
+             new_weight_sums: torch.Tensor, sinks: int, recent: int, max_context: int, kept: torch.Tensor,
+             new_context_lens: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """Keep min(budgets[s], context_lens[s]) tokens of every sequence, layer and K/V head: the first ``sinks``, the last
+    ``recent`` and those with the largest weight_sums (float32 [seqs, layers, kv_heads, tokens]); their rows move to the front, in
+    order.  new_weight_sums (same shape and strides; weight_sums itself, or other memory) receives the kept sums, then zeros;
+    kept (int32 [seqs, layers, kv_heads, width]) their old positions, new_context_lens the new lengths."""
+    where = "pkv_kv_evict"
+    dev = _current_device()
+    for t in (context_lens, budgets, kept):
+        if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
+            _refuse(where, t, _I32)
+    if block_tables.dtype is not _I32 or block_tables.get_device() != dev or block_tables.stride(-1) != 1:
+        _refuse(where, block_tables, _I32)
+    for t in (weight_sums, new_weight_sums):
+        if t.dtype is not _F32 or t.get_device() != dev or t.stride(-1) != 1:
+            _refuse(where, t, _F32)
+    num_seqs, shape, strides = context_lens.numel(), weight_sums.shape, weight_sums.stride()
+    heads = (pool.num_kv_heads if isinstance(pool, (KVPool, PkvPool)) else 0)
+    if len(shape) != 4 or shape[0] < num_seqs or shape[2] != heads or shape[3] < max_context or \
+            new_weight_sums.shape != shape or new_weight_sums.stride() != strides or budgets.numel() != num_seqs:
+        raise ValueError(f"{where}: weight_sums and new_weight_sums are [seqs, layers, kv_heads, max_context tokens or more] "
+                         f"with the same strides, budgets is [seqs]")
+    layers, width = shape[1], kept.shape[-1]
+    if kept.shape != (num_seqs, layers, heads, width):
+        raise ValueError(f"{where}: kept is [seqs, layers, kv_heads, width], got {tuple(kept.shape)}")
+    new = None
+    if new_context_lens is not None:
+        new = new_context_lens.data_ptr()
+        if new_context_lens.dtype is not _I32 or new_context_lens.get_device() != dev or \
+                not new_context_lens.is_contiguous():
+            _refuse(where, new_context_lens, _I32)
+        if new_context_lens.numel() < num_seqs:
+            raise ValueError(f"{where}: new_context_lens has {new_context_lens.numel()} entries for {num_seqs} sequences")
+    rc = _lib.pkv_kv_evict(
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), block_tables.data_ptr(), block_table_stride,
+        layer_stride, layers, context_lens.data_ptr(), budgets.data_ptr(), num_seqs, max_context, width, sinks, recent,
+        weight_sums.data_ptr(), new_weight_sums.data_ptr(), strides[0], strides[1], strides[2], kept.data_ptr(), width,
+        new, _status_ptr(where, status, dev), _stream(stream))
     if rc:
         raise PkvError(where, rc)
 
