@@ -4,16 +4,19 @@
 // What is kept of ctx tokens with B = min(budget, ctx):  the first a = min(sinks, B), the last r = min(recent, B - a), and of
 // the tokens between them the B - a - r with the largest sums; of equal sums the earlier token.
 //
-// A unit is one (sequence, layer, K/V head); it belongs to one CTA or one cluster of CTAs.
+// A unit is one (sequence, layer, K/V head); it belongs to one CTA or one cluster of CTAs, each of which holds the sums of an
+// equal run of the tokens in shared memory (where they fit).
 //  * Selection: sums are mapped to 32-bit keys of the same order and the key of rank B - a - r is found digit by digit from
-//    the top (8 bits a pass, a histogram in shared memory, summed over the cluster); the passes end early once a digit's
-//    bin is needed whole.  Then every warp counts what its share of the tokens keeps, in order, and writes the kept
-//    positions, ascending.
+//    the top (11, 11 and 10 bits, a histogram in shared memory, added up over the cluster); the passes end once a bin is
+//    needed whole, which is after the second where the sums differ.  A prefix sum over the tokens then gives every kept one
+//    its place, and its position and sum are written there.
 //  * Moving: kept[k] >= k, ascending, so the rows that round i of the move writes (positions i R .. (i + 1) R - 1) lie at or
 //    before everything that later rounds read, and a barrier between a round's loads and its stores is all the order there
-//    has to be.  A row's K and V (2 x 128 B) are moved by 16 threads, 16 bytes each; the next round's places are
-//    looked up while this round's loads are under way.
+//    has to be.  A row's K and V (2 x 128 B) are moved by 16 threads, 16 bytes each, through a ring in shared memory
+//    (cp.async), each thread storing what it loaded itself.
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "host_common.h"
 #include "pkv_device.cuh"
@@ -21,14 +24,13 @@
 namespace pkv {
 namespace {
 
-constexpr int kEvThreads = 256;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
-constexpr int kEvRows = 128;                                  // rows of a round and CTA
-constexpr int kEvChunks = 2 * kRowBytes / 16;                 // 16-byte chunks of a row's K and V: 16
-constexpr int kEvLoads = kEvRows * kEvChunks / kEvThreads;    // chunks a thread has in flight: 8
-constexpr int kDigitBits = 8, kBins = 1 << kDigitBits;
-static_assert(kBins == kEvThreads, "a thread owns one bin");
+constexpr int kEvChunks = 2 * kRowBytes / 16;  // 16-byte chunks of a row's K and V: 16
+constexpr int kEvLook = 512;                   // rows of a CTA whose old positions are fetched at once
+constexpr int kMaxBins = 2048;                 // of a digit of 11 bits, or of one of 8 bits in eight copies
+constexpr int kRun = 4;                        // tokens of a thread in one step of the list
+constexpr int kEvMaxPages = 4096;              // block-table entries that a CTA may hold (16 KiB)
+constexpr size_t kEvMaxSmem = 200 * 1024;      // dynamic shared memory of a CTA at the most
 
 struct EvictArgs {
   uint8_t *k_base, *v_base;
@@ -46,22 +48,39 @@ struct EvictArgs {
   long long kept_stride;
   int32_t *new_lens, *status;
   int cluster;
+  int sums_bytes;   // of the CTA's sums in shared memory, in front of the histograms
+  int pages_bytes;  // of the unit's block-table entries behind the buffer, 0 where they are read from global memory
+  int buffer_bytes;  // rows in flight; before that sums and histograms
 };
 
+template <int kThreads>
 struct EvictSmem {
-  unsigned hist[2][kBins];
-  int warp_part[kEvWarps];
-  int2 warp_count[kEvWarps];          // (kept for certain, equal to the threshold) of a warp's share
-  int2 rank_count[kEvMaxCluster];     // the same of every CTA of the cluster
-  long long from[2][kEvRows], to[2][kEvRows];  // byte offsets of a round's rows in either half of the pool; from < 0: stays
+  unsigned warp_part[2][kThreads / 32];
+  int2 warp_count[kThreads / 32];  // (kept for certain, equal to the threshold) of a warp's tokens
+  int2 rank_count[kEvMaxCluster];  // the same of every CTA of the cluster
+  int from[2][kEvLook];            // old positions of the CTA's next rows
+  unsigned bins[2][256];           // cluster: the CTA's counts of a pass
   unsigned digit, need;
   int whole;
 };
 
 // Order-preserving map of a sum to 32 bits: NaN below everything, the two zeros equal.
 __device__ __forceinline__ unsigned sum_key(float f) {
-  const unsigned u = __float_as_uint(f == 0.f ? 0.f : f);
-  return f != f ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const unsigned u = __float_as_uint(f + 0.f);  // (-0 + 0 = 0)
+  return f != f ? 0u : u ^ (unsigned(int(u) >> 31) | 0x80000000u);
+}
+
+// Asynchronous copies from global to shared memory (one group per commit).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 __device__ __forceinline__ unsigned ld_cluster_u32(uint32_t addr) {
@@ -74,16 +93,25 @@ __device__ __forceinline__ void st_cluster_s2(uint32_t addr, int2 v) {
   asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
-__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a) {
-  __shared__ EvictSmem sm;
+// kRows: rows of a round and CTA; kRing: rounds whose rows are held or on their way; kStaged: sums in shared memory.
+template <int kThreads, int kRows, int kRing, bool kStaged, bool kCluster>
+__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
+  // digits: 11, 11 and 10 bits in a CTA of its own; 8 bits each in a cluster, where every CTA reads every other's bins
+  constexpr int kDigit = kCluster ? 8 : 11, kPasses = kCluster ? 4 : 3, kBins = 1 << kDigit;
+  constexpr int kCopies = kCluster ? 8 : 1;  // of every bin: few bins and many keys of nearly the same exponent
+  constexpr int kWarps = kThreads / 32, kTile = kRun * kThreads, kThreadBins = kBins > kThreads ? kBins / kThreads : 1;
+  constexpr int kRowStep = kThreads / kEvChunks, kLoads = kRows / kRowStep, kRounds = kEvLook / kRows;
+  static_assert(kRounds >= kRing && kLoads >= 1, "");
+  __shared__ EvictSmem<kThreads> sm;
+  extern __shared__ __align__(16) uint8_t buffer[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = a.cluster, rank = int(blockIdx.x) % C;
+  const int C = kCluster ? a.cluster : 1, rank = kCluster ? int(blockIdx.x) % C : 0;
   const unsigned unit = blockIdx.x / unsigned(C);
   const int g = int(unit % kKvHeads), layer = int(unit / kKvHeads % unsigned(a.num_layers));
   const int s = int(unit / kKvHeads / unsigned(a.num_layers));
   griddep_launch_dependents();
   auto barrier = [&]() {
-    if (C > 1)
+    if (kCluster)
       cluster_sync();
     else
       __syncthreads();
@@ -104,8 +132,28 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
   const float *sums = a.sums + at;
   float *new_sums = a.new_sums + at;
   int32_t *kept = a.kept + (((long long)s * a.num_layers + layer) * kKvHeads + g) * a.kept_stride;
+  const int32_t *table = a.block_tables + (long long)s * a.bt_stride + (long long)layer * a.layer_stride;
   const int head = min(a.sinks, B), tail = ctx - min(a.recent, B - head);  // candidates: head <= t < tail
   const int p0 = int((long long)rank * ctx / C), p1 = int((long long)(rank + 1) * ctx / C);  // this CTA's tokens
+
+  // ---- this CTA's sums and the unit's block-table entries into shared memory, where they fit ----
+  const float *own = reinterpret_cast<const float *>(buffer);
+  unsigned *hists = reinterpret_cast<unsigned *>(buffer + a.sums_bytes);
+  const int32_t *pages = table;
+  if (kStaged)
+    for (int t = p0 + tid; t < p1; t += kThreads) cp_async4(smem_addr(own + (t - p0)), sums + t);
+  if (a.pages_bytes > 0) {
+    pages = reinterpret_cast<const int32_t *>(buffer + a.buffer_bytes);
+    const int blocks = (ctx + kPageTokens - 1) / kPageTokens;
+    for (int i = tid; i < blocks; i += kThreads) cp_async4(smem_addr(pages + i), table + i);
+  }
+  cp_async_commit();
+  const int bin0 = tid * kThreadBins;
+  const bool has_bins = kBins >= kThreads || tid < kBins;
+  for (int i = tid; i < kBins * kCopies; i += kThreads) hists[i] = 0u;
+  cp_async_wait<0>();
+  __syncthreads();
+  auto sum_at = [&](int t) { return kStaged ? own[t - p0] : sums[t]; };
 
   // ---- threshold: kept are the candidates whose key is above T, and the first `ties` whose key is T ----
   unsigned T = 0xffffffffu, ties = 0;
@@ -116,48 +164,70 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
   } else if (need > 0) {
     const int c0 = max(p0, head), c1 = min(p1, tail);
     unsigned prefix = 0;
-    sm.hist[0][tid] = 0;
-    __syncthreads();
 #pragma unroll 1
-    for (int pass = 0; pass < 32 / kDigitBits; ++pass) {
-      const int shift = 32 - kDigitBits * (pass + 1);
-      unsigned *hist = sm.hist[pass & 1];
-      for (int t0 = c0 + warp * 32; t0 < c1; t0 += kEvThreads) {
-        const int t = t0 + lane;
-        bool in = t < c1;
-        const unsigned key = in ? sum_key(sums[t]) : 0u;
-        in = in && (pass == 0 || key >> (shift + kDigitBits) == prefix);
-        const unsigned bin = in ? key >> shift & (kBins - 1) : kBins;
-        const unsigned same = __match_any_sync(0xffffffffu, bin);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], unsigned(__popc(same)));
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int shift = max(0, 32 - kDigit * (pass + 1)), bits = min(kDigit, 32 - kDigit * pass);
+#pragma unroll 4
+      for (int t = c0 + tid; t < c1; t += kThreads) {
+        const unsigned key = sum_key(sum_at(t));
+        if (pass == 0 || key >> (shift + bits) == prefix)
+          atomicAdd(&hists[(key >> shift & ((1u << bits) - 1u)) * kCopies + lane % kCopies], 1u);
       }
-      barrier();
-      sm.hist[(pass & 1) ^ 1][tid] = 0;  // the next pass's: every CTA has read what the pass before left there
-      unsigned mine = 0;                 // of bin tid, over the cluster
-      if (C > 1) {
-        const uint32_t addr = smem_addr(&hist[tid]);
-        for (int r = 0; r < C; ++r) mine += ld_cluster_u32(cluster_map(addr, uint32_t(r)));
-      } else {
-        mine = hist[tid];
+      __syncthreads();
+      // this thread's bins over the cluster, and the keys in them and in all bins above; the next pass starts from 0
+      unsigned c[kThreadBins] = {};
+      if (has_bins) {
+#pragma unroll
+        for (int i = 0; i < kThreadBins * kCopies; ++i) {
+          c[i / kCopies] += hists[bin0 * kCopies + i];
+          hists[bin0 * kCopies + i] = 0u;
+        }
       }
-      // keys in the bins above this one
+      if (kCluster) {
+        if (has_bins) sm.bins[pass & 1][tid] = c[0];
+        cluster_sync();  // (and what the pass before last left in bins has been read)
+        if (has_bins) {
+          unsigned part[kEvMaxCluster];  // all on their way before the first is used, and no two CTAs at the same one first
+#pragma unroll
+          for (int r = 0; r < kEvMaxCluster; ++r)
+            part[r] = r < C ? ld_cluster_u32(cluster_map(smem_addr(&sm.bins[pass & 1][tid]), uint32_t((r + rank) % C))) : 0u;
+          c[0] = 0;
+#pragma unroll
+          for (int r = 0; r < kEvMaxCluster; ++r) c[0] += part[r];
+        }
+      }
+      unsigned mine = 0;
+#pragma unroll
+      for (int i = 0; i < kThreadBins; ++i) mine += c[i];
       unsigned up = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned y = __shfl_down_sync(0xffffffffu, up, o);
         if (lane + o < 32) up += y;
       }
-      if (lane == 0) sm.warp_part[warp] = int(up);
+      if (lane == 0) sm.warp_part[pass & 1][warp] = up;
       __syncthreads();
-      for (int w = warp + 1; w < kEvWarps; ++w) up += unsigned(sm.warp_part[w]);
-      const unsigned above = up - mine;
-      if (above < need && need <= up) {
-        sm.digit = unsigned(tid);
-        sm.need = need - above;
-        sm.whole = need == up;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const unsigned x = sm.warp_part[pass & 1][w];
+        if (w > warp) up += x;
+      }
+      if (up - mine < need && need <= up) {  // the bin of the key of rank `need` is one of this thread's
+        unsigned above = up - mine;
+        bool found = false;
+#pragma unroll
+        for (int i = kThreadBins - 1; i >= 0; --i) {
+          if (!found && above + c[i] >= need) {
+            found = true;
+            sm.digit = unsigned(bin0 + i);
+            sm.need = need - above;
+            sm.whole = need == above + c[i];
+          }
+          above += c[i];
+        }
       }
       __syncthreads();
-      prefix = prefix << kDigitBits | sm.digit;
+      prefix = prefix << bits | sm.digit;
       need = sm.need;
       if (sm.whole) {  // every key with this prefix is kept
         T = (prefix << shift) - 1u;
@@ -169,105 +239,208 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
     }
   }
 
-  // ---- kept positions, ascending: a warp's share is a run of tokens ----
-  const int share = (p1 - p0 + kEvWarps - 1) / kEvWarps;
-  const int w0 = min(p0 + warp * share, p1), w1 = min(w0 + share, p1);
-  auto classify = [&](int t, bool &sure, bool &equal) {
-    const bool in = t < w1, fixed = in && (t < head || t >= tail);
-    const unsigned key = in && !fixed ? sum_key(sums[t]) : 0u;
-    sure = fixed || (in && key > T);
+  // ---- kept positions, ascending ----
+  auto classify = [&](int t, float v, bool &sure, bool &equal) {
+    const bool in = t < p1, fixed = unsigned(t - head) >= unsigned(tail - head);
+    const unsigned key = sum_key(v);
+    sure = in && (fixed || key > T);
     equal = in && !fixed && key == T;
   };
-  int2 count = make_int2(0, 0);
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    bool sure, equal;
-    classify(t0 + lane, sure, equal);
-    count.x += __popc(__ballot_sync(0xffffffffu, sure));
-    count.y += __popc(__ballot_sync(0xffffffffu, equal));
-  }
-  if (lane == 0) sm.warp_count[warp] = count;
-  __syncthreads();
-  if (C > 1) {
+  int2 before = make_int2(0, 0);  // (kept for certain, equal to T) in front of this CTA's tokens
+  if (kCluster) {
+    int2 count = make_int2(0, 0);
+#pragma unroll 4
+    for (int t = p0 + tid; t < p1; t += kThreads) {
+      bool sure, equal;
+      classify(t, sum_at(t), sure, equal);
+      count.x += sure;
+      count.y += equal;
+    }
+    count.x = __reduce_add_sync(0xffffffffu, count.x);
+    count.y = __reduce_add_sync(0xffffffffu, count.y);
+    if (lane == 0) sm.warp_count[warp] = count;
+    __syncthreads();
     if (tid < C) {
       int2 all = make_int2(0, 0);
-      for (int w = 0; w < kEvWarps; ++w) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
         all.x += sm.warp_count[w].x;
         all.y += sm.warp_count[w].y;
       }
       st_cluster_s2(cluster_map(smem_addr(&sm.rank_count[rank]), uint32_t(tid)), all);
     }
     cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      before.x += sm.rank_count[r].x;
+      before.y += sm.rank_count[r].y;
+    }
   }
-  int2 before = make_int2(0, 0);
-  for (int r = 0; r < rank; ++r) {
-    before.x += sm.rank_count[r].x;
-    before.y += sm.rank_count[r].y;
-  }
-  for (int w = 0; w < warp; ++w) {
-    before.x += sm.warp_count[w].x;
-    before.y += sm.warp_count[w].y;
-  }
-  const unsigned below = (1u << lane) - 1u;
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    bool sure, equal;
-    classify(t0 + lane, sure, equal);
-    const unsigned ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, equal);
-    const int eq = before.y + __popc(me & below);
-    if (sure || (equal && unsigned(eq) < ties))
-      __stcg(kept + before.x + __popc(ms & below) + min(unsigned(eq), ties), t0 + lane);
-    before.x += __popc(ms);
-    before.y += __popc(me);
-  }
-  barrier();  // the list is complete, and nobody reads sums for the selection any more
-
-  // ---- the rows move ----
-  const int32_t *table = a.block_tables + (long long)s * a.bt_stride + (long long)layer * a.layer_stride;
-  const long long in_page = (long long)g * kPageTokens * kRowBytes;
-  const int rounds = (B + kEvRows * C - 1) / (kEvRows * C);
-  float w_now = 0.f, w_next = 0.f;
-  auto look_up = [&](int i, float &w) {  // places of round i's rows, by threads 0 .. kEvRows - 1
-    const int k = (i * C + rank) * kEvRows + tid;
-    long long from = -1, to = -1;
-    if (k < B) {
-      const int src = __ldcg(kept + k);
-      w = sums[src];
-      if (src != k) {
-        const int sp = __ldg(table + src / kPageTokens), dp = __ldg(table + k / kPageTokens);
-        if (unsigned(sp) >= unsigned(a.num_pages) || unsigned(dp) >= unsigned(a.num_pages)) {
-          report(a.status, PKV_DEV_BAD_PAGE);
-        } else {
-          from = sp * a.page_stride + in_page + (src % kPageTokens) * kRowBytes;
-          to = dp * a.page_stride + in_page + (k % kPageTokens) * kRowBytes;
+  // (sums held here are written over from now on: the barriers above followed the last CTA's copy of them)
+#pragma unroll 1
+  for (int base = p0; base < p1; base += kTile) {
+    const int t = base + tid * kRun;
+    float v[kRun];
+    if (kStaged) {  // (the buffer holds whole tiles; what lies behind p1 is not looked at)
+      *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(own + (t - p0));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) v[j] = t + j < p1 ? sums[t + j] : 0.f;
+    }
+    unsigned sure = 0, equal = 0;  // bit j: token t + j
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      bool x, y;
+      classify(t + j, v[j], x, y);
+      sure |= unsigned(x) << j;
+      equal |= unsigned(y) << j;
+    }
+    const unsigned mine = unsigned(__popc(sure)) | unsigned(__popc(equal)) << 16;
+    unsigned upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) sm.warp_part[0][warp] = upto;
+    __syncthreads();
+    unsigned all = 0, front = upto - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const unsigned x = sm.warp_part[0][w];
+      if (w < warp) front += x;
+      all += x;
+    }
+    unsigned x = unsigned(before.x) + (front & 0xffffu), y = unsigned(before.y) + (front >> 16);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const bool is = sure >> j & 1, eq = equal >> j & 1;
+      if (is || (eq && y < ties)) {
+        const unsigned k = x + min(y, ties);
+        if (k < unsigned(B)) {  // (always, unless somebody else writes the sums meanwhile)
+          __stcg(kept + k, t + j);
+          if (kStaged) new_sums[k] = v[j];
         }
       }
+      x += is;
+      y += eq;
     }
-    sm.from[i & 1][tid] = from;
-    sm.to[i & 1][tid] = to;
+    before.x += int(all & 0xffffu);
+    before.y += int(all >> 16);
+    __syncthreads();  // the warps' counts have been read
+  }
+  barrier();  // the list is complete, and nobody reads sums for the selection any more
+  if (!kStaged) {
+    // the kept sums move as the rows do: a barrier between a round's loads and its stores
+    for (int k0 = 0; k0 < B; k0 += C * kThreads) {
+      const int k = k0 + rank * kThreads + tid;
+      const float v = k < B ? sums[min(unsigned(__ldcg(kept + k)), unsigned(ctx - 1))] : 0.f;
+      barrier();
+      if (k < B) new_sums[k] = v;
+    }
+    barrier();
+  }
+
+  // ---- the rows move ----
+  const int rounds = (B + kRows * C - 1) / (kRows * C);
+  auto row = [&](int i, int r) { return (i * C + rank) * kRows + r; };  // row r of this CTA in round i
+  auto look_up = [&](int j) {  // old positions of the rows of rounds j kRounds .. (j + 1) kRounds - 1
+#pragma unroll
+    for (int r = tid; r < kEvLook; r += kThreads) {
+      const int k = row(j * kRounds + r / kRows, r % kRows);
+      int src = k < B ? __ldcg(kept + k) : k;
+      if (unsigned(src) >= unsigned(ctx)) src = k;
+      sm.from[j & 1][r] = src;  // (a row that stays where it is does not move)
+    }
   };
-  uint8_t *half = ((tid & 8) ? a.v_base : a.k_base) + (tid & 7) * 16;
-  if (tid < kEvRows) look_up(0, w_now);
-  __syncthreads();
+  // a thread moves the same 16-byte chunk of every kRowStep-th row
+  uint8_t *half = ((tid & 8) ? a.v_base : a.k_base) + (long long)g * kPageTokens * kRowBytes + (tid & 7) * 16;
+  const int r0 = tid / kEvChunks;
+  auto moves = [&](int i, int r, int &sp, int &dp, int &src, int &k) {
+    k = row(i, r);
+    src = sm.from[i / kRounds & 1][i % kRounds * kRows + r];
+    if (src == k) return false;
+    sp = pages[src / kPageTokens];
+    dp = pages[k / kPageTokens];
+    return unsigned(sp) < unsigned(a.num_pages) && unsigned(dp) < unsigned(a.num_pages);
+  };
+  auto load = [&](int i) {
+    if (i < rounds) {
+      if (i % kRounds == 0) {
+        look_up(i / kRounds);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        int sp, dp, src, k;
+        if (moves(i, j * kRowStep + r0, sp, dp, src, k))
+          cp_async16(smem_addr(buffer) + (((i % kRing) * kLoads + j) * kThreads + tid) * 16,
+                     half + sp * a.page_stride + (src % kPageTokens) * kRowBytes);
+        else if (src != k && tid % kEvChunks == 0)
+          report(a.status, PKV_DEV_BAD_PAGE);
+      }
+    }
+    cp_async_commit();
+  };
+  auto store = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      int sp, dp, src, k;
+      if (moves(i, j * kRowStep + r0, sp, dp, src, k))
+        *reinterpret_cast<uint4 *>(half + dp * a.page_stride + (k % kPageTokens) * kRowBytes) =
+            *reinterpret_cast<const uint4 *>(buffer + (((i % kRing) * kLoads + j) * kThreads + tid) * 16);
+    }
+  };
+  // Round i's stores come a step after its loads have landed in every CTA of the cluster, so that the barrier's latency
+  // passes under other rounds' copies.  (What the barrier orders is loads that have landed before stores that follow: it
+  // need not publish the stores before it.)
+#pragma unroll 1
+  for (int i = 0; i < kRing - 1; ++i) load(i);
+  for (int t = B + rank * kThreads + tid; t < ctx; t += C * kThreads) new_sums[t] = 0.f;  // (under the first copies)
 #pragma unroll 1
   for (int i = 0; i < rounds; ++i) {
-    uint4 x[kEvLoads];
-#pragma unroll
-    for (int j = 0; j < kEvLoads; ++j) {
-      const long long from = sm.from[i & 1][j * (kEvThreads / kEvChunks) + tid / kEvChunks];
-      if (from >= 0) x[j] = *reinterpret_cast<const uint4 *>(half + from);
+    cp_async_wait<kRing - 2>();
+    if (kCluster) {
+      __syncwarp();
+      if (i > 0) cluster_wait();
+      cluster_arrive_relaxed();
+    } else {
+      __syncthreads();
     }
-    if (i + 1 < rounds && tid < kEvRows) look_up(i + 1, w_next);
-    barrier();  // every row of the round, and every sum up to the next round's, is in registers
-#pragma unroll
-    for (int j = 0; j < kEvLoads; ++j) {
-      const int r = j * (kEvThreads / kEvChunks) + tid / kEvChunks;
-      if (sm.from[i & 1][r] >= 0) *reinterpret_cast<uint4 *>(half + sm.to[i & 1][r]) = x[j];
-    }
-    const int k = (i * C + rank) * kEvRows + tid;
-    if (tid < kEvRows && k < B) new_sums[k] = w_now;
-    w_now = w_next;
-    __syncthreads();  // the places have been read
+    if (i > 0) store(i - 1);
+    load(i + kRing - 1);
   }
-  for (int t = B + rank * kEvThreads + tid; t < ctx; t += C * kEvThreads) new_sums[t] = 0.f;
+  if (rounds > 0) {
+    __syncwarp();
+    if (kCluster) cluster_wait();
+    store(rounds - 1);
+  }
+}
+
+using EvictKernel = void (*)(EvictArgs);
+constexpr EvictKernel kEvictMany = kv_evict_kernel<256, 32, 4, true, false>;
+constexpr EvictKernel kEvictFew = kv_evict_kernel<512, 64, 6, true, false>;
+constexpr EvictKernel kEvictCluster = kv_evict_kernel<512, 64, 5, true, true>;
+constexpr EvictKernel kEvictLong = kv_evict_kernel<512, 64, 5, false, true>;
+
+// Shared-memory limits of the kernels on the current device.
+int setup_evict_attributes() {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return PKV_ERR_CUDA;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev]) {
+    for (EvictKernel kernel : {kEvictMany, kEvictFew, kEvictCluster, kEvictLong})
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kEvMaxSmem)) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+      }
+    done[dev] = true;
+  }
+  return PKV_OK;
 }
 
 // Whether two ranges of bytes share one.
@@ -289,7 +462,7 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   if (rc != PKV_OK) return rc;
   if (num_seqs < 0 || num_layers < 1 || max_context < 0 || max_context > (1 << 30) || max_budget < 0 || sinks < 0 ||
       recent < 0 || block_table_stride < 0 || layer_stride < 0 || kept_stride < max_budget ||
-      sums_head_stride < max_context || sums_layer_stride < 0 || sums_seq_stride < 0 ||
+      pool->num_pages > (1 << 27) || sums_head_stride < max_context || sums_layer_stride < 0 || sums_seq_stride < 0 ||
       (long long)num_seqs * num_layers > 0x7fffffffLL / (pkv::kKvHeads * pkv::kEvMaxCluster))
     return PKV_ERR_SHAPE;
   // a row of sums belongs to one (sequence, layer, head)
@@ -348,14 +521,35 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   a.new_lens = new_context_lens;
   a.status = device_status;
   const long long units = (long long)num_seqs * num_layers * pkv::kKvHeads;
-  const int sms = pkv::device_sm_count();
-  const long long slots = 4ll * (sms > 0 ? sms : 148);
+  int sms = pkv::device_sm_count();
+  if (sms <= 0) sms = 148;
   a.cluster = 1;
-  while (a.cluster < pkv::kEvMaxCluster && units * a.cluster * 2 <= slots && max_context >= a.cluster * 2 * pkv::kEvRows)
-    a.cluster *= 2;
+  while (a.cluster < pkv::kEvMaxCluster && units * a.cluster * 2 <= sms && max_context >= a.cluster * 2048) a.cluster *= 2;
+  const int pages = (max_context + pkv::kPageTokens - 1) / pkv::kPageTokens;
+  a.pages_bytes = pages <= pkv::kEvMaxPages ? (pages * 4 + 15) / 16 * 16 : 0;
+  pkv::EvictKernel kernel = a.cluster > 1 ? pkv::kEvictCluster : units > 2 * sms ? pkv::kEvictMany : pkv::kEvictFew;
+  int threads = 512, ring = a.cluster > 1 ? 5 * 64 : 6 * 64;
+  if (a.cluster == 1 && units > 2 * sms) {
+    threads = 256;
+    ring = 4 * 32;
+  }
+  const size_t hists = pkv::kMaxBins * sizeof(unsigned), tile = size_t(threads) * pkv::kRun;
+  size_t buffer = size_t(ring) * 2 * pkv::kRowBytes;
+  size_t sums_bytes = ((size_t(max_context) + a.cluster - 1) / a.cluster + tile - 1) / tile * tile * 4;
+  if (sums_bytes + hists + a.pages_bytes > pkv::kEvMaxSmem) {
+    kernel = pkv::kEvictLong;
+    threads = 512;
+    buffer = size_t(5 * 64) * 2 * pkv::kRowBytes;
+    sums_bytes = 0;
+  }
+  if (sums_bytes + hists > buffer) buffer = sums_bytes + hists;
+  a.sums_bytes = int(sums_bytes);
+  a.buffer_bytes = int(buffer);
+  if (pkv::setup_evict_attributes() != PKV_OK) return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(units * a.cluster));
-  cfg.blockDim = dim3(pkv::kEvThreads);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = buffer + a.pages_bytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -364,7 +558,7 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, pkv::kv_evict_kernel, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
     cudaGetLastError();
     return PKV_ERR_LAUNCH;
   }

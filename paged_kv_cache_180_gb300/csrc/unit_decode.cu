@@ -37,13 +37,13 @@ namespace {
 
 constexpr int kUnitWarps = 8;
 constexpr int kUnitThreads = kUnitWarps * 32;
-constexpr int kUnitStages = 3;                               // pages a warp has in flight
+constexpr int kDeepRing = 3, kShallowRing = 2;               // pages a warp has in flight
 constexpr int kMaxCluster = 8;                               // CTAs that share a unit at the most
 constexpr int kBoxBytes = kPageTokens * kRowBytes;           // one head's K (or V) rows of a page: 2 KiB
 constexpr int kUnitOut = kGroup * kHeadDim;                  // output values of a unit: 256
 constexpr int kScorePage = kPageTokens * int(sizeof(float4));  // scores of a page: 256 B
 constexpr int kChipPages = 448;                              // pages of a CTA whose scores fit into shared memory
-constexpr int kMinPages = kUnitWarps;                        // pages a CTA of a cluster gets at the least
+constexpr int kMinPages = 4;                                 // pages a CTA of a cluster gets at the least
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kUnitOut == kUnitThreads, "a thread owns one output value");
 
@@ -68,14 +68,15 @@ struct UnitArgs {
   int32_t *status;
 };
 
+template <int kStages>
 struct __align__(1024) UnitSmem {
-  uint8_t kv[kUnitWarps][kUnitStages][2][kBoxBytes];  // 128-byte swizzled
+  uint8_t kv[kUnitWarps][kStages][2][kBoxBytes];  // 128-byte swizzled
   float acc[kUnitWarps][kGroup][kHeadDim];            // the warps' states
   float2 ml[kUnitWarps][kGroup];                      // (maximum in log2 units, sum)
   float recv_acc[kUnitOut];                           // this CTA's slice of the outputs from every CTA of the cluster
   float2 recv_ml[kMaxCluster][kGroup];
   float2 fin[kGroup];                                 // (maximum, 1 / sum) of the unit
-  uint64_t full[kUnitWarps][kUnitStages];
+  uint64_t full[kUnitWarps][kStages];
 };
 
 // D = A B with a zero accumulator.
@@ -95,10 +96,11 @@ __device__ __forceinline__ void st_cluster_f1(uint32_t addr, float v) {
 // A maximum that exponents may be taken against: -infinity (no key, or none of finite score) becomes 0.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
-template <bool kWeights>
+template <bool kWeights, int kStages>
 __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __grid_constant__ UnitArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  UnitSmem &sm = *reinterpret_cast<UnitSmem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  using Smem = UnitSmem<kStages>;
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = a.cluster, rank = int(blockIdx.x) % C;
   const unsigned unit = blockIdx.x / unsigned(C);
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
     }
   }
   if (lane == 0) {
-    for (int i = 0; i < kUnitStages; ++i) mbar_init(&sm.full[warp][i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[warp][i], 1);
     mbar_init_fence();
     if (warp == 0) {
       prefetch_tensormap(&a.tmap_k);
@@ -182,14 +184,14 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
     }
     __syncwarp();
     ++issued;
-    if (++ist == kUnitStages) ist = 0;
+    if (++ist == kStages) ist = 0;
   };
-  for (int i = 0; i < kUnitStages && i < cnt; ++i) issue();
+  for (int i = 0; i < kStages && i < cnt; ++i) issue();
 
   float4 *sc = nullptr;  // scores of this CTA's pages, [page - pa][token], one value for each of the four query heads
   if (kWeights)
     sc = a.scores != nullptr ? a.scores + ((long long)unit * a.score_pages + pa) * kPageTokens
-                             : reinterpret_cast<float4 *>(reinterpret_cast<uint8_t *>(&sm) + sizeof(UnitSmem));
+                             : reinterpret_cast<float4 *>(reinterpret_cast<uint8_t *>(&sm) + sizeof(Smem));
 
   const int quad = lane & 3, hrow = lane >> 2;
   const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: lane i addresses row i % 8 of matrix i / 8
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
       // give up: what is in flight lands (bounded again) before the CTA may end
       report(a.status, PKV_DEV_TIMEOUT);
       if (lane == 0)
-        for (int j = i; j < issued; ++j) mbar_wait(&sm.full[warp][j % kUnitStages], uint32_t(j / kUnitStages) & 1);
+        for (int j = i; j < issued; ++j) mbar_wait(&sm.full[warp][j % kStages], uint32_t(j / kStages) & 1);
       __syncwarp();
       break;
     }
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
     }
     __syncwarp();  // the stage has been read by every lane
     if (issued < cnt) issue();
-    if (++st == kUnitStages) {
+    if (++st == kStages) {
       st = 0;
       parity ^= 1;
     }
@@ -368,7 +370,9 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
   }
 }
 
-constexpr size_t kUnitSmemBytes = sizeof(UnitSmem) + 1024;
+template <int kStages>
+constexpr size_t unit_smem_bytes() { return sizeof(UnitSmem<kStages>) + 1024; }
+constexpr size_t kSmemPerSm = 227 * 1024, kSmemReserved = 1024;  // of an SM's shared memory, and what a CTA takes besides its own
 
 // Shared-memory limits of the kernels on the current device.
 int setup_unit_attributes() {
@@ -381,13 +385,17 @@ int setup_unit_attributes() {
   }
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(unit_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kUnitSmemBytes)) != cudaSuccess ||
-        cudaFuncSetAttribute(unit_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kUnitSmemBytes) + kChipPages * kScorePage) != cudaSuccess) {
-      cudaGetLastError();
-      return PKV_ERR_CUDA;
-    }
+    const struct {
+      void (*kernel)(UnitArgs);
+      size_t bytes;
+    } all[] = {{unit_decode_kernel<false, kDeepRing>, unit_smem_bytes<kDeepRing>()},
+               {unit_decode_kernel<true, kDeepRing>, unit_smem_bytes<kDeepRing>() + kChipPages * kScorePage},
+               {unit_decode_kernel<true, kShallowRing>, unit_smem_bytes<kShallowRing>() + kChipPages * kScorePage}};
+    for (const auto &k : all)
+      if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.bytes)) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+      }
     done[dev] = true;
   }
   return PKV_OK;
@@ -440,14 +448,22 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
   a.scores = nullptr;
   a.score_pages = pages;
   a.status = device_status;
-  size_t smem = kUnitSmemBytes;
+  void (*kernel)(UnitArgs) = unit_decode_kernel<false, kDeepRing>;
+  size_t smem = unit_smem_bytes<kDeepRing>();
   if (sums != nullptr) {
+    kernel = unit_decode_kernel<true, kDeepRing>;
     while (a.cluster < kMaxCluster && (pages + a.cluster - 1) / a.cluster > kChipPages) a.cluster *= 2;
     const long long share = (pages + a.cluster - 1) / a.cluster;
-    if (share <= kChipPages)
-      smem += size_t(share) * kScorePage;
-    else
+    if (share <= kChipPages) {
+      const size_t scores = size_t(share) * kScorePage;
+      if (smem + scores > kSmemPerSm / 2 - kSmemReserved && unit_smem_bytes<kShallowRing>() + scores <= kSmemPerSm / 2 - kSmemReserved) {
+        kernel = unit_decode_kernel<true, kShallowRing>;
+        smem = unit_smem_bytes<kShallowRing>();
+      }
+      smem += scores;
+    } else {
       a.scores = static_cast<float4 *>(workspace);
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(units * a.cluster));
@@ -470,8 +486,7 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
   }
   cfg.attrs = attr;
   cfg.numAttrs = unsigned(n_attr);
-  const cudaError_t err = sums != nullptr ? cudaLaunchKernelEx(&cfg, unit_decode_kernel<true>, a)
-                                          : cudaLaunchKernelEx(&cfg, unit_decode_kernel<false>, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err != cudaSuccess) {
     cudaGetLastError();
     return PKV_ERR_LAUNCH;
