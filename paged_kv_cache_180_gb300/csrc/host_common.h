@@ -40,4 +40,9 @@ int pool_tensor_maps(const pkv_pool *pool, int box_rows, CUtensorMap *tk, CUtens
 int query_tensor_map(const void *q, int rows, int num_q_heads, int head_dim, int box_heads, int box_rows,
                      CUtensorMap *map);
 
+// TMA tensor map of outputs out[rows][num_q_heads][head_dim] (fp32 or bf16) for boxes of 128 bytes x box_heads x
+// box_rows, 128-byte swizzled; cached.  PKV_OK or an error.
+int output_tensor_map(const void *out, int rows, int num_q_heads, int head_dim, bool bf16, int box_heads, int box_rows,
+                      CUtensorMap *map);
+
 }  // namespace pkv

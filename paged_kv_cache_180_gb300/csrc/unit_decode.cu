@@ -105,8 +105,6 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
   const int C = a.cluster, rank = int(blockIdx.x) % C;
   const unsigned unit = blockIdx.x / unsigned(C);
   const int s = int(unit / kKvHeads), g = int(unit % kKvHeads);
-  griddep_launch_dependents();
-
   const int ctx = __ldg(a.context_lens + s);
   const long long out_at = ((long long)s * kQHeads + g * kGroup) * kHeadDim;
   auto store = [&](int i, float v) {
@@ -117,6 +115,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
   };
   if (ctx <= 0 || ctx > a.max_context) {
     griddep_wait();
+    griddep_launch_dependents();
     if (rank == 0) {
       if (ctx != 0 && g == 0 && tid == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
       store(tid, 0.f);
@@ -160,6 +159,8 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
   // no CTA writes into another's shared memory before that one has started: this arrival, waited for before the push
   if (C > 1) cluster_arrive_relaxed();
   griddep_wait();  // pages and sums may have been written by the kernel before this one
+  // (not before the wait: what the next kernel reads at once may come from a kernel before this one)
+  griddep_launch_dependents();
 
   const uint64_t policy = policy_evict_first();
   int issued = 0, ist = 0;  // pages issued, stage of the next one

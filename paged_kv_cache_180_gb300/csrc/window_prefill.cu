@@ -5,18 +5,27 @@
 //   A = { t <= p : t < sinks or t > p - window },  p = context_lens[s] - n_s + (i - query_start[s]).
 //
 // tcgen05 tensor cores, accumulators in tensor memory:
-//  * Tile: 32 query tokens of a sequence against one K/V head g; its 128 rows (row = 4 * token + head in group) share every
-//    K/V row loaded.  The pages its rows see (the sinks' and those from the first row's window on; none between)
-//    are numbered without the gap and go four to a block of 64 keys, so that the sinks cost one page and not a block.
-//    The grid is persistent, two CTAs to an SM; the tiles are dealt in a snake over the latest-first list.
-//  * S = Q K^T into one of two TMEM buffers; P goes back over its own S and is the TMEM A operand of O += P V, with
-//    V followed by 16 columns of a constant atom whose first is 1, so that O's column 64 adds up the row sums.  With fp32
-//    output P has two bf16 terms (16 bits), with bf16 output one.
-//  * Warps 0-3 own a row a thread (softmax, division, store), warp 4 loads by TMA, warp 5 issues the MMAs.
-//  * A row's reference maximum moves only when a block's maximum exceeds it by more than 8 in the exponent.
+//  * An item is 64 query tokens of a sequence against one K/V head: two tiles of 32 tokens, 128 rows each (row = 4 * token +
+//    head in group).  Both tiles use each K/V block that is loaded, or one of them where the other sees nothing of it.  The
+//    pages that the item's rows see (the sinks' and those from the first row's window on; none between) are numbered without
+//    the gap and go eight to a block of 128 keys, so that the sinks cost a page and not a block.
+//    Where there are fewer items than half the SMs, they have one tile.
+//  * The grid is persistent, one CTA to an SM; the items that there are (a prefix sum over the sequences' lengths, made by
+//    every CTA) are dealt in a snake, each sequence's latest first.
+//  * Q_t stays in tensor memory (its rows' own threads put it there).  A block's S_t = Q_t K^T is computed in two halves of 64
+//    keys, into TMEM buffers of their own; P goes back over its half and is the TMEM A operand of O_t += P V.  So while the
+//    softmax works on one half the tensor core has P V of the other and its next S, and shared memory feeds it K and V
+//    alone.  With fp32 output P has two bf16 terms (16 bits), with bf16 output one.  Row sums are added up in registers.
+//  * The exponents of a row refer to the maximum of the scores of its tile's first block, seen by the row or not, and stay
+//    there: weights are floats, so they may well be far from 1.  A row whose sum leaves [2^-90, 2^112] is computed again.
+//  * The tensor core truncates what it adds up.  With fp32 output O is therefore taken out after every 1024 keys and added
+//    to the row in `out`, whose last value is the quotient.
+//  * A warp's finished rows go through shared memory and a TMA store: stored by their threads, 256 bytes apart, they took 3400
+//    cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored directly.)
 //  * Keys that a row does not see get weight 0.  Their V meets that weight in the product all the same, so a NaN or an
 //    infinity in it would reach rows that do not see it: a row whose output is not finite is computed again at the end,
 //    from the keys that it sees alone, by its own thread (slowly).
+//  * Warps 0-3 and 4-7 own a row of tile 0 and 1 a thread.  Warp 8 loads by TMA; warps 9 and 10 issue the MMAs of a tile each.
 //  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing work, waits
 //    (bounded) for what is in flight, frees its tensor memory and exits.
 #include <cuda.h>
@@ -31,30 +40,42 @@
 namespace pkv {
 namespace {
 
-constexpr int kWpTok = 32;                             // query tokens per tile
+constexpr int kWpTok = 32;                             // query tokens of a tile
+constexpr int kWpTiles = 2;                            // tiles of an item
+constexpr int kWpItemTok = kWpTok * kWpTiles;
 constexpr int kWpRows = kWpTok * kGroup;               // M = 128
-constexpr int kWpKeys = 64;                            // keys per block
+constexpr int kWpKeys = 128;                           // keys of a block
 constexpr int kWpPagesPerBlock = kWpKeys / kPageTokens;
-constexpr int kWpStages = 4;                           // K/V blocks in flight
-constexpr int kWpThreads = 192;                        // warps 0-3 softmax, 4 loads, 5 MMA
-constexpr int kWpCtasPerSm = 2;
-constexpr int kWpMaxTiles = 64;                        // tiles one CTA walks (its tile table in shared memory)
+constexpr unsigned kWpStages = 4;                      // K/V blocks in flight
+constexpr int kWpThreads = kWpTiles * kWpRows + 96;    // softmax groups, loader, issuers
+constexpr int kWpLoader = kWpTiles * 4, kWpIssuers = kWpLoader + 1;  // warps
+constexpr int kWpHalf = kWpKeys / 2;                   // keys of an S buffer
+constexpr int kWpMaxItems = 64;                        // items a CTA walks (its table in shared memory)
 constexpr int kWpBox = kPageTokens * kRowBytes;        // one head's rows of one page: 2 KiB
-constexpr int kWpTileBytes = kWpKeys * kRowBytes;      // K (or V) of one block: 8 KiB
-constexpr uint32_t kWpTmemCols = 256;
-constexpr uint32_t kColS = 0;                          // S buffers at columns 0 and 64
-constexpr uint32_t kColO = 128;                        // O: columns 128 .. 191, row sum l at 192 (193 .. 207 zero)
-constexpr int kPvN = kHeadDim + 16;                    // P V's N: V's 64 columns and 16 of the ones atom
+constexpr int kWpTileBytes = kWpKeys * kRowBytes;      // K (or V) of one block: 16 KiB
+constexpr int kWpRun = 8;                              // blocks that O adds up at once with fp32 output
+constexpr uint32_t kWpTmemCols = 512;
+// columns of S_0, S_1 (128 each), of O_0, O_1 (64) and of Q_0, Q_1 (32)
+constexpr uint32_t kColS = 0, kColO = kWpTiles * kWpKeys, kColQ = kColO + kWpTiles * kHeadDim;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleLog2 = 8.f;                    // move a row's reference max when exceeded by more
+constexpr float kSumMin = 8.077935669463161e-28f, kSumMax = 5.192296858534828e33f;  // 2^-90, 2^112
 
-constexpr uint32_t kIdescS = idesc_bf16(kWpRows, kWpKeys, false);   // B = K rows (K-major)
-constexpr uint32_t kIdescPV = idesc_bf16(kWpRows, kPvN, true);  // B = [V | ones] (MN-major)
+constexpr uint32_t kIdescS = idesc_bf16(kWpRows, kWpHalf, false);   // B = K rows (K-major)
+constexpr uint32_t kIdescPV = idesc_bf16(kWpRows, kHeadDim, true);  // B = V (MN-major)
+
+// A box from shared memory to global memory, in the thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, const void *smem_src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(smem_addr(smem_src))
+               : "memory");
+}
+
+#define WP_R8(c, i) c(v[i]), c(v[i + 1]), c(v[i + 2]), c(v[i + 3]), c(v[i + 4]), c(v[i + 5]), c(v[i + 6]), c(v[i + 7])
 
 struct WindowArgs {
   CUtensorMap tmap_k;  // boxes of one head's 16 rows of one page
   CUtensorMap tmap_v;
-  CUtensorMap tmap_q;  // boxes of 32 query rows x one group's 4 heads (rows past num_q_rows read as zeros)
+  CUtensorMap tmap_o;  // boxes of 8 output rows x one group's 4 heads x 128 bytes
   int num_pages;
   void *out;       // [total][32][64] fp32 or bf16
   const uint16_t *q;
@@ -69,63 +90,53 @@ struct WindowArgs {
   int num_q_rows;
   int max_context;
   int max_query;
-  int tiles_per_seq;
-  int num_tiles;  // num_seqs * tiles_per_seq * 8
-  float scale_log2;   // |scale| * log2(e)
-  float move_thresh;  // scores (unscaled) by which a block's max must pass the reference to move it
-  int neg;            // scale < 0: a row's reference is the max of -s (the min of s)
+  int item_tok;       // query tokens of an item: 64, or 32 (its first tile alone)
+  int items_per_seq;  // of max_query query tokens and one K/V head
+  int most_items;     // num_seqs * items_per_seq * 8
+  float scale_log2;  // scale * log2(e)
   int32_t *status;
 };
 
-// One work tile: 32 query tokens of sequence s (from t0) against K/V head g.
-struct WpTile {
+// One item: item_tok query tokens of sequence s (from t0) against K/V head g.
+struct WpItem {
   int s, g, t0, n, q0, ctx, nblocks;
   int npages;  // pages its rows see
   int front;   // of them the sinks' pages before the window
   int skip;    // pages between that no row sees
-  int run;      // has queries and a valid context
-  int invalid;  // has queries, invalid context: its rows are zeroed
+  int run;      // valid lengths
+  int invalid;  // invalid ones: its rows are zeroed
 };
 
 struct __align__(1024) WpSmem {
-  uint8_t q[2][kWpRows * kRowBytes];       // two tiles' Q, row = 4 * token + head, 128-byte swizzled
-  uint8_t k[kWpStages][kWpTileBytes];      // 64 keys x 128 B per stage
+  uint8_t k[kWpStages][kWpTileBytes];  // 128 keys x 128 B per stage, 128-byte swizzled
   uint8_t v[kWpStages][kWpTileBytes];
-  uint8_t ones[kWpTileBytes];              // the second MN atom of P V's B: 1 in column 0 of every key row
-  uint64_t q_full[2];
-  uint64_t q_empty[2];
-  uint64_t kv_full[kWpStages];
-  uint64_t kv_empty[kWpStages];
-  uint64_t s_full[2];
-  uint64_t s_free[2];  // the P V that read a buffer's P is done: S may be written again
-  uint64_t p_full[2];  // per P buffer: every softmax thread wrote its row of P (one barrier per
-                       // buffer, so a thread already on the next block cannot complete this phase)
-  uint64_t p_free[2];  // per P buffer: the P V of a block done (O, and everything before, may be read);
-                       // per buffer so that the phase waited for is never two behind
-  uint64_t mma_done;
-  int kv_bad[kWpStages];  // per stage: bit pp set when page pp of the block is invalid (loaded as zeros)
-  WpTile tiles[kWpMaxTiles];  // this CTA's tiles in walking order, read once from global memory
+  uint8_t rows[kWpTiles * 4][2][32 * 128];  // a warp's finished rows, 128 bytes of each at a time, swizzled
+  uint64_t q_full[kWpTiles];  // the tile's Q is in tensor memory (a warp arrives once)
+  uint64_t kv_full[kWpStages], kv_empty[kWpStages];
+  uint64_t s_full[kWpTiles][2];  // S of the half of the tile's next block is there, and its bad pages are known
+  uint64_t p_full[kWpTiles][2];  // every row of P of it (a warp arrives once), and O has been read where it starts anew
+  uint64_t o_full[kWpTiles];  // the P V that ends a run, or the item, is done
+  uint64_t mma_done[kWpTiles];
+  int kv_bad[kWpStages];  // bit pp set when page pp of the block is invalid (loaded as zeros)
+  WpItem items[kWpMaxItems];  // this CTA's, in walking order
+  int warp_sum[kWpThreads / 32];
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kWpSmemBytes = sizeof(WpSmem) + 1024;
 
-// Tile ti of the grid-wide list: latest token tiles first, then sequence, then K/V head.
-__device__ __forceinline__ WpTile wp_tile(const WindowArgs &a, int ti) {
-  WpTile t;
-  const int per_rank = a.num_seqs * kKvHeads;
-  const int rank = ti / per_rank, rem = ti % per_rank;
-  t.s = rem / kKvHeads;
-  t.g = rem % kKvHeads;
-  t.t0 = (a.tiles_per_seq - 1 - rank) * kWpTok;
-  t.q0 = __ldg(a.query_start + t.s);
-  t.n = __ldg(a.query_start + t.s + 1) - t.q0;
-  t.ctx = __ldg(a.context_lens + t.s);
-  const bool has = t.n != 0 && (t.n < 0 || t.t0 < t.n);
-  t.invalid = has && (t.n < 0 || t.n > a.max_query || t.ctx < 0 || t.ctx > a.max_context || t.n > t.ctx || t.q0 < 0 ||
-                      t.n > a.num_q_rows - t.q0);
-  t.run = has && !t.invalid;
-  const int first_pos = t.run ? t.ctx - t.n + t.t0 : 0, last_pos = t.run ? t.ctx - t.n + min(t.t0 + kWpTok, t.n) - 1 : 0;
+// What an item of sequence s (query tokens t0 .. of n from row q0 on, ctx cached tokens) has to know.
+__device__ __forceinline__ WpItem wp_item(const WindowArgs &a, int s, int g, int t0, int q0, int n, int ctx) {
+  WpItem t;
+  t.s = s;
+  t.g = g;
+  t.t0 = t0;
+  t.q0 = q0;
+  t.n = n;
+  t.ctx = ctx;
+  t.invalid = n > a.max_query || ctx < 0 || ctx > a.max_context || n > ctx || q0 < 0 || n > a.num_q_rows - q0;
+  t.run = !t.invalid;
+  const int first_pos = t.run ? ctx - n + t0 : 0, last_pos = t.run ? ctx - n + min(t0 + a.item_tok, n) - 1 : 0;
   const int lo = max(0, first_pos - a.window + 1), sink = min(a.sinks, lo);
   t.front = (sink + kPageTokens - 1) / kPageTokens;
   t.skip = max(lo / kPageTokens, t.front) - t.front;
@@ -134,98 +145,147 @@ __device__ __forceinline__ WpTile wp_tile(const WindowArgs &a, int ti) {
   return t;
 }
 
-// Block-table index of page v of a tile.
-__device__ __forceinline__ int logical_page(const WpTile &t, int v) { return v < t.front ? v : v + t.skip; }
+// Block-table index of page v of an item.
+__device__ __forceinline__ int logical_page(const WpItem &t, int v) { return v < t.front ? v : v + t.skip; }
 
-// Bounded wait that gives up at once when another role has already aborted.
-// Returns true when the phase completed.
+// The blocks of an item that a tile uses: those with a key in [0, sinks) (j < sinks) or [first row's window, last row's
+// position] (first <= j <= last).
+struct WpTile {
+  int sinks, first, last;  // last < 0: the tile has no queries
+  __device__ __forceinline__ int begin() const { return sinks > 0 ? 0 : first; }
+  __device__ __forceinline__ int next(int j) const { return j + 1 < first && j + 1 >= sinks ? first : j + 1; }
+};
+__device__ __forceinline__ WpTile tile_of(const WindowArgs &a, const WpItem &t, int tile) {
+  const int t0 = t.t0 + tile * kWpTok, pos = t.ctx - t.n + t0;
+  auto present = [&](int page) {  // number of the page, or of the next one that is there
+    return page < t.front ? page : max(page - t.skip, t.front);
+  };
+  WpTile w;
+  w.first = present(max(0, pos - a.window + 1) / kPageTokens) / kWpPagesPerBlock;
+  w.last = -1;
+  if (t0 < t.n && tile * kWpTok < a.item_tok)
+    w.last = present((t.ctx - t.n + min(t0 + kWpTok, t.n) - 1) / kPageTokens) / kWpPagesPerBlock;
+  w.sinks = (present(a.sinks / kPageTokens + (a.sinks % kPageTokens != 0)) + kWpPagesPerBlock - 1) / kWpPagesPerBlock;
+  return w;
+}
+
+// 32 TMEM columns, not waited for: v may be used after tmem_ld32_wait(v).
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : WP_R8("=r", 0), WP_R8("=r", 8), WP_R8("=r", 16), WP_R8("=r", 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : WP_R8("+r", 0), WP_R8("+r", 8), WP_R8("+r", 16), WP_R8("+r", 24)
+               :
+               : "memory");
+}
+
+// 32 TMEM columns stored; complete after tmem_st_wait().
+__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      WP_R8("r", 0), WP_R8("r", 8), WP_R8("r", 16), WP_R8("r", 24)
+      : "memory");
+}
+__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st16_async(taddr, v); }
+
+// Bounded wait of a whole warp that gives up once another role has; one answer for all lanes.  Returns true when the
+// phase completed.
 __device__ __forceinline__ bool wp_wait(WpSmem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (*reinterpret_cast<volatile int *>(&sm.abort)) return false;
-  if (mbar_wait(bar, parity)) return true;
-  *reinterpret_cast<volatile int *>(&sm.abort) = 1;
-  report(status, PKV_DEV_TIMEOUT);
-  return false;
-}
-
-template <bool kMin>
-__device__ __forceinline__ float ext3(float a, float b, float c) {
-  return kMin ? min3f(a, b, c) : max3f(a, b, c);
-}
-
-// Largest (kMin: smallest) of 64 values: a tree of three-input max (32 instructions, 4 deep).
-template <bool kMin>
-__device__ __forceinline__ float extreme64(const float (&x)[64]) {
-  float m[22];
-#pragma unroll
-  for (int i = 0; i < 21; ++i) m[i] = ext3<kMin>(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
-  m[21] = x[63];
-  float n[8];
-#pragma unroll
-  for (int i = 0; i < 7; ++i) n[i] = ext3<kMin>(m[3 * i], m[3 * i + 1], m[3 * i + 2]);
-  n[7] = m[21];
-  const float a = ext3<kMin>(n[0], n[1], n[2]), b = ext3<kMin>(n[3], n[4], n[5]);
-  const float c = kMin ? fminf(n[6], n[7]) : fmaxf(n[6], n[7]);
-  return ext3<kMin>(a, b, c);
-}
-
-// The first n keys of a page as a mask of 16 bits.
-__device__ __forceinline__ unsigned first_keys(int n) {
-  return n <= 0 ? 0u : n >= kPageTokens ? 0xffffu : (1u << n) - 1u;
-}
-
-// max over the keys whose bit in `valid` is set of sigma * s, sigma = -1 when neg.
-__device__ __forceinline__ float signed_max(const float (&sv)[64], bool masked, uint64_t valid, bool neg) {
-  if (!masked) return neg ? -extreme64<true>(sv) : extreme64<false>(sv);
-  float xm[64];
-  const float off = neg ? INFINITY : -INFINITY;
-#pragma unroll
-  for (int c = 0; c < 64; ++c) xm[c] = (valid >> c) & 1 ? sv[c] : off;
-  return neg ? -extreme64<true>(xm) : extreme64<false>(xm);
-}
-
-// P = 2^((s - m) * c) for the 64 keys of a block as bf16 hi + lo parts, keys 2i and
-// 2i + 1 packed in word i; with kMasked, keys whose bit in `valid` is clear get 0.
-template <bool kMasked, bool kTwo>
-__device__ __forceinline__ void block_probs(const float (&sv)[64], uint64_t valid, float m, float2 c2,
-                                            uint32_t (&hi)[32], uint32_t (&lo)[32]) {
-  // exponent arguments (s - m) c as one packed fused multiply-add: s c + (-m c)
-  const float2 mc = make_float2(-m * c2.x, -m * c2.y);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float2 e = fma_f32x2(make_float2(sv[2 * i], sv[2 * i + 1]), c2, mc);
-    float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
-    if (kMasked) {
-      p0 = (valid >> (2 * i)) & 1 ? p0 : 0.f;
-      p1 = (valid >> (2 * i + 1)) & 1 ? p1 : 0.f;
-    }
-    hi[i] = pack_bf16x2(p0, p1);
-    if (kTwo) {
-      const float2 r = sub_f32x2(make_float2(p0, p1), make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
-      lo[i] = pack_bf16x2(r.x, r.y);
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    const bool late = global_ns() - t0 > kWaitLimitNs;
+    if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int *>(&sm.abort) != 0)) {
+      if (__any_sync(0xffffffffu, late)) {
+        *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+        report(status, PKV_DEV_TIMEOUT);
+      }
+      return false;
     }
   }
+  return true;
 }
 
-// 32 values of an output row from element `at` on.
+// Bits [0, n) of 32.
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
+// Largest (kMin: smallest) of 32 scores.
+template <bool kMin>
+__device__ __forceinline__ float extreme32(const uint32_t (&s)[32]) {
+  float m[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const float x = __uint_as_float(s[3 * i]), y = __uint_as_float(s[3 * i + 1]), z = __uint_as_float(s[3 * i + 2]);
+    m[i] = kMin ? min3f(x, y, z) : max3f(x, y, z);
+  }
+  const float u = __uint_as_float(s[30]), v = __uint_as_float(s[31]);
+  m[10] = kMin ? fminf(u, v) : fmaxf(u, v);
+#pragma unroll
+  for (int n = 11; n > 1; n = (n + 2) / 3)
+#pragma unroll
+    for (int i = 0; i < (n + 2) / 3; ++i) {
+      const float x = m[3 * i], y = 3 * i + 1 < n ? m[3 * i + 1] : x, z = 3 * i + 2 < n ? m[3 * i + 2] : x;
+      m[i] = kMin ? min3f(x, y, z) : max3f(x, y, z);
+    }
+  return m[0];
+}
+
+// P = 2^(s c - m) for 32 keys as one or two bf16 terms, keys 2i and 2i + 1 packed in word i, the second term behind the
+// first (with kMasked, keys whose bit in `valid` is clear get 0); returns their sum.
+template <bool kMasked, bool kTwo>
+__device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t valid, float m, float c,
+                                               uint32_t (&p16)[kTwo ? 32 : 16]) {
+  const float2 c2 = make_float2(c, c), mc = make_float2(-m, -m);
+  float2 sum[4] = {};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, mc);
+    float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+    if (kMasked) {
+      p.x = (valid >> (2 * i)) & 1 ? p.x : 0.f;
+      p.y = (valid >> (2 * i + 1)) & 1 ? p.y : 0.f;
+    }
+    sum[i % 4] = add_f32x2(sum[i % 4], p);
+    const uint32_t hi = pack_bf16x2(p.x, p.y);
+    p16[i] = hi;
+    if constexpr (kTwo) {
+      const float2 r = sub_f32x2(p, make_float2(bf16_lo(hi), bf16_hi(hi)));
+      p16[16 + i] = pack_bf16x2(r.x, r.y);
+    }
+  }
+  const float2 t = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
+  return t.x + t.y;
+}
+
+// 16 values of an output row from element `at` on.
 template <bool kBf16Out>
-__device__ __forceinline__ void store_row(void *out, long long at, const float (&v)[32]) {
+__device__ __forceinline__ void store_row(void *out, long long at, const float (&v)[16]) {
   if (kBf16Out) {
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
 #pragma unroll
-    for (int c = 0; c < 32; c += 8)
+    for (int c = 0; c < 16; c += 8)
       dst[c / 8] = make_uint4(pack_bf16x2(v[c], v[c + 1]), pack_bf16x2(v[c + 2], v[c + 3]),
                               pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));
   } else {
     float *dst = static_cast<float *>(out) + at;
     if ((reinterpret_cast<uintptr_t>(out) & 31u) == 0) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
+      for (int c = 0; c < 16; c += 8) {
         const float x[8] = {v[c], v[c + 1], v[c + 2], v[c + 3], v[c + 4], v[c + 5], v[c + 6], v[c + 7]};
         st_global_v8(dst + c, x);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 32; c += 4)
+      for (int c = 0; c < 16; c += 4)
         *reinterpret_cast<float4 *>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
     }
   }
@@ -233,22 +293,22 @@ __device__ __forceinline__ void store_row(void *out, long long at, const float (
 
 // Row `tok` of tile t, query head g * 4 + hh, from the keys that it sees alone: the maximum first, then the sums.
 template <bool kBf16Out>
-__device__ __noinline__ void recompute_row(const WindowArgs &a, const WpTile &t, int tok, int hh) {
+__device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t, int tok, int hh) {
   const int pos = t.ctx - t.n + t.t0 + tok;
   const long long row = ((long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh) * kHeadDim;
   const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + row);
   const int32_t *table = a.block_tables + (long long)t.s * a.bt_stride;
-  const float scale = a.neg ? -a.scale_log2 : a.scale_log2;
+  const float scale = a.scale_log2;
   const int lo = max(0, pos - a.window + 1);
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, lost = 0.f;  // l and what its additions have lost so far
   bool nan = false;
-  float o[2][32];
+  float o[4][16];
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
       if (m == -INFINITY) m = 0.f;
 #pragma unroll
-      for (int c = 0; c < 32; ++c) o[0][c] = o[1][c] = 0.f;
+      for (int c = 0; c < 64; ++c) o[c / 16][c % 16] = 0.f;
     }
 #pragma unroll 1
     for (int v = 0; v < t.npages; ++v) {
@@ -278,8 +338,9 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpTile &t,
           nan |= x != x || x == INFINITY;  // a maximum of +infinity leaves no softmax
           continue;
         }
-        const float p = ex2_approx(x - m);
-        l += p;
+        const float p = ex2_approx(x - m), y = p - lost, sum = l + y;
+        lost = (sum - l) - y;
+        l = sum;
         if (p == 0.f) continue;
         const uint4 *vr = reinterpret_cast<const uint4 *>(a.v_base + at + r * kRowBytes);
 #pragma unroll
@@ -288,7 +349,7 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpTile &t,
           const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float &o0 = o[c / 4][8 * (c % 4) + 2 * i], &o1 = o[c / 4][8 * (c % 4) + 2 * i + 1];
+            float &o0 = o[c / 2][8 * (c % 2) + 2 * i], &o1 = o[c / 2][8 * (c % 2) + 2 * i + 1];
             o0 = fmaf(p, bf16_lo(vw[i]), o0);
             o1 = fmaf(p, bf16_hi(vw[i]), o1);
           }
@@ -298,85 +359,101 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpTile &t,
   }
   const float inv = nan ? NAN : l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    o[0][c] *= inv;
-    o[1][c] *= inv;
+  for (int part = 0; part < 4; ++part) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) o[part][c] *= inv;
+    store_row<kBf16Out>(a.out, row + 16 * part, o[part]);
   }
-  store_row<kBf16Out>(a.out, row, o[0]);
-  store_row<kBf16Out>(a.out, row + 32, o[1]);
 }
 
-// Persistent: each CTA walks its tiles of the snake order (at most kWpMaxTiles;
-// their descriptors are read from global memory once, in parallel, into shared memory).
-// Every role walks the same table and skips the same tiles, so their running block
-// counters agree.  The loader fetches the next tile's Q and block-table entries while the
-// current tile computes; the MMA warp starts the next tile's S during the current one's
-// last blocks; the softmax warps finish a tile (read O, divide, store) only after writing
-// P for the next tile's first block, so the wait for the last P V overlaps useful work.
+// Every role walks the same table of this CTA's items and skips the same items and blocks, so that their running counters
+// agree.
 template <bool kBf16Out>
-__global__ void __launch_bounds__(kWpThreads, kWpCtasPerSm) window_prefill_kernel(const __grid_constant__ WindowArgs a) {
+__global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __grid_constant__ WindowArgs a) {
   extern __shared__ uint8_t smem_raw[];
   WpSmem &sm = *reinterpret_cast<WpSmem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Tile k of this CTA: k * G + c on even rounds and k * G + (G - 1 - c) on odd ones, a snake
-  // over the latest-first list that evens out the CTAs' key blocks.
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same for all lanes, and the compiler knows it)
+  // Item k of this CTA: k * G + c on even rounds and k * G + (G - 1 - c) on odd ones.
   const int G = int(gridDim.x), c = int(blockIdx.x);
-  auto tile_index = [&](int k) { return k * G + ((k & 1) ? G - 1 - c : c); };
-  int nt = 0;  // <= kWpMaxTiles
-  while (nt < kWpMaxTiles && tile_index(nt) < a.num_tiles) ++nt;
+  auto item_index = [&](int k) { return k * G + ((k & 1) ? G - 1 - c : c); };
+  int nt = 0;  // <= kWpMaxItems
+  while (nt < kWpMaxItems && item_index(nt) < a.most_items) ++nt;
 
-  if (tid < nt) sm.tiles[tid] = wp_tile(a, tile_index(tid));
+  if (tid < kWpMaxItems) sm.items[tid].run = sm.items[tid].invalid = 0;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.q_full[i], 1);
-      mbar_init(&sm.q_empty[i], 1);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_free[i], 1);
-    }
-    for (int i = 0; i < kWpStages; ++i) {
+    for (unsigned i = 0; i < kWpStages; ++i) {
       mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 1);
+      mbar_init(&sm.kv_empty[i], kWpTiles);
     }
-    mbar_init(&sm.p_full[0], kWpRows);
-    mbar_init(&sm.p_full[1], kWpRows);
-    mbar_init(&sm.p_free[0], 1);
-    mbar_init(&sm.p_free[1], 1);
-    mbar_init(&sm.mma_done, 1);
+    for (int t = 0; t < kWpTiles; ++t) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.s_full[t][h], 2);
+        mbar_init(&sm.p_full[t][h], kWpRows / 32);
+      }
+      mbar_init(&sm.mma_done[t], 1);
+      mbar_init(&sm.o_full[t], 1);
+      mbar_init(&sm.q_full[t], kWpRows / 32);
+    }
     sm.abort = 0;
     mbar_init_fence();
   }
-  if (tid < kWpRows) {
-    // ones block: key row r (of 64) holds bf16 1.0 in element 0 (its 128-byte-swizzled position)
-    for (int i = tid; i < kWpKeys * 8; i += kWpRows) {
-      const int r = i >> 3, c = i & 7;
-      *reinterpret_cast<uint4 *>(sm.ones + r * kRowBytes + ((c ^ (r & 7)) << 4)) =
-          make_uint4(c == 0 ? 0x3f80u : 0u, 0u, 0u, 0u);
-    }
-    fence_proxy_async_smem();
-  }
-  if (warp == 5) tmem_alloc(&sm.tmem_base, kWpTmemCols);
+  if (warp == kWpLoader) tmem_alloc(&sm.tmem_base, kWpTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  uint64_t redo = 0;  // softmax threads: bit k set where this thread's row of tile k has to be computed again
-  // index of the first running tile at or after k
+  // The list of items: sequence after sequence, its tokens from the last ones to the first, 8 K/V heads each.  A thread takes
+  // a sequence, counts its items and, by a prefix sum, finds which of this CTA's items they are.
+  bool negative = false;  // a sequence of less than no query tokens, reported once the kernel before this one has ended
+  for (int base = 0, before = 0; base < a.num_seqs; base += kWpThreads) {
+    const int s = base + tid;
+    int q0 = 0, n = 0, ctx = 0;
+    if (s < a.num_seqs) {
+      q0 = __ldg(a.query_start + s);
+      n = __ldg(a.query_start + s + 1) - q0;
+      ctx = __ldg(a.context_lens + s);
+    }
+    negative |= n < 0;
+    const int count = n <= 0 ? 0 : min((n - 1) / a.item_tok + 1, a.items_per_seq);
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) sm.warp_sum[warp] = upto;
+    __syncthreads();
+    int all = 0, first = before + upto - count;
+    for (int w = 0; w < kWpThreads / 32; ++w) {
+      if (w < warp) first += sm.warp_sum[w];
+      all += sm.warp_sum[w];
+    }
+    if (count > 0)
+      for (int k = 0; k < nt; ++k) {
+        const int i = item_index(k), u = i / kKvHeads - first;
+        if (u >= 0 && u < count) sm.items[k] = wp_item(a, s, i % kKvHeads, (count - 1 - u) * a.item_tok, q0, n, ctx);
+      }
+    before += all;
+    __syncthreads();
+  }
+  negative = __syncthreads_or(negative);
+  uint64_t redo = 0;  // softmax threads: bit k set where this thread's row of item k has to be computed again
+  // index of the first running item at or after k
   auto next_run = [&](int k) {
-    while (k < nt && !sm.tiles[k].run) ++k;
+    while (k < nt && !sm.items[k].run) ++k;
     return k;
   };
 
-  if (warp == 4) {
-    // ================= loader: Q tiles and K/V blocks (tiled TMA) =================
+  if (warp == kWpLoader) {
+    // ================= loader: K/V blocks (tiled TMA) =================
     const uint64_t policy = policy_evict_last();
-    const uint64_t policy_q = policy_evict_first();  // each query row is read by one tile
     if (lane == 0) {
       prefetch_tensormap(&a.tmap_k);
       prefetch_tensormap(&a.tmap_v);
-      prefetch_tensormap(&a.tmap_q);
     }
-    // block-table entries of a tile's first 128 pages: page lp sits in lane lp % 32, slot lp / 32
-    auto load_entries = [&](const WpTile &t, int (&e)[4]) {
+    // block-table entries of an item's first 128 pages: page lp sits in lane lp % 32, slot lp / 32
+    auto load_entries = [&](const WpItem &t, int (&e)[4]) {
       const int32_t *table = a.block_tables + (long long)t.s * a.bt_stride;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -384,232 +461,308 @@ __global__ void __launch_bounds__(kWpThreads, kWpCtasPerSm) window_prefill_kerne
         e[k] = lp < t.npages ? __ldg(table + logical_page(t, lp)) : -1;
       }
     };
-    // Q of tile t into buffer qb: one tiled TMA box of 32 query rows x the group's 4 heads,
-    // landing as rows 4 * token + head, 128-byte swizzled (rows past num_q_rows read as zeros;
-    // padding rows past n are the next sequence's queries: computed, never written)
-    auto load_q = [&](const WpTile &t, int qb) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.q_full[qb], kWpRows * kRowBytes);
-        tma_load_3d(sm.q[qb], &a.tmap_q, 0, t.g * kGroup, t.q0 + t.t0, &sm.q_full[qb], policy_q);
-      }
-      __syncwarp();
-    };
-    long long gb = 0;  // K/V blocks issued so far
-    int lt = 0;        // running tiles started so far
+    unsigned gb = 0;   // K/V blocks issued so far
     bool ok = true;
     int k = next_run(0);
     int ent[4] = {-1, -1, -1, -1};
     if (k < nt) {
-      load_entries(sm.tiles[k], ent);
-      load_q(sm.tiles[k], 0);
+      load_entries(sm.items[k], ent);
     }
-    // launched with overlap (PKV_OVERLAP_PREVIOUS), the kernel before this one (the append of
-    // the prompt's K/V) may still be running: the pages are read only once it has completed
+    // launched with overlap (PKV_OVERLAP_PREVIOUS), the kernel before this one (the append of the prompt's K/V) may still
+    // be running: the pages are read only once it has completed
     griddep_wait();
     while (ok && k < nt) {
-      const WpTile t = sm.tiles[k];
+      const WpItem t = sm.items[k];
       const int kn = next_run(k + 1);
       int ent_next[4] = {-1, -1, -1, -1};
-      if (kn < nt) load_entries(sm.tiles[kn], ent_next);  // in flight while this tile's blocks go out
+      if (kn < nt) load_entries(sm.items[kn], ent_next);  // in flight while this item's blocks go out
       const int32_t *table = a.block_tables + (long long)t.s * a.bt_stride;
       for (int j = 0; j < t.nblocks; ++j, ++gb) {
-        const int st = int(gb % kWpStages);
+        const unsigned st = gb % kWpStages;
         if (gb >= kWpStages) {
-          const bool w = wp_wait(sm, &sm.kv_empty[st], uint32_t(gb / kWpStages - 1) & 1, a.status);
-          if (!__all_sync(0xffffffffu, w)) {
+          if (!wp_wait(sm, &sm.kv_empty[st], (gb / kWpStages - 1) & 1, a.status)) {
             ok = false;
             break;
           }
         }
         int page[kWpPagesPerBlock], bad = 0;
+        const bool near = j * kWpPagesPerBlock < 128;  // the block's entries lie in one of the registers
+        const int q4 = j * kWpPagesPerBlock >> 5, some = q4 == 0 ? ent[0] : q4 == 1 ? ent[1] : q4 == 2 ? ent[2] : ent[3];
 #pragma unroll
         for (int pp = 0; pp < kWpPagesPerBlock; ++pp) {
           const int lp = j * kWpPagesPerBlock + pp;
-          int e;
-          if (lp < 128) {
-            const int q = lp >> 5;
-            e = __shfl_sync(0xffffffffu, q == 0 ? ent[0] : q == 1 ? ent[1] : q == 2 ? ent[2] : ent[3], lp & 31);
-          } else {
-            e = lp < t.npages ? __ldg(table + logical_page(t, lp)) : -1;
-          }
-          page[pp] = -1;  // outside the pool: TMA fills the box with zeros
-          if (lp < t.npages) {
-            if (e >= 0 && e < a.num_pages)
-              page[pp] = e;
-            else
-              bad |= 1 << pp;
-          }
+          const int e = near            ? __shfl_sync(0xffffffffu, some, lp & 31)
+                        : lp < t.npages ? __ldg(table + logical_page(t, lp))
+                                        : -1;
+          const bool ok_id = unsigned(e) < unsigned(a.num_pages);
+          page[pp] = ok_id ? e : -1;  // outside the pool: TMA fills the box with zeros
+          if (!ok_id && lp < t.npages) bad |= 1 << pp;
         }
-        if (lane == 0) {
+        if (elect_one()) {
           if (bad) report(a.status, PKV_DEV_BAD_PAGE);
           sm.kv_bad[st] = bad;
           mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kWpTileBytes);
 #pragma unroll
-          for (int pp = 0; pp < kWpPagesPerBlock; ++pp) {
+          for (int pp = 0; pp < kWpPagesPerBlock; ++pp)
             tma_load_3d(sm.k[st] + pp * kWpBox, &a.tmap_k, 0, t.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
+#pragma unroll
+          for (int pp = 0; pp < kWpPagesPerBlock; ++pp)
             tma_load_3d(sm.v[st] + pp * kWpBox, &a.tmap_v, 0, t.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
-          }
         }
         __syncwarp();
-        if (j == min(1, t.nblocks - 1) && kn < nt) {
-          // the next tile's Q, once the tile before this one released its buffer
-          const int qb = (lt + 1) & 1;
-          if (lt + 1 >= 2) {
-            const bool w = wp_wait(sm, &sm.q_empty[qb], uint32_t((lt + 1) / 2 - 1) & 1, a.status);
-            if (!__all_sync(0xffffffffu, w)) {
-              ok = false;
-              break;
-            }
-          }
-          load_q(sm.tiles[kn], qb);
-        }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) ent[q] = ent_next[q];
       k = kn;
-      ++lt;
     }
     // every copy issued has landed before the CTA exits
-    if (lane == 0)
-      for (long long j = gb > kWpStages ? gb - kWpStages : 0; j < gb; ++j)
-        mbar_wait(&sm.kv_full[int(j % kWpStages)], uint32_t(j / kWpStages) & 1);
+    if (lane == 0) {
+      for (unsigned j = gb > kWpStages ? gb - kWpStages : 0; j < gb; ++j)
+        mbar_wait(&sm.kv_full[j % kWpStages], (j / kWpStages) & 1);
+    }
     __syncwarp();
-  } else if (warp == 5) {
-    // ================= MMA issuer (one thread issues, the warp waits) =================
-    long long gb = 0;          // blocks whose S was issued
-    long long pend = -1;       // block whose P V is still to issue
-    bool pend_first = false;   // ... and whether it starts its tile (O is overwritten, not accumulated)
-    int lt = 0;
+  } else if (warp >= kWpIssuers) {
+    // ================= issuers: the MMAs of a tile each (one thread issues, the warp waits) =================
+    const int tile = warp - kWpIssuers;
+    const uint32_t sa = tmem + kColS + tile * kWpKeys, oa = tmem + kColO + tile * kHeadDim,
+                   qa = tmem + kColQ + tile * (kHeadDim / 2);
+    const uint64_t k_desc = sw128_desc(smem_addr(sm.k), 16, 1024), v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
+    unsigned gb = 0;                // blocks of the items before
+    unsigned passed = 0;            // blocks given back (each tile gives back every one of them)
+    unsigned qs = 0, pvs = 0;       // Q's and blocks of P taken up
     bool ok = true;
-    auto issue_pv = [&]() {
-      bool w = wp_wait(sm, &sm.p_full[pend & 1], uint32_t(pend >> 1) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const int st = int(pend % kWpStages), b = int(pend & 1);
-        const uint32_t vb = smem_addr(sm.v[st]);
-        const uint32_t pa = tmem + kColS + b * kWpKeys;  // P hi in its 32 first columns, P lo in the next 32
-        const uint32_t to_ones = smem_addr(sm.ones) - vb;  // stride to the second (ones) MN atom
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_tmem_a(tmem + kColO, pa + kk * 8, sw128_desc(vb + kk * 2048, to_ones, 1024), kIdescPV,
-                        (pend_first && kk == 0) ? 0u : 1u);
-        if (!kBf16Out) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_tmem_a(tmem + kColO, pa + 32 + kk * 8, sw128_desc(vb + kk * 2048, to_ones, 1024), kIdescPV, 1u);
-        }
-        tc_commit(&sm.p_free[b]);
-        tc_commit(&sm.kv_empty[st]);
-        tc_commit(&sm.s_free[b]);
+    auto pass_to = [&](unsigned block) {  // the tile uses none of the blocks before `block` that it has not given back
+      while (passed < block) {
+        if (!wp_wait(sm, &sm.kv_full[passed % kWpStages], (passed / kWpStages) & 1, a.status)) return false;
+        if (elect_one()) mbar_arrive(&sm.kv_empty[passed % kWpStages]);
+        __syncwarp();
+        ++passed;
       }
-      __syncwarp();
-      pend = -1;
       return true;
     };
-    for (int k = next_run(0); ok && k < nt; k = next_run(k + 1)) {
-      const WpTile t = sm.tiles[k];
-      const int qb = lt & 1;
-      bool w = wp_wait(sm, &sm.q_full[qb], uint32_t(lt / 2) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) break;
-      const uint32_t q_base = smem_addr(sm.q[qb]);
-      for (int j = 0; j < t.nblocks; ++j, ++gb) {
-        const int st = int(gb % kWpStages), b = int(gb & 1);
-        w = wp_wait(sm, &sm.kv_full[st], uint32_t(gb / kWpStages) & 1, a.status);
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
+    auto landed = [&](const WpItem &t, int j, unsigned st) {  // block j of the item, in stage st
+      if (!wp_wait(sm, &sm.kv_full[st], ((gb + j) / kWpStages) & 1, a.status)) return false;
+      if (j == t.nblocks - 1) {
         // V rows at or past the context in the sequence's last page (stale pool bytes) become zeros
-        if (j == t.nblocks - 1) {
-          const int row0 = (t.npages - 1 - j * kWpPagesPerBlock) * kPageTokens;  // the tile's last page in the block
-          const int live = t.ctx - logical_page(t, t.npages - 1) * kPageTokens;
-          if (live < kPageTokens) {
-            uint8_t *vt = sm.v[st] + (row0 + live) * kRowBytes;
-            for (int idx = lane; idx < (kPageTokens - live) * 8; idx += 32)
-              *reinterpret_cast<uint4 *>(vt + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-          }
+        const int row0 = (t.npages - 1 - j * kWpPagesPerBlock) * kPageTokens;  // the item's last page in the block
+        const int live = t.ctx - logical_page(t, t.npages - 1) * kPageTokens;
+        if (live < kPageTokens) {
+          uint8_t *vt = sm.v[st] + (row0 + live) * kRowBytes;
+          for (int idx = lane; idx < (kPageTokens - live) * 8; idx += 32)
+            *reinterpret_cast<uint4 *>(vt + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
         }
         __syncwarp();
-        if (gb >= 2) {
-          w = wp_wait(sm, &sm.s_free[b], uint32_t(gb / 2 - 1) & 1, a.status);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t kb = smem_addr(sm.k[st]);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma(tmem + kColS + b * kWpKeys, sw128_desc(q_base + kk * 32, 16, 1024),
-                   sw128_desc(kb + kk * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
-          tc_commit(&sm.s_full[b]);
-          if (j == t.nblocks - 1) tc_commit(&sm.q_empty[qb]);  // the tile's last read of its Q
-        }
-        __syncwarp();
-        if (pend >= 0 && !issue_pv()) {
-          ok = false;
-          break;
-        }
-        pend = gb;
-        pend_first = (j == 0);
       }
-      ++lt;
+      tc_fence_after();
+      return true;
+    };
+    auto issue_s = [&](unsigned st, int h) {  // S of a half of the block in stage st
+      if (elect_one()) {
+        const uint64_t kd = k_desc + uint32_t((st * kWpTileBytes + h * (kWpTileBytes / 2)) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_tmem_a(sa + h * kWpHalf, qa + kk * 8, kd + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
+        tc_commit(&sm.s_full[tile][h]);
+        mbar_arrive(&sm.s_full[tile][h]);  // (hands on the loader's word about bad pages)
+      }
+      __syncwarp();
+    };
+    // P V of a half of the block in stage st; the block starts, or ends, a sum in O
+    auto issue_pv = [&](unsigned st, int h, bool starts, bool ends) {
+      if (!wp_wait(sm, &sm.p_full[tile][h], pvs & 1, a.status)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        // P: 16 columns for each 32 keys, the second terms of the same keys behind the first ones
+        const uint64_t vd = v_desc + uint32_t((st * kWpTileBytes + h * (kWpTileBytes / 2)) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kWpHalf / 16; ++kk) {
+          const uint32_t pa = sa + h * kWpHalf + (kk / 2) * 32 + (kk % 2) * 8;
+          tc_mma_tmem_a(oa, pa, vd + kk * (2048 >> 4), kIdescPV, (starts && h == 0 && kk == 0) ? 0u : 1u);
+          if (!kBf16Out) tc_mma_tmem_a(oa, pa + 16, vd + kk * (2048 >> 4), kIdescPV, 1u);
+        }
+        if (h == 1) {
+          if (ends) tc_commit(&sm.o_full[tile]);
+          tc_commit(&sm.kv_empty[st]);
+        }
+      }
+      __syncwarp();
+      return true;
+    };
+#pragma unroll 1
+    for (int k = next_run(0); ok && k < nt; k = next_run(k + 1)) {
+      const WpItem &t = sm.items[k];
+      const WpTile w = tile_of(a, t, tile);
+      if (w.last >= 0) {
+        int j = w.begin(), used = 0;
+        ok = pass_to(gb + j);
+        unsigned st = (gb + j) % kWpStages;
+        ok = ok && landed(t, j, st) && wp_wait(sm, &sm.q_full[tile], qs++ & 1, a.status);
+        if (ok) {
+          tc_fence_after();
+          issue_s(st, 0);
+          issue_s(st, 1);
+        }
+#pragma unroll 1
+        while (ok) {
+          const bool last = j == w.last, starts = kBf16Out ? used == 0 : used % kWpRun == 0;
+          const bool ends = last || (!kBf16Out && used % kWpRun == kWpRun - 1);
+          const int jn = w.next(j);
+          const unsigned sn = (gb + jn) % kWpStages;
+          // the next block's S goes half by half behind P V of this one's; where blocks lie between that the tile does not
+          // use, this one is given back first (their copies may wait for its stage)
+          const bool near = !last && jn == j + 1;
+          ok = issue_pv(st, 0, starts, ends);
+          if (near) {
+            ok = ok && landed(t, jn, sn);
+            if (ok) issue_s(sn, 0);
+          }
+          ok = ok && issue_pv(st, 1, starts, ends);
+          ++pvs;
+          ++passed;
+          if (!ok || last) break;
+          if (!near) {
+            ok = pass_to(gb + jn) && landed(t, jn, sn);
+            if (!ok) break;
+            issue_s(sn, 0);
+          }
+          issue_s(sn, 1);
+          j = jn;
+          st = sn;
+          ++used;
+        }
+      }
+      if (ok) ok = pass_to(gb + t.nblocks);
+      gb += t.nblocks;
     }
-    if (ok && pend >= 0) issue_pv();
     // every MMA issued has completed before the tensor memory is freed
-    if (lane == 0) {
-      tc_commit(&sm.mma_done);
-      mbar_wait(&sm.mma_done, 0);
+    if (elect_one()) {
+      tc_commit(&sm.mma_done[tile]);
+      mbar_wait(&sm.mma_done[tile], 0);
     }
     __syncwarp();
   } else {
-    // ================= softmax warps: thread = row = 4 * token + head =================
-    griddep_wait();  // the first global write below comes after the kernel before this one
-    const int r = tid, tok = r >> 2, hh = r & 3;
-    const uint32_t lane_base = tmem + (uint32_t(32 * warp) << 16);
-    long long gb = 0;
-    bool ok = true;
-    // the tile whose O is still to be read, divided and stored
-    bool fin = false;
-    int fin_q0 = 0, fin_t0 = 0, fin_n = 0, fin_g = 0, fin_k = 0;
-    auto finish = [&]() {
-      // wait for the tile's last P V (global block gb - 1); O, and its row-sum column, are final
-      const bool w = wp_wait(sm, &sm.p_free[(gb - 1) & 1], uint32_t((gb - 1) >> 1) & 1, a.status);
-      if (!__all_sync(0xffffffffu, w)) return false;
-      tc_fence_after();
-      const float l_sum = __uint_as_float(tmem_ld1(lane_base + kColO + kHeadDim));
-      const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
-      const long long row = ((long long)(fin_q0 + fin_t0 + tok) * kQHeads + fin_g * kGroup + hh) * kHeadDim;
-      float finite = 0.f;  // stays 0 where every value of the row is finite
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t o[32];
-        tmem_ld32(lane_base + kColO + 32 * half, o);
-        float v[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          v[c] = __uint_as_float(o[c]) * inv;
-          finite = fmaf(v[c], 0.f, finite);
-        }
-        if (fin_t0 + tok < fin_n) store_row<kBf16Out>(a.out, row + 32 * half, v);
+    // ================= softmax groups: thread = row = 4 * token + head of tile `tile` =================
+    const int tile = warp >> 2, r = tid & (kWpRows - 1), tok = tile * kWpTok + (r >> 2), hh = r & 3;
+    const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim;
+    // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there.
+    uint32_t qn[kHeadDim / 2];
+    auto fetch_q = [&](int k) {
+      k = next_run(k);
+      const bool there = k < nt && sm.items[k].t0 + tok < sm.items[k].n;
+      const uint4 *src = nullptr;
+      if (there) {
+        const WpItem &t = sm.items[k];
+        const long long row = (long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh;
+        src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim);
       }
-      if (fin_t0 + tok < fin_n && !(finite == 0.f)) redo |= 1ull << fin_k;
-      fin = false;
+#pragma unroll
+      for (int i = 0; i < kHeadDim / 8; ++i) {
+        const uint4 x = there ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        qn[4 * i] = x.x, qn[4 * i + 1] = x.y, qn[4 * i + 2] = x.z, qn[4 * i + 3] = x.w;
+      }
+    };
+    fetch_q(0);
+    griddep_wait();  // the first global write below comes after the kernel before this one
+    // (not before the wait: what the next kernel reads at once may come from a kernel before this one)
+    griddep_launch_dependents();
+    if (negative && blockIdx.x == 0 && tid == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
+    const float scale = a.scale_log2;
+    unsigned gb = 0;
+    uint32_t blocks = 0, drained = 0;  // blocks of this tile so far, and times that O was taken out
+    bool ok = true;
+    // O to be taken out once the next P is written: 0 none, 1 a run's, 2 the item's
+    int drain = 0, d_k = 0;
+    float d_sum = 0.f;
+    bool d_more = false;  // earlier runs lie in `out`
+    auto take_out = [&]() {
+      if (!wp_wait(sm, &sm.o_full[tile], drained & 1, a.status)) return false;
+      ++drained;
+      tc_fence_after();
+      const WpItem &t = sm.items[d_k];
+      const bool d_row = t.t0 + tok < t.n;  // the row has a query
+      const long long d_at = ((long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh) * kHeadDim;
+      float finite = 0.f;  // stays 0 where every value of the row is finite
+      const float inv = drain == 1 ? 1.f : d_sum != 0.f ? 1.f / d_sum : 0.f;
+      // the warp's 8 tokens by TMA, where the item ends and they are the sequence's own
+      const int first_tok = t.t0 + tile * kWpTok + 8 * (warp & 3);
+      const bool boxed = drain == 2 && first_tok + 8 <= t.n;
+      uint8_t *mine = sm.rows[warp][0] + lane * 128;
+      if (boxed) {
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the rows before have been read
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int part = 0; part < kHeadDim; part += 16) {
+        uint32_t o[16];
+        tmem_ld16_async(o_addr + part, o);
+        tmem_ld_wait(o);
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]);
+        if (!kBf16Out && d_more && d_row) {
+          const float4 *old = reinterpret_cast<const float4 *>(static_cast<const float *>(a.out) + d_at + part);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 x = old[i];
+            v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v[i] *= inv;
+          finite = fmaf(v[i], 0.f, finite);
+        }
+        if (boxed) {
+          if constexpr (kBf16Out) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4 *>(mine + (((part / 8 + i) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                             pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4 *>(mine + (part / 32) * 4096 + (((part % 32 / 4 + i) ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        } else if (d_row) {
+          store_row<kBf16Out>(a.out, d_at + part, v);
+        }
+      }
+      if (boxed) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) {
+          tma_store_3d(&a.tmap_o, 0, t.g * kGroup, t.q0 + first_tok, sm.rows[warp][0]);
+          if (!kBf16Out) tma_store_3d(&a.tmap_o, 32, t.g * kGroup, t.q0 + first_tok, sm.rows[warp][1]);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        __syncwarp();
+      }
+      if (drain == 2 && d_row && !(finite == 0.f && d_sum >= kSumMin && d_sum <= kSumMax)) redo |= 1ull << d_k;
+      drain = 0;
+      return true;
+    };
+    auto written = [&](int h) {  // P of a half is there
+      tmem_st_wait();
+      // O of the run or item before, before the issuer starts it anew
+      if (h == 0 && drain != 0 && !take_out()) return false;
+      tc_fence_before();
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&sm.p_full[tile][h]);
       return true;
     };
     for (int k = 0; ok && k < nt; ++k) {
-      const WpTile t = sm.tiles[k];
+      const WpItem &t = sm.items[k];
       if (t.invalid) {
-        // invalid sequence: zero this tile's rows (its tokens, query heads 4g .. 4g+3)
+        // invalid sequence: zero this item's rows (its tokens, query heads 4g .. 4g+3)
         if (t.t0 == 0 && t.g == 0 && tid == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
-        // (the last tile of more query tokens than max_query takes all that are left)
+        // (the last item of more query tokens than max_query takes all that are left)
         const long long left = t.n - t.t0;
-        const long long rows = (t.t0 + kWpTok >= a.max_query ? left : min((long long)kWpTok, left)) * kGroup * kHeadDim;
-        for (long long i = tid; i < rows; i += kWpRows) {
+        const long long toks = t.t0 + a.item_tok >= a.max_query ? left : min((long long)a.item_tok, left);
+        for (long long i = tid; i < toks * kGroup * kHeadDim; i += kWpTiles * kWpRows) {
           const long long row = (long long)t.q0 + t.t0 + i / (kGroup * kHeadDim);
           const long long at = (row * kQHeads + t.g * kGroup) * kHeadDim + i % (kGroup * kHeadDim);
           if (row < 0 || row >= a.num_q_rows) continue;
@@ -621,114 +774,160 @@ __global__ void __launch_bounds__(kWpThreads, kWpCtasPerSm) window_prefill_kerne
         continue;
       }
       if (!t.run) continue;
+      const WpTile w = tile_of(a, t, tile);
+      if (w.last < 0) {
+        fetch_q(k + 1);
+        gb += t.nblocks;
+        continue;
+      }
+      tmem_st32(lane_base + kColQ + tile * (kHeadDim / 2), qn);
+      tc_fence_before();
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&sm.q_full[tile]);
+      fetch_q(k + 1);
       const int pos = t.ctx - t.n + min(t.t0 + tok, t.n - 1);
       const int lo = max(0, pos - a.window + 1);
-      // reference max of the row's sigma * s (sigma = sign of scale): the exponents are
-      // |scale| log2(e) (sigma s - m) = (sigma |scale| log2(e)) (s - sigma m)
-      float m_ref = -INFINITY;
-      const float sig = a.neg ? -1.f : 1.f;
-      const float2 c2 = make_float2(sig * a.scale_log2, sig * a.scale_log2);
-      for (int j = 0; j < t.nblocks; ++j, ++gb) {
-        const int b = int(gb & 1), st = int(gb % kWpStages);
-        // S of block j, and (already complete) the stage's load, for its bad-page mask
-        bool w = wp_wait(sm, &sm.s_full[b], uint32_t(gb >> 1) & 1, a.status) &&
-                 wp_wait(sm, &sm.kv_full[st], uint32_t(gb / kWpStages) & 1, a.status);
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        float sv[64];
-        {
-          uint32_t x0[32], x1[32];
-          tmem_ld32(lane_base + kColS + b * kWpKeys, x0);
-          tmem_ld32(lane_base + kColS + b * kWpKeys + 32, x1);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            sv[c] = __uint_as_float(x0[c]);
-            sv[32 + c] = __uint_as_float(x1[c]);
-          }
-        }
-        // keys outside the row's window and sinks, and the keys of invalid pages (loaded as zeros), are masked: left
-        // out of the max, weight 0
-        const int bad = sm.kv_bad[st];
-        const int page0 = logical_page(t, j * kWpPagesPerBlock) * kPageTokens;                            // first key
-        const int page3 = logical_page(t, j * kWpPagesPerBlock + kWpPagesPerBlock - 1) * kPageTokens;
-        const bool masked = !(page3 + kPageTokens - 1 <= pos && page0 >= lo && bad == 0);
-        uint64_t valid = ~0ull;
-        if (masked) {
-          valid = 0;
-#pragma unroll
-          for (int pp = 0; pp < kWpPagesPerBlock; ++pp) {
-            const int key0 = logical_page(t, j * kWpPagesPerBlock + pp) * kPageTokens;
-            const unsigned seen = first_keys(pos + 1 - key0) & (~first_keys(lo - key0) | first_keys(a.sinks - key0));
-            if (!((bad >> pp) & 1)) valid |= uint64_t(seen & 0xffffu) << (pp * kPageTokens);
-          }
-        }
-        const float mx = signed_max(sv, masked, valid, a.neg != 0);  // in units of sigma * s
-        // move the reference max on the first block that has a key for the row, and when a block's max passes it
-        // by more than 8 in the exponent (a factor 2^8)
-        const bool move = mx > m_ref + a.move_thresh && m_ref > -INFINITY;  // (O is zero before a row's first key)
-        float alpha = 1.f;
-        if (move) alpha = ex2_approx((m_ref - mx) * a.scale_log2);
-        if (move || m_ref == -INFINITY) m_ref = mx;
-        const float m_use = m_ref == -INFINITY ? 0.f : sig * m_ref;  // (a row without a key so far)
-        // P = 2^((s - m) * scale log2 e) as bf16 hi + lo, keys 2c and 2c + 1 packed in
-        // column c (the A operand of P V); the row sum comes from P V's ones column
-        uint32_t hi[32], plo[32];
-        if (!masked)
-          block_probs<false, !kBf16Out>(sv, valid, m_use, c2, hi, plo);
-        else
-          block_probs<true, !kBf16Out>(sv, valid, m_use, c2, hi, plo);
-        // P overwrites this block's S in tensor memory (its S is in registers; the P V
-        // that last read this buffer finished before S was written)
-        tmem_st32(lane_base + kColS + b * kWpKeys, hi);
-        if (!kBf16Out) tmem_st32(lane_base + kColS + b * kWpKeys + 32, plo);
-        if (j == 0 && fin && !finish()) {  // the previous tile's P V is done once this P is out
-          ok = false;
-          break;
-        }
-        if (j >= 1 && __any_sync(0xffffffffu, move)) {
-          // a row's reference max moved: once the previous block's P V is done, rescale
-          // its O and row sum (before a tile's first block there is nothing to rescale)
-          w = wp_wait(sm, &sm.p_free[(gb - 1) & 1], uint32_t((gb - 1) >> 1) & 1, a.status);
-          if (!__all_sync(0xffffffffu, w)) {
+      const int front = t.front, skip = t.skip, nblocks = t.nblocks;
+      auto first_key = [&](int v) { return (v < front ? v : v + skip) * kPageTokens; };  // of page v
+      // blocks inner0 .. inner1 - 1 hold only keys that every row of the warp sees: from the last row's window on, up to the
+      // first row's position
+      const int pos0 = __shfl_sync(0xffffffffu, pos, 0), lo31 = __shfl_sync(0xffffffffu, lo, 31);
+      const int inner0 = ((lo31 + kPageTokens - 1) / kPageTokens - skip + kWpPagesPerBlock - 1) / kWpPagesPerBlock;
+      const int inner1 = ((pos0 + 1) / kPageTokens - skip) / kWpPagesPerBlock;
+      float m = 0.f;                     // the exponents' reference, times log2(e) scale
+      float sum = 0.f, run_sum = 0.f;    // of the finished runs, and of this one
+      int used = 0;
+      bool more = false;
+      uint32_t x0[32], x1[32];  // quarters of S
+      bool loaded = false;      // the next block's first one has been asked for
+#pragma unroll 1
+      for (int j = w.begin();; j = w.next(j)) {
+        if (!loaded) {
+          if (!wp_wait(sm, &sm.s_full[tile][0], blocks & 1, a.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[32];
-            tmem_ld32(lane_base + kColO + 32 * half, o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st32(lane_base + kColO + 32 * half, o);
-          }
-          tmem_st1(lane_base + kColO + kHeadDim,
-                   __float_as_uint(__uint_as_float(tmem_ld1(lane_base + kColO + kHeadDim)) * alpha));
         }
-        tc_fence_before();  // the reads of O above precede this tile's first P V (ordered by p_full)
-        mbar_arrive(&sm.p_full[b]);
+        const int bad = sm.kv_bad[(gb + j) % kWpStages];
+        if (used == 0) {
+          // the reference: from the block's first 64 keys (any finite value near the scores will do)
+          uint32_t y[32];
+          tmem_ld32(s_addr, y);
+          m = scale < 0.f ? extreme32<true>(y) : extreme32<false>(y);
+          tmem_ld32(s_addr + 32, y);
+          m = (scale < 0.f ? fminf(m, extreme32<true>(y)) : fmaxf(m, extreme32<false>(y))) * scale;
+          if (!(fabsf(m) < INFINITY)) m = 0.f;
+        }
+        // P overwrites the columns of the S that it comes from.  Keys outside the row's window and sinks, and the keys of
+        // invalid pages (loaded as zeros), get weight 0.
+        if (bad == 0 && j >= inner0 && j < inner1) {
+          // every quarter is on its way while the one before it is worked on
+          uint32_t p16[kBf16Out ? 16 : 32];
+          if (!loaded) tmem_ld32_async(s_addr, x0);
+          tmem_ld32_wait(x0);
+          tmem_ld32_async(s_addr + 32, x1);
+          run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
+          store_p(s_addr, p16);
+          tmem_ld32_wait(x1);
+          ok = wp_wait(sm, &sm.s_full[tile][1], blocks & 1, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld32_async(s_addr + 64, x0);
+          run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
+          store_p(s_addr + 32, p16);
+          if (!written(0)) {
+            ok = false;
+            break;
+          }
+          tmem_ld32_wait(x0);
+          tmem_ld32_async(s_addr + 96, x1);
+          run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
+          store_p(s_addr + 64, p16);
+          tmem_ld32_wait(x1);
+          loaded = j + 1 < inner1 && j < w.last &&
+                   __all_sync(0xffffffffu, mbar_try_wait(&sm.s_full[tile][0], (blocks + 1) & 1));
+          if (loaded) {
+            tc_fence_after();
+            tmem_ld32_async(s_addr, x0);
+          }
+          run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
+          store_p(s_addr + 96, p16);
+          written(1);
+        } else {
+          if (loaded) tmem_ld32_wait(x0);  // (asked for before the block's bad pages were known)
+          loaded = false;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) {
+              if (!wp_wait(sm, &sm.s_full[tile][1], blocks & 1, a.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            // columns of [0, pos] without those before the window, or with the sinks among them (where pages are left out,
+            // the sinks lie before them and the window behind); invalid pages take theirs out
+            const int at0 = j * kWpKeys + h * kWpHalf, shift = skip * kPageTokens + at0;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+              uint32_t valid = first_bits(pos + 1 - shift - 32 * part) &
+                               (~first_bits(lo - shift - 32 * part) | first_bits(a.sinks - at0 - 32 * part));
+              if ((bad >> (4 * h + 2 * part)) & 1) valid &= 0xffff0000u;
+              if ((bad >> (4 * h + 2 * part)) & 2) valid &= 0x0000ffffu;
+              uint32_t p16[kBf16Out ? 16 : 32];
+              if (__any_sync(0xffffffffu, valid != 0u)) {
+                tmem_ld32(s_addr + h * kWpHalf + 32 * part, x0);
+                if (__all_sync(0xffffffffu, valid == ~0u))
+                  run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
+                else
+                  run_sum += quarter_probs<true, !kBf16Out>(x0, valid, m, scale, p16);
+              } else {  // keys that none of the warp's rows sees
+#pragma unroll
+                for (int i = 0; i < (kBf16Out ? 16 : 32); ++i) p16[i] = 0u;
+              }
+              store_p(s_addr + h * kWpHalf + 32 * part, p16);
+            }
+            if (!written(h)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (!ok) break;
+        ++blocks;
+        if (++used % kWpRun == 0) {
+          sum += run_sum;  // row sums in two levels: equal weights round the same way at every addition
+          run_sum = 0.f;
+          if (!kBf16Out) {
+            drain = 1;
+            d_more = more;
+            d_k = k;
+            more = true;
+          }
+        }
+        if (j == w.last) break;
       }
       if (!ok) break;
-      fin = true;
-      fin_q0 = t.q0;
-      fin_t0 = t.t0;
-      fin_n = t.n;
-      fin_g = t.g;
-      fin_k = k;
+      gb += nblocks;
+      // the item's last block: what is taken out last is divided
+      d_more = drain == 1 ? d_more : more;
+      drain = 2;
+      d_k = k;
+      d_sum = sum + run_sum;
     }
-    if (ok && fin) finish();
+    if (ok && drain != 0) take_out();
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // every row has been written
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kWpLoader) {
     tc_fence_after();
     tmem_dealloc(tmem, kWpTmemCols);
   }
   for (int k = 0; redo != 0; ++k, redo >>= 1)
-    if (redo & 1) recompute_row<kBf16Out>(a, sm.tiles[k], tid >> 2, tid & 3);
+    if (redo & 1) recompute_row<kBf16Out>(a, sm.items[k], (tid >> 7) * kWpTok + ((tid & 127) >> 2), tid & 3);
 }
 
 // Shared-memory limits of the kernels on the current device.
@@ -777,14 +976,20 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   if (!pkv::aligned16(q) || !pkv::aligned16(out) || (reinterpret_cast<uintptr_t>(query_start) & 3u) ||
       (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return PKV_ERR_ALIGN;
-  const long long tiles = (max_query + pkv::kWpTok - 1) / pkv::kWpTok;
-  if ((long long)num_seqs * tiles * pkv::kKvHeads > 0x3fffffffLL) return PKV_ERR_SHAPE;
+  const int sms = pkv::device_sm_count() > 0 ? pkv::device_sm_count() : 148;
+  // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 10.5 us so and 12.1 in
+  // items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 56 us and 41.
+  const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
+  const int item_tok = (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
+  const long long items = (max_query + item_tok - 1) / item_tok;
+  if ((long long)num_seqs * items * pkv::kKvHeads > 0x3fffffffLL) return PKV_ERR_SHAPE;
   rc = pkv::setup_window_attributes();
   if (rc != PKV_OK) return rc;
   pkv::WindowArgs a;
   rc = pkv::pool_tensor_maps(pool, pkv::kPageTokens, &a.tmap_k, &a.tmap_v);
   if (rc != PKV_OK) return rc;
-  rc = pkv::query_tensor_map(q, num_q_rows, pkv::kQHeads, pkv::kHeadDim, pkv::kGroup, pkv::kWpTok, &a.tmap_q);
+  rc = pkv::output_tensor_map(out, num_q_rows, pkv::kQHeads, pkv::kHeadDim, (flags & PKV_OUT_BF16) != 0, pkv::kGroup, 8,
+                              &a.tmap_o);
   if (rc != PKV_OK) return rc;
   a.num_pages = pool->num_pages;
   a.num_q_rows = num_q_rows;
@@ -802,22 +1007,19 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   a.num_seqs = num_seqs;
   a.max_context = max_context;
   a.max_query = max_query;
-  a.tiles_per_seq = int(tiles);
-  a.scale_log2 = fabsf(scale) * pkv::kLog2e;
-  a.move_thresh = a.scale_log2 > 0.f ? pkv::kRescaleLog2 / a.scale_log2 : INFINITY;
-  a.neg = scale < 0.f ? 1 : 0;
+  a.item_tok = item_tok;
+  a.items_per_seq = int(items);
+  a.scale_log2 = scale * pkv::kLog2e;
   a.status = device_status;
-  a.num_tiles = int((long long)num_seqs * tiles * pkv::kKvHeads);
-  const int sms = pkv::device_sm_count();
-  const int resident = (sms > 0 ? sms : 148) * pkv::kWpCtasPerSm;
-  const int by_table = (a.num_tiles + pkv::kWpMaxTiles - 1) / pkv::kWpMaxTiles;  // tiles per CTA <= kWpMaxTiles
-  const int g = resident > by_table ? resident : by_table;
+  a.most_items = int((long long)num_seqs * items * pkv::kKvHeads);
+  const int by_table = (a.most_items + pkv::kWpMaxItems - 1) / pkv::kWpMaxItems;  // items per CTA <= kWpMaxItems
+  const int g = sms > by_table ? sms : by_table;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.num_tiles < g ? a.num_tiles : g));
+  cfg.gridDim = dim3(unsigned(a.most_items < g ? a.most_items : g));
   cfg.blockDim = dim3(pkv::kWpThreads);
   cfg.dynamicSmemBytes = pkv::kWpSmemBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  // programmatic stream serialization: the set-up (tile table, block-table entries, the first tile's Q) overlaps the
+  // programmatic stream serialization: the set-up (item table, block-table entries, the first item's Q) overlaps the
   // end of the kernel before this one
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
