@@ -43,6 +43,7 @@ constexpr int kBoxBytes = kPageTokens * kRowBytes;           // one head's K (or
 constexpr int kUnitOut = kGroup * kHeadDim;                  // output values of a unit: 256
 constexpr int kScorePage = kPageTokens * int(sizeof(float4));  // scores of a page: 256 B
 constexpr int kChipPages = 448;                              // pages of a CTA whose scores fit into shared memory
+constexpr int kSumsAhead = 8;                                // sums of a thread fetched before they are needed
 constexpr int kMinPages = 4;                                 // pages a CTA of a cluster gets at the least
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kUnitOut == kUnitThreads, "a thread owns one output value");
@@ -308,6 +309,17 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
     if (hrow < kGroup) *reinterpret_cast<float2 *>(&sm.acc[warp][hrow][8 * nd + 2 * quad]) = make_float2(v0, v1);
   }
   if (hrow < kGroup && quad == 0) sm.ml[warp][hrow] = make_float2(m_run, l_run);
+  // the sums of the CTA's first tokens, on their way while the states are merged
+  const int first = pa * kPageTokens, behind = int(min((long long)ctx, (long long)pb * kPageTokens));
+  float *sums = kWeights ? a.sums + (long long)s * a.seq_stride + (long long)g * a.head_stride : nullptr;
+  float old[kSumsAhead];
+  if (kWeights) {
+#pragma unroll
+    for (int i = 0; i < kSumsAhead; ++i) {
+      const int t = first + tid + i * kUnitThreads;
+      old[i] = t < behind && a.decay != 0.f ? sums[t] : 0.f;
+    }
+  }
   __syncthreads();
   const int h = tid / kHeadDim, d = tid % kHeadDim;
   float M = -INFINITY, L = 0.f, A = 0.f;
@@ -358,16 +370,20 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
   }
   if (kWeights) {
     const float2 f0 = sm.fin[0], f1 = sm.fin[1], f2 = sm.fin[2], f3 = sm.fin[3];
-    const int t0 = pa * kPageTokens;
-    const int t1 = int(min((long long)ctx, (long long)pb * kPageTokens));
-    float *sums = a.sums + (long long)s * a.seq_stride + (long long)g * a.head_stride;
-#pragma unroll 4
-    for (int t = t0 + tid; t < t1; t += kUnitThreads) {
-      const float4 x = sc[t - t0];
+    auto add = [&](int t, float before) {
+      const float4 x = sc[t - first];
       const float w = (ex2_approx(x.x - f0.x) * f0.y + ex2_approx(x.y - f1.x) * f1.y) +
                       (ex2_approx(x.z - f2.x) * f2.y + ex2_approx(x.w - f3.x) * f3.y);
-      sums[t] = a.decay == 0.f ? w : fmaf(a.decay, sums[t], w);
+      sums[t] = a.decay == 0.f ? w : fmaf(a.decay, before, w);
+    };
+#pragma unroll
+    for (int i = 0; i < kSumsAhead; ++i) {
+      const int t = first + tid + i * kUnitThreads;
+      if (t < behind) add(t, old[i]);
     }
+#pragma unroll 4
+    for (int t = first + tid + kSumsAhead * kUnitThreads; t < behind; t += kUnitThreads)
+      add(t, a.decay == 0.f ? 0.f : sums[t]);
   }
 }
 
