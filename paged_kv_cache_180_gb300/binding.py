@@ -411,21 +411,20 @@ def kv_copy_pages(pool: KVPool | PkvPool, src_pages: torch.Tensor, dst_pages: to
         raise PkvError(where, rc)
 
 
-def _attention_args(where: str, out, q, ints, block_tables, status) -> tuple[int, int | None]:
-    """Checks what the window and weights calls share; (flag of out's type, pointer of the status word)."""
-    dev, kind = _current_device(), out.dtype
-    for t in ints:
-        if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous():
-            _refuse(where, t, _I32)
+def _attention_args(where: str, out, q, lens, block_tables, status):
+    """Checks what the window and weights calls share; (device, flag of out's type, heads, pointer of the status word)."""
+    dev, kind, qs, os_ = _current_device(), out.dtype, q.shape, out.shape
+    if lens.dtype is not _I32 or lens.get_device() != dev or not lens.is_contiguous():
+        _refuse(where, lens, _I32)
     if q.dtype is not _BF16 or q.get_device() != dev or not q.is_contiguous():
         _refuse(where, q, _BF16)
     if block_tables.dtype is not _I32 or block_tables.get_device() != dev or block_tables.stride(-1) != 1:
         _refuse(where, block_tables, _I32)
     if (kind is not _F32 and kind is not _BF16) or out.get_device() != dev or not out.is_contiguous():
         _refuse(where, out, "float32 or bfloat16")
-    if len(q.shape) != 3 or out.shape[1:] != q.shape[1:] or len(out.shape) != 3:
+    if len(qs) != 3 or len(os_) != 3 or os_[1] != qs[1] or os_[2] != qs[2]:
         raise ValueError(f"{where}: q and out are [rows, heads, dim]")
-    return OUT_BF16 if kind is _BF16 else 0, _status_ptr(where, status, dev)
+    return dev, OUT_BF16 if kind is _BF16 else 0, qs[1], None if status is None else _status_ptr(where, status, dev)
 
 
 def paged_window_decode_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: torch.Tensor, block_tables: torch.Tensor,
@@ -437,12 +436,12 @@ def paged_window_decode_attention(pool: KVPool | PkvPool, out: torch.Tensor, q: 
     PKV_OVERLAP_PREVIOUS (only when the kernel before it on the stream writes none of q, context_lens or
     block_tables, e.g. the new tokens' kv_append)."""
     where = "pkv_paged_window_decode_attention"
-    flags, st = _attention_args(where, out, q, (context_lens,), block_tables, status)
+    _, flags, heads, st = _attention_args(where, out, q, context_lens, block_tables, status)
     num_seqs = context_lens.numel()
     if q.shape[0] < num_seqs or out.shape[0] < num_seqs:
         raise ValueError(f"{where}: {num_seqs} sequences, q has {q.shape[0]} rows and out {out.shape[0]}")
     rc = _lib.pkv_paged_window_decode_attention(
-        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q.shape[1],
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), heads,
         block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_context, scale, window, sinks,
         st, flags | (OVERLAP_PREVIOUS if overlap_previous else 0), _stream(stream))
     if rc:
@@ -458,12 +457,14 @@ def paged_window_prefill_attention(pool: KVPool | PkvPool, out: torch.Tensor, q:
     overlap_previous: launch with PKV_OVERLAP_PREVIOUS (only when the kernel before it on the stream writes none of q,
     query_start, context_lens or block_tables, e.g. the prompt's kv_append)."""
     where = "pkv_paged_window_prefill_attention"
-    flags, st = _attention_args(where, out, q, (query_start, context_lens), block_tables, status)
+    dev, flags, heads, st = _attention_args(where, out, q, context_lens, block_tables, status)
     num_seqs = context_lens.numel()
+    if query_start.dtype is not _I32 or query_start.get_device() != dev or not query_start.is_contiguous():
+        _refuse(where, query_start, _I32)
     if query_start.numel() != num_seqs + 1:
         raise ValueError(f"{where}: query_start is [seqs + 1]")
     rc = _lib.pkv_paged_window_prefill_attention(
-        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q.shape[1],
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), heads,
         min(q.shape[0], out.shape[0]), query_start.data_ptr(), block_tables.data_ptr(), block_table_stride,
         context_lens.data_ptr(), num_seqs, max_query, max_context, scale, window, sinks, st,
         flags | (OVERLAP_PREVIOUS if overlap_previous else 0), _stream(stream))
@@ -488,8 +489,8 @@ def paged_decode_attention_weights(pool: KVPool | PkvPool, out: torch.Tensor, q:
     weight_sums (float32 [seqs, kv_heads, tokens], any strides with contiguous tokens): sums = decay * sums + weights.
     out: float32 or bfloat16 [seqs, heads, dim].  overlap_previous: as for paged_window_decode_attention."""
     where = "pkv_paged_decode_attention_weights"
-    flags, st = _attention_args(where, out, q, (context_lens,), block_tables, status)
-    num_seqs, dev, shape = context_lens.numel(), _current_device(), weight_sums.shape
+    dev, flags, q_heads, st = _attention_args(where, out, q, context_lens, block_tables, status)
+    num_seqs, shape = context_lens.numel(), weight_sums.shape
     if q.shape[0] < num_seqs or out.shape[0] < num_seqs:
         raise ValueError(f"{where}: {num_seqs} sequences, q has {q.shape[0]} rows and out {out.shape[0]}")
     if weight_sums.dtype is not _F32 or weight_sums.get_device() != dev or weight_sums.stride(-1) != 1:
@@ -500,7 +501,7 @@ def paged_decode_attention_weights(pool: KVPool | PkvPool, out: torch.Tensor, q:
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         _refuse(where, workspace, "uint8")
     rc = _lib.pkv_paged_decode_attention_weights(
-        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q.shape[1],
+        ctypes.byref(pool.desc if isinstance(pool, KVPool) else pool), out.data_ptr(), q.data_ptr(), q_heads,
         block_tables.data_ptr(), block_table_stride, context_lens.data_ptr(), num_seqs, max_context, scale,
         weight_sums.data_ptr(), weight_sums.stride(0), weight_sums.stride(1), decay,
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, st,
