@@ -462,7 +462,7 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   if (rc != PKV_OK) return rc;
   if (num_seqs < 0 || num_layers < 1 || max_context < 0 || max_context > (1 << 30) || max_budget < 0 || sinks < 0 ||
       recent < 0 || block_table_stride < 0 || layer_stride < 0 || kept_stride < max_budget ||
-      pool->num_pages > (1 << 27) || sums_head_stride < max_context || sums_layer_stride < 0 || sums_seq_stride < 0 ||
+      sums_head_stride < max_context || sums_layer_stride < 0 || sums_seq_stride < 0 ||
       (long long)num_seqs * num_layers > 0x7fffffffLL / (pkv::kKvHeads * pkv::kEvMaxCluster))
     return PKV_ERR_SHAPE;
   // a row of sums belongs to one (sequence, layer, head)
@@ -494,6 +494,10 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   for (const void *p : {static_cast<const void *>(context_lens), static_cast<const void *>(budgets)})
     if (pkv::ranges_overlap(kept, list, p, lens) || pkv::ranges_overlap(new_weight_sums, sums, p, lens))
       return PKV_ERR_SHAPE;
+  if (new_context_lens != nullptr &&
+      (pkv::ranges_overlap(new_context_lens, lens, kept, list) || pkv::ranges_overlap(new_context_lens, lens, weight_sums, sums) ||
+       pkv::ranges_overlap(new_context_lens, lens, new_weight_sums, sums)))
+    return PKV_ERR_SHAPE;
   if (pkv::ranges_overlap(kept, list, weight_sums, sums) || pkv::ranges_overlap(kept, list, new_weight_sums, sums))
     return PKV_ERR_SHAPE;
   pkv::EvictArgs a;

@@ -788,7 +788,6 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       const int pos = t.ctx - t.n + min(t.t0 + tok, t.n - 1);
       const int lo = max(0, pos - a.window + 1);
       const int front = t.front, skip = t.skip, nblocks = t.nblocks;
-      auto first_key = [&](int v) { return (v < front ? v : v + skip) * kPageTokens; };  // of page v
       // blocks inner0 .. inner1 - 1 hold only keys that every row of the warp sees: from the last row's window on, up to the
       // first row's position
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0), lo31 = __shfl_sync(0xffffffffu, lo, 31);

@@ -113,6 +113,7 @@ def test_evict_refusals(b):
                      (dict(bts=-1), -2), (dict(ls=-1), -2), (dict(head=2047), -2), (dict(layer=8 * 2048 - 1), -2),
                      (dict(seq=2 * 8 * 2048 - 1), -2), (dict(new=far + 4096), -2), (dict(nl=BASE), -2), (dict(nl=BASE + 64), -2),
                      (dict(kept=far), -2), (dict(kept=2 * far + 64), -2), (dict(kept=BASE), -2), (dict(new=BASE), -2),
+                     (dict(nl=far + 4), -2), (dict(nl=2 * far), -2), (dict(nl=3 * far + 8), -2),
                      (dict(layers=1 << 25), -2)]:
         assert call(**kw) == code, kw
     assert call(n=0) == 0 and call(max=0) == 0

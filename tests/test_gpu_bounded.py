@@ -457,6 +457,33 @@ def test_weights_of_a_long_context(pkv):
         assert ((sums[0, :, :ctx].double() - want).norm() < 2e-6 * want.norm()).item() and (sums[0, :, ctx:] == 0).all()
 
 
+def test_weights_behind_the_append_that_it_overlaps(pkv):
+    c = B.Cache([900, 130, 77], seed=42)
+    host = _sums(c, 43)
+    want_sums = U.to_dev(host)
+    want, _ = _weights(pkv, c, want_sums, 0.9)
+    empty, status = _pool(pkv, oracle.Pool(c.wl.num_pages)), _status()
+    parts = [c.wl.kv_tokens(s, 0) for s in range(3)]
+    k, v = (U.to_dev(np.concatenate([p[i] for p in parts])) for i in (0, 1))
+    slots = U.to_dev(np.concatenate([c.wl.slot_mapping(s, 0, 0, int(c.lens[s])) for s in range(3)]))
+    q, bt, lens, out, sums = U.to_dev(c.q), U.to_dev(c.bt), U.to_dev(c.lens), _out(3, False), U.to_dev(host)
+    pkv.kv_append(empty, k, v, slots, status)
+    pkv.paged_decode_attention_weights(empty, out, q, bt, bt.shape[1], lens, c.max_context, c.scale, sums, 0.9, None, status,
+                                       overlap_previous=True)
+    assert np.array_equal(_guarded(out, 3), want) and torch.equal(sums, want_sums) and int(status.item()) == 0
+
+
+def test_weights_longest_first(pkv):
+    # more units than are resident at once: sequences are taken by length, ties and empty ones among them
+    r = np.random.RandomState(9)
+    contexts = r.randint(0, 200, 60).tolist() + [0, 0, 150, 150, 150, 1]
+    _check_weights(pkv, B.Cache(contexts, seed=44), 0.9)
+    c = B.Cache(contexts, seed=45)
+    c.lens[3], c.lens[10] = -4, c.max_context + 1
+    c.bt[3] = c.bt[10] = -1
+    _check_weights(pkv, c, 1.0)
+
+
 def test_weights_strides_streams_and_graphs(pkv):
     c = B.Cache([300, 130, 77], seed=39)
     host = _sums(c, 40)
@@ -566,6 +593,38 @@ def test_evict_shares_of_a_unit(pkv, contexts, layers, in_place):
     for keep, ties in ((0.5, 0), (0.9, 2), (0.07, 1)):
         e = Evict(contexts, layers, seed=42, ties=ties, extra=9)
         _check_evict(pkv, e, [max(1, int(c * keep)) for c in contexts], 4, 30, in_place)
+
+
+@pytest.mark.parametrize("contexts,blocks", [([5000], 4200), ([300] * 9 + [700], 4200), ([5000], 25600)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_bounds_far_above_the_lengths(pkv, contexts, blocks, in_place):
+    # bounds that leave the block tables, or the sums as well, in global memory, in clusters and without
+    e = Evict(contexts, seed=47, ties=2, max_blocks=blocks)
+    _check_evict(pkv, e, [c // 2 for c in contexts], 4, 30, in_place)
+
+
+def test_evict_streams_and_graphs(pkv):
+    e = Evict([700, 90], 2, seed=48)
+    want = _run_evict(pkv, e, [300, 50], 4, 30)
+    side = torch.cuda.Stream()
+    got = _run_evict(pkv, e, [300, 50], 4, 30, stream=side)
+    assert torch.equal(got[0].buffer.view(torch.int16), want[0].buffer.view(torch.int16)) and np.array_equal(got[3], want[3])
+    # captured, and replayed over fresh contents of the same buffers
+    pool, fresh = _pool(pkv, e.pool), _pool(pkv, e.pool)
+    sums, budgets, lens = U.to_dev(e.sums), U.to_dev(np.array([300, 50], np.int32)), U.to_dev(e.lens)
+    bt, kept = U.to_dev(e.bt), torch.full((2, 2, 8, 300), -1, dtype=torch.int32, device=U.dev())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.kv_evict(pool, bt, bt.stride(0), bt.stride(1), lens, budgets, sums, sums, 4, 30, e.max_context, kept)
+    for _ in range(3):
+        pool.buffer.copy_(fresh.buffer)
+        sums.copy_(U.to_dev(e.sums))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(pool.buffer.view(torch.int16), want[0].buffer.view(torch.int16))
+        assert np.array_equal(kept.cpu().numpy(), want[3])
+        assert all(torch.equal(sums[s, :, :, :n], want[2][s, :, :, :n]) for s, n in ((0, 700), (1, 90)))
 
 
 def test_evict_special_sums(pkv):
