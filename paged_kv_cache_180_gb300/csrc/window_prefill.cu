@@ -240,7 +240,9 @@ __device__ __forceinline__ float extreme32(const uint32_t (&s)[32]) {
 }
 
 // P = 2^(s c - m) for 32 keys as one or two bf16 terms, keys 2i and 2i + 1 packed in word i, the second term behind the
-// first (with kMasked, keys whose bit in `valid` is clear get 0); returns their sum.
+// first (with kMasked, keys whose bit in `valid` is clear get 0).  Returns their sum; of two terms, the sum of what they hold:
+// a weight's rounding then cancels in the quotient as far as the weight makes up the row (errors of 1.7e-6 of the output's
+// norm for 2.2e-6, 4 % of the time).  With one term that gives 2.2e-3 for 2.3e-3 and takes 12 %.
 template <bool kMasked, bool kTwo>
 __device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t valid, float m, float c,
                                                uint32_t (&p16)[kTwo ? 32 : 16]) {
@@ -254,12 +256,16 @@ __device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t
       p.x = (valid >> (2 * i)) & 1 ? p.x : 0.f;
       p.y = (valid >> (2 * i + 1)) & 1 ? p.y : 0.f;
     }
-    sum[i % 4] = add_f32x2(sum[i % 4], p);
     const uint32_t hi = pack_bf16x2(p.x, p.y);
     p16[i] = hi;
     if constexpr (kTwo) {
-      const float2 r = sub_f32x2(p, make_float2(bf16_lo(hi), bf16_hi(hi)));
-      p16[16 + i] = pack_bf16x2(r.x, r.y);
+      const float2 hf = make_float2(bf16_lo(hi), bf16_hi(hi)), r = sub_f32x2(p, hf);
+      const uint32_t lo = pack_bf16x2(r.x, r.y);
+      p16[16 + i] = lo;
+      sum[i % 4] = add_f32x2(sum[i % 4], hf);
+      sum[(i + 2) % 4] = add_f32x2(sum[(i + 2) % 4], make_float2(bf16_lo(lo), bf16_hi(lo)));
+    } else {
+      sum[i % 4] = add_f32x2(sum[i % 4], p);
     }
   }
   const float2 t = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
