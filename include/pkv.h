@@ -503,7 +503,7 @@ int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *out, const vo
  *   out, q, scale, flags  as for pkv_paged_window_decode_attention (with PKV_OVERLAP_PREVIOUS the sums are read after the
  *                  kernel before it has completed).  max_context at most 2^30.
  * A token of a page that is left out (PKV_DEV_BAD_PAGE) has weight 0.  A sequence of invalid context gets zero rows and keeps its
- * sums.  Results do not depend on timing.  One kernel launch.
+ * sums.  Strides at most 2^38 elements.  Results do not depend on timing.  One kernel launch.
  */
 int pkv_paged_decode_attention_weights(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
                                        const int32_t *block_tables, int64_t block_table_stride,
@@ -513,7 +513,7 @@ int pkv_paged_decode_attention_weights(const pkv_pool *pool, void *out, const vo
                                        void *stream);
 
 /* Workspace bytes of pkv_paged_decode_attention_weights: the scores of contexts too long to keep them on chip.  0 up to
- * max_context = 57344, and on bad arguments. */
+ * max_context = 57344, and on bad arguments (more than 2^24 sequences or 2^30 tokens among them). */
 size_t pkv_weights_workspace_bytes(int num_seqs, int max_context);
 
 /*
@@ -534,8 +534,9 @@ size_t pkv_weights_workspace_bytes(int num_seqs, int max_context);
  * What is written may not overlap context_lens, budgets, the sums that are read, or each other (PKV_ERR_SHAPE).
  * A context < 0 or > max_context sets PKV_DEV_BAD_CONTEXT, a budget < 0 or min(budget, ctx) > max_budget PKV_DEV_BAD_BUDGET: that
  * sequence's rows, sums and list stay, its new length is the old one.  A row whose source or target page id is
- * invalid is not moved (PKV_DEV_BAD_PAGE).  Rows behind B keep their bytes.  Sequences must not share the pages that hold
- * their tokens (pkv_alloc_write_page sees to that).  max_context at most 2^30.  No workspace, one kernel launch.
+ * invalid is not moved (PKV_DEV_BAD_PAGE).  Rows behind B keep their bytes.  No two (s, layer) may share a page that holds
+ * their tokens (pkv_alloc_write_page sees to that).  max_context at most 2^30 (0: the sums may be null), strides at most 2^38
+ * elements (kept_stride 2^31).  No workspace, one kernel launch.
  */
 int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, int64_t block_table_stride, int64_t layer_stride,
                  int num_layers, const int32_t *context_lens, const int32_t *budgets, int num_seqs, int max_context,

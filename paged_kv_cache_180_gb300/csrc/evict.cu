@@ -465,6 +465,11 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
       sums_head_stride < max_context || sums_layer_stride < 0 || sums_seq_stride < 0 ||
       (long long)num_seqs * num_layers > 0x7fffffffLL / (pkv::kKvHeads * pkv::kEvMaxCluster))
     return PKV_ERR_SHAPE;
+  // (no array has 2^38 elements; what is computed from the strides below stays within 64 bits)
+  constexpr int64_t kFar = int64_t(1) << 38;
+  if (kept_stride > kFar >> 7 || sums_head_stride > kFar || sums_layer_stride > kFar || sums_seq_stride > kFar ||
+      (num_seqs > 1 && (num_seqs - 1) * sums_seq_stride > kFar) || (num_layers - 1) * sums_layer_stride > kFar)
+    return PKV_ERR_SHAPE;
   // a row of sums belongs to one (sequence, layer, head)
   const long long heads = pkv::kKvHeads * sums_head_stride;
   const bool layers_inside = (num_layers == 1 || sums_layer_stride >= heads) &&
@@ -472,9 +477,10 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   const bool seqs_inside = (num_seqs <= 1 || sums_seq_stride >= heads) &&
                            (num_layers == 1 || sums_layer_stride >= (num_seqs <= 1 ? heads : num_seqs * sums_seq_stride));
   if (num_seqs > 0 && !layers_inside && !seqs_inside) return PKV_ERR_SHAPE;
-  if (num_seqs == 0 || max_context == 0) return PKV_OK;
-  if (block_tables == nullptr || context_lens == nullptr || budgets == nullptr || weight_sums == nullptr ||
-      new_weight_sums == nullptr || (kept == nullptr && max_budget > 0))
+  if (num_seqs == 0) return PKV_OK;
+  // (without cached tokens there are no sums, and without a budget there is no list; the new lengths are written all the same)
+  if (block_tables == nullptr || context_lens == nullptr || budgets == nullptr ||
+      ((weight_sums == nullptr || new_weight_sums == nullptr) && max_context > 0) || (kept == nullptr && max_budget > 0))
     return PKV_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
        reinterpret_cast<uintptr_t>(budgets) | reinterpret_cast<uintptr_t>(weight_sums) |

@@ -575,7 +575,7 @@ extern "C" int pkv_paged_window_decode_attention(const pkv_pool *pool, void *out
 }
 
 extern "C" size_t pkv_weights_workspace_bytes(int num_seqs, int max_context) {
-  if (num_seqs < 0 || max_context < 0) return 0;
+  if (num_seqs < 0 || num_seqs > (1 << 24) || max_context < 0 || max_context > (1 << 30)) return 0;
   const long long pages = ((long long)max_context + pkv::kPageTokens - 1) / pkv::kPageTokens;
   if (pages <= (long long)pkv::kMaxCluster * pkv::kChipPages) return 0;
   return size_t(num_seqs) * pkv::kKvHeads * size_t(pages) * pkv::kScorePage;
@@ -592,13 +592,14 @@ extern "C" int pkv_paged_decode_attention_weights(const pkv_pool *pool, void *ou
                                       num_seqs, max_context, scale, flags);
   if (rc != PKV_OK) return rc;
   if (!(decay >= 0.f && decay <= 1.f)) return PKV_ERR_SCALE;
-  if (max_context > (1 << 30)) return PKV_ERR_SHAPE;
+  constexpr int64_t kFar = int64_t(1) << 38;  // (no array has as many elements; a stride times a count stays within 64 bits)
+  if (max_context > (1 << 30) || seq_stride > kFar || head_stride > kFar) return PKV_ERR_SHAPE;
   // heads, and sequences, may not share a row of sums
   const bool heads_inside = head_stride >= max_context && (num_seqs <= 1 || seq_stride >= pkv::kKvHeads * head_stride);
   const bool seqs_inside = num_seqs > 1 && seq_stride >= max_context && head_stride >= seq_stride * num_seqs;
   if (head_stride < 0 || seq_stride < 0 || (!heads_inside && !seqs_inside)) return PKV_ERR_SHAPE;
   if (num_seqs == 0) return PKV_OK;
-  if (weight_sums == nullptr) return PKV_ERR_NULL;
+  if (weight_sums == nullptr && max_context > 0) return PKV_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(weight_sums) & 3u) return PKV_ERR_ALIGN;
   const size_t need = pkv_weights_workspace_bytes(num_seqs, max_context);
   if (need > 0 && workspace == nullptr) return PKV_ERR_NULL;

@@ -89,6 +89,10 @@ def test_weights_refusals(b):
         assert call(**kw) == code, kw
     assert call(n=0) == 0
     assert call(n=0, seq=2048, head=4 * 2048) in (0, -2)
+    for kw, code in [(dict(seq=(1 << 38) + 1), -2), (dict(head=1 << 61, seq=0), -2), (dict(max=0, sums=0, lens=0), -1)]:
+        assert call(**kw) == code, kw
+    assert b.weights_workspace_bytes((1 << 24) + 1, 70000) == 0 and b.weights_workspace_bytes(4, (1 << 30) + 1) == 0
+    assert b.weights_workspace_bytes(1 << 24, 1 << 30) == 1 << 61
     assert b.weights_workspace_bytes(4, 57344) == 0 and b.weights_workspace_bytes(-1, 70000) == 0
     assert b.weights_workspace_bytes(4, 57345) == 4 * 8 * 3585 * 16 * 16  # a float4 for every token of every unit
 
@@ -116,7 +120,13 @@ def test_evict_refusals(b):
                      (dict(nl=far + 4), -2), (dict(nl=2 * far), -2), (dict(nl=3 * far + 8), -2),
                      (dict(layers=1 << 25), -2)]:
         assert call(**kw) == code, kw
-    assert call(n=0) == 0 and call(max=0) == 0
+    assert call(n=0) == 0
+    # nothing cached: the sums may be null, not the lengths; far strides do not wrap around
+    for kw, code in [(dict(max=0, sums=0, new=0, lens=0), -1), (dict(max=0, sums=0, new=0, budget=4, kept=0), -1),
+                     (dict(seq=(1 << 38) + 1), -2), (dict(seq=1 << 62), -2), (dict(n=5, seq=1 << 37), -2),
+                     (dict(layer=1 << 62), -2), (dict(layers=6, layer=1 << 37), -2), (dict(head=1 << 61), -2),
+                     (dict(ks=(1 << 31) + 1), -2)]:
+        assert call(**kw) == code, kw
 
 
 # ---- the oracle itself -----------------------------------------------------------------------

@@ -694,6 +694,72 @@ def test_evict_refusals_of_the_binding(pkv):
         assert err.value.code == -2
 
 
+def test_nothing_cached(pkv):
+    """Bounds of 0: zero rows, lengths of 0, and the report where a length is not 0."""
+    e = Evict([100, 40], 2, seed=47)
+    pool, bt = _pool(pkv, e.pool), U.to_dev(e.bt)
+    sums = torch.empty(2, 2, 8, 0, device=U.dev())
+    for lens, new, code in (([0, 0], [0, 0], 0), ([0, 40], [0, 40], 2)):
+        lens, budgets, status = U.to_dev(np.array(lens, np.int32)), U.to_dev(np.array([7, 0], np.int32)), _status()
+        kept = torch.zeros(2, 2, 8, 0, dtype=torch.int32, device=U.dev())
+        got = torch.full((2,), -1, dtype=torch.int32, device=U.dev())
+        pkv.kv_evict(pool, bt, bt.stride(0), bt.stride(1), lens, budgets, sums, sums, 4, 4, 0, kept, got, status)
+        assert got.cpu().tolist() == new and int(status.item()) == code
+        q, out, status = torch.zeros(2, 32, 64, dtype=torch.bfloat16, device=U.dev()), torch.ones(2, 32, 64, device=U.dev()), _status()
+        pkv.paged_decode_attention_weights(pool, out, q, bt[:, 0], bt.stride(0), lens, 0, 0.125, sums[:, 0], 1.0, None, status)
+        assert (out == 0).all() and int(status.item()) == code
+        out.fill_(1)
+        pkv.paged_window_decode_attention(pool, out, q, bt[:, 0], bt.stride(0), lens, 0, 0.125, 8, 1, status)
+        assert (out == 0).all() and int(status.item()) == code
+    assert np.array_equal(U.bits(pool.view()), e.pool.data)
+
+
+def test_attention_refusals_of_the_binding(pkv):
+    e = Evict([100, 40], 1, seed=48)
+    pool, bt, lens = _pool(pkv, e.pool), U.to_dev(e.bt[:, 0]), U.to_dev(np.array([100, 40], np.int32))
+    q, out = torch.zeros(2, 32, 64, dtype=torch.bfloat16, device=U.dev()), torch.ones(2, 32, 64, device=U.dev())
+    start, sums = U.to_dev(np.array([0, 1, 2], np.int32)), torch.zeros(2, 8, e.max_context, device=U.dev())
+    base = dict(out=out, q=q, bt=bt, lens=lens, start=start, sums=sums, ws=None, status=None)
+
+    def window(**kw):
+        a = base | kw
+        pkv.paged_window_decode_attention(pool, a["out"], a["q"], a["bt"], 64, a["lens"], e.max_context, 0.125, 8, 1, a["status"])
+
+    def prefill(**kw):
+        a = base | kw
+        pkv.paged_window_prefill_attention(pool, a["out"], a["q"], a["start"], a["bt"], 64, a["lens"], 1, e.max_context, 0.125, 8,
+                                           1, a["status"])
+
+    def weights(**kw):
+        a = base | kw
+        pkv.paged_decode_attention_weights(pool, a["out"], a["q"], a["bt"], 64, a["lens"], e.max_context, 0.125, a["sums"], 1.0,
+                                           a["ws"], a["status"])
+
+    common = (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:, :, ::2]), dict(q=q.view(64, 64)), dict(out=out.half()),
+              dict(out=out.cpu()), dict(out=out[:, :16]), dict(out=out[..., :32].contiguous()), dict(lens=lens.long()),
+              dict(lens=lens.cpu()), dict(bt=bt.long()), dict(bt=bt[:, ::2]), dict(bt=bt.cpu()), dict(status=start.long()))
+    for call in (window, prefill, weights):
+        for kw in common:
+            with pytest.raises(ValueError):
+                call(**kw)
+    for call in (window, weights):
+        for kw in (dict(q=q[:1]), dict(out=out[:1])):
+            with pytest.raises(ValueError):
+                call(**kw)
+    for kw in (dict(start=start.long()), dict(start=start[:2]), dict(start=start.cpu())):
+        with pytest.raises(ValueError):
+            prefill(**kw)
+    for kw in (dict(sums=sums.double()), dict(sums=sums[:1]), dict(sums=sums[:, :4]), dict(sums=sums[..., :-1]),
+               dict(sums=sums.transpose(1, 2)), dict(sums=sums.cpu()), dict(ws=torch.zeros(16))):
+        with pytest.raises(ValueError):
+            weights(**kw)
+    for kw in (dict(sums=sums[:, :1].expand(2, 8, -1)), dict(sums=sums[:1].expand(2, -1, -1))):  # shared elements
+        with pytest.raises(pkv.PkvError) as err:
+            weights(**kw)
+        assert err.value.code == -2
+    assert (out == 1).all() and (sums == 0).all()
+
+
 # ---- together -----------------------------------------------------------------------------------------
 def test_a_bounded_cache_from_prompt_to_eviction_and_on(pkv):
     """Two layers: prompts by windowed prefill, decode steps that add up weights, eviction, pages given back, decode steps on
