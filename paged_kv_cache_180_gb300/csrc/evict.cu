@@ -27,8 +27,10 @@ namespace {
 constexpr int kEvMaxCluster = 8;
 constexpr int kEvChunks = 2 * kRowBytes / 16;  // 16-byte chunks of a row's K and V: 16
 constexpr int kEvLook = 512;                   // rows of a CTA whose old positions are fetched at once
-constexpr int kMaxBins = 2048;                 // of a digit of 11 bits, or of one of 8 bits in eight copies
+constexpr int kMaxBins = 2048;                 // of a digit of 11 bits, or of one of 9 bits in four copies
+constexpr int kClusterBins = 512;
 constexpr int kRun = 4;                        // tokens of a thread in one step of the list
+constexpr int kStep = 32 * kRun;               // tokens of a warp in one
 constexpr int kEvMaxPages = 4096;              // block-table entries that a CTA may hold (16 KiB)
 constexpr size_t kEvMaxSmem = 200 * 1024;      // dynamic shared memory of a CTA at the most
 
@@ -57,9 +59,10 @@ template <int kThreads>
 struct EvictSmem {
   unsigned warp_part[2][kThreads / 32];
   int2 warp_count[kThreads / 32];  // (kept for certain, equal to the threshold) of a warp's tokens
-  int2 rank_count[kEvMaxCluster];  // the same of every CTA of the cluster
+  int2 count;                      // of the CTA's tokens
   int from[2][kEvLook];            // old positions of the CTA's next rows
-  unsigned bins[2][256];           // cluster: the CTA's counts of a pass
+  unsigned bins[2][kClusterBins];  // cluster: the CTA's counts of a pass
+  uint2 range;                     // cluster: smallest and largest key of the CTA's candidates
   unsigned digit, need;
   int whole;
 };
@@ -89,17 +92,13 @@ __device__ __forceinline__ unsigned ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void st_cluster_s2(uint32_t addr, int2 v) {
-  asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-
 // kRows: rows of a round and CTA; kRing: rounds whose rows are held or on their way; kStaged: sums in shared memory.
 template <int kThreads, int kRows, int kRing, bool kStaged, bool kCluster>
 __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
-  // digits: 11, 11 and 10 bits in a CTA of its own; 8 bits each in a cluster, where every CTA reads every other's bins
-  constexpr int kDigit = kCluster ? 8 : 11, kPasses = kCluster ? 4 : 3, kBins = 1 << kDigit;
-  constexpr int kCopies = kCluster ? 8 : 1;  // of every bin: few bins and many keys of nearly the same exponent
-  constexpr int kWarps = kThreads / 32, kTile = kRun * kThreads, kThreadBins = kBins > kThreads ? kBins / kThreads : 1;
+  // digits: 11, 11 and 10 bits in a CTA of its own; 9 bits each in a cluster, where every CTA reads every other's bins
+  constexpr int kDigit = kCluster ? 9 : 11, kBins = 1 << kDigit, kCopies = kMaxBins / kBins;
+  static_assert(!kCluster || kBins == kClusterBins, "");
+  constexpr int kWarps = kThreads / 32, kThreadBins = kBins > kThreads ? kBins / kThreads : 1;
   constexpr int kRowStep = kThreads / kEvChunks, kLoads = kRows / kRowStep, kRounds = kEvLook / kRows;
   static_assert(kRounds >= kRing && kLoads >= 1, "");
   __shared__ EvictSmem<kThreads> sm;
@@ -163,15 +162,40 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
     ties = need;
   } else if (need > 0) {
     const int c0 = max(p0, head), c1 = min(p1, tail);
-    unsigned prefix = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < kPasses; ++pass) {
-      const int shift = max(0, 32 - kDigit * (pass + 1)), bits = min(kDigit, 32 - kDigit * pass);
+    unsigned lo = 0;  // keys looked at: lo <= key < lo + 2^(shift + kDigit)
+    int shift = 32 - kDigit;
+    if (kCluster) {
+      // many keys of nearly the same exponent: the digits divide the range that there is
+      unsigned least = ~0u, most = 0u;
 #pragma unroll 4
       for (int t = c0 + tid; t < c1; t += kThreads) {
         const unsigned key = sum_key(sum_at(t));
-        if (pass == 0 || key >> (shift + bits) == prefix)
-          atomicAdd(&hists[(key >> shift & ((1u << bits) - 1u)) * kCopies + lane % kCopies], 1u);
+        least = min(least, key);
+        most = max(most, key);
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) sm.warp_part[0][warp] = least, sm.warp_part[1][warp] = most;
+      __syncthreads();
+      if (tid < 32) {
+        least = __reduce_min_sync(0xffffffffu, tid < kWarps ? sm.warp_part[0][tid] : ~0u);
+        most = __reduce_max_sync(0xffffffffu, tid < kWarps ? sm.warp_part[1][tid] : 0u);
+        if (tid == 0) sm.range = make_uint2(least, most);
+      }
+      cluster_sync();
+      const uint32_t there = cluster_map(smem_addr(&sm.range), uint32_t((lane + rank) % C));
+      least = __reduce_min_sync(0xffffffffu, ld_cluster_u32(there));
+      most = __reduce_max_sync(0xffffffffu, ld_cluster_u32(there + 4));
+      lo = least;
+      shift = max(0, 32 - __clz(int(most - least)) - kDigit);
+    }
+    int bits = kDigit;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+#pragma unroll 4
+      for (int t = c0 + tid; t < c1; t += kThreads) {
+        const unsigned d = (sum_key(sum_at(t)) - lo) >> shift;
+        if (d < 1u << bits) atomicAdd(&hists[d * kCopies + lane % kCopies], 1u);
       }
       __syncthreads();
       // this thread's bins over the cluster, and the keys in them and in all bins above; the next pass starts from 0
@@ -227,15 +251,19 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
         }
       }
       __syncthreads();
-      prefix = prefix << bits | sm.digit;
+      lo += sm.digit << shift;
       need = sm.need;
-      if (sm.whole) {  // every key with this prefix is kept
-        T = (prefix << shift) - 1u;
-        ties = 0;
+      if (sm.whole) {  // every key from lo on is kept
+        T = lo - 1u;
         break;
       }
-      T = prefix;
-      ties = need;
+      if (shift == 0) {
+        T = lo;
+        ties = need;
+        break;
+      }
+      bits = min(kDigit, shift);
+      shift -= bits;
     }
   }
 
@@ -246,54 +274,63 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
     sure = in && (fixed || key > T);
     equal = in && !fixed && key == T;
   };
-  int2 before = make_int2(0, 0);  // (kept for certain, equal to T) in front of this CTA's tokens
-  if (kCluster) {
-    int2 count = make_int2(0, 0);
-#pragma unroll 4
-    for (int t = p0 + tid; t < p1; t += kThreads) {
-      bool sure, equal;
-      classify(t, sum_at(t), sure, equal);
-      count.x += sure;
-      count.y += equal;
-    }
-    count.x = __reduce_add_sync(0xffffffffu, count.x);
-    count.y = __reduce_add_sync(0xffffffffu, count.y);
-    if (lane == 0) sm.warp_count[warp] = count;
-    __syncthreads();
-    if (tid < C) {
-      int2 all = make_int2(0, 0);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        all.x += sm.warp_count[w].x;
-        all.y += sm.warp_count[w].y;
-      }
-      st_cluster_s2(cluster_map(smem_addr(&sm.rank_count[rank]), uint32_t(tid)), all);
-    }
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      before.x += sm.rank_count[r].x;
-      before.y += sm.rank_count[r].y;
-    }
-  }
-  // (sums held here are written over from now on: the barriers above followed the last CTA's copy of them)
-#pragma unroll 1
-  for (int base = p0; base < p1; base += kTile) {
-    const int t = base + tid * kRun;
-    float v[kRun];
-    if (kStaged) {  // (the buffer holds whole tiles; what lies behind p1 is not looked at)
+  // every warp looks at an equal run of the CTA's tokens, twice: to count, and to write
+  const int run = ((p1 - p0 + kWarps - 1) / kWarps + kRun - 1) / kRun * kRun;
+  const int w0 = p0 + warp * run, w1 = min(p1, w0 + run);
+  float v[kRun];
+  unsigned sure, equal;  // bit j: token t + j
+  auto look = [&](int t) {
+    if (kStaged) {  // (the buffer goes on behind p1; what lies there is not used)
       *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(own + (t - p0));
     } else {
 #pragma unroll
-      for (int j = 0; j < kRun; ++j) v[j] = t + j < p1 ? sums[t + j] : 0.f;
+      for (int j = 0; j < kRun; ++j) v[j] = t + j < w1 ? sums[t + j] : 0.f;
     }
-    unsigned sure = 0, equal = 0;  // bit j: token t + j
+    sure = equal = 0;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      bool x, y;
-      classify(t + j, v[j], x, y);
-      sure |= unsigned(x) << j;
-      equal |= unsigned(y) << j;
+      const bool in = t + j < w1, fixed = unsigned(t + j - head) >= unsigned(tail - head);
+      const unsigned key = sum_key(v[j]);
+      sure |= unsigned(in && (fixed || key > T)) << j;
+      equal |= unsigned(in && !fixed && key == T) << j;
     }
+  };
+  int2 before = make_int2(0, 0);  // (kept for certain, equal to T) in front of this warp's tokens
+#pragma unroll 2
+  for (int base = w0; base < w1; base += kStep) {
+    look(base + lane * kRun);
+    before.x += __popc(sure);
+    before.y += __popc(equal);
+  }
+  before.x = __reduce_add_sync(0xffffffffu, before.x);
+  before.y = __reduce_add_sync(0xffffffffu, before.y);
+  if (lane == 0) sm.warp_count[warp] = before;
+  __syncthreads();
+  before = make_int2(0, 0);
+  int2 all = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int2 c = sm.warp_count[w];
+    if (w < warp) before.x += c.x, before.y += c.y;
+    all.x += c.x;
+    all.y += c.y;
+  }
+  if (kCluster) {
+    if (tid == 0) sm.count = all;
+    cluster_sync();
+    int2 c = make_int2(0, 0);  // of the CTAs in front
+    if (lane < rank) {
+      const uint32_t there = cluster_map(smem_addr(&sm.count), uint32_t(lane));
+      c = make_int2(int(ld_cluster_u32(there)), int(ld_cluster_u32(there + 4)));
+    }
+    before.x += __reduce_add_sync(0xffffffffu, c.x);
+    before.y += __reduce_add_sync(0xffffffffu, c.y);
+  }
+  // (sums held here are written over from now on: the barriers above followed the last CTA's copy of them)
+#pragma unroll 2
+  for (int base = w0; base < w1; base += kStep) {
+    const int t = base + lane * kRun;
+    look(t);
     const unsigned mine = unsigned(__popc(sure)) | unsigned(__popc(equal)) << 16;
     unsigned upto = mine;
 #pragma unroll
@@ -301,16 +338,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
       const unsigned y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    if (lane == 31) sm.warp_part[0][warp] = upto;
-    __syncthreads();
-    unsigned all = 0, front = upto - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const unsigned x = sm.warp_part[0][w];
-      if (w < warp) front += x;
-      all += x;
-    }
-    unsigned x = unsigned(before.x) + (front & 0xffffu), y = unsigned(before.y) + (front >> 16);
+    unsigned x = unsigned(before.x) + ((upto - mine) & 0xffffu), y = unsigned(before.y) + ((upto - mine) >> 16);
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       const bool is = sure >> j & 1, eq = equal >> j & 1;
@@ -324,9 +352,9 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
       x += is;
       y += eq;
     }
-    before.x += int(all & 0xffffu);
-    before.y += int(all >> 16);
-    __syncthreads();  // the warps' counts have been read
+    const unsigned step = __shfl_sync(0xffffffffu, upto, 31);
+    before.x += int(step & 0xffffu);
+    before.y += int(step >> 16);
   }
   barrier();  // the list is complete, and nobody reads sums for the selection any more
   if (!kStaged) {
