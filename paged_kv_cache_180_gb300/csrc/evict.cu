@@ -61,7 +61,8 @@ struct EvictSmem {
   int2 warp_count[kThreads / 32];  // (kept for certain, equal to the threshold) of a warp's tokens
   int2 count;                      // of the CTA's tokens
   int from[2][kEvLook];            // old positions of the CTA's next rows
-  unsigned bins[2][kClusterBins];  // cluster: the CTA's counts of a pass
+  // cluster: the CTA's counts of a pass; what the CTAs have in the bins that this one adds up; the sums; those of each 32 bins
+  unsigned bins[kClusterBins], part[kClusterBins], share[kClusterBins], group[kClusterBins / 32];
   uint2 range;                     // cluster: smallest and largest key of the CTA's candidates
   unsigned digit, need;
   int whole;
@@ -97,7 +98,7 @@ template <int kThreads, int kRows, int kRing, bool kStaged, bool kCluster>
 __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
   // digits: 11, 11 and 10 bits in a CTA of its own; 9 bits each in a cluster, where every CTA reads every other's bins
   constexpr int kDigit = kCluster ? 9 : 11, kBins = 1 << kDigit, kCopies = kMaxBins / kBins;
-  static_assert(!kCluster || kBins == kClusterBins, "");
+  static_assert(!kCluster || (kBins == kClusterBins && kBins == kThreads), "");
   constexpr int kWarps = kThreads / 32, kThreadBins = kBins > kThreads ? kBins / kThreads : 1;
   constexpr int kRowStep = kThreads / kEvChunks, kLoads = kRows / kRowStep, kRounds = kEvLook / kRows;
   static_assert(kRounds >= kRing && kLoads >= 1, "");
@@ -198,8 +199,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
         if (d < 1u << bits) atomicAdd(&hists[d * kCopies + lane % kCopies], 1u);
       }
       __syncthreads();
-      // this thread's bins over the cluster, and the keys in them and in all bins above; the next pass starts from 0
-      unsigned c[kThreadBins] = {};
+      unsigned c[kThreadBins] = {};  // this thread's bins; the next pass starts from 0
       if (has_bins) {
 #pragma unroll
         for (int i = 0; i < kThreadBins * kCopies; ++i) {
@@ -208,46 +208,73 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
         }
       }
       if (kCluster) {
-        if (has_bins) sm.bins[pass & 1][tid] = c[0];
-        cluster_sync();  // (and what the pass before last left in bins has been read)
-        if (has_bins) {
-          unsigned part[kEvMaxCluster];  // all on their way before the first is used, and no two CTAs at the same one first
-#pragma unroll
-          for (int r = 0; r < kEvMaxCluster; ++r)
-            part[r] = r < C ? ld_cluster_u32(cluster_map(smem_addr(&sm.bins[pass & 1][tid]), uint32_t((r + rank) % C))) : 0u;
-          c[0] = 0;
-#pragma unroll
-          for (int r = 0; r < kEvMaxCluster; ++r) c[0] += part[r];
+        // Every CTA adds up its share of the bins over the cluster, and the sums of each 32 of them; the sums say which 32 hold
+        // the key of rank `need`.  (Every CTA reading all bins of all others took 5000 cycles a pass.)
+        const int slice = kBins / C;
+        sm.bins[tid] = c[0];
+        cluster_sync();
+        sm.part[tid] = ld_cluster_u32(cluster_map(smem_addr(&sm.bins[rank * slice + tid % slice]), uint32_t(tid / slice)));
+        __syncthreads();
+        if (tid < slice) {
+          unsigned x = 0;
+          for (int r = 0; r < C; ++r) x += sm.part[r * slice + tid];
+          sm.share[tid] = x;
+          x = __reduce_add_sync(0xffffffffu, x);
+          if (lane == 0) sm.group[warp] = x;
         }
-      }
-      unsigned mine = 0;
+        cluster_sync();
+        if (warp == 0) {
+          auto from_top = [&](unsigned x) {  // sum of the lanes from this one on
 #pragma unroll
-      for (int i = 0; i < kThreadBins; ++i) mine += c[i];
-      unsigned up = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_down_sync(0xffffffffu, up, o);
-        if (lane + o < 32) up += y;
-      }
-      if (lane == 0) sm.warp_part[pass & 1][warp] = up;
-      __syncthreads();
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const unsigned x = sm.warp_part[pass & 1][w];
-        if (w > warp) up += x;
-      }
-      if (up - mine < need && need <= up) {  // the bin of the key of rank `need` is one of this thread's
-        unsigned above = up - mine;
-        bool found = false;
-#pragma unroll
-        for (int i = kThreadBins - 1; i >= 0; --i) {
-          if (!found && above + c[i] >= need) {
-            found = true;
-            sm.digit = unsigned(bin0 + i);
-            sm.need = need - above;
-            sm.whole = need == above + c[i];
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned y = __shfl_down_sync(0xffffffffu, x, o);
+              if (lane + o < 32) x += y;
+            }
+            return x;
+          };
+          const int groups = slice / 32;
+          const unsigned x = lane < kBins / 32 ? ld_cluster_u32(cluster_map(smem_addr(&sm.group[lane % groups]), lane / groups)) : 0u;
+          unsigned up = from_top(x);
+          const int at = 31 - __clz(int(__ballot_sync(0xffffffffu, up >= need)));  // the group
+          const unsigned above = __shfl_sync(0xffffffffu, up - x, at);
+          const unsigned y = ld_cluster_u32(cluster_map(smem_addr(&sm.share[at % groups * 32 + lane]), uint32_t(at / groups)));
+          up = from_top(y) + above;
+          if (up - y < need && need <= up) {
+            sm.digit = unsigned(at * 32 + lane);
+            sm.need = need - (up - y);
+            sm.whole = need == up;
           }
-          above += c[i];
+        }
+      } else {
+        unsigned mine = 0;
+#pragma unroll
+        for (int i = 0; i < kThreadBins; ++i) mine += c[i];
+        unsigned up = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned y = __shfl_down_sync(0xffffffffu, up, o);
+          if (lane + o < 32) up += y;
+        }
+        if (lane == 0) sm.warp_part[pass & 1][warp] = up;
+        __syncthreads();
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const unsigned x = sm.warp_part[pass & 1][w];
+          if (w > warp) up += x;
+        }
+        if (up - mine < need && need <= up) {  // the bin of the key of rank `need` is one of this thread's
+          unsigned above = up - mine;
+          bool found = false;
+#pragma unroll
+          for (int i = kThreadBins - 1; i >= 0; --i) {
+            if (!found && above + c[i] >= need) {
+              found = true;
+              sm.digit = unsigned(bin0 + i);
+              sm.need = need - above;
+              sm.whole = need == above + c[i];
+            }
+            above += c[i];
+          }
         }
       }
       __syncthreads();
