@@ -533,7 +533,6 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     const uint32_t sa = tmem + kColS + tile * kWpKeys, oa = tmem + kColO + tile * kHeadDim,
                    qa = tmem + kColQ + tile * (kHeadDim / 2);
     const uint64_t k_desc = sw128_desc(smem_addr(sm.k), 16, 1024), v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
-    unsigned gb = 0;                // blocks of the items before
     unsigned passed = 0;            // blocks given back (each tile gives back every one of them)
     unsigned qs = 0, pvs = 0;       // Q's and blocks of P taken up
     bool ok = true;
@@ -546,8 +545,26 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       }
       return true;
     };
-    auto landed = [&](const WpItem &t, int j, unsigned st) {  // block j of the item, in stage st
-      if (!wp_wait(sm, &sm.kv_full[st], ((gb + j) / kWpStages) & 1, a.status)) return false;
+    // The blocks that the tile uses: number j of item k, which has `base` blocks before it.
+    struct Cursor {
+      int k, j;
+      unsigned base;
+      WpTile w;
+    };
+    auto first_block = [&](Cursor &c) {  // of the tile's first item at or behind c.k; false: there is none
+      for (c.k = next_run(c.k); c.k < nt; c.k = next_run(c.k + 1)) {
+        c.w = tile_of(a, sm.items[c.k], tile);
+        c.j = c.w.begin();
+        if (c.w.last >= 0) return true;
+        c.base += sm.items[c.k].nblocks;
+      }
+      return false;
+    };
+    auto ready = [&](const Cursor &c, bool fresh) {  // the block has landed, and Q where it is an item's first
+      const WpItem &t = sm.items[c.k];
+      const int j = c.j;
+      const unsigned block = c.base + j, st = block % kWpStages;
+      if (!wp_wait(sm, &sm.kv_full[st], (block / kWpStages) & 1, a.status)) return false;
       if (j == t.nblocks - 1) {
         // V rows at or past the context in the sequence's last page (stale pool bytes) become zeros
         const int row0 = (t.npages - 1 - j * kWpPagesPerBlock) * kPageTokens;  // the item's last page in the block
@@ -560,6 +577,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         }
         __syncwarp();
       }
+      if (fresh && !wp_wait(sm, &sm.q_full[tile], qs++ & 1, a.status)) return false;
       tc_fence_after();
       return true;
     };
@@ -595,52 +613,51 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       __syncwarp();
       return true;
     };
-#pragma unroll 1
-    for (int k = next_run(0); ok && k < nt; k = next_run(k + 1)) {
-      const WpItem &t = sm.items[k];
-      const WpTile w = tile_of(a, t, tile);
-      if (w.last >= 0) {
-        int j = w.begin(), used = 0;
-        ok = pass_to(gb + j);
-        unsigned st = (gb + j) % kWpStages;
-        ok = ok && landed(t, j, st) && wp_wait(sm, &sm.q_full[tile], qs++ & 1, a.status);
-        if (ok) {
-          tc_fence_after();
-          issue_s(st, 0);
-          issue_s(st, 1);
-        }
-#pragma unroll 1
-        while (ok) {
-          const bool last = j == w.last, starts = kBf16Out ? used == 0 : used % kWpRun == 0;
-          const bool ends = last || (!kBf16Out && used % kWpRun == kWpRun - 1);
-          const int jn = w.next(j);
-          const unsigned sn = (gb + jn) % kWpStages;
-          // the next block's S goes half by half behind P V of this one's; where blocks lie between that the tile does not
-          // use, this one is given back first (their copies may wait for its stage)
-          const bool near = !last && jn == j + 1;
-          ok = issue_pv(st, 0, starts, ends);
-          if (near) {
-            ok = ok && landed(t, jn, sn);
-            if (ok) issue_s(sn, 0);
-          }
-          ok = ok && issue_pv(st, 1, starts, ends);
-          ++pvs;
-          ++passed;
-          if (!ok || last) break;
-          if (!near) {
-            ok = pass_to(gb + jn) && landed(t, jn, sn);
-            if (!ok) break;
-            issue_s(sn, 0);
-          }
-          issue_s(sn, 1);
-          j = jn;
-          st = sn;
-          ++used;
-        }
+    Cursor c = {0, 0, 0u, {0, 0, -1}};
+    bool more = first_block(c);
+    if (more) {
+      ok = pass_to(c.base + c.j) && ready(c, true);
+      if (ok) {
+        issue_s((c.base + c.j) % kWpStages, 0);
+        issue_s((c.base + c.j) % kWpStages, 1);
       }
-      if (ok) ok = pass_to(gb + t.nblocks);
-      gb += t.nblocks;
     }
+    int used = 0;
+#pragma unroll 1
+    while (ok && more) {
+      const bool last = c.j == c.w.last, starts = kBf16Out ? used == 0 : used % kWpRun == 0;
+      const bool ends = last || (!kBf16Out && used % kWpRun == kWpRun - 1);
+      Cursor n = c;
+      if (last) {
+        n.base += sm.items[c.k].nblocks;
+        ++n.k;
+        more = first_block(n);
+      } else {
+        n.j = c.w.next(c.j);
+      }
+      const unsigned block = c.base + c.j, follows = n.base + n.j, st = block % kWpStages, sn = follows % kWpStages;
+      // The next block's S goes half by half behind P V of this one's, from one item to the next as well.  Where blocks lie
+      // between that the tile does not use, this one is given back first (their copies may wait for its stage).
+      const bool near = more && follows == block + 1;
+      ok = issue_pv(st, 0, starts, ends);
+      if (near) {
+        ok = ok && ready(n, last);
+        if (ok) issue_s(sn, 0);
+      }
+      ok = ok && issue_pv(st, 1, starts, ends);
+      ++pvs;
+      ++passed;
+      if (ok && more) {
+        if (!near) {
+          ok = pass_to(follows) && ready(n, last);
+          if (ok) issue_s(sn, 0);
+        }
+        if (ok) issue_s(sn, 1);
+      }
+      used = last ? 0 : used + 1;
+      c = n;
+    }
+    if (ok) ok = pass_to(c.base);
     // every MMA issued has completed before the tensor memory is freed
     if (elect_one()) {
       tc_commit(&sm.mma_done[tile]);
@@ -652,24 +669,36 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     const int tile = warp >> 2, r = tid & (kWpRows - 1), tok = tile * kWpTok + (r >> 2), hh = r & 3;
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim;
-    // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there.
+    // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there, so that the next
+    // item's first S is computed while this one's last P is (16 x 512 fp32 41.3 us for 42.8, 200 queries 10.6 for 11.1; 4 x 2048,
+    // of longer items, 141 for 140).
     uint32_t qn[kHeadDim / 2];
-    auto fetch_q = [&](int k) {
-      k = next_run(k);
-      const bool there = k < nt && sm.items[k].t0 + tok < sm.items[k].n;
-      const uint4 *src = nullptr;
-      if (there) {
-        const WpItem &t = sm.items[k];
+    int q_item = -1;  // whose Q has been fetched: the tile's next
+    auto fetch_q = [&]() {
+      do q_item = next_run(q_item + 1);
+      while (q_item < nt && (tile * kWpTok >= a.item_tok || sm.items[q_item].t0 + tile * kWpTok >= sm.items[q_item].n));
+      if (q_item < nt) {
+        const WpItem &t = sm.items[q_item];
+        const bool there = t.t0 + tok < t.n;
         const long long row = (long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh;
-        src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim);
-      }
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim);
 #pragma unroll
-      for (int i = 0; i < kHeadDim / 8; ++i) {
-        const uint4 x = there ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        qn[4 * i] = x.x, qn[4 * i + 1] = x.y, qn[4 * i + 2] = x.z, qn[4 * i + 3] = x.w;
+        for (int i = 0; i < kHeadDim / 8; ++i) {
+          const uint4 x = there ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          qn[4 * i] = x.x, qn[4 * i + 1] = x.y, qn[4 * i + 2] = x.z, qn[4 * i + 3] = x.w;
+        }
       }
     };
-    fetch_q(0);
+    auto hand_on_q = [&]() {  // the next item's Q
+      if (q_item >= nt) return;
+      tmem_st32(lane_base + kColQ + tile * (kHeadDim / 2), qn);
+      tc_fence_before();
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&sm.q_full[tile]);
+      fetch_q();
+    };
+    fetch_q();
+    hand_on_q();
     griddep_wait();  // the first global write below comes after the kernel before this one
     // (not before the wait: what the next kernel reads at once may come from a kernel before this one)
     griddep_launch_dependents();
@@ -782,23 +811,17 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       if (!t.run) continue;
       const WpTile w = tile_of(a, t, tile);
       if (w.last < 0) {
-        fetch_q(k + 1);
         gb += t.nblocks;
         continue;
       }
-      tmem_st32(lane_base + kColQ + tile * (kHeadDim / 2), qn);
-      tc_fence_before();
-      __syncwarp();
-      if (elect_one()) mbar_arrive(&sm.q_full[tile]);
-      fetch_q(k + 1);
       const int pos = t.ctx - t.n + min(t.t0 + tok, t.n - 1);
       const int lo = max(0, pos - a.window + 1);
-      const int front = t.front, skip = t.skip, nblocks = t.nblocks;
+      const int skip = t.skip, nblocks = t.nblocks;
       // blocks inner0 .. inner1 - 1 hold only keys that every row of the warp sees: from the last row's window on, up to the
       // first row's position
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0), lo31 = __shfl_sync(0xffffffffu, lo, 31);
       const int inner0 = ((lo31 + kPageTokens - 1) / kPageTokens - skip + kWpPagesPerBlock - 1) / kWpPagesPerBlock;
-      const int inner1 = ((pos0 + 1) / kPageTokens - skip) / kWpPagesPerBlock;
+      const int inner1 = min(((pos0 + 1) / kPageTokens - skip) / kWpPagesPerBlock, w.last);
       float m = 0.f;                     // the exponents' reference, times log2(e) scale
       float sum = 0.f, run_sum = 0.f;    // of the finished runs, and of this one
       int used = 0;
@@ -850,7 +873,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
           run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
           store_p(s_addr + 64, p16);
           tmem_ld32_wait(x1);
-          loaded = j + 1 < inner1 && j < w.last &&
+          loaded = j + 1 < inner1 &&
                    __all_sync(0xffffffffu, mbar_try_wait(&sm.s_full[tile][0], (blocks + 1) & 1));
           if (loaded) {
             tc_fence_after();
@@ -870,6 +893,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
                 break;
               }
               tc_fence_after();
+              if (j == w.last) hand_on_q();
             }
             // columns of [0, pos] without those before the window, or with the sinks among them (where pages are left out,
             // the sinks lie before them and the window behind); invalid pages take theirs out
