@@ -23,6 +23,10 @@
 //    nothing.
 //  * With weight sums the scores (base 2, fp32) wait in shared memory, 16 bytes a token, until the unit's maximum and sum
 //    are known; where a CTA's share does not fit (more than kChipPages pages), in the workspace.
+//
+// What bounds it: large batches HBM, 256 windows of 2032 tokens in 155 us (1.08 GB at 6.9 TB/s), 256 x 2048 with weight sums in 166 to
+// 171 (1.11 GB at 6.5 to 6.7 TB/s); ragged batches the last CTAs, 64 windows of up to 1000 in 24.2 us and weight sums of 64 x 1 .. 2048
+// in 23.7, 5.2 to 5.4 TB/s; one sequence the latencies of one pass, 4.1 and 5.9 us (table entry, pages, states exchanged).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -42,7 +46,7 @@ constexpr int kMaxCluster = 8;                               // CTAs that share 
 constexpr int kBoxBytes = kPageTokens * kRowBytes;           // one head's K (or V) rows of a page: 2 KiB
 constexpr int kUnitOut = kGroup * kHeadDim;                  // output values of a unit: 256
 constexpr int kScorePage = kPageTokens * int(sizeof(float4));  // scores of a page: 256 B
-constexpr int kChipPages = 448;                              // pages of a CTA whose scores fit into shared memory
+constexpr int kChipPages = 448;                              // pages of a CTA whose scores fit into shared memory beside a ring
 constexpr int kSumsAhead = 8;                                // sums of a thread fetched before they are needed
 constexpr int kMaxSorted = 128;                              // sequences that a CTA ranks by length
 constexpr int kMinPages = 4;                                 // pages a CTA of a cluster gets at the least
@@ -409,7 +413,8 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
 
 template <int kStages>
 constexpr size_t unit_smem_bytes() { return sizeof(UnitSmem<kStages>) + 1024; }
-constexpr size_t kSmemPerSm = 227 * 1024, kSmemReserved = 1024;  // of an SM's shared memory, and what a CTA takes besides its own
+constexpr size_t kPairSmem = 227 * 1024 / 2 - 1024;  // shared memory of a CTA that shares its SM with another one
+constexpr int kPairPages = int((kPairSmem - unit_smem_bytes<kShallowRing>()) / kScorePage);  // whose scores fit then: 150
 
 // Shared-memory limits of the kernels on the current device.
 int setup_unit_attributes() {
@@ -445,7 +450,9 @@ long long max_unit_pages(int max_context, int window, int sinks) {
   return all < seen ? all : seen;
 }
 
-// CTAs to a unit: as many as fill the SMs with two each, as long as every warp has a page.
+// CTAs to a unit: as many as fill the SMs with two each, as long as each gets a few pages.  1 / 2 / 4 / 8 of them: one sequence,
+// window of 512 (34 pages), 5.4 / 5.2 / 4.5 / 4.0 us; weight sums of one sequence of 2048, 14.9 / 10.3 / 7.4 / 5.8; 64 windows of up to
+// 1000 (512 units) 24.4 / 31.2 / 38.6 / 63.2; 256 windows of 2032 157 / 166 / 202 / 296.
 int unit_cluster(long long units, long long pages) {
   const int sms = device_sm_count();
   const long long slots = 2ll * (sms > 0 ? sms : 148);
@@ -495,11 +502,18 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
   size_t smem = unit_smem_bytes<kDeepRing>();
   if (sums != nullptr) {
     kernel = unit_decode_kernel<true, kDeepRing>;
-    while (a.cluster < kMaxCluster && (pages + a.cluster - 1) / a.cluster > kChipPages) a.cluster *= 2;
+    // Shares small enough for two CTAs to an SM, where clusters of 8 get that far: 32 sequences of 16384 tokens take 190 us (220 with
+    // one), 8 of them 47 (57), 64 of 4096 101 (110), 64 of 1 .. 8192 110 (114), 40 of 1 .. 4096 36.8 (36.3).  Else shares that fit at
+    // all (the workspace takes as long, 217 us for 219, but needs 256 bytes a page).
+    auto split = [&](long long most) {
+      while (a.cluster < kMaxCluster && (pages + a.cluster - 1) / a.cluster > most) a.cluster *= 2;
+    };
+    split(pages <= kMaxCluster * kPairPages ? kPairPages : kChipPages);
     const long long share = (pages + a.cluster - 1) / a.cluster;
     if (share <= kChipPages) {
       const size_t scores = size_t(share) * kScorePage;
-      if (smem + scores > kSmemPerSm / 2 - kSmemReserved && unit_smem_bytes<kShallowRing>() + scores <= kSmemPerSm / 2 - kSmemReserved) {
+      // the ring of two stages where it brings a second CTA to the SM: 256 sequences of 2048 tokens 177 us (210 with three stages)
+      if (smem + scores > kPairSmem && unit_smem_bytes<kShallowRing>() + scores <= kPairSmem) {
         kernel = unit_decode_kernel<true, kShallowRing>;
         smem = unit_smem_bytes<kShallowRing>();
       }
