@@ -42,7 +42,8 @@ namespace {
 constexpr int kUnitWarps = 8;
 constexpr int kUnitThreads = kUnitWarps * 32;
 constexpr int kDeepRing = 3, kShallowRing = 2;               // pages a warp has in flight
-constexpr int kMaxCluster = 8;                               // CTAs that share a unit at the most
+constexpr int kMaxCluster = 16;                              // CTAs that share a unit at the most
+constexpr int kFarCluster = 8;                               // the same where they need an SM each
 constexpr int kBoxBytes = kPageTokens * kRowBytes;           // one head's K (or V) rows of a page: 2 KiB
 constexpr int kUnitOut = kGroup * kHeadDim;                  // output values of a unit: 256
 constexpr int kScorePage = kPageTokens * int(sizeof(float4));  // scores of a page: 256 B
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) unit_decode_kernel(const __gr
     if (tid < slice || (kWeights && tid < kGroup)) {
       const int i = rank * slice + tid;
       const bool outs = tid < slice;
-      // (with weight sums threads 0-3 look after heads 0-3 as well; a slice holds 32 values or more)
+      // (with weight sums threads 0-3 look after heads 0-3 as well; a slice holds 16 values or more)
 #pragma unroll 1
       for (int k = outs ? 0 : 1; k < (kWeights && tid < kGroup ? 2 : 1); ++k) {
         const int hh = k == 0 ? i / kHeadDim : tid;
@@ -434,7 +435,8 @@ int setup_unit_attributes() {
                {unit_decode_kernel<true, kDeepRing>, unit_smem_bytes<kDeepRing>() + kChipPages * kScorePage},
                {unit_decode_kernel<true, kShallowRing>, unit_smem_bytes<kShallowRing>() + kChipPages * kScorePage}};
     for (const auto &k : all)
-      if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.bytes)) != cudaSuccess) {
+      if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(k.bytes)) != cudaSuccess ||
+          cudaFuncSetAttribute(k.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
       }
@@ -452,12 +454,15 @@ long long max_unit_pages(int max_context, int window, int sinks) {
 
 // CTAs to a unit: as many as fill the SMs with two each, as long as each gets a few pages.  1 / 2 / 4 / 8 of them: one sequence,
 // window of 512 (34 pages), 5.4 / 5.2 / 4.5 / 4.0 us; weight sums of one sequence of 2048, 14.9 / 10.3 / 7.4 / 5.8; 64 windows of up to
-// 1000 (512 units) 24.4 / 31.2 / 38.6 / 63.2; 256 windows of 2032 157 / 166 / 202 / 296.
-int unit_cluster(long long units, long long pages) {
+// 1000 (512 units) 24.4 / 31.2 / 38.6 / 63.2; 256 windows of 2032 157 / 166 / 202 / 296.  16 (a cluster of them takes most of a GPC, so
+// no more than one for each) where there are twice as many pages still: windows of 32768 19.0 us for 23.7, of 4096 5.7 for 6.5, of
+// 1000 4.3 for 4.0; two sequences, windows of 8192, 12.4 for 10.7.
+int unit_cluster(long long units, long long pages, int most) {
   const int sms = device_sm_count();
   const long long slots = 2ll * (sms > 0 ? sms : 148);
   int c = 1;
-  while (c < kMaxCluster && units * c * 2 <= slots && pages >= 2ll * c * kMinPages) c *= 2;
+  while (c < kFarCluster && units * c * 2 <= slots && pages >= 2ll * c * kMinPages) c *= 2;
+  if (c == kFarCluster && most > c && units * most * 2 <= slots && pages >= 2ll * most * kMinPages) c = most;
   return c;
 }
 
@@ -484,7 +489,8 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
   a.window = window;
   a.sinks = sinks;
   a.scale_log2 = scale * kLog2e;
-  a.cluster = unit_cluster(units, pages);
+  const bool paired = sums == nullptr || pages <= kMaxCluster * kPairPages;  // two CTAs find room on an SM
+  a.cluster = unit_cluster(units, pages, paired ? kMaxCluster : kFarCluster);
   // More units than are resident at once, but not many times as many, and lengths that may differ: the longest first, so that
   // no long one is left at the end (weight sums of 64 sequences of 1 .. 2048 tokens: 23.5 us for 25.2).  Windows of 1000 over
   // 1 .. 8192 tokens, most of them full, take 26.1 us so and 24.2 without; batches of many rounds gain nothing.
@@ -505,10 +511,8 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
     // Shares small enough for two CTAs to an SM, where clusters of 8 get that far: 32 sequences of 16384 tokens take 190 us (220 with
     // one), 8 of them 47 (57), 64 of 4096 101 (110), 64 of 1 .. 8192 110 (114), 40 of 1 .. 4096 36.8 (36.3).  Else shares that fit at
     // all (the workspace takes as long, 217 us for 219, but needs 256 bytes a page).
-    auto split = [&](long long most) {
-      while (a.cluster < kMaxCluster && (pages + a.cluster - 1) / a.cluster > most) a.cluster *= 2;
-    };
-    split(pages <= kMaxCluster * kPairPages ? kPairPages : kChipPages);
+    const int most = paired ? kPairPages : kChipPages;
+    while (a.cluster < (paired ? kMaxCluster : kFarCluster) && (pages + a.cluster - 1) / a.cluster > most) a.cluster *= 2;
     const long long share = (pages + a.cluster - 1) / a.cluster;
     if (share <= kChipPages) {
       const size_t scores = size_t(share) * kScorePage;
@@ -591,7 +595,7 @@ extern "C" int pkv_paged_window_decode_attention(const pkv_pool *pool, void *out
 extern "C" size_t pkv_weights_workspace_bytes(int num_seqs, int max_context) {
   if (num_seqs < 0 || num_seqs > (1 << 24) || max_context < 0 || max_context > (1 << 30)) return 0;
   const long long pages = ((long long)max_context + pkv::kPageTokens - 1) / pkv::kPageTokens;
-  if (pages <= (long long)pkv::kMaxCluster * pkv::kChipPages) return 0;
+  if (pages <= (long long)pkv::kFarCluster * pkv::kChipPages) return 0;
   return size_t(num_seqs) * pkv::kKvHeads * size_t(pages) * pkv::kScorePage;
 }
 

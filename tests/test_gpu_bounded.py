@@ -396,6 +396,16 @@ def test_weights_shares_of_a_unit(pkv, contexts):
     _check_weights(pkv, B.Cache(contexts, seed=33), 1.0)
 
 
+@pytest.mark.parametrize("contexts,blocks", [([300] * 9 + [700], 512), ([40] * 30 + [900], 2300), ([2000, 1], 2300),
+                                             ([20] * 60, 512), ([6000], 2500), ([130, 0, 5000], 4200)])
+def test_bounds_far_above_the_lengths(pkv, contexts, blocks):
+    """Shares of a unit go by the bound on the lengths: short ones leave most of a cluster without pages."""
+    c = B.Cache(contexts, seed=39, max_blocks=blocks)
+    _check_weights(pkv, c, 0.9)
+    _check_decode(pkv, c, 1 << 30, 0, bf16=True)
+    _check_decode(pkv, c, 256, 3)
+
+
 @pytest.mark.parametrize("scale", [1.0, -0.125, 0.0])
 def test_weights_scales(pkv, scale):
     _check_weights(pkv, B.Cache([700, 40, 90], seed=34), 0.5, scale=scale)
