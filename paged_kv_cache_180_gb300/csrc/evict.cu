@@ -1,19 +1,29 @@
 // Eviction: per sequence, layer and K/V head the cached tokens with the largest weight sums are kept, with the first few
 // and the most recent ones, and their rows move together at the front of the sequence, in order and in place.
 //
-// What is kept of ctx tokens with B = min(budget, ctx):  the first a = min(sinks, B), the last r = min(recent, B - a), and of
-// the tokens between them the B - a - r with the largest sums; of equal sums the earlier token.
+// What is kept of ctx tokens with B = min(budget, ctx):  the first a = min(sinks, B), the last r = min(recent, B - a), and
+// of the tokens between them the B - a - r with the largest sums; of equal sums the earlier token.
 //
-// A unit is one (sequence, layer, K/V head); it belongs to one CTA or one cluster of CTAs, each of which holds the sums of an
-// equal run of the tokens in shared memory (where they fit).
+// A unit is one (sequence, layer, K/V head); it belongs to one CTA or one cluster of CTAs, each of which holds the sums of
+// an equal run of the tokens in shared memory (where they fit).
 //  * Selection: sums are mapped to 32-bit keys of the same order and the key of rank B - a - r is found digit by digit from
 //    the top (11, 11 and 10 bits, a histogram in shared memory, added up over the cluster); the passes end once a bin is
 //    needed whole, which is after the second where the sums differ.  A prefix sum over the tokens then gives every kept one
 //    its place, and its position and sum are written there.
-//  * Moving: kept[k] >= k, ascending, so the rows that round i of the move writes (positions i R .. (i + 1) R - 1) lie at or
-//    before everything that later rounds read, and a barrier between a round's loads and its stores is all the order there
-//    has to be.  A row's K and V (2 x 128 B) are moved by 16 threads, 16 bytes each, through a ring in shared memory
+//  * Moving: kept[k] >= k, ascending, so the rows that round i of the move writes (positions i R .. (i + 1) R - 1) lie at
+//    or before everything that later rounds read, and a barrier between a round's loads and its stores is all the order
+//    there has to be.  A row's K and V (2 x 128 B) are moved by 16 threads, 16 bytes each, through a ring in shared memory
 //    (cp.async), each thread storing what it loaded itself.
+//
+// What bounds it: large batches HBM, 64 sequences of 1024 .. 2048 tokens in 16 layers cut to 60 % in 626 us (3.95 GB, 6.3
+// TB/s, 93 % of the copy rate); few units the chain before the first row moves.  One sequence's 16 layers of 2048 tokens:
+// 20 us, of them 9 until the first rows have landed (launch and lengths 0.8, sums 0.8, selection 2.6, list 1.5, first rows
+// 1.9) and 10 at the rate of HBM.  Two long documents, 57000 tokens cut to a quarter: 57 us, of them 20 selection and list
+// (a cluster barrier and what is read behind it take 0.7) and 20 to 26 the rows, in 27 to 30 rounds.
+//  * Passes over digits, because a sort moves what selection only counts; 11 bits in a CTA of its own, as the exponent
+//    decides little. In a cluster the range of the keys is found first: without it the first pass, of a few bins, decided
+//    next to nothing.
+//  * Rows go through shared memory rather than registers, so that four to six rounds are in flight.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -61,7 +71,8 @@ struct EvictSmem {
   int2 warp_count[kThreads / 32];  // (kept for certain, equal to the threshold) of a warp's tokens
   int2 count;                      // of the CTA's tokens
   int from[2][kEvLook];            // old positions of the CTA's next rows
-  // cluster: the CTA's counts of a pass; what the CTAs have in the bins that this one adds up; the sums; those of each 32 bins
+  // cluster: the CTA's counts of a pass; what the CTAs have in the bins that this one adds up; the sums; those of each 32
+  // bins
   unsigned bins[kClusterBins], part[kClusterBins], share[kClusterBins], group[kClusterBins / 32];
   uint2 range;                     // cluster: smallest and largest key of the CTA's candidates
   unsigned digit, need;
@@ -208,8 +219,8 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
         }
       }
       if (kCluster) {
-        // Every CTA adds up its share of the bins over the cluster, and the sums of each 32 of them; the sums say which 32 hold
-        // the key of rank `need`.  (Every CTA reading all bins of all others took 5000 cycles a pass.)
+        // Every CTA adds up its share of the bins over the cluster, and the sums of each 32 of them; the sums say which 32
+        // hold the key of rank `need`.  (Every CTA reading all bins of all others took 5000 cycles a pass.)
         const int slice = kBins / C;
         sm.bins[tid] = c[0];
         cluster_sync();
@@ -233,7 +244,8 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
             return x;
           };
           const int groups = slice / 32;
-          const unsigned x = lane < kBins / 32 ? ld_cluster_u32(cluster_map(smem_addr(&sm.group[lane % groups]), lane / groups)) : 0u;
+          const uint32_t there = cluster_map(smem_addr(&sm.group[lane % groups]), uint32_t(lane % (kBins / 32) / groups));
+          const unsigned x = lane < kBins / 32 ? ld_cluster_u32(there) : 0u;
           unsigned up = from_top(x);
           const int at = 31 - __clz(int(__ballot_sync(0xffffffffu, up >= need)));  // the group
           const unsigned above = __shfl_sync(0xffffffffu, up - x, at);
@@ -533,7 +545,8 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
                            (num_layers == 1 || sums_layer_stride >= (num_seqs <= 1 ? heads : num_seqs * sums_seq_stride));
   if (num_seqs > 0 && !layers_inside && !seqs_inside) return PKV_ERR_SHAPE;
   if (num_seqs == 0) return PKV_OK;
-  // (without cached tokens there are no sums, and without a budget there is no list; the new lengths are written all the same)
+  // (without cached tokens there are no sums, and without a budget there is no list; the new lengths are written all the
+  // same)
   if (block_tables == nullptr || context_lens == nullptr || budgets == nullptr ||
       ((weight_sums == nullptr || new_weight_sums == nullptr) && max_context > 0) || (kept == nullptr && max_budget > 0))
     return PKV_ERR_NULL;
@@ -588,10 +601,17 @@ extern "C" int pkv_kv_evict(const pkv_pool *pool, const int32_t *block_tables, i
   const long long units = (long long)num_seqs * num_layers * pkv::kKvHeads;
   int sms = pkv::device_sm_count();
   if (sms <= 0) sms = 148;
+  // CTAs to a unit: as many as find SMs, with a thousand tokens for each two of them.  Two sequences of 57000 tokens, one
+  // layer (16 units), take 225 / 69 / 57 / 59 us with 1 / 4 / 8 / 16 of them; one of 2048 tokens (8 units) 15.9 us with 2,
+  // 13.2 with 4 and 12.4 with 8, but two layers of it 13.4 with 4 and 15.8 with 8; one of 1024 tokens 10.7 with 1, 13.0
+  // with 2, 11.7 with 4 or 8.
   a.cluster = 1;
-  while (a.cluster < pkv::kEvMaxCluster && units * a.cluster * 2 <= sms && max_context >= a.cluster * 2048) a.cluster *= 2;
+  while (a.cluster < pkv::kEvMaxCluster && units * a.cluster * 2 <= sms && max_context >= (a.cluster < 2 ? 2 : a.cluster) * 1024)
+    a.cluster *= 2;
   const int pages = (max_context + pkv::kPageTokens - 1) / pkv::kPageTokens;
   a.pages_bytes = pages <= pkv::kEvMaxPages ? (pages * 4 + 15) / 16 * 16 : 0;
+  // Many units: small CTAs, several to an SM, so that one selects while others move: 64 x 16 layers 626 us, with the large
+  // ones 652; 16 layers of one sequence (128 units) 26.7 us with the small ones, 19.3 with the large ones.
   pkv::EvictKernel kernel = a.cluster > 1 ? pkv::kEvictCluster : units > 2 * sms ? pkv::kEvictMany : pkv::kEvictFew;
   int threads = 512, ring = a.cluster > 1 ? 5 * 64 : 6 * 64;
   if (a.cluster == 1 && units > 2 * sms) {

@@ -24,9 +24,10 @@
 //  * With weight sums the scores (base 2, fp32) wait in shared memory, 16 bytes a token, until the unit's maximum and sum
 //    are known; where a CTA's share does not fit (more than kChipPages pages), in the workspace.
 //
-// What bounds it: large batches HBM, 256 windows of 2032 tokens in 155 us (1.08 GB at 6.9 TB/s), 256 x 2048 with weight sums in 166 to
-// 171 (1.11 GB at 6.5 to 6.7 TB/s); ragged batches the last CTAs, 64 windows of up to 1000 in 24.2 us and weight sums of 64 x 1 .. 2048
-// in 23.7, 5.2 to 5.4 TB/s; one sequence the latencies of one pass, 4.1 and 5.9 us (table entry, pages, states exchanged).
+// What bounds it: large batches HBM, 256 windows of 2032 tokens in 155 us (1.08 GB at 6.9 TB/s), 256 x 2048 with weight
+// sums in 166 to 171 (1.11 GB at 6.5 to 6.7 TB/s); ragged batches the last CTAs, 64 windows of up to 1000 in 24.2 us and
+// weight sums of 64 x 1 .. 2048 in 23.7, 5.2 to 5.4 TB/s; one sequence the latencies of one pass, 4.1 and 5.9 us (table
+// entry, pages, states exchanged).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -47,7 +48,7 @@ constexpr int kFarCluster = 8;                               // the same where t
 constexpr int kBoxBytes = kPageTokens * kRowBytes;           // one head's K (or V) rows of a page: 2 KiB
 constexpr int kUnitOut = kGroup * kHeadDim;                  // output values of a unit: 256
 constexpr int kScorePage = kPageTokens * int(sizeof(float4));  // scores of a page: 256 B
-constexpr int kChipPages = 448;                              // pages of a CTA whose scores fit into shared memory beside a ring
+constexpr int kChipPages = 448;                              // pages of a CTA whose scores fit on chip beside a ring
 constexpr int kSumsAhead = 8;                                // sums of a thread fetched before they are needed
 constexpr int kMaxSorted = 128;                              // sequences that a CTA ranks by length
 constexpr int kMinPages = 4;                                 // pages a CTA of a cluster gets at the least
@@ -448,15 +449,16 @@ int setup_unit_attributes() {
 // Pages that a unit sees at the most, given the bound on the lengths.
 long long max_unit_pages(int max_context, int window, int sinks) {
   const long long all = ((long long)max_context + kPageTokens - 1) / kPageTokens;
-  const long long seen = ((long long)sinks + kPageTokens - 1) / kPageTokens + ((long long)window + kPageTokens - 2) / kPageTokens + 1;
+  const long long seen = ((long long)sinks + kPageTokens - 1) / kPageTokens +
+                         ((long long)window + kPageTokens - 2) / kPageTokens + 1;
   return all < seen ? all : seen;
 }
 
-// CTAs to a unit: as many as fill the SMs with two each, as long as each gets a few pages.  1 / 2 / 4 / 8 of them: one sequence,
-// window of 512 (34 pages), 5.4 / 5.2 / 4.5 / 4.0 us; weight sums of one sequence of 2048, 14.9 / 10.3 / 7.4 / 5.8; 64 windows of up to
-// 1000 (512 units) 24.4 / 31.2 / 38.6 / 63.2; 256 windows of 2032 157 / 166 / 202 / 296.  16 (a cluster of them takes most of a GPC, so
-// no more than one for each) where there are twice as many pages still: windows of 32768 19.0 us for 23.7, of 4096 5.7 for 6.5, of
-// 1000 4.3 for 4.0; two sequences, windows of 8192, 12.4 for 10.7.
+// CTAs to a unit: as many as fill the SMs with two each, as long as each gets a few pages.  1 / 2 / 4 / 8 of them: one
+// sequence, window of 512 (34 pages), 5.4 / 5.2 / 4.5 / 4.0 us; weight sums of one sequence of 2048, 14.9 / 10.3 / 7.4 /
+// 5.8; 64 windows of up to 1000 (512 units) 24.4 / 31.2 / 38.6 / 63.2; 256 windows of 2032 157 / 166 / 202 / 296.  16 (a
+// cluster of them takes most of a GPC, so no more than one for each) where there are twice as many pages still: windows of
+// 32768 19.0 us for 23.7, of 4096 5.7 for 6.5, of 1000 4.3 for 4.0; two sequences, windows of 8192, 12.4 for 10.7.
 int unit_cluster(long long units, long long pages, int most) {
   const int sms = device_sm_count();
   const long long slots = 2ll * (sms > 0 ? sms : 148);
@@ -491,9 +493,9 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
   a.scale_log2 = scale * kLog2e;
   const bool paired = sums == nullptr || pages <= kMaxCluster * kPairPages;  // two CTAs find room on an SM
   a.cluster = unit_cluster(units, pages, paired ? kMaxCluster : kFarCluster);
-  // More units than are resident at once, but not many times as many, and lengths that may differ: the longest first, so that
-  // no long one is left at the end (weight sums of 64 sequences of 1 .. 2048 tokens: 23.5 us for 25.2).  Windows of 1000 over
-  // 1 .. 8192 tokens, most of them full, take 26.1 us so and 24.2 without; batches of many rounds gain nothing.
+  // More units than are resident at once, but not many times as many, and lengths that may differ: the longest first, so
+  // that no long one is left at the end (weight sums of 64 sequences of 1 .. 2048 tokens: 23.5 us for 25.2).  Windows of
+  // 1000 over 1 .. 8192 tokens, most of them full, take 26.1 us so and 24.2 without; batches of many rounds gain nothing.
   const int sms = device_sm_count();
   const bool whole = (long long)window + sinks >= max_context;
   a.sort = a.cluster == 1 && whole && units > 2ll * (sms > 0 ? sms : 148) && num_seqs <= kMaxSorted ? num_seqs : 0;
@@ -508,15 +510,16 @@ int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
   size_t smem = unit_smem_bytes<kDeepRing>();
   if (sums != nullptr) {
     kernel = unit_decode_kernel<true, kDeepRing>;
-    // Shares small enough for two CTAs to an SM, where clusters of 8 get that far: 32 sequences of 16384 tokens take 190 us (220 with
-    // one), 8 of them 47 (57), 64 of 4096 101 (110), 64 of 1 .. 8192 110 (114), 40 of 1 .. 4096 36.8 (36.3).  Else shares that fit at
-    // all (the workspace takes as long, 217 us for 219, but needs 256 bytes a page).
+    // Shares small enough for two CTAs to an SM, where clusters of 8 get that far: 32 sequences of 16384 tokens take 190 us
+    // (220 with one), 8 of them 47 (57), 64 of 4096 101 (110), 64 of 1 .. 8192 110 (114), 40 of 1 .. 4096 36.8 (36.3).
+    // Else shares that fit at all (the workspace takes as long, 217 us for 219, but needs 256 bytes a page).
     const int most = paired ? kPairPages : kChipPages;
     while (a.cluster < (paired ? kMaxCluster : kFarCluster) && (pages + a.cluster - 1) / a.cluster > most) a.cluster *= 2;
     const long long share = (pages + a.cluster - 1) / a.cluster;
     if (share <= kChipPages) {
       const size_t scores = size_t(share) * kScorePage;
-      // the ring of two stages where it brings a second CTA to the SM: 256 sequences of 2048 tokens 177 us (210 with three stages)
+      // the ring of two stages where it brings a second CTA to the SM: 256 sequences of 2048 tokens 177 us (210 with three
+      // stages)
       if (smem + scores > kPairSmem && unit_smem_bytes<kShallowRing>() + scores <= kPairSmem) {
         kernel = unit_decode_kernel<true, kShallowRing>;
         smem = unit_smem_bytes<kShallowRing>();

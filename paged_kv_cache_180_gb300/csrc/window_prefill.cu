@@ -5,29 +5,41 @@
 //   A = { t <= p : t < sinks or t > p - window },  p = context_lens[s] - n_s + (i - query_start[s]).
 //
 // tcgen05 tensor cores, accumulators in tensor memory:
-//  * An item is 64 query tokens of a sequence against one K/V head: two tiles of 32 tokens, 128 rows each (row = 4 * token +
-//    head in group).  Both tiles use each K/V block that is loaded, or one of them where the other sees nothing of it.  The
-//    pages that the item's rows see (the sinks' and those from the first row's window on; none between) are numbered without
-//    the gap and go eight to a block of 128 keys, so that the sinks cost a page and not a block.
-//    Where there are fewer items than half the SMs, they have one tile.
+//  * An item is 64 query tokens of a sequence against one K/V head: two tiles of 32 tokens, 128 rows each (row = 4 * token
+//    + head in group).  Both tiles use each K/V block that is loaded, or one of them where the other sees nothing of it.
+//    The pages that the item's rows see (the sinks' and those from the first row's window on; none between) are numbered
+//    without the gap and go eight to a block of 128 keys, so that the sinks cost a page and not a block. Where there are
+//    fewer items than half the SMs, they have one tile.
 //  * The grid is persistent, one CTA to an SM; the items that there are (a prefix sum over the sequences' lengths, made by
 //    every CTA) are dealt in a snake, each sequence's latest first.
-//  * Q_t stays in tensor memory (its rows' own threads put it there).  A block's S_t = Q_t K^T is computed in two halves of 64
-//    keys, into TMEM buffers of their own; P goes back over its half and is the TMEM A operand of O_t += P V.  So while the
-//    softmax works on one half the tensor core has P V of the other and its next S, and shared memory feeds it K and V
+//  * Q_t stays in tensor memory (its rows' own threads put it there).  A block's S_t = Q_t K^T is computed in two halves of
+//    64 keys, into TMEM buffers of their own; P goes back over its half and is the TMEM A operand of O_t += P V.  So while
+//    the softmax works on one half the tensor core has P V of the other and its next S, and shared memory feeds it K and V
 //    alone.  With fp32 output P has two bf16 terms (16 bits), with bf16 output one.  Row sums are added up in registers.
 //  * The exponents of a row refer to the maximum of the scores of its tile's first block, seen by the row or not, and stay
 //    there: weights are floats, so they may well be far from 1.  A row whose sum leaves [2^-90, 2^112] is computed again.
 //  * The tensor core truncates what it adds up.  With fp32 output O is therefore taken out after every 1024 keys and added
 //    to the row in `out`, whose last value is the quotient.
-//  * A warp's finished rows go through shared memory and a TMA store: stored by their threads, 256 bytes apart, they took 3400
-//    cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored directly.)
+//  * A warp's finished rows go through shared memory and a TMA store: stored by their threads, 256 bytes apart, they took
+//    3400 cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored
+//    directly.)
 //  * Keys that a row does not see get weight 0.  Their V meets that weight in the product all the same, so a NaN or an
 //    infinity in it would reach rows that do not see it: a row whose output is not finite is computed again at the end,
 //    from the keys that it sees alone, by its own thread (slowly).
-//  * Warps 0-3 and 4-7 own a row of tile 0 and 1 a thread.  Warp 8 loads by TMA; warps 9 and 10 issue the MMAs of a tile each.
+//  * Warps 0-3 and 4-7 own a row of tile 0 and 1 a thread.  Warp 8 loads by TMA; warps 9 and 10 issue the MMAs of a tile
+//    each.
 //  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing work, waits
 //    (bounded) for what is in flight, frees its tensor memory and exits.
+//
+// What bounds it: 4 x 2048 queries, windows of 2000, bf16 output, take 141 us (135 GFLOP, 960 TFLOP/s, half of the measured
+// bf16 peak): tensor pipe 42 %, exponentials 40 %, issue slots 46 %, so nothing is full; two softmax warps a scheduler wait
+// for S, exponentials and stores in turn, and registers (168 a thread) and tensor memory (all 512 columns are taken) leave
+// no room for a third.  Built and slower: two CTAs to an SM with one S buffer a tile (151 to 161 us), one issuing warp for
+// both tiles (62 cycles a product), softmax warps that issue for themselves (166).  With fp32 output the second terms take
+// 2.5 times the instructions a weight: 2048 queries, windows of 4096, 154 us for 76.  Short windows: 16 x 512 queries,
+// windows of 128, fp32 in 41 us, 12900 cycles an item of two blocks, of them 2000 waiting for its S, 1800 taking out the O
+// before it, the rest four masked halves.  200 queries of one sequence: 10.3 us, the latencies of one item (lists and
+// set-up 2, first K/V 2, blocks and output the rest).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -240,9 +252,9 @@ __device__ __forceinline__ float extreme32(const uint32_t (&s)[32]) {
 }
 
 // P = 2^(s c - m) for 32 keys as one or two bf16 terms, keys 2i and 2i + 1 packed in word i, the second term behind the
-// first (with kMasked, keys whose bit in `valid` is clear get 0).  Returns their sum; of two terms, the sum of what they hold:
-// a weight's rounding then cancels in the quotient as far as the weight makes up the row (errors of 1.7e-6 of the output's
-// norm for 2.2e-6, 4 % of the time).  With one term that gives 2.2e-3 for 2.3e-3 and takes 12 %.
+// first (with kMasked, keys whose bit in `valid` is clear get 0).  Returns their sum; of two terms, the sum of what they
+// hold: a weight's rounding then cancels in the quotient as far as the weight makes up the row (errors of 1.7e-6 of the
+// output's norm for 2.2e-6, 4 % of the time).  With one term that gives 2.2e-3 for 2.3e-3 and takes 12 %.
 template <bool kMasked, bool kTwo>
 __device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t valid, float m, float c,
                                                uint32_t (&p16)[kTwo ? 32 : 16]) {
@@ -409,8 +421,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  // The list of items: sequence after sequence, its tokens from the last ones to the first, 8 K/V heads each.  A thread takes
-  // a sequence, counts its items and, by a prefix sum, finds which of this CTA's items they are.
+  // The list of items: sequence after sequence, its tokens from the last ones to the first, 8 K/V heads each.  A thread
+  // takes a sequence, counts its items and, by a prefix sum, finds which of this CTA's items they are.
   bool negative = false;  // a sequence of less than no query tokens, reported once the kernel before this one has ended
   for (int base = 0, before = 0; base < a.num_seqs; base += kWpThreads) {
     const int s = base + tid;
@@ -669,9 +681,9 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     const int tile = warp >> 2, r = tid & (kWpRows - 1), tok = tile * kWpTok + (r >> 2), hh = r & 3;
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim;
-    // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there, so that the next
-    // item's first S is computed while this one's last P is (16 x 512 fp32 41.3 us for 42.8, 200 queries 10.6 for 11.1; 4 x 2048,
-    // of longer items, 141 for 140).
+    // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there, so that the
+    // next item's first S is computed while this one's last P is (16 x 512 fp32 41.3 us for 42.8, 200 queries 10.6 for
+    // 11.1; 4 x 2048, of longer items, 141 for 140).
     uint32_t qn[kHeadDim / 2];
     int q_item = -1;  // whose Q has been fetched: the tile's next
     auto fetch_q = [&]() {
@@ -1006,8 +1018,8 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
       (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return PKV_ERR_ALIGN;
   const int sms = pkv::device_sm_count() > 0 ? pkv::device_sm_count() : 148;
-  // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 10.5 us so and 12.1 in
-  // items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 56 us and 41.
+  // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 10.2 us so and
+  // 12.2 in items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 52 us and 41.
   const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
   const int item_tok = (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
   const long long items = (max_query + item_tok - 1) / item_tok;
