@@ -650,6 +650,43 @@ def test_evict_special_sums(pkv):
             _check_evict(pkv, e, budgets, 1, 3, in_place)
 
 
+@pytest.mark.parametrize("contexts", [[2048], [5000], [20000], [3000, 2500]])  # clusters of 4, 4, 8 and 2
+def test_evict_special_sums_in_clusters(pkv, contexts):
+    """Digits of a cluster divide the range of the keys: the whole range, none at all, one value far from the others, ties."""
+    e = Evict(contexts, seed=49)
+    r = np.random.RandomState(50)
+    plain = e.sums.copy()
+    n = plain.shape[-1]
+    kinds = [plain * np.where(r.rand(*plain.shape) < 0.5, -1, 1).astype(np.float32), np.full_like(plain, 0.25),
+             np.where(r.rand(*plain.shape) < 0.001, np.float32(1e30), np.float32(1e-30)), np.floor(plain * 2),
+             r.randint(0, 1 << 32, plain.shape, dtype=np.uint64).astype(np.uint32).view(np.float32)]  # NaN, infinities, all sizes
+    one = np.zeros_like(plain)
+    one[..., n // 3] = 1
+    kinds.append(one)
+    for sums in kinds:
+        e.sums = np.ascontiguousarray(sums.astype(np.float32))
+        for keep in (0, 9, 10, 1501, n):
+            _check_evict(pkv, e, [min(keep, c) for c in contexts], 4, 5, in_place=keep % 2 == 1)
+
+
+def test_evict_other_strides(pkv):
+    """Layers outside sequences, in the sums and the tables, and rows of sums longer than the bound."""
+    e = Evict([700, 90, 0, 1300], 2, seed=52, extra=3)
+    want = _run_evict(pkv, e, [300, 50, 4, 1300], 4, 30)
+    pool, status = _pool(pkv, e.pool), _status()
+    sums = U.to_dev(np.ascontiguousarray(e.sums.transpose(1, 0, 2, 3))).transpose(0, 1)
+    bt = U.to_dev(np.ascontiguousarray(e.bt.transpose(1, 0, 2))).transpose(0, 1)
+    kept = torch.full((4, 2, 8, 1300), -1, dtype=torch.int32, device=U.dev())
+    pkv.kv_evict(pool, bt, bt.stride(0), bt.stride(1), U.to_dev(e.lens), U.to_dev(np.array([300, 50, 4, 1300], np.int32)), sums,
+                 sums, 4, 30, e.max_context, kept, None, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and np.array_equal(kept.cpu().numpy(), want[3])
+    assert torch.equal(pool.buffer.view(torch.int16), want[0].buffer.view(torch.int16))
+    for s, n in enumerate((700, 90, 0, 1300)):
+        assert torch.equal(sums[s, :, :, :n], want[2][s, :, :, :n])
+        assert np.array_equal(sums[s, :, :, n:].cpu().numpy(), e.sums[s, :, :, n:])
+
+
 def test_evict_bad_arguments_on_the_device(pkv):
     e = Evict([100, 200, 64, 33, 50], 2, seed=44)
     e.lens = np.array([-1, 200, e.max_context + 1, 33, 50], np.int32)
