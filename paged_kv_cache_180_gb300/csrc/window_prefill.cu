@@ -840,15 +840,30 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       bool more = false;
       uint32_t x0[32], x1[32];  // quarters of S
       bool loaded = false;      // the next block's first one has been asked for
-#pragma unroll 1
-      for (int j = w.begin();; j = w.next(j)) {
+      auto arrived = [&]() {  // the block's first half, where it has not been asked for
         if (!loaded) {
-          if (!wp_wait(sm, &sm.s_full[tile][0], blocks & 1, a.status)) {
-            ok = false;
-            break;
-          }
+          if (!wp_wait(sm, &sm.s_full[tile][0], blocks & 1, a.status)) return false;
           tc_fence_after();
         }
+        return true;
+      };
+      auto end_block = [&]() {
+        ++blocks;
+        if (++used % kWpRun == 0) {
+          sum += run_sum;  // row sums in two levels: equal weights round the same way at every addition
+          run_sum = 0.f;
+          if (!kBf16Out) {
+            drain = 1;
+            d_more = more;
+            d_k = k;
+            more = true;
+          }
+        }
+      };
+#pragma unroll 1
+      for (int j = w.begin();;) {
+        ok = arrived();
+        if (!ok) break;
         const int bad = sm.kv_bad[(gb + j) % kWpStages];
         if (used == 0) {
           // the reference: from the block's first 64 keys (any finite value near the scores will do)
@@ -862,38 +877,49 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         // P overwrites the columns of the S that it comes from.  Keys outside the row's window and sinks, and the keys of
         // invalid pages (loaded as zeros), get weight 0.
         if (bad == 0 && j >= inner0 && j < inner1) {
-          // every quarter is on its way while the one before it is worked on
-          uint32_t p16[kBf16Out ? 16 : 32];
-          if (!loaded) tmem_ld32_async(s_addr, x0);
-          tmem_ld32_wait(x0);
-          tmem_ld32_async(s_addr + 32, x1);
-          run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
-          store_p(s_addr, p16);
-          tmem_ld32_wait(x1);
-          ok = wp_wait(sm, &sm.s_full[tile][1], blocks & 1, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          tmem_ld32_async(s_addr + 64, x0);
-          run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
-          store_p(s_addr + 32, p16);
-          if (!written(0)) {
-            ok = false;
-            break;
-          }
-          tmem_ld32_wait(x0);
-          tmem_ld32_async(s_addr + 96, x1);
-          run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
-          store_p(s_addr + 64, p16);
-          tmem_ld32_wait(x1);
-          loaded = j + 1 < inner1 &&
-                   __all_sync(0xffffffffu, mbar_try_wait(&sm.s_full[tile][0], (blocks + 1) & 1));
-          if (loaded) {
+          bool plain = true;
+#pragma unroll 1
+          while (true) {
+            // every quarter is on its way while the one before it is worked on
+            uint32_t p16[kBf16Out ? 16 : 32];
+            if (!loaded) tmem_ld32_async(s_addr, x0);
+            tmem_ld32_wait(x0);
+            tmem_ld32_async(s_addr + 32, x1);
+            run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
+            store_p(s_addr, p16);
+            tmem_ld32_wait(x1);
+            ok = wp_wait(sm, &sm.s_full[tile][1], blocks & 1, a.status);
+            if (!ok) break;
             tc_fence_after();
-            tmem_ld32_async(s_addr, x0);
+            tmem_ld32_async(s_addr + 64, x0);
+            run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
+            store_p(s_addr + 32, p16);
+            ok = written(0);
+            if (!ok) break;
+            tmem_ld32_wait(x0);
+            tmem_ld32_async(s_addr + 96, x1);
+            run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
+            store_p(s_addr + 64, p16);
+            tmem_ld32_wait(x1);
+            loaded = j + 1 < inner1 &&
+                     __all_sync(0xffffffffu, mbar_try_wait(&sm.s_full[tile][0], (blocks + 1) & 1));
+            if (loaded) {
+              tc_fence_after();
+              tmem_ld32_async(s_addr, x0);
+            }
+            run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
+            store_p(s_addr + 96, p16);
+            written(1);
+            if (j + 1 >= inner1) break;
+            end_block();
+            ++j;
+            ok = arrived();
+            if (!ok) break;
+            plain = sm.kv_bad[(gb + j) % kWpStages] == 0;
+            if (!plain) break;
           }
-          run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
-          store_p(s_addr + 96, p16);
-          written(1);
+          if (!ok) break;
+          if (!plain) continue;  // with a mask
         } else {
           if (loaded) tmem_ld32_wait(x0);  // (asked for before the block's bad pages were known)
           loaded = false;
@@ -936,18 +962,9 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
           }
         }
         if (!ok) break;
-        ++blocks;
-        if (++used % kWpRun == 0) {
-          sum += run_sum;  // row sums in two levels: equal weights round the same way at every addition
-          run_sum = 0.f;
-          if (!kBf16Out) {
-            drain = 1;
-            d_more = more;
-            d_k = k;
-            more = true;
-          }
-        }
+        end_block();
         if (j == w.last) break;
+        j = w.next(j);
       }
       if (!ok) break;
       gb += nblocks;
