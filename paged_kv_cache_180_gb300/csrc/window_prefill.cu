@@ -31,7 +31,7 @@
 //  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing work, waits
 //    (bounded) for what is in flight, frees its tensor memory and exits.
 //
-// What bounds it: 4 x 2048 queries, windows of 2000, bf16 output, take 141 us (135 GFLOP, 960 TFLOP/s, half of the measured
+// What bounds it: 4 x 2048 queries, windows of 2000, bf16 output, take 140 us (135 GFLOP, 965 TFLOP/s, half of the measured
 // bf16 peak): tensor pipe 42 %, exponentials 40 %, issue slots 46 %, so nothing is full; two softmax warps a scheduler wait
 // for S, exponentials and stores in turn, and registers (168 a thread) and tensor memory (all 512 columns are taken) leave
 // no room for a third.  Built and slower: two CTAs to an SM with one S buffer a tile (151 to 161 us), one issuing warp for
