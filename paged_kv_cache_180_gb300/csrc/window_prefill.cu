@@ -1071,7 +1071,9 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   a.status = device_status;
   a.most_items = int((long long)num_seqs * items * pkv::kKvHeads);
   const int by_table = (a.most_items + pkv::kWpMaxItems - 1) / pkv::kWpMaxItems;  // items per CTA <= kWpMaxItems
-  const int g = sms > by_table ? sms : by_table;
+  // in whole rounds of the SMs: a few CTAs more than there are SMs would take as long as all of them (40 x 2048 queries,
+  // windows of 128, bf16 310 us in 304 CTAs, 538 in 160)
+  const int g = by_table > sms ? (by_table + sms - 1) / sms * sms : sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.most_items < g ? a.most_items : g));
   cfg.blockDim = dim3(pkv::kWpThreads);

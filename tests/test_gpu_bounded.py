@@ -240,6 +240,12 @@ def test_window_prefill_longer(pkv, contexts, nodes, window, sinks, bf16):
     tree_limits.assert_precise(got, ref, c.starts, bf16)
 
 
+def test_window_prefill_more_items_than_the_tables_of_all_sms_hold(pkv):
+    r = np.random.RandomState(53)
+    ctx = r.randint(0, 40, 1400)
+    _check_prefill(pkv, B.Cache(ctx.tolist(), np.minimum(ctx, r.randint(0, 4, 1400)).tolist(), seed=54), 9, 2)
+
+
 @pytest.mark.parametrize("scale", [1.0, -0.125, 0.0, 1e-30, -1.0])
 def test_window_prefill_scales(pkv, scale):
     _check_prefill(pkv, B.Cache([300, 70], [60, 33], seed=23), 90, 4, scale=scale)
