@@ -489,6 +489,34 @@ def test_weights_behind_the_append_that_it_overlaps(pkv):
     assert np.array_equal(_guarded(out, 3), want) and torch.equal(sums, want_sums) and int(status.item()) == 0
 
 
+@pytest.mark.parametrize("contexts", [[5000], [2500, 1], [300] * 40])  # clusters of 16 and 8, single CTAs
+def test_shares_of_any_kind_behind_the_append_and_side_by_side(pkv, contexts):
+    n = len(contexts)
+    c = B.Cache(contexts, seed=55)
+    host = _sums(c, 56)
+    want_sums = U.to_dev(host)
+    want, _ = _weights(pkv, c, want_sums, 1.0)
+    want_window, _ = _window_decode(pkv, c, 1 << 30, 0)
+    empty, status = _pool(pkv, oracle.Pool(c.wl.num_pages)), _status()
+    parts = [c.wl.kv_tokens(s, 0) for s in range(n)]
+    k, v = (U.to_dev(np.concatenate([p[i] for p in parts])) for i in (0, 1))
+    slots = U.to_dev(np.concatenate([c.wl.slot_mapping(s, 0, 0, int(c.lens[s])) for s in range(n)]))
+    q, bt, lens, sums = U.to_dev(c.q), U.to_dev(c.bt), U.to_dev(c.lens), U.to_dev(host)
+    outs = [_out(n, False) for _ in range(4)]
+    args = (bt, bt.shape[1], lens, c.max_context, c.scale)
+    pkv.kv_append(empty, k, v, slots, status)
+    pkv.paged_decode_attention_weights(empty, outs[0], q, *args, sums, 1.0, None, status, overlap_previous=True)
+    pkv.paged_window_decode_attention(empty, outs[1], q, *args, 1 << 30, 0, status, overlap_previous=True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for o, stream in zip(outs[2:], streams):
+            pkv.paged_window_decode_attention(empty, o, q, *args, 1 << 30, 0, status, stream=stream)
+    assert np.array_equal(_guarded(outs[0], n), want) and torch.equal(sums, want_sums) and int(status.item()) == 0
+    for o in outs[1:]:
+        assert np.array_equal(_guarded(o, n), want_window)
+
+
 def test_weights_longest_first(pkv):
     # more units than are resident at once: sequences are taken by length, ties and empty ones among them
     r = np.random.RandomState(9)
