@@ -104,7 +104,7 @@ struct WindowArgs {
   int max_query;
   int item_tok;       // query tokens of an item: 64, or 32 (its first tile alone)
   int items_per_seq;  // of max_query query tokens and one K/V head
-  int most_items;     // num_seqs * items_per_seq * 8
+  int most_items;     // num_seqs * items_per_seq * 8, or 4 where the tiles take a K/V head each
   float scale_log2;  // scale * log2(e)
   int32_t *status;
 };
@@ -284,8 +284,8 @@ __device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t
   return t.x + t.y;
 }
 
-// 16 values of an output row from element `at` on.
-template <bool kBf16Out>
+// 16 values of an output row from element `at` on; kWide: 32 bytes at once where the row allows it.
+template <bool kBf16Out, bool kWide>
 __device__ __forceinline__ void store_row(void *out, long long at, const float (&v)[16]) {
   if (kBf16Out) {
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
@@ -295,7 +295,7 @@ __device__ __forceinline__ void store_row(void *out, long long at, const float (
                               pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));
   } else {
     float *dst = static_cast<float *>(out) + at;
-    if ((reinterpret_cast<uintptr_t>(out) & 31u) == 0) {
+    if (kWide && (reinterpret_cast<uintptr_t>(out) & 31u) == 0) {
 #pragma unroll
       for (int c = 0; c < 16; c += 8) {
         const float x[8] = {v[c], v[c + 1], v[c + 2], v[c + 3], v[c + 4], v[c + 5], v[c + 6], v[c + 7]};
@@ -309,11 +309,11 @@ __device__ __forceinline__ void store_row(void *out, long long at, const float (
   }
 }
 
-// Row `tok` of tile t, query head g * 4 + hh, from the keys that it sees alone: the maximum first, then the sums.
+// Row `tok` of item t, query head g * 4 + hh, from the keys that it sees alone: the maximum first, then the sums.
 template <bool kBf16Out>
-__device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t, int tok, int hh) {
+__device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t, int g, int tok, int hh) {
   const int pos = t.ctx - t.n + t.t0 + tok;
-  const long long row = ((long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh) * kHeadDim;
+  const long long row = ((long long)(t.q0 + t.t0 + tok) * kQHeads + g * kGroup + hh) * kHeadDim;
   const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + row);
   const int32_t *table = a.block_tables + (long long)t.s * a.bt_stride;
   const float scale = a.scale_log2;
@@ -332,7 +332,7 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t,
     for (int v = 0; v < t.npages; ++v) {
       const int lp = logical_page(t, v), page = __ldg(table + lp);
       if (unsigned(page) >= unsigned(a.num_pages)) continue;
-      const long long at = page * a.page_stride + (long long)t.g * kWpBox;
+      const long long at = page * a.page_stride + (long long)g * kWpBox;
 #pragma unroll 1
       for (int r = 0; r < kPageTokens; ++r) {
         const int key = lp * kPageTokens + r;
@@ -380,13 +380,14 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t,
   for (int part = 0; part < 4; ++part) {
 #pragma unroll
     for (int c = 0; c < 16; ++c) o[part][c] *= inv;
-    store_row<kBf16Out>(a.out, row + 16 * part, o[part]);
+    // (not 32 bytes at once: in one build only the first of the row's eight such stores arrived, though those of the fast path did)
+    store_row<kBf16Out, false>(a.out, row + 16 * part, o[part]);
   }
 }
 
 // Every role walks the same table of this CTA's items and skips the same items and blocks, so that their running counters
-// agree.
-template <bool kBf16Out>
+// agree.  kPair: an item is one tile's tokens against two K/V heads, a tile each; blocks alternate between them.
+template <bool kBf16Out, bool kPair>
 __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __grid_constant__ WindowArgs a) {
   extern __shared__ uint8_t smem_raw[];
   WpSmem &sm = *reinterpret_cast<WpSmem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
   if (tid == 0) {
     for (unsigned i = 0; i < kWpStages; ++i) {
       mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], kWpTiles);
+      mbar_init(&sm.kv_empty[i], kPair ? 1 : kWpTiles);
     }
     for (int t = 0; t < kWpTiles; ++t) {
       for (int h = 0; h < 2; ++h) {
@@ -449,13 +450,16 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     }
     if (count > 0)
       for (int k = 0; k < nt; ++k) {
-        const int i = item_index(k), u = i / kKvHeads - first;
-        if (u >= 0 && u < count) sm.items[k] = wp_item(a, s, i % kKvHeads, (count - 1 - u) * a.item_tok, q0, n, ctx);
+        constexpr int kHeads = kPair ? kKvHeads / 2 : kKvHeads;
+        const int i = item_index(k), u = i / kHeads - first;
+        if (u >= 0 && u < count)
+          sm.items[k] = wp_item(a, s, i % kHeads * (kKvHeads / kHeads), (count - 1 - u) * a.item_tok, q0, n, ctx);
       }
     before += all;
     __syncthreads();
   }
   negative = __syncthreads_or(negative);
+  constexpr int kShift = kPair ? 1 : 0;  // blocks of an item: nblocks << kShift
   uint64_t redo = 0;  // softmax threads: bit k set where this thread's row of item k has to be computed again
   // index of the first running item at or after k
   auto next_run = [&](int k) {
@@ -495,7 +499,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       int ent_next[4] = {-1, -1, -1, -1};
       if (kn < nt) load_entries(sm.items[kn], ent_next);  // in flight while this item's blocks go out
       const int32_t *table = a.block_tables + (long long)t.s * a.bt_stride;
-      for (int j = 0; j < t.nblocks; ++j, ++gb) {
+      for (int b = 0; b < t.nblocks << kShift; ++b, ++gb) {
+        const int j = b >> kShift, head = kPair ? t.g + (b & 1) : t.g;
         const unsigned st = gb % kWpStages;
         if (gb >= kWpStages) {
           if (!wp_wait(sm, &sm.kv_empty[st], (gb / kWpStages - 1) & 1, a.status)) {
@@ -522,10 +527,10 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
           mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kWpTileBytes);
 #pragma unroll
           for (int pp = 0; pp < kWpPagesPerBlock; ++pp)
-            tma_load_3d(sm.k[st] + pp * kWpBox, &a.tmap_k, 0, t.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
+            tma_load_3d(sm.k[st] + pp * kWpBox, &a.tmap_k, 0, head * kPageTokens, page[pp], &sm.kv_full[st], policy);
 #pragma unroll
           for (int pp = 0; pp < kWpPagesPerBlock; ++pp)
-            tma_load_3d(sm.v[st] + pp * kWpBox, &a.tmap_v, 0, t.g * kPageTokens, page[pp], &sm.kv_full[st], policy);
+            tma_load_3d(sm.v[st] + pp * kWpBox, &a.tmap_v, 0, head * kPageTokens, page[pp], &sm.kv_full[st], policy);
         }
         __syncwarp();
       }
@@ -541,7 +546,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     __syncwarp();
   } else if (warp >= kWpIssuers) {
     // ================= issuers: the MMAs of a tile each (one thread issues, the warp waits) =================
-    const int tile = warp - kWpIssuers;
+    const int tile = warp - kWpIssuers, part = kPair ? 0 : tile;  // the tile's share of the item's tokens
     const uint32_t sa = tmem + kColS + tile * kWpKeys, oa = tmem + kColO + tile * kHeadDim,
                    qa = tmem + kColQ + tile * (kHeadDim / 2);
     const uint64_t k_desc = sw128_desc(smem_addr(sm.k), 16, 1024), v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     unsigned qs = 0, pvs = 0;       // Q's and blocks of P taken up
     bool ok = true;
     auto pass_to = [&](unsigned block) {  // the tile uses none of the blocks before `block` that it has not given back
-      while (passed < block) {
+      while (!kPair && passed < block) {
         if (!wp_wait(sm, &sm.kv_full[passed % kWpStages], (passed / kWpStages) & 1, a.status)) return false;
         if (elect_one()) mbar_arrive(&sm.kv_empty[passed % kWpStages]);
         __syncwarp();
@@ -565,17 +570,18 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     };
     auto first_block = [&](Cursor &c) {  // of the tile's first item at or behind c.k; false: there is none
       for (c.k = next_run(c.k); c.k < nt; c.k = next_run(c.k + 1)) {
-        c.w = tile_of(a, sm.items[c.k], tile);
+        c.w = tile_of(a, sm.items[c.k], part);
         c.j = c.w.begin();
         if (c.w.last >= 0) return true;
-        c.base += sm.items[c.k].nblocks;
+        c.base += sm.items[c.k].nblocks << kShift;
       }
       return false;
     };
+    auto block_of = [&](const Cursor &c) { return c.base + unsigned(kPair ? 2 * c.j + tile : c.j); };
     auto ready = [&](const Cursor &c, bool fresh) {  // the block has landed, and Q where it is an item's first
       const WpItem &t = sm.items[c.k];
       const int j = c.j;
-      const unsigned block = c.base + j, st = block % kWpStages;
+      const unsigned block = block_of(c), st = block % kWpStages;
       if (!wp_wait(sm, &sm.kv_full[st], (block / kWpStages) & 1, a.status)) return false;
       if (j == t.nblocks - 1) {
         // V rows at or past the context in the sequence's last page (stale pool bytes) become zeros
@@ -628,10 +634,10 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     Cursor c = {0, 0, 0u, {0, 0, -1}};
     bool more = first_block(c);
     if (more) {
-      ok = pass_to(c.base + c.j) && ready(c, true);
+      ok = pass_to(block_of(c)) && ready(c, true);
       if (ok) {
-        issue_s((c.base + c.j) % kWpStages, 0);
-        issue_s((c.base + c.j) % kWpStages, 1);
+        issue_s(block_of(c) % kWpStages, 0);
+        issue_s(block_of(c) % kWpStages, 1);
       }
     }
     int used = 0;
@@ -641,16 +647,17 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       const bool ends = last || (!kBf16Out && used % kWpRun == kWpRun - 1);
       Cursor n = c;
       if (last) {
-        n.base += sm.items[c.k].nblocks;
+        n.base += sm.items[c.k].nblocks << kShift;
         ++n.k;
         more = first_block(n);
       } else {
         n.j = c.w.next(c.j);
       }
-      const unsigned block = c.base + c.j, follows = n.base + n.j, st = block % kWpStages, sn = follows % kWpStages;
+      const unsigned block = block_of(c), follows = block_of(n), st = block % kWpStages, sn = follows % kWpStages;
       // The next block's S goes half by half behind P V of this one's, from one item to the next as well.  Where blocks lie
       // between that the tile does not use, this one is given back first (their copies may wait for its stage).
-      const bool near = more && follows == block + 1;
+      // (A pair's tile uses every second block, all of those, and the other ones are not its to give back.)
+      const bool near = more && (kPair || follows == block + 1);
       ok = issue_pv(st, 0, starts, ends);
       if (near) {
         ok = ok && ready(n, last);
@@ -678,7 +685,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     __syncwarp();
   } else {
     // ================= softmax groups: thread = row = 4 * token + head of tile `tile` =================
-    const int tile = warp >> 2, r = tid & (kWpRows - 1), tok = tile * kWpTok + (r >> 2), hh = r & 3;
+    const int tile = warp >> 2, share = kPair ? 0 : tile, r = tid & (kWpRows - 1), tok = share * kWpTok + (r >> 2), hh = r & 3;
+    auto head_of = [&](const WpItem &t) { return kPair ? t.g + tile : t.g; };
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim;
     // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there, so that the
@@ -688,11 +696,11 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     int q_item = -1;  // whose Q has been fetched: the tile's next
     auto fetch_q = [&]() {
       do q_item = next_run(q_item + 1);
-      while (q_item < nt && (tile * kWpTok >= a.item_tok || sm.items[q_item].t0 + tile * kWpTok >= sm.items[q_item].n));
+      while (q_item < nt && (share * kWpTok >= a.item_tok || sm.items[q_item].t0 + share * kWpTok >= sm.items[q_item].n));
       if (q_item < nt) {
         const WpItem &t = sm.items[q_item];
         const bool there = t.t0 + tok < t.n;
-        const long long row = (long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh;
+        const long long row = (long long)(t.q0 + t.t0 + tok) * kQHeads + head_of(t) * kGroup + hh;
         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim);
 #pragma unroll
         for (int i = 0; i < kHeadDim / 8; ++i) {
@@ -729,11 +737,11 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       tc_fence_after();
       const WpItem &t = sm.items[d_k];
       const bool d_row = t.t0 + tok < t.n;  // the row has a query
-      const long long d_at = ((long long)(t.q0 + t.t0 + tok) * kQHeads + t.g * kGroup + hh) * kHeadDim;
+      const long long d_at = ((long long)(t.q0 + t.t0 + tok) * kQHeads + head_of(t) * kGroup + hh) * kHeadDim;
       float finite = 0.f;  // stays 0 where every value of the row is finite
       const float inv = drain == 1 ? 1.f : d_sum != 0.f ? 1.f / d_sum : 0.f;
       // the warp's 8 tokens by TMA, where the item ends and they are the sequence's own
-      const int first_tok = t.t0 + tile * kWpTok + 8 * (warp & 3);
+      const int first_tok = t.t0 + share * kWpTok + 8 * (warp & 3);
       const bool boxed = drain == 2 && first_tok + 8 <= t.n;
       uint8_t *mine = sm.rows[warp][0] + lane * 128;
       if (boxed) {
@@ -775,15 +783,15 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
                   make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         } else if (d_row) {
-          store_row<kBf16Out>(a.out, d_at + part, v);
+          store_row<kBf16Out, true>(a.out, d_at + part, v);
         }
       }
       if (boxed) {
         fence_proxy_async_smem();
         __syncwarp();
         if (elect_one()) {
-          tma_store_3d(&a.tmap_o, 0, t.g * kGroup, t.q0 + first_tok, sm.rows[warp][0]);
-          if (!kBf16Out) tma_store_3d(&a.tmap_o, 32, t.g * kGroup, t.q0 + first_tok, sm.rows[warp][1]);
+          tma_store_3d(&a.tmap_o, 0, head_of(t) * kGroup, t.q0 + first_tok, sm.rows[warp][0]);
+          if (!kBf16Out) tma_store_3d(&a.tmap_o, 32, head_of(t) * kGroup, t.q0 + first_tok, sm.rows[warp][1]);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         __syncwarp();
@@ -804,14 +812,15 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     for (int k = 0; ok && k < nt; ++k) {
       const WpItem &t = sm.items[k];
       if (t.invalid) {
-        // invalid sequence: zero this item's rows (its tokens, query heads 4g .. 4g+3)
+        // invalid sequence: zero this item's rows (its tokens, the query heads of its K/V heads)
         if (t.t0 == 0 && t.g == 0 && tid == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
         // (the last item of more query tokens than max_query takes all that are left)
         const long long left = t.n - t.t0;
         const long long toks = t.t0 + a.item_tok >= a.max_query ? left : min((long long)a.item_tok, left);
-        for (long long i = tid; i < toks * kGroup * kHeadDim; i += kWpTiles * kWpRows) {
-          const long long row = (long long)t.q0 + t.t0 + i / (kGroup * kHeadDim);
-          const long long at = (row * kQHeads + t.g * kGroup) * kHeadDim + i % (kGroup * kHeadDim);
+        constexpr int kWidth = (kGroup * kHeadDim) << kShift;
+        for (long long i = tid; i < toks * kWidth; i += kWpTiles * kWpRows) {
+          const long long row = (long long)t.q0 + t.t0 + i / kWidth;
+          const long long at = (row * kQHeads + t.g * kGroup) * kHeadDim + i % kWidth;
           if (row < 0 || row >= a.num_q_rows) continue;
           if (kBf16Out)
             static_cast<uint16_t *>(a.out)[at] = 0;
@@ -821,14 +830,14 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         continue;
       }
       if (!t.run) continue;
-      const WpTile w = tile_of(a, t, tile);
+      const WpTile w = tile_of(a, t, share);
       if (w.last < 0) {
-        gb += t.nblocks;
+        gb += t.nblocks << kShift;
         continue;
       }
       const int pos = t.ctx - t.n + min(t.t0 + tok, t.n - 1);
       const int lo = max(0, pos - a.window + 1);
-      const int skip = t.skip, nblocks = t.nblocks;
+      const int skip = t.skip;
       // blocks inner0 .. inner1 - 1 hold only keys that every row of the warp sees: from the last row's window on, up to the
       // first row's position
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0), lo31 = __shfl_sync(0xffffffffu, lo, 31);
@@ -864,7 +873,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       for (int j = w.begin();;) {
         ok = arrived();
         if (!ok) break;
-        const int bad = sm.kv_bad[(gb + j) % kWpStages];
+        const int bad = sm.kv_bad[(gb + (kPair ? 2 * j + tile : j)) % kWpStages];
         if (used == 0) {
           // the reference: from the block's first 64 keys (any finite value near the scores will do)
           uint32_t y[32];
@@ -915,7 +924,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
             ++j;
             ok = arrived();
             if (!ok) break;
-            plain = sm.kv_bad[(gb + j) % kWpStages] == 0;
+            plain = sm.kv_bad[(gb + (kPair ? 2 * j + tile : j)) % kWpStages] == 0;
             if (!plain) break;
           }
           if (!ok) break;
@@ -967,7 +976,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         j = w.next(j);
       }
       if (!ok) break;
-      gb += nblocks;
+      gb += t.nblocks << kShift;
       // the item's last block: what is taken out last is divided
       d_more = drain == 1 ? d_more : more;
       drain = 2;
@@ -985,8 +994,16 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     tmem_dealloc(tmem, kWpTmemCols);
   }
   for (int k = 0; redo != 0; ++k, redo >>= 1)
-    if (redo & 1) recompute_row<kBf16Out>(a, sm.items[k], (tid >> 7) * kWpTok + ((tid & 127) >> 2), tid & 3);
+    if (redo & 1) {
+      const int tile = tid >> 7;
+      recompute_row<kBf16Out>(a, sm.items[k], sm.items[k].g + (kPair ? tile : 0), (kPair ? 0 : tile * kWpTok) + ((tid & 127) >> 2),
+                              tid & 3);
+    }
 }
+
+using WindowKernel = void (*)(WindowArgs);
+constexpr WindowKernel kWindowKernels[] = {window_prefill_kernel<false, false>, window_prefill_kernel<true, false>,
+                                           window_prefill_kernel<false, true>, window_prefill_kernel<true, true>};
 
 // Shared-memory limits of the kernels on the current device.
 int setup_window_attributes() {
@@ -999,13 +1016,11 @@ int setup_window_attributes() {
   }
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(window_prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kWpSmemBytes)) != cudaSuccess ||
-        cudaFuncSetAttribute(window_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(kWpSmemBytes)) != cudaSuccess) {
-      cudaGetLastError();
-      return PKV_ERR_CUDA;
-    }
+    for (WindowKernel kernel : kWindowKernels)
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWpSmemBytes)) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+      }
     done[dev] = true;
   }
   return PKV_OK;
@@ -1038,7 +1053,8 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 10.2 us so and
   // 12.2 in items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 52 us and 41.
   const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
-  const int item_tok = (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
+  const bool pair = max_query <= pkv::kWpTok && (long long)num_seqs * pkv::kKvHeads > sms;
+  const int item_tok = pair || (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
   const long long items = (max_query + item_tok - 1) / item_tok;
   if ((long long)num_seqs * items * pkv::kKvHeads > 0x3fffffffLL) return PKV_ERR_SHAPE;
   rc = pkv::setup_window_attributes();
@@ -1069,7 +1085,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   a.items_per_seq = int(items);
   a.scale_log2 = scale * pkv::kLog2e;
   a.status = device_status;
-  a.most_items = int((long long)num_seqs * items * pkv::kKvHeads);
+  a.most_items = int((long long)num_seqs * items * (pair ? pkv::kKvHeads / 2 : pkv::kKvHeads));
   const int by_table = (a.most_items + pkv::kWpMaxItems - 1) / pkv::kWpMaxItems;  // items per CTA <= kWpMaxItems
   // in whole rounds of the SMs: a few CTAs more than there are SMs would take as long as all of them (40 x 2048 queries,
   // windows of 128, bf16 310 us in 304 CTAs, 538 in 160)
@@ -1086,9 +1102,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & PKV_OVERLAP_PREVIOUS) ? 1 : 0;
-  const cudaError_t err = (flags & PKV_OUT_BF16) ? cudaLaunchKernelEx(&cfg, pkv::window_prefill_kernel<true>, a)
-                                                 : cudaLaunchKernelEx(&cfg, pkv::window_prefill_kernel<false>, a);
-  if (err != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pkv::kWindowKernels[(pair ? 2 : 0) + (flags & PKV_OUT_BF16 ? 1 : 0)], a) != cudaSuccess) {
     cudaGetLastError();
     return PKV_ERR_LAUNCH;
   }

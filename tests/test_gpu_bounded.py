@@ -240,6 +240,74 @@ def test_window_prefill_longer(pkv, contexts, nodes, window, sinks, bf16):
     tree_limits.assert_precise(got, ref, c.starts, bf16)
 
 
+# more than 19 sequences of at most 32 queries: two K/V heads to an item
+def _many_spans(seed, n=26, top=700):
+    r = np.random.RandomState(seed)
+    ctx = r.randint(0, top, n)
+    ctx[:4] = (top, 33, 16, 1)
+    nodes = np.minimum(ctx, r.randint(0, 33, n))
+    nodes[:3] = (32, 32, 8)
+    return B.Cache(ctx.tolist(), nodes.tolist(), seed=seed)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (16, 1), (33, 17), (128, 4), (1000, 0), (2, 300), (200, 40)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_window_prefill_short_spans(pkv, window, sinks, bf16):
+    _check_prefill(pkv, _many_spans(57), window, sinks, bf16)
+
+
+def test_window_prefill_short_spans_of_long_contexts(pkv):
+    ctx, nodes = [2500, 40, 1700] + [600] * 20, [5, 32, 17] + [1, 2, 7, 31] * 5
+    c = B.Cache(ctx, nodes, seed=58)
+    for window, sinks, bf16 in ((2100, 20, False), (100000, 0, False), (1300, 4, True)):   # sums taken out after 1024 keys
+        _check_prefill(pkv, c, window, sinks, bf16)
+
+
+def test_window_prefill_short_spans_bad_lengths_pages_and_values(pkv):
+    c = _many_spans(59)
+    big = [s for s in range(26) if c.lens[s] > 250 and c.nodes[s] > 3]
+    bt = c.bt.copy()
+    bt[big[0], 3], bt[big[1], int(c.lens[big[1]]) // 16 - 1] = -7, c.pool.num_pages + 5
+    _check_prefill(pkv, c, 1000, 2, bt=bt)
+    lens = c.lens.copy()
+    lens[big[0]], lens[big[1]], lens[big[2]] = 3, -5, c.max_context + 1            # fewer tokens than queries, bad lengths
+    got, status = _window_prefill(pkv, c, 64, 2, lens=lens, bt=c.bt)
+    ref, err, _, _ = c.prefill(64, 2, lens=lens)
+    assert status == err == 2 and np.abs(got - ref).max() < 1e-4
+    for s in big[:3]:
+        assert (got[c.starts[s]:c.starts[s + 1]] == 0).all()
+    # NaN in V of one head's token: rows that see it are NaN, all others as if it were not there
+    s, head, window = big[3], 5, 40
+    t = int(c.lens[s]) - int(c.nodes[s]) - 20
+    want = c.prefill(window, 0)[0]
+    c.token(s, t, 1)[head] = 0x7fc0
+    got, status = _window_prefill(pkv, c, window, 0)
+    hit = np.zeros((c.rows, 32), bool)
+    for j in range(c.nodes[s]):
+        if t in bounded.seen_by(int(c.lens[s]) - c.nodes[s] + j, window, 0):
+            hit[c.starts[s] + j, 4 * head:4 * head + 4] = True
+    assert status == 0 and hit.any() and not np.isfinite(got[hit]).any()
+    assert np.abs(got[~hit] - want[~hit]).max() < 2e-5
+
+
+def test_window_prefill_short_spans_in_graphs(pkv):
+    c = _many_spans(60, 40, 300)
+    want, _ = _window_prefill(pkv, c, 100, 4)
+    pool, status, out = _pool(pkv, c.pool), _status(), _out(c.rows, False)
+    q, bt, lens, starts = U.to_dev(c.q), U.to_dev(c.bt), U.to_dev(c.lens), U.to_dev(c.starts)
+    args = (bt, bt.shape[1], lens, c.max_query, c.max_context, c.scale, 100, 4, status)
+    pkv.paged_window_prefill_attention(pool, out, q, starts, *args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for overlap in (False, True):
+            pkv.paged_window_prefill_attention(pool, out, q, starts, *args, overlap_previous=overlap)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        assert np.array_equal(_guarded(out, c.rows), want) and int(status.item()) == 0
+
+
 def test_window_prefill_more_items_than_the_tables_of_all_sms_hold(pkv):
     r = np.random.RandomState(53)
     ctx = r.randint(0, 40, 1400)
