@@ -8,8 +8,9 @@
 //  * An item is 64 query tokens of a sequence against one K/V head: two tiles of 32 tokens, 128 rows each (row = 4 * token
 //    + head in group).  Both tiles use each K/V block that is loaded, or one of them where the other sees nothing of it.
 //    The pages that the item's rows see (the sinks' and those from the first row's window on; none between) are numbered
-//    without the gap and go eight to a block of 128 keys, so that the sinks cost a page and not a block. Where there are
-//    fewer items than half the SMs, they have one tile.
+//    without the gap and go eight to a block of 128 keys, so that the sinks cost a page and not a block.  Where there are
+//    fewer items than half the SMs, they have one tile.  Where no sequence has more than 32 query tokens, and there are
+//    more sequences than fill the SMs, an item is one tile's tokens against two K/V heads, a tile each.
 //  * The grid is persistent, one CTA to an SM; the items that there are (a prefix sum over the sequences' lengths, made by
 //    every CTA) are dealt in a snake, each sequence's latest first.
 //  * Q_t stays in tensor memory (its rows' own threads put it there).  A block's S_t = Q_t K^T is computed in two halves of
@@ -36,7 +37,7 @@
 // for S, exponentials and stores in turn, and registers (168 a thread) and tensor memory (all 512 columns are taken) leave
 // no room for a third.  Built and slower: two CTAs to an SM with one S buffer a tile (151 to 161 us), one issuing warp for
 // both tiles (62 cycles a product), softmax warps that issue for themselves (166).  With fp32 output the second terms take
-// 2.5 times the instructions a weight: 2048 queries, windows of 4096, 154 us for 76.  Short windows: 16 x 512 queries,
+// 2.5 times the instructions a weight: 2048 queries, windows of 4096, 146 us for 76.  Short windows: 16 x 512 queries,
 // windows of 128, fp32 in 41 us, 12900 cycles an item of two blocks, of them 2000 waiting for its S, 1800 taking out the O
 // before it, the rest four masked halves.  200 queries of one sequence: 10.3 us, the latencies of one item (lists and
 // set-up 2, first K/V 2, blocks and output the rest).
@@ -380,7 +381,8 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t,
   for (int part = 0; part < 4; ++part) {
 #pragma unroll
     for (int c = 0; c < 16; ++c) o[part][c] *= inv;
-    // (not 32 bytes at once: in one build only the first of the row's eight such stores arrived, though those of the fast path did)
+    // (not 32 bytes at once: in one build only the first of the row's eight such stores arrived, though those of the fast
+    // path did)
     store_row<kBf16Out, false>(a.out, row + 16 * part, o[part]);
   }
 }
@@ -685,7 +687,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     __syncwarp();
   } else {
     // ================= softmax groups: thread = row = 4 * token + head of tile `tile` =================
-    const int tile = warp >> 2, share = kPair ? 0 : tile, r = tid & (kWpRows - 1), tok = share * kWpTok + (r >> 2), hh = r & 3;
+    const int tile = warp >> 2, share = kPair ? 0 : tile;  // ... and its share of the item's tokens
+    const int r = tid & (kWpRows - 1), tok = share * kWpTok + (r >> 2), hh = r & 3;
     auto head_of = [&](const WpItem &t) { return kPair ? t.g + tile : t.g; };
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim;
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       }
       const int pos = t.ctx - t.n + min(t.t0 + tok, t.n - 1);
       const int lo = max(0, pos - a.window + 1);
-      const int skip = t.skip;
+      const int skip = t.skip, nblocks = t.nblocks << kShift;
       // blocks inner0 .. inner1 - 1 hold only keys that every row of the warp sees: from the last row's window on, up to the
       // first row's position
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0), lo31 = __shfl_sync(0xffffffffu, lo, 31);
@@ -976,7 +979,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         j = w.next(j);
       }
       if (!ok) break;
-      gb += t.nblocks << kShift;
+      gb += nblocks;
       // the item's last block: what is taken out last is divided
       d_more = drain == 1 ? d_more : more;
       drain = 2;
@@ -996,8 +999,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
   for (int k = 0; redo != 0; ++k, redo >>= 1)
     if (redo & 1) {
       const int tile = tid >> 7;
-      recompute_row<kBf16Out>(a, sm.items[k], sm.items[k].g + (kPair ? tile : 0), (kPair ? 0 : tile * kWpTok) + ((tid & 127) >> 2),
-                              tid & 3);
+      recompute_row<kBf16Out>(a, sm.items[k], sm.items[k].g + (kPair ? tile : 0),
+                              (kPair ? 0 : tile * kWpTok) + ((tid & 127) >> 2), tid & 3);
     }
 }
 
@@ -1053,6 +1056,9 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 10.2 us so and
   // 12.2 in items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 52 us and 41.
   const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
+  // No more than 32 queries a sequence fill one tile: two heads then share the CTA, 256 x 4 queries, windows of 512, fp32
+  // in 87 us (123 with the second tile idle), 64 x 16 in 31 (41), 3000 x 10 of 100 in 353 (538), 40 x 32 of 200 in 14.3
+  // (13.9).  While every (sequence, head) finds an SM of its own it has that one.
   const bool pair = max_query <= pkv::kWpTok && (long long)num_seqs * pkv::kKvHeads > sms;
   const int item_tok = pair || (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
   const long long items = (max_query + item_tok - 1) / item_tok;
