@@ -17,8 +17,9 @@
 //    64 keys, into TMEM buffers of their own; P goes back over its half and is the TMEM A operand of O_t += P V.  So while
 //    the softmax works on one half the tensor core has P V of the other and its next S, and shared memory feeds it K and V
 //    alone.  With fp32 output P has two bf16 terms (16 bits), with bf16 output one.  Row sums are added up in registers.
-//  * The exponents of a row refer to the maximum of the scores of its tile's first block, seen by the row or not, and stay
-//    there: weights are floats, so they may well be far from 1.  A row whose sum leaves [2^-90, 2^112] is computed again.
+//  * The exponents of a row refer to the largest score of some keys of its tile's first block, seen by the row or by another
+//    one of the item, and stay there: weights are floats, so they may well be far from 1.  A row whose sum leaves
+//    [2^-90, 2^112] is computed again.
 //  * The tensor core truncates what it adds up.  With fp32 output O is therefore taken out after every 1024 keys and added
 //    to the row in `out`, whose last value is the quotient.
 //  * A warp's finished rows go through shared memory and a TMA store: stored by their threads, 256 bytes apart, they took
@@ -231,25 +232,26 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
 }
 
-// Largest (kMin: smallest) of 32 scores.
+// Of 32 keys from `key` on, `gone` pages behind those that an item's numbering gives them: the ones in [0, pos] that lie at or
+// past lo, or before `sinks` (where pages are left out, the sinks lie before them and the window behind).  Bits 0, 1 of `bad`:
+// the keys' first, second page is invalid.
+__device__ __forceinline__ uint32_t seen_keys(int key, int gone, int lo, int pos, int sinks, int bad) {
+  const int at = key + gone * kPageTokens;
+  uint32_t seen = first_bits(pos + 1 - at) & (~first_bits(lo - at) | first_bits(sinks - key));
+  if (bad & 1) seen &= 0xffff0000u;
+  if (bad & 2) seen &= 0x0000ffffu;
+  return seen;
+}
+
+// Largest (kMin: smallest) of a page's scores.
 template <bool kMin>
-__device__ __forceinline__ float extreme32(const uint32_t (&s)[32]) {
-  float m[11];
+__device__ __forceinline__ float extreme16(const uint32_t (&s)[16]) {
+  auto of3 = [](float x, float y, float z) { return kMin ? min3f(x, y, z) : max3f(x, y, z); };
+  float m[5];
 #pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    const float x = __uint_as_float(s[3 * i]), y = __uint_as_float(s[3 * i + 1]), z = __uint_as_float(s[3 * i + 2]);
-    m[i] = kMin ? min3f(x, y, z) : max3f(x, y, z);
-  }
-  const float u = __uint_as_float(s[30]), v = __uint_as_float(s[31]);
-  m[10] = kMin ? fminf(u, v) : fmaxf(u, v);
-#pragma unroll
-  for (int n = 11; n > 1; n = (n + 2) / 3)
-#pragma unroll
-    for (int i = 0; i < (n + 2) / 3; ++i) {
-      const float x = m[3 * i], y = 3 * i + 1 < n ? m[3 * i + 1] : x, z = 3 * i + 2 < n ? m[3 * i + 2] : x;
-      m[i] = kMin ? min3f(x, y, z) : max3f(x, y, z);
-    }
-  return m[0];
+  for (int i = 0; i < 5; ++i)
+    m[i] = of3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
+  return of3(of3(m[0], m[1], m[2]), of3(m[3], m[4], __uint_as_float(s[15])), m[0]);
 }
 
 // P = 2^(s c - m) for 32 keys as one or two bf16 terms, keys 2i and 2i + 1 packed in word i, the second term behind the
@@ -878,12 +880,28 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         if (!ok) break;
         const int bad = sm.kv_bad[(gb + (kPair ? 2 * j + tile : j)) % kWpStages];
         if (used == 0) {
-          // the reference: from the block's first 64 keys (any finite value near the scores will do)
-          uint32_t y[32];
-          tmem_ld32(s_addr, y);
-          m = scale < 0.f ? extreme32<true>(y) : extreme32<false>(y);
-          tmem_ld32(s_addr + 32, y);
-          m = (scale < 0.f ? fminf(m, extreme32<true>(y)) : fmaxf(m, extreme32<false>(y))) * scale;
+          // The reference: the largest score of the first of the block's first four pages of which every key is seen by some
+          // row of the item and lies at or before the tile's last position (any finite value near the scores will do); where
+          // there is no such page, of such keys of the first page, which has one.  Keys that nobody sees count for nothing:
+          // they may be rows of the pool behind the context, of any value.
+          const int p0 = t.ctx - t.n + t.t0, p1 = t.ctx - t.n + min(t.t0 + (share + 1) * kWpTok, t.n) - 1;
+          const int first = max(0, p0 - a.window + 1);
+          const uint32_t seen0 = seen_keys(j * kWpKeys, skip, first, p1, a.sinks, bad),
+                         seen1 = seen_keys(j * kWpKeys + 32, skip, first, p1, a.sinks, bad >> 2);
+          const int page = (seen0 & 0xffffu) == 0xffffu ? 0
+                           : seen0 >> 16 == 0xffffu     ? 1
+                           : (seen1 & 0xffffu) == 0xffffu ? 2
+                           : seen1 >> 16 == 0xffffu       ? 3
+                                                          : 0;
+          const uint32_t keys = page == 0 ? seen0 : 0xffffu;
+          const float none = scale < 0.f ? INFINITY : -INFINITY;
+          uint32_t y[16];
+          tmem_ld16_async(s_addr + page * kPageTokens, y);
+          tmem_ld_wait(y);
+#pragma unroll
+          for (int i = 0; i < kPageTokens; ++i) y[i] = keys >> i & 1u ? y[i] : __float_as_uint(none);
+          m = scale < 0.f ? extreme16<true>(y) : extreme16<false>(y);
+          m *= scale;
           if (!(fabsf(m) < INFINITY)) m = 0.f;
         }
         // P overwrites the columns of the S that it comes from.  Keys outside the row's window and sinks, and the keys of
@@ -945,15 +963,10 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
               tc_fence_after();
               if (j == w.last) hand_on_q();
             }
-            // columns of [0, pos] without those before the window, or with the sinks among them (where pages are left out,
-            // the sinks lie before them and the window behind); invalid pages take theirs out
-            const int at0 = j * kWpKeys + h * kWpHalf, shift = skip * kPageTokens + at0;
 #pragma unroll 1
             for (int part = 0; part < 2; ++part) {
-              uint32_t valid = first_bits(pos + 1 - shift - 32 * part) &
-                               (~first_bits(lo - shift - 32 * part) | first_bits(a.sinks - at0 - 32 * part));
-              if ((bad >> (4 * h + 2 * part)) & 1) valid &= 0xffff0000u;
-              if ((bad >> (4 * h + 2 * part)) & 2) valid &= 0x0000ffffu;
+              const uint32_t valid = seen_keys(j * kWpKeys + h * kWpHalf + 32 * part, skip, lo, pos, a.sinks,
+                                               bad >> (4 * h + 2 * part));
               uint32_t p16[kBf16Out ? 16 : 32];
               if (__any_sync(0xffffffffu, valid != 0u)) {
                 tmem_ld32(s_addr + h * kWpHalf + 32 * part, x0);
