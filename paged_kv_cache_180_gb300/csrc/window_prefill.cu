@@ -21,9 +21,9 @@
 //    one of the item, and stay there: weights are floats, so they may well be far from 1.  A row whose sum leaves
 //    [2^-90, 2^112] is computed again.
 //  * The tensor core truncates what it adds up.  With fp32 output O is therefore taken out after every 1024 keys and added
-//    to the row in `out`, whose last value is the quotient.
-//  * A warp's finished rows go through shared memory and a TMA store: stored by their threads, 256 bytes apart, they took
-//    3400 cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored
+//    up, with rounding, in shared memory.
+//  * A warp's finished rows go through the same shared memory and a TMA store: stored by their threads, 256 bytes apart, they
+//    took 3400 cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored
 //    directly.)
 //  * Keys that a row does not see get weight 0.  Their V meets that weight in the product all the same, so a NaN or an
 //    infinity in it would reach rows that do not see it: a row whose output is not finite is computed again at the end,
@@ -124,7 +124,7 @@ struct WpItem {
 struct __align__(1024) WpSmem {
   uint8_t k[kWpStages][kWpTileBytes];  // 128 keys x 128 B per stage, 128-byte swizzled
   uint8_t v[kWpStages][kWpTileBytes];
-  uint8_t rows[kWpTiles * 4][2][32 * 128];  // a warp's finished rows, 128 bytes of each at a time, swizzled
+  uint8_t rows[kWpTiles * 4][2][32 * 128];  // a warp's rows, 128 bytes of each at a time, swizzled: sums of runs, then the output
   uint64_t q_full[kWpTiles];  // the tile's Q is in tensor memory (a warp arrives once)
   uint64_t kv_full[kWpStages], kv_empty[kWpStages];
   uint64_t s_full[kWpTiles][2];  // S of the half of the tile's next block is there, and its bad pages are known
@@ -735,40 +735,64 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     // O to be taken out once the next P is written: 0 none, 1 a run's, 2 the item's
     int drain = 0, d_k = 0;
     float d_sum = 0.f;
-    bool d_more = false;  // earlier runs lie in `out`
-    auto take_out = [&]() {
+    bool d_more = false;  // the sum of earlier runs lies in the warp's rows
+    uint8_t *mine = sm.rows[warp][0] + lane * 128;
+    auto mine_at = [&](int part, int i) {  // fp32 values part + 4 i .. + 3 of the row
+      return reinterpret_cast<float4 *>(mine + (part / 32) * 4096 + (((part % 32 / 4 + i) ^ (lane & 7)) << 4));
+    };
+    auto o_ready = [&]() {
       if (!wp_wait(sm, &sm.o_full[tile], drained & 1, a.status)) return false;
       ++drained;
       tc_fence_after();
+      return true;
+    };
+    auto rows_free = [&]() {  // the rows that were stored last have been read
+      if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    };
+    auto values = [&](int part, float (&v)[16]) {  // of O, and of the runs before
+      uint32_t o[16];
+      tmem_ld16_async(o_addr + part, o);
+      tmem_ld_wait(o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]);
+      if (!kBf16Out && d_more) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *mine_at(part, i);
+          v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+        }
+      }
+    };
+    auto take_run = [&]() {
+      if (!o_ready()) return false;
+      if (!d_more) rows_free();
+#pragma unroll 1
+      for (int part = 0; part < kHeadDim; part += 16) {
+        float v[16];
+        values(part, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *mine_at(part, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+      drain = 0;
+      return true;
+    };
+    auto take_item = [&]() {
+      if (!o_ready()) return false;
       const WpItem &t = sm.items[d_k];
       const bool d_row = t.t0 + tok < t.n;  // the row has a query
       const long long d_at = ((long long)(t.q0 + t.t0 + tok) * kQHeads + head_of(t) * kGroup + hh) * kHeadDim;
       float finite = 0.f;  // stays 0 where every value of the row is finite
-      const float inv = drain == 1 ? 1.f : d_sum != 0.f ? 1.f / d_sum : 0.f;
-      // the warp's 8 tokens by TMA, where the item ends and they are the sequence's own
+      const float inv = d_sum != 0.f ? 1.f / d_sum : 0.f;
+      // the warp's 8 tokens by TMA, where they are the sequence's own
       const int first_tok = t.t0 + share * kWpTok + 8 * (warp & 3);
-      const bool boxed = drain == 2 && first_tok + 8 <= t.n;
-      uint8_t *mine = sm.rows[warp][0] + lane * 128;
-      if (boxed) {
-        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the rows before have been read
-        __syncwarp();
-      }
+      const bool boxed = first_tok + 8 <= t.n;
+      if (boxed) rows_free();
 #pragma unroll 1
       for (int part = 0; part < kHeadDim; part += 16) {
-        uint32_t o[16];
-        tmem_ld16_async(o_addr + part, o);
-        tmem_ld_wait(o);
         float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]);
-        if (!kBf16Out && d_more && d_row) {
-          const float4 *old = reinterpret_cast<const float4 *>(static_cast<const float *>(a.out) + d_at + part);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 x = old[i];
-            v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
-          }
-        }
+        values(part, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           v[i] *= inv;
@@ -784,8 +808,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4 *>(mine + (part / 32) * 4096 + (((part % 32 / 4 + i) ^ (lane & 7)) << 4)) =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              *mine_at(part, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         } else if (d_row) {
           store_row<kBf16Out, true>(a.out, d_at + part, v);
@@ -801,18 +824,15 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         }
         __syncwarp();
       }
-      if (drain == 2 && d_row && !(finite == 0.f && d_sum >= kSumMin && d_sum <= kSumMax)) redo |= 1ull << d_k;
+      if (d_row && !(finite == 0.f && d_sum >= kSumMin && d_sum <= kSumMax)) redo |= 1ull << d_k;
       drain = 0;
       return true;
     };
     auto written = [&](int h) {  // P of a half is there
       tmem_st_wait();
-      // O of the run or item before, before the issuer starts it anew
-      if (h == 0 && drain != 0 && !take_out()) return false;
       tc_fence_before();
       __syncwarp();
       if (elect_one()) mbar_arrive(&sm.p_full[tile][h]);
-      return true;
     };
     for (int k = 0; ok && k < nt; ++k) {
       const WpItem &t = sm.items[k];
@@ -906,7 +926,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
         }
         // P overwrites the columns of the S that it comes from.  Keys outside the row's window and sinks, and the keys of
         // invalid pages (loaded as zeros), get weight 0.
-        if (bad == 0 && j >= inner0 && j < inner1) {
+        if (bad == 0 && j >= inner0 && j < inner1 && drain != 2) {
           bool plain = true;
 #pragma unroll 1
           while (true) {
@@ -924,8 +944,12 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
             tmem_ld32_async(s_addr + 64, x0);
             run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
             store_p(s_addr + 32, p16);
-            ok = written(0);
-            if (!ok) break;
+            if (drain != 0) {  // O of the run before, before the issuer starts it anew
+              tmem_st_wait();
+              ok = take_run();
+              if (!ok) break;
+            }
+            written(0);
             tmem_ld32_wait(x0);
             tmem_ld32_async(s_addr + 96, x1);
             run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
@@ -980,10 +1004,12 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
               }
               store_p(s_addr + h * kWpHalf + 32 * part, p16);
             }
-            if (!written(h)) {
-              ok = false;
-              break;
+            if (h == 0 && drain != 0) {
+              tmem_st_wait();
+              ok = drain == 1 ? take_run() : take_item();
+              if (!ok) break;
             }
+            written(h);
           }
         }
         if (!ok) break;
@@ -999,7 +1025,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       d_k = k;
       d_sum = sum + run_sum;
     }
-    if (ok && drain != 0) take_out();
+    if (ok && drain != 0) take_item();
     if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // every row has been written
     __syncwarp();
   }

@@ -6,6 +6,8 @@ import torch
 from oracle import bounded
 from tests import bounded_util as B
 from tests import gpu_util as U
+from tests import spec_util as S
+from tests import tree_limits
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,16 @@ def test_what_nobody_sees_reaches_nothing(pkv, shape, bf16):
             got = _prefill(pkv, c, pool, window, sinks, bf16, scale)
             want = got if want is None else want
             assert torch.equal(got, want), (window, sinks, hex(k), float((got - want).abs().max()))
+
+
+@pytest.mark.parametrize("contexts,nodes", [([1024, 1025, 2048, 2049, 3000], [8, 9, 32, 33, 1]), ([2048, 1100], [2048, 70]),
+                                            ([1024, 1040, 2050] * 8, [8, 5, 32] * 8)])
+def test_runs_of_a_row_are_added_up_in_fp32(pkv, contexts, nodes):
+    """Rows of one to three runs of 1024 keys, runs that end with the item, rows stored by boxes and by their threads."""
+    c = B.Cache(contexts, nodes, seed=72)
+    want, _, size, spread = c.prefill(1 << 30, 0)
+    got = _prefill(pkv, c, c.pool.data, 1 << 30, 0, False, c.scale)
+    S.assert_within(got.double().cpu().numpy(), want, S.bound(want, size, spread, c.scale, 3000, False), "window prefill")
+    tree_limits.assert_precise(got.cpu().numpy(), want, c.starts, False)
+    for _ in range(5):
+        assert torch.equal(_prefill(pkv, c, c.pool.data, 1 << 30, 0, False, c.scale), got)
