@@ -20,8 +20,8 @@
 //  * The exponents of a row refer to the largest score of some keys of its tile's first block, seen by the row or by another
 //    one of the item, and stay there: weights are floats, so they may well be far from 1.  A row whose sum leaves
 //    [2^-90, 2^112] is computed again.
-//  * The tensor core truncates what it adds up.  With fp32 output O is therefore taken out after every 1024 keys and added
-//    up, with rounding, in shared memory.
+//  * The tensor core truncates what it adds up.  O is therefore taken out after every run of 1024 keys (fp32 output) or 16384
+//    keys (bf16 output: one run over 2^24 equal weights lost 15 %), and runs are added up, with rounding, in shared memory.
 //  * A warp's finished rows go through the same shared memory and a TMA store: stored by their threads, 256 bytes apart, they
 //    took 3400 cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored
 //    directly.)
@@ -67,7 +67,9 @@ constexpr int kWpHalf = kWpKeys / 2;                   // keys of an S buffer
 constexpr int kWpMaxItems = 64;                        // items a CTA walks (its table in shared memory)
 constexpr int kWpBox = kPageTokens * kRowBytes;        // one head's rows of one page: 2 KiB
 constexpr int kWpTileBytes = kWpKeys * kRowBytes;      // K (or V) of one block: 16 KiB
-constexpr int kWpRun = 8;                              // blocks that O adds up at once with fp32 output
+template <bool kBf16>
+constexpr int kWpRun = kBf16 ? 128 : 8;                // blocks that O adds up at once
+constexpr int kWpSumRun = 8;                           // blocks whose weights are added up at once
 constexpr uint32_t kWpTmemCols = 512;
 // columns of S_0, S_1 (128 each), of O_0, O_1 (64) and of Q_0, Q_1 (32)
 constexpr uint32_t kColS = 0, kColO = kWpTiles * kWpKeys, kColQ = kColO + kWpTiles * kHeadDim;
@@ -647,8 +649,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     int used = 0;
 #pragma unroll 1
     while (ok && more) {
-      const bool last = c.j == c.w.last, starts = kBf16Out ? used == 0 : used % kWpRun == 0;
-      const bool ends = last || (!kBf16Out && used % kWpRun == kWpRun - 1);
+      const bool last = c.j == c.w.last, starts = used % kWpRun<kBf16Out> == 0;
+      const bool ends = last || used % kWpRun<kBf16Out> == kWpRun<kBf16Out> - 1;
       Cursor n = c;
       if (last) {
         n.base += sm.items[c.k].nblocks << kShift;
@@ -756,7 +758,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       tmem_ld_wait(o);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]);
-      if (!kBf16Out && d_more) {
+      if (d_more) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 x = *mine_at(part, i);
@@ -883,15 +885,15 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       };
       auto end_block = [&]() {
         ++blocks;
-        if (++used % kWpRun == 0) {
+        if (++used % kWpSumRun == 0) {
           sum += run_sum;  // row sums in two levels: equal weights round the same way at every addition
           run_sum = 0.f;
-          if (!kBf16Out) {
-            drain = 1;
-            d_more = more;
-            d_k = k;
-            more = true;
-          }
+        }
+        if (used % kWpRun<kBf16Out> == 0) {
+          drain = 1;
+          d_more = more;
+          d_k = k;
+          more = true;
         }
       };
 #pragma unroll 1

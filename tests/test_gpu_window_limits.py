@@ -1,4 +1,4 @@
-"""Limits of window prefill: what pools hold where nobody looks."""
+"""Limits of window prefill: what pools hold where nobody looks, and sums over long windows."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +8,7 @@ from tests import bounded_util as B
 from tests import gpu_util as U
 from tests import spec_util as S
 from tests import tree_limits
+from workloads import rng
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,77 @@ def test_runs_of_a_row_are_added_up_in_fp32(pkv, contexts, nodes):
     tree_limits.assert_precise(got.cpu().numpy(), want, c.starts, False)
     for _ in range(5):
         assert torch.equal(_prefill(pkv, c, c.pool.data, 1 << 30, 0, False, c.scale), got)
+
+
+def repeated_pages(pkv, pages, bf16, seed, positive=False, order=(0,), keys=None, seconds=None):
+    """(output, expected output, weighted sum of |V|) of one query over a context of `pages` pages: those of `order`, then
+    page 1, whose keys are equal, again and again.  keys(K): sets the K of the pages [page][head][row][dim] as bits.
+    `seconds`: a list that receives the time the call took."""
+    ctx, ids = 16 * pages, max(2, max(order) + 1)
+    draw = lambda tag, n: rng.normal_bf16(rng.stream_key(seed, tag), 0, n)  # noqa: E731
+    kv = draw("kv", ids * 2 * 8 * 16 * 64).reshape(ids, 2, 8, 16, 64)
+    kv[1, 0] = kv[1, 0, :, :1]                                  # one K row, sixteen times
+    if keys is None:
+        kv[0, 0, :, 0, 7] = 0x4180                              # token 0: K_7 = 16
+    else:
+        keys(kv[:, 0])
+    if positive:
+        kv[:, 1] = kv[:, 1] & 0x7FFF                            # V > 0
+    q = draw("q", 32 * 64).reshape(1, 32, 64)
+    q[..., 7] = (q[..., 7] & 0x7F) | 0x3F80                     # q_7 in [1, 2)
+    pool = pkv.KVPool(ids, device=U.dev())
+    pool.buffer.copy_(U.to_dev(kv).view(-1))
+    bt = torch.ones(1, pages, dtype=torch.int32, device=U.dev())
+    bt[:, :len(order)] = torch.tensor(order, dtype=torch.int32, device=U.dev())
+    out = torch.full((1, 32, 64), float("nan"), device=U.dev(), dtype=torch.bfloat16 if bf16 else torch.float32)
+    status = torch.zeros(1, dtype=torch.int32, device=U.dev())
+    args = (pool, out, U.to_dev(q), torch.tensor([0, 1], dtype=torch.int32, device=U.dev()), bt, pages,
+            torch.tensor([ctx], dtype=torch.int32, device=U.dev()), 1, ctx, 0.125, ctx, 0, status)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ends[0].record()
+    pkv.paged_window_prefill_attention(*args)
+    ends[1].record()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    if seconds is not None:
+        seconds.append(ends[0].elapsed_time(ends[1]) * 1e-3)
+    K, V = (rng.bf16_bits_to_f64(kv[:, i]).transpose(1, 0, 2, 3).reshape(8, ids * 16, 64) for i in (0, 1))
+    times = np.array([order.count(i) for i in range(ids)], float)
+    times[1] += pages - len(order)
+    times = np.repeat(times, 16)
+    x = np.einsum("sghd,gtd->sght", rng.bf16_bits_to_f64(q).reshape(1, 8, 4, 64), K) * 0.125
+    w = np.exp(x - x[..., times > 0].max(-1, keepdims=True)) * times
+    w /= w.sum(-1, keepdims=True)
+    ref, size = (np.einsum("sght,gtd->sghd", w, v).reshape(1, 32, 64) for v in (V, np.abs(V)))
+    return out.double().cpu().numpy(), ref, size
+
+
+def _within(got, ref, size, lim):
+    worst = float((np.abs(got - ref) / size).max())
+    assert (np.abs(got - ref) <= size * lim).all(), (worst, lim)
+
+
+def test_fp32_output_of_28000_equal_weights(pkv):
+    got, ref, size = repeated_pages(pkv, 1750, False, 121)
+    # relative to the weighted |V|: the one weight's split into two bf16 terms 2^-18; 8 blocks of 16 truncating MMAs a run,
+    # 64 * 2^-24 of it in the mean of the growing sum; score and exponential 2^-19 + 2^-22; the row sum 8 + 16 + 14 half steps of
+    # 2^-24 (32 keys, run, 28 runs), the same 14 for O
+    lim = 2.0 ** -18 + 64 * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22 + (38 + 14) * 2.0 ** -24
+    _within(got, ref, size, lim)
+
+
+def test_bf16_output_of_a_window_of_millions_of_equal_weights(pkv):
+    got, ref, size = repeated_pages(pkv, 1 << 20, True, 122, positive=True)
+    # the one weight as a single bf16 term 2^-8 and the output 2^-8; 128 blocks of 8 truncating MMAs a run (1024 2^-24), 1024
+    # runs of O and 16384 of the row sum added up (512 and 8192 times 2^-24), a run's row sum (8 + 16) 2^-24, score, exponential
+    lim = 2 * 2.0 ** -8 + (1024 + 512 + 8192 + 24) * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22
+    _within(got, ref, size, lim)
+
+
+@pytest.mark.parametrize("contexts,nodes", [([16384, 16385, 16500], [3, 40, 1]), ([33000], [70])])
+def test_bf16_output_of_windows_of_several_runs(pkv, contexts, nodes):
+    c = B.Cache(contexts, nodes, seed=73)
+    want, _, size, spread = c.prefill(1 << 30, 0)
+    got = _prefill(pkv, c, c.pool.data, 1 << 30, 0, True, c.scale).double().cpu().numpy()
+    S.assert_within(got, want, S.bound(want, size, spread, c.scale, max(contexts), True), "window prefill")
+    tree_limits.assert_precise(got, want, c.starts, True)
