@@ -155,3 +155,18 @@ def test_bf16_output_of_windows_of_several_runs(pkv, contexts, nodes):
     got = _prefill(pkv, c, c.pool.data, 1 << 30, 0, True, c.scale).double().cpu().numpy()
     S.assert_within(got, want, S.bound(want, size, spread, c.scale, max(contexts), True), "window prefill")
     tree_limits.assert_precise(got, want, c.starts, True)
+
+
+def _grown(K):
+    # the first 64 keys score about 0, a later one about 200 and the repeated ones a little less: out of the fast path's range
+    K[1, :, :, 7] = 0x447A                                      # 1000
+    K[2, :, 5, 7] = 0x447C                                      # 1008
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_sums_of_rows_that_are_computed_again(pkv, bf16):
+    got, ref, size = repeated_pages(pkv, 1750, bf16, 123, order=(0, 0, 0, 0, 2), keys=_grown)
+    # 110 stretches of 256 equal weights: (256 + 110) / 2 * 2^-24 in O and in the row sum; the exponential and the division 2^-22;
+    # the scores (exponents of up to 2^9.5: 6 roundings of 2^-24) move weight between the one key, 0.2 % at the most, and the others
+    lim = (256 + 110) * 2.0 ** -24 + 2.0 ** -22 + 0.002 * 6 * 2.0 ** (9.5 - 24) + (2.0 ** -8 if bf16 else 0)
+    _within(got, ref, size, lim)
