@@ -290,8 +290,9 @@ __device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t
   return t.x + t.y;
 }
 
-// 16 values of an output row from element `at` on; kWide: 32 bytes at once where the row allows it.
-template <bool kBf16Out, bool kWide>
+// 16 values of an output row from element `at` on, 16 bytes at a time.  (A store of 32 bytes, st.global.v8.f32, wrote only the
+// first of its eight floats where rows are computed again, every time, whatever the row.)
+template <bool kBf16Out>
 __device__ __forceinline__ void store_row(void *out, long long at, const float (&v)[16]) {
   if (kBf16Out) {
     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
@@ -300,18 +301,9 @@ __device__ __forceinline__ void store_row(void *out, long long at, const float (
       dst[c / 8] = make_uint4(pack_bf16x2(v[c], v[c + 1]), pack_bf16x2(v[c + 2], v[c + 3]),
                               pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));
   } else {
-    float *dst = static_cast<float *>(out) + at;
-    if (kWide && (reinterpret_cast<uintptr_t>(out) & 31u) == 0) {
+    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
 #pragma unroll
-      for (int c = 0; c < 16; c += 8) {
-        const float x[8] = {v[c], v[c + 1], v[c + 2], v[c + 3], v[c + 4], v[c + 5], v[c + 6], v[c + 7]};
-        st_global_v8(dst + c, x);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 16; c += 4)
-        *reinterpret_cast<float4 *>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-    }
+    for (int c = 0; c < 16; c += 4) dst[c / 4] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
   }
 }
 
@@ -407,9 +399,7 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t,
       o[part][4 * c + 2] = x.z * inv;
       o[part][4 * c + 3] = x.w * inv;
     }
-    // (not 32 bytes at once: in one build only the first of the row's eight such stores arrived, though those of the fast
-    // path did)
-    store_row<kBf16Out, false>(a.out, row + 16 * part, o[part]);
+    store_row<kBf16Out>(a.out, row + 16 * part, o[part]);
   }
 }
 
@@ -835,7 +825,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
               *mine_at(part, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         } else if (d_row) {
-          store_row<kBf16Out, true>(a.out, d_at + part, v);
+          store_row<kBf16Out>(a.out, d_at + part, v);
         }
       }
       if (boxed) {
