@@ -564,6 +564,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     __syncwarp();
   } else if (warp >= kWpIssuers) {
     // ================= issuers: the MMAs of a tile each (one thread issues, the warp waits) =================
+    griddep_wait();  // (nothing to do before the loader; their waits are not to run out on the kernel before)
     const int tile = warp - kWpIssuers, part = kPair ? 0 : tile;  // the tile's share of the item's tokens
     const uint32_t sa = tmem + kColS + tile * kWpKeys, oa = tmem + kColO + tile * kHeadDim,
                    qa = tmem + kColQ + tile * (kHeadDim / 2);

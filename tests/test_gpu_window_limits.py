@@ -170,3 +170,84 @@ def test_sums_of_rows_that_are_computed_again(pkv, bf16):
     # the scores (exponents of up to 2^9.5: 6 roundings of 2^-24) move weight between the one key, 0.2 % at the most, and the others
     lim = (256 + 110) * 2.0 ** -24 + 2.0 ** -22 + 0.002 * 6 * 2.0 ** (9.5 - 24) + (2.0 ** -8 if bf16 else 0)
     _within(got, ref, size, lim)
+
+
+@pytest.fixture(scope="module")
+def slow(pkv):
+    """A call that takes longer than a wait inside a kernel may (2 s): one query over keys that make its rows be computed
+    again, every key some 0.5 us at the least.  Gives a function that launches it and one that says how long it took."""
+    kv = rng.normal_bf16(rng.stream_key(124, "kv"), 0, 3 * 2 * 8 * 16 * 64).reshape(3, 2, 8, 16, 64)
+    kv[1, 0] = kv[1, 0, :, :1]
+    _grown(kv[:, 0])
+    q = rng.normal_bf16(rng.stream_key(124, "q"), 0, 32 * 64).reshape(1, 32, 64)
+    q[..., 7] = (q[..., 7] & 0x7F) | 0x3F80
+    pool, q = pkv.KVPool(3, device=U.dev()), U.to_dev(q)
+    pool.buffer.copy_(U.to_dev(kv).view(-1))
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    status, out = torch.zeros(1, dtype=torch.int32, device=U.dev()), torch.empty(1, 32, 64, device=U.dev())
+    starts = torch.tensor([0, 1], dtype=torch.int32, device=U.dev())
+
+    def prepare(pages):
+        bt = torch.ones(1, pages, dtype=torch.int32, device=U.dev())
+        bt[0, :5] = torch.tensor([0, 0, 0, 0, 2])
+        lens = torch.tensor([16 * pages], dtype=torch.int32, device=U.dev())
+
+        def launch():
+            ends[0].record()
+            pkv.paged_window_prefill_attention(pool, out, q, starts, bt, pages, lens, 1, 16 * pages, 0.125, 16 * pages, 0, status)
+        return launch
+
+    def took():
+        ends[1].record()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return ends[0].elapsed_time(ends[1]) * 1e-3
+
+    for _ in range(2):
+        prepare(4000)()
+        seconds = took()
+    pages = int(4000 * 2.8 / seconds)
+    assert pages < 400_000, seconds
+    return prepare(pages), took
+
+
+def _follower(pkv, name):
+    """(call(overlap), its output)"""
+    c = B.Cache([300, 130, 77], [100, 130, 5] if "prefill" in name else None, seed=74)
+    pool = pkv.KVPool(c.pool.num_pages, device=U.dev())
+    pool.buffer.copy_(U.to_dev(c.pool.data).view(-1))
+    q, bt, lens, starts = U.to_dev(c.q), U.to_dev(c.bt), U.to_dev(c.lens), U.to_dev(c.starts)
+    out = torch.full((c.rows, 32, 64), float("nan"), device=U.dev())
+    status = torch.zeros(1, dtype=torch.int32, device=U.dev())
+    sums = torch.zeros(3, 8, c.max_context, device=U.dev())
+
+    def call(overlap):
+        if name == "window prefill":
+            pkv.paged_window_prefill_attention(pool, out, q, starts, bt, bt.shape[1], lens, c.max_query, c.max_context, c.scale, 90,
+                                               4, status, overlap_previous=overlap)
+        elif name == "prefill":
+            pkv.paged_prefill_attention(pool, out, q, starts, bt, bt.shape[1], lens, c.max_query, c.max_context, c.scale, status,
+                                        overlap_previous=overlap)
+        elif name == "window decode":
+            pkv.paged_window_decode_attention(pool, out, q, bt, bt.shape[1], lens, c.max_context, c.scale, 90, 4, status,
+                                              overlap_previous=overlap)
+        else:
+            pkv.paged_decode_attention_weights(pool, out, q, bt, bt.shape[1], lens, c.max_context, c.scale, sums, 0.0, None,
+                                               status, overlap_previous=overlap)
+    return call, out, status
+
+
+@pytest.mark.parametrize("name", ["window prefill", "window decode", "weights"])
+def test_waits_do_not_run_out_on_the_kernel_before(pkv, slow, name):
+    """A call launched before a kernel of more than 2 s has ended."""
+    launch, took = slow
+    call, out, status = _follower(pkv, name)
+    call(False)
+    torch.cuda.synchronize()
+    want = out.clone()
+    out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    launch()
+    call(True)
+    assert took() > 2.4
+    assert int(status.item()) == 0 and torch.equal(out, want)
