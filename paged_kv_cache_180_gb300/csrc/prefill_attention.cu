@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kPfThreads, kPfCtasPerSm) paged_prefill_kernel
     __syncwarp();
   } else if (warp == 5) {
     // ================= MMA issuer (one thread issues, the warp waits) =================
+    griddep_wait();  // (nothing to do before the loader; its waits are not to run out on the kernel before)
     long long gb = 0;          // blocks whose S was issued
     long long pend = -1;       // block whose P V is still to issue
     bool pend_first = false;   // ... and whether it starts its tile (O is overwritten, not accumulated)

@@ -237,7 +237,7 @@ def _follower(pkv, name):
     return call, out, status
 
 
-@pytest.mark.parametrize("name", ["window prefill", "window decode", "weights"])
+@pytest.mark.parametrize("name", ["window prefill", "window decode", "weights", "prefill"])
 def test_waits_do_not_run_out_on_the_kernel_before(pkv, slow, name):
     """A call launched before a kernel of more than 2 s has ended."""
     launch, took = slow
