@@ -854,14 +854,13 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       if (t.invalid) {
         // invalid sequence: zero this item's rows (its tokens, the query heads of its K/V heads)
         if (t.t0 == 0 && t.g == 0 && tid == 0) report(a.status, PKV_DEV_BAD_CONTEXT);
-        // (the last item of more query tokens than max_query takes all that are left)
-        const long long left = t.n - t.t0;
+        // (the last item of more query tokens than max_query takes all that are left, as far as there are rows)
+        const long long left = t.n - t.t0, at0 = (long long)t.q0 + t.t0;
         const long long toks = t.t0 + a.item_tok >= a.max_query ? left : min((long long)a.item_tok, left);
+        const long long row0 = max(at0, 0ll), row1 = min(at0 + toks, (long long)a.num_q_rows);
         constexpr int kWidth = (kGroup * kHeadDim) << kShift;
-        for (long long i = tid; i < toks * kWidth; i += kWpTiles * kWpRows) {
-          const long long row = (long long)t.q0 + t.t0 + i / kWidth;
-          const long long at = (row * kQHeads + t.g * kGroup) * kHeadDim + i % kWidth;
-          if (row < 0 || row >= a.num_q_rows) continue;
+        for (long long i = tid; i < (row1 - row0) * kWidth; i += kWpTiles * kWpRows) {
+          const long long at = ((row0 + i / kWidth) * kQHeads + t.g * kGroup) * kHeadDim + i % kWidth;
           if (kBf16Out)
             static_cast<uint16_t *>(a.out)[at] = 0;
           else

@@ -251,3 +251,28 @@ def test_waits_do_not_run_out_on_the_kernel_before(pkv, slow, name):
     call(True)
     assert took() > 2.4
     assert int(status.item()) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("seqs", [1, 30])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("first,behind,zeros", [(0, (1 << 31) - 1, (0, 40)), (7, (1 << 31) - 1, (7, 40)),
+                                                (-(1 << 31) + 9, 5, (0, 5)), (-20, 3, (0, 3)), (40, (1 << 31) - 1, (40, 40))])
+def test_query_starts_far_outside_the_rows(pkv, seqs, bf16, first, behind, zeros):
+    """A sequence of two thousand million query tokens gets zero rows where there are rows, and takes no longer than that."""
+    pool = pkv.KVPool(4, device=U.dev())
+    pool.buffer.zero_()
+    starts = np.full(seqs + 1, behind, np.int32)
+    starts[0] = first
+    out = torch.ones(40, 32, 64, device=U.dev(), dtype=torch.bfloat16 if bf16 else torch.float32)
+    q = torch.zeros(40, 32, 64, dtype=torch.bfloat16, device=U.dev())
+    status = torch.zeros(1, dtype=torch.int32, device=U.dev())
+    bt, lens = torch.zeros(seqs, 4, dtype=torch.int32, device=U.dev()), torch.full((seqs,), 64, dtype=torch.int32, device=U.dev())
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for e in ends:
+        pkv.paged_window_prefill_attention(pool, out, q, U.to_dev(starts), bt, 4, lens, 20, 64, 0.125, 8, 0, status)
+        e.record()
+    torch.cuda.synchronize()
+    want = torch.ones(40, dtype=torch.bool, device=U.dev())
+    want[zeros[0]:zeros[1]] = False
+    assert int(status.item()) == 2 and torch.equal((out == 1).all(-1).all(-1), want) and (out[~want] == 0).all()
+    assert ends[0].elapsed_time(ends[1]) < 50
