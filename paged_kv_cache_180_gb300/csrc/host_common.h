@@ -9,6 +9,9 @@
 
 namespace pkv {
 
+// Cached tokens of a sequence at the most.
+constexpr int kMaxTokens = 0x7fffffff - 63;  // 2^31 - 64
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The one geometry this build compiles.

@@ -566,7 +566,7 @@ int check_unit_call(const pkv_pool *pool, const void *out, const void *q, int nu
   const int rc = check_pool(pool);
   if (rc != PKV_OK) return rc;
   if (num_q_heads != kQHeads) return PKV_ERR_UNSUPPORTED;
-  if (num_seqs < 0 || num_seqs > (1 << 24) || max_context < 0 || max_context > 0x7fffffff - 64 || bt_stride < 0)
+  if (num_seqs < 0 || num_seqs > (1 << 24) || max_context < 0 || max_context > kMaxTokens || bt_stride < 0)
     return PKV_ERR_SHAPE;
   if (num_seqs == 0) return PKV_OK;
   if (out == nullptr || q == nullptr || block_tables == nullptr || context_lens == nullptr) return PKV_ERR_NULL;

@@ -239,8 +239,8 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
 // past lo, or before `sinks` (where pages are left out, the sinks lie before them and the window behind).  Bits 0, 1 of `bad`:
 // the keys' first, second page is invalid.
 __device__ __forceinline__ uint32_t seen_keys(int key, int gone, int lo, int pos, int sinks, int bad) {
-  const int at = key + gone * kPageTokens;
-  uint32_t seen = first_bits(pos + 1 - at) & (~first_bits(lo - at) | first_bits(sinks - key));
+  const int d = gone * kPageTokens;  // (at most lo where pages are left out; key + d may pass 2^31)
+  uint32_t seen = first_bits(pos + 1 - d - key) & (~first_bits(lo - d - key) | first_bits(sinks - key));
   if (bad & 1) seen &= 0xffff0000u;
   if (bad & 2) seen &= 0x0000ffffu;
   return seen;
@@ -1096,7 +1096,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   if (rc != PKV_OK) return rc;
   if (num_q_heads != pkv::kQHeads) return PKV_ERR_UNSUPPORTED;
   if (num_seqs < 0 || num_seqs > (1 << 24) || max_query < 0 || max_query > (1 << 20) || max_context < 0 ||
-      max_context > 0x7fffffff - 64 || block_table_stride < 0 || num_q_rows < 0 || window < 1 || sinks < 0)
+      max_context > pkv::kMaxTokens || block_table_stride < 0 || num_q_rows < 0 || window < 1 || sinks < 0)
     return PKV_ERR_SHAPE;
   if (num_seqs == 0 || max_query == 0 || num_q_rows == 0) return PKV_OK;
   if (out == nullptr || q == nullptr || query_start == nullptr || block_tables == nullptr || context_lens == nullptr)

@@ -276,3 +276,29 @@ def test_query_starts_far_outside_the_rows(pkv, seqs, bf16, first, behind, zeros
     want[zeros[0]:zeros[1]] = False
     assert int(status.item()) == 2 and torch.equal((out == 1).all(-1).all(-1), want) and (out[~want] == 0).all()
     assert ends[0].elapsed_time(ends[1]) < 50
+
+
+def test_the_longest_context(pkv):
+    """2^31 - 64 tokens of which the window and the sinks are there: the same bits as from a short context that ends alike."""
+    ctx, n, window, sinks = (1 << 31) - 64, 70, 300, 4
+    c = B.Cache([640], [n], seed=75)
+    pool = pkv.KVPool(c.pool.num_pages, device=U.dev())
+    pool.buffer.copy_(U.to_dev(c.pool.data).view(-1))
+    short = U.to_dev(c.hide(window, sinks))
+    blocks = ctx // 16
+    far = torch.full((1, blocks), -1, dtype=torch.int32, device=U.dev())
+    far[0, 0], far[0, blocks - 30:] = short[0, 0], short[0, 10:40]
+    q, starts = U.to_dev(c.q), U.to_dev(c.starts)
+    status = torch.zeros(1, dtype=torch.int32, device=U.dev())
+    for dtype in (torch.float32, torch.bfloat16):
+        got = []
+        for bt, length in ((short, 640), (far, ctx)):
+            lens = torch.tensor([length], dtype=torch.int32, device=U.dev())
+            prefill, decode = (torch.full((k, 32, 64), float("nan"), dtype=dtype, device=U.dev()) for k in (n, 1))
+            pkv.paged_window_prefill_attention(pool, prefill, q, starts, bt, bt.shape[1], lens, n, length, c.scale, window, sinks,
+                                               status)
+            pkv.paged_window_decode_attention(pool, decode, q[n - 1:], bt, bt.shape[1], lens, length, c.scale, window, sinks, status)
+            got += [prefill, decode]
+        assert torch.isfinite(got[0]).all() and torch.equal(got[0], got[2]) and torch.isfinite(got[1]).all()
+        assert torch.allclose(got[1], got[3], rtol=2.0 ** -7 if dtype == torch.bfloat16 else 1e-5, atol=1e-6)
+    assert int(status.item()) == 0
