@@ -302,3 +302,25 @@ def test_the_longest_context(pkv):
         assert torch.isfinite(got[0]).all() and torch.equal(got[0], got[2]) and torch.isfinite(got[1]).all()
         assert torch.allclose(got[1], got[3], rtol=2.0 ** -7 if dtype == torch.bfloat16 else 1e-5, atol=1e-6)
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("window,sinks", [((1 << 31) - 1, 0), ((1 << 31) - 1, (1 << 31) - 1), (1, (1 << 31) - 1), ((1 << 31) - 2, 3)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_the_largest_windows_and_sinks(pkv, window, sinks, bf16):
+    c = B.Cache([0, 1, 2, 15, 16, 17, 33, 64, 65, 100, 600, 1500], seed=76)
+    want, _, size, spread, weights = c.decode(window, sinks)
+    out = torch.full((12, 32, 64), float("nan"), device=U.dev(), dtype=torch.bfloat16 if bf16 else torch.float32)
+    status = torch.zeros(1, dtype=torch.int32, device=U.dev())
+    pool = pkv.KVPool(c.pool.num_pages, device=U.dev())
+    pool.buffer.copy_(U.to_dev(c.pool.data).view(-1))
+    pkv.paged_window_decode_attention(pool, out, U.to_dev(c.q), U.to_dev(c.bt), c.bt.shape[1], U.to_dev(c.lens), c.max_context,
+                                      c.scale, window, sinks, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    lim = B.decode_bound(want, size, spread, c.scale, max(t.size for t, _ in weights.values()), bf16)
+    S.assert_within(out.double().cpu().numpy(), want, lim, "window decode")
+    for shape in SHAPES.values():
+        c = B.Cache(*shape, seed=77)
+        want, _, size, spread = c.prefill(window, sinks)
+        got = _prefill(pkv, c, c.pool.data, window, sinks, bf16, c.scale).double().cpu().numpy()
+        S.assert_within(got, want, S.bound(want, size, spread, c.scale, 300, bf16), "window prefill")
