@@ -307,12 +307,6 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
   }
 
   // ---- kept positions, ascending ----
-  auto classify = [&](int t, float v, bool &sure, bool &equal) {
-    const bool in = t < p1, fixed = unsigned(t - head) >= unsigned(tail - head);
-    const unsigned key = sum_key(v);
-    sure = in && (fixed || key > T);
-    equal = in && !fixed && key == T;
-  };
   // every warp looks at an equal run of the CTA's tokens, twice: to count, and to write
   const int run = ((p1 - p0 + kWarps - 1) / kWarps + kRun - 1) / kRun * kRun;
   const int w0 = p0 + warp * run, w1 = min(p1, w0 + run);

@@ -469,10 +469,10 @@ int unit_cluster(long long units, long long pages, int most) {
 }
 
 // Common part of the two entry points; `sums` null: window decode.
-int unit_decode(const pkv_pool *pool, void *out, const void *q, int num_q_heads, const int32_t *block_tables,
-                int64_t bt_stride, const int32_t *context_lens, int num_seqs, int max_context, float scale, int window,
-                int sinks, float *sums, int64_t seq_stride, int64_t head_stride, float decay, void *workspace,
-                size_t workspace_bytes, int32_t *device_status, unsigned flags, void *stream) {
+int unit_decode(const pkv_pool *pool, void *out, const void *q, const int32_t *block_tables, int64_t bt_stride,
+                const int32_t *context_lens, int num_seqs, int max_context, float scale, int window, int sinks, float *sums,
+                int64_t seq_stride, int64_t head_stride, float decay, void *workspace, int32_t *device_status,
+                unsigned flags, void *stream) {
   UnitArgs a;
   int rc = pool_tensor_maps(pool, kPageTokens, &a.tmap_k, &a.tmap_v);
   if (rc != PKV_OK) return rc;
@@ -590,9 +590,8 @@ extern "C" int pkv_paged_window_decode_attention(const pkv_pool *pool, void *out
   if (rc != PKV_OK) return rc;
   if (window < 1 || sinks < 0) return PKV_ERR_SHAPE;
   if (num_seqs == 0) return PKV_OK;
-  return pkv::unit_decode(pool, out, q, num_q_heads, block_tables, block_table_stride, context_lens, num_seqs,
-                          max_context, scale, window, sinks, nullptr, 0, 0, 0.f, nullptr, 0, device_status, flags,
-                          stream);
+  return pkv::unit_decode(pool, out, q, block_tables, block_table_stride, context_lens, num_seqs, max_context, scale,
+                          window, sinks, nullptr, 0, 0, 0.f, nullptr, device_status, flags, stream);
 }
 
 extern "C" size_t pkv_weights_workspace_bytes(int num_seqs, int max_context) {
@@ -626,7 +625,7 @@ extern "C" int pkv_paged_decode_attention_weights(const pkv_pool *pool, void *ou
   if (need > 0 && workspace == nullptr) return PKV_ERR_NULL;
   if (need > 0 && !pkv::aligned16(workspace)) return PKV_ERR_ALIGN;
   if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
-  return pkv::unit_decode(pool, out, q, num_q_heads, block_tables, block_table_stride, context_lens, num_seqs,
-                          max_context, scale, 0x7fffffff, 0, weight_sums, seq_stride, head_stride, decay, workspace,
-                          workspace_bytes, device_status, flags, stream);
+  return pkv::unit_decode(pool, out, q, block_tables, block_table_stride, context_lens, num_seqs, max_context, scale,
+                          0x7fffffff, 0, weight_sums, seq_stride, head_stride, decay, workspace, device_status, flags,
+                          stream);
 }

@@ -87,8 +87,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int 
                : "memory");
 }
 
-#define WP_R8(c, i) c(v[i]), c(v[i + 1]), c(v[i + 2]), c(v[i + 3]), c(v[i + 4]), c(v[i + 5]), c(v[i + 6]), c(v[i + 7])
-
 struct WindowArgs {
   CUtensorMap tmap_k;  // boxes of one head's 16 rows of one page
   CUtensorMap tmap_v;
@@ -186,30 +184,8 @@ __device__ __forceinline__ WpTile tile_of(const WindowArgs &a, const WpItem &t, 
   return w;
 }
 
-// 32 TMEM columns, not waited for: v may be used after tmem_ld32_wait(v).
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : WP_R8("=r", 0), WP_R8("=r", 8), WP_R8("=r", 16), WP_R8("=r", 24)
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : WP_R8("+r", 0), WP_R8("+r", 8), WP_R8("+r", 16), WP_R8("+r", 24)
-               :
-               : "memory");
-}
-
-// 32 TMEM columns stored; complete after tmem_st_wait().
-__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      WP_R8("r", 0), WP_R8("r", 8), WP_R8("r", 16), WP_R8("r", 24)
-      : "memory");
-}
+// P of a quarter of a block, stored in TMEM; complete after tmem_st_wait().
+__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[32]) { tmem_st32_async(taddr, v); }
 __device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st16_async(taddr, v); }
 
 // Bounded wait of a whole warp that gives up once another role has; one answer for all lanes.  Returns true when the
@@ -947,11 +923,11 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
             // every quarter is on its way while the one before it is worked on
             uint32_t p16[kBf16Out ? 16 : 32];
             if (!loaded) tmem_ld32_async(s_addr, x0);
-            tmem_ld32_wait(x0);
+            tmem_ld_wait(x0);
             tmem_ld32_async(s_addr + 32, x1);
             run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
             store_p(s_addr, p16);
-            tmem_ld32_wait(x1);
+            tmem_ld_wait(x1);
             ok = wp_wait(sm, &sm.s_full[tile][1], blocks & 1, a.status);
             if (!ok) break;
             tc_fence_after();
@@ -964,11 +940,11 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
               if (!ok) break;
             }
             written(0);
-            tmem_ld32_wait(x0);
+            tmem_ld_wait(x0);
             tmem_ld32_async(s_addr + 96, x1);
             run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
             store_p(s_addr + 64, p16);
-            tmem_ld32_wait(x1);
+            tmem_ld_wait(x1);
             loaded = j + 1 < inner1 &&
                      __all_sync(0xffffffffu, mbar_try_wait(&sm.s_full[tile][0], (blocks + 1) & 1));
             if (loaded) {
@@ -989,7 +965,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
           if (!ok) break;
           if (!plain) continue;  // with a mask
         } else {
-          if (loaded) tmem_ld32_wait(x0);  // (asked for before the block's bad pages were known)
+          if (loaded) tmem_ld_wait(x0);  // (asked for before the block's bad pages were known)
           loaded = false;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
