@@ -479,8 +479,9 @@ int pkv_paged_window_decode_attention(const pkv_pool *pool, void *out, const voi
  * and flags as above (with PKV_OVERLAP_PREVIOUS query_start is read at once, too).
  * A sequence whose lengths do not fit (n_s < 0, > max_query or > context_lens[s], a context < 0 or > max_context, query
  * rows past num_q_rows) gets zero rows and PKV_DEV_BAD_CONTEXT; a bad page id inside a row's A_i sets PKV_DEV_BAD_PAGE and
- * that page is left out.  A NaN or infinity in K or V reaches only the rows that see its token: rows whose output would not be
- * finite are computed again from the keys that they see (microseconds for each key).  No workspace, one kernel launch.
+ * that page is left out.  Finite values at tokens that no query sees change no bit of the output.  A NaN or infinity in K or V
+ * reaches only the rows that see its token: rows whose output would not be finite are computed again from the keys that they
+ * see (microseconds for each key).  No workspace, one kernel launch.
  */
 int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *out, const void *q, int num_q_heads, int num_q_rows,
                                        const int32_t *query_start, const int32_t *block_tables,
@@ -504,6 +505,9 @@ int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *out, const vo
  *                  kernel before it has completed).  max_context at most 2^30.
  * A token of a page that is left out (PKV_DEV_BAD_PAGE) has weight 0.  A sequence of invalid context gets zero rows and keeps its
  * sums.  Strides at most 2^38 elements.  Results do not depend on timing.  One kernel launch.
+ * max_context also says how a sequence is split: bounds far above the lengths cost time.  64 sequences of 2048 tokens take 48
+ * us with a bound of 2048, 61 with 4096, 104 with 16384, 230 with 38400, 195 with 38401 to 57344 and 110 above; one such
+ * sequence 6 us with any.
  */
 int pkv_paged_decode_attention_weights(const pkv_pool *pool, void *out, const void *q, int num_q_heads,
                                        const int32_t *block_tables, int64_t block_table_stride,

@@ -33,15 +33,15 @@
 //  * Every mbarrier wait is bounded (about 2 s): on expiry the CTA reports PKV_DEV_TIMEOUT, stops issuing work, waits
 //    (bounded) for what is in flight, frees its tensor memory and exits.
 //
-// What bounds it: 4 x 2048 queries, windows of 2000, bf16 output, take 140 us (135 GFLOP, 965 TFLOP/s, half of the measured
-// bf16 peak): tensor pipe 42 %, exponentials 40 %, issue slots 46 %, so nothing is full; two softmax warps a scheduler wait
+// What bounds it: 4 x 2048 queries, windows of 2000, bf16 output, take 143 us (135 GFLOP, 946 TFLOP/s, half of the measured
+// bf16 peak): tensor pipe 42 %, exponentials 39 %, issue slots 45 %, so nothing is full; two softmax warps a scheduler wait
 // for S, exponentials and stores in turn, and registers (168 a thread) and tensor memory (all 512 columns are taken) leave
 // no room for a third.  Built and slower: two CTAs to an SM with one S buffer a tile (151 to 161 us), one issuing warp for
 // both tiles (62 cycles a product), softmax warps that issue for themselves (166).  With fp32 output the second terms take
-// 2.5 times the instructions a weight: 2048 queries, windows of 4096, 146 us for 76.  Short windows: 16 x 512 queries,
-// windows of 128, fp32 in 41 us, 12900 cycles an item of two blocks, of them 2000 waiting for its S, 1800 taking out the O
-// before it, the rest four masked halves.  200 queries of one sequence: 10.3 us, the latencies of one item (lists and
-// set-up 2, first K/V 2, blocks and output the rest).
+// 2.5 times the instructions a weight: 2048 queries, windows of 4096, 121 us for 77 (148 while the sums of runs went through
+// global memory).  Short windows: 16 x 300..512 queries, windows of 128, fp32 in 42 us, some 13000 cycles an item of two
+// blocks, of them 2000 waiting for its S, 1800 taking out the O before it, the rest four masked halves.  200 queries of one
+// sequence: 10.5 us, the latencies of one item (lists and set-up 2, first K/V 2, blocks and output the rest).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1086,7 +1086,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   // 12.2 in items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 52 us and 41.
   const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
   // No more than 32 queries a sequence fill one tile: two heads then share the CTA, 256 x 4 queries, windows of 512, fp32
-  // in 87 us (123 with the second tile idle), 64 x 16 in 31 (41), 3000 x 10 of 100 in 353 (538), 40 x 32 of 200 in 14.3
+  // in 88 us (123 with the second tile idle), 64 x 16 in 31 (41), 3000 x 10 of 100 in 353 (538), 40 x 32 of 200 in 14.3
   // (13.9).  While every (sequence, head) finds an SM of its own it has that one.
   const bool pair = max_query <= pkv::kWpTok && (long long)num_seqs * pkv::kKvHeads > sms;
   const int item_tok = pair || (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
