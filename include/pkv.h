@@ -475,7 +475,7 @@ int pkv_paged_window_decode_attention(const pkv_pool *pool, void *out, const voi
  *   A_i = { t <= p_i : t < sinks or t > p_i - window },  p_i = context_lens[s] - n_s + (i - query_start[s]).
  *
  * Arguments as for pkv_paged_prefill_attention, except: out is float32, or bf16 with PKV_OUT_BF16 (the weights then carry
- * bf16's 8 significant bits into the product with V; with float32 16); max_query at most 2^20; window, sinks, scale
+ * bf16's 8 significant bits into the product with V; with float32 24); max_query at most 2^20; window, sinks, scale
  * and flags as above (with PKV_OVERLAP_PREVIOUS query_start is read at once, too).
  * A sequence whose lengths do not fit (n_s < 0, > max_query or > context_lens[s], a context < 0 or > max_context, query
  * rows past num_q_rows) gets zero rows and PKV_DEV_BAD_CONTEXT; a bad page id inside a row's A_i sets PKV_DEV_BAD_PAGE and

@@ -13,15 +13,20 @@
 //    more sequences than fill the SMs, an item is one tile's tokens against two K/V heads, a tile each.
 //  * The grid is persistent, one CTA to an SM; the items that there are (a prefix sum over the sequences' lengths, made by
 //    every CTA) are dealt in a snake, each sequence's latest first.
-//  * Q_t stays in tensor memory (its rows' own threads put it there).  A block's S_t = Q_t K^T is computed in two halves of
-//    64 keys, into TMEM buffers of their own; P goes back over its half and is the TMEM A operand of O_t += P V.  So while
-//    the softmax works on one half the tensor core has P V of the other and its next S, and shared memory feeds it K and V
-//    alone.  With fp32 output P has two bf16 terms (16 bits), with bf16 output one.  Row sums are added up in registers.
+//  * A block's S_t = Q_t K^T is computed in two halves of 64 keys, into TMEM buffers of their own; P goes back over its half
+//    and is the TMEM A operand of O_t += P V.  So while the softmax works on one half the tensor core has P V of the other and
+//    its next S.  With bf16 output P has one bf16 term, and Q stays in tensor memory (its rows' own threads put it there), so
+//    that shared memory feeds the tensor core K and V alone.  With fp32 output P has three bf16 terms, 24 bits (with two,
+//    the weights' rounding alone is 1.7e-6 of the output's norm); the third ones take Q's place and more, and Q lies in
+//    shared memory.  Row sums are added up in registers.
 //  * The exponents of a row refer to the largest score of some keys of its tile's first block, seen by the row or by another
 //    one of the item, and stay there: weights are floats, so they may well be far from 1.  A row whose sum leaves
 //    [2^-90, 2^112] is computed again.
-//  * The tensor core truncates what it adds up.  O is therefore taken out after every run of 1024 keys (fp32 output) or 16384
+//  * The tensor core truncates what it adds up.  O is therefore taken out after every run of 256 keys (fp32 output) or 16384
 //    keys (bf16 output: one run over 2^24 equal weights lost 15 %), and runs are added up, with rounding, in shared memory.
+//    fp32 output, windows of 128 / 1000 / 15000: runs of 128 keys have errors of 3.0e-7 / 5.0e-7 / 6.8e-7 of the output's norm,
+//    of 256 4.4e-7 / 8.5e-7 / 9.6e-7, of 1024 4.4e-7 / 2.9e-6 / 3.1e-6; fp32 arithmetic in torch 2.6e-7 / 6.3e-7 / 2.2e-6.
+//    128 instead of 256 keys take 6 % more time for windows of 128 and 11 % for long ones, 1024 save 6 % there.
 //  * A warp's finished rows go through the same shared memory and a TMA store: stored by their threads, 256 bytes apart, they
 //    took 3400 cycles a tile.  (The last few tokens of a sequence, where a box would reach into the next one, are stored
 //    directly.)
@@ -37,11 +42,11 @@
 // bf16 peak): tensor pipe 42 %, exponentials 39 %, issue slots 45 %, so nothing is full; two softmax warps a scheduler wait
 // for S, exponentials and stores in turn, and registers (168 a thread) and tensor memory (all 512 columns are taken) leave
 // no room for a third.  Built and slower: two CTAs to an SM with one S buffer a tile (151 to 161 us), one issuing warp for
-// both tiles (62 cycles a product), softmax warps that issue for themselves (166).  With fp32 output the second terms take
-// 2.5 times the instructions a weight: 2048 queries, windows of 4096, 121 us for 77 (148 while the sums of runs went through
-// global memory).  Short windows: 16 x 300..512 queries, windows of 128, fp32 in 42 us, some 13000 cycles an item of two
-// blocks, of them 2000 waiting for its S, 1800 taking out the O before it, the rest four masked halves.  200 queries of one
-// sequence: 10.5 us, the latencies of one item (lists and set-up 2, first K/V 2, blocks and output the rest).
+// both tiles (62 cycles a product), softmax warps that issue for themselves (166).  With fp32 output P V is
+// three times the products and a weight 2.5 times the instructions: 2048 queries, windows of 4096, 154 us for 77 (121 with two
+// terms and runs of 1024 keys).  Short windows: 16 x 300..512 queries, windows of 128, fp32 in 41 us, some 13000 cycles an item
+// of two blocks, of them 2000 waiting for its S, 1800 taking out the O before it, the rest four masked halves.  200 queries
+// of one sequence: 11.3 us, the latencies of one item (lists and set-up 2, first K/V 2, blocks and output the rest).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -64,16 +69,18 @@ constexpr unsigned kWpStages = 4;                      // K/V blocks in flight
 constexpr int kWpThreads = kWpTiles * kWpRows + 96;    // softmax groups, loader, issuers
 constexpr int kWpLoader = kWpTiles * 4, kWpIssuers = kWpLoader + 1;  // warps
 constexpr int kWpHalf = kWpKeys / 2;                   // keys of an S buffer
-constexpr int kWpMaxItems = 64;                        // items a CTA walks (its table in shared memory)
+template <bool kBf16>
+constexpr int kWpMaxItems = kBf16 ? 64 : 32;           // items a CTA walks (its table in shared memory)
 constexpr int kWpBox = kPageTokens * kRowBytes;        // one head's rows of one page: 2 KiB
 constexpr int kWpTileBytes = kWpKeys * kRowBytes;      // K (or V) of one block: 16 KiB
 template <bool kBf16>
-constexpr int kWpRun = kBf16 ? 128 : 8;                // blocks that O adds up at once
+constexpr int kWpRun = kBf16 ? 128 : 2;                // blocks that O adds up at once
 constexpr int kWpSumRun = 8;                           // blocks whose weights are added up at once
 constexpr int kWpStretch = 16;                         // pages that a row computed again adds up at once
 constexpr uint32_t kWpTmemCols = 512;
-// columns of S_0, S_1 (128 each), of O_0, O_1 (64) and of Q_0, Q_1 (32)
-constexpr uint32_t kColS = 0, kColO = kWpTiles * kWpKeys, kColQ = kColO + kWpTiles * kHeadDim;
+// columns of S_0, S_1 (128 each) and of O_0, O_1 (64); then with bf16 output of Q_0, Q_1 (32), with fp32 output of the third
+// terms of P_0, P_1 (64)
+constexpr uint32_t kColS = 0, kColO = kWpTiles * kWpKeys, kColQ = kColO + kWpTiles * kHeadDim, kColLow = kColQ;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSumMin = 8.077935669463161e-28f, kSumMax = 5.192296858534828e33f;  // 2^-90, 2^112
 
@@ -90,6 +97,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int 
 struct WindowArgs {
   CUtensorMap tmap_k;  // boxes of one head's 16 rows of one page
   CUtensorMap tmap_v;
+  CUtensorMap tmap_q;  // with fp32 output: boxes of 8 query rows x one group's 4 heads
   CUtensorMap tmap_o;  // boxes of 8 output rows x one group's 4 heads x 128 bytes
   int num_pages;
   void *out;       // [total][32][64] fp32 or bf16
@@ -122,23 +130,27 @@ struct WpItem {
   int invalid;  // invalid ones: its rows are zeroed
 };
 
+template <bool kBf16>
 struct __align__(1024) WpSmem {
   uint8_t k[kWpStages][kWpTileBytes];  // 128 keys x 128 B per stage, 128-byte swizzled
   uint8_t v[kWpStages][kWpTileBytes];
+  uint8_t q[kBf16 ? 0 : kWpTiles][kWpRows * kRowBytes];  // with fp32 output: Q, 128-byte swizzled
   uint8_t rows[kWpTiles * 4][2][32 * 128];  // a warp's rows, 128 bytes of each at a time, swizzled: sums of runs, then the output
-  uint64_t q_full[kWpTiles];  // the tile's Q is in tensor memory (a warp arrives once)
+  uint64_t q_full[kWpTiles];  // the tile's Q is there (in tensor memory: a warp arrives once)
   uint64_t kv_full[kWpStages], kv_empty[kWpStages];
   uint64_t s_full[kWpTiles][2];  // S of the half of the tile's next block is there, and its bad pages are known
   uint64_t p_full[kWpTiles][2];  // every row of P of it (a warp arrives once), and O has been read where it starts anew
   uint64_t o_full[kWpTiles];  // the P V that ends a run, or the item, is done
   uint64_t mma_done[kWpTiles];
   int kv_bad[kWpStages];  // bit pp set when page pp of the block is invalid (loaded as zeros)
-  WpItem items[kWpMaxItems];  // this CTA's, in walking order
+  WpItem items[kWpMaxItems<kBf16>];  // this CTA's, in walking order
   int warp_sum[kWpThreads / 32];
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kWpSmemBytes = sizeof(WpSmem) + 1024;
+template <bool kBf16>
+constexpr size_t kWpSmemBytes = sizeof(WpSmem<kBf16>) + 1024;
+static_assert(kWpSmemBytes<false> <= 227 * 1024 && kWpSmemBytes<true> <= 227 * 1024, "");
 
 // What an item of sequence s (query tokens t0 .. of n from row q0 on, ctx cached tokens) has to know.
 __device__ __forceinline__ WpItem wp_item(const WindowArgs &a, int s, int g, int t0, int q0, int n, int ctx) {
@@ -184,13 +196,10 @@ __device__ __forceinline__ WpTile tile_of(const WindowArgs &a, const WpItem &t, 
   return w;
 }
 
-// P of a quarter of a block, stored in TMEM; complete after tmem_st_wait().
-__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[32]) { tmem_st32_async(taddr, v); }
-__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st16_async(taddr, v); }
-
 // Bounded wait of a whole warp that gives up once another role has; one answer for all lanes.  Returns true when the
 // phase completed.
-__device__ __forceinline__ bool wp_wait(WpSmem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
+template <class Smem>
+__device__ __forceinline__ bool wp_wait(Smem &sm, uint64_t *bar, uint32_t parity, int32_t *status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const unsigned long long t0 = global_ns();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
@@ -233,37 +242,58 @@ __device__ __forceinline__ float extreme16(const uint32_t (&s)[16]) {
   return of3(of3(m[0], m[1], m[2]), of3(m[3], m[4], __uint_as_float(s[15])), m[0]);
 }
 
-// P = 2^(s c - m) for 32 keys as one or two bf16 terms, keys 2i and 2i + 1 packed in word i, the second term behind the
-// first (with kMasked, keys whose bit in `valid` is clear get 0).  Returns their sum; of two terms, the sum of what they
-// hold: a weight's rounding then cancels in the quotient as far as the weight makes up the row (errors of 1.7e-6 of the
-// output's norm for 2.2e-6, 4 % of the time).  With one term that gives 2.2e-3 for 2.3e-3 and takes 12 %.
-template <bool kMasked, bool kTwo>
-__device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t valid, float m, float c,
-                                               uint32_t (&p16)[kTwo ? 32 : 16]) {
+// P = 2^(s c - m) for 32 keys (with kMasked, keys whose bit in `valid` is clear get 0) as bf16 terms, stored in TMEM over the S
+// that they come from, two keys to a column: one term with bf16 output; with fp32 output three (24 bits), the second ones
+// behind the first, the third ones at `low`.  Complete after tmem_st_wait().  Returns the weights' sum.  (Sums of the
+// rounded weights: with one term errors of 2.2e-3 for 2.3e-3, for 12 % of the time.)
+template <bool kMasked, bool kBf16>
+__device__ __forceinline__ float quarter_probs(const uint32_t (&s)[32], uint32_t valid, float m, float c, uint32_t taddr,
+                                               uint32_t low) {
   const float2 c2 = make_float2(c, c), mc = make_float2(-m, -m);
   float2 sum[4] = {};
+  constexpr int kStep = kBf16 ? 16 : 8;  // words stored at once
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, mc);
-    float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-    if (kMasked) {
-      p.x = (valid >> (2 * i)) & 1 ? p.x : 0.f;
-      p.y = (valid >> (2 * i + 1)) & 1 ? p.y : 0.f;
-    }
-    const uint32_t hi = pack_bf16x2(p.x, p.y);
-    p16[i] = hi;
-    if constexpr (kTwo) {
-      const float2 hf = make_float2(bf16_lo(hi), bf16_hi(hi)), r = sub_f32x2(p, hf);
-      const uint32_t lo = pack_bf16x2(r.x, r.y);
-      p16[16 + i] = lo;
-      sum[i % 4] = add_f32x2(sum[i % 4], hf);
-      sum[(i + 2) % 4] = add_f32x2(sum[(i + 2) % 4], make_float2(bf16_lo(lo), bf16_hi(lo)));
-    } else {
+  for (int at = 0; at < 16; at += kStep) {
+    uint32_t t0[kStep], t1[8], t2[8];
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      const int i = at + k;
+      const float2 e = fma_f32x2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, mc);
+      float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+      if (kMasked) {
+        p.x = (valid >> (2 * i)) & 1 ? p.x : 0.f;
+        p.y = (valid >> (2 * i + 1)) & 1 ? p.y : 0.f;
+      }
       sum[i % 4] = add_f32x2(sum[i % 4], p);
+      t0[k] = pack_bf16x2(p.x, p.y);
+      if constexpr (!kBf16) {
+        p = sub_f32x2(p, make_float2(bf16_lo(t0[k]), bf16_hi(t0[k])));
+        t1[k] = pack_bf16x2(p.x, p.y);
+        p = sub_f32x2(p, make_float2(bf16_lo(t1[k]), bf16_hi(t1[k])));
+        t2[k] = pack_bf16x2(p.x, p.y);
+      }
+    }
+    if constexpr (kBf16) {
+      tmem_st16_async(taddr, t0);
+    } else {
+      tmem_st8_async(taddr + at, t0);
+      tmem_st8_async(taddr + 16 + at, t1);
+      tmem_st8_async(low + at, t2);
     }
   }
   const float2 t = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
   return t.x + t.y;
+}
+
+// The same for keys that no row sees: zeros.
+template <bool kBf16>
+__device__ __forceinline__ void no_probs(uint32_t taddr, uint32_t low) {
+  const uint32_t zero[16] = {};
+  tmem_st16_async(taddr, zero);
+  if (!kBf16) {
+    tmem_st16_async(taddr + 16, zero);
+    tmem_st16_async(low, zero);
+  }
 }
 
 // 16 values of an output row from element `at` on, 16 bytes at a time.  (A store of 32 bytes, st.global.v8.f32, wrote only the
@@ -384,16 +414,16 @@ __device__ __noinline__ void recompute_row(const WindowArgs &a, const WpItem &t,
 template <bool kBf16Out, bool kPair>
 __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __grid_constant__ WindowArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  WpSmem &sm = *reinterpret_cast<WpSmem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  WpSmem<kBf16Out> &sm = *reinterpret_cast<WpSmem<kBf16Out> *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same for all lanes, and the compiler knows it)
   // Item k of this CTA: k * G + c on even rounds and k * G + (G - 1 - c) on odd ones.
   const int G = int(gridDim.x), c = int(blockIdx.x);
   auto item_index = [&](int k) { return k * G + ((k & 1) ? G - 1 - c : c); };
   int nt = 0;  // <= kWpMaxItems
-  while (nt < kWpMaxItems && item_index(nt) < a.most_items) ++nt;
+  while (nt < kWpMaxItems<kBf16Out> && item_index(nt) < a.most_items) ++nt;
 
-  if (tid < kWpMaxItems) sm.items[tid].run = sm.items[tid].invalid = 0;
+  if (tid < kWpMaxItems<kBf16Out>) sm.items[tid].run = sm.items[tid].invalid = 0;
   if (tid == 0) {
     for (unsigned i = 0; i < kWpStages; ++i) {
       mbar_init(&sm.kv_full[i], 1);
@@ -406,7 +436,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       }
       mbar_init(&sm.mma_done[t], 1);
       mbar_init(&sm.o_full[t], 1);
-      mbar_init(&sm.q_full[t], kWpRows / 32);
+      mbar_init(&sm.q_full[t], kBf16Out ? kWpRows / 32 : 1);
     }
     sm.abort = 0;
     mbar_init_fence();
@@ -543,7 +573,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     griddep_wait();  // (nothing to do before the loader; their waits are not to run out on the kernel before)
     const int tile = warp - kWpIssuers, part = kPair ? 0 : tile;  // the tile's share of the item's tokens
     const uint32_t sa = tmem + kColS + tile * kWpKeys, oa = tmem + kColO + tile * kHeadDim,
-                   qa = tmem + kColQ + tile * (kHeadDim / 2);
+                   qa = tmem + kColQ + tile * (kHeadDim / 2), la = tmem + kColLow + tile * (kWpKeys / 2);
+    const uint64_t q_desc = sw128_desc(smem_addr(sm.q) + tile * (kWpRows * kRowBytes), 16, 1024);  // (fp32 output)
     const uint64_t k_desc = sw128_desc(smem_addr(sm.k), 16, 1024), v_desc = sw128_desc(smem_addr(sm.v), 16, 1024);
     unsigned passed = 0;            // blocks given back (each tile gives back every one of them)
     unsigned qs = 0, pvs = 0;       // Q's and blocks of P taken up
@@ -598,8 +629,12 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       if (elect_one()) {
         const uint64_t kd = k_desc + uint32_t((st * kWpTileBytes + h * (kWpTileBytes / 2)) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_tmem_a(sa + h * kWpHalf, qa + kk * 8, kd + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          if constexpr (kBf16Out)
+            tc_mma_tmem_a(sa + h * kWpHalf, qa + kk * 8, kd + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
+          else
+            tc_mma(sa + h * kWpHalf, q_desc + kk * (32 >> 4), kd + kk * (32 >> 4), kIdescS, kk > 0 ? 1u : 0u);
+        }
         tc_commit(&sm.s_full[tile][h]);
         mbar_arrive(&sm.s_full[tile][h]);  // (hands on the loader's word about bad pages)
       }
@@ -610,14 +645,22 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       if (!wp_wait(sm, &sm.p_full[tile][h], pvs & 1, a.status)) return false;
       tc_fence_after();
       if (elect_one()) {
-        // P: 16 columns for each 32 keys, the second terms of the same keys behind the first ones
+        // P: 16 columns for each 32 keys, the second terms of the same keys behind the first ones, third terms in columns of
+        // their own; the small ones first
         const uint64_t vd = v_desc + uint32_t((st * kWpTileBytes + h * (kWpTileBytes / 2)) >> 4);
+        const uint32_t fresh = starts && h == 0 ? 0u : 1u;
+        if constexpr (!kBf16Out) {
 #pragma unroll
-        for (int kk = 0; kk < kWpHalf / 16; ++kk) {
-          const uint32_t pa = sa + h * kWpHalf + (kk / 2) * 32 + (kk % 2) * 8;
-          tc_mma_tmem_a(oa, pa, vd + kk * (2048 >> 4), kIdescPV, (starts && h == 0 && kk == 0) ? 0u : 1u);
-          if (!kBf16Out) tc_mma_tmem_a(oa, pa + 16, vd + kk * (2048 >> 4), kIdescPV, 1u);
+          for (int kk = 0; kk < kWpHalf / 16; ++kk)
+            tc_mma_tmem_a(oa, la + h * (kWpHalf / 2) + kk * 8, vd + kk * (2048 >> 4), kIdescPV, kk == 0 ? fresh : 1u);
+#pragma unroll
+          for (int kk = 0; kk < kWpHalf / 16; ++kk)
+            tc_mma_tmem_a(oa, sa + h * kWpHalf + (kk / 2) * 32 + (kk % 2) * 8 + 16, vd + kk * (2048 >> 4), kIdescPV, 1u);
         }
+#pragma unroll
+        for (int kk = 0; kk < kWpHalf / 16; ++kk)
+          tc_mma_tmem_a(oa, sa + h * kWpHalf + (kk / 2) * 32 + (kk % 2) * 8, vd + kk * (2048 >> 4), kIdescPV,
+                        kBf16Out && kk == 0 ? fresh : 1u);
         if (h == 1) {
           if (ends) tc_commit(&sm.o_full[tile]);
           tc_commit(&sm.kv_empty[st]);
@@ -684,16 +727,23 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     const int r = tid & (kWpRows - 1), tok = share * kWpTok + (r >> 2), hh = r & 3;
     auto head_of = [&](const WpItem &t) { return kPair ? t.g + tile : t.g; };
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim;
-    // The row's Q: fetched an item ahead, put into tensor memory once the last S of the item before is there, so that the
-    // next item's first S is computed while this one's last P is (16 x 512 fp32 41.3 us for 42.8, 200 queries 10.6 for
-    // 11.1; 4 x 2048, of longer items, 141 for 140).
-    uint32_t qn[kHeadDim / 2];
-    int q_item = -1;  // whose Q has been fetched: the tile's next
-    auto fetch_q = [&]() {
+    const uint32_t s_addr = lane_base + kColS + tile * kWpKeys, o_addr = lane_base + kColO + tile * kHeadDim,
+                   low_addr = lane_base + kColLow + tile * (kWpKeys / 2);
+    // Q of the tile's next item, once the last S of the one before is there, so that the next item's first S is computed while
+    // this one's last P is (16 x 512 fp32 41.3 us for 42.8, 200 queries 10.6 for 11.1; 4 x 2048, of longer items, 141 for
+    // 140).  With bf16 output every row's own thread fetches it an item ahead and puts it into tensor memory; with fp32
+    // output, where the weights' third terms take those columns, it goes to shared memory by TMA.
+    uint32_t qn[kBf16Out ? kHeadDim / 2 : 1];
+    int q_item = -1;  // the tile's next item
+    uint32_t q_sent = 0;  // boxes that this thread has asked for
+    auto next_q = [&]() {
       do q_item = next_run(q_item + 1);
       while (q_item < nt && (share * kWpTok >= a.item_tok || sm.items[q_item].t0 + share * kWpTok >= sm.items[q_item].n));
-      if (q_item < nt) {
+    };
+    auto fetch_q = [&]() {
+      next_q();
+      if constexpr (kBf16Out) {
+        if (q_item >= nt) return;
         const WpItem &t = sm.items[q_item];
         const bool there = t.t0 + tok < t.n;
         const long long row = (long long)(t.q0 + t.t0 + tok) * kQHeads + head_of(t) * kGroup + hh;
@@ -707,10 +757,24 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
     };
     auto hand_on_q = [&]() {  // the next item's Q
       if (q_item >= nt) return;
-      tmem_st32(lane_base + kColQ + tile * (kHeadDim / 2), qn);
-      tc_fence_before();
-      __syncwarp();
-      if (elect_one()) mbar_arrive(&sm.q_full[tile]);
+      if constexpr (kBf16Out) {
+        tmem_st32(lane_base + kColQ + tile * (kHeadDim / 2), qn);
+        tc_fence_before();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&sm.q_full[tile]);
+      } else if ((warp & 3) == 0) {
+        const WpItem &t = sm.items[q_item];
+        if (elect_one()) {
+          // (rows past the sequence's are the next one's, zeros, or what was there: computed, never written)
+          const int first_tok = t.t0 + share * kWpTok, boxes = min(kWpTok / 8, (t.n - first_tok + 7) / 8);
+          mbar_arrive_expect_tx(&sm.q_full[tile], boxes * (8 * kGroup * kRowBytes));
+          for (int i = 0; i < boxes; ++i)
+            tma_load_3d(sm.q[tile] + i * (8 * kGroup * kRowBytes), &a.tmap_q, 0, head_of(t) * kGroup, t.q0 + first_tok + 8 * i,
+                        &sm.q_full[tile], policy_evict_first());
+          ++q_sent;
+        }
+        __syncwarp();
+      }
       fetch_q();
     };
     fetch_q();
@@ -921,19 +985,16 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
 #pragma unroll 1
           while (true) {
             // every quarter is on its way while the one before it is worked on
-            uint32_t p16[kBf16Out ? 16 : 32];
             if (!loaded) tmem_ld32_async(s_addr, x0);
             tmem_ld_wait(x0);
             tmem_ld32_async(s_addr + 32, x1);
-            run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
-            store_p(s_addr, p16);
+            run_sum += quarter_probs<false, kBf16Out>(x0, ~0u, m, scale, s_addr, low_addr);
             tmem_ld_wait(x1);
             ok = wp_wait(sm, &sm.s_full[tile][1], blocks & 1, a.status);
             if (!ok) break;
             tc_fence_after();
             tmem_ld32_async(s_addr + 64, x0);
-            run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
-            store_p(s_addr + 32, p16);
+            run_sum += quarter_probs<false, kBf16Out>(x1, ~0u, m, scale, s_addr + 32, low_addr + 16);
             if (drain != 0) {  // O of the run before, before the issuer starts it anew
               tmem_st_wait();
               ok = take_run();
@@ -942,8 +1003,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
             written(0);
             tmem_ld_wait(x0);
             tmem_ld32_async(s_addr + 96, x1);
-            run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
-            store_p(s_addr + 64, p16);
+            run_sum += quarter_probs<false, kBf16Out>(x0, ~0u, m, scale, s_addr + 64, low_addr + 32);
             tmem_ld_wait(x1);
             loaded = j + 1 < inner1 &&
                      __all_sync(0xffffffffu, mbar_try_wait(&sm.s_full[tile][0], (blocks + 1) & 1));
@@ -951,8 +1011,7 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
               tc_fence_after();
               tmem_ld32_async(s_addr, x0);
             }
-            run_sum += quarter_probs<false, !kBf16Out>(x1, ~0u, m, scale, p16);
-            store_p(s_addr + 96, p16);
+            run_sum += quarter_probs<false, kBf16Out>(x1, ~0u, m, scale, s_addr + 96, low_addr + 48);
             written(1);
             if (j + 1 >= inner1) break;
             end_block();
@@ -981,18 +1040,16 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
             for (int part = 0; part < 2; ++part) {
               const uint32_t valid = seen_keys(j * kWpKeys + h * kWpHalf + 32 * part, skip, lo, pos, a.sinks,
                                                bad >> (4 * h + 2 * part));
-              uint32_t p16[kBf16Out ? 16 : 32];
+              const uint32_t to = s_addr + h * kWpHalf + 32 * part, low = low_addr + h * (kWpHalf / 2) + 16 * part;
               if (__any_sync(0xffffffffu, valid != 0u)) {
-                tmem_ld32(s_addr + h * kWpHalf + 32 * part, x0);
+                tmem_ld32(to, x0);
                 if (__all_sync(0xffffffffu, valid == ~0u))
-                  run_sum += quarter_probs<false, !kBf16Out>(x0, ~0u, m, scale, p16);
+                  run_sum += quarter_probs<false, kBf16Out>(x0, ~0u, m, scale, to, low);
                 else
-                  run_sum += quarter_probs<true, !kBf16Out>(x0, valid, m, scale, p16);
+                  run_sum += quarter_probs<true, kBf16Out>(x0, valid, m, scale, to, low);
               } else {  // keys that none of the warp's rows sees
-#pragma unroll
-                for (int i = 0; i < (kBf16Out ? 16 : 32); ++i) p16[i] = 0u;
+                no_probs<kBf16Out>(to, low);
               }
-              store_p(s_addr + h * kWpHalf + 32 * part, p16);
             }
             if (h == 0 && drain != 0) {
               tmem_st_wait();
@@ -1016,6 +1073,8 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
       d_sum = sum + run_sum;
     }
     if (ok && drain != 0) take_item();
+    if (q_sent > 0) mbar_wait(&sm.q_full[tile], (q_sent - 1) & 1);  // no copy is on its way
+    __syncwarp();
     if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // every row has been written
     __syncwarp();
   }
@@ -1048,8 +1107,9 @@ int setup_window_attributes() {
   }
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    for (WindowKernel kernel : kWindowKernels)
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWpSmemBytes)) != cudaSuccess) {
+    for (int i = 0; i < 4; ++i)
+      if (cudaFuncSetAttribute(kWindowKernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(i & 1 ? kWpSmemBytes<true> : kWpSmemBytes<false>)) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
       }
@@ -1086,7 +1146,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   // 12.2 in items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 52 us and 41.
   const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
   // No more than 32 queries a sequence fill one tile: two heads then share the CTA, 256 x 4 queries, windows of 512, fp32
-  // in 88 us (123 with the second tile idle), 64 x 16 in 31 (41), 3000 x 10 of 100 in 353 (538), 40 x 32 of 200 in 14.3
+  // in 88 us (123 with the second tile idle; both with two terms a weight, 101 us with three), 64 x 16 in 31 (41), 3000 x 10 of 100 in 353 (538), 40 x 32 of 200 in 14.3
   // (13.9).  While every (sequence, head) finds an SM of its own it has that one.
   const bool pair = max_query <= pkv::kWpTok && (long long)num_seqs * pkv::kKvHeads > sms;
   const int item_tok = pair || (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
@@ -1096,6 +1156,8 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   if (rc != PKV_OK) return rc;
   pkv::WindowArgs a;
   rc = pkv::pool_tensor_maps(pool, pkv::kPageTokens, &a.tmap_k, &a.tmap_v);
+  if (rc != PKV_OK) return rc;
+  rc = pkv::query_tensor_map(q, num_q_rows, pkv::kQHeads, pkv::kHeadDim, pkv::kGroup, 8, &a.tmap_q);
   if (rc != PKV_OK) return rc;
   rc = pkv::output_tensor_map(out, num_q_rows, pkv::kQHeads, pkv::kHeadDim, (flags & PKV_OUT_BF16) != 0, pkv::kGroup, 8,
                               &a.tmap_o);
@@ -1121,14 +1183,16 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   a.scale_log2 = scale * pkv::kLog2e;
   a.status = device_status;
   a.most_items = int((long long)num_seqs * items * (pair ? pkv::kKvHeads / 2 : pkv::kKvHeads));
-  const int by_table = (a.most_items + pkv::kWpMaxItems - 1) / pkv::kWpMaxItems;  // items per CTA <= kWpMaxItems
+  const bool bf16 = (flags & PKV_OUT_BF16) != 0;
+  const int table = bf16 ? pkv::kWpMaxItems<true> : pkv::kWpMaxItems<false>;
+  const int by_table = (a.most_items + table - 1) / table;  // items per CTA <= table
   // in whole rounds of the SMs: a few CTAs more than there are SMs would take as long as all of them (40 x 2048 queries,
   // windows of 128, bf16 310 us in 304 CTAs, 538 in 160)
   const int g = by_table > sms ? (by_table + sms - 1) / sms * sms : sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.most_items < g ? a.most_items : g));
   cfg.blockDim = dim3(pkv::kWpThreads);
-  cfg.dynamicSmemBytes = pkv::kWpSmemBytes;
+  cfg.dynamicSmemBytes = bf16 ? pkv::kWpSmemBytes<true> : pkv::kWpSmemBytes<false>;
   cfg.stream = static_cast<cudaStream_t>(stream);
   // programmatic stream serialization: the set-up (item table, block-table entries, the first item's Q) overlaps the
   // end of the kernel before this one
@@ -1137,7 +1201,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & PKV_OVERLAP_PREVIOUS) ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, pkv::kWindowKernels[(pair ? 2 : 0) + (flags & PKV_OUT_BF16 ? 1 : 0)], a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pkv::kWindowKernels[(pair ? 2 : 0) + (bf16 ? 1 : 0)], a) != cudaSuccess) {
     cudaGetLastError();
     return PKV_ERR_LAUNCH;
   }

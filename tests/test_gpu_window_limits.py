@@ -324,3 +324,18 @@ def test_the_largest_windows_and_sinks(pkv, window, sinks, bf16):
         want, _, size, spread = c.prefill(window, sinks)
         got = _prefill(pkv, c, c.pool.data, window, sinks, bf16, c.scale).double().cpu().numpy()
         S.assert_within(got, want, S.bound(want, size, spread, c.scale, 300, bf16), "window prefill")
+
+
+@pytest.mark.parametrize("contexts,nodes,window,sinks", [([1100, 3000], [64, 40], 1000, 4), ([3000], [33], 2900, 0),
+                                                         ([600, 200, 333], [200, 200, 1], 256, 4), ([9000], [2], 8000, 1),
+                                                         ([2500, 1300, 40] * 8, [9, 32, 3] * 8, 1200, 4)])
+def test_fp32_output_has_the_precision_of_fp32_arithmetic(pkv, contexts, nodes, window, sinks):
+    """Norm of the error over the output's, by sequence.  Three bf16 terms of a weight: 2^-25.  48 MMAs to a run of 256 keys,
+    each of which truncates O by half a unit in the mean, 2^-24 of a number of its size, 0.72 of that over a binade: with V of
+    both signs O grows as the root of their number, 48 * 2 / 3 * 0.72 * 2^-24 = 1.4e-6 at the most (where all go the same way);
+    score and exponential 2^-19 / sqrt(3) = 1.1e-6 at exponents of up to 2^4.  The root of the squares' sum: 1.8e-6."""
+    c = B.Cache(contexts, nodes, seed=78)
+    want = c.prefill(window, sinks)[0]
+    got = _prefill(pkv, c, c.pool.data, window, sinks, False, c.scale).double().cpu().numpy()
+    errors = tree_limits.norm_errors(got, want, c.starts)
+    assert max(errors) < 1.8e-6, errors
