@@ -948,36 +948,36 @@ __global__ void __launch_bounds__(kWpThreads, 1) window_prefill_kernel(const __g
           more = true;
         }
       };
+      // The reference: the largest score of the first of the first block's first four pages of which every key is seen by some
+      // row of the item and lies at or before the tile's last position (any finite value near the scores will do); where there
+      // is no such page, of such keys of the first page, which has one.  Keys that nobody sees count for nothing: they may be
+      // rows of the pool behind the context, of any value.  (The scores of an invalid page are 0.)
+      {
+        const int key = w.begin() * kWpKeys, p0 = t.ctx - t.n + t.t0, first = max(0, p0 - a.window + 1);
+        const int p1 = t.ctx - t.n + min(t.t0 + (share + 1) * kWpTok, t.n) - 1;
+        const uint32_t seen0 = seen_keys(key, skip, first, p1, a.sinks, 0), seen1 = seen_keys(key + 32, skip, first, p1, a.sinks, 0);
+        const int page = (seen0 & 0xffffu) == 0xffffu   ? 0
+                         : seen0 >> 16 == 0xffffu       ? 1
+                         : (seen1 & 0xffffu) == 0xffffu ? 2
+                         : seen1 >> 16 == 0xffffu       ? 3
+                                                        : 0;
+        const uint32_t keys = page == 0 ? seen0 : 0xffffu;
+        ok = arrived();
+        if (!ok) break;
+        const float none = scale < 0.f ? INFINITY : -INFINITY;
+        uint32_t y[16];
+        tmem_ld16_async(s_addr + page * kPageTokens, y);
+        tmem_ld_wait(y);
+#pragma unroll
+        for (int i = 0; i < kPageTokens; ++i) y[i] = keys >> i & 1u ? y[i] : __float_as_uint(none);
+        m = (scale < 0.f ? extreme16<true>(y) : extreme16<false>(y)) * scale;
+        if (!(fabsf(m) < INFINITY)) m = 0.f;
+      }
 #pragma unroll 1
       for (int j = w.begin();;) {
         ok = arrived();
         if (!ok) break;
         const int bad = sm.kv_bad[(gb + (kPair ? 2 * j + tile : j)) % kWpStages];
-        if (used == 0) {
-          // The reference: the largest score of the first of the block's first four pages of which every key is seen by some
-          // row of the item and lies at or before the tile's last position (any finite value near the scores will do); where
-          // there is no such page, of such keys of the first page, which has one.  Keys that nobody sees count for nothing:
-          // they may be rows of the pool behind the context, of any value.
-          const int p0 = t.ctx - t.n + t.t0, p1 = t.ctx - t.n + min(t.t0 + (share + 1) * kWpTok, t.n) - 1;
-          const int first = max(0, p0 - a.window + 1);
-          const uint32_t seen0 = seen_keys(j * kWpKeys, skip, first, p1, a.sinks, bad),
-                         seen1 = seen_keys(j * kWpKeys + 32, skip, first, p1, a.sinks, bad >> 2);
-          const int page = (seen0 & 0xffffu) == 0xffffu ? 0
-                           : seen0 >> 16 == 0xffffu     ? 1
-                           : (seen1 & 0xffffu) == 0xffffu ? 2
-                           : seen1 >> 16 == 0xffffu       ? 3
-                                                          : 0;
-          const uint32_t keys = page == 0 ? seen0 : 0xffffu;
-          const float none = scale < 0.f ? INFINITY : -INFINITY;
-          uint32_t y[16];
-          tmem_ld16_async(s_addr + page * kPageTokens, y);
-          tmem_ld_wait(y);
-#pragma unroll
-          for (int i = 0; i < kPageTokens; ++i) y[i] = keys >> i & 1u ? y[i] : __float_as_uint(none);
-          m = scale < 0.f ? extreme16<true>(y) : extreme16<false>(y);
-          m *= scale;
-          if (!(fabsf(m) < INFINITY)) m = 0.f;
-        }
         // P overwrites the columns of the S that it comes from.  Keys outside the row's window and sinks, and the keys of
         // invalid pages (loaded as zeros), get weight 0.
         if (bad == 0 && j >= inner0 && j < inner1 && drain != 2) {
