@@ -39,14 +39,14 @@
 //    (bounded) for what is in flight, frees its tensor memory and exits.
 //
 // What bounds it: 4 x 2048 queries, windows of 2000, bf16 output, take 143 us (135 GFLOP, 946 TFLOP/s, half of the measured
-// bf16 peak): tensor pipe 42 %, exponentials 39 %, issue slots 45 %, so nothing is full; two softmax warps a scheduler wait
+// bf16 peak): tensor pipe 42 %, exponentials 40 %, issue slots 45 %, so nothing is full; two softmax warps a scheduler wait
 // for S, exponentials and stores in turn, and registers (168 a thread) and tensor memory (all 512 columns are taken) leave
 // no room for a third.  Built and slower: two CTAs to an SM with one S buffer a tile (151 to 161 us), one issuing warp for
 // both tiles (62 cycles a product), softmax warps that issue for themselves (166).  With fp32 output P V is
 // three times the products and a weight 2.5 times the instructions: 2048 queries, windows of 4096, 154 us for 77 (121 with two
 // terms and runs of 1024 keys).  Short windows: 16 x 300..512 queries, windows of 128, fp32 in 41 us, some 13000 cycles an item
 // of two blocks, of them 2000 waiting for its S, 1800 taking out the O before it, the rest four masked halves.  200 queries
-// of one sequence: 11.3 us, the latencies of one item (lists and set-up 2, first K/V 2, blocks and output the rest).
+// of one sequence: 11.2 to 11.6 us, the latencies of one item (lists and set-up 2, first K/V 2, blocks and output the rest).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1142,12 +1142,13 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
       (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return PKV_ERR_ALIGN;
   const int sms = pkv::device_sm_count() > 0 ? pkv::device_sm_count() : 148;
-  // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 10.2 us so and
-  // 12.2 in items of two tiles; 16 x 512 queries, ten items of one tile to an SM, 52 us and 41.
+  // Items of one tile while nearly all of them find an SM of their own: 200 queries of one sequence take 11.4 us so and
+  // 13.1 in items of two tiles; 16 x 300..512 queries, ten items of one tile to an SM, 58.7 us and 40.9.
   const long long pairs = (max_query + pkv::kWpItemTok - 1) / pkv::kWpItemTok;
   // No more than 32 queries a sequence fill one tile: two heads then share the CTA, 256 x 4 queries, windows of 512, fp32
-  // in 88 us (123 with the second tile idle; both with two terms a weight, 101 us with three), 64 x 16 in 31 (41), 3000 x 10 of 100 in 353 (538), 40 x 32 of 200 in 14.3
-  // (13.9).  While every (sequence, head) finds an SM of its own it has that one.
+  // in 99 us (156 with the second tile idle), 64 x 16 in 34 (50), 3000 x 10 of 100 in 368 (617), 40 x 32 of 200 in 18.1
+  // (20.1); bf16 74.6 (92.4), 26.7 (32.1), 296 (492), 14.7 (15.3).  While every (sequence, head) finds an SM of its own it
+  // has that one.
   const bool pair = max_query <= pkv::kWpTok && (long long)num_seqs * pkv::kKvHeads > sms;
   const int item_tok = pair || (long long)num_seqs * pairs * pkv::kKvHeads * 2 <= sms ? pkv::kWpTok : pkv::kWpItemTok;
   const long long items = (max_query + item_tok - 1) / item_tok;
@@ -1187,7 +1188,7 @@ extern "C" int pkv_paged_window_prefill_attention(const pkv_pool *pool, void *ou
   const int table = bf16 ? pkv::kWpMaxItems<true> : pkv::kWpMaxItems<false>;
   const int by_table = (a.most_items + table - 1) / table;  // items per CTA <= table
   // in whole rounds of the SMs: a few CTAs more than there are SMs would take as long as all of them (40 x 2048 queries,
-  // windows of 128, bf16 310 us in 304 CTAs, 538 in 160)
+  // windows of 128, bf16 320 us in 304 CTAs, 573 in 160; fp32 385 in 456, 510 in 320)
   const int g = by_table > sms ? (by_table + sms - 1) / sms * sms : sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.most_items < g ? a.most_items : g));
